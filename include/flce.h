@@ -230,6 +230,55 @@ flce_status flce_vocab_shard_bwd(const void* hidden, const void* weight_shard,
                                  void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Log probabilities of given tokens at the LM head, with entropy and top
+ * alternatives, for scoring, preference or policy-gradient losses and serving
+ * (N from one token of one sequence up).  With z = X W^T / temperature:
+ *   lse[n]     = log sum_v exp z_nv
+ *   logp[n]    = z_{n,t_n} - lse[n]
+ *   entropy[n] = -sum_v p_nv log p_nv,  p = exp(z - lse)          (or NULL)
+ *   top_ids    [N, top_k] int32, top_logp [N, top_k] fp32: the top_k <= 32
+ *              largest z_nv - lse[n], best first; equal logits by the lower id
+ *              (NULL when top_k is 0)
+ * A row whose target is ignore_index gets 0 (ids -1).  A row whose target lies
+ * outside [0, V) gets NaN (ids -1) and FLCE_EBADTARGET in the status word; the
+ * other rows are right.  A row with NaN or +inf logits gets NaN.  After a
+ * pipeline time-out (FLCE_ETIMEOUT) every scored row is NaN.
+ * The N x V logits are not kept: the workspace (flce_logprobs_workspace_bytes;
+ * less runs in smaller chunks, down to 128 rows) stays below 5% of their bf16
+ * size, or 64 MiB (256 MiB with top alternatives) where that is more.
+ * 0 < temperature < inf.  Sizes, alignment, streams and errors as flce_fwd_bwd;
+ * top_k > V is FLCE_EINVAL, top_k > 32 FLCE_EUNSUPPORTED.
+ */
+size_t flce_logprobs_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t top_k);
+flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t* targets,
+                          int64_t N, int64_t H, int64_t V, int32_t ignore_index,
+                          float temperature, int32_t top_k, float* logp, float* entropy,
+                          float* lse, int32_t* top_ids, float* top_logp, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/*
+ * Its gradient: of L = sum_n grad_logp[n] logp[n] + grad_entropy[n] entropy[n],
+ *   dz_nv = (g_n ([v = t_n] - p_nv) - e_n p_nv (log p_nv + entropy[n])) / temperature
+ *   grad_hidden = dz W (bf16 [N,H]; rows of ignored tokens are +0.0)
+ *   grad_weight = dz^T X ([V,H] fp32, or bf16 with FLCE_GW_BF16)
+ * lse and entropy are those flce_logprobs gave for the same inputs (entropy may
+ * be NULL when grad_entropy is).  Either of grad_logp and grad_entropy may be
+ * NULL (zero), and either of grad_hidden and grad_weight (not wanted).  The
+ * logits are computed again chunk by chunk; dz is rounded to bf16 once, from
+ * the fp32 accumulator, and the sums over it are kept in fp32, in a fixed order.
+ * Targets outside [0, V) are treated as ignored (FLCE_EBADTARGET in the status
+ * word); after a time-out the first element of each gradient is NaN.
+ */
+size_t flce_logprobs_bwd_workspace_bytes(int64_t N, int64_t H, int64_t V, uint32_t flags);
+flce_status flce_logprobs_bwd(const void* hidden, const void* weight, const int32_t* targets,
+                              int64_t N, int64_t H, int64_t V, int32_t ignore_index,
+                              uint32_t flags, float temperature, const float* lse,
+                              const float* entropy, const float* grad_logp,
+                              const float* grad_entropy, void* grad_hidden,
+                              float* grad_weight, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
  * grad_hidden (bf16 [N,H]) and grad_weight (fp32 [V,H]) multiplied in place by
  * the fp32 scalar at device address `scale` (read on the device, so the call
  * does not synchronise).  This is the backward of the fused op inside an
@@ -321,7 +370,8 @@ flce_status flce_fwd_bwd_noalloc(const void* hidden, const void* weight,
  * of its tcgen05 GEMM launches on the call's stream and counts every kernel
  * it launches.  flce_profile_end() synchronises those events and returns, per
  * GEMM launch kind (0 = logits, 1 = backward: grad_hidden and grad_weight
- * tiles in one launch, 2 = unused), the summed device time in milliseconds
+ * tiles in one launch, 2 = the logits of the token log probabilities, forward
+ * and backward), the summed device time in milliseconds
  * and the number of launches, plus the total number of kernels launched.  Any output pointer may be NULL.  Profiling is
  * process-wide and not meant to be used from several threads at once.
  */

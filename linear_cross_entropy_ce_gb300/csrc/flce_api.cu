@@ -45,17 +45,13 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-struct DeviceState {
-  bool ready = false;
-  int sms = 0;
-  int major = 0;
-  int pairs = 0;   // CTA pairs of the GEMM that fit on the device at once
-};
-
 constexpr int MAX_DEVICES = 64;
 std::mutex g_dev_mu;
 DeviceState g_dev[MAX_DEVICES];
 
+}  // namespace
+
+namespace flce {
 cudaError_t device_state(DeviceState* out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -83,6 +79,9 @@ unsigned long long wait_timeout_ns() {
   }();
   return v;
 }
+}  // namespace flce
+
+namespace {
 
 // ---------------------------------------------------------------------------
 // workspace plan
@@ -91,13 +90,10 @@ struct Plan {
   long long N = 0, H = 0, V = 0, C = 0, ldz = 0, n_chunks = 0;
   int nvt = 0, nparts = 0, splits = 1, kb_per_split = 0;
   long long n_counters = 0, flags_per_chunk = 0;
-  bool fwd_only = false, norm = false, gw32 = false;
+  bool fwd_only = false, norm = false, gw32 = false, probs = false;
   size_t o_idx = 0, o_rl = 0, o_cnt = 0, o_xc = 0, o_tc = 0, o_zt = 0, o_part = 0, o_z = 0, o_dx = 0, o_rinv = 0,
-         o_dg = 0, o_gw = 0, total = 0;
+         o_dg = 0, o_gw = 0, o_rowc = 0, total = 0;
 };
-
-inline size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
-inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
 
 constexpr int DEFAULT_PAIRS = 76;
 constexpr int MAX_SPLITS = 16;   // splits are summed one after another: keep the chain short
@@ -106,10 +102,12 @@ constexpr int DX_UNIT_KB = 128;  // preferred K blocks of one dX unit
 // Workspace layout for chunks of C rows.  Only the bf16 C x V logits buffer
 // (absent for the forward-only call) grows with V; with a bf16 grad_weight
 // (gw32) the fp32 V x H accumulator of grad_weight lives here as well.
+// probs: the backward of the token log probabilities (per-row constants).
 Plan layout(long long N, long long H, long long V, long long C, int S, bool fwd_only, bool norm = false,
-            bool gw32 = false) {
+            bool gw32 = false, bool probs = false) {
   Plan p;
   p.N = N; p.H = H; p.V = V; p.C = C; p.fwd_only = fwd_only; p.norm = norm; p.gw32 = gw32 && !fwd_only;
+  p.probs = probs;
   p.ldz = cdiv(V, 64) * 64;
   p.nvt = static_cast<int>(cdiv(V, BN));
   p.nparts = static_cast<int>(cdiv(V, PART_COLS));
@@ -143,6 +141,7 @@ Plan layout(long long N, long long H, long long V, long long C, int S, bool fwd_
     p.o_rinv = off; off += al256(size_t(C) * 4);
     p.o_dg = off;   off += al256(size_t(p.n_chunks) * H * 4);
   }
+  if (probs) { p.o_rowc = off; off += al256(size_t(C) * sizeof(DzRow)); }
   if (p.gw32) { p.o_gw = off; off += al256(size_t(V) * H * 4); }
   p.total = off;
   return p;
@@ -181,26 +180,29 @@ int preferred_splits(long long C, long long H, long long V, int pairs) {
 long long max_chunk(long long N) { return cdiv(N, BM) * BM; }
 
 Plan plan_for_chunk(long long N, long long H, long long V, long long C, bool fwd_only, int pairs, size_t bytes,
-                    bool norm = false, bool gw32 = false) {
-  Plan p = layout(N, H, V, C, preferred_splits(C, H, V, pairs), fwd_only, norm, gw32);
-  if (p.total > bytes) p = layout(N, H, V, C, 1, fwd_only, norm, gw32);
+                    bool norm = false, bool gw32 = false, bool probs = false) {
+  Plan p = layout(N, H, V, C, preferred_splits(C, H, V, pairs), fwd_only, norm, gw32, probs);
+  if (p.total > bytes) p = layout(N, H, V, C, 1, fwd_only, norm, gw32, probs);
   return p;
 }
 
 // Largest chunk (multiple of 128 rows) whose plan fits in `bytes`.
 bool plan_for_bytes(long long N, long long H, long long V, bool fwd_only, size_t bytes, int pairs, Plan* out,
-                    bool norm = false, bool gw32 = false) {
+                    bool norm = false, bool gw32 = false, bool probs = false) {
   long long lo = BM, hi = max_chunk(N);
-  if (layout(N, H, V, lo, 1, fwd_only, norm, gw32).total > bytes) return false;
+  if (layout(N, H, V, lo, 1, fwd_only, norm, gw32, probs).total > bytes) return false;
   while (lo < hi) {   // the size shrinks as C grows only through the d(gain) partials: bisect on the total
     const long long mid = ((lo / BM + hi / BM + 1) / 2) * BM;
-    if (layout(N, H, V, mid, 1, fwd_only, norm, gw32).total <= bytes) lo = mid;
+    if (layout(N, H, V, mid, 1, fwd_only, norm, gw32, probs).total <= bytes) lo = mid;
     else hi = mid - BM;
   }
-  *out = plan_for_chunk(N, H, V, lo, fwd_only, pairs, bytes, norm, gw32);
+  *out = plan_for_chunk(N, H, V, lo, fwd_only, pairs, bytes, norm, gw32, probs);
   return true;
 }
 
+}  // namespace
+
+namespace flce {
 int device_pairs() {
   DeviceState d;
   if (device_state(&d) == cudaSuccess) return d.pairs;
@@ -211,29 +213,32 @@ int device_pairs() {
 bool sizes_ok(long long N, long long H, long long V) {
   return N >= 1 && H >= 8 && V >= 1 && N < (1ll << 31) && V < (1ll << 31) && H <= (1ll << 20) && H % 8 == 0;
 }
+}  // namespace flce
+
+namespace {
 
 // The default plan: chunk buffers within 5% of the bf16 logits (never below
 // one 128-row chunk), plus the fp32 grad_weight accumulator when the caller
 // asked for a bf16 grad_weight.
-size_t default_bytes(long long N, long long H, long long V, bool fwd_only, bool norm = false, bool gw32 = false) {
+size_t default_bytes(long long N, long long H, long long V, bool fwd_only, bool norm = false, bool gw32 = false,
+                     bool probs = false) {
   if (!sizes_ok(N, H, V)) return 0;
   gw32 = gw32 && !fwd_only;
   const size_t budget = size_t(N) * size_t(V) * 2 / 20 + (gw32 ? al256(size_t(V) * H * 4) : 0);
   const int pairs = device_pairs();
   Plan p;
-  if (plan_for_bytes(N, H, V, fwd_only, budget, pairs, &p, norm, gw32)) return p.total;
-  return plan_for_chunk(N, H, V, BM, fwd_only, pairs, ~size_t(0), norm, gw32).total;
+  if (plan_for_bytes(N, H, V, fwd_only, budget, pairs, &p, norm, gw32, probs)) return p.total;
+  return plan_for_chunk(N, H, V, BM, fwd_only, pairs, ~size_t(0), norm, gw32, probs).total;
 }
 
 constexpr uint32_t KNOWN_FLAGS = FLCE_REDUCE_SUM | FLCE_GW_BF16;
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+}  // namespace
 
+namespace flce {
 bool make_map(CUtensorMap* m, const void* base, unsigned long long inner, unsigned long long outer,
               unsigned long long row_bytes, unsigned box_inner, unsigned box_outer,
-              CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+              CUtensorMapDataType dtype, CUtensorMapSwizzle swizzle) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {inner, outer};
@@ -244,6 +249,9 @@ bool make_map(CUtensorMap* m, const void* base, unsigned long long inner, unsign
             CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+}  // namespace flce
+
+namespace {
 
 // ---------------------------------------------------------------------------
 // launch profiling (flce_profile_begin / flce_profile_end)
@@ -282,6 +290,9 @@ cudaEvent_t prof_event() {
 // launch of the process to withhold one pipeline signal, with this wait limit.
 std::atomic<unsigned long long> g_stall_armed{0};
 
+}  // namespace
+
+namespace flce {
 // Launch a GEMM, bracketed by events when profiling is on.
 cudaError_t gemm_launch(const GemmArgs& g0, const GemmMaps& m, int grid, cudaStream_t st) {
   GemmArgs g = g0;
@@ -309,13 +320,14 @@ void count_launches(long long n) {
   std::lock_guard<std::mutex> lk(p.mu);
   if (p.on) p.launches += n;
 }
+}  // namespace flce
 
-template <typename T>
-T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws) + off); }
+namespace {
 
 // One call of the library: the plain fused op, the forward-only loss, the
-// fused final RMSNorm, or one of the two passes over a vocabulary shard.
-enum JobKind { JOB_FWD_BWD, JOB_LOSS, JOB_SHARD_STATS, JOB_SHARD_BWD };
+// fused final RMSNorm, one of the two passes over a vocabulary shard, or the
+// backward of the token log probabilities.
+enum JobKind { JOB_FWD_BWD, JOB_LOSS, JOB_SHARD_STATS, JOB_SHARD_BWD, JOB_PROBS_BWD };
 
 struct Job {
   JobKind kind = JOB_FWD_BWD;
@@ -337,7 +349,11 @@ struct Job {
   float* row_max = nullptr;          // shard statistics
   float* row_sumexp = nullptr;
   float* row_zt = nullptr;
-  const float* lse = nullptr;        // global log-sum-exp for the shard backward
+  const float* lse = nullptr;        // global log-sum-exp for the shard backward, of z / temperature for JOB_PROBS_BWD
+  const float* entropy = nullptr;    // JOB_PROBS_BWD
+  const float* grad_logp = nullptr;
+  const float* grad_entropy = nullptr;
+  float temperature = 1.f;
   void* ws = nullptr;
   size_t ws_bytes = 0;
   void* stream = nullptr;
@@ -350,12 +366,20 @@ flce_status run(const Job& j) {
   if (norm && (!j.grad_gain || !aligned16(j.gain) || !aligned4(j.grad_gain) || !(j.eps >= 0.f))) return FLCE_EINVAL;
   if (!j.hidden || !j.weight || !j.targets || !j.ws) return FLCE_EINVAL;
   if ((j.kind == JOB_FWD_BWD || j.kind == JOB_LOSS) && (!j.loss || !j.n_valid)) return FLCE_EINVAL;
-  if (!fwd_only && (!j.grad_hidden || !j.grad_weight)) return FLCE_EINVAL;
+  const bool probs = j.kind == JOB_PROBS_BWD;
+  const int skip = probs ? (j.grad_hidden ? 0 : SKIP_DX) | (j.grad_weight ? 0 : SKIP_DW) : 0;
+  if (!fwd_only && !probs && (!j.grad_hidden || !j.grad_weight)) return FLCE_EINVAL;
   if (j.kind == JOB_SHARD_STATS && (!j.row_max || !j.row_sumexp || !j.row_zt)) return FLCE_EINVAL;
   if (j.kind == JOB_SHARD_BWD && !j.lse) return FLCE_EINVAL;
   if (j.flags & ~KNOWN_FLAGS) return FLCE_EINVAL;
   const bool gw_bf16 = (j.flags & FLCE_GW_BF16) != 0;
-  if (gw_bf16 && j.kind != JOB_FWD_BWD) return FLCE_EINVAL;   // forward-only and shard calls have no such output
+  if (gw_bf16 && j.kind != JOB_FWD_BWD && !probs) return FLCE_EINVAL;   // forward-only and shard calls have no such output
+  if (probs) {
+    if (skip == (SKIP_DX | SKIP_DW) || !j.lse || (!j.grad_logp && !j.grad_entropy)) return FLCE_EINVAL;
+    if (j.grad_entropy && !j.entropy) return FLCE_EINVAL;
+    if ((gw_bf16 && !j.grad_weight) || bad_temperature(j.temperature)) return FLCE_EINVAL;
+    if (!aligned4(j.entropy) || !aligned4(j.grad_logp) || !aligned4(j.grad_entropy)) return FLCE_EUNSUPPORTED;
+  }
   if (N < 1 || H < 1 || V < 1 || j.v0 < 0 || j.V_total < j.v0 + V) return FLCE_EINVAL;
   if (!sizes_ok(N, H, V) || j.V_total >= (1ll << 31)) return FLCE_EUNSUPPORTED;
   if (!aligned16(j.hidden) || !aligned16(j.weight) || !aligned16(j.ws) || !aligned4(j.targets) ||
@@ -368,7 +392,7 @@ flce_status run(const Job& j) {
   if (device_state(&dev) != cudaSuccess) { cudaGetLastError(); return FLCE_ECUDA; }
   if (dev.major < 10) return FLCE_EUNSUPPORTED;
   Plan p;
-  if (!plan_for_bytes(N, H, V, fwd_only, j.ws_bytes, dev.pairs, &p, norm, gw_bf16)) return FLCE_EWORKSPACE;
+  if (!plan_for_bytes(N, H, V, fwd_only, j.ws_bytes, dev.pairs, &p, norm, gw_bf16, probs)) return FLCE_EWORKSPACE;
 
   cudaStream_t st = static_cast<cudaStream_t>(j.stream);
   void* ws = j.ws;
@@ -396,9 +420,10 @@ flce_status run(const Job& j) {
   if (!fwd_only)
     ok = ok && make_map(&bm.a0, z, V, p.C, p.ldz * 2, BK, BM) && make_map(&bm.b0, j.weight, H, V, hb, 64, BK) &&
          make_map(&bm.a1, z, V, p.C, p.ldz * 2, 64, BK) && make_map(&bm.b1, xc, H, p.C, hb, 64, BK) &&
-         make_map(&bm.out, gwacc, H, V, static_cast<unsigned long long>(H) * 4, 32, 64,
-                  CU_TENSOR_MAP_DATA_TYPE_FLOAT32, CU_TENSOR_MAP_SWIZZLE_128B);
+         (!gwacc || make_map(&bm.out, gwacc, H, V, static_cast<unsigned long long>(H) * 4, 32, 64,
+                             CU_TENSOR_MAP_DATA_TYPE_FLOAT32, CU_TENSOR_MAP_SWIZZLE_128B));
   if (!ok) return FLCE_ECUDA;
+  if (!gwacc) bm.out = bm.b1;   // never stored through, but its descriptor is prefetched
 
   const int reduce_sum = (j.flags & FLCE_REDUCE_SUM) ? 1 : 0;
   GemmArgs g;
@@ -432,22 +457,30 @@ flce_status run(const Job& j) {
   // (Llama-3-8B head, full-model shape).
   g.pf_threads = p.C <= 512 ? 1 : 0;
   g.dxacc = dxacc;
+  g.skip = skip;
+  DzRow* rowc = probs ? at<DzRow>(ws, p.o_rowc) : nullptr;
+  g.rowc = rowc;
+  if (probs) g.c2 = 1.4426950408889634f / j.temperature;
 
   // persistent grids: CTA pairs, no more than fit on the device at once
   const long long mt = cdiv(p.C, PAIR_M), ht = cdiv(H, BN);
   const int grid_logits = 2 * static_cast<int>(std::min<long long>(mt * p.nvt, dev.pairs));
   const int grid_bwd =
-      2 * static_cast<int>(std::min<long long>(mt * ht * p.splits + cdiv(V, PAIR_M) * ht, dev.pairs));
+      2 * static_cast<int>(std::min<long long>(
+              ((skip & SKIP_DX) ? 0 : mt * ht * p.splits) + ((skip & SKIP_DW) ? 0 : cdiv(V, PAIR_M) * ht), dev.pairs));
 
   auto chk = [](cudaError_t e) { return e == cudaSuccess; };
   const bool stats = j.kind == JOB_SHARD_STATS;
   const int v0 = static_cast<int>(j.v0);
-  count_launches(1 + (fwd_only ? 0 : 1) + (j.kind == JOB_SHARD_BWD ? 0 : 1) + p.n_chunks * (norm ? 4 : 2) +
-                 (norm ? 1 : 0) + (p.gw32 ? 1 : 0));
+  if (probs)   // prep, zeroed rows, one gather per chunk, failure mark, rounding
+    count_launches(2 + (j.grad_hidden ? 1 : 0) + p.n_chunks + (p.gw32 ? 1 : 0));
+  else
+    count_launches(1 + (fwd_only ? 0 : 1) + (j.kind == JOB_SHARD_BWD ? 0 : 1) + p.n_chunks * (norm ? 4 : 2) +
+                   (norm ? 1 : 0) + (p.gw32 ? 1 : 0));
   if (!chk(launch_prep(j.targets, N, static_cast<int>(j.V_total), j.ii, hdr, idx, j.n_valid, counters,
                        p.n_counters, st)))
     return FLCE_ECUDA;
-  if (!fwd_only && !chk(launch_zero_ignored(hdr, idx, N, H * (j.grad_hidden_f32 ? 4 : 2), j.grad_hidden, st)))
+  if (!fwd_only && j.grad_hidden && !chk(launch_zero_ignored(hdr, idx, N, H * (j.grad_hidden_f32 ? 4 : 2), j.grad_hidden, st)))
     return FLCE_ECUDA;
   if (stats && !chk(launch_shard_stats_ignored(hdr, idx, N, j.row_max, j.row_sumexp, j.row_zt, st)))
     return FLCE_ECUDA;
@@ -458,12 +491,16 @@ flce_status run(const Job& j) {
       if (!chk(launch_gather_norm(static_cast<const uint16_t*>(j.hidden), j.targets, hdr, idx, c0, g.C, g.H,
                                   static_cast<const uint16_t*>(j.gain), j.eps, xc, tc, rinv, st)))
         return FLCE_ECUDA;
+    } else if (probs) {
+      if (!chk(launch_gather_dz(static_cast<const uint16_t*>(j.hidden), j.targets, hdr, idx, c0, g.C, g.H,
+                                j.temperature, j.lse, j.entropy, j.grad_logp, j.grad_entropy, xc, tc, rowc, st)))
+        return FLCE_ECUDA;
     } else if (!chk(launch_gather(static_cast<const uint16_t*>(j.hidden), j.targets, hdr, idx, c0, g.C, g.H, xc,
                                   tc, v0, g.V, st))) {
       return FLCE_ECUDA;
     }
     int* sync = counters + c * (2 + p.flags_per_chunk);
-    g.mode = MODE_LOGITS;
+    g.mode = probs ? MODE_DZ : MODE_LOGITS;   // MODE_DZ leaves the finished dz in z
     g.counter = sync;
     if (!chk(gemm_launch(g, fm, grid_logits, st))) return FLCE_ECUDA;
     if (stats) {
@@ -472,7 +509,7 @@ flce_status run(const Job& j) {
         return FLCE_ECUDA;
       continue;
     }
-    if (!chk(launch_lse_dz(hdr, c0, g.C, g.V, p.ldz, p.nparts, part, zt, tc, rl, z, reduce_sum, fwd_only ? 0 : 1,
+    if (!probs && !chk(launch_lse_dz(hdr, c0, g.C, g.V, p.ldz, p.nparts, part, zt, tc, rl, z, reduce_sum, fwd_only ? 0 : 1,
                            j.lse, idx, st)))
       return FLCE_ECUDA;
     if (fwd_only) continue;
@@ -492,6 +529,8 @@ flce_status run(const Job& j) {
   }
   if (norm && !chk(launch_dgain_reduce(dgp, p.n_chunks, g.H, j.grad_gain, st))) return FLCE_ECUDA;
   if (p.gw32 && !chk(launch_f32_to_bf16(gwacc, V * H, reinterpret_cast<uint16_t*>(j.grad_weight), st)))
+    return FLCE_ECUDA;
+  if (probs && !chk(launch_mark_failed(hdr, static_cast<uint16_t*>(j.grad_hidden), j.grad_weight, gw_bf16, st)))
     return FLCE_ECUDA;
   return FLCE_OK;
 }
@@ -692,6 +731,28 @@ flce_status flce_vocab_shard_bwd(const void* hidden, const void* weight_shard, c
   return run(j);
 }
 
+size_t flce_logprobs_bwd_workspace_bytes(int64_t N, int64_t H, int64_t V, uint32_t flags) {
+  if (flags & ~FLCE_GW_BF16) return 0;
+  return default_bytes(N, H, V, false, false, (flags & FLCE_GW_BF16) != 0, true);
+}
+
+flce_status flce_logprobs_bwd(const void* hidden, const void* weight, const int32_t* targets, int64_t N, int64_t H,
+                              int64_t V, int32_t ignore_index, uint32_t flags, float temperature, const float* lse,
+                              const float* entropy, const float* grad_logp, const float* grad_entropy,
+                              void* grad_hidden, float* grad_weight, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  if (flags & ~FLCE_GW_BF16) return FLCE_EINVAL;
+  Job j;
+  j.kind = JOB_PROBS_BWD;
+  j.hidden = hidden; j.weight = weight; j.targets = targets;
+  j.N = N; j.H = H; j.V = V; j.V_total = V; j.ii = ignore_index; j.flags = flags;
+  j.temperature = temperature; j.lse = lse; j.entropy = entropy;
+  j.grad_logp = grad_logp; j.grad_entropy = grad_entropy;
+  j.grad_hidden = grad_hidden; j.grad_weight = grad_weight;
+  j.ws = workspace; j.ws_bytes = workspace_bytes; j.stream = stream;
+  return run(j);
+}
+
 flce_status flce_scale_grads(void* grad_hidden, float* grad_weight, int64_t N, int64_t H, int64_t V,
                              const float* scale, void* stream) {
   if (!grad_hidden || !grad_weight || !scale) return FLCE_EINVAL;
@@ -732,9 +793,10 @@ flce_status flce_profile_end(double* gemm_ms, int64_t* gemm_launches, int64_t* k
     if (cudaEventSynchronize(r.stop) != cudaSuccess || cudaEventElapsedTime(&t, r.start, r.stop) != cudaSuccess) {
       cudaGetLastError();
       st = FLCE_ECUDA;
-    } else if (r.mode >= 0 && r.mode < 3) {
-      ms[r.mode] += t;
-      ++cnt[r.mode];
+    } else if (r.mode >= 0) {
+      const int kind = r.mode < MODE_STATS ? r.mode : 2;
+      ms[kind] += t;
+      ++cnt[kind];
     }
     p.pool.push_back(r.start);
     p.pool.push_back(r.stop);

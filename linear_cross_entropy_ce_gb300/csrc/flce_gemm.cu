@@ -24,6 +24,12 @@
 //                grad_weight read-modify-write: where the grad_hidden GEMM is
 //                split, the claim order spreads the dX units evenly through
 //                the dW units so both kinds run at once.
+//   MODE_STATS   z = Xc W^T again for the token log probabilities: per row and
+//                part the max m, sum 2^d and sum d 2^d of d = (z - m) c2 (the
+//                entropy needs the third), the target logit and, for top
+//                alternatives, the fp32 logits.
+//   MODE_DZ      z = Xc W^T once more, turned in registers into the gradient
+//                of the logits (bf16) that MODE_BWD consumes.
 //
 // Each tile is 256 x 256 and is computed by a CTA pair (a cluster of two CTAs
 // on two SMs) with tcgen05.mma.cta_group::2: each CTA stages its 128 rows of
@@ -183,13 +189,14 @@ struct Shape {
   int units;
 };
 
+template <bool PROBS>
 __device__ __forceinline__ Shape make_shape(const GemmArgs& a) {
   Shape s;
   const long long nv = a.hdr[HDR_NVALID];
   const long long rem = nv - a.c0;
   s.Cl = rem <= 0 ? 0 : (rem >= a.C ? a.C : static_cast<int>(rem));
   s.mt = (s.Cl + PAIR_M - 1) / PAIR_M;
-  if (a.mode == MODE_LOGITS) {
+  if (PROBS || a.mode == MODE_LOGITS) {
     s.nt = a.nvt;
     s.kbt = (a.H + BK - 1) / BK;
     s.n_dx = 0;
@@ -199,9 +206,9 @@ __device__ __forceinline__ Shape make_shape(const GemmArgs& a) {
   } else {
     s.nt = (a.H + BN - 1) / BN;
     s.kbt = 0;
-    s.n_dx = s.mt * s.nt * a.splits;
+    s.n_dx = (a.skip & SKIP_DX) ? 0 : s.mt * s.nt * a.splits;
     s.dw_mt = (a.V + PAIR_M - 1) / PAIR_M;
-    const int n_dw = s.dw_mt * s.nt;
+    const int n_dw = (a.skip & SKIP_DW) ? 0 : s.dw_mt * s.nt;
     s.units = s.Cl > 0 ? s.n_dx + n_dw : 0;
     s.dx_span = s.n_dx;   // dX units first
     if (a.interleave && s.Cl > 0) {
@@ -233,10 +240,11 @@ struct Unit {
 // together share one slice of W; then N; then the vocabulary split, so every
 // split is claimed after the previous one of its tile.  dW units walk N
 // fastest so they share one slab of dz.
+template <bool PROBS>
 __device__ __forceinline__ Unit decode_unit(const GemmArgs& a, const Shape& s, int u) {
   Unit t;
   t.split = 0;
-  if (a.mode == MODE_LOGITS) {
+  if (PROBS || a.mode == MODE_LOGITS) {
     const int m = u % s.mt, n = u / s.mt;
     t.kind = U_LOGITS; t.m0 = m * PAIR_M; t.n0 = n * BN; t.ntile = n; t.kb0 = 0; t.kb1 = s.kbt;
     return t;
@@ -332,6 +340,124 @@ __device__ __forceinline__ void epi_logits(const GemmArgs& a, const Shape& s, co
   if (rv) {
     a.part[static_cast<size_t>(grow) * a.nparts + c0 / PART_COLS] = make_float2(mx, sum);
     if (tl >= 0 && tl < ncol) a.zt[grow] = ztv;
+  }
+}
+
+// Statistics of one row and part.  With c2 = log2(e) / temperature and
+// d = (z - max) c2 <= 0: sum 2^d and sum d 2^d, from which the row kernel
+// forms log-sum-exp and entropy.  The stats array is part-major, so a warp's
+// 32 rows store 128 contiguous bytes per value.
+__device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, const Unit& t, int row0, int col0,
+                                          uint32_t tbase, int r) {
+  const int grow = row0 + r;
+  const bool rv = grow < s.Cl;
+  const int c0 = t.n0 + col0;
+  const int tl = (rv ? a.tc[grow] : -1) - c0;
+  const int ncol = min(GROUP_COLS, a.V - c0);
+  if (ncol <= 0) return;                          // uniform over the warpgroup
+  float mx = -INFINITY, ztv = 0.f;
+  float* zrow = a.zf + static_cast<size_t>(grow) * a.ldz + c0;
+  const bool store = a.zf != nullptr && rv;
+#pragma unroll 1
+  for (int j = 0; j < GROUP_COLS / 32; ++j) {
+    float v[32];
+    ptx::tmem_ld32(tbase + j * 32, v);
+    if (j * 32 + 32 <= ncol) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) mx = fmaxf(mx, v[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (j * 32 + k < ncol) mx = fmaxf(mx, v[k]);
+    }
+    if (static_cast<unsigned>(tl - j * 32) < 32u) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (j * 32 + k == tl) ztv = v[k];
+    }
+    if (store && c0 + j * 32 < a.ldz) {
+#pragma unroll
+      for (int k = 0; k < 32; k += 8)
+        ptx::st_global_v8(zrow + j * 32 + k, __float_as_uint(v[k]), __float_as_uint(v[k + 1]),
+                          __float_as_uint(v[k + 2]), __float_as_uint(v[k + 3]), __float_as_uint(v[k + 4]),
+                          __float_as_uint(v[k + 5]), __float_as_uint(v[k + 6]), __float_as_uint(v[k + 7]));
+    }
+  }
+  const float mb = mx == -INFINITY ? 0.f : -mx * a.c2;   // a part of nothing but -inf sums to zero
+  float sum = 0.f, dsum = 0.f;
+#pragma unroll 1
+  for (int j = 0; j < GROUP_COLS / 32; ++j) {
+    float v[32];
+    ptx::tmem_ld32(tbase + j * 32, v);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float d = fmaf(v[k], a.c2, mb);
+      const float e = ptx::ex2(d);
+      if (j * 32 + k < ncol) {
+        sum += e;
+        dsum = fmaf(fmaxf(d, -1e30f), e, dsum);   // 0 for a logit of -inf
+      }
+    }
+  }
+  // mb is rounded: every d above is too large by rho = mx c2 + mb (exact in the
+  // fused multiply-add), which matters where the logits are large
+  const float rho = mx == -INFINITY ? 0.f : fmaf(mx, a.c2, mb);
+  const float back = ptx::ex2(-rho);
+  dsum = back * fmaf(-rho, sum, dsum);
+  sum *= back;
+  if (rv) {
+    const size_t np = static_cast<size_t>(a.nparts) * a.C;
+    float* p = a.stats + static_cast<size_t>(c0 / PART_COLS) * a.C + grow;
+    p[0] = mx;
+    p[np] = sum;
+    p[2 * np] = dsum;
+    if (tl >= 0 && tl < ncol) a.zt[grow] = ztv;
+  }
+}
+
+// Gradient of the logits of one row and part, written as bf16 once: of the
+// fp32 accumulator, so the only rounding before the consuming GEMMs is that
+// of dz itself (relative 2^-9).  Rows between the valid ones and the next
+// multiple of 128 are written too (as zeros, their constants being zero): the
+// grad_weight GEMM reads them.
+__device__ __forceinline__ void epi_dz(const GemmArgs& a, const Shape& s, const Unit& t, int row0, int col0,
+                                       uint32_t tbase, int r) {
+  const int grow = row0 + r;
+  const bool rw = grow < min(a.C, (s.Cl + BM - 1) / BM * BM);
+  const int c0 = t.n0 + col0;
+  const int tl = (rw ? a.tc[grow] : -1) - c0;
+  const int ncol = min(GROUP_COLS, a.V - c0);
+  if (ncol <= 0) return;                          // uniform over the warpgroup
+  DzRow q = {0.f, 0.f, 0.f, 0.f};
+  if (rw) q = a.rowc[grow];
+  uint16_t* zrow = a.z + static_cast<size_t>(grow) * a.ldz + c0;
+#pragma unroll 1
+  for (int j = 0; j < GROUP_COLS / 32; ++j) {
+    float v[32];
+    ptx::tmem_ld32(tbase + j * 32, v);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float l2 = fmaf(v[k], a.c2, -q.lse2);
+      v[k] = ptx::ex2(l2) * fmaf(q.b, fmaxf(l2, -1e30f), q.a);   // 0 for a logit of -inf
+    }
+    if (static_cast<unsigned>(tl - j * 32) < 32u) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (j * 32 + k == tl) v[k] += q.g;
+    }
+    if (j * 32 + 32 > ncol) {   // the block straddles the end of the vocabulary
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (j * 32 + k >= ncol) v[k] = 0.f;
+    }
+    if (rw && c0 + j * 32 < a.ldz) {
+      uint32_t pk[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) pk[k] = ptx::pack_bf16x2(v[2 * k], v[2 * k + 1]);
+      uint16_t* dst = zrow + j * 32;
+      ptx::st_global_v8(dst, pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6], pk[7]);
+      ptx::st_global_v8(dst + 16, pk[8], pk[9], pk[10], pk[11], pk[12], pk[13], pk[14], pk[15]);
+    }
   }
 }
 
@@ -502,6 +628,9 @@ __device__ __forceinline__ bool epi_dx_split(const GemmArgs& a, const Shape& s, 
   return true;
 }
 
+// PROBS selects the two modes of the token log probabilities (MODE_STATS,
+// MODE_DZ); a kernel of their own leaves the loss kernel's registers alone.
+template <bool PROBS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     flce_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -512,10 +641,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   const uint32_t rank = ptx::cluster_ctarank();
   const bool lead = rank == 0;
 
-  const Shape s = make_shape(a);   // identical in both CTAs of a pair
-  if (a.mode == MODE_BWD && s.Cl == 0) {
+  const Shape s = make_shape<PROBS>(a);   // identical in both CTAs of a pair
+  if (!PROBS && a.mode == MODE_BWD && s.Cl == 0) {
     // Empty first chunk (no valid token at all): grad_weight is zero.
-    if (a.first_chunk) {
+    if (a.first_chunk && !(a.skip & SKIP_DW)) {
       const size_t n4 = static_cast<size_t>(a.V) * a.H / 4;
       float4* gw = reinterpret_cast<float4*>(a.grad_weight);
       for (size_t i = static_cast<size_t>(blockIdx.x) * NUM_THREADS + threadIdx.x; i < n4;
@@ -547,7 +676,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     ptx::mbar_fence_init();
     ptx::tma_prefetch_desc(&maps.a0);
     ptx::tma_prefetch_desc(&maps.b0);
-    if (a.mode == MODE_BWD) {
+    if (!PROBS && a.mode == MODE_BWD) {
       ptx::tma_prefetch_desc(&maps.a1);
       ptx::tma_prefetch_desc(&maps.b1);
       ptx::tma_prefetch_desc(&maps.out);
@@ -565,7 +694,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   const uint64_t to = a.timeout_ns;
   int* hdr = const_cast<int*>(a.hdr);
   const int half = static_cast<int>(rank) * BM;   // this CTA's rows (A) / columns (B) inside a pair tile
-  const uint32_t nstages = a.mode == MODE_LOGITS ? STAGES_LOGITS : STAGES;
+  const uint32_t nstages = PROBS || a.mode == MODE_LOGITS ? STAGES_LOGITS : STAGES;
 
   if (warp == 0 && lane == 0) {
     // ---------------- (CTA 0: scheduler +) TMA producer ----------------
@@ -603,7 +732,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       }
       if (++sslot == SCHED_SLOTS) { sslot = 0; sphase ^= 1u; }
       if (u < 0) break;
-      const Unit t = decode_unit(a, s, u);
+      const Unit t = decode_unit<PROBS>(a, s, u);
       if (lead && t.kb1 - t.kb0 <= SHORT_TILE_KB) next = atomicAdd(a.counter, 1);
       for (int kb = t.kb0; kb < t.kb1; ++kb) {
         if (!wait_stage(&ctl->empty[stage], phase ^ 1u, ctl, to, hdr, W_STAGE_EMPTY, u | (stage << 24))) { ok = false; break; }
@@ -649,7 +778,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       ptx::mbar_arrive(&ctl->sempty[sslot]);
       if (++sslot == SCHED_SLOTS) { sslot = 0; sphase ^= 1u; }
       if (u < 0) break;
-      const Unit t = decode_unit(a, s, u);
+      const Unit t = decode_unit<PROBS>(a, s, u);
       const int a_mn = t.kind == U_DW ? 1 : 0;
       const int b_mn = t.kind == U_LOGITS ? 0 : 1;
       const uint32_t idesc = ptx::idesc_bf16_f32(PAIR_M, BN, a_mn, b_mn);
@@ -716,7 +845,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       if (++sslot == SCHED_SLOTS) { sslot = 0; sphase ^= 1u; }
       if (u < 0) break;
       if ((seq++ & 1u) != static_cast<uint32_t>(set)) continue;   // the other set's tile
-      const Unit t = decode_unit(a, s, u);
+      const Unit t = decode_unit<PROBS>(a, s, u);
       if (t.kind == U_DW && a.accumulate && a.pf_threads) {
         // this thread's row of the grad_weight tile (128 fp32 = 4 lines) into
         // L2 before the reduce-adds; plain prefetches leave the TMA unit to
@@ -735,7 +864,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       const uint32_t tbase = tmem + (static_cast<uint32_t>(q * 32) << 16) + set * BN + col0;
       const int row0 = t.m0 + half;
       bool cont = true;
-      if (t.kind == U_LOGITS)
+      if constexpr (PROBS) {
+        if (a.mode == MODE_STATS) epi_stats(a, s, t, row0, col0, tbase, r);
+        else epi_dz(a, s, t, row0, col0, tbase, r);
+      } else if (t.kind == U_LOGITS)
         epi_logits(a, s, t, row0, col0, tbase, r);
       else if (t.kind == U_DX && a.splits == 1)
         epi_dx_direct(a, s, t, row0, col0, tbase, r);
@@ -770,7 +902,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 int gemm_smem_bytes() { return SMEM_BYTES; }
 
 cudaError_t gemm_prepare(int /*device*/) {
-  return cudaFuncSetAttribute(flce_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  cudaError_t e = cudaFuncSetAttribute(flce_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(flce_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
 }
 
 cudaError_t gemm_max_pairs(int* pairs) {
@@ -785,12 +919,13 @@ cudaError_t gemm_max_pairs(int* pairs) {
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(pairs, flce_gemm_kernel, &cfg);
+  return cudaOccupancyMaxActiveClusters(pairs, flce_gemm_kernel<false>, &cfg);
 }
 
 cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps& m, int grid, cudaStream_t st) {
   // grid counts CTAs and must be even (pairs)
-  flce_gemm_kernel<<<grid, NUM_THREADS, SMEM_BYTES, st>>>(m, a);
+  if (a.mode == MODE_STATS || a.mode == MODE_DZ) flce_gemm_kernel<true><<<grid, NUM_THREADS, SMEM_BYTES, st>>>(m, a);
+  else flce_gemm_kernel<false><<<grid, NUM_THREADS, SMEM_BYTES, st>>>(m, a);
   return cudaGetLastError();
 }
 

@@ -36,6 +36,20 @@ enum GemmMode : int {
   MODE_BWD = 1,     // one launch holding both consumers of dz:
                     //   grad_hidden rows = dz W          (units [0, n_dx))
                     //   grad_weight (+)= dz^T Xc         (units [n_dx, n_dx + n_dw))
+  MODE_STATS = 2,   // z = Xc W^T, epilogue: per 128-column part the max, sum exp and sum of (log weight x exp),
+                    // z_t, and the fp32 logits themselves where top alternatives are asked for
+  MODE_DZ = 3,      // z = Xc W^T again, epilogue: dz of the token log probabilities and entropies, from the
+                    // rows' log-sum-exp, entropy and upstream gradients, as bf16
+};
+
+// Unit kinds a MODE_BWD launch leaves out (GemmArgs::skip).
+constexpr int SKIP_DX = 1;
+constexpr int SKIP_DW = 2;
+
+// Per-row constants of MODE_DZ, with l2 = z c - lse2 (the base-2 log probability):
+// dz = 2^l2 (a + b l2) + [v = t] g.
+struct DzRow {
+  float lse2, a, b, g;
 };
 
 struct GemmArgs {
@@ -71,6 +85,12 @@ struct GemmArgs {
   float* grad_hidden_f32; // [N][H] fp32 instead of grad_hidden when not null (vocabulary shards)
   float* grad_weight;   // [V][H] fp32 (zero fill of an empty first chunk)
   const float* dxacc;   // [C][H] fp32 sum of the grad_hidden splits (splits > 1)
+  // MODE_STATS, MODE_DZ
+  int skip;             // BWD: SKIP_DX, SKIP_DW
+  float c2;             // log2(e) / temperature: z c2 is the scaled logit in base-2 units
+  float* stats;         // STATS: [3][nparts][C] part max (raw z), sum of 2^d, sum of d 2^d, d = (z - max) c2
+  float* zf;            // STATS: [C][ldz] fp32 logits, or null
+  const DzRow* rowc;    // DZ: [C] (rows past the valid ones hold zeros)
 };
 
 // Tensor maps of one launch.  LOGITS: a0 = Xc (K-major), b0 = W (K-major).
@@ -86,6 +106,32 @@ cudaError_t gemm_prepare(int device);
 cudaError_t gemm_max_pairs(int* pairs);   // CTA pairs resident at once (current device)
 cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps& m, int grid, cudaStream_t s);
 
+// Host helpers shared by the entry points (flce_api.cu).
+struct DeviceState {
+  bool ready = false;
+  int sms = 0;
+  int major = 0;
+  int pairs = 0;   // CTA pairs of the GEMM that fit on the device at once
+};
+cudaError_t device_state(DeviceState* out);
+int device_pairs();
+unsigned long long wait_timeout_ns();
+bool make_map(CUtensorMap* m, const void* base, unsigned long long inner, unsigned long long outer,
+              unsigned long long row_bytes, unsigned box_inner, unsigned box_outer,
+              CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+              CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
+// Launch a GEMM, bracketed by events when profiling is on.
+cudaError_t gemm_launch(const GemmArgs& g0, const GemmMaps& m, int grid, cudaStream_t st);
+void count_launches(long long n);
+bool sizes_ok(long long N, long long H, long long V);
+
+inline size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
+inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+template <typename T>
+T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws) + off); }
+
 // Elementwise / bookkeeping kernels (flce_aux.cu).
 cudaError_t launch_prep(const int* targets, long long N, int V, int ignore_index,
                         int* hdr, int* idx, int* n_valid_out, int* counters, long long n_counters,
@@ -95,6 +141,14 @@ cudaError_t launch_zero_ignored(const int* hdr, const int* idx, long long N, lon
 cudaError_t launch_gather(const uint16_t* hidden, const int* targets, const int* hdr,
                           const int* idx, long long c0, int C, int H,
                           uint16_t* xc, int* tc, int v0, int vs, cudaStream_t s);
+// Token log probabilities (flce_logprobs.cu).
+cudaError_t launch_gather_dz(const uint16_t* hidden, const int* targets, const int* hdr, const int* idx,
+                             long long c0, int C, int H, float temperature, const float* lse, const float* entropy,
+                             const float* grad_logp, const float* grad_entropy, uint16_t* xc, int* tc, DzRow* rowc,
+                             cudaStream_t s);
+cudaError_t launch_mark_failed(const int* hdr, uint16_t* grad_hidden, float* grad_weight, int gw_bf16,
+                               cudaStream_t s);
+bool bad_temperature(float t);
 cudaError_t launch_lse_dz(const int* hdr, long long c0, int C, int V, long long ldz,
                           int nparts, const float2* part, const float* zt, const int* tc,
                           float* rl, uint16_t* z, int reduce_sum, int make_dz,

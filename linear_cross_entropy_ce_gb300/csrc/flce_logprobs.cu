@@ -1,0 +1,361 @@
+// Token log probabilities at the LM head, with entropy and top alternatives,
+// without the N x V logits:
+//
+//   z = X W^T / T,   lse_n = log sum_v exp z_nv,   logp_n = z_{n,t_n} - lse_n,
+//   H_n = -sum_v p_nv log p_nv = lse_n - sum_v p_nv z_nv,   p = exp(z - lse),
+//   and the K largest z_nv with their ids (equal values: the lowest id first).
+//
+// The tcgen05 GEMM (MODE_STATS) leaves per row and 128-column part the max m,
+// S = sum 2^d and D = sum d 2^d of d = (z - m) c2, c2 = log2(e)/T.  Two parts
+// merge at the larger max M with f = 2^((m - M) c2):
+//   S <- f S,   D <- f (D + (m - M) c2 S)      (d grows by (m - M) c2)
+// so that log2 sum = M c2 + log2 S and H = ln 2 (log2 S - D / S).
+//
+// Top alternatives: every one of a row's K best logits lies in one of its K
+// best parts (parts ordered by their max, equal ones by position: K better
+// parts each hold a better logit, an equal one having a lower id), so of the
+// fp32 logits of a chunk only K parts of 128 columns are read back per row.
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "flce.h"
+#include "flce_internal.h"
+#include "flce_ptx.cuh"
+#include "flce_topk.cuh"
+
+namespace flce {
+namespace {
+
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+
+__device__ __forceinline__ int chunk_rows(const int* hdr, long long c0, int C) {
+  const long long rem = static_cast<long long>(hdr[HDR_NVALID]) - c0;
+  return rem <= 0 ? 0 : (rem >= C ? C : static_cast<int>(rem));
+}
+
+// Chunk rows and their targets in a dense [C, H] tile source (rows up to the
+// next multiple of 128 are zero), with the constants of MODE_DZ:
+//   dz = (g ([v = t] - p) - e p (log p + H)) / T.
+__global__ void __launch_bounds__(128)
+    gather_dz_kernel(const uint16_t* __restrict__ X, const int* __restrict__ t, const int* hdr,
+                     const int* __restrict__ idx, long long c0, int C, int H, float temperature,
+                     const float* __restrict__ lse, const float* __restrict__ entropy,
+                     const float* __restrict__ grad_logp, const float* __restrict__ grad_entropy,
+                     uint16_t* __restrict__ xc, int* __restrict__ tc, DzRow* __restrict__ rowc) {
+  const int r = blockIdx.x;
+  const int Cl = chunk_rows(hdr, c0, C);
+  if (r >= min(C, (Cl + BM - 1) / BM * BM)) return;
+  uint4* dst = reinterpret_cast<uint4*>(xc + static_cast<size_t>(r) * H);
+  const int n16 = H / 8;
+  if (r >= Cl) {
+    for (int c = threadIdx.x; c < n16; c += blockDim.x) dst[c] = make_uint4(0u, 0u, 0u, 0u);
+    if (threadIdx.x == 0) {
+      tc[r] = -1;
+      rowc[r] = DzRow{0.f, 0.f, 0.f, 0.f};
+    }
+    return;
+  }
+  const long long row = idx[c0 + r];
+  const uint4* src = reinterpret_cast<const uint4*>(X + row * H);
+  for (int c = threadIdx.x; c < n16; c += blockDim.x) dst[c] = src[c];
+  if (threadIdx.x == 0) {
+    const float it = 1.f / temperature;
+    const float g = grad_logp ? grad_logp[row] : 0.f;
+    const float e = grad_entropy ? grad_entropy[row] : 0.f;
+    tc[r] = t[row];
+    rowc[r] = DzRow{lse[row] * LOG2E, -it * (grad_entropy ? fmaf(e, entropy[row], g) : g), -it * LN2 * e, it * g};
+  }
+}
+
+// Running statistics of a set of logits, in units of log2 (see above).
+struct Stat {
+  float m, s, d;   // max (raw), sum 2^x, sum x 2^x with x = (z - m) c2
+};
+
+__device__ __forceinline__ Stat merge(const Stat& a, const Stat& b, float c2) {
+  Stat r;
+  r.m = fmaxf(a.m, b.m);
+  // a side whose max is -inf holds nothing: its factor is 0 (the clamp also
+  // turns -inf - -inf into it)
+  const float xa = fmaxf((a.m - r.m) * c2, -1e20f), xb = fmaxf((b.m - r.m) * c2, -1e20f);
+  const float fa = ptx::ex2(xa), fb = ptx::ex2(xb);
+  r.s = fa * a.s + fb * b.s;
+  r.d = fa * fmaf(xa, a.s, a.d) + fb * fmaf(xb, b.s, b.d);
+  return r;
+}
+
+// One chunk's rows: lane = row (part-major statistics: coalesced), the parts
+// dealt to the block's warps and merged in a fixed order.  Reads 12 bytes per
+// row and part.
+constexpr int ROWS_WARPS = 8;
+__global__ void __launch_bounds__(32 * ROWS_WARPS)
+    logprob_rows_kernel(const int* hdr, const int* __restrict__ idx, long long c0, int C, int nparts,
+                        const float* __restrict__ stats, const float* __restrict__ zt, float c2,
+                        float* __restrict__ logp, float* __restrict__ entropy, float* __restrict__ lse,
+                        float2* __restrict__ ml) {
+  __shared__ Stat part[ROWS_WARPS][32];
+  const int Cl = chunk_rows(hdr, c0, C);
+  const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+  const int r = blockIdx.x * 32 + lane;
+  if (blockIdx.x * 32 >= Cl) return;
+  Stat acc = {-INFINITY, 0.f, 0.f};
+  if (r < Cl) {
+    const size_t np = static_cast<size_t>(nparts) * C;
+#pragma unroll 4
+    for (int p = w; p < nparts; p += ROWS_WARPS) {
+      const float* q = stats + static_cast<size_t>(p) * C + r;
+      acc = merge(acc, Stat{q[0], q[np], q[2 * np]}, c2);
+    }
+  }
+  part[w][lane] = acc;
+  __syncthreads();
+  if (w != 0 || r >= Cl) return;
+#pragma unroll
+  for (int k = 1; k < ROWS_WARPS; ++k) acc = merge(acc, part[k][lane], c2);
+  // after a pipeline time-out the statistics are not to be trusted
+  if (hdr[HDR_STATUS] & STATUS_TIMEOUT) acc.m = __int_as_float(0x7fc00000);
+  const float l2s = log2f(acc.s);
+  const long long row = idx[c0 + r];
+  logp[row] = fmaf(zt[r] - acc.m, c2, -l2s) * LN2;
+  lse[row] = fmaf(acc.m, c2, l2s) * LN2;
+  if (entropy) entropy[row] = fmaf(0.f, acc.m, l2s - acc.d / acc.s) * LN2;   // NaN where the max is not finite
+  if (ml) ml[r] = make_float2(acc.m, l2s);
+}
+
+// Rows left out: 0 for an ignored token, NaN for a target outside [0, V).
+__global__ void logprob_left_out_kernel(const int* hdr, const int* __restrict__ idx, const int* __restrict__ t,
+                                        long long N, int ii, int K, float* logp, float* entropy, float* lse,
+                                        int* top_ids, float* top_logp) {
+  for (long long i = hdr[HDR_NVALID] + static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < N;
+       i += static_cast<long long>(gridDim.x) * blockDim.x) {
+    const long long row = idx[i];
+    const float v = t[row] == ii ? 0.f : __int_as_float(0x7fc00000);
+    logp[row] = v;
+    lse[row] = v;
+    if (entropy) entropy[row] = v;
+    for (int k = 0; k < K; ++k) {
+      top_ids[row * K + k] = -1;
+      top_logp[row * K + k] = v;
+    }
+  }
+}
+
+// Top alternatives of one row per block: the K best parts by (max, position),
+// then the K best of their logits by (value, id).
+constexpr int TOP_WARPS = 4;
+__global__ void __launch_bounds__(32 * TOP_WARPS)
+    logprob_top_kernel(const int* hdr, const int* __restrict__ idx, long long c0, int C, int V, long long ldz,
+                       int nparts, int K, const float* __restrict__ stats, const float* __restrict__ zf,
+                       const float2* __restrict__ ml, float c2, int* __restrict__ top_ids,
+                       float* __restrict__ top_logp) {
+  __shared__ float sv[TOP_WARPS][32];
+  __shared__ int si[TOP_WARPS][32];
+  const int r = blockIdx.x;
+  if (r >= chunk_rows(hdr, c0, C)) return;
+  const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+  TopK best;
+  best.clear();
+  for (int p0 = w * 32; p0 < nparts; p0 += TOP_WARPS * 32) {
+    const int p = p0 + lane;
+    best.offer(p < nparts ? stats[static_cast<size_t>(p) * C + r] : 0.f, p, p < nparts, K, lane);
+  }
+  best.merge_block<TOP_WARPS>(sv, si, K, lane, w);   // every warp holds the K best parts
+  const int parts = best.id;
+  best.clear();
+  const float* zr = zf + static_cast<size_t>(r) * ldz;
+  for (int j = w; j < K; j += TOP_WARPS) {
+    const int p = __shfl_sync(0xffffffffu, parts, j);
+    if (p == TopK::NONE) continue;
+#pragma unroll
+    for (int g = 0; g < PART_COLS / 32; ++g) {
+      const long long v = static_cast<long long>(p) * PART_COLS + g * 32 + lane;
+      best.offer(v < V ? zr[v] : 0.f, static_cast<int>(v), v < V, K, lane);
+    }
+  }
+  best.merge_block<TOP_WARPS>(sv, si, K, lane, w);
+  if (w == 0 && lane < K) {
+    const long long row = idx[c0 + r];
+    const bool some = best.id != TopK::NONE;   // false only where fewer than K logits are numbers
+    top_ids[row * K + lane] = some ? best.id : -1;
+    top_logp[row * K + lane] = some ? fmaf(best.v - ml[r].x, c2, -ml[r].y) * LN2 : __int_as_float(0x7fc00000);
+  }
+}
+
+// The gradients of a call whose pipeline timed out begin with a NaN, so that a
+// caller who never reads the status still sees that they are not to be trusted.
+__global__ void mark_failed_kernel(const int* hdr, uint16_t* grad_hidden, float* grad_weight, int gw_bf16) {
+  if (!(hdr[HDR_STATUS] & STATUS_TIMEOUT)) return;
+  if (grad_hidden) grad_hidden[0] = 0x7fc0;
+  if (grad_weight && gw_bf16) reinterpret_cast<uint16_t*>(grad_weight)[0] = 0x7fc0;
+  else if (grad_weight) grad_weight[0] = __int_as_float(0x7fc00000);
+}
+
+// ---------------------------------------------------------------------------
+// workspace of the forward
+// ---------------------------------------------------------------------------
+struct LpPlan {
+  long long C = 0, n_chunks = 0, ldz = 0;
+  int nvt = 0, nparts = 0;
+  size_t o_idx = 0, o_cnt = 0, o_xc = 0, o_tc = 0, o_zt = 0, o_ml = 0, o_stats = 0, o_zf = 0, total = 0;
+};
+
+LpPlan lp_layout(long long N, long long H, long long V, long long C, int K) {
+  LpPlan p;
+  p.C = C;
+  p.n_chunks = cdiv(N, C);
+  p.ldz = cdiv(V, 64) * 64;
+  p.nvt = static_cast<int>(cdiv(V, BN));
+  p.nparts = static_cast<int>(cdiv(V, PART_COLS));
+  size_t off = al256(HDR_WORDS * sizeof(int));
+  auto take = [&off](size_t bytes) {
+    const size_t o = off;
+    off += al256(bytes);
+    return o;
+  };
+  p.o_idx = take(size_t(N) * 4);
+  p.o_cnt = take(size_t(p.n_chunks) * 4);
+  p.o_xc = take(size_t(C) * H * 2);
+  p.o_tc = take(size_t(C) * 4);
+  p.o_zt = take(size_t(C) * 4);
+  p.o_ml = take(size_t(C) * 8);
+  p.o_stats = take(size_t(C) * p.nparts * 12);
+  if (K > 0) p.o_zf = take(size_t(C) * p.ldz * 4);
+  p.total = off;
+  return p;
+}
+
+// Largest chunk (a multiple of 128 rows) whose plan fits in `bytes`.
+bool lp_plan(long long N, long long H, long long V, int K, size_t bytes, LpPlan* out) {
+  long long lo = 1, hi = cdiv(N, BM);
+  if (lp_layout(N, H, V, BM, K).total > bytes) return false;
+  while (lo < hi) {
+    const long long mid = (lo + hi + 1) / 2;
+    if (lp_layout(N, H, V, mid * BM, K).total <= bytes) lo = mid;
+    else hi = mid - 1;
+  }
+  *out = lp_layout(N, H, V, lo * BM, K);
+  return true;
+}
+
+// Default workspace: 5% of the bf16 logits as for the loss, but no less than
+// what lets small problems run in one chunk (64 MiB; 256 MiB with the fp32
+// logits of top alternatives, whose chunks would else be too short to feed the
+// tensor cores between two readings of the weight).
+size_t lp_default_bytes(long long N, long long H, long long V, int K) {
+  if (!sizes_ok(N, H, V) || K < 0 || K > TopK::MAX || K > V) return 0;
+  const size_t budget = std::max(size_t(N) * size_t(V) * 2 / 20, size_t(K > 0 ? 256 : 64) << 20);
+  LpPlan p;
+  if (lp_plan(N, H, V, K, budget, &p)) return p.total;
+  return lp_layout(N, H, V, BM, K).total;
+}
+
+}  // namespace
+
+bool bad_temperature(float t) { return !(t > 0.f) || !std::isfinite(t) || !std::isfinite(LOG2E / t); }
+
+cudaError_t launch_mark_failed(const int* hdr, uint16_t* grad_hidden, float* grad_weight, int gw_bf16,
+                               cudaStream_t s) {
+  mark_failed_kernel<<<1, 1, 0, s>>>(hdr, grad_hidden, grad_weight, gw_bf16);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gather_dz(const uint16_t* hidden, const int* targets, const int* hdr, const int* idx, long long c0,
+                             int C, int H, float temperature, const float* lse, const float* entropy,
+                             const float* grad_logp, const float* grad_entropy, uint16_t* xc, int* tc, DzRow* rowc,
+                             cudaStream_t s) {
+  gather_dz_kernel<<<C, 128, 0, s>>>(hidden, targets, hdr, idx, c0, C, H, temperature, lse, entropy, grad_logp,
+                                     grad_entropy, xc, tc, rowc);
+  return cudaGetLastError();
+}
+
+}  // namespace flce
+
+using namespace flce;
+
+extern "C" {
+
+size_t flce_logprobs_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t top_k) {
+  return lp_default_bytes(N, H, V, top_k);
+}
+
+flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t* targets, int64_t N, int64_t H,
+                          int64_t V, int32_t ignore_index, float temperature, int32_t top_k, float* logp,
+                          float* entropy, float* lse, int32_t* top_ids, float* top_logp, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  if (!hidden || !weight || !targets || !logp || !lse || !workspace) return FLCE_EINVAL;
+  if (N < 1 || H < 1 || V < 1 || top_k < 0 || top_k > V || bad_temperature(temperature)) return FLCE_EINVAL;
+  if (top_k > 0 && (!top_ids || !top_logp)) return FLCE_EINVAL;
+  if (!sizes_ok(N, H, V) || top_k > TopK::MAX) return FLCE_EUNSUPPORTED;
+  if (!aligned16(hidden) || !aligned16(weight) || !aligned16(workspace) || !aligned4(targets) || !aligned4(logp) ||
+      !aligned4(entropy) || !aligned4(lse) || !aligned4(top_ids) || !aligned4(top_logp))
+    return FLCE_EUNSUPPORTED;
+  DeviceState dev;
+  if (device_state(&dev) != cudaSuccess) { cudaGetLastError(); return FLCE_ECUDA; }
+  if (dev.major < 10) return FLCE_EUNSUPPORTED;
+  LpPlan p;
+  if (!lp_plan(N, H, V, top_k, workspace_bytes, &p)) return FLCE_EWORKSPACE;
+
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int* hdr = at<int>(workspace, 0);
+  int* idx = at<int>(workspace, p.o_idx);
+  int* counters = at<int>(workspace, p.o_cnt);
+  uint16_t* xc = at<uint16_t>(workspace, p.o_xc);
+  int* tc = at<int>(workspace, p.o_tc);
+  float* zt = at<float>(workspace, p.o_zt);
+  float2* ml = at<float2>(workspace, p.o_ml);
+  float* stats = at<float>(workspace, p.o_stats);
+  float* zf = top_k > 0 ? at<float>(workspace, p.o_zf) : nullptr;
+
+  GemmMaps m;
+  std::memset(&m, 0, sizeof(m));
+  const unsigned long long hb = static_cast<unsigned long long>(H) * 2;
+  if (!make_map(&m.a0, xc, H, p.C, hb, BK, BM) || !make_map(&m.b0, weight, H, V, hb, BK, BN / 2)) return FLCE_ECUDA;
+
+  GemmArgs g;
+  std::memset(&g, 0, sizeof(g));
+  g.mode = MODE_STATS;
+  g.hdr = hdr;
+  g.status = hdr + HDR_STATUS;
+  g.C = static_cast<int>(p.C);
+  g.H = static_cast<int>(H);
+  g.V = static_cast<int>(V);
+  g.ldz = p.ldz;
+  g.nvt = p.nvt;
+  g.nparts = p.nparts;
+  g.timeout_ns = wait_timeout_ns();
+  g.tc = tc;
+  g.zt = zt;
+  g.stats = stats;
+  g.zf = zf;
+  g.c2 = LOG2E / temperature;
+
+  const int grid = 2 * static_cast<int>(std::min<long long>(cdiv(p.C, PAIR_M) * p.nvt, dev.pairs));
+  auto chk = [](cudaError_t e) { return e == cudaSuccess; };
+  count_launches(2 + p.n_chunks * (top_k > 0 ? 3 : 2));
+  if (!chk(launch_prep(targets, N, static_cast<int>(V), ignore_index, hdr, idx, nullptr, counters, p.n_chunks, st)))
+    return FLCE_ECUDA;
+  logprob_left_out_kernel<<<static_cast<int>(std::min<long long>(cdiv(N, 256), 1216)), 256, 0, st>>>(
+      hdr, idx, targets, N, ignore_index, top_k, logp, entropy, lse, top_ids, top_logp);
+  if (!chk(cudaGetLastError())) return FLCE_ECUDA;
+  for (long long c = 0; c < p.n_chunks; ++c) {
+    g.c0 = c * p.C;
+    g.counter = counters + c;
+    if (!chk(launch_gather(static_cast<const uint16_t*>(hidden), targets, hdr, idx, g.c0, g.C, g.H, xc, tc, 0, g.V,
+                           st)) ||
+        !chk(gemm_launch(g, m, grid, st)))
+      return FLCE_ECUDA;
+    logprob_rows_kernel<<<static_cast<int>(cdiv(p.C, 32)), 32 * ROWS_WARPS, 0, st>>>(
+        hdr, idx, g.c0, g.C, p.nparts, stats, zt, g.c2, logp, entropy, lse, top_k > 0 ? ml : nullptr);
+    if (!chk(cudaGetLastError())) return FLCE_ECUDA;
+    if (top_k > 0) {
+      logprob_top_kernel<<<g.C, 32 * TOP_WARPS, 0, st>>>(hdr, idx, g.c0, g.C, g.V, p.ldz, p.nparts, top_k, stats, zf,
+                                                         ml, g.c2, top_ids, top_logp);
+      if (!chk(cudaGetLastError())) return FLCE_ECUDA;
+    }
+  }
+  return FLCE_OK;
+}
+
+}  // extern "C"

@@ -9,6 +9,7 @@ call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -86,6 +87,15 @@ def library() -> ctypes.CDLL:
     lib.flce_vocab_finish.restype = ctypes.c_int
     lib.flce_vocab_shard_bwd.argtypes = [vp, vp, vp, i64, i64, i64, i64, i64, i32, u32, vp, vp, vp, vp, sz, vp]
     lib.flce_vocab_shard_bwd.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    lib.flce_logprobs_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    lib.flce_logprobs_workspace_bytes.restype = sz
+    lib.flce_logprobs.argtypes = [vp, vp, vp, i64, i64, i64, i32, f32, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.flce_logprobs.restype = ctypes.c_int
+    lib.flce_logprobs_bwd_workspace_bytes.argtypes = [i64, i64, i64, u32]
+    lib.flce_logprobs_bwd_workspace_bytes.restype = sz
+    lib.flce_logprobs_bwd.argtypes = [vp, vp, vp, i64, i64, i64, i32, u32, f32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.flce_logprobs_bwd.restype = ctypes.c_int
     lib.flce_scale_grads.argtypes = [vp, vp, i64, i64, i64, vp, vp]
     lib.flce_scale_grads.restype = ctypes.c_int
     lib.flce_profile_begin.argtypes = []
@@ -378,6 +388,181 @@ class LinearCrossEntropy(torch.nn.Module):
         return linear_cross_entropy(hidden, self.weight, targets, self.ignore_index, self.reduction)
 
 
+# ---------------------------------------------------------------------------
+# token log probabilities, with entropy and top alternatives
+# ---------------------------------------------------------------------------
+
+TOP_K_MAX = 32
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """The device and stream of a call: outputs and workspaces allocated inside
+    belong to that stream, so their memory is reused only behind its work."""
+    with torch.cuda.device(device):
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        elif not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        with torch.cuda.stream(stream):
+            yield ctypes.c_void_p(stream.cuda_stream)
+
+
+def _check_buffer(t, name, shape, dtype, device):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a {dtype} tensor")
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be contiguous, of shape {tuple(shape)}, on {device}")
+
+
+def _outputs(out, specs, device) -> dict:
+    """The caller's output dict, checked, or new tensors; a spec of None is not produced."""
+    o = out if out is not None else {}
+    for name, spec in specs.items():
+        if spec is None:
+            o[name] = None
+        elif o.get(name) is None:
+            o[name] = torch.empty(spec[0], dtype=spec[1], device=device)
+        else:
+            _check_buffer(o[name], name, spec[0], spec[1], device)
+    return o
+
+
+def _check_same_device(*tensors):
+    dev = tensors[0].device
+    for t in tensors[1:]:
+        if t.device != dev:
+            raise ValueError("all tensors must be on one device")
+    return dev
+
+
+def _check_workspace(workspace, device):
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+
+
+def token_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100, *,
+                   temperature: float = 1.0, top_k: int = 0, entropy: bool = True,
+                   workspace: Optional[torch.Tensor] = None, out: Optional[dict] = None, stream=None) -> dict:
+    """Log probabilities of the given tokens under ``softmax(hidden @ weight.T / temperature)``.
+
+    Returns fp32 [N] ``logp``, ``lse`` and (unless ``entropy=False``) ``entropy``;
+    with ``top_k`` > 0 also ``top_ids`` (int32 [N, top_k]) and ``top_logp`` (fp32),
+    best first, equal logits by the lower id.  Rows whose target is
+    ``ignore_index`` hold 0 (ids -1); rows whose target lies outside [0, V) hold
+    NaN and set the status word."""
+    N, H, V = _check_inputs(hidden, weight, targets)
+    dev = _check_same_device(hidden, weight, targets)
+    top_k = int(top_k)
+    if not 0 <= top_k <= min(TOP_K_MAX, V):
+        raise ValueError(f"top_k must lie in [0, {min(TOP_K_MAX, V)}]")
+    with _on(dev, stream) as st:
+        if workspace is None:
+            nb = library().flce_logprobs_workspace_bytes(N, H, V, top_k)
+            if nb == 0:
+                raise FlceError(FLCE_EINVAL, "workspace size")
+            workspace = new_workspace(nb, dev)
+        _check_workspace(workspace, dev)
+        row = ((N,), torch.float32)
+        o = _outputs(out, {"logp": row, "lse": row, "entropy": row if entropy else None,
+                           "top_ids": ((N, top_k), torch.int32) if top_k else None,
+                           "top_logp": ((N, top_k), torch.float32) if top_k else None}, dev)
+        _ok(library().flce_logprobs(_ptr(hidden), _ptr(weight), _ptr(targets), N, H, V, int(ignore_index),
+                                    float(temperature), top_k, _ptr(o["logp"]), _ptr(o["entropy"]), _ptr(o["lse"]),
+                                    _ptr(o["top_ids"]), _ptr(o["top_logp"]), _ptr(workspace), workspace.numel(), st),
+            "flce_logprobs")
+    o["workspace"] = workspace
+    return o
+
+
+def token_logprobs_bwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                       entropy: Optional[torch.Tensor], grad_logp: Optional[torch.Tensor],
+                       grad_entropy: Optional[torch.Tensor] = None, ignore_index: int = -100, *,
+                       temperature: float = 1.0, grad_weight_dtype=torch.float32, need_hidden: bool = True,
+                       need_weight: bool = True, workspace: Optional[torch.Tensor] = None,
+                       out: Optional[dict] = None, stream=None) -> dict:
+    """Gradients of ``sum(grad_logp * logp + grad_entropy * entropy)``.
+
+    ``lse`` and ``entropy`` are those of :func:`token_logprobs` on the same
+    inputs (``entropy`` may be None without ``grad_entropy``).  Returns
+    ``grad_hidden`` (bf16 [N, H]) and ``grad_weight`` ([V, H], fp32 or bf16), or
+    only the one asked for: a frozen head or a frozen trunk saves its product."""
+    N, H, V = _check_inputs(hidden, weight, targets)
+    dev = _check_same_device(hidden, weight, targets)
+    if not (need_hidden or need_weight):
+        raise ValueError("need_hidden or need_weight must be set")
+    if grad_logp is None and grad_entropy is None:
+        raise ValueError("grad_logp or grad_entropy must be given")
+    if grad_entropy is not None and entropy is None:
+        raise ValueError("grad_entropy needs the entropy")
+    for name, t in (("lse", lse), ("entropy", entropy), ("grad_logp", grad_logp), ("grad_entropy", grad_entropy)):
+        if t is not None or name == "lse":
+            _check_buffer(t, name, (N,), torch.float32, dev)
+    flags = _flags("mean", grad_weight_dtype) if need_weight else 0
+    with _on(dev, stream) as st:
+        if workspace is None:
+            nb = library().flce_logprobs_bwd_workspace_bytes(N, H, V, flags)
+            if nb == 0:
+                raise FlceError(FLCE_EINVAL, "workspace size")
+            workspace = new_workspace(nb, dev)
+        _check_workspace(workspace, dev)
+        o = _outputs(out, {"grad_hidden": ((N, H), torch.bfloat16) if need_hidden else None,
+                           "grad_weight": ((V, H), grad_weight_dtype) if need_weight else None}, dev)
+        _ok(library().flce_logprobs_bwd(_ptr(hidden), _ptr(weight), _ptr(targets), N, H, V, int(ignore_index), flags,
+                                        float(temperature), _ptr(lse), _ptr(entropy), _ptr(grad_logp),
+                                        _ptr(grad_entropy), _ptr(o["grad_hidden"]), _ptr(o["grad_weight"]),
+                                        _ptr(workspace), workspace.numel(), st), "flce_logprobs_bwd")
+    o["workspace"] = workspace
+    return o
+
+
+class _LinearLogProbsFn(torch.autograd.Function):
+    """The backward recomputes the logits chunk by chunk from the saved log-sum-exp."""
+
+    @staticmethod
+    def forward(ctx, hidden, weight, targets, ignore_index, temperature):
+        hidden, weight, targets = hidden.contiguous(), weight.contiguous(), targets.contiguous()
+        o = token_logprobs(hidden, weight, targets, ignore_index, temperature=temperature)
+        ctx.save_for_backward(hidden, weight, targets, o["lse"], o["entropy"])
+        ctx.args = (ignore_index, temperature)
+        ctx.set_materialize_grads(False)
+        return o["logp"], o["entropy"]
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_logp, grad_entropy):
+        need_hidden, need_weight = ctx.needs_input_grad[:2]
+        if not (need_hidden or need_weight) or (grad_logp is None and grad_entropy is None):
+            return None, None, None, None, None
+        hidden, weight, targets, lse, entropy = ctx.saved_tensors
+        ignore_index, temperature = ctx.args
+        gl = None if grad_logp is None else grad_logp.to(torch.float32).contiguous()
+        ge = None if grad_entropy is None else grad_entropy.to(torch.float32).contiguous()
+        o = token_logprobs_bwd(hidden, weight, targets, lse, entropy, gl, ge, ignore_index, temperature=temperature,
+                               grad_weight_dtype=weight.dtype, need_hidden=need_hidden, need_weight=need_weight)
+        return o["grad_hidden"], o["grad_weight"], None, None, None
+
+
+def linear_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
+                    temperature: float = 1.0):
+    """``(logp, entropy)`` of the given tokens at the LM head, fp32 [N] each, with
+    autograd support: the head of a policy-gradient or preference loss."""
+    return _LinearLogProbsFn.apply(hidden, weight, targets, ignore_index, temperature)
+
+
+class LinearLogProbs(torch.nn.Module):
+    """LM head as token log probabilities: ``logp, entropy = module(hidden, targets)``."""
+
+    def __init__(self, weight: torch.Tensor, ignore_index: int = -100, temperature: float = 1.0):
+        super().__init__()
+        self.weight = torch.nn.Parameter(weight)
+        self.ignore_index = ignore_index
+        self.temperature = temperature
+
+    def forward(self, hidden: torch.Tensor, targets: torch.Tensor):
+        return linear_logprobs(hidden, self.weight, targets, self.ignore_index, self.temperature)
+
+
 def query_status(workspace: torch.Tensor, stream=None) -> int:
     """Synchronise the stream and return the device status of the last call."""
     return int(library().flce_query_status(_ptr(workspace), _stream(stream)))
@@ -416,7 +601,7 @@ def profile_end() -> dict:
     s = library().flce_profile_end(ms, n, ctypes.byref(total))
     if s != FLCE_OK:
         raise FlceError(s, "flce_profile_end")
-    names = ("logits", "backward", "unused")
+    names = ("logits", "backward", "logprobs")
     return {"gemm_ms": dict(zip(names, list(ms))), "gemm_launches": dict(zip(names, list(n))),
             "kernel_launches": int(total.value)}
 
