@@ -245,7 +245,7 @@ flce_status flce_vocab_shard_bwd(const void* hidden, const void* weight_shard,
  * pipeline time-out (FLCE_ETIMEOUT) every scored row is NaN.
  * The N x V logits are not kept: the workspace (flce_logprobs_workspace_bytes;
  * less runs in smaller chunks, down to 128 rows) stays below 5% of their bf16
- * size, or 64 MiB (256 MiB with top alternatives) where that is more.
+ * size, or 64 MiB (1 GiB with top alternatives) where that is more.
  * 0 < temperature < inf.  Sizes, alignment, streams and errors as flce_fwd_bwd;
  * top_k > V is FLCE_EINVAL, top_k > 32 FLCE_EUNSUPPORTED.
  */
@@ -268,6 +268,9 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
  * the fp32 accumulator, and the sums over it are kept in fp32, in a fixed order.
  * Targets outside [0, V) are treated as ignored (FLCE_EBADTARGET in the status
  * word); after a time-out the first element of each gradient is NaN.
+ * Workspace: flce_logprobs_bwd_workspace_bytes (5% of the bf16 logits, or 1 GiB
+ * where that is more and the problem needs it; plus V*H*4 bytes with
+ * FLCE_GW_BF16); less runs in smaller chunks.
  */
 size_t flce_logprobs_bwd_workspace_bytes(int64_t N, int64_t H, int64_t V, uint32_t flags);
 flce_status flce_logprobs_bwd(const void* hidden, const void* weight, const int32_t* targets,
@@ -277,6 +280,36 @@ flce_status flce_logprobs_bwd(const void* hidden, const void* weight, const int3
                               const float* grad_entropy, void* grad_hidden,
                               float* grad_weight, void* workspace, size_t workspace_bytes,
                               void* stream);
+
+/*
+ * Scaled embedding lookup, the other reader of a tied [V,H] weight:
+ *   out[n] = scale * weight[ids[n]]      (fp32 product, rounded once to dtype)
+ * weight [V,H] and out [N,H] are of `dtype`; ids [N] int32.  A row whose id
+ * lies outside [0, V) is NaN.  No workspace.  H % 8 == 0, 16-byte alignment.
+ */
+#define FLCE_BF16 0
+#define FLCE_F16  1
+#define FLCE_F32  2
+flce_status flce_embedding(const void* weight, const int32_t* ids, int64_t N, int64_t H,
+                           int64_t V, int32_t dtype, float scale, void* out, void* stream);
+
+/*
+ * Its gradient, by sorted ids:
+ *   grad_weight[v] = scale * sum_{n : ids[n] = v} grad_out[n]
+ * summed in fp32 in a fixed order (repeated calls agree bit for bit), scaled,
+ * and rounded once to grad_dtype; rows of ids that do not occur are +0.0.  With
+ * FLCE_ACCUMULATE (fp32 grad_weight only) the sums are added to grad_weight and
+ * the other rows are neither read nor written: the gradient of a tied weight on
+ * top of the head's (flce_fwd_bwd, flce_logprobs_bwd).  Tokens whose id is
+ * padding_idx (< V; negative: none) add nothing; ids outside [0, V) add nothing
+ * and set FLCE_EBADTARGET in the status word.  N <= 2^30.
+ */
+#define FLCE_ACCUMULATE 0x4u
+size_t flce_embedding_bwd_workspace_bytes(int64_t N, int64_t H, int64_t V);
+flce_status flce_embedding_bwd(const void* grad_out, const int32_t* ids, int64_t N, int64_t H,
+                               int64_t V, int32_t dtype, float scale, int32_t padding_idx,
+                               uint32_t flags, void* grad_weight, int32_t grad_dtype,
+                               void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * grad_hidden (bf16 [N,H]) and grad_weight (fp32 [V,H]) multiplied in place by

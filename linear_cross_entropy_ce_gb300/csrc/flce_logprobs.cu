@@ -240,12 +240,11 @@ bool lp_plan(long long N, long long H, long long V, int K, size_t bytes, LpPlan*
 }
 
 // Default workspace: 5% of the bf16 logits as for the loss, but no less than
-// what lets small problems run in one chunk (64 MiB; 256 MiB with the fp32
-// logits of top alternatives, whose chunks would else be too short to feed the
-// tensor cores between two readings of the weight).
+// what lets problems of a few thousand tokens run in one chunk (64 MiB; 1 GiB
+// with the fp32 logits of top alternatives): every chunk reads the weight.
 size_t lp_default_bytes(long long N, long long H, long long V, int K) {
   if (!sizes_ok(N, H, V) || K < 0 || K > TopK::MAX || K > V) return 0;
-  const size_t budget = std::max(size_t(N) * size_t(V) * 2 / 20, size_t(K > 0 ? 256 : 64) << 20);
+  const size_t budget = std::max(size_t(N) * size_t(V) * 2 / 20, size_t(K > 0 ? 1024 : 64) << 20);
   LpPlan p;
   if (lp_plan(N, H, V, K, budget, &p)) return p.total;
   return lp_layout(N, H, V, BM, K).total;

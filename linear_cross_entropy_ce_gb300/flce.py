@@ -96,6 +96,12 @@ def library() -> ctypes.CDLL:
     lib.flce_logprobs_bwd_workspace_bytes.restype = sz
     lib.flce_logprobs_bwd.argtypes = [vp, vp, vp, i64, i64, i64, i32, u32, f32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.flce_logprobs_bwd.restype = ctypes.c_int
+    lib.flce_embedding.argtypes = [vp, vp, i64, i64, i64, i32, f32, vp, vp]
+    lib.flce_embedding.restype = ctypes.c_int
+    lib.flce_embedding_bwd_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.flce_embedding_bwd_workspace_bytes.restype = sz
+    lib.flce_embedding_bwd.argtypes = [vp, vp, i64, i64, i64, i32, f32, i32, u32, vp, i32, vp, sz, vp]
+    lib.flce_embedding_bwd.restype = ctypes.c_int
     lib.flce_scale_grads.argtypes = [vp, vp, i64, i64, i64, vp, vp]
     lib.flce_scale_grads.restype = ctypes.c_int
     lib.flce_profile_begin.argtypes = []
@@ -551,16 +557,134 @@ def linear_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.T
 
 
 class LinearLogProbs(torch.nn.Module):
-    """LM head as token log probabilities: ``logp, entropy = module(hidden, targets)``."""
+    """LM head as token log probabilities: ``logp, entropy = module(hidden, targets)``;
+    the weight may be an embedding's (tied)."""
 
     def __init__(self, weight: torch.Tensor, ignore_index: int = -100, temperature: float = 1.0):
         super().__init__()
-        self.weight = torch.nn.Parameter(weight)
+        self.weight = weight if isinstance(weight, torch.nn.Parameter) else torch.nn.Parameter(weight)
         self.ignore_index = ignore_index
         self.temperature = temperature
 
     def forward(self, hidden: torch.Tensor, targets: torch.Tensor):
         return linear_logprobs(hidden, self.weight, targets, self.ignore_index, self.temperature)
+
+
+# ---------------------------------------------------------------------------
+# scaled embedding and its gradient
+# ---------------------------------------------------------------------------
+
+FLCE_ACCUMULATE = 0x4
+EMBEDDING_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _check_rows(t, name):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in EMBEDDING_DTYPES:
+        raise TypeError(f"{name} must be bfloat16, float16 or float32")
+    if t.dim() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous matrix")
+    return t.shape
+
+
+def _check_ids(ids):
+    if ids.dtype != torch.int32:
+        raise TypeError("ids must be int32")
+    if ids.dim() != 1 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous vector")
+    return ids.shape[0]
+
+
+def embedding_fwd(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *, out: Optional[torch.Tensor] = None,
+                  stream=None) -> torch.Tensor:
+    """``scale * weight[ids]``, rounded once to the weight's dtype; rows of ids outside [0, V) are NaN."""
+    V, H = _check_rows(weight, "weight")
+    N = _check_ids(ids)
+    dev = _check_same_device(weight, ids)
+    with _on(dev, stream) as st:
+        out = _outputs({"out": out}, {"out": ((N, H), weight.dtype)}, dev)["out"]
+        _ok(library().flce_embedding(_ptr(weight), _ptr(ids), N, H, V, EMBEDDING_DTYPES[weight.dtype], float(scale),
+                                     _ptr(out), st), "flce_embedding")
+    return out
+
+
+def embedding_bwd(grad_out: torch.Tensor, ids: torch.Tensor, num_rows: int, scale: float = 1.0,
+                  padding_idx: Optional[int] = None, *, grad_weight_dtype=torch.float32, accumulate: bool = False,
+                  workspace: Optional[torch.Tensor] = None, out: Optional[dict] = None, stream=None) -> dict:
+    """``grad_weight`` [num_rows, H] of :func:`embedding_fwd`, summed in fp32 in a fixed order.
+
+    With ``accumulate=True`` the sums are added to ``out["grad_weight"]`` (fp32)
+    in place, touching only the rows of ids that occur: the embedding's share of
+    a tied weight's gradient on top of the head's."""
+    N, H = _check_rows(grad_out, "grad_out")
+    if _check_ids(ids) != N:
+        raise ValueError("shape mismatch")
+    dev = _check_same_device(grad_out, ids)
+    V = int(num_rows)
+    if grad_weight_dtype not in EMBEDDING_DTYPES:
+        raise TypeError("grad_weight_dtype must be bfloat16, float16 or float32")
+    if padding_idx is not None and not 0 <= padding_idx < V:
+        raise ValueError("padding_idx must lie in [0, num_rows)")
+    if accumulate and (out is None or out.get("grad_weight") is None):
+        raise ValueError("accumulate needs out['grad_weight']")
+    if accumulate and grad_weight_dtype != torch.float32:
+        raise TypeError("accumulate needs a float32 grad_weight")
+    with _on(dev, stream) as st:
+        if workspace is None:
+            nb = library().flce_embedding_bwd_workspace_bytes(N, H, V)
+            if nb == 0:
+                raise FlceError(FLCE_EINVAL, "workspace size")
+            workspace = new_workspace(nb, dev)
+        _check_workspace(workspace, dev)
+        o = _outputs(out, {"grad_weight": ((V, H), grad_weight_dtype)}, dev)
+        _ok(library().flce_embedding_bwd(_ptr(grad_out), _ptr(ids), N, H, V, EMBEDDING_DTYPES[grad_out.dtype],
+                                         float(scale), -1 if padding_idx is None else int(padding_idx),
+                                         FLCE_ACCUMULATE if accumulate else 0, _ptr(o["grad_weight"]),
+                                         EMBEDDING_DTYPES[grad_weight_dtype], _ptr(workspace), workspace.numel(), st),
+            "flce_embedding_bwd")
+    o["workspace"] = workspace
+    return o
+
+
+class _EmbeddingFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, weight, ids, scale, padding_idx):
+        ids = ids.contiguous()
+        ctx.save_for_backward(ids)
+        ctx.args = (weight.shape[0], weight.dtype, scale, padding_idx)
+        return embedding_fwd(weight.contiguous(), ids, scale)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_out):
+        if not ctx.needs_input_grad[0]:
+            return None, None, None, None
+        V, dtype, scale, padding_idx = ctx.args
+        o = embedding_bwd(grad_out.contiguous(), ctx.saved_tensors[0], V, scale, padding_idx, grad_weight_dtype=dtype)
+        return o["grad_weight"], None, None, None
+
+
+def embedding(ids: torch.Tensor, weight: torch.Tensor, scale: float = 1.0,
+              padding_idx: Optional[int] = None) -> torch.Tensor:
+    """``scale * weight[ids]`` for int32 ids [N], with autograd support; tokens whose
+    id is ``padding_idx`` are looked up but add nothing to the gradient."""
+    if padding_idx is not None and not 0 <= padding_idx < weight.shape[0]:
+        raise ValueError("padding_idx must lie in [0, V)")
+    return _EmbeddingFn.apply(weight, ids, scale, padding_idx)
+
+
+class ScaledEmbedding(torch.nn.Module):
+    """Token embedding ``scale * weight[ids]``; the weight may be an LM head's (tied)."""
+
+    def __init__(self, weight: torch.Tensor, scale: float = 1.0, padding_idx: Optional[int] = None):
+        super().__init__()
+        self.weight = weight if isinstance(weight, torch.nn.Parameter) else torch.nn.Parameter(weight)
+        self.scale = scale
+        self.padding_idx = padding_idx
+
+    def forward(self, ids: torch.Tensor) -> torch.Tensor:
+        return embedding(ids, self.weight, self.scale, self.padding_idx)
 
 
 def query_status(workspace: torch.Tensor, stream=None) -> int:
