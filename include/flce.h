@@ -246,7 +246,7 @@ flce_status flce_vocab_shard_bwd(const void* hidden, const void* weight_shard,
  * The N x V logits are not kept: the workspace (flce_logprobs_workspace_bytes;
  * less runs in smaller chunks, down to 128 rows) stays below 5% of their bf16
  * size, or 64 MiB (1 GiB with top alternatives) where that is more.
- * 0 < temperature < inf.  Sizes, alignment, streams and errors as flce_fwd_bwd;
+ * 0 < temperature < inf.  V <= 2^31 - 512; other sizes, alignment, streams and errors as flce_fwd_bwd;
  * top_k > V is FLCE_EINVAL, top_k > 32 FLCE_EUNSUPPORTED.
  */
 size_t flce_logprobs_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t top_k);

@@ -63,6 +63,7 @@ cudaError_t device_state(DeviceState* out) {
     if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&d.major, cudaDevAttrComputeCapabilityMajor, dev)) != cudaSuccess) return e;
     if ((e = gemm_prepare(dev)) != cudaSuccess) return e;
+    if ((e = stream_prepare()) != cudaSuccess) return e;
     if ((e = gemm_max_pairs(&d.pairs)) != cudaSuccess) return e;
     if (d.pairs < 1) return cudaErrorInvalidConfiguration;
     d.ready = true;
@@ -203,6 +204,13 @@ bool plan_for_bytes(long long N, long long H, long long V, bool fwd_only, size_t
 }  // namespace
 
 namespace flce {
+int device_sms() {
+  DeviceState d;
+  if (device_state(&d) == cudaSuccess) return d.sms;
+  cudaGetLastError();
+  return 2 * DEFAULT_PAIRS;
+}
+
 int device_pairs() {
   DeviceState d;
   if (device_state(&d) == cudaSuccess) return d.pairs;
@@ -300,25 +308,40 @@ std::atomic<unsigned long long> g_stall_armed{0};
 }  // namespace
 
 namespace flce {
+unsigned long long take_armed_stall() { return g_stall_armed.exchange(0); }
+
+ProfScope prof_launch_begin(cudaStream_t st) {
+  ProfScope r;
+  Profiler& p = prof();
+  std::lock_guard<std::mutex> lk(p.mu);
+  r.on = p.on;
+  if (r.on) {
+    r.start = prof_event();
+    r.stop = prof_event();
+    if (r.start) cudaEventRecord(r.start, st);
+  }
+  return r;
+}
+
+void prof_launch_end(const ProfScope& r, int mode, cudaStream_t st) {
+  if (!r.on) return;
+  Profiler& p = prof();
+  std::lock_guard<std::mutex> lk(p.mu);
+  if (r.stop) cudaEventRecord(r.stop, st);
+  if (r.start && r.stop) p.recs.push_back(ProfRecord{mode, r.start, r.stop});
+  ++p.launches;
+}
+
 // Launch a GEMM, bracketed by events when profiling is on.
 cudaError_t gemm_launch(const GemmArgs& g0, const GemmMaps& m, int grid, cudaStream_t st) {
   GemmArgs g = g0;
-  if (const unsigned long long t = g_stall_armed.exchange(0)) {
+  if (const unsigned long long t = take_armed_stall()) {
     g.debug_stall = 1;
     g.timeout_ns = t;
   }
-  Profiler& p = prof();
-  std::unique_lock<std::mutex> lk(p.mu);
-  if (!p.on) {
-    lk.unlock();
-    return launch_gemm(g, m, grid, st);
-  }
-  ProfRecord r{g.mode, prof_event(), prof_event()};
-  if (r.start) cudaEventRecord(r.start, st);
-  cudaError_t e = launch_gemm(g, m, grid, st);
-  if (r.stop) cudaEventRecord(r.stop, st);
-  if (r.start && r.stop) p.recs.push_back(r);
-  ++p.launches;
+  const ProfScope r = prof_launch_begin(st);
+  const cudaError_t e = launch_gemm(g, m, grid, st);
+  prof_launch_end(r, g.mode, st);
   return e;
 }
 

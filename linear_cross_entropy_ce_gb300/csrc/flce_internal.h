@@ -115,6 +115,7 @@ struct DeviceState {
 };
 cudaError_t device_state(DeviceState* out);
 int device_pairs();
+int device_sms();
 unsigned long long wait_timeout_ns();
 bool make_map(CUtensorMap* m, const void* base, unsigned long long inner, unsigned long long outer,
               unsigned long long row_bytes, unsigned box_inner, unsigned box_outer,
@@ -123,6 +124,16 @@ bool make_map(CUtensorMap* m, const void* base, unsigned long long inner, unsign
 // Launch a GEMM, bracketed by events when profiling is on.
 cudaError_t gemm_launch(const GemmArgs& g0, const GemmMaps& m, int grid, cudaStream_t st);
 void count_launches(long long n);
+// Events around a tcgen05 launch of `mode` while profiling is on (begin gives a
+// handle for end; a call without profiling costs one lock).
+struct ProfScope {
+  cudaEvent_t start = nullptr, stop = nullptr;
+  bool on = false;
+};
+ProfScope prof_launch_begin(cudaStream_t st);
+void prof_launch_end(const ProfScope& p, int mode, cudaStream_t st);
+// Time limit armed by flce_debug_arm_stall for the next tcgen05 launch, or 0; disarms.
+unsigned long long take_armed_stall();
 bool sizes_ok(long long N, long long H, long long V);
 
 inline size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -141,6 +152,36 @@ cudaError_t launch_zero_ignored(const int* hdr, const int* idx, long long N, lon
 cudaError_t launch_gather(const uint16_t* hidden, const int* targets, const int* hdr,
                           const int* idx, long long c0, int C, int H,
                           uint16_t* xc, int* tc, int v0, int vs, cudaStream_t s);
+// Few tokens: the weight streamed once past all of them (flce_stream.cu).
+constexpr int STREAM_MAX_TOKENS = 128;
+struct StreamArgs {
+  int N, H, V, K;          // K: top alternatives
+  int ctas;
+  float c2;
+  int ii;
+  unsigned long long timeout_ns;
+  int debug_stall;
+  const int* targets;
+  int* hdr;
+  float* zt;               // [N]
+  float4* stat;            // [N][ctas] max, sum, weighted sum
+  float* top_v;            // [N][ctas][K]
+  int* top_i;
+  int* fail;               // [ctas]
+  float* logp;
+  float* entropy;          // or null
+  float* lse;
+  int* top_ids;
+  float* top_logp;
+};
+struct StreamMaps {
+  CUtensorMap x, w[4];     // w[k]: boxes of 128 >> k weight rows
+};
+int stream_ctas(long long V, int sms);
+int stream_tokens(int N);   // N padded to the tile sizes of the kernel
+cudaError_t stream_prepare();
+cudaError_t launch_stream(const StreamArgs& a, const StreamMaps& m, cudaStream_t s);
+
 // Token log probabilities (flce_logprobs.cu).
 cudaError_t launch_gather_dz(const uint16_t* hidden, const int* targets, const int* hdr, const int* idx,
                              long long c0, int C, int H, float temperature, const float* lse, const float* entropy,
@@ -149,6 +190,7 @@ cudaError_t launch_gather_dz(const uint16_t* hidden, const int* targets, const i
 cudaError_t launch_mark_failed(const int* hdr, uint16_t* grad_hidden, float* grad_weight, int gw_bf16,
                                cudaStream_t s);
 bool bad_temperature(float t);
+constexpr long long PROBS_MAX_V = (1ll << 31) - 512;   // ids rounded up to a tile stay in 32 bits
 cudaError_t launch_lse_dz(const int* hdr, long long c0, int C, int V, long long ldz,
                           int nparts, const float2* part, const float* zt, const int* tc,
                           float* rl, uint16_t* z, int reduce_sum, int make_dz,

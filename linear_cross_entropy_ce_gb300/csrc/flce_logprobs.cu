@@ -22,13 +22,11 @@
 #include "flce.h"
 #include "flce_internal.h"
 #include "flce_ptx.cuh"
+#include "flce_softmax.cuh"
 #include "flce_topk.cuh"
 
 namespace flce {
 namespace {
-
-constexpr float LOG2E = 1.4426950408889634f;
-constexpr float LN2 = 0.6931471805599453f;
 
 __device__ __forceinline__ int chunk_rows(const int* hdr, long long c0, int C) {
   const long long rem = static_cast<long long>(hdr[HDR_NVALID]) - c0;
@@ -67,23 +65,6 @@ __global__ void __launch_bounds__(128)
     tc[r] = t[row];
     rowc[r] = DzRow{lse[row] * LOG2E, -it * (grad_entropy ? fmaf(e, entropy[row], g) : g), -it * LN2 * e, it * g};
   }
-}
-
-// Running statistics of a set of logits, in units of log2 (see above).
-struct Stat {
-  float m, s, d;   // max (raw), sum 2^x, sum x 2^x with x = (z - m) c2
-};
-
-__device__ __forceinline__ Stat merge(const Stat& a, const Stat& b, float c2) {
-  Stat r;
-  r.m = fmaxf(a.m, b.m);
-  // a side whose max is -inf holds nothing: its factor is 0 (the clamp also
-  // turns -inf - -inf into it)
-  const float xa = fmaxf((a.m - r.m) * c2, -1e20f), xb = fmaxf((b.m - r.m) * c2, -1e20f);
-  const float fa = ptx::ex2(xa), fb = ptx::ex2(xb);
-  r.s = fa * a.s + fb * b.s;
-  r.d = fa * fmaf(xa, a.s, a.d) + fb * fmaf(xb, b.s, b.d);
-  return r;
 }
 
 // One chunk's rows: lane = row (part-major statistics: coalesced), the parts
@@ -243,11 +224,38 @@ bool lp_plan(long long N, long long H, long long V, int K, size_t bytes, LpPlan*
 // what lets problems of a few thousand tokens run in one chunk (64 MiB; 1 GiB
 // with the fp32 logits of top alternatives): every chunk reads the weight.
 size_t lp_default_bytes(long long N, long long H, long long V, int K) {
-  if (!sizes_ok(N, H, V) || K < 0 || K > TopK::MAX || K > V) return 0;
   const size_t budget = std::max(size_t(N) * size_t(V) * 2 / 20, size_t(K > 0 ? 1024 : 64) << 20);
   LpPlan p;
   if (lp_plan(N, H, V, K, budget, &p)) return p.total;
   return lp_layout(N, H, V, BM, K).total;
+}
+
+}  // namespace
+
+namespace {
+
+// Workspace of the streaming form (N <= STREAM_MAX_TOKENS).
+struct StreamPlan {
+  int ctas = 0;
+  size_t o_zt = 0, o_stat = 0, o_tv = 0, o_ti = 0, o_fail = 0, total = 0;
+};
+
+StreamPlan stream_plan(long long N, long long V, int K, int sms) {
+  StreamPlan p;
+  p.ctas = stream_ctas(V, sms);
+  size_t off = al256(HDR_WORDS * sizeof(int));
+  auto take = [&off](size_t bytes) {
+    const size_t o = off;
+    off += al256(bytes);
+    return o;
+  };
+  p.o_zt = take(size_t(N) * 4);
+  p.o_stat = take(size_t(N) * p.ctas * 16);
+  p.o_tv = take(size_t(N) * p.ctas * K * 4);
+  p.o_ti = take(size_t(N) * p.ctas * K * 4);
+  p.o_fail = take(size_t(p.ctas) * 4);
+  p.total = off;
+  return p;
 }
 
 }  // namespace
@@ -276,6 +284,8 @@ using namespace flce;
 extern "C" {
 
 size_t flce_logprobs_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t top_k) {
+  if (!sizes_ok(N, H, V) || V > PROBS_MAX_V || top_k < 0 || top_k > TopK::MAX || top_k > V) return 0;
+  if (N <= STREAM_MAX_TOKENS) return stream_plan(N, V, top_k, device_sms()).total;
   return lp_default_bytes(N, H, V, top_k);
 }
 
@@ -286,18 +296,51 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
   if (!hidden || !weight || !targets || !logp || !lse || !workspace) return FLCE_EINVAL;
   if (N < 1 || H < 1 || V < 1 || top_k < 0 || top_k > V || bad_temperature(temperature)) return FLCE_EINVAL;
   if (top_k > 0 && (!top_ids || !top_logp)) return FLCE_EINVAL;
-  if (!sizes_ok(N, H, V) || top_k > TopK::MAX) return FLCE_EUNSUPPORTED;
+  if (!sizes_ok(N, H, V) || V > PROBS_MAX_V || top_k > TopK::MAX) return FLCE_EUNSUPPORTED;
   if (!aligned16(hidden) || !aligned16(weight) || !aligned16(workspace) || !aligned4(targets) || !aligned4(logp) ||
       !aligned4(entropy) || !aligned4(lse) || !aligned4(top_ids) || !aligned4(top_logp))
     return FLCE_EUNSUPPORTED;
   DeviceState dev;
   if (device_state(&dev) != cudaSuccess) { cudaGetLastError(); return FLCE_ECUDA; }
   if (dev.major < 10) return FLCE_EUNSUPPORTED;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int* hdr = at<int>(workspace, 0);
+  if (N <= STREAM_MAX_TOKENS) {
+    const StreamPlan p = stream_plan(N, V, top_k, dev.sms);
+    if (p.total > workspace_bytes) return FLCE_EWORKSPACE;
+    StreamArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.N = static_cast<int>(N); a.H = static_cast<int>(H); a.V = static_cast<int>(V); a.K = top_k;
+    a.ctas = p.ctas;
+    a.c2 = LOG2E / temperature;
+    a.ii = ignore_index;
+    a.timeout_ns = wait_timeout_ns();
+    if (const unsigned long long t = take_armed_stall()) {
+      a.debug_stall = 1;
+      a.timeout_ns = t;
+    }
+    a.targets = targets;
+    a.hdr = hdr;
+    a.zt = at<float>(workspace, p.o_zt);
+    a.stat = at<float4>(workspace, p.o_stat);
+    a.top_v = at<float>(workspace, p.o_tv);
+    a.top_i = at<int>(workspace, p.o_ti);
+    a.fail = at<int>(workspace, p.o_fail);
+    a.logp = logp; a.entropy = entropy; a.lse = lse; a.top_ids = top_ids; a.top_logp = top_logp;
+    StreamMaps m;
+    const unsigned long long hb = static_cast<unsigned long long>(H) * 2;
+    bool ok = make_map(&m.x, hidden, H, N, hb, BK, stream_tokens(a.N));
+    for (int k = 0; k < 4; ++k) ok = ok && make_map(&m.w[k], weight, H, V, hb, BK, 128u >> k);
+    if (!ok) return FLCE_ECUDA;
+    const ProfScope prof = prof_launch_begin(st);
+    const cudaError_t e = launch_stream(a, m, st);
+    prof_launch_end(prof, MODE_STATS, st);
+    count_launches(1);   // the merge
+    return e == cudaSuccess ? FLCE_OK : FLCE_ECUDA;
+  }
   LpPlan p;
   if (!lp_plan(N, H, V, top_k, workspace_bytes, &p)) return FLCE_EWORKSPACE;
 
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int* hdr = at<int>(workspace, 0);
   int* idx = at<int>(workspace, p.o_idx);
   int* counters = at<int>(workspace, p.o_cnt);
   uint16_t* xc = at<uint16_t>(workspace, p.o_xc);

@@ -344,10 +344,11 @@ def test_python_refusals_on_gpu(env):
             f()
 
 
-def test_time_out_is_seen(env):
+@pytest.mark.parametrize("N", [3, 128, 300])
+def test_time_out_is_seen(env, N):
     """A withheld pipeline signal: the wait runs out, the status says so, and the outputs are NaN."""
     flce, torch, dev = env
-    X, W, t = problem(300, 64, 2000, seed=1)
+    X, W, t = problem(N, 64, 2000, seed=1)
     h, w, tt = to_gpu(torch, dev, X, W, t)
     o = flce.token_logprobs(h, w, tt)
     flce.debug_arm_stall(50_000_000)
