@@ -268,9 +268,10 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
  * the fp32 accumulator, and the sums over it are kept in fp32, in a fixed order.
  * Targets outside [0, V) are treated as ignored (FLCE_EBADTARGET in the status
  * word); after a time-out the first element of each gradient is NaN.
- * Workspace: flce_logprobs_bwd_workspace_bytes (5% of the bf16 logits, or 1 GiB
+ * Workspace: flce_logprobs_bwd_workspace_bytes (5% of the bf16 logits, or 2 GiB
  * where that is more and the problem needs it; plus V*H*4 bytes with
- * FLCE_GW_BF16); less runs in smaller chunks.
+ * FLCE_GW_BF16 where that does not hold the batch in one chunk); less runs in
+ * smaller chunks.
  */
 size_t flce_logprobs_bwd_workspace_bytes(int64_t N, int64_t H, int64_t V, uint32_t flags);
 flce_status flce_logprobs_bwd(const void* hidden, const void* weight, const int32_t* targets,

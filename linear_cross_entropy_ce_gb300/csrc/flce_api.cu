@@ -108,11 +108,12 @@ Plan layout(long long N, long long H, long long V, long long C, int S, bool fwd_
             bool gw32 = false, bool probs = false) {
   Plan p;
   p.N = N; p.H = H; p.V = V; p.C = C; p.fwd_only = fwd_only; p.norm = norm; p.gw32 = gw32 && !fwd_only;
-  p.probs = probs;
   p.ldz = cdiv(V, 64) * 64;
   p.nvt = static_cast<int>(cdiv(V, BN));
   p.nparts = static_cast<int>(cdiv(V, PART_COLS));
   p.n_chunks = cdiv(N, C);
+  p.probs = probs;
+  if (probs && p.n_chunks == 1) p.gw32 = false;   // one chunk: the tiles are complete sums, stored as bf16
   const long long kbt = cdiv(V, BK);
   if (fwd_only) S = 1;
   p.kb_per_split = static_cast<int>(cdiv(kbt, S));
@@ -191,6 +192,11 @@ Plan plan_for_chunk(long long N, long long H, long long V, long long C, bool fwd
 bool plan_for_bytes(long long N, long long H, long long V, bool fwd_only, size_t bytes, int pairs, Plan* out,
                     bool norm = false, bool gw32 = false, bool probs = false) {
   long long lo = BM, hi = max_chunk(N);
+  // one chunk needs no fp32 accumulator for a bf16 grad_weight: less than several
+  if (probs && gw32 && layout(N, H, V, hi, 1, fwd_only, norm, gw32, probs).total <= bytes) {
+    *out = plan_for_chunk(N, H, V, hi, fwd_only, pairs, bytes, norm, gw32, probs);
+    return true;
+  }
   if (layout(N, H, V, lo, 1, fwd_only, norm, gw32, probs).total > bytes) return false;
   while (lo < hi) {   // the size shrinks as C grows only through the d(gain) partials: bisect on the total
     const long long mid = ((lo / BM + hi / BM + 1) / 2) * BM;
@@ -233,13 +239,15 @@ size_t default_bytes(long long N, long long H, long long V, bool fwd_only, bool 
   if (!sizes_ok(N, H, V)) return 0;
   gw32 = gw32 && !fwd_only;
   size_t budget = size_t(N) * size_t(V) * 2 / 20;
-  // The backward of the token log probabilities may always use 1 GiB (under
-  // 0.4% of the memory): each chunk reads and rewrites the fp32 grad_weight,
+  // The backward of the token log probabilities may always use 2 GiB (under
+  // 0.8% of the memory): each chunk reads and rewrites the fp32 grad_weight,
   // and 5% of the logits of a few thousand tokens makes chunks of 128 rows
   // (4096 tokens, 30% ignored, at 4096 x 128256: forward and backward 24.2 ms,
-  // 9.2 ms in one chunk).
-  if (probs) budget = std::max(budget, size_t(1) << 30);
-  if (gw32) budget += al256(size_t(V) * H * 4);
+  // 9.2 ms in one chunk).  A bf16 grad_weight that one chunk completes needs
+  // no fp32 accumulator either.
+  if (probs) budget = std::max(budget, size_t(2) << 30);
+  if (gw32 && !(probs && layout(N, H, V, max_chunk(N), 1, false, norm, true, true).total <= budget))
+    budget += al256(size_t(V) * H * 4);
   const int pairs = device_pairs();
   Plan p;
   if (plan_for_bytes(N, H, V, fwd_only, budget, pairs, &p, norm, gw32, probs)) return p.total;
@@ -442,6 +450,8 @@ flce_status run(const Job& j) {
   // region that is rounded to the bf16 output at the end
   float* gwacc = p.gw32 ? at<float>(ws, p.o_gw) : j.grad_weight;
 
+  const bool direct = gw_bf16 && !p.gw32;   // the tiles hold finished sums: stored as bf16 at once
+
   GemmMaps fm, bm;   // forward (logits) and backward (dX + dW) launches
   std::memset(&fm, 0, sizeof(fm));
   std::memset(&bm, 0, sizeof(bm));
@@ -450,8 +460,9 @@ flce_status run(const Job& j) {
   if (!fwd_only)
     ok = ok && make_map(&bm.a0, z, V, p.C, p.ldz * 2, BK, BM) && make_map(&bm.b0, j.weight, H, V, hb, 64, BK) &&
          make_map(&bm.a1, z, V, p.C, p.ldz * 2, 64, BK) && make_map(&bm.b1, xc, H, p.C, hb, 64, BK) &&
-         (!gwacc || make_map(&bm.out, gwacc, H, V, static_cast<unsigned long long>(H) * 4, 32, 64,
-                             CU_TENSOR_MAP_DATA_TYPE_FLOAT32, CU_TENSOR_MAP_SWIZZLE_128B));
+         (!gwacc || (direct ? make_map(&bm.out, gwacc, H, V, hb, 64, 64)
+                            : make_map(&bm.out, gwacc, H, V, static_cast<unsigned long long>(H) * 4, 32, 64,
+                                       CU_TENSOR_MAP_DATA_TYPE_FLOAT32, CU_TENSOR_MAP_SWIZZLE_128B)));
   if (!ok) return FLCE_ECUDA;
   if (!gwacc) bm.out = bm.b1;   // never stored through, but its descriptor is prefetched
 
@@ -488,6 +499,7 @@ flce_status run(const Job& j) {
   g.pf_threads = p.C <= 512 ? 1 : 0;
   g.dxacc = dxacc;
   g.skip = skip;
+  g.gw_bf16 = direct ? 1 : 0;
   DzRow* rowc = probs ? at<DzRow>(ws, p.o_rowc) : nullptr;
   g.rowc = rowc;
   if (probs) g.c2 = 1.4426950408889634f / j.temperature;

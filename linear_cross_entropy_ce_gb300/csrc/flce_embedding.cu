@@ -31,8 +31,8 @@ namespace {
 // ---------------------------------------------------------------------------
 struct Bf16 {
   static constexpr int SIZE = 2;
-  static __device__ __forceinline__ void load(const void* p, float (&f)[8]) {
-    const uint4 w = *static_cast<const uint4*>(p);
+  using Raw = uint4;
+  static __device__ __forceinline__ void unpack(const Raw& w, float (&f)[8]) {
     const uint32_t q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -48,8 +48,8 @@ struct Bf16 {
 
 struct F16 {
   static constexpr int SIZE = 2;
-  static __device__ __forceinline__ void load(const void* p, float (&f)[8]) {
-    const uint4 w = *static_cast<const uint4*>(p);
+  using Raw = uint4;
+  static __device__ __forceinline__ void unpack(const Raw& w, float (&f)[8]) {
     const __half2* h = reinterpret_cast<const __half2*>(&w);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -69,8 +69,11 @@ struct F16 {
 
 struct F32 {
   static constexpr int SIZE = 4;
-  static __device__ __forceinline__ void load(const void* p, float (&f)[8]) {
-    const float4 a = static_cast<const float4*>(p)[0], b = static_cast<const float4*>(p)[1];
+  struct Raw {
+    float4 a, b;
+  };
+  static __device__ __forceinline__ void unpack(const Raw& w, float (&f)[8]) {
+    const float4 a = w.a, b = w.b;
     f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
     f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
   }
@@ -80,31 +83,64 @@ struct F32 {
   }
 };
 
-// ---------------------------------------------------------------------------
-// lookup: one thread per 8 columns of a row, grid-stride
-// ---------------------------------------------------------------------------
-constexpr int LOOKUP_THREADS = 256;
-
 template <typename T>
-__global__ void __launch_bounds__(LOOKUP_THREADS)
-    embedding_kernel(const unsigned char* __restrict__ W, const int* __restrict__ ids, long long N, int H8, int V,
+__device__ __forceinline__ void load8(const void* p, float (&f)[8]) {
+  T::unpack(*static_cast<const typename T::Raw*>(p), f);
+}
+
+constexpr int COLS = 32 * 8;   // columns a warp moves at once: 8 per lane
+
+// ---------------------------------------------------------------------------
+// lookup: a warp moves ROWS rows of one slice of 256 columns, all of them in
+// flight at once (the latency of id, row and store is what a warp waits for).
+// ---------------------------------------------------------------------------
+constexpr int LOOKUP_WARPS = 8;
+
+template <typename T, int ROWS>
+__global__ void __launch_bounds__(32 * LOOKUP_WARPS)
+    embedding_kernel(const unsigned char* __restrict__ W, const int* __restrict__ ids, int N, int H, int V, int slices,
                      float scale, unsigned char* __restrict__ out) {
-  const long long total = N * H8;
-  for (long long i = static_cast<long long>(blockIdx.x) * LOOKUP_THREADS + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * LOOKUP_THREADS) {
-    const long long n = i / H8;
-    const int c = static_cast<int>(i - n * H8);
-    const int v = ids[n];
-    float f[8];
-    if (v >= 0 && v < V) {
-      T::load(W + (static_cast<long long>(v) * H8 + c) * (8 * T::SIZE), f);
+  const long long warp = static_cast<long long>(blockIdx.x) * LOOKUP_WARPS + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  const long long n0 = warp / slices * ROWS;
+  const int h = static_cast<int>(warp % slices) * COLS + lane * 8;
+  if (n0 >= N || h >= H) return;
+  int v[ROWS];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] *= scale;
+  for (int k = 0; k < ROWS; ++k) v[k] = n0 + k < N ? ids[n0 + k] : -1;
+  typename T::Raw x[ROWS];
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k)
+    if (static_cast<unsigned>(v[k]) < static_cast<unsigned>(V))
+      x[k] = *reinterpret_cast<const typename T::Raw*>(W + (static_cast<long long>(v[k]) * H + h) * T::SIZE);
+#pragma unroll
+  for (int k = 0; k < ROWS; ++k) {
+    if (n0 + k >= N) break;
+    float f[8];
+    if (static_cast<unsigned>(v[k]) < static_cast<unsigned>(V)) {
+      T::unpack(x[k], f);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) f[q] *= scale;
     } else {   // an id outside the table: a row of NaN
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] = __int_as_float(0x7fc00000);
+      for (int q = 0; q < 8; ++q) f[q] = __int_as_float(0x7fc00000);
     }
-    T::store(out + i * (8 * T::SIZE), f);
+    T::store(out + ((n0 + k) * H + h) * T::SIZE, f);
+  }
+}
+
+template <typename T>
+void launch_lookup(const void* W, const int* ids, long long N, int H, int V, float scale, void* out, cudaStream_t st) {
+  const int slices = static_cast<int>(cdiv(H, COLS));
+  const unsigned char* w = static_cast<const unsigned char*>(W);
+  unsigned char* o = static_cast<unsigned char*>(out);
+  // four rows a warp once that still fills the GPU (152 SMs x 16 warps)
+  if (N * slices >= 4 * 16 * 152) {
+    const unsigned grid = static_cast<unsigned>(cdiv(cdiv(N, 4) * slices, LOOKUP_WARPS));
+    embedding_kernel<T, 4><<<grid, 32 * LOOKUP_WARPS, 0, st>>>(w, ids, static_cast<int>(N), H, V, slices, scale, o);
+  } else {
+    const unsigned grid = static_cast<unsigned>(cdiv(N * slices, LOOKUP_WARPS));
+    embedding_kernel<T, 1><<<grid, 32 * LOOKUP_WARPS, 0, st>>>(w, ids, static_cast<int>(N), H, V, slices, scale, o);
   }
 }
 
@@ -117,38 +153,48 @@ constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int SORT_MAX_BITS = 9;
 constexpr int SORT_BINS = 1 << SORT_MAX_BITS;
 static_assert(SORT_BINS == SORT_THREADS, "one thread per bin");
-constexpr int SORT_ITEMS = 8;                           // per thread
-constexpr int SORT_TILE = SORT_THREADS * SORT_ITEMS;
+// Items per thread: small tiles keep the few thousand tokens of a step on many
+// SMs; past 2^17 tokens larger ones bound the counts each tile has to add up.
+constexpr int SORT_ITEMS_SMALL = 4;
+constexpr int SORT_ITEMS_LARGE = 16;
+constexpr long long SORT_LARGE = 1ll << 17;
 
-__device__ __forceinline__ int sort_key(const int* ids, long long i, int V, int padding, int* hdr) {
+__device__ __forceinline__ int sort_key(const int* ids, long long i, int V, int padding) {
   const int v = ids[i];
-  if (v < 0 || v >= V) {
-    atomicOr(hdr + HDR_STATUS, STATUS_BADTARGET);
-    return V;
-  }
-  return v == padding ? V : v;
+  return v < 0 || v >= V || v == padding ? V : v;
 }
 
-// Counts of one digit, per tile.  first: keys come from ids.
-template <bool FIRST>
+// Every kernel but the first is launched while its predecessor drains and waits
+// for its end.  What a predecessor wrote is therefore read through plain
+// pointers only: loads through const __restrict__ ones may be taken for
+// invariant and moved ahead of the wait.  All positions, tokens and ids read
+// back from the workspace are checked against their arrays before use.
+
+// Counts of one digit, per tile.  FIRST: the keys come from the ids, and ids
+// outside the table are flagged per tile.
+template <bool FIRST, int ITEMS>
 __global__ void __launch_bounds__(SORT_THREADS)
-    sort_count_kernel(const int* __restrict__ keys, int N, int V, int padding, int* hdr, int shift, int bits,
-                      int* __restrict__ counts) {
+    sort_count_kernel(const int* keys, int N, int V, int padding, int* bad, int shift, int bits, int* counts) {
   __shared__ int bin[SORT_BINS];
+  ptx::grid_launch_dependents();
   bin[threadIdx.x] = 0;
   __syncthreads();
+  if (!FIRST) ptx::grid_dependency_wait();
   const int mask = (1 << bits) - 1;
-  const long long base = static_cast<long long>(blockIdx.x) * SORT_TILE;
+  const long long base = static_cast<long long>(blockIdx.x) * (SORT_THREADS * ITEMS);
+  int outside = 0;
 #pragma unroll
-  for (int k = 0; k < SORT_ITEMS; ++k) {
+  for (int k = 0; k < ITEMS; ++k) {
     const long long i = base + k * SORT_THREADS + threadIdx.x;
     if (i < N) {
-      const int key = FIRST ? sort_key(keys, i, V, padding, hdr) : keys[i];
+      const int key = FIRST ? sort_key(keys, i, V, padding) : keys[i];
+      if (FIRST && key == V) outside |= keys[i] < 0 || keys[i] >= V;
       atomicAdd(&bin[(key >> shift) & mask], 1);
     }
   }
-  __syncthreads();
+  outside = __syncthreads_or(outside);
   counts[blockIdx.x * SORT_BINS + threadIdx.x] = bin[threadIdx.x];
+  if (FIRST && threadIdx.x == 0) bad[blockIdx.x] = outside;
 }
 
 __device__ __forceinline__ int block_exclusive_scan(int x, int* scratch) {
@@ -178,24 +224,37 @@ __device__ __forceinline__ int block_exclusive_scan(int x, int* scratch) {
 // Every item moves to (items of smaller digits) + (items of its digit in
 // earlier tiles) + (its rank among the tile's items of its digit).  A warp
 // ranks its 32 x ITEMS consecutive items in order, so the sort is stable.
-template <bool FIRST>
+template <bool FIRST, int ITEMS>
 __global__ void __launch_bounds__(SORT_THREADS)
-    sort_scatter_kernel(const int* __restrict__ keys, const int* __restrict__ toks, int N, int V, int padding,
-                        int* hdr, int shift, int bits, const int* __restrict__ counts, int tiles,
-                        int* __restrict__ out_keys, int* __restrict__ out_toks) {
+    sort_scatter_kernel(const int* keys, const int* toks, int N, int V, int padding, int shift, int bits,
+                        const int* counts, int tiles, int* out_keys, int* out_toks) {
   __shared__ int cnt[SORT_WARPS][SORT_BINS];
   __shared__ int scratch[32];
   const int tid = threadIdx.x, lane = tid % 32, w = tid / 32;
+  ptx::grid_launch_dependents();
   for (int k = 0; k < SORT_WARPS; ++k) cnt[k][tid] = 0;
   __syncthreads();
   const int mask = (1 << bits) - 1;
-  int key[SORT_ITEMS], rank[SORT_ITEMS];
-  const long long base = static_cast<long long>(blockIdx.x) * SORT_TILE + w * (32 * SORT_ITEMS);
+  int key[ITEMS], tok[ITEMS], rank[ITEMS];
+  const long long base = static_cast<long long>(blockIdx.x) * (SORT_THREADS * ITEMS) + w * (32 * ITEMS);
+  ptx::grid_dependency_wait();
 #pragma unroll
-  for (int k = 0; k < SORT_ITEMS; ++k) {
+  for (int k = 0; k < ITEMS; ++k) {
     const long long i = base + k * 32 + lane;
-    const bool ok = i < N;
-    key[k] = ok ? (FIRST ? sort_key(keys, i, V, padding, hdr) : keys[i]) : -1;
+    key[k] = i < N ? (FIRST ? sort_key(keys, i, V, padding) : keys[i]) : -1;
+    tok[k] = FIRST ? static_cast<int>(i) : (i < N ? toks[i] : 0);
+  }
+  // thread d: total of digit d and its items in earlier tiles
+  int total = 0, earlier = 0;
+#pragma unroll 16
+  for (int b = 0; b < tiles; ++b) {
+    const int c = counts[b * SORT_BINS + tid];
+    total += c;
+    earlier += b < static_cast<int>(blockIdx.x) ? c : 0;
+  }
+#pragma unroll
+  for (int k = 0; k < ITEMS; ++k) {
+    const bool ok = base + k * 32 + lane < N;
     const int d = ok ? (key[k] >> shift) & mask : SORT_BINS;   // past the end: a group of their own
     const unsigned same = __match_any_sync(0xffffffffu, d);
     int before = 0;
@@ -206,15 +265,7 @@ __global__ void __launch_bounds__(SORT_THREADS)
     rank[k] = before + __popc(same & ((1u << lane) - 1u));
   }
   __syncthreads();
-  // thread d: total of digit d, its items in earlier tiles, then the warps' offsets
-  int total = 0, earlier = 0;
-#pragma unroll 8
-  for (int b = 0; b < tiles; ++b) {
-    const int c = counts[b * SORT_BINS + tid];
-    total += c;
-    earlier += b < static_cast<int>(blockIdx.x) ? c : 0;
-  }
-  int off = block_exclusive_scan(total, scratch) + earlier;
+  int off = block_exclusive_scan(total, scratch) + earlier;   // then the warps' offsets
   for (int k = 0; k < SORT_WARPS; ++k) {
     const int c = cnt[k][tid];
     cnt[k][tid] = off;
@@ -222,12 +273,13 @@ __global__ void __launch_bounds__(SORT_THREADS)
   }
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < SORT_ITEMS; ++k) {
-    const long long i = base + k * 32 + lane;
-    if (i < N) {
+  for (int k = 0; k < ITEMS; ++k) {
+    if (base + k * 32 + lane < N) {
       const int pos = cnt[w][(key[k] >> shift) & mask] + rank[k];
-      out_keys[pos] = key[k];
-      out_toks[pos] = FIRST ? static_cast<int>(i) : toks[i];
+      if (static_cast<unsigned>(pos) < static_cast<unsigned>(N)) {
+        out_keys[pos] = key[k];
+        out_toks[pos] = tok[k];
+      }
     }
   }
 }
@@ -236,7 +288,8 @@ __global__ void __launch_bounds__(SORT_THREADS)
 // sums over runs of equal ids
 // ---------------------------------------------------------------------------
 constexpr int SEG_WARPS = 8;
-constexpr int SEG_COLS = 32 * 8;       // columns of a warp's slice
+constexpr int MIN_CHUNK = 32;          // sorted entries per chunk, and
+constexpr int MAX_CHUNKS = 4096;       // at most this many chunks (two partial sums of H floats each)
 constexpr int ZERO_ROWS = 32;          // grad_weight rows a warp looks up at once
 
 struct SegArgs {
@@ -250,6 +303,9 @@ struct SegArgs {
   int accumulate;
   unsigned char* gw;
   float* part;           // [n_chunks][2][H]: 0 = sum of the run that came in, 1 = of the run that goes out
+  int* hdr;
+  const int* bad;        // [tiles] whether a tile of the first sort pass held an id outside the table
+  int tiles;
   long long seg_warps;   // warps of the first kind; the others set rows to zero
 };
 
@@ -261,7 +317,7 @@ __device__ __forceinline__ void write_row(const SegArgs& a, int v, int h, const 
   for (int k = 0; k < 8; ++k) f[k] = s[k] * a.scale;
   if (a.accumulate) {
     float g[8];
-    O::load(p, g);
+    load8<O>(p, g);
 #pragma unroll
     for (int k = 0; k < 8; ++k) f[k] += g[k];
   }
@@ -270,33 +326,36 @@ __device__ __forceinline__ void write_row(const SegArgs& a, int v, int h, const 
 
 template <typename T, typename O>
 __device__ __forceinline__ void segments(const SegArgs& a, long long warp, int lane) {
+  constexpr int SEG_ROWS = 16 / T::SIZE;   // rows a warp has in flight: 128 bytes a lane
   const int c = static_cast<int>(warp / a.slices), slice = static_cast<int>(warp % a.slices);
-  const int h = slice * SEG_COLS + lane * 8;
+  const int h = slice * COLS + lane * 8;
   const bool live = h < a.H;
   const int i0 = c * a.chunk, i1 = min(a.N, i0 + a.chunk);
   const int before = i0 > 0 ? a.keys[i0 - 1] : -1;
   const int after = i1 < a.N ? a.keys[i1] : a.V;
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const unsigned nv = static_cast<unsigned>(a.V), nn = static_cast<unsigned>(a.N);
   int cur = a.keys[i0];
   bool came_in = cur == before;
   for (int g0 = i0; g0 < i1; g0 += 32) {
     const int m = min(32, i1 - g0);
     const int my_key = lane < m ? a.keys[g0 + lane] : a.V;
     const int my_tok = lane < m ? a.toks[g0 + lane] : 0;
-    for (int j0 = 0; j0 < m; j0 += 4) {
-      float x[4][8];
+    for (int j0 = 0; j0 < m; j0 += SEG_ROWS) {
+      typename T::Raw x[SEG_ROWS];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int key = __shfl_sync(0xffffffffu, my_key, j0 + q);
-        const long long tok = __shfl_sync(0xffffffffu, my_tok, j0 + q);
-        if (live && key < a.V) T::load(a.dout + (tok * a.H + h) * T::SIZE, x[q]);
+      for (int q = 0; q < SEG_ROWS; ++q) {
+        const unsigned key = __shfl_sync(0xffffffffu, my_key, j0 + q);
+        const unsigned tok = __shfl_sync(0xffffffffu, my_tok, j0 + q);
+        if (live && key < nv && tok < nn)
+          x[q] = *reinterpret_cast<const typename T::Raw*>(a.dout + (static_cast<long long>(tok) * a.H + h) * T::SIZE);
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < SEG_ROWS; ++q) {
         if (j0 + q >= m) break;
         const int key = __shfl_sync(0xffffffffu, my_key, j0 + q);
         if (key != cur) {   // uniform over the warp: the run ends inside the chunk
-          if (live && cur < a.V) {
+          if (live && static_cast<unsigned>(cur) < nv) {
             if (came_in) F32::store(a.part + (2ll * c) * a.H + h, s);
             else write_row<O>(a, cur, h, s);
           }
@@ -305,21 +364,23 @@ __device__ __forceinline__ void segments(const SegArgs& a, long long warp, int l
           cur = key;
           came_in = false;
         }
-        if (live && key < a.V) {
+        if (live && static_cast<unsigned>(key) < nv) {
+          float f[8];
+          T::unpack(x[q], f);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) s[k] += x[q][k];
+          for (int k = 0; k < 8; ++k) s[k] += f[k];
         }
       }
     }
   }
-  if (!live || cur >= a.V) return;
+  if (!live || static_cast<unsigned>(cur) >= nv) return;
   if (came_in) F32::store(a.part + (2ll * c) * a.H + h, s);
   else if (cur == after) F32::store(a.part + (2ll * c + 1) * a.H + h, s);
   else write_row<O>(a, cur, h, s);
 }
 
 // First position whose key is >= v.
-__device__ __forceinline__ int lower_bound(const int* __restrict__ keys, int n, int v) {
+__device__ __forceinline__ int lower_bound(const int* keys, int n, int v) {
   int lo = 0, len = n;
   while (len > 0) {
     const int half = len / 2;
@@ -334,9 +395,11 @@ __device__ __forceinline__ int lower_bound(const int* __restrict__ keys, int n, 
 }
 
 template <typename T, typename O>
-__global__ void __launch_bounds__(32 * SEG_WARPS) embedding_segments_kernel(const SegArgs a) {
+__global__ void __launch_bounds__(32 * SEG_WARPS, 2) embedding_segments_kernel(const SegArgs a) {
   const long long warp = static_cast<long long>(blockIdx.x) * SEG_WARPS + threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
+  ptx::grid_launch_dependents();
+  ptx::grid_dependency_wait();
   if (warp < a.seg_warps) {
     if (warp < static_cast<long long>(a.n_chunks) * a.slices) segments<T, O>(a, warp, lane);
     return;
@@ -344,9 +407,9 @@ __global__ void __launch_bounds__(32 * SEG_WARPS) embedding_segments_kernel(cons
   // rows whose id does not occur
   const long long r0 = (warp - a.seg_warps) * ZERO_ROWS;
   if (r0 >= a.V) return;
-  const int v = static_cast<int>(r0) + lane;
   bool absent = false;
-  if (v < a.V) {
+  if (r0 + lane < a.V) {
+    const int v = static_cast<int>(r0 + lane);
     const int at = lower_bound(a.keys, a.N, v);
     absent = at >= a.N || a.keys[at] != v;
   }
@@ -361,36 +424,66 @@ __global__ void __launch_bounds__(32 * SEG_WARPS) embedding_segments_kernel(cons
 }
 
 // A run that goes out of chunk c and comes into c + 1, c + 2, ...: its partial
-// sums in chunk order.  One warp per chunk and column slice.
+// sums.  One block per chunk and column slice; the chain (a token that makes a
+// tenth of 65536 has 200 links) is cut in as many equal parts as there are
+// warps, and their sums are added in order.
+constexpr int JOIN_WARPS = 8;
+constexpr int JOIN_LINKS = 4;          // partial sums a warp has in flight
+
 template <typename O>
-__global__ void __launch_bounds__(32 * SEG_WARPS) embedding_join_kernel(const SegArgs a) {
-  const long long warp = static_cast<long long>(blockIdx.x) * SEG_WARPS + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  if (warp >= static_cast<long long>(a.n_chunks) * a.slices) return;
-  const int c = static_cast<int>(warp / a.slices), slice = static_cast<int>(warp % a.slices);
-  const int h = slice * SEG_COLS + lane * 8;
+__global__ void __launch_bounds__(32 * JOIN_WARPS) embedding_join_kernel(const SegArgs a) {
+  __shared__ __align__(16) float sums[JOIN_WARPS][COLS];
+  const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int c = static_cast<int>(blockIdx.x / a.slices), slice = static_cast<int>(blockIdx.x % a.slices);
+  ptx::grid_dependency_wait();
+  if (blockIdx.x == 0) {   // the status word of the call
+    int outside = 0;
+    for (int t = threadIdx.x; t < a.tiles; t += 32 * JOIN_WARPS) outside |= a.bad[t];
+    outside = __syncthreads_or(outside);
+    if (threadIdx.x == 0) {
+      a.hdr[HDR_STATUS] = outside ? STATUS_BADTARGET : 0;
+      a.hdr[HDR_STALL] = a.hdr[HDR_STALL_COUNT] = 0;
+    }
+  }
   const int i0 = c * a.chunk, i1 = min(a.N, i0 + a.chunk);
-  if (i1 >= a.N) return;
+  if (i1 >= a.N) return;   // uniform over the block, as the following
   const int v = a.keys[i1 - 1];
-  if (v >= a.V || a.keys[i1] != v) return;
+  if (static_cast<unsigned>(v) >= static_cast<unsigned>(a.V) || a.keys[i1] != v) return;
   if (i0 > 0 && a.keys[i0] == v && a.keys[i0 - 1] == v) return;   // the run began in an earlier chunk
-  if (h >= a.H) return;
-  float s[8];
-  F32::load(a.part + (2ll * c + 1) * a.H + h, s);
-  const int end = lower_bound(a.keys, a.N, v + 1);   // past the run
-  const int last = (end - 1) / a.chunk;
-#pragma unroll 4
-  for (int k = c + 1; k <= last; ++k) {
-    float x[8];
-    F32::load(a.part + (2ll * k) * a.H + h, x);
+  const int h = slice * COLS + lane * 8;
+  const int last = (lower_bound(a.keys, a.N, v + 1) - 1) / a.chunk;   // the run's last chunk
+  const int links = last - c;
+  const int k0 = c + 1 + static_cast<int>(static_cast<long long>(links) * w / JOIN_WARPS);
+  const int k1 = c + 1 + static_cast<int>(static_cast<long long>(links) * (w + 1) / JOIN_WARPS);
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (h < a.H) {
+    if (w == 0) load8<F32>(a.part + (2ll * c + 1) * a.H + h, s);
+    for (int k = k0; k < k1; k += JOIN_LINKS) {
+      F32::Raw x[JOIN_LINKS];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) s[q] += x[q];
+      for (int q = 0; q < JOIN_LINKS; ++q)
+        if (k + q < k1) x[q] = *reinterpret_cast<const F32::Raw*>(a.part + (2ll * (k + q)) * a.H + h);
+#pragma unroll
+      for (int q = 0; q < JOIN_LINKS; ++q) {
+        if (k + q >= k1) break;
+        float f[8];
+        F32::unpack(x[q], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] += f[j];
+      }
+    }
+  }
+  F32::store(&sums[w][lane * 8], s);
+  __syncthreads();
+  if (w != 0 || h >= a.H) return;
+#pragma unroll
+  for (int k = 1; k < JOIN_WARPS; ++k) {
+    float f[8];
+    load8<F32>(&sums[k][lane * 8], f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] += f[j];
   }
   write_row<O>(a, v, h, s);
-}
-
-__global__ void clear_header_kernel(int* hdr) {
-  if (threadIdx.x < HDR_WORDS) hdr[threadIdx.x] = 0;
 }
 
 // ---------------------------------------------------------------------------
@@ -398,7 +491,7 @@ __global__ void clear_header_kernel(int* hdr) {
 // ---------------------------------------------------------------------------
 struct EmbPlan {
   int tiles = 0, passes = 0, bits = 0, chunk = 0, n_chunks = 0;
-  size_t o_keys[2] = {0, 0}, o_toks[2] = {0, 0}, o_cnt = 0, o_part = 0, total = 0;
+  size_t o_keys[2] = {0, 0}, o_toks[2] = {0, 0}, o_cnt = 0, o_bad = 0, o_part = 0, total = 0;
 };
 
 EmbPlan emb_plan(long long N, long long H, long long V) {
@@ -407,8 +500,8 @@ EmbPlan emb_plan(long long N, long long H, long long V) {
   while ((V >> key_bits) != 0) ++key_bits;   // keys 0 .. V
   p.passes = static_cast<int>(cdiv(key_bits, SORT_MAX_BITS));
   p.bits = static_cast<int>(cdiv(key_bits, p.passes));
-  p.tiles = static_cast<int>(cdiv(N, SORT_TILE));
-  p.chunk = 32;
+  p.tiles = static_cast<int>(cdiv(N, SORT_THREADS * (N <= SORT_LARGE ? SORT_ITEMS_SMALL : SORT_ITEMS_LARGE)));
+  p.chunk = static_cast<int>(cdiv(std::max<long long>(MIN_CHUNK, cdiv(N, MAX_CHUNKS)), 32) * 32);
   p.n_chunks = static_cast<int>(cdiv(N, p.chunk));
   size_t off = al256(HDR_WORDS * sizeof(int));
   auto take = [&off](size_t bytes) {
@@ -421,6 +514,7 @@ EmbPlan emb_plan(long long N, long long H, long long V) {
     p.o_toks[k] = take(size_t(N) * 4);
   }
   p.o_cnt = take(size_t(p.tiles) * SORT_BINS * 4);
+  p.o_bad = take(size_t(p.tiles) * 4);
   p.o_part = take(size_t(p.n_chunks) * 2 * H * 4);
   p.total = off;
   return p;
@@ -428,16 +522,41 @@ EmbPlan emb_plan(long long N, long long H, long long V) {
 
 bool emb_sizes_ok(long long N, long long H, long long V) { return sizes_ok(N, H, V) && N <= (1ll << 30); }
 
+struct SortPass {
+  const int *keys, *toks;
+  int N, V, padding, shift, bits, tiles;
+  int *bad, *counts, *out_keys, *out_toks;
+};
+
+template <bool FIRST, int ITEMS>
+cudaError_t sort_pass(const SortPass& s, cudaStream_t st) {
+  cudaError_t e;
+  if (FIRST) {   // behind everything before the call
+    sort_count_kernel<FIRST, ITEMS><<<s.tiles, SORT_THREADS, 0, st>>>(s.keys, s.N, s.V, s.padding, s.bad, s.shift,
+                                                                      s.bits, s.counts);
+    e = cudaGetLastError();
+  } else {
+    e = launch_dependent(sort_count_kernel<FIRST, ITEMS>, s.tiles, SORT_THREADS, st, s.keys, s.N, s.V, s.padding, s.bad,
+                         s.shift, s.bits, s.counts);
+  }
+  if (e != cudaSuccess) return e;
+  return launch_dependent(sort_scatter_kernel<FIRST, ITEMS>, s.tiles, SORT_THREADS, st, s.keys, s.toks, s.N, s.V,
+                          s.padding, s.shift, s.bits, s.counts, s.tiles, s.out_keys, s.out_toks);
+}
+
 template <typename T, typename O>
-void launch_segments(const SegArgs& a, long long blocks, cudaStream_t st) {
-  embedding_segments_kernel<T, O><<<static_cast<unsigned>(blocks), 32 * SEG_WARPS, 0, st>>>(a);
+cudaError_t sums(const SegArgs& a, long long blocks, cudaStream_t st) {
+  const cudaError_t e =
+      launch_dependent(embedding_segments_kernel<T, O>, static_cast<unsigned>(blocks), 32 * SEG_WARPS, st, a);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(embedding_join_kernel<O>, static_cast<unsigned>(a.n_chunks * a.slices), 32 * JOIN_WARPS, st, a);
 }
 
 template <typename T>
-void launch_segments(const SegArgs& a, int out_dtype, long long blocks, cudaStream_t st) {
-  if (out_dtype == FLCE_BF16) launch_segments<T, Bf16>(a, blocks, st);
-  else if (out_dtype == FLCE_F16) launch_segments<T, F16>(a, blocks, st);
-  else launch_segments<T, F32>(a, blocks, st);
+cudaError_t sums(const SegArgs& a, int out_dtype, long long blocks, cudaStream_t st) {
+  if (out_dtype == FLCE_BF16) return sums<T, Bf16>(a, blocks, st);
+  if (out_dtype == FLCE_F16) return sums<T, F16>(a, blocks, st);
+  return sums<T, F32>(a, blocks, st);
 }
 
 bool known_dtype(int d) { return d == FLCE_BF16 || d == FLCE_F16 || d == FLCE_F32; }
@@ -456,15 +575,12 @@ flce_status flce_embedding(const void* weight, const int32_t* ids, int64_t N, in
   DeviceState dev;
   if (device_state(&dev) != cudaSuccess) { cudaGetLastError(); return FLCE_ECUDA; }
   if (dev.major < 10) return FLCE_EUNSUPPORTED;
-  const int H8 = static_cast<int>(H / 8);
-  const unsigned grid = static_cast<unsigned>(std::min<long long>(cdiv(N * H8, LOOKUP_THREADS), 1 << 20));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned char* w = static_cast<const unsigned char*>(weight);
-  unsigned char* o = static_cast<unsigned char*>(out);
+  const int h = static_cast<int>(H), v = static_cast<int>(V);
   count_launches(1);
-  if (dtype == FLCE_BF16) embedding_kernel<Bf16><<<grid, LOOKUP_THREADS, 0, st>>>(w, ids, N, H8, static_cast<int>(V), scale, o);
-  else if (dtype == FLCE_F16) embedding_kernel<F16><<<grid, LOOKUP_THREADS, 0, st>>>(w, ids, N, H8, static_cast<int>(V), scale, o);
-  else embedding_kernel<F32><<<grid, LOOKUP_THREADS, 0, st>>>(w, ids, N, H8, static_cast<int>(V), scale, o);
+  if (dtype == FLCE_BF16) launch_lookup<Bf16>(weight, ids, N, h, v, scale, out, st);
+  else if (dtype == FLCE_F16) launch_lookup<F16>(weight, ids, N, h, v, scale, out, st);
+  else launch_lookup<F32>(weight, ids, N, h, v, scale, out, st);
   return cudaGetLastError() == cudaSuccess ? FLCE_OK : FLCE_ECUDA;
 }
 
@@ -494,23 +610,17 @@ flce_status flce_embedding_bwd(const void* grad_out, const int32_t* ids, int64_t
   int* cnt = at<int>(workspace, p.o_cnt);
   const int n = static_cast<int>(N), v = static_cast<int>(V);
 
-  count_launches(3 + 2 * p.passes);
-  clear_header_kernel<<<1, HDR_WORDS, 0, st>>>(hdr);
-  if (cudaGetLastError() != cudaSuccess) return FLCE_ECUDA;
+  int* bad = at<int>(workspace, p.o_bad);
+
+  count_launches(2 + 2 * p.passes);
   for (int k = 0; k < p.passes; ++k) {
-    const int shift = k * p.bits;
-    const int *ki = keys[(k + 1) & 1], *ti = toks[(k + 1) & 1];
-    int *ko = keys[k & 1], *to = toks[k & 1];
-    if (k == 0) {
-      sort_count_kernel<true><<<p.tiles, SORT_THREADS, 0, st>>>(ids, n, v, padding_idx, hdr, shift, p.bits, cnt);
-      sort_scatter_kernel<true><<<p.tiles, SORT_THREADS, 0, st>>>(ids, nullptr, n, v, padding_idx, hdr, shift, p.bits,
-                                                                  cnt, p.tiles, ko, to);
-    } else {
-      sort_count_kernel<false><<<p.tiles, SORT_THREADS, 0, st>>>(ki, n, v, padding_idx, hdr, shift, p.bits, cnt);
-      sort_scatter_kernel<false><<<p.tiles, SORT_THREADS, 0, st>>>(ki, ti, n, v, padding_idx, hdr, shift, p.bits, cnt,
-                                                                   p.tiles, ko, to);
-    }
-    if (cudaGetLastError() != cudaSuccess) return FLCE_ECUDA;
+    const SortPass s = {k == 0 ? ids : keys[(k + 1) & 1], toks[(k + 1) & 1], n, v, padding_idx, k * p.bits, p.bits,
+                        p.tiles, bad, cnt, keys[k & 1], toks[k & 1]};
+    const bool large = N > SORT_LARGE;
+    const cudaError_t e =
+        k == 0 ? (large ? sort_pass<true, SORT_ITEMS_LARGE>(s, st) : sort_pass<true, SORT_ITEMS_SMALL>(s, st))
+               : (large ? sort_pass<false, SORT_ITEMS_LARGE>(s, st) : sort_pass<false, SORT_ITEMS_SMALL>(s, st));
+    if (e != cudaSuccess) return FLCE_ECUDA;
   }
   SegArgs a;
   a.keys = keys[(p.passes - 1) & 1];
@@ -518,24 +628,23 @@ flce_status flce_embedding_bwd(const void* grad_out, const int32_t* ids, int64_t
   a.dout = static_cast<const unsigned char*>(grad_out);
   a.N = n; a.H = static_cast<int>(H); a.V = v;
   a.chunk = p.chunk; a.n_chunks = p.n_chunks;
-  a.slices = static_cast<int>(cdiv(H, SEG_COLS));
+  a.slices = static_cast<int>(cdiv(H, COLS));
   a.scale = scale;
   a.accumulate = (flags & FLCE_ACCUMULATE) ? 1 : 0;
   a.gw = static_cast<unsigned char*>(grad_weight);
   a.part = at<float>(workspace, p.o_part);
+  a.hdr = hdr;
+  a.bad = bad;
+  a.tiles = p.tiles;
   const long long seg_blocks = cdiv(static_cast<long long>(a.n_chunks) * a.slices, SEG_WARPS);
   const long long zero_blocks = a.accumulate ? 0 : cdiv(cdiv(V, ZERO_ROWS), SEG_WARPS);
   if (seg_blocks + zero_blocks >= (1ll << 31)) return FLCE_EUNSUPPORTED;
   a.seg_warps = seg_blocks * SEG_WARPS;
-  if (dtype == FLCE_BF16) launch_segments<Bf16>(a, grad_dtype, seg_blocks + zero_blocks, st);
-  else if (dtype == FLCE_F16) launch_segments<F16>(a, grad_dtype, seg_blocks + zero_blocks, st);
-  else launch_segments<F32>(a, grad_dtype, seg_blocks + zero_blocks, st);
-  if (cudaGetLastError() != cudaSuccess) return FLCE_ECUDA;
-  const unsigned join_blocks = static_cast<unsigned>(seg_blocks);
-  if (grad_dtype == FLCE_BF16) embedding_join_kernel<Bf16><<<join_blocks, 32 * SEG_WARPS, 0, st>>>(a);
-  else if (grad_dtype == FLCE_F16) embedding_join_kernel<F16><<<join_blocks, 32 * SEG_WARPS, 0, st>>>(a);
-  else embedding_join_kernel<F32><<<join_blocks, 32 * SEG_WARPS, 0, st>>>(a);
-  return cudaGetLastError() == cudaSuccess ? FLCE_OK : FLCE_ECUDA;
+  const long long blocks = seg_blocks + zero_blocks;
+  const cudaError_t e = dtype == FLCE_BF16  ? sums<Bf16>(a, grad_dtype, blocks, st)
+                        : dtype == FLCE_F16 ? sums<F16>(a, grad_dtype, blocks, st)
+                                            : sums<F32>(a, grad_dtype, blocks, st);
+  return e == cudaSuccess ? FLCE_OK : FLCE_ECUDA;
 }
 
 }  // extern "C"

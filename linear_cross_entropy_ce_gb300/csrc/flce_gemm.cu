@@ -50,6 +50,7 @@
 // STATUS_TIMEOUT.
 #include "flce_internal.h"
 #include "flce_ptx.cuh"
+#include "flce_softmax.cuh"
 
 namespace flce {
 namespace {
@@ -86,7 +87,6 @@ constexpr uint32_t EPI_BAR_GROUP = 1 + EPI_SETS;   // + warpgroup index: per-war
 constexpr uint32_t TMEM_COLS = 2 * BN;
 constexpr int MN_BLOCK_BYTES = 64 * 128;    // 64 K rows x 128 B (64 bf16 along M or N)
 constexpr uint16_t PAIR_MASK = 0x3;
-constexpr float LOG2E = 1.4426950408889634f;
 
 struct Ctl {
   uint64_t full[STAGES_LOGITS];  // CTA 0: both CTAs' loads of a stage landed
@@ -355,62 +355,57 @@ __device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, con
   const int tl = (rv ? a.tc[grow] : -1) - c0;
   const int ncol = min(GROUP_COLS, a.V - c0);
   if (ncol <= 0) return;                          // uniform over the warpgroup
-  float mx = -INFINITY, ztv = 0.f;
+  float ztv = 0.f;
   float* zrow = a.zf + static_cast<size_t>(grow) * a.ldz + c0;
   const bool store = a.zf != nullptr && rv;
+  Stat st = {-INFINITY, 0.f, 0.f};
 #pragma unroll 1
   for (int j = 0; j < GROUP_COLS / 32; ++j) {
+    if (j * 32 >= ncol) break;                    // uniform
     float v[32];
     ptx::tmem_ld32(tbase + j * 32, v);
-    if (j * 32 + 32 <= ncol) {
-#pragma unroll
-      for (int k = 0; k < 32; ++k) mx = fmaxf(mx, v[k]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (j * 32 + k < ncol) mx = fmaxf(mx, v[k]);
-    }
     if (static_cast<unsigned>(tl - j * 32) < 32u) {
 #pragma unroll
       for (int k = 0; k < 32; ++k)
         if (j * 32 + k == tl) ztv = v[k];
     }
-    if (store && c0 + j * 32 < a.ldz) {
+    if (store) {
 #pragma unroll
       for (int k = 0; k < 32; k += 8)
         ptx::st_global_v8(zrow + j * 32 + k, __float_as_uint(v[k]), __float_as_uint(v[k + 1]),
                           __float_as_uint(v[k + 2]), __float_as_uint(v[k + 3]), __float_as_uint(v[k + 4]),
                           __float_as_uint(v[k + 5]), __float_as_uint(v[k + 6]), __float_as_uint(v[k + 7]));
     }
-  }
-  const float mb = mx == -INFINITY ? 0.f : -mx * a.c2;   // a part of nothing but -inf sums to zero
-  float sum = 0.f, dsum = 0.f;
-#pragma unroll 1
-  for (int j = 0; j < GROUP_COLS / 32; ++j) {
-    float v[32];
-    ptx::tmem_ld32(tbase + j * 32, v);
+    if (j * 32 + 32 > ncol) {                     // the block straddles the end of the vocabulary
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (j * 32 + k >= ncol) v[k] = -INFINITY;
+    }
+    float mx = v[0];
+#pragma unroll
+    for (int k = 1; k < 32; ++k) mx = fmaxf(mx, v[k]);
+    const bool none = !(mx > -INFINITY);          // nothing but -inf (or NaN, which the sums keep)
+    const float mb = none ? 0.f : -mx * a.c2;
+    float sum = 0.f, dsum = 0.f;
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
       const float d = fmaf(v[k], a.c2, mb);
       const float e = ptx::ex2(d);
-      if (j * 32 + k < ncol) {
-        sum += e;
-        dsum = fmaf(fmaxf(d, -1e30f), e, dsum);   // 0 for a logit of -inf
-      }
+      sum += e;
+      dsum = fmaf(fmaxf(d, -1e30f), e, dsum);     // 0 for a logit of -inf
     }
+    // mb is rounded: every d is too large by rho = mx c2 + mb (exact in the
+    // fused multiply-add), which matters where the logits are large
+    const float rho = none ? 0.f : fmaf(mx, a.c2, mb);
+    const float back = ptx::ex2(-rho);
+    st = merge(st, Stat{mx, back * sum, back * fmaf(-rho, sum, dsum)}, a.c2);
   }
-  // mb is rounded: every d above is too large by rho = mx c2 + mb (exact in the
-  // fused multiply-add), which matters where the logits are large
-  const float rho = mx == -INFINITY ? 0.f : fmaf(mx, a.c2, mb);
-  const float back = ptx::ex2(-rho);
-  dsum = back * fmaf(-rho, sum, dsum);
-  sum *= back;
   if (rv) {
     const size_t np = static_cast<size_t>(a.nparts) * a.C;
     float* p = a.stats + static_cast<size_t>(c0 / PART_COLS) * a.C + grow;
-    p[0] = mx;
-    p[np] = sum;
-    p[2 * np] = dsum;
+    p[0] = st.m;
+    p[np] = st.s;
+    p[2 * np] = st.d;
     if (tl >= 0 && tl < ncol) a.zt[grow] = ztv;
   }
 }
@@ -540,6 +535,47 @@ __device__ __forceinline__ void block_to_global(const CUtensorMap* map, int ncol
   }
 }
 
+// The same block as finished bf16 values (a grad_weight whose sum over the
+// tokens is complete in one tile): boxes of 64 rows x 64 bf16 columns, half the
+// bytes and half the boxes of the fp32 store, and no pass that rounds it later.
+__device__ __forceinline__ void block_to_global_bf16(const CUtensorMap* map, int ncols_total, int h0, int row0,
+                                                     uint32_t tbase, int r, bool leader, uint32_t bar, uint8_t* buf) {
+  constexpr int COLS16 = 2 * OUT_COLS;
+  const int left = ncols_total - h0;
+  const int nsl = left <= 0 ? 0 : min(GROUP_COLS / COLS16, (left + COLS16 - 1) / COLS16);
+  const int half = r / OUT_ROWS, rr = r % OUT_ROWS;
+  uint8_t* row = buf + rr * (COLS16 * 2);
+#pragma unroll 1
+  for (int j = 0; j < nsl; ++j) {   // uniform over the warpgroup
+    uint32_t pk[32];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float v[32];
+      ptx::tmem_ld32(tbase + j * COLS16 + i * 32, v);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) pk[16 * i + k] = ptx::pack_bf16x2(v[2 * k], v[2 * k + 1]);
+    }
+    const int h = h0 + j * COLS16;
+#pragma unroll 1
+    for (int b = 0; b < BM / OUT_ROWS; ++b) {
+      if (leader) ptx::bulk_wait_read_0();          // the previous box's store has read the buffer
+      ptx::named_bar_sync(bar, GROUP_THREADS);
+      if (half == b) {
+#pragma unroll
+        for (int g = 0; g < 8; ++g)                 // 128-byte swizzle
+          *reinterpret_cast<uint4*>(row + ((g ^ (rr & 7)) << 4)) =
+              make_uint4(pk[4 * g], pk[4 * g + 1], pk[4 * g + 2], pk[4 * g + 3]);
+        ptx::fence_proxy_async_smem();
+      }
+      ptx::named_bar_sync(bar, GROUP_THREADS);
+      if (leader) {
+        ptx::tma_store_2d(map, buf, h, row0 + b * OUT_ROWS);
+        ptx::bulk_commit();
+      }
+    }
+  }
+}
+
 // One warp's 32 accumulator rows x 128 fp32 columns -> dst rows [row0,
 // row0 + 32), columns [h0, h0 + 128) of a [rows][ncols] fp32 array, 16
 // columns at a time: a tcgen05 load gives each thread one row, the slice is
@@ -645,7 +681,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   if (!PROBS && a.mode == MODE_BWD && s.Cl == 0) {
     // Empty first chunk (no valid token at all): grad_weight is zero.
     if (a.first_chunk && !(a.skip & SKIP_DW)) {
-      const size_t n4 = static_cast<size_t>(a.V) * a.H / 4;
+      const size_t n4 = static_cast<size_t>(a.V) * a.H / (a.gw_bf16 ? 8 : 4);
       float4* gw = reinterpret_cast<float4*>(a.grad_weight);
       for (size_t i = static_cast<size_t>(blockIdx.x) * NUM_THREADS + threadIdx.x; i < n4;
            i += static_cast<size_t>(gridDim.x) * NUM_THREADS)
@@ -873,6 +909,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         epi_dx_direct(a, s, t, row0, col0, tbase, r);
       else if (t.kind == U_DX)
         cont = epi_dx_split(a, s, t, row0, col0, half_idx, rank, tbase, r, q, lane, leader, gbar, wbuf, ctl);
+      else if (a.gw_bf16)
+        block_to_global_bf16(&maps.out, a.H, t.n0 + col0, row0, tbase, r, leader, gbar, gstg);
       else
         block_to_global(&maps.out, a.H, t.n0 + col0, row0, a.accumulate != 0, tbase, r, leader, gbar, gstg);
       ptx::tc_fence_before();

@@ -87,6 +87,7 @@ struct GemmArgs {
   const float* dxacc;   // [C][H] fp32 sum of the grad_hidden splits (splits > 1)
   // MODE_STATS, MODE_DZ
   int skip;             // BWD: SKIP_DX, SKIP_DW
+  int gw_bf16;          // BWD of a call with one chunk: grad_weight tiles are rounded and stored as bf16
   float c2;             // log2(e) / temperature: z c2 is the scaled logit in base-2 units
   float* stats;         // STATS: [3][nparts][C] part max (raw z), sum of 2^d, sum of d 2^d, d = (z - max) c2
   float* zf;            // STATS: [C][ldz] fp32 logits, or null
@@ -142,6 +143,23 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 template <typename T>
 T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws) + off); }
+
+// Launch whose blocks may come up while the previous kernel of the stream still
+// runs; the kernel has to call ptx::grid_dependency_wait() before it reads or
+// writes anything that kernel (or an earlier one) touches.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned blocks, unsigned threads, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
 
 // Elementwise / bookkeeping kernels (flce_aux.cu).
 cudaError_t launch_prep(const int* targets, long long N, int V, int ignore_index,

@@ -69,63 +69,88 @@ __global__ void __launch_bounds__(128)
 
 // One chunk's rows: lane = row (part-major statistics: coalesced), the parts
 // dealt to the block's warps and merged in a fixed order.  Reads 12 bytes per
-// row and part.
-constexpr int ROWS_WARPS = 8;
-__global__ void __launch_bounds__(32 * ROWS_WARPS)
-    logprob_rows_kernel(const int* hdr, const int* __restrict__ idx, long long c0, int C, int nparts,
-                        const float* __restrict__ stats, const float* __restrict__ zt, float c2,
-                        float* __restrict__ logp, float* __restrict__ entropy, float* __restrict__ lse,
-                        float2* __restrict__ ml) {
+// row and part; 32 warps with four parts in flight each, since a block waits
+// for nothing but these loads (1002 parts: 58 us with 8 warps and one part at
+// a time).  Blocks past the chunk's (first chunk only) write the rows left out:
+// 0 for an ignored token, NaN for a target outside [0, V).
+constexpr int ROWS_WARPS = 32;
+constexpr int ROWS_BATCH = 4;
+
+struct RowArgs {
+  const int* hdr;
+  const int* idx;
+  const int* targets;
+  long long c0, N;
+  int C, nparts, ii, K, row_blocks;
+  const float* stats;
+  const float* zt;
+  float c2;
+  float *logp, *entropy, *lse;
+  float2* ml;
+  int* top_ids;
+  float* top_logp;
+};
+
+__global__ void __launch_bounds__(32 * ROWS_WARPS) logprob_rows_kernel(const RowArgs a) {
   __shared__ Stat part[ROWS_WARPS][32];
-  const int Cl = chunk_rows(hdr, c0, C);
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+  if (static_cast<int>(blockIdx.x) >= a.row_blocks) {
+    const long long step = static_cast<long long>(gridDim.x - a.row_blocks) * blockDim.x;
+    for (long long i = a.hdr[HDR_NVALID] + static_cast<long long>(blockIdx.x - a.row_blocks) * blockDim.x + threadIdx.x;
+         i < a.N; i += step) {
+      const long long row = a.idx[i];
+      const float v = a.targets[row] == a.ii ? 0.f : __int_as_float(0x7fc00000);
+      a.logp[row] = v;
+      a.lse[row] = v;
+      if (a.entropy) a.entropy[row] = v;
+      for (int k = 0; k < a.K; ++k) {
+        a.top_ids[row * a.K + k] = -1;
+        a.top_logp[row * a.K + k] = v;
+      }
+    }
+    return;
+  }
+  const int Cl = chunk_rows(a.hdr, a.c0, a.C);
   const int r = blockIdx.x * 32 + lane;
-  if (blockIdx.x * 32 >= Cl) return;
+  if (static_cast<int>(blockIdx.x) * 32 >= Cl) return;
   Stat acc = {-INFINITY, 0.f, 0.f};
   if (r < Cl) {
-    const size_t np = static_cast<size_t>(nparts) * C;
-#pragma unroll 4
-    for (int p = w; p < nparts; p += ROWS_WARPS) {
-      const float* q = stats + static_cast<size_t>(p) * C + r;
-      acc = merge(acc, Stat{q[0], q[np], q[2 * np]}, c2);
+    const size_t np = static_cast<size_t>(a.nparts) * a.C;
+    for (int p0 = w; p0 < a.nparts; p0 += ROWS_BATCH * ROWS_WARPS) {
+      Stat q[ROWS_BATCH];
+#pragma unroll
+      for (int k = 0; k < ROWS_BATCH; ++k) {
+        const int p = p0 + k * ROWS_WARPS;
+        const float* f = a.stats + static_cast<size_t>(p) * a.C + r;
+        q[k] = p < a.nparts ? Stat{f[0], f[np], f[2 * np]} : Stat{-INFINITY, 0.f, 0.f};
+      }
+      static_assert(ROWS_BATCH == 4, "pairwise");
+      acc = merge(acc, merge(merge(q[0], q[1], a.c2), merge(q[2], q[3], a.c2), a.c2), a.c2);
     }
   }
   part[w][lane] = acc;
-  __syncthreads();
-  if (w != 0 || r >= Cl) return;
 #pragma unroll
-  for (int k = 1; k < ROWS_WARPS; ++k) acc = merge(acc, part[k][lane], c2);
-  // after a pipeline time-out the statistics are not to be trusted
-  if (hdr[HDR_STATUS] & STATUS_TIMEOUT) acc.m = __int_as_float(0x7fc00000);
-  const float l2s = log2f(acc.s);
-  const long long row = idx[c0 + r];
-  logp[row] = fmaf(zt[r] - acc.m, c2, -l2s) * LN2;
-  lse[row] = fmaf(acc.m, c2, l2s) * LN2;
-  if (entropy) entropy[row] = fmaf(0.f, acc.m, l2s - acc.d / acc.s) * LN2;   // NaN where the max is not finite
-  if (ml) ml[r] = make_float2(acc.m, l2s);
-}
-
-// Rows left out: 0 for an ignored token, NaN for a target outside [0, V).
-__global__ void logprob_left_out_kernel(const int* hdr, const int* __restrict__ idx, const int* __restrict__ t,
-                                        long long N, int ii, int K, float* logp, float* entropy, float* lse,
-                                        int* top_ids, float* top_logp) {
-  for (long long i = hdr[HDR_NVALID] + static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < N;
-       i += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const long long row = idx[i];
-    const float v = t[row] == ii ? 0.f : __int_as_float(0x7fc00000);
-    logp[row] = v;
-    lse[row] = v;
-    if (entropy) entropy[row] = v;
-    for (int k = 0; k < K; ++k) {
-      top_ids[row * K + k] = -1;
-      top_logp[row * K + k] = v;
-    }
+  for (int o = ROWS_WARPS / 2; o > 0; o >>= 1) {   // fixed order
+    __syncthreads();
+    if (w < o) part[w][lane] = merge(part[w][lane], part[w + o][lane], a.c2);
   }
+  if (w != 0 || r >= Cl) return;
+  acc = part[0][lane];
+  // after a pipeline time-out the statistics are not to be trusted
+  if (a.hdr[HDR_STATUS] & STATUS_TIMEOUT) acc.m = __int_as_float(0x7fc00000);
+  const float l2s = log2f(acc.s);
+  const long long row = a.idx[a.c0 + r];
+  a.logp[row] = fmaf(a.zt[r] - acc.m, a.c2, -l2s) * LN2;
+  a.lse[row] = fmaf(acc.m, a.c2, l2s) * LN2;
+  if (a.entropy) a.entropy[row] = fmaf(0.f, acc.m, l2s - acc.d / acc.s) * LN2;   // NaN where the max is not finite
+  if (a.K > 0) a.ml[r] = make_float2(acc.m, l2s);
 }
 
 // Top alternatives of one row per block: the K best parts by (max, position),
-// then the K best of their logits by (value, id).
+// then the K best of their logits by (value, id).  The loads of eight groups
+// (one or two parts) are in flight at a time.
 constexpr int TOP_WARPS = 4;
+constexpr int TOP_BATCH = 8;
 __global__ void __launch_bounds__(32 * TOP_WARPS)
     logprob_top_kernel(const int* hdr, const int* __restrict__ idx, long long c0, int C, int V, long long ldz,
                        int nparts, int K, const float* __restrict__ stats, const float* __restrict__ zf,
@@ -138,24 +163,38 @@ __global__ void __launch_bounds__(32 * TOP_WARPS)
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   TopK best;
   best.clear();
-  for (int p0 = w * 32; p0 < nparts; p0 += TOP_WARPS * 32) {
-    const int p = p0 + lane;
-    best.offer(p < nparts ? stats[static_cast<size_t>(p) * C + r] : 0.f, p, p < nparts, K, lane);
+  for (int p0 = w * 32; p0 < nparts; p0 += TOP_BATCH * TOP_WARPS * 32) {
+    float x[TOP_BATCH];
+#pragma unroll
+    for (int k = 0; k < TOP_BATCH; ++k) {
+      const int p = p0 + k * (TOP_WARPS * 32) + lane;
+      x[k] = p < nparts ? stats[static_cast<size_t>(p) * C + r] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < TOP_BATCH; ++k) {
+      const int p = p0 + k * (TOP_WARPS * 32) + lane;
+      best.offer(x[k], p, p < nparts, K, lane);
+    }
   }
-  best.merge_block<TOP_WARPS>(sv, si, K, lane, w);   // every warp holds the K best parts
+  best.merge_block<TOP_WARPS>(sv, si, lane, w);   // every warp holds the K best parts
   const int parts = best.id;
   best.clear();
   const float* zr = zf + static_cast<size_t>(r) * ldz;
-  for (int j = w; j < K; j += TOP_WARPS) {
-    const int p = __shfl_sync(0xffffffffu, parts, j);
-    if (p == TopK::NONE) continue;
+  for (int j = w; j < K; j += 2 * TOP_WARPS) {
+    float x[TOP_BATCH];
+    int v[TOP_BATCH];
 #pragma unroll
-    for (int g = 0; g < PART_COLS / 32; ++g) {
-      const long long v = static_cast<long long>(p) * PART_COLS + g * 32 + lane;
-      best.offer(v < V ? zr[v] : 0.f, static_cast<int>(v), v < V, K, lane);
+    for (int k = 0; k < TOP_BATCH; ++k) {
+      const int jj = j + (k / 4) * TOP_WARPS;
+      const int p = __shfl_sync(0xffffffffu, parts, jj & 31);
+      const long long at = static_cast<long long>(p) * PART_COLS + (k % 4) * 32 + lane;
+      v[k] = jj < K && p != TopK::NONE && at < V ? static_cast<int>(at) : -1;
+      x[k] = v[k] >= 0 ? zr[v[k]] : 0.f;
     }
+#pragma unroll
+    for (int k = 0; k < TOP_BATCH; ++k) best.offer(x[k], v[k], v[k] >= 0, K, lane);
   }
-  best.merge_block<TOP_WARPS>(sv, si, K, lane, w);
+  best.merge_block<TOP_WARPS>(sv, si, lane, w);
   if (w == 0 && lane < K) {
     const long long row = idx[c0 + r];
     const bool some = best.id != TopK::NONE;   // false only where fewer than K logits are numbers
@@ -375,12 +414,16 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
 
   const int grid = 2 * static_cast<int>(std::min<long long>(cdiv(p.C, PAIR_M) * p.nvt, dev.pairs));
   auto chk = [](cudaError_t e) { return e == cudaSuccess; };
-  count_launches(2 + p.n_chunks * (top_k > 0 ? 3 : 2));
+  count_launches(1 + p.n_chunks * (top_k > 0 ? 3 : 2));
   if (!chk(launch_prep(targets, N, static_cast<int>(V), ignore_index, hdr, idx, nullptr, counters, p.n_chunks, st)))
     return FLCE_ECUDA;
-  logprob_left_out_kernel<<<static_cast<int>(std::min<long long>(cdiv(N, 256), 1216)), 256, 0, st>>>(
-      hdr, idx, targets, N, ignore_index, top_k, logp, entropy, lse, top_ids, top_logp);
-  if (!chk(cudaGetLastError())) return FLCE_ECUDA;
+  RowArgs ra;
+  ra.hdr = hdr; ra.idx = idx; ra.targets = targets;
+  ra.N = N; ra.C = g.C; ra.nparts = p.nparts; ra.ii = ignore_index; ra.K = top_k;
+  ra.row_blocks = static_cast<int>(cdiv(p.C, 32));
+  ra.stats = stats; ra.zt = zt; ra.c2 = g.c2;
+  ra.logp = logp; ra.entropy = entropy; ra.lse = lse; ra.ml = ml; ra.top_ids = top_ids; ra.top_logp = top_logp;
+  const int left_blocks = static_cast<int>(std::min<long long>(cdiv(N, 32 * ROWS_WARPS), 152));
   for (long long c = 0; c < p.n_chunks; ++c) {
     g.c0 = c * p.C;
     g.counter = counters + c;
@@ -388,8 +431,8 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
                            st)) ||
         !chk(gemm_launch(g, m, grid, st)))
       return FLCE_ECUDA;
-    logprob_rows_kernel<<<static_cast<int>(cdiv(p.C, 32)), 32 * ROWS_WARPS, 0, st>>>(
-        hdr, idx, g.c0, g.C, p.nparts, stats, zt, g.c2, logp, entropy, lse, top_k > 0 ? ml : nullptr);
+    ra.c0 = g.c0;
+    logprob_rows_kernel<<<ra.row_blocks + (c == 0 ? left_blocks : 0), 32 * ROWS_WARPS, 0, st>>>(ra);
     if (!chk(cudaGetLastError())) return FLCE_ECUDA;
     if (top_k > 0) {
       logprob_top_kernel<<<g.C, 32 * TOP_WARPS, 0, st>>>(hdr, idx, g.c0, g.C, g.V, p.ldz, p.nparts, top_k, stats, zf,

@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = ctl->tmem_base;
+  ptx::grid_launch_dependents();   // the merge kernel's blocks may come up; they wait for this grid's end
 
   if (warp == 0 && lane == 0) {
     // ---------------- TMA producer ----------------
@@ -321,18 +322,50 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) a.fail[blockIdx.x] = *reinterpret_cast<volatile int*>(&ctl->abort);
 }
 
-// One token per block: its row from the CTAs' statistics and lists.
+// One token per block: its row from the CTAs' statistics and lists.  Launched
+// while the first kernel drains (programmatic dependent launch); what it reads
+// is loaded in one go, since the latency of a few dependent loads is all there
+// is to it.
 constexpr int MERGE_WARPS = 8;
-__global__ void __launch_bounds__(32 * MERGE_WARPS) logprob_stream_merge_kernel(const StreamArgs a) {
+constexpr int MERGE_THREADS = 32 * MERGE_WARPS;
+constexpr int MERGE_BATCH = 4;   // list entries per thread in flight
+__global__ void __launch_bounds__(MERGE_THREADS) logprob_stream_merge_kernel(const StreamArgs a) {
   __shared__ Stat part[MERGE_WARPS];
   __shared__ float sv[MERGE_WARPS][32];
   __shared__ int si[MERGE_WARPS][32];
   const int n = blockIdx.x, tid = threadIdx.x, lane = tid % 32, w = tid / 32;
-  int failed = 0;
-  for (int b = tid; b < a.ctas; b += 32 * MERGE_WARPS) failed |= a.fail[b];
-  failed = __syncthreads_or(failed);
   const int t = a.targets[n];
   const bool bad = t != a.ii && (t < 0 || t >= a.V);
+  ptx::grid_dependency_wait();
+  const size_t base = static_cast<size_t>(n) * a.ctas * a.K;
+  const int entries = a.ctas * a.K;
+  const float zt = bad || t == a.ii ? 0.f : a.zt[n];
+  float cv[MERGE_BATCH];
+  int ci[MERGE_BATCH];
+  auto fetch = [&](int e0) {
+#pragma unroll
+    for (int k = 0; k < MERGE_BATCH; ++k) {
+      const int e = e0 + k * MERGE_THREADS + tid;
+      ci[k] = e < entries ? a.top_i[base + e] : TopK::NONE;
+      cv[k] = e < entries ? a.top_v[base + e] : 0.f;
+    }
+  };
+  fetch(0);
+  int failed = 0;
+  Stat acc = {-INFINITY, 0.f, 0.f};
+  for (int b = tid; b < a.ctas; b += MERGE_THREADS) {
+    failed |= a.fail[b];
+    const float4 q = a.stat[static_cast<size_t>(n) * a.ctas + b];
+    acc = merge(acc, Stat{q.x, q.y, q.z}, a.c2);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {   // fixed order; lane 0 holds the result
+    const Stat other = {__shfl_down_sync(0xffffffffu, acc.m, o), __shfl_down_sync(0xffffffffu, acc.s, o),
+                        __shfl_down_sync(0xffffffffu, acc.d, o)};
+    acc = merge(acc, other, a.c2);
+  }
+  if (lane == 0) part[w] = acc;
+  failed = __syncthreads_or(failed);
   if (tid == 0 && (failed || bad))
     atomicOr(a.hdr + HDR_STATUS, (failed ? STATUS_TIMEOUT : 0) | (bad ? STATUS_BADTARGET : 0));
   if (failed || bad || t == a.ii) {
@@ -348,39 +381,26 @@ __global__ void __launch_bounds__(32 * MERGE_WARPS) logprob_stream_merge_kernel(
     }
     return;
   }
-  Stat acc = {-INFINITY, 0.f, 0.f};
-  for (int b = tid; b < a.ctas; b += 32 * MERGE_WARPS) {
-    const float4 q = a.stat[static_cast<size_t>(n) * a.ctas + b];
-    acc = merge(acc, Stat{q.x, q.y, q.z}, a.c2);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {   // fixed order; lane 0 holds the result
-    const Stat other = {__shfl_down_sync(0xffffffffu, acc.m, o), __shfl_down_sync(0xffffffffu, acc.s, o),
-                        __shfl_down_sync(0xffffffffu, acc.d, o)};
-    acc = merge(acc, other, a.c2);
-  }
-  if (lane == 0) part[w] = acc;
-  __syncthreads();
   acc = part[0];
 #pragma unroll
   for (int k = 1; k < MERGE_WARPS; ++k) acc = merge(acc, part[k], a.c2);
   const float l2s = log2f(acc.s);
   if (tid == 0) {
-    a.logp[n] = fmaf(a.zt[n] - acc.m, a.c2, -l2s) * LN2;
+    a.logp[n] = fmaf(zt - acc.m, a.c2, -l2s) * LN2;
     a.lse[n] = fmaf(acc.m, a.c2, l2s) * LN2;
     if (a.entropy) a.entropy[n] = fmaf(0.f, acc.m, l2s - acc.d / acc.s) * LN2;
   }
   if (a.K == 0) return;
   TopK best;
   best.clear();
-  const size_t base = static_cast<size_t>(n) * a.ctas * a.K;
-  const int entries = a.ctas * a.K;
-  for (int e0 = w * 32; e0 < entries; e0 += 32 * MERGE_WARPS) {
-    const int e = e0 + lane;
-    const int id = e < entries ? a.top_i[base + e] : TopK::NONE;
-    best.offer(id != TopK::NONE ? a.top_v[base + e] : 0.f, id, id != TopK::NONE, a.K, lane);
+  for (int e0 = 0;;) {
+#pragma unroll
+    for (int k = 0; k < MERGE_BATCH; ++k) best.offer(cv[k], ci[k], ci[k] != TopK::NONE, a.K, lane);
+    e0 += MERGE_BATCH * MERGE_THREADS;
+    if (e0 >= entries) break;
+    fetch(e0);
   }
-  best.merge_block<MERGE_WARPS>(sv, si, a.K, lane, w);
+  best.merge_block<MERGE_WARPS>(sv, si, lane, w);
   if (w == 0 && lane < a.K) {
     const bool some = best.id != TopK::NONE;   // false only where fewer than K logits are numbers
     a.top_ids[static_cast<size_t>(n) * a.K + lane] = some ? best.id : -1;
@@ -425,8 +445,7 @@ cudaError_t launch_stream(const StreamArgs& a, const StreamMaps& m, cudaStream_t
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  logprob_stream_merge_kernel<<<a.N, 32 * MERGE_WARPS, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(logprob_stream_merge_kernel, a.N, MERGE_THREADS, s, a);
 }
 
 }  // namespace flce

@@ -1,6 +1,6 @@
 // A warp's running list of the K <= 32 best (value, id) pairs, best first:
 // larger values first, equal values by the lower id.  Lane j holds entry j;
-// NaN is never taken.  The order of the offers does not change the result.
+// NaN is never taken.  The order of the offers does not change the first K.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -22,18 +22,52 @@ struct TopK {
     id = NONE;
   }
 
+  static __device__ __forceinline__ bool better(float av, int ai, float bv, int bi) {
+    return av > bv || (av == bv && ai < bi);
+  }
+
+  // One compare-exchange with the lane at distance o.
+  static __device__ __forceinline__ void exchange(float& v, int& id, int o, bool keep_better) {
+    const float pv = __shfl_xor_sync(0xffffffffu, v, o);
+    const int pi = __shfl_xor_sync(0xffffffffu, id, o);
+    if (better(pv, pi, v, id) == keep_better) { v = pv; id = pi; }
+  }
+
+  // The 32 best of this list and another sorted one (lane j holds its entry
+  // j): the better of entry i and the other's entry 31 - i are those 32, in a
+  // bitonic order that five exchanges sort.
+  __device__ __forceinline__ void merge(float ov, int oi, int lane) {
+    ov = __shfl_xor_sync(0xffffffffu, ov, 31);
+    oi = __shfl_xor_sync(0xffffffffu, oi, 31);
+    if (better(ov, oi, v, id)) { v = ov; id = oi; }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) exchange(v, id, o, (lane & o) == 0);
+  }
+
   // Every lane offers one candidate (where ok).  Few pass the threshold once
-  // the list has filled, so the loop over those that do is short.
+  // the list has filled: those are inserted one by one; more than a handful
+  // are sorted and merged.
   __device__ __forceinline__ void offer(float cv, int cid, bool ok, int k, int lane) {
     const float tv = __shfl_sync(0xffffffffu, v, k - 1);
     const int ti = __shfl_sync(0xffffffffu, id, k - 1);
-    unsigned m = __ballot_sync(0xffffffffu, ok && (cv > tv || (cv == tv && cid < ti)));
-    while (m) {   // uniform over the warp
+    const bool pass = ok && better(cv, cid, tv, ti);
+    unsigned m = __ballot_sync(0xffffffffu, pass);
+    if (m == 0) return;                    // uniform over the warp, as all below
+    if (__popc(m) > 4) {
+      if (!pass) { cv = -INFINITY; cid = NONE; }
+#pragma unroll
+      for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int o = size / 2; o > 0; o >>= 1) exchange(cv, cid, o, ((lane & o) == 0) == ((lane & size) == 0));
+      merge(cv, cid, lane);
+      return;
+    }
+    while (m) {
       const int src = __ffs(m) - 1;
       m &= m - 1;
       const float nv = __shfl_sync(0xffffffffu, cv, src);
       const int ni = __shfl_sync(0xffffffffu, cid, src);
-      const int pos = __popc(__ballot_sync(0xffffffffu, v > nv || (v == nv && id < ni)));   // entries before it
+      const int pos = __popc(__ballot_sync(0xffffffffu, better(v, id, nv, ni)));   // entries before it
       const float uv = __shfl_up_sync(0xffffffffu, v, 1);
       const int ui = __shfl_up_sync(0xffffffffu, id, 1);
       if (lane > pos) { v = uv; id = ui; }
@@ -43,7 +77,7 @@ struct TopK {
 
   // The lists of the block's WARPS warps become one, held by every warp.
   template <int WARPS>
-  __device__ __forceinline__ void merge_block(float (*sv)[32], int (*si)[32], int k, int lane, int w) {
+  __device__ __forceinline__ void merge_block(float (*sv)[32], int (*si)[32], int lane, int w) {
     __syncthreads();
     sv[w][lane] = v;
     si[w][lane] = id;
@@ -51,7 +85,7 @@ struct TopK {
 #pragma unroll 1
     for (int o = 1; o < WARPS; ++o) {
       const int from = (w + o) % WARPS;
-      offer(sv[from][lane], si[from][lane], lane < k && si[from][lane] != NONE, k, lane);
+      merge(sv[from][lane], si[from][lane], lane);
     }
   }
 };

@@ -401,17 +401,38 @@ class LinearCrossEntropy(torch.nn.Module):
 TOP_K_MAX = 32
 
 
-@contextlib.contextmanager
-def _on(device, stream):
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+class _on:
     """The device and stream of a call: outputs and workspaces allocated inside
-    belong to that stream, so their memory is reused only behind its work."""
-    with torch.cuda.device(device):
+    belong to that stream, so their memory is reused only behind its work.  The
+    usual call (current device, current stream) switches nothing: entering
+    torch's device and stream contexts costs 18 us, several times the launch of
+    a small kernel."""
+
+    __slots__ = ("device", "stream", "contexts")
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.contexts = device, stream, None
+
+    def __enter__(self) -> int:
+        if self.stream is None and self.device.index == torch.cuda.current_device():
+            return torch._C._cuda_getCurrentRawStream(self.device.index)
+        self.contexts = contextlib.ExitStack()
+        self.contexts.enter_context(torch.cuda.device(self.device))
+        stream = self.stream
         if stream is None:
-            stream = torch.cuda.current_stream(device)
+            stream = torch.cuda.current_stream(self.device)
         elif not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        with torch.cuda.stream(stream):
-            yield ctypes.c_void_p(stream.cuda_stream)
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        self.contexts.enter_context(torch.cuda.stream(stream))
+        return stream.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.contexts is not None:
+            self.contexts.__exit__(*exc)
 
 
 def _check_buffer(t, name, shape, dtype, device):
@@ -473,9 +494,9 @@ def token_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Te
         o = _outputs(out, {"logp": row, "lse": row, "entropy": row if entropy else None,
                            "top_ids": ((N, top_k), torch.int32) if top_k else None,
                            "top_logp": ((N, top_k), torch.float32) if top_k else None}, dev)
-        _ok(library().flce_logprobs(_ptr(hidden), _ptr(weight), _ptr(targets), N, H, V, int(ignore_index),
-                                    float(temperature), top_k, _ptr(o["logp"]), _ptr(o["entropy"]), _ptr(o["lse"]),
-                                    _ptr(o["top_ids"]), _ptr(o["top_logp"]), _ptr(workspace), workspace.numel(), st),
+        _ok(library().flce_logprobs(_addr(hidden), _addr(weight), _addr(targets), N, H, V, int(ignore_index),
+                                    float(temperature), top_k, _addr(o["logp"]), _addr(o["entropy"]), _addr(o["lse"]),
+                                    _addr(o["top_ids"]), _addr(o["top_logp"]), _addr(workspace), workspace.numel(), st),
             "flce_logprobs")
     o["workspace"] = workspace
     return o
@@ -514,10 +535,10 @@ def token_logprobs_bwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torc
         _check_workspace(workspace, dev)
         o = _outputs(out, {"grad_hidden": ((N, H), torch.bfloat16) if need_hidden else None,
                            "grad_weight": ((V, H), grad_weight_dtype) if need_weight else None}, dev)
-        _ok(library().flce_logprobs_bwd(_ptr(hidden), _ptr(weight), _ptr(targets), N, H, V, int(ignore_index), flags,
-                                        float(temperature), _ptr(lse), _ptr(entropy), _ptr(grad_logp),
-                                        _ptr(grad_entropy), _ptr(o["grad_hidden"]), _ptr(o["grad_weight"]),
-                                        _ptr(workspace), workspace.numel(), st), "flce_logprobs_bwd")
+        _ok(library().flce_logprobs_bwd(_addr(hidden), _addr(weight), _addr(targets), N, H, V, int(ignore_index), flags,
+                                        float(temperature), _addr(lse), _addr(entropy), _addr(grad_logp),
+                                        _addr(grad_entropy), _addr(o["grad_hidden"]), _addr(o["grad_weight"]),
+                                        _addr(workspace), workspace.numel(), st), "flce_logprobs_bwd")
     o["workspace"] = workspace
     return o
 
@@ -604,8 +625,8 @@ def embedding_fwd(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *
     dev = _check_same_device(weight, ids)
     with _on(dev, stream) as st:
         out = _outputs({"out": out}, {"out": ((N, H), weight.dtype)}, dev)["out"]
-        _ok(library().flce_embedding(_ptr(weight), _ptr(ids), N, H, V, EMBEDDING_DTYPES[weight.dtype], float(scale),
-                                     _ptr(out), st), "flce_embedding")
+        _ok(library().flce_embedding(_addr(weight), _addr(ids), N, H, V, EMBEDDING_DTYPES[weight.dtype], float(scale),
+                                     _addr(out), st), "flce_embedding")
     return out
 
 
@@ -638,10 +659,10 @@ def embedding_bwd(grad_out: torch.Tensor, ids: torch.Tensor, num_rows: int, scal
             workspace = new_workspace(nb, dev)
         _check_workspace(workspace, dev)
         o = _outputs(out, {"grad_weight": ((V, H), grad_weight_dtype)}, dev)
-        _ok(library().flce_embedding_bwd(_ptr(grad_out), _ptr(ids), N, H, V, EMBEDDING_DTYPES[grad_out.dtype],
+        _ok(library().flce_embedding_bwd(_addr(grad_out), _addr(ids), N, H, V, EMBEDDING_DTYPES[grad_out.dtype],
                                          float(scale), -1 if padding_idx is None else int(padding_idx),
-                                         FLCE_ACCUMULATE if accumulate else 0, _ptr(o["grad_weight"]),
-                                         EMBEDDING_DTYPES[grad_weight_dtype], _ptr(workspace), workspace.numel(), st),
+                                         FLCE_ACCUMULATE if accumulate else 0, _addr(o["grad_weight"]),
+                                         EMBEDDING_DTYPES[grad_weight_dtype], _addr(workspace), workspace.numel(), st),
             "flce_embedding_bwd")
     o["workspace"] = workspace
     return o

@@ -233,6 +233,29 @@ def test_gradients(env, N, H, V, ignored, T, gl, ge, bf16, grid):
     assert torch.equal(one["grad_hidden"], d["grad_hidden"]) and torch.equal(two["grad_weight"], d["grad_weight"])
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+def test_gradients_in_chunks(env, bf16):
+    """A workspace for 128 rows: grad_weight accumulates over chunks in fp32 and is rounded at the end."""
+    flce, torch, dev = env
+    N, H, V = 700, 136, 1000
+    X, W, t = problem(N, H, V, seed=3, ignored=0.1)
+    g = np.random.default_rng(1).standard_normal(N).astype(np.float32)
+    h, w, tt = to_gpu(torch, dev, X, W, t)
+    tg = torch.from_numpy(g).to(dev)
+    dt = torch.bfloat16 if bf16 else torch.float32
+    o = flce.token_logprobs(h, w, tt)
+    nb = flce.workspace_bytes(N, H, V, chunk_rows=128, grad_weight_dtype=dt) + 4096   # and the rows' constants
+    d = flce.token_logprobs_bwd(h, w, tt, o["lse"], None, tg, grad_weight_dtype=dt, workspace=flce.new_workspace(nb, dev))
+    ref = logprobs_grad_oracle(X, W, t, g, None)
+    for k, rounds in (("hidden", 1), ("weight", int(bf16))):
+        tol = ref["mag_" + k] * (2.0 ** -8 + 2e-4) * (1 + 2.0 ** -8) + rounds * 2.0 ** -8 * np.abs(ref["grad_" + k])
+        assert np.all(np.abs(np64(d["grad_" + k]) - ref["grad_" + k]) <= tol + 1e-30), k
+    whole = flce.token_logprobs_bwd(h, w, tt, o["lse"], None, tg, grad_weight_dtype=dt)
+    assert torch.equal(whole["grad_hidden"], d["grad_hidden"])   # complete per chunk
+    none = flce.token_logprobs_bwd(h, w, torch.full_like(tt, -100), o["lse"], None, tg, grad_weight_dtype=dt)
+    assert not none["grad_hidden"].any() and not none["grad_weight"].any()
+
+
 def test_autograd_step(env):
     """A clipped policy-gradient loss through the module, against autograd in fp64."""
     flce, torch, dev = env

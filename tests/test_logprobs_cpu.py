@@ -62,9 +62,10 @@ def test_workspace_sizes(flce):
     assert 0 < lib.flce_logprobs_workspace_bytes(N, H, V, 0) <= 0.05 * N * V * 2
     assert 0 < lib.flce_logprobs_workspace_bytes(64, H, V, 8) <= 256 << 20
     assert 0 < lib.flce_logprobs_workspace_bytes(N, H, V, 8) <= 1 << 30
-    assert 0 < lib.flce_logprobs_bwd_workspace_bytes(N, H, V, 0) <= 1 << 30
-    assert 0 < lib.flce_logprobs_bwd_workspace_bytes(8 * N, H, V, 0) <= 0.05 * 8 * N * V * 2
-    assert lib.flce_logprobs_bwd_workspace_bytes(N, H, V, 2) > V * H * 4
+    assert 0 < lib.flce_logprobs_bwd_workspace_bytes(N, H, V, 0) <= 2 << 30
+    assert 0 < lib.flce_logprobs_bwd_workspace_bytes(16 * N, H, V, 0) <= 0.05 * 16 * N * V * 2
+    assert lib.flce_logprobs_bwd_workspace_bytes(N, H, V, 2) > V * H * 4   # the accumulator of several chunks
+    assert lib.flce_logprobs_bwd_workspace_bytes(4096, H, V, 2) < 2 << 30  # one chunk: none
     for bad in [(0, H, V, 0), (N, 63, V, 0), (N, H, V, 33), (N, H, 4, 5), (N, H, V, -1)]:
         assert lib.flce_logprobs_workspace_bytes(*bad) == 0
     assert lib.flce_logprobs_bwd_workspace_bytes(N, H, V, 1) == 0
