@@ -64,6 +64,7 @@ cudaError_t device_state(DeviceState* out) {
     if ((e = cudaDeviceGetAttribute(&d.major, cudaDevAttrComputeCapabilityMajor, dev)) != cudaSuccess) return e;
     if ((e = gemm_prepare(dev)) != cudaSuccess) return e;
     if ((e = stream_prepare()) != cudaSuccess) return e;
+    if ((e = embedding_prepare()) != cudaSuccess) return e;
     if ((e = gemm_max_pairs(&d.pairs)) != cudaSuccess) return e;
     if (d.pairs < 1) return cudaErrorInvalidConfiguration;
     d.ready = true;

@@ -14,8 +14,8 @@
 //             that crosses a chunk's edge leaves a partial sum per chunk.
 //   join      the partial sums of each crossing run, in chunk order.
 // In the same launch as the segments, the rows of ids that do not occur are
-// set to zero (found by binary search in the sorted ids), so the dense
-// gradient is written exactly once.
+// set to zero, so the dense gradient is written exactly once; these blocks
+// need the ids only, not their order, and run while the sort does.
 #include <algorithm>
 #include <cuda_fp16.h>
 
@@ -170,11 +170,24 @@ __device__ __forceinline__ int sort_key(const int* ids, long long i, int V, int 
 // invariant and moved ahead of the wait.  All positions, tokens and ids read
 // back from the workspace are checked against their arrays before use.
 
+// Lanes of the warp with the same digit (of `bits` bits) as this one, among
+// those with ok; one ballot per bit.
+__device__ __forceinline__ unsigned same_digit(int d, int bits, bool ok) {
+  unsigned m = __ballot_sync(0xffffffffu, ok);
+  for (int b = 0; b < bits; ++b) {
+    const bool on = (d >> b) & 1;
+    const unsigned y = __ballot_sync(0xffffffffu, on);
+    m &= on ? y : ~y;
+  }
+  return m;
+}
+
 // Counts of one digit, per tile.  FIRST: the keys come from the ids, and ids
 // outside the table are flagged per tile.
 template <bool FIRST, int ITEMS>
 __global__ void __launch_bounds__(SORT_THREADS)
-    sort_count_kernel(const int* keys, int N, int V, int padding, int* bad, int shift, int bits, int* counts) {
+    sort_count_kernel(const int* ids, const int2* items, int N, int V, int padding, int* bad, int shift, int bits,
+                      int* counts) {
   __shared__ int bin[SORT_BINS];
   ptx::grid_launch_dependents();
   bin[threadIdx.x] = 0;
@@ -187,8 +200,8 @@ __global__ void __launch_bounds__(SORT_THREADS)
   for (int k = 0; k < ITEMS; ++k) {
     const long long i = base + k * SORT_THREADS + threadIdx.x;
     if (i < N) {
-      const int key = FIRST ? sort_key(keys, i, V, padding) : keys[i];
-      if (FIRST && key == V) outside |= keys[i] < 0 || keys[i] >= V;
+      const int key = FIRST ? sort_key(ids, i, V, padding) : items[i].x;
+      if (FIRST && key == V) outside |= ids[i] < 0 || ids[i] >= V;
       atomicAdd(&bin[(key >> shift) & mask], 1);
     }
   }
@@ -197,6 +210,7 @@ __global__ void __launch_bounds__(SORT_THREADS)
   if (FIRST && threadIdx.x == 0) bad[blockIdx.x] = outside;
 }
 
+template <int WARPS>
 __device__ __forceinline__ int block_exclusive_scan(int x, int* scratch) {
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   int inc = x;
@@ -208,14 +222,14 @@ __device__ __forceinline__ int block_exclusive_scan(int x, int* scratch) {
   if (lane == 31) scratch[w] = inc;
   __syncthreads();
   if (w == 0) {
-    const int t = lane < SORT_WARPS ? scratch[lane] : 0;
+    const int t = lane < WARPS ? scratch[lane] : 0;
     int ti = t;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(0xffffffffu, ti, o);
       if (lane >= o) ti += y;
     }
-    if (lane < SORT_WARPS) scratch[lane] = ti - t;
+    if (lane < WARPS) scratch[lane] = ti - t;
   }
   __syncthreads();
   return scratch[w] + inc - x;
@@ -226,8 +240,8 @@ __device__ __forceinline__ int block_exclusive_scan(int x, int* scratch) {
 // ranks its 32 x ITEMS consecutive items in order, so the sort is stable.
 template <bool FIRST, int ITEMS>
 __global__ void __launch_bounds__(SORT_THREADS)
-    sort_scatter_kernel(const int* keys, const int* toks, int N, int V, int padding, int shift, int bits,
-                        const int* counts, int tiles, int* out_keys, int* out_toks) {
+    sort_scatter_kernel(const int* ids, const int2* items, int N, int V, int padding, int shift, int bits,
+                        const int* counts, int tiles, int2* out) {
   __shared__ int cnt[SORT_WARPS][SORT_BINS];
   __shared__ int scratch[32];
   const int tid = threadIdx.x, lane = tid % 32, w = tid / 32;
@@ -235,14 +249,15 @@ __global__ void __launch_bounds__(SORT_THREADS)
   for (int k = 0; k < SORT_WARPS; ++k) cnt[k][tid] = 0;
   __syncthreads();
   const int mask = (1 << bits) - 1;
-  int key[ITEMS], tok[ITEMS], rank[ITEMS];
+  int2 it[ITEMS];
+  int rank[ITEMS];
   const long long base = static_cast<long long>(blockIdx.x) * (SORT_THREADS * ITEMS) + w * (32 * ITEMS);
   ptx::grid_dependency_wait();
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {
     const long long i = base + k * 32 + lane;
-    key[k] = i < N ? (FIRST ? sort_key(keys, i, V, padding) : keys[i]) : -1;
-    tok[k] = FIRST ? static_cast<int>(i) : (i < N ? toks[i] : 0);
+    it[k] = make_int2(-1, 0);
+    if (i < N) it[k] = FIRST ? make_int2(sort_key(ids, i, V, padding), static_cast<int>(i)) : items[i];
   }
   // thread d: total of digit d and its items in earlier tiles
   int total = 0, earlier = 0;
@@ -255,8 +270,8 @@ __global__ void __launch_bounds__(SORT_THREADS)
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {
     const bool ok = base + k * 32 + lane < N;
-    const int d = ok ? (key[k] >> shift) & mask : SORT_BINS;   // past the end: a group of their own
-    const unsigned same = __match_any_sync(0xffffffffu, d);
+    const int d = (it[k].x >> shift) & mask;
+    const unsigned same = same_digit(d, bits, ok);
     int before = 0;
     if (ok) before = cnt[w][d];
     __syncwarp();
@@ -265,7 +280,7 @@ __global__ void __launch_bounds__(SORT_THREADS)
     rank[k] = before + __popc(same & ((1u << lane) - 1u));
   }
   __syncthreads();
-  int off = block_exclusive_scan(total, scratch) + earlier;   // then the warps' offsets
+  int off = block_exclusive_scan<SORT_WARPS>(total, scratch) + earlier;   // then the warps' offsets
   for (int k = 0; k < SORT_WARPS; ++k) {
     const int c = cnt[k][tid];
     cnt[k][tid] = off;
@@ -275,12 +290,114 @@ __global__ void __launch_bounds__(SORT_THREADS)
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {
     if (base + k * 32 + lane < N) {
-      const int pos = cnt[w][(key[k] >> shift) & mask] + rank[k];
-      if (static_cast<unsigned>(pos) < static_cast<unsigned>(N)) {
-        out_keys[pos] = key[k];
-        out_toks[pos] = tok[k];
+      const int pos = cnt[w][(it[k].x >> shift) & mask] + rank[k];
+      if (static_cast<unsigned>(pos) < static_cast<unsigned>(N)) out[pos] = it[k];
+    }
+  }
+}
+
+// The whole sort of up to 16384 tokens in one launch: a cluster of eight blocks
+// holds the items in registers, adds up its digit counts through distributed
+// shared memory and moves the items through L2 between passes.  (Past that the
+// scattered stores of eight SMs take longer than three more launches.)
+constexpr int CS_BLOCKS = 8;
+constexpr int CS_THREADS = 1024;
+constexpr int CS_WARPS = CS_THREADS / 32;
+constexpr int CS_MAX_ITEMS = 2;
+constexpr long long CS_MAX = static_cast<long long>(CS_BLOCKS) * CS_THREADS * CS_MAX_ITEMS;
+constexpr int CS_SMEM = (CS_WARPS + 1) * SORT_BINS * 4;
+
+struct ClusterSort {
+  const int* ids;
+  int N, V, padding, passes, bits;
+  int* bad;
+  int2 *items0, *items1;   // even passes write 0
+};
+
+template <int ITEMS>
+__global__ void __cluster_dims__(CS_BLOCKS, 1, 1) __launch_bounds__(CS_THREADS)
+    sort_cluster_kernel(const ClusterSort a) {
+  extern __shared__ int sort_smem[];
+  int(*cnt)[SORT_BINS] = reinterpret_cast<int(*)[SORT_BINS]>(sort_smem);   // [CS_WARPS][SORT_BINS]
+  int* hist = sort_smem + CS_WARPS * SORT_BINS;                            // this block's counts, read by the others
+  __shared__ int scratch[32];
+  const int tid = threadIdx.x, lane = tid % 32, w = tid / 32;
+  const int rank_ = static_cast<int>(ptx::cluster_ctarank());
+  const int base = (rank_ * CS_THREADS + w * 32) * ITEMS;
+  const int mask = (1 << a.bits) - 1;
+  ptx::grid_launch_dependents();
+  int2 it[ITEMS];
+  int rank[ITEMS];
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const int shift = pass * a.bits;
+    const int2* in = pass & 1 ? a.items0 : a.items1;
+    int2* out = pass & 1 ? a.items1 : a.items0;
+    int outside = 0;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const int i = base + k * 32 + lane;
+      it[k] = make_int2(-1, i);
+      if (i < a.N) {
+        if (pass == 0) {
+          const int v = a.ids[i];
+          const bool bad = v < 0 || v >= a.V;
+          outside |= bad;
+          it[k].x = bad || v == a.padding ? a.V : v;
+        } else {
+          it[k] = __ldcg(in + i);
+        }
       }
     }
+    for (int k = 0; k < CS_WARPS * SORT_BINS / CS_THREADS; ++k) sort_smem[k * CS_THREADS + tid] = 0;
+    outside = __syncthreads_or(outside);
+    if (pass == 0 && tid == 0) a.bad[rank_] = outside;
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      const bool ok = base + k * 32 + lane < a.N;
+      const int d = (it[k].x >> shift) & mask;
+      const unsigned same = same_digit(d, a.bits, ok);
+      int before = 0;
+      if (ok) before = cnt[w][d];
+      __syncwarp();
+      if (ok && lane == __ffs(same) - 1) cnt[w][d] = before + __popc(same);
+      __syncwarp();
+      rank[k] = before + __popc(same & ((1u << lane) - 1u));
+    }
+    __syncthreads();
+    if (tid < SORT_BINS) {
+      int t = 0;
+#pragma unroll
+      for (int k = 0; k < CS_WARPS; ++k) t += cnt[k][tid];
+      hist[tid] = t;
+    }
+    ptx::cluster_sync();
+    int total = 0, earlier = 0;
+    if (tid < SORT_BINS) {
+#pragma unroll
+      for (int b = 0; b < CS_BLOCKS; ++b) {
+        const int c = ptx::ld_shared_cluster(ptx::map_to_rank(hist + tid, b));
+        total += c;
+        earlier += b < rank_ ? c : 0;
+      }
+    }
+    int off = block_exclusive_scan<CS_WARPS>(total, scratch) + earlier;
+    if (tid < SORT_BINS) {
+#pragma unroll
+      for (int k = 0; k < CS_WARPS; ++k) {
+        const int c = cnt[k][tid];
+        cnt[k][tid] = off;
+        off += c;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      if (base + k * 32 + lane < a.N) {
+        const int pos = cnt[w][(it[k].x >> shift) & mask] + rank[k];
+        if (static_cast<unsigned>(pos) < static_cast<unsigned>(a.N)) out[pos] = it[k];
+      }
+    }
+    ptx::cluster_sync();   // the items have moved, and no block reads this one's counts any more
   }
 }
 
@@ -291,10 +408,10 @@ constexpr int SEG_WARPS = 8;
 constexpr int MIN_CHUNK = 32;          // sorted entries per chunk, and
 constexpr int MAX_CHUNKS = 4096;       // at most this many chunks (two partial sums of H floats each)
 constexpr int ZERO_ROWS = 32;          // grad_weight rows a warp looks up at once
+constexpr int ZERO_MAX_ROWS = 8192;    // rows a block marks at most (1 KB of bits)
 
 struct SegArgs {
-  const int* keys;       // sorted ids, [N]
-  const int* toks;
+  const int2* items;     // (id, token) sorted by id, [N]
   const unsigned char* dout;
   int N, H, V;
   int chunk;             // entries per chunk
@@ -306,7 +423,12 @@ struct SegArgs {
   int* hdr;
   const int* bad;        // [tiles] whether a tile of the first sort pass held an id outside the table
   int tiles;
-  long long seg_warps;   // warps of the first kind; the others set rows to zero
+  const int* ids;        // the unsorted ids, and
+  int padding;
+  int scan;              // whether the zeroing blocks go by them
+  int seg_blocks;        // blocks that add up runs, and
+  int zero_blocks;       // blocks that set rows to zero
+  int zero_rows;         // rows per such block
 };
 
 template <typename O>
@@ -331,29 +453,28 @@ __device__ __forceinline__ void segments(const SegArgs& a, long long warp, int l
   const int h = slice * COLS + lane * 8;
   const bool live = h < a.H;
   const int i0 = c * a.chunk, i1 = min(a.N, i0 + a.chunk);
-  const int before = i0 > 0 ? a.keys[i0 - 1] : -1;
-  const int after = i1 < a.N ? a.keys[i1] : a.V;
+  const int before = i0 > 0 ? a.items[i0 - 1].x : -1;
+  const int after = i1 < a.N ? a.items[i1].x : a.V;
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   const unsigned nv = static_cast<unsigned>(a.V), nn = static_cast<unsigned>(a.N);
-  int cur = a.keys[i0];
+  int cur = a.items[i0].x;
   bool came_in = cur == before;
   for (int g0 = i0; g0 < i1; g0 += 32) {
     const int m = min(32, i1 - g0);
-    const int my_key = lane < m ? a.keys[g0 + lane] : a.V;
-    const int my_tok = lane < m ? a.toks[g0 + lane] : 0;
+    const int2 my = lane < m ? a.items[g0 + lane] : make_int2(a.V, 0);
     for (int j0 = 0; j0 < m; j0 += SEG_ROWS) {
       typename T::Raw x[SEG_ROWS];
 #pragma unroll
       for (int q = 0; q < SEG_ROWS; ++q) {
-        const unsigned key = __shfl_sync(0xffffffffu, my_key, j0 + q);
-        const unsigned tok = __shfl_sync(0xffffffffu, my_tok, j0 + q);
+        const unsigned key = __shfl_sync(0xffffffffu, my.x, j0 + q);
+        const unsigned tok = __shfl_sync(0xffffffffu, my.y, j0 + q);
         if (live && key < nv && tok < nn)
           x[q] = *reinterpret_cast<const typename T::Raw*>(a.dout + (static_cast<long long>(tok) * a.H + h) * T::SIZE);
       }
 #pragma unroll
       for (int q = 0; q < SEG_ROWS; ++q) {
         if (j0 + q >= m) break;
-        const int key = __shfl_sync(0xffffffffu, my_key, j0 + q);
+        const int key = __shfl_sync(0xffffffffu, my.x, j0 + q);
         if (key != cur) {   // uniform over the warp: the run ends inside the chunk
           if (live && static_cast<unsigned>(cur) < nv) {
             if (came_in) F32::store(a.part + (2ll * c) * a.H + h, s);
@@ -380,11 +501,11 @@ __device__ __forceinline__ void segments(const SegArgs& a, long long warp, int l
 }
 
 // First position whose key is >= v.
-__device__ __forceinline__ int lower_bound(const int* keys, int n, int v) {
+__device__ __forceinline__ int lower_bound(const int2* items, int n, int v) {
   int lo = 0, len = n;
   while (len > 0) {
     const int half = len / 2;
-    if (keys[lo + half] < v) {
+    if (items[lo + half].x < v) {
       lo += half + 1;
       len -= half + 1;
     } else {
@@ -394,47 +515,105 @@ __device__ __forceinline__ int lower_bound(const int* keys, int n, int v) {
   return lo;
 }
 
-template <typename T, typename O>
-__global__ void __launch_bounds__(32 * SEG_WARPS, 2) embedding_segments_kernel(const SegArgs a) {
-  const long long warp = static_cast<long long>(blockIdx.x) * SEG_WARPS + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  ptx::grid_launch_dependents();
-  ptx::grid_dependency_wait();
-  if (warp < a.seg_warps) {
-    if (warp < static_cast<long long>(a.n_chunks) * a.slices) segments<T, O>(a, warp, lane);
-    return;
+// The rows of one block whose id does not occur.  With `scan`, the block reads
+// all the ids (from L2) and marks those of its rows, so it need not wait for
+// the sort; else it looks its rows up in the sorted ids.
+template <typename O>
+__device__ __forceinline__ void zero_absent(const SegArgs& a, int block, unsigned* seen) {
+  constexpr int THREADS = 32 * SEG_WARPS;
+  const long long r0 = static_cast<long long>(block) * a.zero_rows;
+  const long long r1 = min(r0 + a.zero_rows, static_cast<long long>(a.V));
+  const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+  if (a.scan) {
+    for (int i = threadIdx.x; i < ZERO_MAX_ROWS / 32; i += THREADS) seen[i] = 0;
+    __syncthreads();
+#pragma unroll 8
+    for (int i = threadIdx.x; i < a.N; i += THREADS) {
+      const int v = a.ids[i];
+      if (v >= r0 && v < r1 && v != a.padding) {
+        const int k = static_cast<int>(v - r0);
+        atomicOr(&seen[k / 32], 1u << (k % 32));
+      }
+    }
+    __syncthreads();
   }
-  // rows whose id does not occur
-  const long long r0 = (warp - a.seg_warps) * ZERO_ROWS;
-  if (r0 >= a.V) return;
-  bool absent = false;
-  if (r0 + lane < a.V) {
-    const int v = static_cast<int>(r0 + lane);
-    const int at = lower_bound(a.keys, a.N, v);
-    absent = at >= a.N || a.keys[at] != v;
-  }
-  unsigned m = __ballot_sync(0xffffffffu, absent);
-  const int row_bytes = a.H * O::SIZE;
-  while (m) {
-    const int k = __ffs(m) - 1;
-    m &= m - 1;
-    uint4* p = reinterpret_cast<uint4*>(a.gw + (r0 + k) * row_bytes);
-    for (int i = lane; i < row_bytes / 16; i += 32) p[i] = make_uint4(0u, 0u, 0u, 0u);
+  const long long row_bytes = static_cast<long long>(a.H) * O::SIZE;
+  for (long long q0 = r0; q0 < r1; q0 += ZERO_ROWS) {
+    unsigned m;   // rows q0 + k that do not occur
+    if (a.scan) {
+      m = ~seen[(q0 - r0) / 32];
+      if (r1 - q0 < 32) m &= (1u << (r1 - q0)) - 1u;
+    } else {
+      bool absent = false;
+      if (q0 + lane < r1) {
+        const int v = static_cast<int>(q0 + lane);
+        const int at = lower_bound(a.items, a.N, v);
+        absent = at >= a.N || a.items[at].x != v;
+      }
+      m = __ballot_sync(0xffffffffu, absent);
+    }
+    for (int n = 0; m; ++n) {   // dealt to the warps
+      const int k = __ffs(m) - 1;
+      m &= m - 1;
+      if (n % SEG_WARPS != w) continue;
+      uint4* p = reinterpret_cast<uint4*>(a.gw + (q0 + k) * row_bytes);
+      for (int i = lane; i < row_bytes / 16; i += 32) p[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
   }
 }
 
+template <typename T, typename O>
+__global__ void __launch_bounds__(32 * SEG_WARPS, 2) embedding_segments_kernel(const SegArgs a) {
+  __shared__ unsigned seen[ZERO_MAX_ROWS / 32];
+  ptx::grid_launch_dependents();
+  // zeroing blocks that need not wait come first, others last
+  const int first = a.scan ? 0 : a.seg_blocks;
+  const int block = static_cast<int>(blockIdx.x);
+  if (block >= first && block < first + a.zero_blocks) {
+    // the sort's first kernel starts behind everything before the call, so
+    // grad_weight may be written from here on
+    if (!a.scan) ptx::grid_dependency_wait();
+    zero_absent<O>(a, block - first, seen);
+    return;
+  }
+  ptx::grid_dependency_wait();
+  const long long warp = static_cast<long long>(block - (a.scan ? a.zero_blocks : 0)) * SEG_WARPS + threadIdx.x / 32;
+  if (warp < static_cast<long long>(a.n_chunks) * a.slices) segments<T, O>(a, warp, threadIdx.x % 32);
+}
+
 // A run that goes out of chunk c and comes into c + 1, c + 2, ...: its partial
-// sums.  One block per chunk and column slice; the chain (a token that makes a
-// tenth of 65536 has 200 links) is cut in as many equal parts as there are
-// warps, and their sums are added in order.
+// sums.  A block looks at eight chunks (of one column slice), one per warp.  A
+// short chain is added up by its warp; a long one (a token that makes a tenth
+// of 65536 has 200 links) by the whole block, cut in as many equal parts as
+// there are warps, whose sums are added in order.
 constexpr int JOIN_WARPS = 8;
-constexpr int JOIN_LINKS = 4;          // partial sums a warp has in flight
+constexpr int JOIN_LINKS = 8;          // partial sums a warp has in flight
+constexpr int JOIN_SHORT = JOIN_LINKS;
+
+__device__ __forceinline__ void add_links(const SegArgs& a, int k0, int k1, int h, float (&s)[8]) {
+  for (int k = k0; k < k1; k += JOIN_LINKS) {
+    F32::Raw x[JOIN_LINKS];
+#pragma unroll
+    for (int q = 0; q < JOIN_LINKS; ++q)
+      if (k + q < k1) x[q] = *reinterpret_cast<const F32::Raw*>(a.part + (2ll * (k + q)) * a.H + h);
+#pragma unroll
+    for (int q = 0; q < JOIN_LINKS; ++q) {
+      if (k + q >= k1) break;
+      float f[8];
+      F32::unpack(x[q], f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] += f[j];
+    }
+  }
+}
 
 template <typename O>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) embedding_join_kernel(const SegArgs a) {
   __shared__ __align__(16) float sums[JOIN_WARPS][COLS];
+  __shared__ int links[JOIN_WARPS];   // of the long chains, else 0
   const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int c = static_cast<int>(blockIdx.x / a.slices), slice = static_cast<int>(blockIdx.x % a.slices);
+  const int c0 = static_cast<int>(blockIdx.x / a.slices) * JOIN_WARPS;
+  const int h = static_cast<int>(blockIdx.x % a.slices) * COLS + lane * 8;
   ptx::grid_dependency_wait();
   if (blockIdx.x == 0) {   // the status word of the call
     int outside = 0;
@@ -445,45 +624,64 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) embedding_join_kernel(const S
       a.hdr[HDR_STALL] = a.hdr[HDR_STALL_COUNT] = 0;
     }
   }
-  const int i0 = c * a.chunk, i1 = min(a.N, i0 + a.chunk);
-  if (i1 >= a.N) return;   // uniform over the block, as the following
-  const int v = a.keys[i1 - 1];
-  if (static_cast<unsigned>(v) >= static_cast<unsigned>(a.V) || a.keys[i1] != v) return;
-  if (i0 > 0 && a.keys[i0] == v && a.keys[i0 - 1] == v) return;   // the run began in an earlier chunk
-  const int h = slice * COLS + lane * 8;
-  const int last = (lower_bound(a.keys, a.N, v + 1) - 1) / a.chunk;   // the run's last chunk
-  const int links = last - c;
-  const int k0 = c + 1 + static_cast<int>(static_cast<long long>(links) * w / JOIN_WARPS);
-  const int k1 = c + 1 + static_cast<int>(static_cast<long long>(links) * (w + 1) / JOIN_WARPS);
-  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (h < a.H) {
-    if (w == 0) load8<F32>(a.part + (2ll * c + 1) * a.H + h, s);
-    for (int k = k0; k < k1; k += JOIN_LINKS) {
-      F32::Raw x[JOIN_LINKS];
+  // this warp's chunk: does a run begin in it and go out, and how many chunks
+  // does it come into?
+  const int c = c0 + w;
+  int n = 0;
+  const long long i0 = static_cast<long long>(c) * a.chunk, i1 = i0 + a.chunk;
+  if (i1 < a.N) {
+    const int v = a.items[i1 - 1].x;
+    const bool from_before = i0 > 0 && a.items[i0 - 1].x == v;
+    if (static_cast<unsigned>(v) < static_cast<unsigned>(a.V) && !from_before) {
+      for (bool more = true; more;) {   // 128 chunks at a time; uniform over the warp
+        int key[4];
 #pragma unroll
-      for (int q = 0; q < JOIN_LINKS; ++q)
-        if (k + q < k1) x[q] = *reinterpret_cast<const F32::Raw*>(a.part + (2ll * (k + q)) * a.H + h);
+        for (int q = 0; q < 4; ++q) {   // first entries of later chunks
+          const long long at = (static_cast<long long>(c) + 1 + n + q * 32 + lane) * a.chunk;
+          key[q] = at < a.N ? a.items[at].x : -1;
+        }
 #pragma unroll
-      for (int q = 0; q < JOIN_LINKS; ++q) {
-        if (k + q >= k1) break;
-        float f[8];
-        F32::unpack(x[q], f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[j] += f[j];
+        for (int q = 0; q < 4; ++q) {
+          if (!more) continue;
+          const unsigned in = __ballot_sync(0xffffffffu, key[q] == v);
+          more = in == 0xffffffffu;
+          n += more ? 32 : __ffs(~in) - 1;
+        }
       }
     }
+    if (n > 0 && n <= JOIN_SHORT && h < a.H) {
+      float s[8];
+      load8<F32>(a.part + (2ll * c + 1) * a.H + h, s);
+      add_links(a, c + 1, c + 1 + n, h, s);
+      write_row<O>(a, v, h, s);
+    }
   }
-  F32::store(&sums[w][lane * 8], s);
+  if (lane == 0) links[w] = n > JOIN_SHORT ? n : 0;
   __syncthreads();
-  if (w != 0 || h >= a.H) return;
+  for (int j = 0; j < JOIN_WARPS; ++j) {
+    const int m = links[j];
+    if (m == 0) continue;   // uniform over the block
+    const int first = c0 + j + 1;
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (h < a.H) {
+      if (w == 0) load8<F32>(a.part + (2ll * first - 1) * a.H + h, s);   // the first chunk's outgoing sum
+      add_links(a, first + static_cast<int>(static_cast<long long>(m) * w / JOIN_WARPS),
+                first + static_cast<int>(static_cast<long long>(m) * (w + 1) / JOIN_WARPS), h, s);
+    }
+    F32::store(&sums[w][lane * 8], s);
+    __syncthreads();
+    if (w == 0 && h < a.H) {
 #pragma unroll
-  for (int k = 1; k < JOIN_WARPS; ++k) {
-    float f[8];
-    load8<F32>(&sums[k][lane * 8], f);
+      for (int k = 1; k < JOIN_WARPS; ++k) {
+        float f[8];
+        load8<F32>(&sums[k][lane * 8], f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] += f[j];
+        for (int q = 0; q < 8; ++q) s[q] += f[q];
+      }
+      write_row<O>(a, a.items[static_cast<long long>(first) * a.chunk - 1].x, h, s);
+    }
+    __syncthreads();
   }
-  write_row<O>(a, v, h, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -491,7 +689,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) embedding_join_kernel(const S
 // ---------------------------------------------------------------------------
 struct EmbPlan {
   int tiles = 0, passes = 0, bits = 0, chunk = 0, n_chunks = 0;
-  size_t o_keys[2] = {0, 0}, o_toks[2] = {0, 0}, o_cnt = 0, o_bad = 0, o_part = 0, total = 0;
+  size_t o_items[2] = {0, 0}, o_cnt = 0, o_bad = 0, o_part = 0, total = 0;
 };
 
 EmbPlan emb_plan(long long N, long long H, long long V) {
@@ -500,7 +698,7 @@ EmbPlan emb_plan(long long N, long long H, long long V) {
   while ((V >> key_bits) != 0) ++key_bits;   // keys 0 .. V
   p.passes = static_cast<int>(cdiv(key_bits, SORT_MAX_BITS));
   p.bits = static_cast<int>(cdiv(key_bits, p.passes));
-  p.tiles = static_cast<int>(cdiv(N, SORT_THREADS * (N <= SORT_LARGE ? SORT_ITEMS_SMALL : SORT_ITEMS_LARGE)));
+  p.tiles = N <= CS_MAX ? CS_BLOCKS : static_cast<int>(cdiv(N, SORT_THREADS * (N <= SORT_LARGE ? SORT_ITEMS_SMALL : SORT_ITEMS_LARGE)));
   p.chunk = static_cast<int>(cdiv(std::max<long long>(MIN_CHUNK, cdiv(N, MAX_CHUNKS)), 32) * 32);
   p.n_chunks = static_cast<int>(cdiv(N, p.chunk));
   size_t off = al256(HDR_WORDS * sizeof(int));
@@ -509,10 +707,7 @@ EmbPlan emb_plan(long long N, long long H, long long V) {
     off += al256(bytes);
     return o;
   };
-  for (int k = 0; k < 2; ++k) {
-    p.o_keys[k] = take(size_t(N) * 4);
-    p.o_toks[k] = take(size_t(N) * 4);
-  }
+  for (int k = 0; k < 2; ++k) p.o_items[k] = take(size_t(N) * sizeof(int2));
   p.o_cnt = take(size_t(p.tiles) * SORT_BINS * 4);
   p.o_bad = take(size_t(p.tiles) * 4);
   p.o_part = take(size_t(p.n_chunks) * 2 * H * 4);
@@ -523,25 +718,33 @@ EmbPlan emb_plan(long long N, long long H, long long V) {
 bool emb_sizes_ok(long long N, long long H, long long V) { return sizes_ok(N, H, V) && N <= (1ll << 30); }
 
 struct SortPass {
-  const int *keys, *toks;
+  const int* ids;
+  const int2* items;
   int N, V, padding, shift, bits, tiles;
-  int *bad, *counts, *out_keys, *out_toks;
+  int *bad, *counts;
+  int2* out;
 };
 
 template <bool FIRST, int ITEMS>
 cudaError_t sort_pass(const SortPass& s, cudaStream_t st) {
   cudaError_t e;
   if (FIRST) {   // behind everything before the call
-    sort_count_kernel<FIRST, ITEMS><<<s.tiles, SORT_THREADS, 0, st>>>(s.keys, s.N, s.V, s.padding, s.bad, s.shift,
-                                                                      s.bits, s.counts);
+    sort_count_kernel<FIRST, ITEMS><<<s.tiles, SORT_THREADS, 0, st>>>(s.ids, s.items, s.N, s.V, s.padding,
+                                                                      s.bad, s.shift, s.bits, s.counts);
     e = cudaGetLastError();
   } else {
-    e = launch_dependent(sort_count_kernel<FIRST, ITEMS>, s.tiles, SORT_THREADS, st, s.keys, s.N, s.V, s.padding, s.bad,
-                         s.shift, s.bits, s.counts);
+    e = launch_dependent(sort_count_kernel<FIRST, ITEMS>, s.tiles, SORT_THREADS, st, s.ids, s.items, s.N, s.V,
+                         s.padding, s.bad, s.shift, s.bits, s.counts);
   }
   if (e != cudaSuccess) return e;
-  return launch_dependent(sort_scatter_kernel<FIRST, ITEMS>, s.tiles, SORT_THREADS, st, s.keys, s.toks, s.N, s.V,
-                          s.padding, s.shift, s.bits, s.counts, s.tiles, s.out_keys, s.out_toks);
+  return launch_dependent(sort_scatter_kernel<FIRST, ITEMS>, s.tiles, SORT_THREADS, st, s.ids, s.items, s.N, s.V,
+                          s.padding, s.shift, s.bits, s.counts, s.tiles, s.out);
+}
+
+template <int ITEMS>
+cudaError_t sort_cluster(const ClusterSort& s, cudaStream_t st) {
+  sort_cluster_kernel<ITEMS><<<CS_BLOCKS, CS_THREADS, CS_SMEM, st>>>(s);
+  return cudaGetLastError();
 }
 
 template <typename T, typename O>
@@ -549,7 +752,8 @@ cudaError_t sums(const SegArgs& a, long long blocks, cudaStream_t st) {
   const cudaError_t e =
       launch_dependent(embedding_segments_kernel<T, O>, static_cast<unsigned>(blocks), 32 * SEG_WARPS, st, a);
   if (e != cudaSuccess) return e;
-  return launch_dependent(embedding_join_kernel<O>, static_cast<unsigned>(a.n_chunks * a.slices), 32 * JOIN_WARPS, st, a);
+  return launch_dependent(embedding_join_kernel<O>, static_cast<unsigned>(cdiv(a.n_chunks, JOIN_WARPS) * a.slices),
+                          32 * JOIN_WARPS, st, a);
 }
 
 template <typename T>
@@ -562,6 +766,13 @@ cudaError_t sums(const SegArgs& a, int out_dtype, long long blocks, cudaStream_t
 bool known_dtype(int d) { return d == FLCE_BF16 || d == FLCE_F16 || d == FLCE_F32; }
 
 }  // namespace
+
+cudaError_t embedding_prepare() {
+  cudaError_t e = cudaFuncSetAttribute(sort_cluster_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, CS_SMEM);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(sort_cluster_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, CS_SMEM);
+  return e;
+}
+
 }  // namespace flce
 
 using namespace flce;
@@ -605,17 +816,22 @@ flce_status flce_embedding_bwd(const void* grad_out, const int32_t* ids, int64_t
   if (p.total > workspace_bytes) return FLCE_EWORKSPACE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int* hdr = at<int>(workspace, 0);
-  int* keys[2] = {at<int>(workspace, p.o_keys[0]), at<int>(workspace, p.o_keys[1])};
-  int* toks[2] = {at<int>(workspace, p.o_toks[0]), at<int>(workspace, p.o_toks[1])};
+  int2* items[2] = {at<int2>(workspace, p.o_items[0]), at<int2>(workspace, p.o_items[1])};
   int* cnt = at<int>(workspace, p.o_cnt);
   const int n = static_cast<int>(N), v = static_cast<int>(V);
 
   int* bad = at<int>(workspace, p.o_bad);
 
-  count_launches(2 + 2 * p.passes);
-  for (int k = 0; k < p.passes; ++k) {
-    const SortPass s = {k == 0 ? ids : keys[(k + 1) & 1], toks[(k + 1) & 1], n, v, padding_idx, k * p.bits, p.bits,
-                        p.tiles, bad, cnt, keys[k & 1], toks[k & 1]};
+  count_launches(2 + (N <= CS_MAX ? 1 : 2 * p.passes));
+  if (N <= CS_MAX) {
+    const ClusterSort s = {ids, n, v, padding_idx, p.passes, p.bits, bad, items[0], items[1]};
+    const long long each = CS_BLOCKS * CS_THREADS;
+    const cudaError_t e = N <= each ? sort_cluster<1>(s, st) : sort_cluster<2>(s, st);
+    if (e != cudaSuccess) return FLCE_ECUDA;
+  }
+  for (int k = 0; N > CS_MAX && k < p.passes; ++k) {
+    const SortPass s = {ids, items[(k + 1) & 1], n, v, padding_idx, k * p.bits, p.bits, p.tiles, bad, cnt,
+                        items[k & 1]};
     const bool large = N > SORT_LARGE;
     const cudaError_t e =
         k == 0 ? (large ? sort_pass<true, SORT_ITEMS_LARGE>(s, st) : sort_pass<true, SORT_ITEMS_SMALL>(s, st))
@@ -623,8 +839,7 @@ flce_status flce_embedding_bwd(const void* grad_out, const int32_t* ids, int64_t
     if (e != cudaSuccess) return FLCE_ECUDA;
   }
   SegArgs a;
-  a.keys = keys[(p.passes - 1) & 1];
-  a.toks = toks[(p.passes - 1) & 1];
+  a.items = items[(p.passes - 1) & 1];
   a.dout = static_cast<const unsigned char*>(grad_out);
   a.N = n; a.H = static_cast<int>(H); a.V = v;
   a.chunk = p.chunk; a.n_chunks = p.n_chunks;
@@ -636,11 +851,18 @@ flce_status flce_embedding_bwd(const void* grad_out, const int32_t* ids, int64_t
   a.hdr = hdr;
   a.bad = bad;
   a.tiles = p.tiles;
+  a.ids = ids;
+  a.padding = padding_idx;
   const long long seg_blocks = cdiv(static_cast<long long>(a.n_chunks) * a.slices, SEG_WARPS);
-  const long long zero_blocks = a.accumulate ? 0 : cdiv(cdiv(V, ZERO_ROWS), SEG_WARPS);
-  if (seg_blocks + zero_blocks >= (1ll << 31)) return FLCE_EUNSUPPORTED;
-  a.seg_warps = seg_blocks * SEG_WARPS;
+  // zeroing: four blocks per SM, of whole groups of 32 rows
+  a.zero_rows = static_cast<int>(std::min<long long>(cdiv(cdiv(V, 4 * 152), ZERO_ROWS) * ZERO_ROWS, ZERO_MAX_ROWS));
+  const long long zero_blocks = a.accumulate ? 0 : cdiv(V, a.zero_rows);
+  // reading all ids is worth it where it is little next to the rows written
+  a.scan = N <= CS_MAX && 16 * N <= static_cast<long long>(a.zero_rows) * H * (grad_dtype == FLCE_F32 ? 4 : 2) ? 1 : 0;
+  a.zero_blocks = static_cast<int>(zero_blocks);
+  a.seg_blocks = static_cast<int>(seg_blocks);
   const long long blocks = seg_blocks + zero_blocks;
+  if (blocks >= (1ll << 31)) return FLCE_EUNSUPPORTED;
   const cudaError_t e = dtype == FLCE_BF16  ? sums<Bf16>(a, grad_dtype, blocks, st)
                         : dtype == FLCE_F16 ? sums<F16>(a, grad_dtype, blocks, st)
                                             : sums<F32>(a, grad_dtype, blocks, st);

@@ -198,6 +198,7 @@ struct StreamMaps {
 int stream_ctas(long long V, int sms);
 int stream_tokens(int N);   // N padded to the tile sizes of the kernel
 cudaError_t stream_prepare();
+cudaError_t embedding_prepare();   // flce_embedding.cu
 cudaError_t launch_stream(const StreamArgs& a, const StreamMaps& m, cudaStream_t s);
 
 // Token log probabilities (flce_logprobs.cu).
