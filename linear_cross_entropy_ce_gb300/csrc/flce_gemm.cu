@@ -381,18 +381,34 @@ __device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, con
       for (int k = 0; k < 32; ++k)
         if (j * 32 + k >= ncol) v[k] = -INFINITY;
     }
+    // Three instructions an element, two of them for pairs: the issue slots are
+    // shared with the warps that feed the MMAs, and six an element slowed those
+    // (tiles of 8 K blocks: 3.6 us each, without the arithmetic 2.7).
     float mx = v[0];
 #pragma unroll
-    for (int k = 1; k < 32; ++k) mx = fmaxf(mx, v[k]);
+    for (int k = 1; k + 1 < 32; k += 2) mx = ptx::max3(mx, v[k], v[k + 1]);
+    mx = fmaxf(mx, v[31]);
     const bool none = !(mx > -INFINITY);          // nothing but -inf (or NaN, which the sums keep)
     const float mb = none ? 0.f : -mx * a.c2;
-    float sum = 0.f, dsum = 0.f;
+    const uint64_t cc = ptx::pack2(a.c2, a.c2), bb = ptx::pack2(mb, mb);
+    uint64_t s2 = 0, d2 = 0;                      // two zeros each
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      const float d = fmaf(v[k], a.c2, mb);
-      const float e = ptx::ex2(d);
-      sum += e;
-      dsum = fmaf(fmaxf(d, -1e30f), e, dsum);     // 0 for a logit of -inf
+    for (int k = 0; k < 32; k += 2) {
+      const uint64_t d = ptx::fma2(ptx::pack2(v[k], v[k + 1]), cc, bb);
+      const float2 x = ptx::unpack2(d);
+      const uint64_t e = ptx::pack2(ptx::ex2(x.x), ptx::ex2(x.y));
+      s2 = ptx::add2(s2, e);
+      d2 = ptx::fma2(d, e, d2);
+    }
+    float sum = ptx::unpack2(s2).x + ptx::unpack2(s2).y;
+    float dsum = ptx::unpack2(d2).x + ptx::unpack2(d2).y;
+    if (dsum != dsum && sum == sum) {             // a logit of -inf: 0 times -inf; it adds nothing
+      dsum = 0.f;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        const float d = fmaf(v[k], a.c2, mb);
+        dsum = fmaf(fmaxf(d, -1e30f), ptx::ex2(d), dsum);
+      }
     }
     // mb is rounded: every d is too large by rho = mx c2 + mb (exact in the
     // fused multiply-add), which matters where the logits are large
@@ -426,14 +442,30 @@ __device__ __forceinline__ void epi_dz(const GemmArgs& a, const Shape& s, const 
   DzRow q = {0.f, 0.f, 0.f, 0.f};
   if (rw) q = a.rowc[grow];
   uint16_t* zrow = a.z + static_cast<size_t>(grow) * a.ldz + c0;
+  const uint64_t cc = ptx::pack2(a.c2, a.c2), bb = ptx::pack2(-q.lse2, -q.lse2);
+  const uint64_t qa = ptx::pack2(q.a, q.a), qb = ptx::pack2(q.b, q.b);
+  const bool entropy = __any_sync(0xffffffffu, q.b != 0.f);   // else the gradient of the log probabilities alone
 #pragma unroll 1
   for (int j = 0; j < GROUP_COLS / 32; ++j) {
     float v[32];
     ptx::tmem_ld32(tbase + j * 32, v);
+    if (entropy) {
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      const float l2 = fmaf(v[k], a.c2, -q.lse2);
-      v[k] = ptx::ex2(l2) * fmaf(q.b, fmaxf(l2, -1e30f), q.a);   // 0 for a logit of -inf
+      for (int k = 0; k < 32; k += 2) {
+        const float2 l = ptx::unpack2(ptx::fma2(ptx::pack2(v[k], v[k + 1]), cc, bb));
+        const uint64_t f = ptx::fma2(ptx::pack2(fmaxf(l.x, -1e30f), fmaxf(l.y, -1e30f)), qb, qa);   // -inf: 0 below
+        const float2 r2 = ptx::unpack2(ptx::mul2(ptx::pack2(ptx::ex2(l.x), ptx::ex2(l.y)), f));
+        v[k] = r2.x;
+        v[k + 1] = r2.y;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 32; k += 2) {
+        const float2 l = ptx::unpack2(ptx::fma2(ptx::pack2(v[k], v[k + 1]), cc, bb));
+        const float2 r2 = ptx::unpack2(ptx::mul2(ptx::pack2(ptx::ex2(l.x), ptx::ex2(l.y)), qa));
+        v[k] = r2.x;
+        v[k + 1] = r2.y;
+      }
     }
     if (static_cast<unsigned>(tl - j * 32) < 32u) {
 #pragma unroll
@@ -730,6 +762,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   const uint64_t to = a.timeout_ns;
   int* hdr = const_cast<int*>(a.hdr);
   const int half = static_cast<int>(rank) * BM;   // this CTA's rows (A) / columns (B) inside a pair tile
+  // The tiles of a PROBS launch all take the same time: pair p takes tiles p,
+  // p + pairs, ... and no claim or hand-off stands between them (0.15 us a
+  // tile).  The others are claimed from a counter.
+  const int pair0 = static_cast<int>(blockIdx.x / 2), npairs = static_cast<int>(gridDim.x / 2);
   const uint32_t nstages = PROBS || a.mode == MODE_LOGITS ? STAGES_LOGITS : STAGES;
 
   if (warp == 0 && lane == 0) {
@@ -743,10 +779,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     // claimed as soon as a short tile starts (its loads hide the atomic); a
     // long tile claims its successor only when its own loads are all issued,
     // so that it never holds work another pair could start.
-    int next = lead ? atomicAdd(a.counter, 1) : -1;
-    for (;;) {
+    int next = !PROBS && lead ? atomicAdd(a.counter, 1) : -1;
+    for (int turn = pair0;; turn += npairs) {
       int u;
-      if (lead) {
+      if (PROBS) {
+        u = turn < s.units ? turn : -1;
+      } else if (lead) {
         if (!wait_phase(&ctl->sempty[sslot], sphase ^ 1u, ctl, to, true, hdr, W_SCHED_EMPTY)) { ok = false; break; }
         if (next < 0) next = atomicAdd(a.counter, 1);
         u = next < s.units ? next : -1;
@@ -769,7 +807,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       if (++sslot == SCHED_SLOTS) { sslot = 0; sphase ^= 1u; }
       if (u < 0) break;
       const Unit t = decode_unit<PROBS>(a, s, u);
-      if (lead && t.kb1 - t.kb0 <= SHORT_TILE_KB) next = atomicAdd(a.counter, 1);
+      if (!PROBS && lead && t.kb1 - t.kb0 <= SHORT_TILE_KB) next = atomicAdd(a.counter, 1);
       for (int kb = t.kb0; kb < t.kb1; ++kb) {
         if (!wait_stage(&ctl->empty[stage], phase ^ 1u, ctl, to, hdr, W_STAGE_EMPTY, u | (stage << 24))) { ok = false; break; }
         uint8_t* sa = smem + stage * STAGE_BYTES;
@@ -808,10 +846,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     // ---------------- MMA issuer for the pair ----------------
     uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, sslot = 0, sphase = 0;
     bool withhold = a.debug_stall != 0;   // test hook, see GemmArgs::debug_stall
-    for (;;) {
-      if (!wait_phase(&ctl->sfull[sslot], sphase, ctl, to, true, hdr, W_SCHED_FULL_MMA)) break;
-      const int u = ctl->sunit[sslot];
-      ptx::mbar_arrive(&ctl->sempty[sslot]);
+    for (int turn = pair0;; turn += npairs) {
+      int u = turn < s.units ? turn : -1;
+      if (!PROBS) {
+        if (!wait_phase(&ctl->sfull[sslot], sphase, ctl, to, true, hdr, W_SCHED_FULL_MMA)) break;
+        u = ctl->sunit[sslot];
+        ptx::mbar_arrive(&ctl->sempty[sslot]);
+      }
       if (++sslot == SCHED_SLOTS) { sslot = 0; sphase ^= 1u; }
       if (u < 0) break;
       const Unit t = decode_unit<PROBS>(a, s, u);
@@ -865,19 +906,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     const uint32_t sempty0 = ptx::map_to_rank(&ctl->sempty[0], 0);
     const uint32_t tempty_mine = ptx::map_to_rank(&ctl->tempty[set], 0);
     uint32_t seq = 0, acc_phase = 0, sslot = 0, sphase = 0;
-    for (;;) {
-      // every wait is followed by a vote so that all threads of the set leave together
-      bool ok = wait_phase(&ctl->sfull[sslot], sphase, ctl, to, true, hdr, W_SCHED_FULL_EPI, sslot << 24);
-      if (!ptx::named_bar_and(sbar, SET_THREADS, ok)) break;
-      // lane 0 reads the slot and hands it back; relaxed (its acquire load
-      // orders the arrive after the read), since a release would wait for
-      // the warp's row stores in flight
-      int u = 0;
-      if (lane == 0) {
-        u = ptx::ld_acquire_shared(&ctl->sunit[sslot]);
-        ptx::mbar_arrive_remote_relaxed(sempty0 + sslot * 8u);
+    for (int turn = pair0;; turn += npairs) {
+      bool ok = true;
+      int u = turn < s.units ? turn : -1;
+      if (!PROBS) {
+        // every wait is followed by a vote so that all threads of the set leave together
+        ok = wait_phase(&ctl->sfull[sslot], sphase, ctl, to, true, hdr, W_SCHED_FULL_EPI, sslot << 24);
+        if (!ptx::named_bar_and(sbar, SET_THREADS, ok)) break;
+        // lane 0 reads the slot and hands it back; relaxed (its acquire load
+        // orders the arrive after the read), since a release would wait for
+        // the warp's row stores in flight
+        u = 0;
+        if (lane == 0) {
+          u = ptx::ld_acquire_shared(&ctl->sunit[sslot]);
+          ptx::mbar_arrive_remote_relaxed(sempty0 + sslot * 8u);
+        }
+        u = __shfl_sync(0xffffffffu, u, 0);
       }
-      u = __shfl_sync(0xffffffffu, u, 0);
       if (++sslot == SCHED_SLOTS) { sslot = 0; sphase ^= 1u; }
       if (u < 0) break;
       if ((seq++ & 1u) != static_cast<uint32_t>(set)) continue;   // the other set's tile
