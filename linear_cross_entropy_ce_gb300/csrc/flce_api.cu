@@ -342,14 +342,14 @@ void prof_launch_end(const ProfScope& r, int mode, cudaStream_t st) {
 }
 
 // Launch a GEMM, bracketed by events when profiling is on.
-cudaError_t gemm_launch(const GemmArgs& g0, const GemmMaps& m, int grid, cudaStream_t st) {
+cudaError_t gemm_launch(const GemmArgs& g0, const GemmMaps& m, int grid, cudaStream_t st, bool dependent) {
   GemmArgs g = g0;
   if (const unsigned long long t = take_armed_stall()) {
     g.debug_stall = 1;
     g.timeout_ns = t;
   }
   const ProfScope r = prof_launch_begin(st);
-  const cudaError_t e = launch_gemm(g, m, grid, st);
+  const cudaError_t e = launch_gemm(g, m, grid, st, dependent);
   prof_launch_end(r, g.mode, st);
   return e;
 }
@@ -515,15 +515,29 @@ flce_status run(const Job& j) {
   auto chk = [](cudaError_t e) { return e == cudaSuccess; };
   const bool stats = j.kind == JOB_SHARD_STATS;
   const int v0 = static_cast<int>(j.v0);
-  if (probs)   // prep, zeroed rows, one gather per chunk, failure mark, rounding
-    count_launches(2 + (j.grad_hidden ? 1 : 0) + p.n_chunks + (p.gw32 ? 1 : 0));
+  const bool front = probs && p.n_chunks == 1 && N <= FRONT_MAX_TOKENS;
+  if (probs)   // front, or prep, zeroed rows and one gather per chunk; failure mark, rounding
+    count_launches((front ? 1 : 1 + (j.grad_hidden ? 1 : 0) + p.n_chunks) + 1 + (p.gw32 ? 1 : 0));
   else
     count_launches(1 + (fwd_only ? 0 : 1) + (j.kind == JOB_SHARD_BWD ? 0 : 1) + p.n_chunks * (norm ? 4 : 2) +
                    (norm ? 1 : 0) + (p.gw32 ? 1 : 0));
-  if (!chk(launch_prep(j.targets, N, static_cast<int>(j.V_total), j.ii, hdr, idx, j.n_valid, counters,
-                       p.n_counters, st)))
+  if (front) {
+    FrontArgs f;
+    std::memset(&f, 0, sizeof(f));
+    f.hidden = static_cast<const uint16_t*>(j.hidden);
+    f.targets = j.targets;
+    f.N = static_cast<int>(N); f.H = g.H; f.V = g.V; f.ii = j.ii; f.C = g.C;
+    f.hdr = hdr; f.idx = idx; f.tc = tc; f.xc = xc; f.counters = counters;
+    f.n_counters = static_cast<int>(p.n_counters);
+    f.rowc = rowc; f.temperature = j.temperature;
+    f.lse_in = j.lse; f.entropy_in = j.entropy; f.grad_logp = j.grad_logp; f.grad_entropy = j.grad_entropy;
+    f.grad_hidden = static_cast<uint16_t*>(j.grad_hidden);
+    if (!chk(launch_probs_front(f, st))) return FLCE_ECUDA;
+  } else if (!chk(launch_prep(j.targets, N, static_cast<int>(j.V_total), j.ii, hdr, idx, j.n_valid, counters,
+                              p.n_counters, st))) {
     return FLCE_ECUDA;
-  if (!fwd_only && j.grad_hidden && !chk(launch_zero_ignored(hdr, idx, N, H * (j.grad_hidden_f32 ? 4 : 2), j.grad_hidden, st)))
+  }
+  if (!fwd_only && !front && j.grad_hidden && !chk(launch_zero_ignored(hdr, idx, N, H * (j.grad_hidden_f32 ? 4 : 2), j.grad_hidden, st)))
     return FLCE_ECUDA;
   if (stats && !chk(launch_shard_stats_ignored(hdr, idx, N, j.row_max, j.row_sumexp, j.row_zt, st)))
     return FLCE_ECUDA;
@@ -535,7 +549,7 @@ flce_status run(const Job& j) {
                                   static_cast<const uint16_t*>(j.gain), j.eps, xc, tc, rinv, st)))
         return FLCE_ECUDA;
     } else if (probs) {
-      if (!chk(launch_gather_dz(static_cast<const uint16_t*>(j.hidden), j.targets, hdr, idx, c0, g.C, g.H,
+      if (!front && !chk(launch_gather_dz(static_cast<const uint16_t*>(j.hidden), j.targets, hdr, idx, c0, g.C, g.H,
                                 j.temperature, j.lse, j.entropy, j.grad_logp, j.grad_entropy, xc, tc, rowc, st)))
         return FLCE_ECUDA;
     } else if (!chk(launch_gather(static_cast<const uint16_t*>(j.hidden), j.targets, hdr, idx, c0, g.C, g.H, xc,
@@ -545,7 +559,7 @@ flce_status run(const Job& j) {
     int* sync = counters + c * (2 + p.flags_per_chunk);
     g.mode = probs ? MODE_DZ : MODE_LOGITS;   // MODE_DZ leaves the finished dz in z
     g.counter = sync;
-    if (!chk(gemm_launch(g, fm, grid_logits, st))) return FLCE_ECUDA;
+    if (!chk(gemm_launch(g, fm, grid_logits, st, front))) return FLCE_ECUDA;
     if (stats) {
       if (!chk(launch_shard_stats(hdr, idx, c0, g.C, p.nparts, part, zt, tc, j.row_max, j.row_sumexp, j.row_zt,
                                   st)))
@@ -561,7 +575,7 @@ flce_status run(const Job& j) {
     g.flags = sync + 2;
     g.accumulate = c > 0 ? 1 : 0;
     g.first_chunk = c == 0 ? 1 : 0;
-    if (!chk(gemm_launch(g, bm, grid_bwd, st))) return FLCE_ECUDA;
+    if (!chk(gemm_launch(g, bm, grid_bwd, st, probs))) return FLCE_ECUDA;
     if (norm && !chk(launch_rmsnorm_bwd(hdr, idx, c0, g.C, g.H, static_cast<const uint16_t*>(j.hidden),
                                         static_cast<const uint16_t*>(j.gain), rinv,
                                         static_cast<uint16_t*>(j.grad_hidden), dgp + c * H, st)))

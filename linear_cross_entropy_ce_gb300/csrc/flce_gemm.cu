@@ -709,6 +709,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   const uint32_t rank = ptx::cluster_ctarank();
   const bool lead = rank == 0;
 
+  // launched dependently (a wait that returns at once otherwise): the previous
+  // kernel's results are read from here on
+  ptx::grid_launch_dependents();
+  ptx::grid_dependency_wait();
   const Shape s = make_shape<PROBS>(a);   // identical in both CTAs of a pair
   if (!PROBS && a.mode == MODE_BWD && s.Cl == 0) {
     // Empty first chunk (no valid token at all): grad_weight is zero.
@@ -1005,11 +1009,20 @@ cudaError_t gemm_max_pairs(int* pairs) {
   return cudaOccupancyMaxActiveClusters(pairs, flce_gemm_kernel<false>, &cfg);
 }
 
-cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps& m, int grid, cudaStream_t st) {
+cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps& m, int grid, cudaStream_t st, bool dependent) {
   // grid counts CTAs and must be even (pairs)
-  if (a.mode == MODE_STATS || a.mode == MODE_DZ) flce_gemm_kernel<true><<<grid, NUM_THREADS, SMEM_BYTES, st>>>(m, a);
-  else flce_gemm_kernel<false><<<grid, NUM_THREADS, SMEM_BYTES, st>>>(m, a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
+  cfg.blockDim = dim3(NUM_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = dependent ? 1 : 0;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (a.mode == MODE_STATS || a.mode == MODE_DZ) return cudaLaunchKernelEx(&cfg, flce_gemm_kernel<true>, m, a);
+  return cudaLaunchKernelEx(&cfg, flce_gemm_kernel<false>, m, a);
 }
 
 }  // namespace flce

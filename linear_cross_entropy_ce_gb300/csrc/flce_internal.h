@@ -105,7 +105,7 @@ struct GemmMaps {
 int gemm_smem_bytes();
 cudaError_t gemm_prepare(int device);
 cudaError_t gemm_max_pairs(int* pairs);   // CTA pairs resident at once (current device)
-cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps& m, int grid, cudaStream_t s);
+cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps& m, int grid, cudaStream_t s, bool dependent);
 
 // Host helpers shared by the entry points (flce_api.cu).
 struct DeviceState {
@@ -123,7 +123,8 @@ bool make_map(CUtensorMap* m, const void* base, unsigned long long inner, unsign
               CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
               CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 // Launch a GEMM, bracketed by events when profiling is on.
-cudaError_t gemm_launch(const GemmArgs& g0, const GemmMaps& m, int grid, cudaStream_t st);
+// dependent: while the previous kernel drains (launch_dependent).
+cudaError_t gemm_launch(const GemmArgs& g0, const GemmMaps& m, int grid, cudaStream_t st, bool dependent = false);
 void count_launches(long long n);
 // Events around a tcgen05 launch of `mode` while profiling is on (begin gives a
 // handle for end; a call without profiling costs one lock).
@@ -152,6 +153,7 @@ cudaError_t launch_dependent(void (*kernel)(P...), unsigned blocks, unsigned thr
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks, 1, 1);
   cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = 0;
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -202,6 +204,26 @@ cudaError_t embedding_prepare();   // flce_embedding.cu
 cudaError_t launch_stream(const StreamArgs& a, const StreamMaps& m, cudaStream_t s);
 
 // Token log probabilities (flce_logprobs.cu).
+// The first launch of a call of one chunk and at most FRONT_MAX_TOKENS tokens;
+// rowc selects the backward.
+constexpr long long FRONT_MAX_TOKENS = 16384;
+struct FrontArgs {
+  const uint16_t* hidden;
+  const int* targets;
+  int N, H, V, ii, C, K;
+  int *hdr, *idx, *tc;
+  uint16_t* xc;
+  int* counters;
+  int n_counters;
+  float *logp, *lse, *entropy;        // forward outputs
+  int* top_ids;
+  float* top_logp;
+  DzRow* rowc;                        // backward
+  float temperature;
+  const float *lse_in, *entropy_in, *grad_logp, *grad_entropy;
+  uint16_t* grad_hidden;              // or null
+};
+cudaError_t launch_probs_front(const FrontArgs& a, cudaStream_t s);
 cudaError_t launch_gather_dz(const uint16_t* hidden, const int* targets, const int* hdr, const int* idx,
                              long long c0, int C, int H, float temperature, const float* lse, const float* entropy,
                              const float* grad_logp, const float* grad_entropy, uint16_t* xc, int* tc, DzRow* rowc,

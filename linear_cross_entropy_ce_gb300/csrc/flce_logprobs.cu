@@ -33,6 +33,15 @@ __device__ __forceinline__ int chunk_rows(const int* hdr, long long c0, int C) {
   return rem <= 0 ? 0 : (rem >= C ? C : static_cast<int>(rem));
 }
 
+// The constants of MODE_DZ of token n (see DzRow).
+__device__ __forceinline__ DzRow dz_row(float temperature, float lse, const float* entropy, const float* grad_logp,
+                                        const float* grad_entropy, long long n) {
+  const float it = 1.f / temperature;
+  const float g = grad_logp ? grad_logp[n] : 0.f;
+  const float e = grad_entropy ? grad_entropy[n] : 0.f;
+  return DzRow{lse * LOG2E, -it * (grad_entropy ? fmaf(e, entropy[n], g) : g), -it * LN2 * e, it * g};
+}
+
 // Chunk rows and their targets in a dense [C, H] tile source (rows up to the
 // next multiple of 128 are zero), with the constants of MODE_DZ:
 //   dz = (g ([v = t] - p) - e p (log p + H)) / T.
@@ -59,11 +68,105 @@ __global__ void __launch_bounds__(128)
   const uint4* src = reinterpret_cast<const uint4*>(X + row * H);
   for (int c = threadIdx.x; c < n16; c += blockDim.x) dst[c] = src[c];
   if (threadIdx.x == 0) {
-    const float it = 1.f / temperature;
-    const float g = grad_logp ? grad_logp[row] : 0.f;
-    const float e = grad_entropy ? grad_entropy[row] : 0.f;
     tc[r] = t[row];
-    rowc[r] = DzRow{lse[row] * LOG2E, -it * (grad_entropy ? fmaf(e, entropy[row], g) : g), -it * LN2 * e, it * g};
+    rowc[r] = dz_row(temperature, lse[row], entropy, grad_logp, grad_entropy, row);
+  }
+}
+
+// Everything before the first GEMM of a call of one chunk, in one launch: the
+// valid tokens' rows gathered into the tile source in order, their targets (and
+// for the backward the constants of MODE_DZ), the outputs of the tokens left
+// out, the header and the GEMMs' counters.  Every block counts the valid
+// targets before its own tokens itself (16384 targets are 64 KB from L2), which
+// costs less than a launch of its own for the scan.
+constexpr int FRONT_THREADS = 256;
+constexpr int FRONT_WARPS = FRONT_THREADS / 32;
+constexpr int FRONT_TOKENS = 16;   // per block
+
+__global__ void __launch_bounds__(FRONT_THREADS) probs_front_kernel(const FrontArgs a) {
+  __shared__ int red[2][FRONT_WARPS];
+  __shared__ int dst[FRONT_TOKENS];
+  const int tid = threadIdx.x, lane = tid % 32, w = tid / 32;
+  ptx::grid_launch_dependents();
+  const int n0 = blockIdx.x * FRONT_TOKENS;
+  int before = 0, total = 0, bad = 0;
+#pragma unroll 8
+  for (int i = tid; i < a.N; i += FRONT_THREADS) {
+    const int x = a.targets[i];
+    const bool in = x >= 0 && x < a.V;
+    const bool valid = in && x != a.ii;
+    total += valid;
+    before += valid && i < n0;
+    bad |= !in && x != a.ii;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+  }
+  if (lane == 0) { red[0][w] = before; red[1][w] = total; }
+  bad = __syncthreads_or(bad);
+  before = total = 0;
+#pragma unroll
+  for (int k = 0; k < FRONT_WARPS; ++k) { before += red[0][k]; total += red[1][k]; }
+  if (blockIdx.x == 0) {
+    if (tid == 0) {
+      a.hdr[HDR_STATUS] = bad ? STATUS_BADTARGET : 0;
+      a.hdr[HDR_NVALID] = total;
+      a.hdr[HDR_STALL] = a.hdr[HDR_STALL_COUNT] = 0;
+    }
+    for (int i = tid; i < a.n_counters; i += FRONT_THREADS) a.counters[i] = 0;
+  }
+  if (w == 0) {   // the place of each token of this block, or -1
+    const int n = n0 + lane;
+    const int x = lane < FRONT_TOKENS && n < a.N ? a.targets[n] : -1;
+    const bool valid = x >= 0 && x < a.V && x != a.ii && lane < FRONT_TOKENS && n < a.N;
+    const unsigned m = __ballot_sync(0xffffffffu, valid);
+    if (lane < FRONT_TOKENS) dst[lane] = valid ? before + __popc(m & ((1u << lane) - 1u)) : -1;
+  }
+  __syncthreads();
+  const int n16 = a.H / 8;
+  for (int k = w; k < FRONT_TOKENS; k += FRONT_WARPS) {   // a warp per token
+    const long long n = n0 + k;
+    if (n >= a.N) break;
+    const int r = dst[k];
+    if (r >= 0) {
+      const uint4* from = reinterpret_cast<const uint4*>(a.hidden + n * a.H);
+      uint4* to = reinterpret_cast<uint4*>(a.xc + static_cast<size_t>(r) * a.H);
+#pragma unroll 4
+      for (int c = lane; c < n16; c += 32) to[c] = from[c];
+      if (lane == 0) {
+        a.tc[r] = a.targets[n];
+        a.idx[r] = static_cast<int>(n);
+        if (a.rowc) a.rowc[r] = dz_row(a.temperature, a.lse_in[n], a.entropy_in, a.grad_logp, a.grad_entropy, n);
+      }
+    } else if (a.rowc) {   // backward: no gradient
+      if (a.grad_hidden) {
+        uint4* to = reinterpret_cast<uint4*>(a.grad_hidden + n * a.H);
+        for (int c = lane; c < n16; c += 32) to[c] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    } else {               // forward: 0 for an ignored token, NaN for a target outside [0, V)
+      const float v = a.targets[n] == a.ii ? 0.f : __int_as_float(0x7fc00000);
+      if (lane == 0) {
+        a.logp[n] = v;
+        a.lse[n] = v;
+        if (a.entropy) a.entropy[n] = v;
+      }
+      if (lane < a.K) {
+        a.top_ids[n * a.K + lane] = -1;
+        a.top_logp[n * a.K + lane] = v;
+      }
+    }
+  }
+  // padding rows up to the next multiple of 128
+  const int end = min(a.C, (total + BM - 1) / BM * BM);
+  for (int r = total + static_cast<int>(blockIdx.x) * FRONT_WARPS + w; r < end; r += gridDim.x * FRONT_WARPS) {
+    uint4* to = reinterpret_cast<uint4*>(a.xc + static_cast<size_t>(r) * a.H);
+    for (int c = lane; c < n16; c += 32) to[c] = make_uint4(0u, 0u, 0u, 0u);
+    if (lane == 0) {
+      a.tc[r] = -1;
+      if (a.rowc) a.rowc[r] = DzRow{0.f, 0.f, 0.f, 0.f};
+    }
   }
 }
 
@@ -94,6 +197,8 @@ struct RowArgs {
 __global__ void __launch_bounds__(32 * ROWS_WARPS) logprob_rows_kernel(const RowArgs a) {
   __shared__ Stat part[ROWS_WARPS][32];
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+  ptx::grid_launch_dependents();
+  ptx::grid_dependency_wait();
   if (static_cast<int>(blockIdx.x) >= a.row_blocks) {
     const long long step = static_cast<long long>(gridDim.x - a.row_blocks) * blockDim.x;
     for (long long i = a.hdr[HDR_NVALID] + static_cast<long long>(blockIdx.x - a.row_blocks) * blockDim.x + threadIdx.x;
@@ -152,13 +257,13 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) logprob_rows_kernel(const Row
 constexpr int TOP_WARPS = 4;
 constexpr int TOP_BATCH = 8;
 __global__ void __launch_bounds__(32 * TOP_WARPS)
-    logprob_top_kernel(const int* hdr, const int* __restrict__ idx, long long c0, int C, int V, long long ldz,
-                       int nparts, int K, const float* __restrict__ stats, const float* __restrict__ zf,
-                       const float2* __restrict__ ml, float c2, int* __restrict__ top_ids,
-                       float* __restrict__ top_logp) {
+    logprob_top_kernel(const int* hdr, const int* idx, long long c0, int C, int V, long long ldz, int nparts, int K,
+                       const float* stats, const float* zf, const float2* ml, float c2, int* top_ids,
+                       float* top_logp) {
   __shared__ float sv[TOP_WARPS][32];
   __shared__ int si[TOP_WARPS][32];
   const int r = blockIdx.x;
+  ptx::grid_dependency_wait();
   if (r >= chunk_rows(hdr, c0, C)) return;
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   TopK best;
@@ -206,6 +311,7 @@ __global__ void __launch_bounds__(32 * TOP_WARPS)
 // The gradients of a call whose pipeline timed out begin with a NaN, so that a
 // caller who never reads the status still sees that they are not to be trusted.
 __global__ void mark_failed_kernel(const int* hdr, uint16_t* grad_hidden, float* grad_weight, int gw_bf16) {
+  ptx::grid_dependency_wait();
   if (!(hdr[HDR_STATUS] & STATUS_TIMEOUT)) return;
   if (grad_hidden) grad_hidden[0] = 0x7fc0;
   if (grad_weight && gw_bf16) reinterpret_cast<uint16_t*>(grad_weight)[0] = 0x7fc0;
@@ -303,7 +409,11 @@ bool bad_temperature(float t) { return !(t > 0.f) || !std::isfinite(t) || !std::
 
 cudaError_t launch_mark_failed(const int* hdr, uint16_t* grad_hidden, float* grad_weight, int gw_bf16,
                                cudaStream_t s) {
-  mark_failed_kernel<<<1, 1, 0, s>>>(hdr, grad_hidden, grad_weight, gw_bf16);
+  return launch_dependent(mark_failed_kernel, 1, 1, s, hdr, grad_hidden, grad_weight, gw_bf16);
+}
+
+cudaError_t launch_probs_front(const FrontArgs& a, cudaStream_t s) {
+  probs_front_kernel<<<static_cast<unsigned>(cdiv(a.N, FRONT_TOKENS)), FRONT_THREADS, 0, s>>>(a);
   return cudaGetLastError();
 }
 
@@ -414,9 +524,8 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
 
   const int grid = 2 * static_cast<int>(std::min<long long>(cdiv(p.C, PAIR_M) * p.nvt, dev.pairs));
   auto chk = [](cudaError_t e) { return e == cudaSuccess; };
-  count_launches(1 + p.n_chunks * (top_k > 0 ? 3 : 2));
-  if (!chk(launch_prep(targets, N, static_cast<int>(V), ignore_index, hdr, idx, nullptr, counters, p.n_chunks, st)))
-    return FLCE_ECUDA;
+  const bool front = p.n_chunks == 1 && N <= FRONT_MAX_TOKENS;
+  count_launches(front ? (top_k > 0 ? 3 : 2) : 1 + p.n_chunks * (top_k > 0 ? 3 : 2));
   RowArgs ra;
   ra.hdr = hdr; ra.idx = idx; ra.targets = targets;
   ra.N = N; ra.C = g.C; ra.nparts = p.nparts; ra.ii = ignore_index; ra.K = top_k;
@@ -424,21 +533,33 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
   ra.stats = stats; ra.zt = zt; ra.c2 = g.c2;
   ra.logp = logp; ra.entropy = entropy; ra.lse = lse; ra.ml = ml; ra.top_ids = top_ids; ra.top_logp = top_logp;
   const int left_blocks = static_cast<int>(std::min<long long>(cdiv(N, 32 * ROWS_WARPS), 152));
+  if (front) {
+    FrontArgs f;
+    std::memset(&f, 0, sizeof(f));
+    f.hidden = static_cast<const uint16_t*>(hidden);
+    f.targets = targets;
+    f.N = static_cast<int>(N); f.H = g.H; f.V = g.V; f.ii = ignore_index; f.C = g.C; f.K = top_k;
+    f.hdr = hdr; f.idx = idx; f.tc = tc; f.xc = xc; f.counters = counters; f.n_counters = 1;
+    f.logp = logp; f.lse = lse; f.entropy = entropy; f.top_ids = top_ids; f.top_logp = top_logp;
+    if (!chk(launch_probs_front(f, st))) return FLCE_ECUDA;
+  } else if (!chk(launch_prep(targets, N, static_cast<int>(V), ignore_index, hdr, idx, nullptr, counters, p.n_chunks,
+                              st))) {
+    return FLCE_ECUDA;
+  }
   for (long long c = 0; c < p.n_chunks; ++c) {
     g.c0 = c * p.C;
     g.counter = counters + c;
-    if (!chk(launch_gather(static_cast<const uint16_t*>(hidden), targets, hdr, idx, g.c0, g.C, g.H, xc, tc, 0, g.V,
-                           st)) ||
-        !chk(gemm_launch(g, m, grid, st)))
+    if (!front && !chk(launch_gather(static_cast<const uint16_t*>(hidden), targets, hdr, idx, g.c0, g.C, g.H, xc, tc, 0,
+                                     g.V, st)))
       return FLCE_ECUDA;
+    if (!chk(gemm_launch(g, m, grid, st, front))) return FLCE_ECUDA;
     ra.c0 = g.c0;
-    logprob_rows_kernel<<<ra.row_blocks + (c == 0 ? left_blocks : 0), 32 * ROWS_WARPS, 0, st>>>(ra);
-    if (!chk(cudaGetLastError())) return FLCE_ECUDA;
-    if (top_k > 0) {
-      logprob_top_kernel<<<g.C, 32 * TOP_WARPS, 0, st>>>(hdr, idx, g.c0, g.C, g.V, p.ldz, p.nparts, top_k, stats, zf,
-                                                         ml, g.c2, top_ids, top_logp);
-      if (!chk(cudaGetLastError())) return FLCE_ECUDA;
-    }
+    if (!chk(launch_dependent(logprob_rows_kernel, ra.row_blocks + (!front && c == 0 ? left_blocks : 0),
+                              32 * ROWS_WARPS, st, ra)))
+      return FLCE_ECUDA;
+    if (top_k > 0 && !chk(launch_dependent(logprob_top_kernel, g.C, 32 * TOP_WARPS, st, hdr, idx, g.c0, g.C, g.V, p.ldz,
+                                           p.nparts, top_k, stats, zf, ml, g.c2, top_ids, top_logp)))
+      return FLCE_ECUDA;
   }
   return FLCE_OK;
 }
