@@ -711,7 +711,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 
   // launched dependently (a wait that returns at once otherwise): the previous
   // kernel's results are read from here on
-  ptx::grid_launch_dependents();
   ptx::grid_dependency_wait();
   const Shape s = make_shape<PROBS>(a);   // identical in both CTAs of a pair
   if (!PROBS && a.mode == MODE_BWD && s.Cl == 0) {

@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(128)
 // costs less than a launch of its own for the scan.
 constexpr int FRONT_THREADS = 256;
 constexpr int FRONT_WARPS = FRONT_THREADS / 32;
-constexpr int FRONT_TOKENS = 16;   // per block
+constexpr int FRONT_TOKENS = FRONT_WARPS;   // per block: one per warp
 
 __global__ void __launch_bounds__(FRONT_THREADS) probs_front_kernel(const FrontArgs a) {
   __shared__ int red[2][FRONT_WARPS];
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(FRONT_THREADS) probs_front_kernel(const FrontA
     if (r >= 0) {
       const uint4* from = reinterpret_cast<const uint4*>(a.hidden + n * a.H);
       uint4* to = reinterpret_cast<uint4*>(a.xc + static_cast<size_t>(r) * a.H);
-#pragma unroll 4
+#pragma unroll 8
       for (int c = lane; c < n16; c += 32) to[c] = from[c];
       if (lane == 0) {
         a.tc[r] = a.targets[n];
@@ -197,7 +197,8 @@ struct RowArgs {
 __global__ void __launch_bounds__(32 * ROWS_WARPS) logprob_rows_kernel(const RowArgs a) {
   __shared__ Stat part[ROWS_WARPS][32];
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
-  ptx::grid_launch_dependents();
+  // no early trigger: the waiting blocks of the top kernel would take the SMs
+  // this one's blocks need (1033 tokens at 4096 x 128256: 17 us)
   ptx::grid_dependency_wait();
   if (static_cast<int>(blockIdx.x) >= a.row_blocks) {
     const long long step = static_cast<long long>(gridDim.x - a.row_blocks) * blockDim.x;
@@ -270,34 +271,35 @@ __global__ void __launch_bounds__(32 * TOP_WARPS)
   best.clear();
   for (int p0 = w * 32; p0 < nparts; p0 += TOP_BATCH * TOP_WARPS * 32) {
     float x[TOP_BATCH];
+    int id[TOP_BATCH];
 #pragma unroll
     for (int k = 0; k < TOP_BATCH; ++k) {
       const int p = p0 + k * (TOP_WARPS * 32) + lane;
       x[k] = p < nparts ? stats[static_cast<size_t>(p) * C + r] : 0.f;
+      id[k] = p < nparts ? p : TopK::NONE;
     }
-#pragma unroll
-    for (int k = 0; k < TOP_BATCH; ++k) {
-      const int p = p0 + k * (TOP_WARPS * 32) + lane;
-      best.offer(x[k], p, p < nparts, K, lane);
-    }
+    best.offer_all(x, id, K, lane);
   }
   best.merge_block<TOP_WARPS>(sv, si, lane, w);   // every warp holds the K best parts
   const int parts = best.id;
+  // K parts hold a logit of at least the K-th part's max: a smaller one is not
+  // among the K best (nothing is left out where fewer parts are numbers)
+  const float least = __shfl_sync(0xffffffffu, best.v, K - 1);
   best.clear();
   const float* zr = zf + static_cast<size_t>(r) * ldz;
   for (int j = w; j < K; j += 2 * TOP_WARPS) {
     float x[TOP_BATCH];
-    int v[TOP_BATCH];
+    int id[TOP_BATCH];
 #pragma unroll
     for (int k = 0; k < TOP_BATCH; ++k) {
       const int jj = j + (k / 4) * TOP_WARPS;
       const int p = __shfl_sync(0xffffffffu, parts, jj & 31);
       const long long at = static_cast<long long>(p) * PART_COLS + (k % 4) * 32 + lane;
-      v[k] = jj < K && p != TopK::NONE && at < V ? static_cast<int>(at) : -1;
-      x[k] = v[k] >= 0 ? zr[v[k]] : 0.f;
+      const bool in = jj < K && p != TopK::NONE && at < V;
+      x[k] = in ? zr[at] : 0.f;
+      id[k] = in && x[k] >= least ? static_cast<int>(at) : TopK::NONE;
     }
-#pragma unroll
-    for (int k = 0; k < TOP_BATCH; ++k) best.offer(x[k], v[k], v[k] >= 0, K, lane);
+    best.offer_all(x, id, K, lane);
   }
   best.merge_block<TOP_WARPS>(sv, si, lane, w);
   if (w == 0 && lane < K) {

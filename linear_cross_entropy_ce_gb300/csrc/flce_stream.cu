@@ -289,9 +289,10 @@ __global__ void __launch_bounds__(THREADS, 1)
               TopK best;
               best.v = list_v[tk * TopK::MAX + lane];
               best.id = list_i[tk * TopK::MAX + lane];
+              int id[8];
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                best.offer(x[j], r0 + j * 32 + lane, j * 32 + lane < rows, a.K, lane);
+              for (int j = 0; j < 8; ++j) id[j] = j * 32 + lane < rows ? r0 + j * 32 + lane : TopK::NONE;
+              best.offer_all(x, id, a.K, lane);
               __syncwarp();
               list_v[tk * TopK::MAX + lane] = best.v;
               list_i[tk * TopK::MAX + lane] = best.id;
@@ -394,8 +395,7 @@ __global__ void __launch_bounds__(MERGE_THREADS) logprob_stream_merge_kernel(con
   TopK best;
   best.clear();
   for (int e0 = 0;;) {
-#pragma unroll
-    for (int k = 0; k < MERGE_BATCH; ++k) best.offer(cv[k], ci[k], ci[k] != TopK::NONE, a.K, lane);
+    best.offer_all(cv, ci, a.K, lane);
     e0 += MERGE_BATCH * MERGE_THREADS;
     if (e0 >= entries) break;
     fetch(e0);

@@ -44,13 +44,13 @@ struct TopK {
     for (int o = 16; o > 0; o >>= 1) exchange(v, id, o, (lane & o) == 0);
   }
 
-  // Every lane offers one candidate (where ok).  Few pass the threshold once
-  // the list has filled: those are inserted one by one; more than a handful
-  // are sorted and merged.
-  __device__ __forceinline__ void offer(float cv, int cid, bool ok, int k, int lane) {
+  // Every lane offers one candidate (id NONE: none).  Few pass the threshold
+  // once the list has filled: those are inserted one by one; more than a
+  // handful are sorted and merged.
+  __device__ __forceinline__ void offer(float cv, int cid, int k, int lane) {
     const float tv = __shfl_sync(0xffffffffu, v, k - 1);
     const int ti = __shfl_sync(0xffffffffu, id, k - 1);
-    const bool pass = ok && better(cv, cid, tv, ti);
+    const bool pass = cid != NONE && better(cv, cid, tv, ti);
     unsigned m = __ballot_sync(0xffffffffu, pass);
     if (m == 0) return;                    // uniform over the warp, as all below
     if (__popc(m) > 4) {
@@ -72,6 +72,35 @@ struct TopK {
       const int ui = __shfl_up_sync(0xffffffffu, id, 1);
       if (lane > pos) { v = uv; id = ui; }
       if (lane == pos) { v = nv; id = ni; }
+    }
+  }
+
+  // Every lane offers B candidates.  Its best one goes first: with the lanes'
+  // best in the list, few of the others pass.
+  template <int B>
+  __device__ __forceinline__ void offer_all(const float (&cv)[B], const int (&cid)[B], int k, int lane) {
+    float bv = -INFINITY;
+    int bi = NONE;
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      if (cid[b] != NONE && better(cv[b], cid[b], bv, bi)) { bv = cv[b]; bi = cid[b]; }
+    const float tv = __shfl_sync(0xffffffffu, v, k - 1);
+    const int ti = __shfl_sync(0xffffffffu, id, k - 1);
+    if (!__any_sync(0xffffffffu, better(bv, bi, tv, ti))) return;
+    offer(bv, bi, k, lane);
+#pragma unroll 1
+    for (;;) {   // the lanes' next best ones
+      float nv = -INFINITY;
+      int ni = NONE;
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+        if (cid[b] != NONE && better(bv, bi, cv[b], cid[b]) && better(cv[b], cid[b], nv, ni)) { nv = cv[b]; ni = cid[b]; }
+      const float wv = __shfl_sync(0xffffffffu, v, k - 1);
+      const int wi = __shfl_sync(0xffffffffu, id, k - 1);
+      if (!__any_sync(0xffffffffu, ni != NONE && better(nv, ni, wv, wi))) return;
+      offer(nv, ni, k, lane);
+      bv = nv;
+      bi = ni;
     }
   }
 
