@@ -149,11 +149,12 @@ T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws)
 // runs; the kernel has to call ptx::grid_dependency_wait() before it reads or
 // writes anything that kernel (or an earlier one) touches.
 template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kernel)(P...), unsigned blocks, unsigned threads, cudaStream_t st, A... args) {
+cudaError_t launch_dependent_smem(void (*kernel)(P...), unsigned blocks, unsigned threads, size_t smem,
+                                  cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks, 1, 1);
   cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = 0;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -161,6 +162,11 @@ cudaError_t launch_dependent(void (*kernel)(P...), unsigned blocks, unsigned thr
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned blocks, unsigned threads, cudaStream_t st,
+                             const A&... args) {
+  return launch_dependent_smem(kernel, blocks, threads, 0, st, args...);
 }
 
 // Elementwise / bookkeeping kernels (flce_aux.cu).
@@ -185,8 +191,11 @@ struct StreamArgs {
   int* hdr;
   float* zt;               // [N]
   float4* stat;            // [N][ctas] max, sum, weighted sum
-  float* top_v;            // [N][ctas][K]
-  int* top_i;
+  float* zf;               // K > 0: [N][ldz] logits, and
+  long long ldz;
+  float* tile_max;         // [N][ctas][max_tiles]
+  uint32_t* group_max;     // [N][32] largest tile max (as an ordered integer) of each of K groups of tiles
+  int max_tiles;           // tiles of a CTA at most
   int* fail;               // [ctas]
   float* logp;
   float* entropy;          // or null
@@ -198,6 +207,7 @@ struct StreamMaps {
   CUtensorMap x, w[4];     // w[k]: boxes of 128 >> k weight rows
 };
 int stream_ctas(long long V, int sms);
+int stream_max_tiles(long long V, int ctas);
 int stream_tokens(int N);   // N padded to the tile sizes of the kernel
 cudaError_t stream_prepare();
 cudaError_t embedding_prepare();   // flce_embedding.cu

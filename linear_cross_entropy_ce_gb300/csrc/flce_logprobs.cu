@@ -384,7 +384,9 @@ namespace {
 // Workspace of the streaming form (N <= STREAM_MAX_TOKENS).
 struct StreamPlan {
   int ctas = 0;
-  size_t o_zt = 0, o_stat = 0, o_tv = 0, o_ti = 0, o_fail = 0, total = 0;
+  int max_tiles = 0;
+  long long ldz = 0;
+  size_t o_zt = 0, o_stat = 0, o_max = 0, o_group = 0, o_zf = 0, o_fail = 0, total = 0;
 };
 
 StreamPlan stream_plan(long long N, long long V, int K, int sms) {
@@ -398,8 +400,13 @@ StreamPlan stream_plan(long long N, long long V, int K, int sms) {
   };
   p.o_zt = take(size_t(N) * 4);
   p.o_stat = take(size_t(N) * p.ctas * 16);
-  p.o_tv = take(size_t(N) * p.ctas * K * 4);
-  p.o_ti = take(size_t(N) * p.ctas * K * 4);
+  p.max_tiles = stream_max_tiles(V, p.ctas);
+  p.ldz = cdiv(V, 32) * 32;
+  if (K > 0) {
+    p.o_max = take(size_t(N) * p.ctas * p.max_tiles * 4);
+    p.o_group = take(size_t(N) * TopK::MAX * 4);
+    p.o_zf = take(size_t(N) * p.ldz * 4);
+  }
   p.o_fail = take(size_t(p.ctas) * 4);
   p.total = off;
   return p;
@@ -474,8 +481,11 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
     a.hdr = hdr;
     a.zt = at<float>(workspace, p.o_zt);
     a.stat = at<float4>(workspace, p.o_stat);
-    a.top_v = at<float>(workspace, p.o_tv);
-    a.top_i = at<int>(workspace, p.o_ti);
+    a.zf = at<float>(workspace, p.o_zf);
+    a.ldz = p.ldz;
+    a.tile_max = at<float>(workspace, p.o_max);
+    a.max_tiles = p.max_tiles;
+    a.group_max = at<uint32_t>(workspace, p.o_group);
     a.fail = at<int>(workspace, p.o_fail);
     a.logp = logp; a.entropy = entropy; a.lse = lse; a.top_ids = top_ids; a.top_logp = top_logp;
     StreamMaps m;
@@ -486,7 +496,7 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
     const ProfScope prof = prof_launch_begin(st);
     const cudaError_t e = launch_stream(a, m, st);
     prof_launch_end(prof, MODE_STATS, st);
-    count_launches(1);   // the merge
+    count_launches(top_k > 0 ? 2 : 1);   // the merge, the clearing
     return e == cudaSuccess ? FLCE_OK : FLCE_ECUDA;
   }
   LpPlan p;

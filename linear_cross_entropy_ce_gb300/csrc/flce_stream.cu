@@ -11,10 +11,16 @@
 // TMA ring of 64-column K blocks, warp 1 issues the MMAs into one of two TMEM
 // accumulators, and eight epilogue warps turn a finished 256 x 32 slice of
 // logits around in shared memory, where each warp takes whole tokens: the
-// running softmax statistics, the target's logit, and the list of the best
-// logits (most tiles hold none: one comparison with the tile's max).  Every CTA
-// leaves per token its statistics and list; the second kernel, a block per
-// token, merges them.
+// running softmax statistics and the target's logit.  Every CTA leaves its
+// statistics per token; the second kernel, a block per token, merges them.
+// For top alternatives a tile's max and, where it matters, its logits are
+// stored, and the second kernel reads back the K best tiles only.  It does not
+// matter where K other tiles are known to have a larger max: the tiles are
+// dealt to K groups, and the least of the groups' maxima (kept in global
+// memory, read once a tile) bounds the K-th best logit from below.  After the
+// first tile of each CTA few pass.  (Storing every logit: 64 tokens, 8
+// alternatives at 2048 x 256000 184 us, with none stored 164; a sorted list per
+// CTA and token: 175, with 32 alternatives 212.)
 //
 // Bound by the weight's bytes: 2 H V at the HBM rate.  Every wait is bounded:
 // on time-out the CTA lets its copies in flight land, waits for its MMAs, frees
@@ -35,22 +41,28 @@ constexpr int EPI_THREADS = 32 * EPI_WARPS;
 constexpr int THREADS = 64 + EPI_THREADS;
 constexpr uint32_t EPI_BAR = 1;
 
-// The ring takes what the slice buffer and the lists leave of 227 KB.
+// The ring takes what the slice buffer leaves of 227 KB.
+constexpr int MAX_STAGES = 6;
 template <int NT>
 struct Cfg {
-  static constexpr int STAGES = NT <= 32 ? 5 : (NT == 64 ? 4 : 3);
-  static constexpr int SLICE = NT < 32 ? NT : 32;                 // tokens turned around at once
+  static constexpr int STAGES = NT == 16 ? 6 : (NT == 128 ? 4 : 5);
+  static constexpr int SLICE = NT == 32 ? 32 : 16;                // tokens turned around at once
   static constexpr int X_BYTES = NT * BK * 2;
   static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
   static constexpr int TURN_BYTES = SLICE * TILE_ROWS * 4;
-  static constexpr int LIST_BYTES = NT * TopK::MAX * 8;
   static constexpr int TMEM_COLS = 4 * NT;                        // two accumulators of two halves
-  static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + TURN_BYTES + LIST_BYTES + NT * 16 + 256;
+  static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + TURN_BYTES + NT * 20 + 256;
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 
+// fp32 as an unsigned integer of the same order; 0 is below every number.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
 struct Ctl {
-  uint64_t full[5], empty[5];
+  uint64_t full[MAX_STAGES], empty[MAX_STAGES];
   uint64_t tfull[2], tempty[2];
   uint64_t mma_done;
   uint32_t tmem_base;
@@ -91,11 +103,11 @@ struct Range {
   }
 };
 
-__device__ __forceinline__ Range my_range(const StreamArgs& a) {
+__device__ __forceinline__ Range range_of(const StreamArgs& a, int cta) {
   const long long units = (static_cast<long long>(a.V) + UNIT_ROWS - 1) / UNIT_ROWS;
   Range r;
-  r.u0 = static_cast<int>(units * blockIdx.x / a.ctas);
-  r.u1 = static_cast<int>(units * (blockIdx.x + 1) / a.ctas);
+  r.u0 = static_cast<int>(units * cta / a.ctas);
+  r.u1 = static_cast<int>(units * (cta + 1) / a.ctas);
   r.tiles = (r.u1 - r.u0 + TILE_ROWS / UNIT_ROWS - 1) / (TILE_ROWS / UNIT_ROWS);
   return r;
 }
@@ -107,13 +119,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* turn = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE_BYTES);          // [SLICE][TILE_ROWS]
-  float* list_v = turn + C::SLICE * TILE_ROWS;                                        // [NT][32]
-  int* list_i = reinterpret_cast<int*>(list_v + NT * TopK::MAX);
-  float4* stat = reinterpret_cast<float4*>(list_i + NT * TopK::MAX);                  // [NT]
-  Ctl* ctl = reinterpret_cast<Ctl*>(stat + NT);
+  float4* stat = reinterpret_cast<float4*>(turn + C::SLICE * TILE_ROWS);              // [NT]
+  uint32_t* bound = reinterpret_cast<uint32_t*>(stat + NT);                           // [NT]
+  Ctl* ctl = reinterpret_cast<Ctl*>(bound + NT);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint64_t to = a.timeout_ns;
-  const Range range = my_range(a);
+  const Range range = range_of(a, static_cast<int>(blockIdx.x));
   const int kbt = (a.H + BK - 1) / BK;
 
   if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -216,14 +227,28 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int w = warp - 2;
     const int q = warp & 3;            // TMEM lane quarter this warp may access
     const int half = w / 4;            // the 128 rows of the tile it reads
-    for (int tk = w; tk < a.N; tk += EPI_WARPS) {
-      list_v[tk * TopK::MAX + lane] = -INFINITY;
-      list_i[tk * TopK::MAX + lane] = TopK::NONE;
+    for (int tk = w; tk < a.N; tk += EPI_WARPS)
       if (lane == 0) stat[tk] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-    }
     __syncwarp();
+    if (a.K > 0) ptx::grid_dependency_wait();   // the groups' maxima have been cleared
     uint32_t acc = 0, acc_phase = 0;
     for (int i = 0; i < range.tiles; ++i) {
+      if (a.K > 0) {   // the bounds of this warp's tokens
+        for (int t0 = w; t0 < a.N; t0 += 4 * EPI_WARPS) {
+          uint32_t g[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int tk = t0 + u * EPI_WARPS;
+            g[u] = tk < a.N && lane < a.K ? ptx::ld_relaxed_gpu(a.group_max + tk * TopK::MAX + lane) : 0xffffffffu;
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t least = __reduce_min_sync(0xffffffffu, g[u]);
+            if (lane == 0 && t0 + u * EPI_WARPS < a.N) bound[t0 + u * EPI_WARPS] = least;
+          }
+        }
+        __syncwarp();
+      }
       const int r0 = range.start(i), rows = min(range.start(i + 1), a.V) - r0;
       const bool ok = wait(&ctl->tfull[acc], acc_phase, ctl, to, a.hdr, S_TMEM_FULL);
       if (!ptx::named_bar_and(EPI_BAR, EPI_THREADS, ok)) break;   // all epilogue threads leave together
@@ -283,21 +308,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (at >= 0 && at < rows) a.zt[tk] = z[at];
           }
           if (a.K > 0) {
-            // ids rise along the range, so an equal logit is never better than a listed one
-            const float worst = list_v[tk * TopK::MAX + a.K - 1];
-            if (mx > worst || list_i[tk * TopK::MAX + a.K - 1] == TopK::NONE) {   // uniform over the warp
-              TopK best;
-              best.v = list_v[tk * TopK::MAX + lane];
-              best.id = list_i[tk * TopK::MAX + lane];
-              int id[8];
+            if (order_key(mx) >= bound[tk]) {
+              float* zf = a.zf + static_cast<size_t>(tk) * a.ldz + r0 + lane;
 #pragma unroll
-              for (int j = 0; j < 8; ++j) id[j] = j * 32 + lane < rows ? r0 + j * 32 + lane : TopK::NONE;
-              best.offer_all(x, id, a.K, lane);
-              __syncwarp();
-              list_v[tk * TopK::MAX + lane] = best.v;
-              list_i[tk * TopK::MAX + lane] = best.id;
-              __syncwarp();
+              for (int j = 0; j < 8; ++j)
+                if (j * 32 + lane < rows) zf[j * 32] = x[j];
+              if (lane == 0) atomicMax(a.group_max + tk * TopK::MAX + (blockIdx.x + i) % a.K, order_key(mx));
             }
+            if (lane == 0)
+              a.tile_max[static_cast<size_t>(tk) * a.ctas * a.max_tiles + blockIdx.x * a.max_tiles + i] = mx;
           }
         }
         ptx::named_bar_sync(EPI_BAR, EPI_THREADS);   // the slice buffer is free again
@@ -306,12 +325,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       if (acc == 0) acc_phase ^= 1u;
     }
     for (int tk = w; tk < a.N; tk += EPI_WARPS) {
-      const size_t o = static_cast<size_t>(tk) * a.ctas + blockIdx.x;
       __syncwarp();
-      if (lane == 0) a.stat[o] = stat[tk];
-      if (lane < a.K) {
-        a.top_v[o * a.K + lane] = list_v[tk * TopK::MAX + lane];
-        a.top_i[o * a.K + lane] = list_i[tk * TopK::MAX + lane];
+      if (lane == 0) {
+        const size_t o = static_cast<size_t>(tk) * a.ctas + blockIdx.x;
+        a.stat[o] = stat[tk];
+        // the last entry of a CTA of fewer tiles than others: NaN is never taken
+        if (a.K > 0 && range.tiles < a.max_tiles)
+          a.tile_max[o * a.max_tiles + a.max_tiles - 1] = __int_as_float(0x7fc00000);
       }
     }
   }
@@ -323,13 +343,14 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (threadIdx.x == 0) a.fail[blockIdx.x] = *reinterpret_cast<volatile int*>(&ctl->abort);
 }
 
-// One token per block: its row from the CTAs' statistics and lists.  Launched
-// while the first kernel drains (programmatic dependent launch); what it reads
-// is loaded in one go, since the latency of a few dependent loads is all there
-// is to it.
+// One token per block: its row from the CTAs' statistics, and its top
+// alternatives from the K best tiles (an alternative lies in one of them, as in
+// the chunked form).  Launched while the first kernel drains; what it reads is
+// loaded in batches, since the latency of a few dependent loads is all there is
+// to it.
 constexpr int MERGE_WARPS = 8;
 constexpr int MERGE_THREADS = 32 * MERGE_WARPS;
-constexpr int MERGE_BATCH = 4;   // list entries per thread in flight
+constexpr int MERGE_BATCH = 4;   // tile maxima per thread in flight
 __global__ void __launch_bounds__(MERGE_THREADS) logprob_stream_merge_kernel(const StreamArgs a) {
   __shared__ Stat part[MERGE_WARPS];
   __shared__ float sv[MERGE_WARPS][32];
@@ -338,17 +359,17 @@ __global__ void __launch_bounds__(MERGE_THREADS) logprob_stream_merge_kernel(con
   const int t = a.targets[n];
   const bool bad = t != a.ii && (t < 0 || t >= a.V);
   ptx::grid_dependency_wait();
-  const size_t base = static_cast<size_t>(n) * a.ctas * a.K;
-  const int entries = a.ctas * a.K;
   const float zt = bad || t == a.ii ? 0.f : a.zt[n];
+  const int tiles = a.K > 0 ? a.ctas * a.max_tiles : 0;
+  const float* tile_max = a.tile_max + static_cast<size_t>(n) * tiles;
   float cv[MERGE_BATCH];
   int ci[MERGE_BATCH];
   auto fetch = [&](int e0) {
 #pragma unroll
     for (int k = 0; k < MERGE_BATCH; ++k) {
       const int e = e0 + k * MERGE_THREADS + tid;
-      ci[k] = e < entries ? a.top_i[base + e] : TopK::NONE;
-      cv[k] = e < entries ? a.top_v[base + e] : 0.f;
+      ci[k] = e < tiles ? e : TopK::NONE;
+      cv[k] = e < tiles ? tile_max[e] : 0.f;
     }
   };
   fetch(0);
@@ -397,8 +418,38 @@ __global__ void __launch_bounds__(MERGE_THREADS) logprob_stream_merge_kernel(con
   for (int e0 = 0;;) {
     best.offer_all(cv, ci, a.K, lane);
     e0 += MERGE_BATCH * MERGE_THREADS;
-    if (e0 >= entries) break;
+    if (e0 >= tiles) break;
     fetch(e0);
+  }
+  best.merge_block<MERGE_WARPS>(sv, si, lane, w);   // every warp holds the K best tiles
+  const int top = best.id;
+  const float least = __shfl_sync(0xffffffffu, best.v, a.K - 1);   // of K logits at least
+  best.clear();
+  const float* z = a.zf + static_cast<size_t>(n) * a.ldz;
+  for (int j = w; j < a.K; j += 2 * MERGE_WARPS) {   // two tiles in flight
+    float x[16];
+    int id[16];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int jj = j + u * MERGE_WARPS;
+      const int e = __shfl_sync(0xffffffffu, top, jj & 31);
+      int r0 = 0, rows = 0;
+      if (jj < a.K && e != TopK::NONE) {
+        const Range r = range_of(a, e / a.max_tiles);
+        r0 = r.start(e % a.max_tiles);
+        rows = min(r.start(e % a.max_tiles + 1), a.V) - r0;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int at = k * 32 + lane;
+        x[u * 8 + k] = at < rows ? z[r0 + at] : 0.f;
+        id[u * 8 + k] = at < rows ? r0 + at : TopK::NONE;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (!(x[k] >= least)) id[k] = TopK::NONE;
+    best.offer_all(x, id, a.K, lane);
   }
   best.merge_block<MERGE_WARPS>(sv, si, lane, w);
   if (w == 0 && lane < a.K) {
@@ -409,17 +460,34 @@ __global__ void __launch_bounds__(MERGE_THREADS) logprob_stream_merge_kernel(con
   }
 }
 
+__global__ void clear_groups_kernel(uint32_t* group_max, int n) {
+  ptx::grid_launch_dependents();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) group_max[i] = 0u;
+}
+
 template <int NT>
 cudaError_t prepare() {
   return cudaFuncSetAttribute(logprob_stream_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NT>::SMEM);
 }
 
 template <int NT>
-void launch(const StreamArgs& a, const StreamMaps& m, cudaStream_t s) {
-  logprob_stream_kernel<NT><<<a.ctas, THREADS, Cfg<NT>::SMEM, s>>>(m, a);
+cudaError_t launch(const StreamArgs& a, const StreamMaps& m, cudaStream_t s) {
+  if (a.K == 0) {
+    logprob_stream_kernel<NT><<<a.ctas, THREADS, Cfg<NT>::SMEM, s>>>(m, a);
+    return cudaGetLastError();
+  }
+  // the weight streams while the groups' maxima are cleared
+  clear_groups_kernel<<<1, 512, 0, s>>>(a.group_max, a.N * TopK::MAX);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_dependent_smem(logprob_stream_kernel<NT>, a.ctas, THREADS, Cfg<NT>::SMEM, s, m, a);
 }
 
 }  // namespace
+
+int stream_max_tiles(long long V, int ctas) {
+  return static_cast<int>(cdiv(cdiv(cdiv(V, UNIT_ROWS), ctas), TILE_ROWS / UNIT_ROWS));
+}
 
 int stream_ctas(long long V, int sms) {
   const long long units = cdiv(V, UNIT_ROWS);
@@ -437,13 +505,13 @@ cudaError_t stream_prepare() {
 int stream_tokens(int N) { return N <= 16 ? 16 : (N <= 32 ? 32 : (N <= 64 ? 64 : 128)); }
 
 cudaError_t launch_stream(const StreamArgs& a, const StreamMaps& m, cudaStream_t s) {
+  cudaError_t e;
   switch (stream_tokens(a.N)) {
-    case 16: launch<16>(a, m, s); break;
-    case 32: launch<32>(a, m, s); break;
-    case 64: launch<64>(a, m, s); break;
-    default: launch<128>(a, m, s); break;
+    case 16: e = launch<16>(a, m, s); break;
+    case 32: e = launch<32>(a, m, s); break;
+    case 64: e = launch<64>(a, m, s); break;
+    default: e = launch<128>(a, m, s); break;
   }
-  cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_dependent(logprob_stream_merge_kernel, a.N, MERGE_THREADS, s, a);
 }

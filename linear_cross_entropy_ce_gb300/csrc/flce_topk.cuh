@@ -104,17 +104,17 @@ struct TopK {
     }
   }
 
-  // The lists of the block's WARPS warps become one, held by every warp.
+  // The lists of the block's WARPS (a power of two) warps become one, held by
+  // every warp: in each of log2(WARPS) rounds a warp merges its partner's list.
   template <int WARPS>
   __device__ __forceinline__ void merge_block(float (*sv)[32], int (*si)[32], int lane, int w) {
-    __syncthreads();
-    sv[w][lane] = v;
-    si[w][lane] = id;
-    __syncthreads();
 #pragma unroll 1
-    for (int o = 1; o < WARPS; ++o) {
-      const int from = (w + o) % WARPS;
-      merge(sv[from][lane], si[from][lane], lane);
+    for (int o = 1; o < WARPS; o <<= 1) {
+      __syncthreads();
+      sv[w][lane] = v;
+      si[w][lane] = id;
+      __syncthreads();
+      merge(sv[w ^ o][lane], si[w ^ o][lane], lane);
     }
   }
 };
