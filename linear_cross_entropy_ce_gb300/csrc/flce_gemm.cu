@@ -343,6 +343,15 @@ __device__ __forceinline__ void epi_logits(const GemmArgs& a, const Shape& s, co
   }
 }
 
+// 128 bytes of one row in four 32-byte stores.
+__device__ __forceinline__ void store_f32x32(float* dst, const float (&v)[32]) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 8)
+    ptx::st_global_v8(dst + k, __float_as_uint(v[k]), __float_as_uint(v[k + 1]), __float_as_uint(v[k + 2]),
+                      __float_as_uint(v[k + 3]), __float_as_uint(v[k + 4]), __float_as_uint(v[k + 5]),
+                      __float_as_uint(v[k + 6]), __float_as_uint(v[k + 7]));
+}
+
 // Statistics of one row and part.  With c2 = log2(e) / temperature and
 // d = (z - max) c2 <= 0: sum 2^d and sum d 2^d, from which the row kernel
 // forms log-sum-exp and entropy.  The stats array is part-major, so a warp's
@@ -357,7 +366,8 @@ __device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, con
   if (ncol <= 0) return;                          // uniform over the warpgroup
   float ztv = 0.f;
   float* zrow = a.zf + static_cast<size_t>(grow) * a.ldz + c0;
-  const bool store = a.zf != nullptr && rv;
+  const bool all = a.K > 0 && a.bound == nullptr && rv;   // every logit is kept
+  const uint32_t bound = a.bound != nullptr && rv ? ptx::ld_relaxed_gpu(a.bound + grow) : 0u;
   Stat st = {-INFINITY, 0.f, 0.f};
 #pragma unroll 1
   for (int j = 0; j < GROUP_COLS / 32; ++j) {
@@ -369,13 +379,7 @@ __device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, con
       for (int k = 0; k < 32; ++k)
         if (j * 32 + k == tl) ztv = v[k];
     }
-    if (store) {
-#pragma unroll
-      for (int k = 0; k < 32; k += 8)
-        ptx::st_global_v8(zrow + j * 32 + k, __float_as_uint(v[k]), __float_as_uint(v[k + 1]),
-                          __float_as_uint(v[k + 2]), __float_as_uint(v[k + 3]), __float_as_uint(v[k + 4]),
-                          __float_as_uint(v[k + 5]), __float_as_uint(v[k + 6]), __float_as_uint(v[k + 7]));
-    }
+    if (all) store_f32x32(zrow + j * 32, v);
     if (j * 32 + 32 > ncol) {                     // the block straddles the end of the vocabulary
 #pragma unroll
       for (int k = 0; k < 32; ++k)
@@ -423,6 +427,30 @@ __device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, con
     p[np] = st.s;
     p[2 * np] = st.d;
     if (tl >= 0 && tl < ncol) a.zt[grow] = ztv;
+  }
+  if (a.bound == nullptr) return;
+  // Top alternatives: the logits of this part are kept unless K other parts of
+  // the row are known to have a larger max.  The parts are dealt to K groups;
+  // the least of the groups' maxima is such a bound, and only a part above it
+  // can raise it.
+  const uint32_t key = order_key(st.m);
+  const bool keep = rv && key >= bound;
+  if (!__any_sync(0xffffffffu, keep)) return;
+  if (keep) {
+    uint32_t* g = a.group_max + static_cast<size_t>(grow) * a.group_stride;
+    atomicMax(g + (c0 / PART_COLS) % a.K, key);
+    uint32_t least = 0xffffffffu;
+    for (int k = 0; k < a.K; k += 4) {   // entries behind the K-th hold the largest integer
+      const uint4 q = __ldcg(reinterpret_cast<const uint4*>(g + k));
+      least = min(least, min(min(q.x, q.y), min(q.z, q.w)));
+    }
+    if (least > bound) atomicMax(a.bound + grow, least);
+  }
+#pragma unroll 1
+  for (int j = 0; j * 32 < ncol; ++j) {   // uniform over the warp
+    float v[32];
+    ptx::tmem_ld32(tbase + j * 32, v);
+    if (keep) store_f32x32(zrow + j * 32, v);
   }
 }
 

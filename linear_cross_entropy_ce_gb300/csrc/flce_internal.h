@@ -90,7 +90,11 @@ struct GemmArgs {
   int gw_bf16;          // BWD of a call with one chunk: grad_weight tiles are rounded and stored as bf16
   float c2;             // log2(e) / temperature: z c2 is the scaled logit in base-2 units
   float* stats;         // STATS: [3][nparts][C] part max (raw z), sum of 2^d, sum of d 2^d, d = (z - max) c2
-  float* zf;            // STATS: [C][ldz] fp32 logits, or null
+  int K;                // STATS: top alternatives, and for K > 0
+  float* zf;            //   [C][ldz] fp32 logits of the parts that may hold one
+  uint32_t* bound;      //   [C] ordered integer that a part's max has to reach, or null: every part is kept
+  uint32_t* group_max;  //   [C][group_stride] largest part max of each of K groups of parts
+  int group_stride;     //   K rounded up to 4
   const DzRow* rowc;    // DZ: [C] (rows past the valid ones hold zeros)
 };
 
@@ -228,6 +232,8 @@ struct FrontArgs {
   float *logp, *lse, *entropy;        // forward outputs
   int* top_ids;
   float* top_logp;
+  uint32_t *bound, *group_max;        // K > 0: cleared
+  int group_stride;
   DzRow* rowc;                        // backward
   float temperature;
   const float *lse_in, *entropy_in, *grad_logp, *grad_entropy;

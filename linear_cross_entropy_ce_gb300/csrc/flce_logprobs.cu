@@ -73,6 +73,20 @@ __global__ void __launch_bounds__(128)
   }
 }
 
+// Bounds of the top alternatives before the first logit; the groups behind the
+// K-th (up to the stride) never bind.
+__device__ __forceinline__ void clear_bounds(uint32_t* bound, uint32_t* group_max, int stride, int K, int C, int first,
+                                             int step) {
+  if (!bound) return;
+  for (int i = first; i < C; i += step) bound[i] = 0u;
+  for (long long i = first; i < static_cast<long long>(C) * stride; i += step)
+    group_max[i] = static_cast<int>(i % stride) < K ? 0u : 0xffffffffu;
+}
+
+__global__ void clear_bounds_kernel(uint32_t* bound, uint32_t* group_max, int stride, int K, int C) {
+  clear_bounds(bound, group_max, stride, K, C, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
+}
+
 // Everything before the first GEMM of a call of one chunk, in one launch: the
 // valid tokens' rows gathered into the tile source in order, their targets (and
 // for the backward the constants of MODE_DZ), the outputs of the tokens left
@@ -158,6 +172,8 @@ __global__ void __launch_bounds__(FRONT_THREADS) probs_front_kernel(const FrontA
       }
     }
   }
+  clear_bounds(a.bound, a.group_max, a.group_stride, a.K, a.C, blockIdx.x * FRONT_THREADS + tid,
+               gridDim.x * FRONT_THREADS);
   // padding rows up to the next multiple of 128
   const int end = min(a.C, (total + BM - 1) / BM * BM);
   for (int r = total + static_cast<int>(blockIdx.x) * FRONT_WARPS + w; r < end; r += gridDim.x * FRONT_WARPS) {
@@ -326,7 +342,9 @@ __global__ void mark_failed_kernel(const int* hdr, uint16_t* grad_hidden, float*
 struct LpPlan {
   long long C = 0, n_chunks = 0, ldz = 0;
   int nvt = 0, nparts = 0;
-  size_t o_idx = 0, o_cnt = 0, o_xc = 0, o_tc = 0, o_zt = 0, o_ml = 0, o_stats = 0, o_zf = 0, total = 0;
+  size_t o_idx = 0, o_cnt = 0, o_xc = 0, o_tc = 0, o_zt = 0, o_ml = 0, o_stats = 0, o_bound = 0, o_group = 0,
+         o_zf = 0, total = 0;
+  int group_stride = 0;
 };
 
 LpPlan lp_layout(long long N, long long H, long long V, long long C, int K) {
@@ -349,7 +367,12 @@ LpPlan lp_layout(long long N, long long H, long long V, long long C, int K) {
   p.o_zt = take(size_t(C) * 4);
   p.o_ml = take(size_t(C) * 8);
   p.o_stats = take(size_t(C) * p.nparts * 12);
-  if (K > 0) p.o_zf = take(size_t(C) * p.ldz * 4);
+  p.group_stride = (K + 3) / 4 * 4;
+  if (K > 0) {
+    p.o_bound = take(size_t(C) * 4);
+    p.o_group = take(size_t(C) * p.group_stride * 4);
+    p.o_zf = take(size_t(C) * p.ldz * 4);
+  }
   p.total = off;
   return p;
 }
@@ -368,10 +391,10 @@ bool lp_plan(long long N, long long H, long long V, int K, size_t bytes, LpPlan*
 }
 
 // Default workspace: 5% of the bf16 logits as for the loss, but no less than
-// what lets problems of a few thousand tokens run in one chunk (64 MiB; 1 GiB
+// what lets problems of a few thousand tokens run in one chunk (64 MiB; 2 GiB
 // with the fp32 logits of top alternatives): every chunk reads the weight.
 size_t lp_default_bytes(long long N, long long H, long long V, int K) {
-  const size_t budget = std::max(size_t(N) * size_t(V) * 2 / 20, size_t(K > 0 ? 1024 : 64) << 20);
+  const size_t budget = std::max(size_t(N) * size_t(V) * 2 / 20, size_t(K > 0 ? 2048 : 64) << 20);
   LpPlan p;
   if (lp_plan(N, H, V, K, budget, &p)) return p.total;
   return lp_layout(N, H, V, BM, K).total;
@@ -531,13 +554,22 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
   g.tc = tc;
   g.zt = zt;
   g.stats = stats;
+  g.K = top_k;
   g.zf = zf;
+  // The bound pays once each of its K groups has several parts (by 16 parts a
+  // group: 1024 tokens x 8 at 2048 x 256000, 2000 parts, GEMM 20% faster; x 32
+  // at 512 x 16000, 125 parts, 15% slower).
+  if (top_k > 0 && p.nparts >= 16 * top_k) {
+    g.bound = at<uint32_t>(workspace, p.o_bound);
+    g.group_max = at<uint32_t>(workspace, p.o_group);
+  }
+  g.group_stride = p.group_stride;
   g.c2 = LOG2E / temperature;
 
   const int grid = 2 * static_cast<int>(std::min<long long>(cdiv(p.C, PAIR_M) * p.nvt, dev.pairs));
   auto chk = [](cudaError_t e) { return e == cudaSuccess; };
   const bool front = p.n_chunks == 1 && N <= FRONT_MAX_TOKENS;
-  count_launches(front ? (top_k > 0 ? 3 : 2) : 1 + p.n_chunks * (top_k > 0 ? 3 : 2));
+  count_launches(front ? (top_k > 0 ? 3 : 2) : 1 + p.n_chunks * (top_k > 0 ? 4 : 2));
   RowArgs ra;
   ra.hdr = hdr; ra.idx = idx; ra.targets = targets;
   ra.N = N; ra.C = g.C; ra.nparts = p.nparts; ra.ii = ignore_index; ra.K = top_k;
@@ -552,6 +584,7 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
     f.targets = targets;
     f.N = static_cast<int>(N); f.H = g.H; f.V = g.V; f.ii = ignore_index; f.C = g.C; f.K = top_k;
     f.hdr = hdr; f.idx = idx; f.tc = tc; f.xc = xc; f.counters = counters; f.n_counters = 1;
+    f.bound = g.bound; f.group_max = g.group_max; f.group_stride = g.group_stride;
     f.logp = logp; f.lse = lse; f.entropy = entropy; f.top_ids = top_ids; f.top_logp = top_logp;
     if (!chk(launch_probs_front(f, st))) return FLCE_ECUDA;
   } else if (!chk(launch_prep(targets, N, static_cast<int>(V), ignore_index, hdr, idx, nullptr, counters, p.n_chunks,
@@ -564,6 +597,10 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
     if (!front && !chk(launch_gather(static_cast<const uint16_t*>(hidden), targets, hdr, idx, g.c0, g.C, g.H, xc, tc, 0,
                                      g.V, st)))
       return FLCE_ECUDA;
+    if (!front && g.bound) {
+      clear_bounds_kernel<<<152, 256, 0, st>>>(g.bound, g.group_max, g.group_stride, top_k, g.C);
+      if (!chk(cudaGetLastError())) return FLCE_ECUDA;
+    }
     if (!chk(gemm_launch(g, m, grid, st, front))) return FLCE_ECUDA;
     ra.c0 = g.c0;
     if (!chk(launch_dependent(logprob_rows_kernel, ra.row_blocks + (!front && c == 0 ? left_blocks : 0),

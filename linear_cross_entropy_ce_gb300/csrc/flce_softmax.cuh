@@ -28,4 +28,10 @@ __device__ __forceinline__ Stat merge(const Stat& a, const Stat& b, float c2) {
   return r;
 }
 
+// fp32 as an unsigned integer of the same order; 0 is below every number.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
 }  // namespace flce

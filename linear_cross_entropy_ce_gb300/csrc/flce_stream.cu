@@ -55,12 +55,6 @@ struct Cfg {
   static_assert(SMEM <= 232448, "shared memory budget");
 };
 
-// fp32 as an unsigned integer of the same order; 0 is below every number.
-__device__ __forceinline__ uint32_t order_key(float v) {
-  const uint32_t u = __float_as_uint(v);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-
 struct Ctl {
   uint64_t full[MAX_STAGES], empty[MAX_STAGES];
   uint64_t tfull[2], tempty[2];

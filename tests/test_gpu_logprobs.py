@@ -133,6 +133,31 @@ def test_sorted_logits(env, N, sign):
     check_forward(o, logprobs_oracle(X, W, t, top_k=32), 1.0, 32)
 
 
+@pytest.mark.parametrize("N,chunk", [(1, 0), (20, 0), (120, 0), (300, 0), (300, 128)])
+@pytest.mark.parametrize("kind", ["random", "rising", "falling", "equal", "peaks"])
+def test_alternatives_over_many_parts(env, N, chunk, kind):
+    """Vocabularies of many more parts than alternatives, where only parts above a running bound are kept."""
+    flce, torch, dev = env
+    V, K = 20003, 8
+    X, W, t = problem(N, 64, V, seed=7, ignored=0.1)
+    if kind != "random":
+        X = np.zeros((N, 64))
+        X[:, 0], X[:, 1] = 1, 1
+        v = np.arange(V)[::-1] if kind == "falling" else np.arange(V)
+        W = np.zeros((V, 64))
+        if kind in ("rising", "falling"):
+            W[:, 0], W[:, 1] = v // 128, (v % 128) / 128   # both exact in bf16
+        elif kind == "peaks":
+            W[(v * 7919) % V < 12, 0] = 3   # a dozen equal peaks far apart
+    T = 1.0 if kind in ("random", "peaks", "equal") else 16.0
+    h, w, tt = to_gpu(torch, dev, X, W, t)
+    kw = {}
+    if chunk:   # the fp32 logits of `chunk` rows and the rest
+        kw["workspace"] = flce.new_workspace((V + 64) * 4 * chunk + (1 << 20), dev)
+    o = flce.token_logprobs(h, w, tt, temperature=T, top_k=K, **kw)
+    check_forward(o, logprobs_oracle(X, W, t, temperature=T, top_k=K), T, K)
+
+
 @pytest.mark.parametrize("N", [4, 150])
 def test_extreme_rows(env, N):
     """A dominant logit, a row of large logits, rows with NaN and inf: only those rows are NaN."""

@@ -61,7 +61,7 @@ def test_workspace_sizes(flce):
     N, H, V = 16384, 4096, 128256
     assert 0 < lib.flce_logprobs_workspace_bytes(N, H, V, 0) <= 0.05 * N * V * 2
     assert 0 < lib.flce_logprobs_workspace_bytes(64, H, V, 8) <= 256 << 20
-    assert 0 < lib.flce_logprobs_workspace_bytes(N, H, V, 8) <= 1 << 30
+    assert 0 < lib.flce_logprobs_workspace_bytes(N, H, V, 8) <= 2 << 30
     assert 0 < lib.flce_logprobs_bwd_workspace_bytes(N, H, V, 0) <= 2 << 30
     assert 0 < lib.flce_logprobs_bwd_workspace_bytes(16 * N, H, V, 0) <= 0.05 * 16 * N * V * 2
     assert lib.flce_logprobs_bwd_workspace_bytes(N, H, V, 2) > V * H * 4   # the accumulator of several chunks
