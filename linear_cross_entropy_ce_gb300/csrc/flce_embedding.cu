@@ -405,7 +405,7 @@ __global__ void __cluster_dims__(CS_BLOCKS, 1, 1) __launch_bounds__(CS_THREADS)
 // sums over runs of equal ids
 // ---------------------------------------------------------------------------
 constexpr int SEG_WARPS = 8;
-constexpr int MIN_CHUNK = 32;          // sorted entries per chunk, and
+constexpr int MIN_CHUNK = 64;          // sorted entries per chunk (32 to 128 tried), and
 constexpr int MAX_CHUNKS = 4096;       // at most this many chunks (two partial sums of H floats each)
 constexpr int ZERO_ROWS = 32;          // grad_weight rows a warp looks up at once
 constexpr int ZERO_MAX_ROWS = 8192;    // rows a block marks at most (1 KB of bits)

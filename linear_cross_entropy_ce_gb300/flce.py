@@ -489,11 +489,19 @@ def token_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Te
             if nb == 0:
                 raise FlceError(FLCE_EINVAL, "workspace size")
             workspace = new_workspace(nb, dev)
-        _check_workspace(workspace, dev)
-        row = ((N,), torch.float32)
-        o = _outputs(out, {"logp": row, "lse": row, "entropy": row if entropy else None,
-                           "top_ids": ((N, top_k), torch.int32) if top_k else None,
-                           "top_logp": ((N, top_k), torch.float32) if top_k else None}, dev)
+        else:
+            _check_workspace(workspace, dev)
+        if out is None:   # spelled out: a decode step is as short as its host work
+            f32 = torch.float32
+            o = {"logp": torch.empty(N, dtype=f32, device=dev), "lse": torch.empty(N, dtype=f32, device=dev),
+                 "entropy": torch.empty(N, dtype=f32, device=dev) if entropy else None,
+                 "top_ids": torch.empty((N, top_k), dtype=torch.int32, device=dev) if top_k else None,
+                 "top_logp": torch.empty((N, top_k), dtype=f32, device=dev) if top_k else None}
+        else:
+            row = ((N,), torch.float32)
+            o = _outputs(out, {"logp": row, "lse": row, "entropy": row if entropy else None,
+                               "top_ids": ((N, top_k), torch.int32) if top_k else None,
+                               "top_logp": ((N, top_k), torch.float32) if top_k else None}, dev)
         _ok(library().flce_logprobs(_addr(hidden), _addr(weight), _addr(targets), N, H, V, int(ignore_index),
                                     float(temperature), top_k, _addr(o["logp"]), _addr(o["entropy"]), _addr(o["lse"]),
                                     _addr(o["top_ids"]), _addr(o["top_logp"]), _addr(workspace), workspace.numel(), st),
@@ -532,7 +540,8 @@ def token_logprobs_bwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torc
             if nb == 0:
                 raise FlceError(FLCE_EINVAL, "workspace size")
             workspace = new_workspace(nb, dev)
-        _check_workspace(workspace, dev)
+        else:
+            _check_workspace(workspace, dev)
         o = _outputs(out, {"grad_hidden": ((N, H), torch.bfloat16) if need_hidden else None,
                            "grad_weight": ((V, H), grad_weight_dtype) if need_weight else None}, dev)
         _ok(library().flce_logprobs_bwd(_addr(hidden), _addr(weight), _addr(targets), N, H, V, int(ignore_index), flags,
@@ -657,7 +666,8 @@ def embedding_bwd(grad_out: torch.Tensor, ids: torch.Tensor, num_rows: int, scal
             if nb == 0:
                 raise FlceError(FLCE_EINVAL, "workspace size")
             workspace = new_workspace(nb, dev)
-        _check_workspace(workspace, dev)
+        else:
+            _check_workspace(workspace, dev)
         o = _outputs(out, {"grad_weight": ((V, H), grad_weight_dtype)}, dev)
         _ok(library().flce_embedding_bwd(_addr(grad_out), _addr(ids), N, H, V, EMBEDDING_DTYPES[grad_out.dtype],
                                          float(scale), -1 if padding_idx is None else int(padding_idx),
