@@ -89,7 +89,9 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctl* ctl, u
   return ptx::mbar_test(bar, parity) || wait_slow(bar, parity, ctl, timeout_ns, honor_abort, hdr, site);
 }
 
-// This CTA's tiles: units [u0, u1) of 16 rows, spread evenly over its tiles.
+// This CTA's tiles: units [u0, u1) of 16 rows, spread evenly over its tiles (a
+// short last tile would fill the ring's stages with few bytes: one token at
+// 4096 x 128256 177 us against 166).
 struct Range {
   int u0, u1, tiles;
   __device__ __forceinline__ int start(int i) const {   // first row of tile i (also: the end of tile i - 1)

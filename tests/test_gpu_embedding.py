@@ -79,6 +79,22 @@ def test_gradient(env, N, H, V, kind, dtype, grad):  # noqa: F811
     assert torch.equal(o["grad_weight"], again["grad_weight"])
 
 
+@pytest.mark.parametrize("N,H,V,kind", [(16384, 16, 300, "zipf"), (16385, 16, 300, "zipf"), (131072, 8, 70000, "zipf"),
+                                        (140001, 8, 5000, "zipf"), (300001, 8, 90, "uniform"), (300001, 8, 3, "one")])
+def test_gradient_of_many_tokens(env, N, H, V, kind):  # noqa: F811
+    """Every form of the sort, chunks of more than 64 tokens, and runs of thousands of chunks."""
+    flce, torch, dev = env
+    ids = draw_ids(N, V, kind, seed=N)
+    d = torch.randn(N, H, generator=torch.Generator().manual_seed(V))
+    o = flce.embedding_bwd(d.to(dev), torch.from_numpy(ids).to(dev), V, 1.5)
+    assert flce.query_status(o["workspace"]) == flce.FLCE_OK
+    ref, mag = np.zeros((V, H)), np.zeros((V, H))
+    np.add.at(ref, ids, 1.5 * d.double().numpy())
+    np.add.at(mag, ids, 1.5 * d.abs().double().numpy())
+    c = np.bincount(ids, minlength=V)[:, None]
+    assert np.all(np.abs(np64(o["grad_weight"]) - ref) <= (c + 2) * 2.0 ** -24 * mag)
+
+
 @pytest.mark.parametrize("N,H,V,kind", [(1, 64, 9, "one"), (5000, 264, 700, "zipf"), (300, 64, 20000, "uniform")])
 def test_accumulate(env, N, H, V, kind):  # noqa: F811
     flce, torch, dev = env
@@ -155,6 +171,42 @@ def test_python_refusals_on_gpu(env):  # noqa: F811
     for f in bad:
         with pytest.raises((ValueError, TypeError, flce.FlceError)):
             f()
+
+
+def test_captured_training_step(env):  # noqa: F811
+    """Embedding, head and both gradients of a tied weight captured as one graph and replayed on new tokens."""
+    flce, torch, dev = env
+    N, H, V = 300, 64, 700
+    _, W, t = problem(N, H, V, seed=3, ignored=0.1)
+    w = torch.from_numpy(W).to(torch.bfloat16).to(dev)
+    adv = torch.randn(N, device=dev)
+    batches = [(torch.from_numpy(draw_ids(N, V, "zipf", s)).to(dev), torch.from_numpy(np.roll(t, s)).to(dev))
+               for s in range(2)]
+
+    def step(ids, targets):
+        leaf = w.detach().requires_grad_(True)
+        x = flce.embedding(ids, leaf, 8.0)
+        logp, ent = flce.linear_logprobs(x, leaf, targets)
+        loss = (logp * adv).sum() + 0.01 * ent.sum()
+        return loss.detach(), torch.autograd.grad(loss, leaf)[0]
+
+    want = [step(*b) for b in batches]
+    ids, targets = (x.clone() for x in batches[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(ids, targets)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(ids, targets)
+    for b, a in ((batches[1], want[1]), (batches[0], want[0])):
+        ids.copy_(b[0])
+        targets.copy_(b[1])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], a[0]) and torch.equal(out[1], a[1])
 
 
 def test_tied_model(env):  # noqa: F811

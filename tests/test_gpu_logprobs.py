@@ -281,6 +281,31 @@ def test_gradients_in_chunks(env, bf16):
     assert not none["grad_hidden"].any() and not none["grad_weight"].any()
 
 
+@pytest.mark.parametrize("N", [5, 200])
+def test_ignore_index_inside_the_vocabulary(env, N):
+    """Any int32 may be the ignore index, an id too."""
+    flce, torch, dev = env
+    X, W, t = problem(N, 64, 40, seed=3)
+    h, w, tt = to_gpu(torch, dev, X, W, t)
+    o = flce.token_logprobs(h, w, tt, ignore_index=int(t[0]), top_k=2)
+    assert flce.query_status(o["workspace"]) == flce.FLCE_OK
+    check_forward(o, logprobs_oracle(X, W, t, ignore_index=int(t[0]), top_k=2), 1.0, 2)
+    d = flce.token_logprobs_bwd(h, w, tt, o["lse"], None, torch.ones(N, device=dev), ignore_index=int(t[0]))
+    assert not d["grad_hidden"][tt == int(t[0])].any() and d["grad_hidden"].any()
+
+
+def test_no_entropy_and_given_outputs(env):
+    flce, torch, dev = env
+    for N in (6, 260):
+        X, W, t = problem(N, 64, 900, seed=3, ignored=0.2)
+        h, w, tt = to_gpu(torch, dev, X, W, t)
+        a = flce.token_logprobs(h, w, tt, entropy=False)
+        b = flce.token_logprobs(h, w, tt)
+        assert a["entropy"] is None and torch.equal(a["logp"], b["logp"]) and torch.equal(a["lse"], b["lse"])
+        again = flce.token_logprobs(h, w, tt, out=b, workspace=b["workspace"])
+        assert again is b and torch.equal(a["logp"], b["logp"])
+
+
 def test_autograd_step(env):
     """A clipped policy-gradient loss through the module, against autograd in fp64."""
     flce, torch, dev = env
