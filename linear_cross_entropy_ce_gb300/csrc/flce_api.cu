@@ -92,7 +92,7 @@ struct Plan {
   long long N = 0, H = 0, V = 0, C = 0, ldz = 0, n_chunks = 0;
   int nvt = 0, nparts = 0, splits = 1, kb_per_split = 0;
   long long n_counters = 0, flags_per_chunk = 0;
-  bool fwd_only = false, norm = false, gw32 = false, probs = false;
+  bool fwd_only = false, norm = false, gw32 = false, probs = false, slabs = false;
   size_t o_idx = 0, o_rl = 0, o_cnt = 0, o_xc = 0, o_tc = 0, o_zt = 0, o_part = 0, o_z = 0, o_dx = 0, o_rinv = 0,
          o_dg = 0, o_gw = 0, o_rowc = 0, total = 0;
 };
@@ -106,7 +106,7 @@ constexpr int DX_UNIT_KB = 128;  // preferred K blocks of one dX unit
 // (gw32) the fp32 V x H accumulator of grad_weight lives here as well.
 // probs: the backward of the token log probabilities (per-row constants).
 Plan layout(long long N, long long H, long long V, long long C, int S, bool fwd_only, bool norm = false,
-            bool gw32 = false, bool probs = false) {
+            bool gw32 = false, bool probs = false, bool slabs = false) {
   Plan p;
   p.N = N; p.H = H; p.V = V; p.C = C; p.fwd_only = fwd_only; p.norm = norm; p.gw32 = gw32 && !fwd_only;
   p.ldz = cdiv(V, 64) * 64;
@@ -119,7 +119,8 @@ Plan layout(long long N, long long H, long long V, long long C, int S, bool fwd_
   if (fwd_only) S = 1;
   p.kb_per_split = static_cast<int>(cdiv(kbt, S));
   p.splits = static_cast<int>(cdiv(kbt, p.kb_per_split));
-  p.flags_per_chunk = p.splits > 1 ? 4 * cdiv(C, PAIR_M) * cdiv(H, BN) : 0;   // (tile, CTA, warpgroup)
+  p.slabs = slabs && p.splits > 1;
+  p.flags_per_chunk = p.splits > 1 && !p.slabs ? 4 * cdiv(C, PAIR_M) * cdiv(H, BN) : 0;   // (tile, CTA, warpgroup)
   p.n_counters = p.n_chunks * (2 + p.flags_per_chunk);   // tile counters, then split flags
   size_t off = al256(HDR_WORDS * sizeof(int));
   p.o_idx = off;  off += al256(size_t(N) * 4);
@@ -134,10 +135,10 @@ Plan layout(long long N, long long H, long long V, long long C, int S, bool fwd_
   // inside that launch (the next chunk's logits rewrite the parts after it):
   // the two share their bytes.
   p.o_part = off;
-  size_t shared = al256(size_t(C) * p.nparts * 8);
+  size_t shared = probs ? 0 : al256(size_t(C) * p.nparts * 8);   // MODE_DZ keeps no parts
   if (!fwd_only && p.splits > 1) {
     p.o_dx = off;
-    shared = std::max(shared, al256(size_t(C) * H * 4));
+    shared = std::max(shared, al256(size_t(C) * H * 4 * (p.slabs ? p.splits : 1)));
   }
   off += shared;
   if (norm) {   // final RMSNorm: 1/rms per chunk row, d(gain) partial per chunk
@@ -161,7 +162,7 @@ Plan layout(long long N, long long H, long long V, long long C, int S, bool fwd_
 // units (~DX_UNIT_KB K blocks) keep the spread even and the launch's tail
 // short.  Not spread: S balances the unit length (kbt / S K blocks of
 // ~0.3 µs) against the chain (S steps of ~4 µs), S ~ sqrt(kbt / 13).
-int preferred_splits(long long C, long long H, long long V, int pairs) {
+int preferred_splits(long long C, long long H, long long V, int pairs, bool* spread_out = nullptr) {
   const long long kbt = cdiv(V, BK);
   const double dx_tiles = double(cdiv(C, PAIR_M)) * double(cdiv(H, BN));
   const double unit = double(PAIR_M) * BN * double(V);
@@ -175,16 +176,43 @@ int preferred_splits(long long C, long long H, long long V, int pairs) {
   const long long n_dw = cdiv(V, PAIR_M) * cdiv(H, BN);
   const long long kb_dw = cdiv(C, BK);
   const long long spread = clamp(std::max<long long>(balance, cdiv(kbt, DX_UNIT_KB)));
-  if (n_dw > static_cast<long long>(pairs) * cdiv(cdiv(kbt, spread), kb_dw)) return static_cast<int>(spread);
+  const bool spreads = n_dw > static_cast<long long>(pairs) * cdiv(cdiv(kbt, spread), kb_dw);
+  if (spread_out) *spread_out = spreads;
+  if (spreads) return static_cast<int>(spread);
   const long long chain = std::llround(std::sqrt(double(kbt) / 13.0));
   return static_cast<int>(clamp(std::min<long long>(balance, chain)));
+}
+
+// The same for the backward of the token log probabilities, whose workspace is
+// not held to 5%: where the units cannot be spread, each split stores a part
+// of its own (a slab) and a kernel adds them up, so no chain limits S.  Units
+// of half a pair's share; a unit of up to 1.25 shares is not split, and the
+// slabs stay within what L2 holds.  (300 tokens at 512 x 16000: 4 chained
+// splits 72 us, 16 slabs 40 us of backward.)
+constexpr int MAX_SLABS = 32;
+constexpr double SLAB_BYTES = 96e6;
+int probs_splits(long long C, long long H, long long V, int pairs, bool* slabs) {
+  bool spread = false;
+  const int S = preferred_splits(C, H, V, pairs, &spread);
+  *slabs = !spread;
+  if (spread) return S;
+  const double kbt = double(cdiv(V, BK));
+  const double work = double(cdiv(C, PAIR_M)) * double(cdiv(H, BN)) * kbt +
+                      double(cdiv(V, PAIR_M)) * double(cdiv(H, BN)) * double(cdiv(C, BK));
+  const double share = work / double(pairs);
+  if (kbt <= 1.25 * share) return 1;
+  double n = std::ceil(kbt / std::max(8.0, 0.5 * share));
+  n = std::min(std::min(n, double(MAX_SLABS)), std::floor(SLAB_BYTES / (double(C) * double(H) * 4.0)));
+  return n < 2.0 ? 1 : static_cast<int>(n);
 }
 
 long long max_chunk(long long N) { return cdiv(N, BM) * BM; }
 
 Plan plan_for_chunk(long long N, long long H, long long V, long long C, bool fwd_only, int pairs, size_t bytes,
                     bool norm = false, bool gw32 = false, bool probs = false) {
-  Plan p = layout(N, H, V, C, preferred_splits(C, H, V, pairs), fwd_only, norm, gw32, probs);
+  bool slabs = false;
+  const int S = probs ? probs_splits(C, H, V, pairs, &slabs) : preferred_splits(C, H, V, pairs);
+  Plan p = layout(N, H, V, C, S, fwd_only, norm, gw32, probs, slabs);
   if (p.total > bytes) p = layout(N, H, V, C, 1, fwd_only, norm, gw32, probs);
   return p;
 }
@@ -500,6 +528,7 @@ flce_status run(const Job& j) {
   g.pf_threads = p.C <= 512 ? 1 : 0;
   g.dxacc = dxacc;
   g.skip = skip;
+  g.slabs = p.slabs ? 1 : 0;
   g.gw_bf16 = direct ? 1 : 0;
   DzRow* rowc = probs ? at<DzRow>(ws, p.o_rowc) : nullptr;
   g.rowc = rowc;
@@ -517,7 +546,8 @@ flce_status run(const Job& j) {
   const int v0 = static_cast<int>(j.v0);
   const bool front = probs && p.n_chunks == 1 && N <= FRONT_MAX_TOKENS;
   if (probs)   // front, or prep, zeroed rows and one gather per chunk; failure mark, rounding
-    count_launches((front ? 1 : 1 + (j.grad_hidden ? 1 : 0) + p.n_chunks) + 1 + (p.gw32 ? 1 : 0));
+    count_launches((front ? 1 : 1 + (j.grad_hidden ? 1 : 0) + p.n_chunks) + 1 + (p.gw32 ? 1 : 0) +
+                   (p.slabs && j.grad_hidden ? p.n_chunks : 0));
   else
     count_launches(1 + (fwd_only ? 0 : 1) + (j.kind == JOB_SHARD_BWD ? 0 : 1) + p.n_chunks * (norm ? 4 : 2) +
                    (norm ? 1 : 0) + (p.gw32 ? 1 : 0));
@@ -576,6 +606,9 @@ flce_status run(const Job& j) {
     g.accumulate = c > 0 ? 1 : 0;
     g.first_chunk = c == 0 ? 1 : 0;
     if (!chk(gemm_launch(g, bm, grid_bwd, st, probs))) return FLCE_ECUDA;
+    if (p.slabs && j.grad_hidden &&
+        !chk(launch_dx_reduce(hdr, idx, c0, g.C, g.H, p.splits, dxacc, static_cast<uint16_t*>(j.grad_hidden), st)))
+      return FLCE_ECUDA;
     if (norm && !chk(launch_rmsnorm_bwd(hdr, idx, c0, g.C, g.H, static_cast<const uint16_t*>(j.hidden),
                                         static_cast<const uint16_t*>(j.gain), rinv,
                                         static_cast<uint16_t*>(j.grad_hidden), dgp + c * H, st)))

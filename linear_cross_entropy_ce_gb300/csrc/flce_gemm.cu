@@ -684,17 +684,20 @@ __device__ __forceinline__ void warp_block_to_global(float* dst, int nrows, int 
 // dX unit of a split vocabulary: split 0 stores its fp32 part, split k waits
 // until split k-1 has landed and reduce-adds onto it, the last split turns
 // the finished fp32 rows into bf16 grad_hidden rows.  Each warpgroup orders
-// its own column half.  Returns false on abort.
+// its own column half.  With slabs every split just stores a part of its own.
+// Returns false on abort.
 __device__ __forceinline__ bool epi_dx_split(const GemmArgs& a, const Shape& s, const Unit& t, int row0, int col0,
                                              int half_idx, uint32_t rank, uint32_t tbase, int r, int q, int lane,
                                              bool leader, uint32_t bar, uint8_t* wbuf, Ctl* ctl) {
   int* flag = a.flags + 4 * t.ntile + 2 * static_cast<int>(rank) + half_idx;
+  const bool chain = a.slabs == 0;
   bool ok = true;
-  if (leader && t.split > 0) ok = wait_flag(flag, t.split, ctl, a.timeout_ns, const_cast<int*>(a.hdr));
+  if (chain && leader && t.split > 0) ok = wait_flag(flag, t.split, ctl, a.timeout_ns, const_cast<int*>(a.hdr));
   if (!ptx::named_bar_and(bar, GROUP_THREADS, ok)) return false;
   const int h0 = t.n0 + col0;
-  float* acc = const_cast<float*>(a.dxacc);
-  warp_block_to_global(acc, a.C, a.H, h0, row0 + q * 32, t.split > 0, tbase, lane, wbuf);
+  float* acc = const_cast<float*>(a.dxacc) + (chain ? 0 : static_cast<size_t>(t.split) * a.C * a.H);
+  warp_block_to_global(acc, a.C, a.H, h0, row0 + q * 32, chain && t.split > 0, tbase, lane, wbuf);
+  if (!chain) return true;
   __threadfence();                          // this part is in global memory before the flag moves on
   ptx::named_bar_sync(bar, GROUP_THREADS);
   if (leader) ptx::st_release_gpu(flag, t.split + 1);

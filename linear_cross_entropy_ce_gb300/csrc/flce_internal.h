@@ -87,6 +87,8 @@ struct GemmArgs {
   const float* dxacc;   // [C][H] fp32 sum of the grad_hidden splits (splits > 1)
   // MODE_STATS, MODE_DZ
   int skip;             // BWD: SKIP_DX, SKIP_DW
+  int slabs;            // BWD, splits > 1: each split stores its fp32 part to dxacc + split C H
+                        // (dx_reduce adds them) instead of adding onto the previous one
   int gw_bf16;          // BWD of a call with one chunk: grad_weight tiles are rounded and stored as bf16
   float c2;             // log2(e) / temperature: z c2 is the scaled logit in base-2 units
   float* stats;         // STATS: [3][nparts][C] part max (raw z), sum of 2^d, sum of d 2^d, d = (z - max) c2
@@ -244,6 +246,8 @@ cudaError_t launch_gather_dz(const uint16_t* hidden, const int* targets, const i
                              long long c0, int C, int H, float temperature, const float* lse, const float* entropy,
                              const float* grad_logp, const float* grad_entropy, uint16_t* xc, int* tc, DzRow* rowc,
                              cudaStream_t s);
+cudaError_t launch_dx_reduce(const int* hdr, const int* idx, long long c0, int C, int H, int splits, const float* parts,
+                             uint16_t* grad_hidden, cudaStream_t s);
 cudaError_t launch_mark_failed(const int* hdr, uint16_t* grad_hidden, float* grad_weight, int gw_bf16,
                                cudaStream_t s);
 bool bad_temperature(float t);

@@ -326,6 +326,45 @@ __global__ void __launch_bounds__(32 * TOP_WARPS)
   }
 }
 
+// grad_hidden rows of a chunk from the fp32 parts of its vocabulary splits,
+// added in order and rounded once.
+constexpr int DXR_THREADS = 256;
+constexpr int DXR_BATCH = 4;   // parts in flight
+__global__ void __launch_bounds__(DXR_THREADS)
+    dx_reduce_kernel(const int* hdr, const int* idx, long long c0, int C, int H, int splits, const float* parts,
+                     uint16_t* grad_hidden) {
+  ptx::grid_dependency_wait();
+  const int Cl = chunk_rows(hdr, c0, C);
+  const int n8 = H / 8;
+  const long long total = static_cast<long long>(Cl) * n8, slab = static_cast<long long>(C) * H;
+  for (long long i = static_cast<long long>(blockIdx.x) * DXR_THREADS + threadIdx.x; i < total;
+       i += static_cast<long long>(gridDim.x) * DXR_THREADS) {
+    const int r = static_cast<int>(i / n8), c = static_cast<int>(i - static_cast<long long>(r) * n8);
+    const float* p = parts + static_cast<long long>(r) * H + c * 8;
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int k0 = 0; k0 < splits; k0 += DXR_BATCH) {
+      float4 x[DXR_BATCH][2];
+#pragma unroll
+      for (int k = 0; k < DXR_BATCH; ++k)
+        if (k0 + k < splits) {
+          const float4* q = reinterpret_cast<const float4*>(p + (k0 + k) * slab);
+          x[k][0] = q[0];
+          x[k][1] = q[1];
+        }
+#pragma unroll
+      for (int k = 0; k < DXR_BATCH; ++k)
+        if (k0 + k < splits) {
+          s[0] += x[k][0].x; s[1] += x[k][0].y; s[2] += x[k][0].z; s[3] += x[k][0].w;
+          s[4] += x[k][1].x; s[5] += x[k][1].y; s[6] += x[k][1].z; s[7] += x[k][1].w;
+        }
+    }
+    const long long tok = idx[c0 + r];
+    reinterpret_cast<uint4*>(grad_hidden + tok * H)[c] =
+        make_uint4(ptx::pack_bf16x2(s[0], s[1]), ptx::pack_bf16x2(s[2], s[3]), ptx::pack_bf16x2(s[4], s[5]),
+                   ptx::pack_bf16x2(s[6], s[7]));
+  }
+}
+
 // The gradients of a call whose pipeline timed out begin with a NaN, so that a
 // caller who never reads the status still sees that they are not to be trusted.
 __global__ void mark_failed_kernel(const int* hdr, uint16_t* grad_hidden, float* grad_weight, int gw_bf16) {
@@ -438,6 +477,12 @@ StreamPlan stream_plan(long long N, long long V, int K, int sms) {
 }  // namespace
 
 bool bad_temperature(float t) { return !(t > 0.f) || !std::isfinite(t) || !std::isfinite(LOG2E / t); }
+
+cudaError_t launch_dx_reduce(const int* hdr, const int* idx, long long c0, int C, int H, int splits, const float* parts,
+                             uint16_t* grad_hidden, cudaStream_t s) {
+  const unsigned blocks = static_cast<unsigned>(std::min<long long>(cdiv(static_cast<long long>(C) * (H / 8), DXR_THREADS), 152 * 8));
+  return launch_dependent(dx_reduce_kernel, blocks, DXR_THREADS, s, hdr, idx, c0, C, H, splits, parts, grad_hidden);
+}
 
 cudaError_t launch_mark_failed(const int* hdr, uint16_t* grad_hidden, float* grad_weight, int gw_bf16,
                                cudaStream_t s) {

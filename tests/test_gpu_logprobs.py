@@ -276,7 +276,10 @@ def test_gradients_in_chunks(env, bf16):
         tol = ref["mag_" + k] * (2.0 ** -8 + 2e-4) * (1 + 2.0 ** -8) + rounds * 2.0 ** -8 * np.abs(ref["grad_" + k])
         assert np.all(np.abs(np64(d["grad_" + k]) - ref["grad_" + k]) <= tol + 1e-30), k
     whole = flce.token_logprobs_bwd(h, w, tt, o["lse"], None, tg, grad_weight_dtype=dt)
-    assert torch.equal(whole["grad_hidden"], d["grad_hidden"])   # complete per chunk
+    # complete per chunk, but the chunk size decides how the sum over the vocabulary is split: two fp32 sums of V terms
+    # in other orders differ by at most 2 V 2^-24 of the sum of magnitudes, and each is rounded to bf16 (2^-8 of it)
+    a, b = np64(whole["grad_hidden"]), np64(d["grad_hidden"])
+    assert np.all(np.abs(a - b) <= 2 * V * 2.0 ** -24 * ref["mag_hidden"] * 1.01 + 2.0 ** -8 * (np.abs(a) + np.abs(b)))
     none = flce.token_logprobs_bwd(h, w, torch.full_like(tt, -100), o["lse"], None, tg, grad_weight_dtype=dt)
     assert not none["grad_hidden"].any() and not none["grad_weight"].any()
 
