@@ -300,8 +300,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const float4 old = stat[tk];
             const Stat t = merge(Stat{old.x, old.y, old.z}, Stat{mx, back * s, back * fmaf(-rho, s, d)}, a.c2);
             stat[tk] = make_float4(t.m, t.s, t.d, 0.f);
-            const int at = a.targets[tk] - r0;
-            if (at >= 0 && at < rows) a.zt[tk] = z[at];
+            const unsigned at = static_cast<unsigned>(a.targets[tk]) - static_cast<unsigned>(r0);
+            if (at < static_cast<unsigned>(rows)) a.zt[tk] = z[at];
           }
           if (a.K > 0) {
             if (order_key(mx) >= bound[tk]) {

@@ -632,10 +632,15 @@ def embedding_fwd(weight: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, *
     V, H = _check_rows(weight, "weight")
     N = _check_ids(ids)
     dev = _check_same_device(weight, ids)
+    if out is not None:
+        _check_buffer(out, "out", (N, H), weight.dtype, dev)
     with _on(dev, stream) as st:
-        out = _outputs({"out": out}, {"out": ((N, H), weight.dtype)}, dev)["out"]
-        _ok(library().flce_embedding(_addr(weight), _addr(ids), N, H, V, EMBEDDING_DTYPES[weight.dtype], float(scale),
-                                     _addr(out), st), "flce_embedding")
+        if out is None:
+            out = torch.empty((N, H), dtype=weight.dtype, device=dev)
+        s = library().flce_embedding(weight.data_ptr(), ids.data_ptr(), N, H, V, EMBEDDING_DTYPES[weight.dtype],
+                                     float(scale), out.data_ptr(), st)
+    if s != FLCE_OK:
+        raise FlceError(s, "flce_embedding")
     return out
 
 
