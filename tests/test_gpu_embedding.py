@@ -117,6 +117,21 @@ def test_accumulate(env, N, H, V, kind):  # noqa: F811
     assert torch.equal(g[rest].nan_to_num(7), base[rest].nan_to_num(7))
 
 
+def test_offsets_past_32_bits(env):  # noqa: F811
+    """A table of 2.3e9 elements, its last rows looked up; a gradient of 9 GB, zero elsewhere."""
+    flce, torch, dev = env
+    V, H, N = 1_100_007, 2056, 300
+    W = torch.zeros(V, H, dtype=torch.bfloat16, device=dev)
+    W[V - 50:] = torch.randn(50, H, device=dev).to(torch.bfloat16)
+    ids = V - 1 - (torch.arange(N, device=dev, dtype=torch.int32) * 7) % 50
+    out = flce.embedding_fwd(W, ids, 2.0)
+    assert torch.equal(out, 2 * W[ids.long()])
+    g = flce.embedding_bwd(out, ids, V)["grad_weight"]
+    ref, mag = embedding_grad_oracle(np64(out), (ids - (V - 50)).cpu().numpy(), 50)
+    assert np.all(np.abs(np64(g[V - 50:]) - ref) <= 8 * 2.0 ** -24 * mag)
+    assert not g[:V - 50].any()
+
+
 def test_gradient_bad_ids(env):  # noqa: F811
     flce, torch, dev = env
     d = torch.randn(6, 64, device=dev)

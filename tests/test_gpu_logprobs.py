@@ -83,7 +83,8 @@ SHAPES = [  # N, H, V, K, ignored, T
     (33, 64, 31, 31, 0.0, 1.0), (61, 136, 16007, 7, 0.1, 0.5), (64, 1024, 4096, 0, 0.5, 1.0),
     (100, 264, 3001, 3, 0.05, 2.0), (127, 128, 2000, 16, 0.3, 1.0), (128, 128, 128, 32, 0.0, 1.0),
     (129, 64, 512, 9, 0.9, 1.0), (257, 192, 1030, 4, 0.1, 1.0), (300, 64, 512, 0, 0.1, 0.9),
-    (700, 520, 4099, 12, 0.3, 1.0), (1000, 256, 16000, 0, 0.05, 1.0)]
+    (700, 520, 4099, 12, 0.3, 1.0), (1000, 256, 16000, 0, 0.05, 1.0), (200, 8, 1, 1, 0.0, 1.0),
+    (200, 8, 300, 32, 0.2, 1.0), (1, 8, 100003, 32, 0.0, 1.0)]
 
 
 @pytest.mark.parametrize("N,H,V,K,ignored,T", SHAPES)
@@ -95,7 +96,8 @@ def test_forward_grid(env, N, H, V, K, ignored, T):
     check_forward(o, logprobs_oracle(X, W, t, temperature=T, top_k=K), T, K)
 
 
-@pytest.mark.parametrize("N,H,V", [(1, 4096, 3000), (40, 1024, 5000), (300, 2048, 1111)])
+@pytest.mark.parametrize("N,H,V", [(1, 4096, 3000), (40, 1024, 5000), (300, 2048, 1111), (3, 16384, 100),
+                                   (130, 16384, 300)])
 def test_forward_continuous(env, N, H, V):
     flce, torch, dev = env
     X, W, t = problem(N, H, V, seed=5, grid=False)
@@ -227,7 +229,9 @@ def test_small_workspace_and_outputs_left_alone(env, N):
 GRADS = [  # N, H, V, ignored, T, logp, entropy, bf16
     (1, 64, 512, 0.0, 1.0, True, True, False), (3, 72, 130, 0.3, 0.7, True, False, True),
     (128, 64, 512, 0.0, 1.0, False, True, False), (300, 64, 512, 0.1, 1.0, True, True, True),
-    (513, 136, 1000, 0.5, 1.3, True, True, False), (640, 520, 2049, 0.05, 1.0, True, True, True)]
+    (513, 136, 1000, 0.5, 1.3, True, True, False), (640, 520, 2049, 0.05, 1.0, True, True, True),
+    (200, 8, 1, 0.0, 1.0, True, True, True), (140, 8, 77, 0.1, 1.0, True, True, False),
+    (300, 256, 9000, 0.2, 1.0, True, True, True)]
 
 
 @pytest.mark.parametrize("N,H,V,ignored,T,gl,ge,bf16", GRADS)
@@ -394,6 +398,41 @@ def test_captured_repeated_and_on_another_stream(env, N, K):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(out, a))
+
+
+@pytest.mark.parametrize("N", [3, 130])
+def test_offsets_past_32_bits(env, N):
+    """A weight of 2.3e9 elements (its gradient 9 GB), zero but for the last rows: logits in closed form."""
+    flce, torch, dev = env
+    V, H, m, K = 1_100_007, 2056, 40, 5
+    X, tail, _ = problem(N, H, m, seed=N)
+    w = torch.zeros(V, H, dtype=torch.bfloat16, device=dev)
+    w[V - m:] = torch.from_numpy(tail).to(torch.bfloat16).to(dev)
+    t = (V - 1 - np.arange(N) % (m + 5)).astype(np.int32)
+    h = torch.from_numpy(X).to(torch.bfloat16).to(dev)
+    o = flce.token_logprobs(h, w, torch.from_numpy(t).to(dev), top_k=K)
+    z = X @ tail.T
+    mx = np.maximum(z.max(1), 0)
+    lse = mx + np.log((V - m) * np.exp(-mx) + np.exp(z - mx[:, None]).sum(1))
+    at = t - (V - m)
+    zt = np.where(at >= 0, z[np.arange(N), np.maximum(at, 0)], 0)
+    # the sum of 8594 parts of equal terms is off by at most (128 + 8594) 2^-24 = 5.2e-4 of itself
+    assert np.all(np.abs(np64(o["lse"]) - lse) <= 6e-4) and np.all(np.abs(np64(o["logp"]) - (zt - lse)) <= 6e-4)
+    order = np.argsort(-z, axis=1, kind="stable")[:, :K]
+    assert (np.take_along_axis(z, order, 1) > 0).all()
+    np.testing.assert_array_equal(o["top_ids"].cpu().numpy(), order + V - m)
+    g = np.random.default_rng(0).standard_normal(N).astype(np.float32)
+    d = flce.token_logprobs_bwd(h, w, torch.from_numpy(t).to(dev), o["lse"], None, torch.from_numpy(g).to(dev))
+    rows = np.r_[0, 1, V // 2, V - m - 1, V - m:V]
+    zr = np.concatenate([np.zeros((N, 4)), z], 1)
+    p = np.exp(zr - lse[:, None])
+    hit = rows[None] == t[:, None]
+    ref, mag = (g[:, None] * (hit - p)).T @ X, (np.abs(g)[:, None] * (hit + p)).T @ np.abs(X)
+    got = np64(d["grad_weight"][torch.from_numpy(rows).to(dev)])
+    assert np.all(np.abs(got - ref) <= mag * (2.0 ** -8 + 1e-3))
+    ref_h = g[:, None] * (np.where(at >= 0, 1, 0)[:, None] * tail[np.maximum(at, 0)] - p[:, 4:] @ tail)
+    mag_h = np.abs(g)[:, None] * (np.abs(tail[np.maximum(at, 0)]) + p[:, 4:] @ np.abs(tail))
+    assert np.all(np.abs(np64(d["grad_hidden"]) - ref_h) <= mag_h * (2.0 ** -7 + 1e-3))
 
 
 def test_python_refusals_on_gpu(env):
