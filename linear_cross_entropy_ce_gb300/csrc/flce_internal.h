@@ -200,7 +200,7 @@ struct StreamArgs {
   float* zf;               // K > 0: [N][ldz] logits, and
   long long ldz;
   float* tile_max;         // [N][ctas][max_tiles]
-  uint32_t* group_max;     // [N][32] largest tile max (as an ordered integer) of each of K groups of tiles
+  uint32_t* group_max;     // [N][32] largest tile max (as an ordered integer) of each of K groups of tiles, or null
   int max_tiles;           // tiles of a CTA at most
   int* fail;               // [ctas]
   float* logp;

@@ -553,7 +553,9 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
     a.ldz = p.ldz;
     a.tile_max = at<float>(workspace, p.o_max);
     a.max_tiles = p.max_tiles;
-    a.group_max = at<uint32_t>(workspace, p.o_group);
+    // With one tile a CTA, all of them finish at once and no bound is known in
+    // time: every logit is kept, and nothing needs clearing.
+    a.group_max = top_k > 0 && p.max_tiles > 1 ? at<uint32_t>(workspace, p.o_group) : nullptr;
     a.fail = at<int>(workspace, p.o_fail);
     a.logp = logp; a.entropy = entropy; a.lse = lse; a.top_ids = top_ids; a.top_logp = top_logp;
     StreamMaps m;
@@ -564,7 +566,7 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
     const ProfScope prof = prof_launch_begin(st);
     const cudaError_t e = launch_stream(a, m, st);
     prof_launch_end(prof, MODE_STATS, st);
-    count_launches(top_k > 0 ? 2 : 1);   // the merge, the clearing
+    count_launches(a.group_max ? 2 : 1);   // the merge, the clearing
     return e == cudaSuccess ? FLCE_OK : FLCE_ECUDA;
   }
   LpPlan p;

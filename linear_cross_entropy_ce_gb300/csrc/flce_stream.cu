@@ -226,10 +226,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int tk = w; tk < a.N; tk += EPI_WARPS)
       if (lane == 0) stat[tk] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
     __syncwarp();
-    if (a.K > 0) ptx::grid_dependency_wait();   // the groups' maxima have been cleared
+    if (a.group_max) ptx::grid_dependency_wait();   // the groups' maxima have been cleared
     uint32_t acc = 0, acc_phase = 0;
     for (int i = 0; i < range.tiles; ++i) {
-      if (a.K > 0) {   // the bounds of this warp's tokens
+      if (a.group_max) {   // the bounds of this warp's tokens
         for (int t0 = w; t0 < a.N; t0 += 4 * EPI_WARPS) {
           uint32_t g[4];
 #pragma unroll
@@ -304,12 +304,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (at < static_cast<unsigned>(rows)) a.zt[tk] = z[at];
           }
           if (a.K > 0) {
-            if (order_key(mx) >= bound[tk]) {
+            if (!a.group_max || order_key(mx) >= bound[tk]) {
               float* zf = a.zf + static_cast<size_t>(tk) * a.ldz + r0 + lane;
 #pragma unroll
               for (int j = 0; j < 8; ++j)
                 if (j * 32 + lane < rows) zf[j * 32] = x[j];
-              if (lane == 0) atomicMax(a.group_max + tk * TopK::MAX + (blockIdx.x + i) % a.K, order_key(mx));
+              if (a.group_max && lane == 0) atomicMax(a.group_max + tk * TopK::MAX + (blockIdx.x + i) % a.K, order_key(mx));
             }
             if (lane == 0)
               a.tile_max[static_cast<size_t>(tk) * a.ctas * a.max_tiles + blockIdx.x * a.max_tiles + i] = mx;
@@ -468,7 +468,7 @@ cudaError_t prepare() {
 
 template <int NT>
 cudaError_t launch(const StreamArgs& a, const StreamMaps& m, cudaStream_t s) {
-  if (a.K == 0) {
+  if (!a.group_max) {
     logprob_stream_kernel<NT><<<a.ctas, THREADS, Cfg<NT>::SMEM, s>>>(m, a);
     return cudaGetLastError();
   }
