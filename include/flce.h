@@ -245,7 +245,7 @@ flce_status flce_vocab_shard_bwd(const void* hidden, const void* weight_shard,
  * pipeline time-out (FLCE_ETIMEOUT) every scored row is NaN.
  * The N x V logits are not kept: the workspace (flce_logprobs_workspace_bytes;
  * less runs in smaller chunks, down to 128 rows) stays below 5% of their bf16
- * size, or 64 MiB (2 GiB with top alternatives) where that is more.
+ * size, or 512 MiB (2 GiB with top alternatives) where that is more.
  * 0 < temperature < inf.  V <= 2^31 - 512; other sizes, alignment, streams and errors as flce_fwd_bwd;
  * top_k > V is FLCE_EINVAL, top_k > 32 FLCE_EUNSUPPORTED.
  */

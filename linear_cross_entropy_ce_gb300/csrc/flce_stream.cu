@@ -22,7 +22,8 @@
 // alternatives at 2048 x 256000 184 us, with none stored 164; a sorted list per
 // CTA and token: 175, with 32 alternatives 212.)
 //
-// Bound by the weight's bytes: 2 H V at the HBM rate.  Every wait is bounded:
+// Bound by the weight's bytes: 2 H V at the HBM rate (4096 x 128256: 158 us for
+// 1 token, 6.66 TB/s; 164 for 64, 172 for 128).  Every wait is bounded:
 // on time-out the CTA lets its copies in flight land, waits for its MMAs, frees
 // TMEM and returns, and the call's rows become NaN (status FLCE_ETIMEOUT).
 #include "flce_internal.h"

@@ -59,7 +59,8 @@ def test_backward_refusals(flce, kw, want):
 def test_workspace_sizes(flce):
     lib = flce.library()
     N, H, V = 16384, 4096, 128256
-    assert 0 < lib.flce_logprobs_workspace_bytes(N, H, V, 0) <= 0.05 * N * V * 2
+    assert 0 < lib.flce_logprobs_workspace_bytes(N, H, V, 0) <= 512 << 20
+    assert 0 < lib.flce_logprobs_workspace_bytes(8 * N, H, V, 0) <= 0.05 * 8 * N * V * 2
     assert 0 < lib.flce_logprobs_workspace_bytes(64, H, V, 8) <= 256 << 20
     assert 0 < lib.flce_logprobs_workspace_bytes(N, H, V, 8) <= 2 << 30
     assert 0 < lib.flce_logprobs_bwd_workspace_bytes(N, H, V, 0) <= 2 << 30
