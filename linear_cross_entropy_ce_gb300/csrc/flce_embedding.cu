@@ -407,10 +407,12 @@ __global__ void __cluster_dims__(CS_BLOCKS, 1, 1) __launch_bounds__(CS_THREADS)
 // sums over runs of equal ids
 // ---------------------------------------------------------------------------
 constexpr int SEG_WARPS = 8;
-constexpr int MIN_CHUNK = 64;          // sorted entries per chunk (32 to 128 tried), and
+constexpr int CHUNK = 64;              // sorted entries per chunk (32 to 128 tried), fewer where that leaves
+constexpr int MIN_CHUNK = 8;           // less than eight warps an SM, and
 constexpr int MAX_CHUNKS = 4096;       // at most this many chunks (two partial sums of H floats each)
 constexpr int ZERO_ROWS = 32;          // grad_weight rows a warp looks up at once
 constexpr int ZERO_MAX_ROWS = 8192;    // rows a block marks at most (1 KB of bits)
+constexpr long long ZERO_BYTES = 768 << 10;
 
 struct SegArgs {
   const int2* items;     // (id, token) sorted by id, [N]
@@ -459,33 +461,38 @@ __device__ __forceinline__ void segments(const SegArgs& a, long long warp, int l
   const int after = i1 < a.N ? a.items[i1].x : a.V;
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   const unsigned nv = static_cast<unsigned>(a.V), nn = static_cast<unsigned>(a.N);
-  int cur = a.items[i0].x;
+  auto group = [&](int g0) { return g0 + lane < i1 ? a.items[g0 + lane] : make_int2(a.V, 0); };
+  typename T::Raw x[SEG_ROWS];   // a rolling window: a row's place is refilled as soon as it has been added
+  auto fetch = [&](const int2& from, int j, typename T::Raw& to) {
+    const unsigned key = __shfl_sync(0xffffffffu, from.x, j), tok = __shfl_sync(0xffffffffu, from.y, j);
+    if (live && key < nv && tok < nn)
+      to = *reinterpret_cast<const typename T::Raw*>(a.dout + (static_cast<long long>(tok) * a.H + h) * T::SIZE);
+  };
+  int2 my = group(i0);
+  int cur = __shfl_sync(0xffffffffu, my.x, 0);
   bool came_in = cur == before;
+#pragma unroll
+  for (int q = 0; q < SEG_ROWS; ++q) fetch(my, q, x[q]);
   for (int g0 = i0; g0 < i1; g0 += 32) {
+    const int2 next = group(g0 + 32);
     const int m = min(32, i1 - g0);
-    const int2 my = lane < m ? a.items[g0 + lane] : make_int2(a.V, 0);
+#pragma unroll 1
     for (int j0 = 0; j0 < m; j0 += SEG_ROWS) {
-      typename T::Raw x[SEG_ROWS];
+      const int2 from = j0 + SEG_ROWS < 32 ? my : next;
 #pragma unroll
       for (int q = 0; q < SEG_ROWS; ++q) {
-        const unsigned key = __shfl_sync(0xffffffffu, my.x, j0 + q);
-        const unsigned tok = __shfl_sync(0xffffffffu, my.y, j0 + q);
-        if (live && key < nv && tok < nn)
-          x[q] = *reinterpret_cast<const typename T::Raw*>(a.dout + (static_cast<long long>(tok) * a.H + h) * T::SIZE);
-      }
-#pragma unroll
-      for (int q = 0; q < SEG_ROWS; ++q) {
-        if (j0 + q >= m) break;
-        const int key = __shfl_sync(0xffffffffu, my.x, j0 + q);
+        const int key = __shfl_sync(0xffffffffu, my.x, j0 + q);   // the table's size behind the last entry
         if (key != cur) {   // uniform over the warp: the run ends inside the chunk
-          if (live && static_cast<unsigned>(cur) < nv) {
+          if (live && static_cast<unsigned>(cur) < nv && j0 + q < m) {
             if (came_in) F32::store(a.part + (2ll * c) * a.H + h, s);
             else write_row<O>(a, cur, h, s);
           }
+          if (j0 + q < m) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) s[k] = 0.f;
-          cur = key;
-          came_in = false;
+            for (int k = 0; k < 8; ++k) s[k] = 0.f;
+            cur = key;
+            came_in = false;
+          }
         }
         if (live && static_cast<unsigned>(key) < nv) {
           float f[8];
@@ -493,8 +500,10 @@ __device__ __forceinline__ void segments(const SegArgs& a, long long warp, int l
 #pragma unroll
           for (int k = 0; k < 8; ++k) s[k] += f[k];
         }
+        fetch(from, (j0 + SEG_ROWS + q) & 31, x[q]);
       }
     }
+    my = next;
   }
   if (!live || static_cast<unsigned>(cur) >= nv) return;
   if (came_in) F32::store(a.part + (2ll * c) * a.H + h, s);
@@ -554,12 +563,16 @@ __device__ __forceinline__ void zero_absent(const SegArgs& a, int block, unsigne
       }
       m = __ballot_sync(0xffffffffu, absent);
     }
-    for (int n = 0; m; ++n) {   // dealt to the warps
+    // a long row by the whole block, others dealt to the warps: fewer places
+    // are written at once
+    const bool whole = row_bytes >= THREADS * 16;
+    for (int n = 0; m; ++n) {
       const int k = __ffs(m) - 1;
       m &= m - 1;
-      if (n % SEG_WARPS != w) continue;
+      if (!whole && n % SEG_WARPS != w) continue;
       uint4* p = reinterpret_cast<uint4*>(a.gw + (q0 + k) * row_bytes);
-      for (int i = lane; i < row_bytes / 16; i += 32) p[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (int i = whole ? static_cast<int>(threadIdx.x) : lane; i < row_bytes / 16; i += whole ? THREADS : 32)
+        p[i] = make_uint4(0u, 0u, 0u, 0u);
     }
   }
 }
@@ -702,7 +715,8 @@ EmbPlan emb_plan(long long N, long long H, long long V) {
   p.passes = static_cast<int>(cdiv(key_bits, SORT_MAX_BITS));
   p.bits = static_cast<int>(cdiv(key_bits, p.passes));
   p.tiles = N <= CS_MAX ? CS_BLOCKS : static_cast<int>(cdiv(N, SORT_THREADS * (N <= SORT_LARGE ? SORT_ITEMS_SMALL : SORT_ITEMS_LARGE)));
-  p.chunk = static_cast<int>(cdiv(std::max<long long>(MIN_CHUNK, cdiv(N, MAX_CHUNKS)), 32) * 32);
+  p.chunk = static_cast<int>(cdiv(std::max<long long>(CHUNK, cdiv(N, MAX_CHUNKS)), 32) * 32);
+  while (p.chunk > MIN_CHUNK && cdiv(N, p.chunk) * cdiv(H, COLS) < 8 * 152) p.chunk /= 2;
   p.n_chunks = static_cast<int>(cdiv(N, p.chunk));
   size_t off = al256(HDR_WORDS * sizeof(int));
   auto take = [&off](size_t bytes) {
@@ -857,11 +871,15 @@ flce_status flce_embedding_bwd(const void* grad_out, const int32_t* ids, int64_t
   a.ids = ids;
   a.padding = padding_idx;
   const long long seg_blocks = cdiv(static_cast<long long>(a.n_chunks) * a.slices, SEG_WARPS);
-  // zeroing: four blocks per SM, of whole groups of 32 rows
-  a.zero_rows = static_cast<int>(std::min<long long>(cdiv(cdiv(V, 4 * 152), ZERO_ROWS) * ZERO_ROWS, ZERO_MAX_ROWS));
+  // zeroing: at least four blocks per SM, of whole groups of 32 rows and of no
+  // more than about 1 MB: larger ones leave a second wave that few SMs share
+  // (16384 tokens at 4096 x 128256: 410 us with 3.6 MB a block, 332 with 1 MB)
+  const long long row_bytes = H * (grad_dtype == FLCE_F32 ? 4 : 2);
+  const long long zero_rows = std::min(cdiv(V, 4 * 152), ZERO_BYTES / row_bytes);
+  a.zero_rows = static_cast<int>(std::min<long long>(std::max(1ll, cdiv(zero_rows, ZERO_ROWS)) * ZERO_ROWS, ZERO_MAX_ROWS));
   const long long zero_blocks = a.accumulate ? 0 : cdiv(V, a.zero_rows);
   // reading all ids is worth it where it is little next to the rows written
-  a.scan = N <= CS_MAX && 16 * N <= static_cast<long long>(a.zero_rows) * H * (grad_dtype == FLCE_F32 ? 4 : 2) ? 1 : 0;
+  a.scan = N <= CS_MAX && 16 * N <= a.zero_rows * row_bytes ? 1 : 0;
   a.zero_blocks = static_cast<int>(zero_blocks);
   a.seg_blocks = static_cast<int>(seg_blocks);
   const long long blocks = seg_blocks + zero_blocks;
