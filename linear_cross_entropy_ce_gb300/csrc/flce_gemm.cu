@@ -1054,8 +1054,9 @@ cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps& m, int grid, cudaStre
   attr.val.programmaticStreamSerializationAllowed = dependent ? 1 : 0;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (a.mode == MODE_STATS || a.mode == MODE_DZ) return cudaLaunchKernelEx(&cfg, flce_gemm_kernel<true>, m, a);
-  return cudaLaunchKernelEx(&cfg, flce_gemm_kernel<false>, m, a);
+  if (a.mode == MODE_STATS || a.mode == MODE_DZ)
+    return launch_result(cudaLaunchKernelEx(&cfg, flce_gemm_kernel<true>, m, a));
+  return launch_result(cudaLaunchKernelEx(&cfg, flce_gemm_kernel<false>, m, a));
 }
 
 }  // namespace flce

@@ -151,6 +151,13 @@ inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3
 template <typename T>
 T* at(void* ws, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(ws) + off); }
 
+// The result of a launch, which does not stay behind as the thread's last error
+// (the next call would take it for its own).
+inline cudaError_t launch_result(cudaError_t e) {
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
 // Launch whose blocks may come up while the previous kernel of the stream still
 // runs; the kernel has to call ptx::grid_dependency_wait() before it reads or
 // writes anything that kernel (or an earlier one) touches.
@@ -167,7 +174,7 @@ cudaError_t launch_dependent_smem(void (*kernel)(P...), unsigned blocks, unsigne
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+  return launch_result(cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...));
 }
 template <typename... P, typename... A>
 cudaError_t launch_dependent(void (*kernel)(P...), unsigned blocks, unsigned threads, cudaStream_t st,
