@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(FRONT_THREADS) probs_front_kernel(const FrontA
   before = total = 0;
 #pragma unroll
   for (int k = 0; k < FRONT_WARPS; ++k) { before += red[0][k]; total += red[1][k]; }
-  if (blockIdx.x == 0) {
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
     if (tid == 0) {
       a.hdr[HDR_STATUS] = bad ? STATUS_BADTARGET : 0;
       a.hdr[HDR_NVALID] = total;
@@ -140,7 +140,10 @@ __global__ void __launch_bounds__(FRONT_THREADS) probs_front_kernel(const FrontA
     if (lane < FRONT_TOKENS) dst[lane] = valid ? before + __popc(m & ((1u << lane) - 1u)) : -1;
   }
   __syncthreads();
-  const int n16 = a.H / 8;
+  // the columns this block moves (16-byte units)
+  const int n16 = a.H / 8, each = (n16 + gridDim.y - 1) / gridDim.y;
+  const int lo = static_cast<int>(blockIdx.y) * each, hi = min(n16, lo + each);
+  const bool first = blockIdx.y == 0;
   for (int k = w; k < FRONT_TOKENS; k += FRONT_WARPS) {   // a warp per token
     const long long n = n0 + k;
     if (n >= a.N) break;
@@ -149,8 +152,8 @@ __global__ void __launch_bounds__(FRONT_THREADS) probs_front_kernel(const FrontA
       const uint4* from = reinterpret_cast<const uint4*>(a.hidden + n * a.H);
       uint4* to = reinterpret_cast<uint4*>(a.xc + static_cast<size_t>(r) * a.H);
 #pragma unroll 8
-      for (int c = lane; c < n16; c += 32) to[c] = from[c];
-      if (lane == 0) {
+      for (int c = lo + lane; c < hi; c += 32) to[c] = from[c];
+      if (first && lane == 0) {
         a.tc[r] = a.targets[n];
         a.idx[r] = static_cast<int>(n);
         if (a.rowc) a.rowc[r] = dz_row(a.temperature, a.lse_in[n], a.entropy_in, a.grad_logp, a.grad_entropy, n);
@@ -158,9 +161,9 @@ __global__ void __launch_bounds__(FRONT_THREADS) probs_front_kernel(const FrontA
     } else if (a.rowc) {   // backward: no gradient
       if (a.grad_hidden) {
         uint4* to = reinterpret_cast<uint4*>(a.grad_hidden + n * a.H);
-        for (int c = lane; c < n16; c += 32) to[c] = make_uint4(0u, 0u, 0u, 0u);
+        for (int c = lo + lane; c < hi; c += 32) to[c] = make_uint4(0u, 0u, 0u, 0u);
       }
-    } else {               // forward: 0 for an ignored token, NaN for a target outside [0, V)
+    } else if (first) {    // forward: 0 for an ignored token, NaN for a target outside [0, V)
       const float v = a.targets[n] == a.ii ? 0.f : __int_as_float(0x7fc00000);
       if (lane == 0) {
         a.logp[n] = v;
@@ -173,14 +176,15 @@ __global__ void __launch_bounds__(FRONT_THREADS) probs_front_kernel(const FrontA
       }
     }
   }
-  clear_bounds(a.bound, a.group_max, a.group_stride, a.K, a.C, blockIdx.x * FRONT_THREADS + tid,
-               gridDim.x * FRONT_THREADS);
+  if (first)
+    clear_bounds(a.bound, a.group_max, a.group_stride, a.K, a.C, blockIdx.x * FRONT_THREADS + tid,
+                 gridDim.x * FRONT_THREADS);
   // padding rows up to the next multiple of 128
   const int end = min(a.C, (total + BM - 1) / BM * BM);
   for (int r = total + static_cast<int>(blockIdx.x) * FRONT_WARPS + w; r < end; r += gridDim.x * FRONT_WARPS) {
     uint4* to = reinterpret_cast<uint4*>(a.xc + static_cast<size_t>(r) * a.H);
-    for (int c = lane; c < n16; c += 32) to[c] = make_uint4(0u, 0u, 0u, 0u);
-    if (lane == 0) {
+    for (int c = lo + lane; c < hi; c += 32) to[c] = make_uint4(0u, 0u, 0u, 0u);
+    if (first && lane == 0) {
       a.tc[r] = -1;
       if (a.rowc) a.rowc[r] = DzRow{0.f, 0.f, 0.f, 0.f};
     }
@@ -331,7 +335,7 @@ __global__ void __launch_bounds__(32 * TOP_WARPS)
 // grad_hidden rows of a chunk from the fp32 parts of its vocabulary splits,
 // added in order and rounded once.  Reads what L2 still holds: S C H 4 bytes.
 constexpr int DXR_THREADS = 256;
-constexpr int DXR_BATCH = 4;   // parts in flight
+constexpr int DXR_BATCH = 8;   // parts in flight
 __global__ void __launch_bounds__(DXR_THREADS)
     dx_reduce_kernel(const int* hdr, const int* idx, long long c0, int C, int H, int splits, const float* parts,
                      uint16_t* grad_hidden) {
@@ -493,7 +497,9 @@ cudaError_t launch_mark_failed(const int* hdr, uint16_t* grad_hidden, float* gra
 }
 
 cudaError_t launch_probs_front(const FrontArgs& a, cudaStream_t s) {
-  probs_front_kernel<<<static_cast<unsigned>(cdiv(a.N, FRONT_TOKENS)), FRONT_THREADS, 0, s>>>(a);
+  // few tokens: several blocks share a row, 1024 columns each
+  const unsigned slices = a.N <= 2048 ? static_cast<unsigned>(std::min<long long>(cdiv(a.H, 1024), 64)) : 1;
+  probs_front_kernel<<<dim3(static_cast<unsigned>(cdiv(a.N, FRONT_TOKENS)), slices), FRONT_THREADS, 0, s>>>(a);
   return cudaGetLastError();
 }
 
