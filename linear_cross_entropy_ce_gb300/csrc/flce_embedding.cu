@@ -528,7 +528,8 @@ __device__ __forceinline__ int lower_bound(const int2* items, int n, int v) {
 
 // The rows of one block whose id does not occur.  With `scan`, the block reads
 // all the ids (from L2) and marks those of its rows, so it need not wait for
-// the sort; else it looks its rows up in the sorted ids.
+// the sort; else its warps look up 32 rows each in the sorted ids (262144 tokens
+// at 64 x 128256: 91 us for the gradient, 111 with one search after another).
 template <typename O>
 __device__ __forceinline__ void zero_absent(const SegArgs& a, int block, unsigned* seen) {
   constexpr int THREADS = 32 * SEG_WARPS;
@@ -546,23 +547,23 @@ __device__ __forceinline__ void zero_absent(const SegArgs& a, int block, unsigne
         atomicOr(&seen[k / 32], 1u << (k % 32));
       }
     }
-    __syncthreads();
+  } else {   // 32 rows a warp; every search is some 20 dependent loads
+    for (long long q = r0 + w * 32; q < r1; q += SEG_WARPS * 32) {
+      bool found = false;
+      if (q + lane < r1) {
+        const int v = static_cast<int>(q + lane);
+        const int at = lower_bound(a.items, a.N, v);
+        found = at < a.N && a.items[at].x == v;
+      }
+      const unsigned m = __ballot_sync(0xffffffffu, found);
+      if (lane == 0) seen[(q - r0) / 32] = m;
+    }
   }
+  __syncthreads();
   const long long row_bytes = static_cast<long long>(a.H) * O::SIZE;
   for (long long q0 = r0; q0 < r1; q0 += ZERO_ROWS) {
-    unsigned m;   // rows q0 + k that do not occur
-    if (a.scan) {
-      m = ~seen[(q0 - r0) / 32];
-      if (r1 - q0 < 32) m &= (1u << (r1 - q0)) - 1u;
-    } else {
-      bool absent = false;
-      if (q0 + lane < r1) {
-        const int v = static_cast<int>(q0 + lane);
-        const int at = lower_bound(a.items, a.N, v);
-        absent = at >= a.N || a.items[at].x != v;
-      }
-      m = __ballot_sync(0xffffffffu, absent);
-    }
+    unsigned m = ~seen[(q0 - r0) / 32];   // rows q0 + k that do not occur
+    if (r1 - q0 < 32) m &= (1u << (r1 - q0)) - 1u;
     // a long row by the whole block, others dealt to the warps: fewer places
     // are written at once
     const bool whole = row_bytes >= THREADS * 16;
@@ -597,12 +598,14 @@ __global__ void __launch_bounds__(32 * SEG_WARPS, 2) embedding_segments_kernel(c
 }
 
 // A run that goes out of chunk c and comes into c + 1, c + 2, ...: its partial
-// sums.  A block looks at eight chunks (of one column slice), one per warp.  A
+// sums.  A block looks at 16 chunks (of one column slice), one per warp.  A
 // short chain is added up by its warp; a long one (a token that makes a tenth
 // of 65536 has 100 links) by the whole block, cut in as many equal parts as
-// there are warps, whose sums are added in order.  Latency: 9 us at 65536 x 512
-// (151 us with one warp per chain).
-constexpr int JOIN_WARPS = 8;
+// there are warps, whose sums are added in order.  Latency: 8 us at 65536 x 512
+// (151 us with one warp per chain).  All tokens alike at 262144 x 64: 130 us for
+// the gradient with 16 warps a block, 147 with eight, 128 with 32, which are up
+// to 17% slower where chains are short.
+constexpr int JOIN_WARPS = 16;
 constexpr int JOIN_LINKS = 8;          // partial sums a warp has in flight
 constexpr int JOIN_SHORT = JOIN_LINKS;
 
@@ -878,7 +881,8 @@ flce_status flce_embedding_bwd(const void* grad_out, const int32_t* ids, int64_t
   const long long zero_rows = std::min(cdiv(V, 4 * 152), ZERO_BYTES / row_bytes);
   a.zero_rows = static_cast<int>(std::min<long long>(std::max(1ll, cdiv(zero_rows, ZERO_ROWS)) * ZERO_ROWS, ZERO_MAX_ROWS));
   const long long zero_blocks = a.accumulate ? 0 : cdiv(V, a.zero_rows);
-  // reading all ids is worth it where it is little next to the rows written
+  // reading all ids is worth it where it is little next to the rows written, and
+  // for no more tokens than that (65536 at 4096 x 128256: 507 us with it, 423 without)
   a.scan = N <= CS_MAX && 16 * N <= a.zero_rows * row_bytes ? 1 : 0;
   a.zero_blocks = static_cast<int>(zero_blocks);
   a.seg_blocks = static_cast<int>(seg_blocks);
