@@ -552,6 +552,28 @@ def token_logprobs_bwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torc
     return o
 
 
+def _leaves(ctx):
+    return [node for node, _ in ctx.next_functions if node is not None and type(node).__name__ == "AccumulateGrad"]
+
+
+def _mark_leaves(ctx, device) -> None:
+    """Notes on each leaf's accumulator the stream it was first used on.  The
+    accumulator keeps that stream, and lives as long as any graph of the leaf."""
+    for node in _leaves(ctx):
+        if "flce_stream" not in node.metadata:
+            node.metadata["flce_stream"] = torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _check_capture(ctx) -> None:
+    """Refuses a captured backward whose leaves belong to a living graph of the
+    default stream: autograd would make that stream, which cannot be captured,
+    wait for the capture, and the process would end."""
+    if torch.cuda.is_current_stream_capturing():
+        if any(node.metadata.get("flce_stream") == 0 for node in _leaves(ctx)):
+            raise RuntimeError("backward captured while an eager graph of the same leaves, made on the default "
+                               "stream, is alive: drop its loss and outputs first, or make it on another stream")
+
+
 class _LinearLogProbsFn(torch.autograd.Function):
     """The backward recomputes the logits chunk by chunk from the saved log-sum-exp."""
 
@@ -562,6 +584,7 @@ class _LinearLogProbsFn(torch.autograd.Function):
         ctx.save_for_backward(hidden, weight, targets, o["lse"], o["entropy"])
         ctx.args = (ignore_index, temperature)
         ctx.set_materialize_grads(False)
+        _mark_leaves(ctx, hidden.device)
         return o["logp"], o["entropy"]
 
     @staticmethod
@@ -570,6 +593,7 @@ class _LinearLogProbsFn(torch.autograd.Function):
         need_hidden, need_weight = ctx.needs_input_grad[:2]
         if not (need_hidden or need_weight) or (grad_logp is None and grad_entropy is None):
             return None, None, None, None, None
+        _check_capture(ctx)
         hidden, weight, targets, lse, entropy = ctx.saved_tensors
         ignore_index, temperature = ctx.args
         gl = None if grad_logp is None else grad_logp.to(torch.float32).contiguous()
@@ -582,7 +606,9 @@ class _LinearLogProbsFn(torch.autograd.Function):
 def linear_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
                     temperature: float = 1.0):
     """``(logp, entropy)`` of the given tokens at the LM head, fp32 [N] each, with
-    autograd support: the head of a policy-gradient or preference loss."""
+    autograd support: the head of a policy-gradient or preference loss.  Forward
+    and backward may be captured into one CUDA graph; an eager graph of the same
+    leaves, made on the default stream and still alive, is refused there."""
     return _LinearLogProbsFn.apply(hidden, weight, targets, ignore_index, temperature)
 
 
@@ -689,6 +715,7 @@ class _EmbeddingFn(torch.autograd.Function):
         ids = ids.contiguous()
         ctx.save_for_backward(ids)
         ctx.args = (weight.shape[0], weight.dtype, scale, padding_idx)
+        _mark_leaves(ctx, weight.device)
         return embedding_fwd(weight.contiguous(), ids, scale)
 
     @staticmethod
@@ -696,6 +723,7 @@ class _EmbeddingFn(torch.autograd.Function):
     def backward(ctx, grad_out):
         if not ctx.needs_input_grad[0]:
             return None, None, None, None
+        _check_capture(ctx)
         V, dtype, scale, padding_idx = ctx.args
         o = embedding_bwd(grad_out.contiguous(), ctx.saved_tensors[0], V, scale, padding_idx, grad_weight_dtype=dtype)
         return o["grad_weight"], None, None, None

@@ -224,6 +224,45 @@ def test_captured_training_step(env):  # noqa: F811
         assert torch.equal(out[0], a[0]) and torch.equal(out[1], a[1])
 
 
+@pytest.mark.parametrize("leaf", ["hidden", "weight", "table"])
+def test_capture_beside_a_living_graph(env, leaf):  # noqa: F811
+    """A backward captured while an eager graph of the same leaf lives on the default stream is refused, before
+    autograd orders that stream behind the capture; the forward alone, and the step once the graph is gone, are not."""
+    flce, torch, dev = env
+    N, H, V = 300, 64, 700
+    X, W, t = problem(N, H, V, seed=5, ignored=0.1)
+    x, w = (torch.from_numpy(a).to(torch.bfloat16).to(dev) for a in (X, W))
+    t = torch.from_numpy(t).to(dev)
+    ids = torch.from_numpy(draw_ids(N, V, "zipf", 2)).to(dev)
+    up = torch.randn(N, H, device=dev, dtype=torch.bfloat16)
+    u = {"hidden": x, "weight": w, "table": w}[leaf].clone().requires_grad_(True)
+
+    def forward():
+        if leaf == "table":
+            return (flce.embedding(ids, u) * up).sum()
+        return flce.linear_logprobs(*((u, w) if leaf == "hidden" else (x, u)), t)[0].sum()
+
+    loss = forward()
+    want = torch.autograd.grad(loss, u, retain_graph=True)[0]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        value = forward()
+    graph.replay()
+    assert torch.equal(value, loss)
+    del value
+    with pytest.raises(RuntimeError, match="alive"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            torch.autograd.grad(forward(), u)
+    del loss
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = torch.autograd.grad(forward(), u)[0]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
 def test_tied_model(env):  # noqa: F811
     """ids -> scaled embedding -> x + tanh(x) -> log probabilities against the same weight; both
     gradients through autograd, and through the calls that add into one fp32 grad_weight."""

@@ -80,3 +80,41 @@ def test_python_refusals(flce):
         flce.token_logprobs(h, w, t)   # not CUDA tensors
     with pytest.raises(ValueError):
         flce.token_logprobs_bwd(h, w, t, torch.zeros(4), None, torch.zeros(4))
+
+
+def test_capture_beside_a_living_graph(flce, monkeypatch):
+    """The marks on a leaf's accumulator live as long as the graphs that use it, and only the default stream's refuse."""
+    torch = pytest.importorskip("torch")
+    now = {"stream": 0, "capturing": False}
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: now["stream"], raising=False)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now["capturing"])
+
+    class Double(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x):
+            flce._mark_leaves(ctx, torch.device("cuda", 0))
+            return 2 * x
+
+        @staticmethod
+        def backward(ctx, g):
+            flce._check_capture(ctx)
+            return 2 * g
+
+    def step(stream, capturing):
+        now.update(stream=stream, capturing=capturing)
+        y = Double.apply(leaf)
+        return y, lambda: torch.autograd.grad(y.sum(), leaf)[0]
+
+    for eager_stream, refused in ((0, True), (7, False)):
+        leaf = torch.ones(3, requires_grad=True)
+        eager = step(eager_stream, False)
+        eager[1]()
+        captured = step(9, True)
+        if refused:
+            with pytest.raises(RuntimeError, match="alive"):
+                captured[1]()
+        else:
+            assert captured[1]().tolist() == [2, 2, 2]
+        del eager, captured
+        assert step(9, True)[1]().tolist() == [2, 2, 2]
+    assert Double.apply(2 * leaf).sum().item() == 12   # not a leaf: nothing to mark
