@@ -309,3 +309,16 @@ def test_tied_model(env):  # noqa: F811
     err = np.abs(np64(d["grad_weight"]) - (np64(one) + e))
     assert np.all(err <= (N + 3) * 2.0 ** -24 * (mag + np.abs(np64(one))))
     assert np.all(np.abs(np64(o["logp"]) - logprobs_oracle(np64(hc), W, t)["logp"]) <= 1e-4)
+
+
+@pytest.mark.parametrize("N,H,V", [(1, 8, 1), (50, 64, 30), (3000, 520, 1000), (20000, 64, 5000)])
+def test_nothing_is_read_behind_padding(env, N, H, V):  # noqa: F811
+    """NaN in the gradients of padding tokens and a workspace full of NaN change no bit."""
+    flce, torch, dev = env
+    ids = torch.from_numpy(draw_ids(N, V, "uniform", 4)).to(dev)
+    g = torch.randn(N, H, device=dev).to(torch.bfloat16)
+    a = flce.embedding_bwd(g, ids, V, 2.0, 0)
+    g[ids == 0] = float("nan")
+    b = flce.embedding_bwd(g, ids, V, 2.0, 0, workspace=torch.full_like(a["workspace"], 255))
+    assert torch.isfinite(a["grad_weight"]).all() and torch.equal(a["grad_weight"], b["grad_weight"])
+    assert not a["grad_weight"][0].any()

@@ -474,3 +474,34 @@ def test_time_out_is_seen(env, N):
     d = flce.token_logprobs_bwd(h, w, tt, o["lse"], o["entropy"], o["logp"])
     assert flce.query_status(d["workspace"]) == flce.FLCE_ETIMEOUT
     assert torch.isnan(d["grad_hidden"][0, 0]) and torch.isnan(d["grad_weight"][0, 0])
+
+
+@pytest.mark.parametrize("N,H,V,ignored", [(1, 64, 100, 1.0), (5, 72, 513, 0.5), (61, 256, 1000, 0.3), (128, 64, 2000, 1.0),
+                                           (129, 64, 100, 0.97), (300, 64, 512, 0.3), (1030, 136, 5000, 0.3)])
+def test_nothing_is_read_behind_ignored_targets(env, N, H, V, ignored):
+    """NaN and inf in ignored tokens' rows and upstream gradients, and a workspace full of NaN, change no bit."""
+    flce, torch, dev = env
+    X, W, t = problem(N, H, V, seed=N, ignored=ignored)
+    h, w, tt = to_gpu(torch, dev, X, W, t)
+    off = tt == -100
+    r = torch.Generator(device=dev).manual_seed(1)
+    g, e = (torch.randn(N, generator=r, device=dev) for _ in range(2))
+
+    def spoil(a, v):
+        a = a.clone()
+        a[off] = v
+        return a
+
+    bad = spoil(h, float("nan"))
+    for K in (0, 5):
+        a = flce.token_logprobs(h, w, tt, top_k=K)
+        b = flce.token_logprobs(bad, w, tt, top_k=K, workspace=torch.full_like(a["workspace"], 255))
+        for k in ("logp", "lse", "entropy") + (("top_ids", "top_logp") if K else ()):
+            assert torch.equal(a[k], b[k]), (K, k)
+    for dt in (torch.float32, torch.bfloat16):
+        c = flce.token_logprobs_bwd(h, w, tt, a["lse"], a["entropy"], g, e, grad_weight_dtype=dt)
+        d = flce.token_logprobs_bwd(bad, w, tt, spoil(a["lse"], float("nan")), spoil(a["entropy"], float("inf")),
+                                    spoil(g, float("inf")), spoil(e, float("nan")), grad_weight_dtype=dt,
+                                    workspace=torch.full_like(c["workspace"], 255))
+        for k in ("grad_hidden", "grad_weight"):
+            assert torch.isfinite(c[k]).all() and torch.equal(c[k], d[k]), (dt, k)
