@@ -505,3 +505,24 @@ def test_nothing_is_read_behind_ignored_targets(env, N, H, V, ignored):
                                     workspace=torch.full_like(c["workspace"], 255))
         for k in ("grad_hidden", "grad_weight"):
             assert torch.isfinite(c[k]).all() and torch.equal(c[k], d[k]), (dt, k)
+
+
+@pytest.mark.parametrize("N", [7, 300])
+def test_gradient_of_bad_targets(env, N):
+    """Targets outside the vocabulary add nothing to the gradients, as ignored ones, and set the status."""
+    flce, torch, dev = env
+    V = 300
+    X, W, t = problem(N, 64, V, seed=2, ignored=0.2)
+    h, w, tt = to_gpu(torch, dev, X, W, t)
+    bad, left_out = tt.clone(), tt.clone()
+    for i, v in ((1, V), (4, -7), (5, 2 ** 31 - 1), (6, -2 ** 31)):
+        bad[i], left_out[i] = v, -100
+    g = torch.randn(N, device=dev)
+    o = flce.token_logprobs(h, w, bad)
+    p = flce.token_logprobs(h, w, left_out)
+    a = flce.token_logprobs_bwd(h, w, bad, o["lse"], o["entropy"], g, g)
+    assert flce.query_status(a["workspace"]) == flce.FLCE_EBADTARGET
+    b = flce.token_logprobs_bwd(h, w, left_out, p["lse"], p["entropy"], g, g)
+    assert flce.query_status(b["workspace"]) == flce.FLCE_OK
+    for k in ("grad_hidden", "grad_weight"):
+        assert torch.equal(a[k], b[k]), k
