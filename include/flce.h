@@ -30,8 +30,12 @@
  *
  * Memory and ownership.  The caller allocates every buffer, including the
  * workspace; the library never allocates device memory.  Inputs are only
- * read.  Outputs are fully overwritten (never accumulated into).  All device
- * pointers must be 16-byte aligned and must not alias one another.
+ * read.  Outputs are fully overwritten (never accumulated into, but for
+ * FLCE_ACCUMULATE).  All device pointers must be 16-byte aligned (arrays of
+ * one 4-byte value per token: 4-byte) and must not alias one another.  A
+ * workspace must be 32-byte aligned where the call keeps logits or their
+ * gradient in it: every call with gradients but flce_embedding_bwd, and
+ * flce_logprobs of more than 128 tokens with top alternatives.
  *
  * Streams.  Each call only enqueues kernels on `stream` (a cudaStream_t
  * passed as void*, NULL = legacy default stream) and returns; nothing
@@ -60,7 +64,7 @@ extern "C" {
 typedef enum flce_status {
   FLCE_OK = 0,
   FLCE_EINVAL = 1,        /* NULL pointer, N/H/V < 1, unknown flag          */
-  FLCE_EUNSUPPORTED = 2,  /* H % 8 != 0, pointer not 16-byte aligned,       */
+  FLCE_EUNSUPPORTED = 2,  /* H % 8 != 0, pointer not aligned as said above,  */
                           /* size beyond the supported range, no sm_100+ GPU */
   FLCE_EWORKSPACE = 3,    /* workspace_bytes below the minimum plan          */
   FLCE_EBADTARGET = 4,    /* (device) a target outside [0,V), not ignored    */

@@ -453,6 +453,7 @@ flce_status run(const Job& j) {
       (j.loss && !aligned4(j.loss)) || (j.n_valid && !aligned4(j.n_valid)) || (j.row_loss && !aligned4(j.row_loss)))
     return FLCE_EUNSUPPORTED;
   if (!fwd_only && (!aligned16(j.grad_hidden) || !aligned16(j.grad_weight))) return FLCE_EUNSUPPORTED;
+  if (!fwd_only && !aligned32(j.ws)) return FLCE_EUNSUPPORTED;   // z is read and written 32 bytes at a time
   if (j.lse && !aligned4(j.lse)) return FLCE_EUNSUPPORTED;
 
   DeviceState dev;

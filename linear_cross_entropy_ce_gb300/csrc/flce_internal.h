@@ -146,6 +146,7 @@ bool sizes_ok(long long N, long long H, long long V);
 
 inline size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 inline long long cdiv(long long a, long long b) { return (a + b - 1) / b; }
+inline bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 template <typename T>

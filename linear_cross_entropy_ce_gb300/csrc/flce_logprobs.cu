@@ -535,6 +535,8 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
   if (!aligned16(hidden) || !aligned16(weight) || !aligned16(workspace) || !aligned4(targets) || !aligned4(logp) ||
       !aligned4(entropy) || !aligned4(lse) || !aligned4(top_ids) || !aligned4(top_logp))
     return FLCE_EUNSUPPORTED;
+  // the logits of the chunked form are stored 32 bytes at a time
+  if (top_k > 0 && N > STREAM_MAX_TOKENS && !aligned32(workspace)) return FLCE_EUNSUPPORTED;
   DeviceState dev;
   if (device_state(&dev) != cudaSuccess) { cudaGetLastError(); return FLCE_ECUDA; }
   if (dev.major < 10) return FLCE_EUNSUPPORTED;
