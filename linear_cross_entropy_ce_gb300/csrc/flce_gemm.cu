@@ -696,6 +696,9 @@ __device__ __forceinline__ bool epi_dx_split(const GemmArgs& a, const Shape& s, 
   const bool chain = a.slabs == 0;
   bool ok = true;
   if (chain && leader && t.split > 0) ok = wait_flag(flag, t.split, ctl, a.timeout_ns, const_cast<int*>(a.hdr));
+  // the warps' buffers are the staging buffer of block_to_global: the box that
+  // a grad_weight tile left on its way has been read before they are written
+  if (leader) ptx::bulk_wait_read_0();
   if (!ptx::named_bar_and(bar, GROUP_THREADS, ok)) return false;
   const int h0 = t.n0 + col0;
   float* acc = const_cast<float*>(a.dxacc) + (chain ? 0 : static_cast<size_t>(t.split) * a.C * a.H);
