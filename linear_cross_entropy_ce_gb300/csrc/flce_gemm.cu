@@ -877,8 +877,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       }
       if (!ok) break;
     }
-    if (!ok && lead) {
-      // let the copies already in flight land before the pair exits
+    if (lead) {
+      // Let the copies in flight land before the pair exits.  Without a
+      // time-out the MMAs have waited for all of them; with one, also where
+      // this thread had issued its last copy before another role gave up.
       for (int i = 0; i < nstages; ++i)
         if (issued_mask & (1u << i)) wait_phase(&ctl->full[i], (issued_parity >> i) & 1u, ctl, to, false, hdr, W_DRAIN);
     }

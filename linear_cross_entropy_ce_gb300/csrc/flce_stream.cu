@@ -184,9 +184,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
       }
     }
-    if (!ok)   // let the copies in flight land before the CTA exits
-      for (int i = 0; i < C::STAGES; ++i)
-        if (issued_mask & (1u << i)) wait(&ctl->full[i], (issued_parity >> i) & 1u, ctl, to, a.hdr, S_DRAIN, false);
+    // Let the copies in flight land before the CTA exits.  Without a time-out
+    // the MMAs have waited for all of them; with one, also where this thread
+    // had issued its last copy before another role gave up.
+    for (int i = 0; i < C::STAGES; ++i)
+      if (issued_mask & (1u << i)) wait(&ctl->full[i], (issued_parity >> i) & 1u, ctl, to, a.hdr, S_DRAIN, false);
   } else if (warp == 1 && lane == 0) {
     // ---------------- MMA issuer ----------------
     constexpr uint32_t idesc = ptx::idesc_bf16_f32(128, NT, 0, 0);
