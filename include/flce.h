@@ -246,7 +246,8 @@ flce_status flce_vocab_shard_bwd(const void* hidden, const void* weight_shard,
  * A row whose target is ignore_index gets 0 (ids -1).  A row whose target lies
  * outside [0, V) gets NaN (ids -1) and FLCE_EBADTARGET in the status word; the
  * other rows are right.  A row with NaN or +inf logits gets NaN.  After a
- * pipeline time-out (FLCE_ETIMEOUT) every scored row is NaN.
+ * pipeline time-out (FLCE_ETIMEOUT) every scored row is NaN (ids -1), those of
+ * chunks that were done before it too.
  * The N x V logits are not kept: the workspace (flce_logprobs_workspace_bytes;
  * less runs in smaller chunks, down to 128 rows) stays below 5% of their bf16
  * size, or 512 MiB (2 GiB with top alternatives) where that is more.
@@ -359,6 +360,8 @@ flce_status flce_query_stall(const void* workspace, int32_t* info /* [4] */, voi
  * becomes FLCE_ETIMEOUT and its loss NaN; the CUDA context stays usable.
  */
 flce_status flce_debug_arm_stall(uint64_t timeout_ns);
+/* The same for the launch behind the next `launches` ones (>= 0): a later chunk of a call. */
+flce_status flce_debug_arm_stall_after(uint64_t timeout_ns, int32_t launches);
 
 /*
  * Diagnostic: enqueue one kernel that waits on a pipeline barrier nothing

@@ -341,11 +341,16 @@ cudaEvent_t prof_event() {
 // Test hook (flce_debug_arm_stall): a non-zero value arms the next GEMM
 // launch of the process to withhold one pipeline signal, with this wait limit.
 std::atomic<unsigned long long> g_stall_armed{0};
+std::atomic<int> g_stall_skip{0};   // tcgen05 launches that pass before it
 
 }  // namespace
 
 namespace flce {
-unsigned long long take_armed_stall() { return g_stall_armed.exchange(0); }
+unsigned long long take_armed_stall() {
+  if (g_stall_armed.load() == 0) return 0;
+  if (g_stall_skip.fetch_sub(1) > 0) return 0;
+  return g_stall_armed.exchange(0);
+}
 
 ProfScope prof_launch_begin(cudaStream_t st) {
   ProfScope r;
@@ -742,7 +747,12 @@ flce_status flce_query_stall(const void* workspace, int32_t* info, void* stream)
 }
 
 flce_status flce_debug_arm_stall(uint64_t timeout_ns) {
-  if (timeout_ns == 0 || timeout_ns > 10000000000ull) return FLCE_EINVAL;
+  return flce_debug_arm_stall_after(timeout_ns, 0);
+}
+
+flce_status flce_debug_arm_stall_after(uint64_t timeout_ns, int32_t launches) {
+  if (timeout_ns == 0 || timeout_ns > 10000000000ull || launches < 0) return FLCE_EINVAL;
+  g_stall_skip.store(launches);
   g_stall_armed.store(timeout_ns);
   return FLCE_OK;
 }

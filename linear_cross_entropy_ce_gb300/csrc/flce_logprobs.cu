@@ -195,8 +195,9 @@ __global__ void __launch_bounds__(FRONT_THREADS) probs_front_kernel(const FrontA
 // dealt to the block's warps and merged in a fixed order.  Reads 12 bytes per
 // row and part; 32 warps with four parts in flight each, since a block waits
 // for nothing but these loads (1002 parts of 723 rows: 11 us; 58 us with 8
-// warps and one part at a time).  Blocks past the chunk's (first chunk only) write the rows left out:
-// 0 for an ignored token, NaN for a target outside [0, V).
+// warps and one part at a time).  Blocks past the chunk's (last chunk only) write the rows left out:
+// 0 for an ignored token, NaN for a target outside [0, V); and after a pipeline
+// time-out NaN for every other row, those of finished chunks too.
 constexpr int ROWS_WARPS = 32;
 constexpr int ROWS_BATCH = 4;
 
@@ -223,9 +224,10 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) logprob_rows_kernel(const Row
   ptx::grid_dependency_wait();
   if (static_cast<int>(blockIdx.x) >= a.row_blocks) {
     const long long step = static_cast<long long>(gridDim.x - a.row_blocks) * blockDim.x;
-    for (long long i = a.hdr[HDR_NVALID] + static_cast<long long>(blockIdx.x - a.row_blocks) * blockDim.x + threadIdx.x;
+    const long long from = (a.hdr[HDR_STATUS] & STATUS_TIMEOUT) ? 0 : a.hdr[HDR_NVALID];
+    for (long long i = from + static_cast<long long>(blockIdx.x - a.row_blocks) * blockDim.x + threadIdx.x;
          i < a.N; i += step) {
-      const long long row = a.idx[i];
+      const long long row = a.idx[i];   // the scored rows come first
       const float v = a.targets[row] == a.ii ? 0.f : __int_as_float(0x7fc00000);
       a.logp[row] = v;
       a.lse[row] = v;
@@ -289,6 +291,14 @@ __global__ void __launch_bounds__(32 * TOP_WARPS)
   ptx::grid_dependency_wait();
   if (r >= chunk_rows(hdr, c0, C)) return;
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+  if (hdr[HDR_STATUS] & STATUS_TIMEOUT) {   // uniform over the grid
+    if (static_cast<int>(threadIdx.x) < K) {
+      const long long at = static_cast<long long>(idx[c0 + r]) * K + threadIdx.x;
+      top_ids[at] = -1;
+      top_logp[at] = __int_as_float(0x7fc00000);
+    }
+    return;
+  }
   TopK best;
   best.clear();
   for (int p0 = w * 32; p0 < nparts; p0 += TOP_BATCH * TOP_WARPS * 32) {
@@ -661,7 +671,7 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
     }
     if (!chk(gemm_launch(g, m, grid, st, front))) return FLCE_ECUDA;
     ra.c0 = g.c0;
-    if (!chk(launch_dependent(logprob_rows_kernel, ra.row_blocks + (!front && c == 0 ? left_blocks : 0),
+    if (!chk(launch_dependent(logprob_rows_kernel, ra.row_blocks + (!front && c == p.n_chunks - 1 ? left_blocks : 0),
                               32 * ROWS_WARPS, st, ra)))
       return FLCE_ECUDA;
     if (top_k > 0 && !chk(launch_dependent(logprob_top_kernel, g.C, 32 * TOP_WARPS, st, hdr, idx, g.c0, g.C, g.V, p.ldz,

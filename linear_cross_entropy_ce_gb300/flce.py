@@ -70,6 +70,8 @@ def library() -> ctypes.CDLL:
     lib.flce_query_stall.restype = ctypes.c_int
     lib.flce_debug_arm_stall.argtypes = [ctypes.c_uint64]
     lib.flce_debug_arm_stall.restype = ctypes.c_int
+    lib.flce_debug_arm_stall_after.argtypes = [ctypes.c_uint64, i32]
+    lib.flce_debug_arm_stall_after.restype = ctypes.c_int
     lib.flce_status_string.argtypes = [ctypes.c_int]
     lib.flce_status_string.restype = ctypes.c_char_p
     lib.flce_rmsnorm_workspace_bytes.argtypes = [i64, i64, i64, u32]
@@ -769,9 +771,9 @@ def query_stall(workspace: torch.Tensor, stream=None) -> dict:
     return {"site": info[0], "cta_rank": info[1], "block": info[2], "count": info[3]}
 
 
-def debug_arm_stall(timeout_ns: int) -> None:
-    """Test hook: the next GEMM launch withholds one pipeline signal (see flce.h)."""
-    s = library().flce_debug_arm_stall(int(timeout_ns))
+def debug_arm_stall(timeout_ns: int, after: int = 0) -> None:
+    """Test hook: the next GEMM launch, or the one behind ``after`` others, withholds one pipeline signal (see flce.h)."""
+    s = library().flce_debug_arm_stall_after(int(timeout_ns), int(after))
     if s != FLCE_OK:
         raise FlceError(s, "flce_debug_arm_stall")
 
