@@ -444,17 +444,24 @@ def _check_buffer(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous, of shape {tuple(shape)}, on {device}")
 
 
-def _outputs(out, specs, device) -> dict:
-    """The caller's output dict, checked, or new tensors; a spec of None is not produced."""
+def _outputs(out, specs, device):
+    """The caller's output dict (or a new one), checked and with what it lacks,
+    and the tensors that the call writes.  A spec of None is not produced: what
+    the dict holds there stays as it is."""
     o = out if out is not None else {}
     for name, spec in specs.items():
-        if spec is None:
-            o[name] = None
-        elif o.get(name) is None:
-            o[name] = torch.empty(spec[0], dtype=spec[1], device=device)
-        else:
+        if spec is not None and o.get(name) is not None:
             _check_buffer(o[name], name, spec[0], spec[1], device)
-    return o
+    made = {}
+    for name, spec in specs.items():
+        if spec is None:
+            made[name] = None
+            o.setdefault(name, None)
+        else:
+            if o.get(name) is None:
+                o[name] = torch.empty(spec[0], dtype=spec[1], device=device)
+            made[name] = o[name]
+    return o, made
 
 
 def _check_same_device(*tensors):
@@ -479,7 +486,8 @@ def token_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Te
     with ``top_k`` > 0 also ``top_ids`` (int32 [N, top_k]) and ``top_logp`` (fp32),
     best first, equal logits by the lower id.  Rows whose target is
     ``ignore_index`` hold 0 (ids -1); rows whose target lies outside [0, V) hold
-    NaN and set the status word."""
+    NaN and set the status word.  ``out`` may hold outputs to write into; it is
+    returned, and entries that are not asked for stay as they are."""
     N, H, V = _check_inputs(hidden, weight, targets)
     dev = _check_same_device(hidden, weight, targets)
     top_k = int(top_k)
@@ -499,15 +507,16 @@ def token_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Te
                  "entropy": torch.empty(N, dtype=f32, device=dev) if entropy else None,
                  "top_ids": torch.empty((N, top_k), dtype=torch.int32, device=dev) if top_k else None,
                  "top_logp": torch.empty((N, top_k), dtype=f32, device=dev) if top_k else None}
+            made = o
         else:
             row = ((N,), torch.float32)
-            o = _outputs(out, {"logp": row, "lse": row, "entropy": row if entropy else None,
-                               "top_ids": ((N, top_k), torch.int32) if top_k else None,
-                               "top_logp": ((N, top_k), torch.float32) if top_k else None}, dev)
+            o, made = _outputs(out, {"logp": row, "lse": row, "entropy": row if entropy else None,
+                                     "top_ids": ((N, top_k), torch.int32) if top_k else None,
+                                     "top_logp": ((N, top_k), torch.float32) if top_k else None}, dev)
         _ok(library().flce_logprobs(_addr(hidden), _addr(weight), _addr(targets), N, H, V, int(ignore_index),
-                                    float(temperature), top_k, _addr(o["logp"]), _addr(o["entropy"]), _addr(o["lse"]),
-                                    _addr(o["top_ids"]), _addr(o["top_logp"]), _addr(workspace), workspace.numel(), st),
-            "flce_logprobs")
+                                    float(temperature), top_k, _addr(made["logp"]), _addr(made["entropy"]),
+                                    _addr(made["lse"]), _addr(made["top_ids"]), _addr(made["top_logp"]),
+                                    _addr(workspace), workspace.numel(), st), "flce_logprobs")
     o["workspace"] = workspace
     return o
 
@@ -544,12 +553,12 @@ def token_logprobs_bwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torc
             workspace = new_workspace(nb, dev)
         else:
             _check_workspace(workspace, dev)
-        o = _outputs(out, {"grad_hidden": ((N, H), torch.bfloat16) if need_hidden else None,
-                           "grad_weight": ((V, H), grad_weight_dtype) if need_weight else None}, dev)
+        o, made = _outputs(out, {"grad_hidden": ((N, H), torch.bfloat16) if need_hidden else None,
+                                 "grad_weight": ((V, H), grad_weight_dtype) if need_weight else None}, dev)
         _ok(library().flce_logprobs_bwd(_addr(hidden), _addr(weight), _addr(targets), N, H, V, int(ignore_index), flags,
                                         float(temperature), _addr(lse), _addr(entropy), _addr(grad_logp),
-                                        _addr(grad_entropy), _addr(o["grad_hidden"]), _addr(o["grad_weight"]),
-                                        _addr(workspace), workspace.numel(), st), "flce_logprobs_bwd")
+                                        _addr(grad_entropy), _addr(made["grad_hidden"]),
+                                        _addr(made["grad_weight"]), _addr(workspace), workspace.numel(), st), "flce_logprobs_bwd")
     o["workspace"] = workspace
     return o
 
@@ -701,7 +710,7 @@ def embedding_bwd(grad_out: torch.Tensor, ids: torch.Tensor, num_rows: int, scal
             workspace = new_workspace(nb, dev)
         else:
             _check_workspace(workspace, dev)
-        o = _outputs(out, {"grad_weight": ((V, H), grad_weight_dtype)}, dev)
+        o, _ = _outputs(out, {"grad_weight": ((V, H), grad_weight_dtype)}, dev)
         _ok(library().flce_embedding_bwd(_addr(grad_out), _addr(ids), N, H, V, EMBEDDING_DTYPES[grad_out.dtype],
                                          float(scale), -1 if padding_idx is None else int(padding_idx),
                                          FLCE_ACCUMULATE if accumulate else 0, _addr(o["grad_weight"]),
