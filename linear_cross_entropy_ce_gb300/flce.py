@@ -356,6 +356,30 @@ def scale_grads(grad_hidden: torch.Tensor, grad_weight: torch.Tensor, scale: tor
         raise FlceError(s, "flce_scale_grads")
 
 
+def _leaves(ctx):
+    return [node for node, _ in ctx.next_functions if node is not None and type(node).__name__ == "AccumulateGrad"]
+
+
+def _mark_leaves(ctx, device) -> None:
+    """Notes on each leaf's accumulator the stream it was first used on.  The
+    accumulator keeps that stream, and lives as long as any graph of the leaf.
+    (What other libraries' operators made first has no note, or that of the first
+    operator here: autograd does not tell an accumulator's stream.)"""
+    for node in _leaves(ctx):
+        if "flce_stream" not in node.metadata:
+            node.metadata["flce_stream"] = torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _check_capture(ctx) -> None:
+    """Refuses a captured backward whose leaves belong to a living graph of the
+    default stream: autograd would make that stream, which cannot be captured,
+    wait for the capture, and the process would end."""
+    if torch.cuda.is_current_stream_capturing():
+        if any(node.metadata.get("flce_stream") == 0 for node in _leaves(ctx)):
+            raise RuntimeError("backward captured while an eager graph of the same leaves, made on the default "
+                               "stream, is alive: drop its loss and outputs first, or make it on another stream")
+
+
 class _LinearCrossEntropyFn(torch.autograd.Function):
     """Forward computes the loss and both gradients in one library call; the
     backward only scales those gradients by the incoming gradient of the loss."""
@@ -365,10 +389,12 @@ class _LinearCrossEntropyFn(torch.autograd.Function):
         o = fwd_bwd(hidden.contiguous(), weight.contiguous(), targets.contiguous(), ignore_index, reduction)
         ctx.grads = (o["grad_hidden"], o["grad_weight"])
         ctx.n_valid = o["n_valid"]
+        _mark_leaves(ctx, hidden.device)
         return o["loss"].reshape(())
 
     @staticmethod
     def backward(ctx, grad_loss):
+        _check_capture(ctx)
         gh, gw = ctx.grads
         ctx.grads = None
         scale_grads(gh, gw, grad_loss.detach().reshape(1).to(torch.float32))
@@ -563,28 +589,6 @@ def token_logprobs_bwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torc
     return o
 
 
-def _leaves(ctx):
-    return [node for node, _ in ctx.next_functions if node is not None and type(node).__name__ == "AccumulateGrad"]
-
-
-def _mark_leaves(ctx, device) -> None:
-    """Notes on each leaf's accumulator the stream it was first used on.  The
-    accumulator keeps that stream, and lives as long as any graph of the leaf."""
-    for node in _leaves(ctx):
-        if "flce_stream" not in node.metadata:
-            node.metadata["flce_stream"] = torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def _check_capture(ctx) -> None:
-    """Refuses a captured backward whose leaves belong to a living graph of the
-    default stream: autograd would make that stream, which cannot be captured,
-    wait for the capture, and the process would end."""
-    if torch.cuda.is_current_stream_capturing():
-        if any(node.metadata.get("flce_stream") == 0 for node in _leaves(ctx)):
-            raise RuntimeError("backward captured while an eager graph of the same leaves, made on the default "
-                               "stream, is alive: drop its loss and outputs first, or make it on another stream")
-
-
 class _LinearLogProbsFn(torch.autograd.Function):
     """The backward recomputes the logits chunk by chunk from the saved log-sum-exp."""
 
@@ -619,7 +623,9 @@ def linear_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.T
     """``(logp, entropy)`` of the given tokens at the LM head, fp32 [N] each, with
     autograd support: the head of a policy-gradient or preference loss.  Forward
     and backward may be captured into one CUDA graph; an eager graph of the same
-    leaves, made on the default stream and still alive, is refused there."""
+    leaves, made by this module on the default stream and still alive, is refused
+    there.  (One made by other operators is not seen, and autograd ends the
+    process: drop it before the capture.)"""
     return _LinearLogProbsFn.apply(hidden, weight, targets, ignore_index, temperature)
 
 
