@@ -153,6 +153,14 @@ def _check_inputs(hidden, weight, targets):
     return N, H, V
 
 
+def _ignored(ignore_index) -> int:
+    """The ignore index as the library takes it: what does not fit 32 bits would become some other token's id."""
+    i = int(ignore_index)
+    if not -2 ** 31 <= i < 2 ** 31:
+        raise ValueError("ignore_index must fit in 32 bits, as the targets do")
+    return i
+
+
 def _flags(reduction: str, grad_weight_dtype=torch.float32) -> int:
     if grad_weight_dtype not in (torch.float32, torch.bfloat16):
         raise TypeError("grad_weight_dtype must be torch.float32 or torch.bfloat16")
@@ -211,7 +219,7 @@ def fwd_bwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, i
         o["row_loss"] = torch.empty(N, dtype=torch.float32, device=dev) if row_loss else None
     if o["grad_weight"].dtype != grad_weight_dtype:
         raise TypeError("out['grad_weight'] does not have grad_weight_dtype")
-    s = library().flce_fwd_bwd(_ptr(hidden), _ptr(weight), _ptr(targets), N, H, V, int(ignore_index),
+    s = library().flce_fwd_bwd(_ptr(hidden), _ptr(weight), _ptr(targets), N, H, V, _ignored(ignore_index),
                                flags, _ptr(o["loss"]), _ptr(o["n_valid"]), _ptr(o.get("row_loss")),
                                _ptr(o["grad_hidden"]), _ptr(o["grad_weight"]), _ptr(workspace),
                                workspace.numel(), _stream(stream))
@@ -250,7 +258,7 @@ def rmsnorm_fwd_bwd(hidden: torch.Tensor, gain: torch.Tensor, weight: torch.Tens
     if o["grad_weight"].dtype != grad_weight_dtype:
         raise TypeError("out['grad_weight'] does not have grad_weight_dtype")
     s = library().flce_rmsnorm_fwd_bwd(_ptr(hidden), _ptr(gain), float(eps), _ptr(weight), _ptr(targets), N, H, V,
-                                       int(ignore_index), flags, _ptr(o["loss"]), _ptr(o["n_valid"]),
+                                       _ignored(ignore_index), flags, _ptr(o["loss"]), _ptr(o["n_valid"]),
                                        _ptr(o.get("row_loss")), _ptr(o["grad_hidden"]), _ptr(o["grad_gain"]),
                                        _ptr(o["grad_weight"]), _ptr(workspace), workspace.numel(), _stream(stream))
     if s != FLCE_OK:
@@ -272,7 +280,7 @@ def loss(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, igno
         o["loss"] = torch.empty(1, dtype=torch.float32, device=dev)
         o["n_valid"] = torch.empty(1, dtype=torch.int32, device=dev)
         o["row_loss"] = torch.empty(N, dtype=torch.float32, device=dev) if row_loss else None
-    s = library().flce_loss(_ptr(hidden), _ptr(weight), _ptr(targets), N, H, V, int(ignore_index),
+    s = library().flce_loss(_ptr(hidden), _ptr(weight), _ptr(targets), N, H, V, _ignored(ignore_index),
                             REDUCE[reduction], _ptr(o["loss"]), _ptr(o["n_valid"]), _ptr(o.get("row_loss")),
                             _ptr(workspace), workspace.numel(), _stream(stream))
     if s != FLCE_OK:
@@ -301,7 +309,7 @@ def vocab_shard_stats(hidden, weight_shard, targets, v0: int, V_total: int, igno
     o = {k: torch.empty(N, dtype=torch.float32, device=dev) for k in ("row_max", "row_sumexp", "row_target_logit")}
     o["n_valid"] = torch.empty(1, dtype=torch.int32, device=dev)
     _ok(library().flce_vocab_shard_stats(_ptr(hidden), _ptr(weight_shard), _ptr(targets), N, H, Vs, v0, V_total,
-                                         int(ignore_index), _ptr(o["row_max"]), _ptr(o["row_sumexp"]),
+                                         _ignored(ignore_index), _ptr(o["row_max"]), _ptr(o["row_sumexp"]),
                                          _ptr(o["row_target_logit"]), _ptr(o["n_valid"]), _ptr(workspace),
                                          workspace.numel(), _stream(stream)), "flce_vocab_shard_stats")
     o["workspace"] = workspace
@@ -322,7 +330,7 @@ def vocab_finish(row_max, row_sumexp, row_target_logit, targets, ignore_index: i
          "loss": torch.empty(1, dtype=torch.float32, device=dev),
          "n_valid": torch.empty(1, dtype=torch.int32, device=dev)}
     _ok(library().flce_vocab_finish(_ptr(row_max), _ptr(row_sumexp), _ptr(row_target_logit), _ptr(targets), N,
-                                    int(ignore_index), REDUCE[reduction], _ptr(o["lse"]), _ptr(o["row_loss"]),
+                                    _ignored(ignore_index), REDUCE[reduction], _ptr(o["lse"]), _ptr(o["row_loss"]),
                                     _ptr(o["loss"]), _ptr(o["n_valid"]), _stream(stream)), "flce_vocab_finish")
     return o
 
@@ -337,7 +345,7 @@ def vocab_shard_bwd(hidden, weight_shard, targets, lse, v0: int, V_total: int, i
     o = {"grad_hidden_partial": torch.empty((N, H), dtype=torch.float32, device=dev),
          "grad_weight": torch.empty((Vs, H), dtype=torch.float32, device=dev)}
     _ok(library().flce_vocab_shard_bwd(_ptr(hidden), _ptr(weight_shard), _ptr(targets), N, H, Vs, v0, V_total,
-                                       int(ignore_index), REDUCE[reduction], _ptr(lse),
+                                       _ignored(ignore_index), REDUCE[reduction], _ptr(lse),
                                        _ptr(o["grad_hidden_partial"]), _ptr(o["grad_weight"]), _ptr(workspace),
                                        workspace.numel(), _stream(stream)), "flce_vocab_shard_bwd")
     o["workspace"] = workspace
@@ -539,7 +547,7 @@ def token_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Te
             o, made = _outputs(out, {"logp": row, "lse": row, "entropy": row if entropy else None,
                                      "top_ids": ((N, top_k), torch.int32) if top_k else None,
                                      "top_logp": ((N, top_k), torch.float32) if top_k else None}, dev)
-        _ok(library().flce_logprobs(_addr(hidden), _addr(weight), _addr(targets), N, H, V, int(ignore_index),
+        _ok(library().flce_logprobs(_addr(hidden), _addr(weight), _addr(targets), N, H, V, _ignored(ignore_index),
                                     float(temperature), top_k, _addr(made["logp"]), _addr(made["entropy"]),
                                     _addr(made["lse"]), _addr(made["top_ids"]), _addr(made["top_logp"]),
                                     _addr(workspace), workspace.numel(), st), "flce_logprobs")
@@ -581,7 +589,7 @@ def token_logprobs_bwd(hidden: torch.Tensor, weight: torch.Tensor, targets: torc
             _check_workspace(workspace, dev)
         o, made = _outputs(out, {"grad_hidden": ((N, H), torch.bfloat16) if need_hidden else None,
                                  "grad_weight": ((V, H), grad_weight_dtype) if need_weight else None}, dev)
-        _ok(library().flce_logprobs_bwd(_addr(hidden), _addr(weight), _addr(targets), N, H, V, int(ignore_index), flags,
+        _ok(library().flce_logprobs_bwd(_addr(hidden), _addr(weight), _addr(targets), N, H, V, _ignored(ignore_index), flags,
                                         float(temperature), _addr(lse), _addr(entropy), _addr(grad_logp),
                                         _addr(grad_entropy), _addr(made["grad_hidden"]),
                                         _addr(made["grad_weight"]), _addr(workspace), workspace.numel(), st), "flce_logprobs_bwd")
