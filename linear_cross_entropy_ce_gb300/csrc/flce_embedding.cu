@@ -237,13 +237,40 @@ __device__ __forceinline__ int block_exclusive_scan(int x, int* scratch) {
   return scratch[w] + inc - x;
 }
 
+// Counts of many tiles: block r turns the counts of a range of tiles into the
+// sums over the range's tiles before each, and leaves the range's total.  A
+// scatter block then reads one row per range, not one per tile, which would
+// make the reads grow with the square of the tokens.  One more launch per digit
+// for that (gradient at H = 8, V = 1000, without and with it: 2^19 tokens 103
+// and 108 us, 2^20, 128 tiles, 155 and 156, 2^22 605 and 542, 2^26 25.3 and 9.3 ms).
+constexpr int SCAN_TILES = 128;    // more tiles than this
+constexpr int SCAN_RANGES = 64;    // their ranges
+constexpr int SCAN_BATCH = 16;     // rows in flight
+__global__ void __launch_bounds__(SORT_THREADS) sort_ranges_kernel(int* counts, int tiles, int each, int* range_sums) {
+  ptx::grid_launch_dependents();
+  ptx::grid_dependency_wait();
+  const int t0 = blockIdx.x * each, t1 = min(tiles, t0 + each);
+  int sum = 0;
+  for (int t = t0; t < t1; t += SCAN_BATCH) {
+    int c[SCAN_BATCH];
+#pragma unroll
+    for (int k = 0; k < SCAN_BATCH; ++k) c[k] = t + k < t1 ? counts[(t + k) * SORT_BINS + threadIdx.x] : 0;
+#pragma unroll
+    for (int k = 0; k < SCAN_BATCH; ++k) {
+      if (t + k < t1) counts[(t + k) * SORT_BINS + threadIdx.x] = sum;
+      sum += c[k];
+    }
+  }
+  range_sums[blockIdx.x * SORT_BINS + threadIdx.x] = sum;
+}
+
 // Every item moves to (items of smaller digits) + (items of its digit in
 // earlier tiles) + (its rank among the tile's items of its digit).  A warp
 // ranks its 32 x ITEMS consecutive items in order, so the sort is stable.
 template <bool FIRST, int ITEMS>
 __global__ void __launch_bounds__(SORT_THREADS)
     sort_scatter_kernel(const int* ids, const int2* items, int N, int V, int padding, int shift, int bits,
-                        const int* counts, int tiles, int2* out) {
+                        const int* counts, int tiles, const int* range_sums, int each, int2* out) {
   __shared__ int cnt[SORT_WARPS][SORT_BINS];
   __shared__ int scratch[32];
   const int tid = threadIdx.x, lane = tid % 32, w = tid / 32;
@@ -263,12 +290,16 @@ __global__ void __launch_bounds__(SORT_THREADS)
   }
   // thread d: total of digit d and its items in earlier tiles
   int total = 0, earlier = 0;
+  const int* rows = each ? range_sums : counts;
+  const int n_rows = each ? (tiles + each - 1) / each : tiles;
+  const int my_row = each ? static_cast<int>(blockIdx.x) / each : static_cast<int>(blockIdx.x);
 #pragma unroll 16
-  for (int b = 0; b < tiles; ++b) {
-    const int c = counts[b * SORT_BINS + tid];
+  for (int b = 0; b < n_rows; ++b) {
+    const int c = rows[b * SORT_BINS + tid];
     total += c;
-    earlier += b < static_cast<int>(blockIdx.x) ? c : 0;
+    earlier += b < my_row ? c : 0;
   }
+  if (each) earlier += counts[blockIdx.x * SORT_BINS + tid];   // of the tiles before this one in its range
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {
     const bool ok = base + k * 32 + lane < N;
@@ -708,7 +739,8 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) embedding_join_kernel(const S
 // ---------------------------------------------------------------------------
 struct EmbPlan {
   int tiles = 0, passes = 0, bits = 0, chunk = 0, n_chunks = 0;
-  size_t o_items[2] = {0, 0}, o_cnt = 0, o_bad = 0, o_part = 0, total = 0;
+  int range_tiles = 0;   // tiles of a range of counts (0: the counts are few)
+  size_t o_items[2] = {0, 0}, o_cnt = 0, o_range = 0, o_bad = 0, o_part = 0, total = 0;
 };
 
 EmbPlan emb_plan(long long N, long long H, long long V) {
@@ -718,6 +750,7 @@ EmbPlan emb_plan(long long N, long long H, long long V) {
   p.passes = static_cast<int>(cdiv(key_bits, SORT_MAX_BITS));
   p.bits = static_cast<int>(cdiv(key_bits, p.passes));
   p.tiles = N <= CS_MAX ? CS_BLOCKS : static_cast<int>(cdiv(N, SORT_THREADS * (N <= SORT_LARGE ? SORT_ITEMS_SMALL : SORT_ITEMS_LARGE)));
+  if (p.tiles > SCAN_TILES) p.range_tiles = static_cast<int>(cdiv(p.tiles, SCAN_RANGES));
   p.chunk = static_cast<int>(cdiv(std::max<long long>(CHUNK, cdiv(N, MAX_CHUNKS)), 32) * 32);
   while (p.chunk > MIN_CHUNK && cdiv(N, p.chunk) * cdiv(H, COLS) < 8 * 152) p.chunk /= 2;
   p.n_chunks = static_cast<int>(cdiv(N, p.chunk));
@@ -729,6 +762,7 @@ EmbPlan emb_plan(long long N, long long H, long long V) {
   };
   for (int k = 0; k < 2; ++k) p.o_items[k] = take(size_t(N) * sizeof(int2));
   p.o_cnt = take(size_t(p.tiles) * SORT_BINS * 4);
+  if (p.range_tiles) p.o_range = take(size_t(SCAN_RANGES) * SORT_BINS * 4);
   p.o_bad = take(size_t(p.tiles) * 4);
   p.o_part = take(size_t(p.n_chunks) * 2 * H * 4);
   p.total = off;
@@ -740,8 +774,8 @@ bool emb_sizes_ok(long long N, long long H, long long V) { return sizes_ok(N, H,
 struct SortPass {
   const int* ids;
   const int2* items;
-  int N, V, padding, shift, bits, tiles;
-  int *bad, *counts;
+  int N, V, padding, shift, bits, tiles, range_tiles;
+  int *bad, *counts, *range_sums;
   int2* out;
 };
 
@@ -757,8 +791,13 @@ cudaError_t sort_pass(const SortPass& s, cudaStream_t st) {
                          s.padding, s.bad, s.shift, s.bits, s.counts);
   }
   if (e != cudaSuccess) return e;
+  if (s.range_tiles) {
+    e = launch_dependent(sort_ranges_kernel, static_cast<unsigned>(cdiv(s.tiles, s.range_tiles)), SORT_THREADS, st,
+                         s.counts, s.tiles, s.range_tiles, s.range_sums);
+    if (e != cudaSuccess) return e;
+  }
   return launch_dependent(sort_scatter_kernel<FIRST, ITEMS>, s.tiles, SORT_THREADS, st, s.ids, s.items, s.N, s.V,
-                          s.padding, s.shift, s.bits, s.counts, s.tiles, s.out);
+                          s.padding, s.shift, s.bits, s.counts, s.tiles, s.range_sums, s.range_tiles, s.out);
 }
 
 template <int ITEMS>
@@ -838,11 +877,12 @@ flce_status flce_embedding_bwd(const void* grad_out, const int32_t* ids, int64_t
   int* hdr = at<int>(workspace, 0);
   int2* items[2] = {at<int2>(workspace, p.o_items[0]), at<int2>(workspace, p.o_items[1])};
   int* cnt = at<int>(workspace, p.o_cnt);
+  int* ranges = at<int>(workspace, p.o_range);
   const int n = static_cast<int>(N), v = static_cast<int>(V);
 
   int* bad = at<int>(workspace, p.o_bad);
 
-  count_launches(2 + (N <= CS_MAX ? 1 : 2 * p.passes));
+  count_launches(2 + (N <= CS_MAX ? 1 : (p.range_tiles ? 3 : 2) * p.passes));
   if (N <= CS_MAX) {
     const ClusterSort s = {ids, n, v, padding_idx, p.passes, p.bits, bad, items[0], items[1]};
     const long long each = CS_BLOCKS * CS_THREADS;
@@ -850,8 +890,8 @@ flce_status flce_embedding_bwd(const void* grad_out, const int32_t* ids, int64_t
     if (e != cudaSuccess) return FLCE_ECUDA;
   }
   for (int k = 0; N > CS_MAX && k < p.passes; ++k) {
-    const SortPass s = {ids, items[(k + 1) & 1], n, v, padding_idx, k * p.bits, p.bits, p.tiles, bad, cnt,
-                        items[k & 1]};
+    const SortPass s = {ids, items[(k + 1) & 1], n, v, padding_idx, k * p.bits, p.bits, p.tiles, p.range_tiles, bad,
+                        cnt, ranges, items[k & 1]};
     const bool large = N > SORT_LARGE;
     const cudaError_t e =
         k == 0 ? (large ? sort_pass<true, SORT_ITEMS_LARGE>(s, st) : sort_pass<true, SORT_ITEMS_SMALL>(s, st))
