@@ -90,7 +90,7 @@ namespace {
 // ---------------------------------------------------------------------------
 struct Plan {
   long long N = 0, H = 0, V = 0, C = 0, ldz = 0, n_chunks = 0;
-  int nvt = 0, nparts = 0, splits = 1, kb_per_split = 0;
+  int nvt = 0, nparts = 0, splits = 1, kb_per_split = 0, tile_counters = 2;
   long long n_counters = 0, flags_per_chunk = 0;
   bool fwd_only = false, norm = false, gw32 = false, probs = false, slabs = false;
   size_t o_idx = 0, o_rl = 0, o_cnt = 0, o_xc = 0, o_tc = 0, o_zt = 0, o_part = 0, o_z = 0, o_dx = 0, o_rinv = 0,
@@ -121,7 +121,8 @@ Plan layout(long long N, long long H, long long V, long long C, int S, bool fwd_
   p.splits = static_cast<int>(cdiv(kbt, p.kb_per_split));
   p.slabs = slabs && p.splits > 1;
   p.flags_per_chunk = p.splits > 1 && !p.slabs ? 4 * cdiv(C, PAIR_M) * cdiv(H, BN) : 0;   // (tile, CTA, warpgroup)
-  p.n_counters = p.n_chunks * (2 + p.flags_per_chunk);   // tile counters, then split flags
+  p.tile_counters = probs ? 1 : 2;   // MODE_DZ deals its tiles without one
+  p.n_counters = p.n_chunks * (p.tile_counters + p.flags_per_chunk);   // tile counters, then split flags
   size_t off = al256(HDR_WORDS * sizeof(int));
   p.o_idx = off;  off += al256(size_t(N) * 4);
   p.o_rl = off;   off += al256(size_t(N) * 4);
@@ -592,9 +593,9 @@ flce_status run(const Job& j) {
                                   tc, v0, g.V, st))) {
       return FLCE_ECUDA;
     }
-    int* sync = counters + c * (2 + p.flags_per_chunk);
+    int* sync = counters + c * (p.tile_counters + p.flags_per_chunk);
     g.mode = probs ? MODE_DZ : MODE_LOGITS;   // MODE_DZ leaves the finished dz in z
-    g.counter = sync;
+    g.counter = probs ? nullptr : sync;
     if (!chk(gemm_launch(g, fm, grid_logits, st, front))) return FLCE_ECUDA;
     if (stats) {
       if (!chk(launch_shard_stats(hdr, idx, c0, g.C, p.nparts, part, zt, tc, j.row_max, j.row_sumexp, j.row_zt,
@@ -607,8 +608,8 @@ flce_status run(const Job& j) {
       return FLCE_ECUDA;
     if (fwd_only) continue;
     g.mode = MODE_BWD;
-    g.counter = sync + 1;
-    g.flags = sync + 2;
+    g.counter = sync + p.tile_counters - 1;
+    g.flags = sync + p.tile_counters;
     g.accumulate = c > 0 ? 1 : 0;
     g.first_chunk = c == 0 ? 1 : 0;
     if (!chk(gemm_launch(g, bm, grid_bwd, st, probs))) return FLCE_ECUDA;

@@ -844,7 +844,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         // the read), since a release would wait for this thread's TMA loads
         ptx::mbar_arrive_remote_relaxed(ptx::map_to_rank(&ctl->sempty[sslot], 0));
       }
-      if (++sslot == SCHED_SLOTS) { sslot = 0; sphase ^= 1u; }
+      if (!PROBS && ++sslot == SCHED_SLOTS) { sslot = 0; sphase ^= 1u; }
       if (u < 0) break;
       const Unit t = decode_unit<PROBS>(a, s, u);
       if (!PROBS && lead && t.kb1 - t.kb0 <= SHORT_TILE_KB) next = atomicAdd(a.counter, 1);
@@ -895,7 +895,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         u = ctl->sunit[sslot];
         ptx::mbar_arrive(&ctl->sempty[sslot]);
       }
-      if (++sslot == SCHED_SLOTS) { sslot = 0; sphase ^= 1u; }
+      if (!PROBS && ++sslot == SCHED_SLOTS) { sslot = 0; sphase ^= 1u; }
       if (u < 0) break;
       const Unit t = decode_unit<PROBS>(a, s, u);
       const int a_mn = t.kind == U_DW ? 1 : 0;
@@ -965,7 +965,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         }
         u = __shfl_sync(0xffffffffu, u, 0);
       }
-      if (++sslot == SCHED_SLOTS) { sslot = 0; sphase ^= 1u; }
+      if (!PROBS && ++sslot == SCHED_SLOTS) { sslot = 0; sphase ^= 1u; }
       if (u < 0) break;
       if ((seq++ & 1u) != static_cast<uint32_t>(set)) continue;   // the other set's tile
       const Unit t = decode_unit<PROBS>(a, s, u);

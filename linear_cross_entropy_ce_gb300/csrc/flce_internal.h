@@ -56,7 +56,7 @@ struct GemmArgs {
   int mode;
   const int* hdr;       // workspace header (n_valid lives in HDR_NVALID)
   int* status;          // workspace header word HDR_STATUS
-  int* counter;         // dynamic tile counter of this launch (zero before it)
+  int* counter;         // LOGITS, BWD: dynamic tile counter of this launch (zero before it)
   long long c0;         // first compacted row of this chunk
   int C;                // chunk capacity (rows)
   int H, V;

@@ -90,7 +90,7 @@ __global__ void clear_bounds_kernel(uint32_t* bound, uint32_t* group_max, int st
 // Everything before the first GEMM of a call of one chunk, in one launch: the
 // valid tokens' rows gathered into the tile source in order, their targets (and
 // for the backward the constants of MODE_DZ), the outputs of the tokens left
-// out, the header and the GEMMs' counters.  Every block counts the valid
+// out, the header and the backward GEMM's counter and flags.  Every block counts the valid
 // targets before its own tokens itself (16384 targets are 64 KB from L2), which
 // costs less than a launch of its own for the scan: 4096 tokens of 512 take 5.7
 // us, against 16 us for the three launches it replaces.
@@ -397,7 +397,7 @@ __global__ void mark_failed_kernel(const int* hdr, uint16_t* grad_hidden, float*
 struct LpPlan {
   long long C = 0, n_chunks = 0, ldz = 0;
   int nvt = 0, nparts = 0;
-  size_t o_idx = 0, o_cnt = 0, o_xc = 0, o_tc = 0, o_zt = 0, o_ml = 0, o_stats = 0, o_bound = 0, o_group = 0,
+  size_t o_idx = 0, o_xc = 0, o_tc = 0, o_zt = 0, o_ml = 0, o_stats = 0, o_bound = 0, o_group = 0,
          o_zf = 0, total = 0;
   int group_stride = 0;
 };
@@ -416,7 +416,6 @@ LpPlan lp_layout(long long N, long long H, long long V, long long C, int K) {
     return o;
   };
   p.o_idx = take(size_t(N) * 4);
-  p.o_cnt = take(size_t(p.n_chunks) * 4);
   p.o_xc = take(size_t(C) * H * 2);
   p.o_tc = take(size_t(C) * 4);
   p.o_zt = take(size_t(C) * 4);
@@ -594,7 +593,6 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
   if (!lp_plan(N, H, V, top_k, workspace_bytes, &p)) return FLCE_EWORKSPACE;
 
   int* idx = at<int>(workspace, p.o_idx);
-  int* counters = at<int>(workspace, p.o_cnt);
   uint16_t* xc = at<uint16_t>(workspace, p.o_xc);
   int* tc = at<int>(workspace, p.o_tc);
   float* zt = at<float>(workspace, p.o_zt);
@@ -651,17 +649,15 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
     f.hidden = static_cast<const uint16_t*>(hidden);
     f.targets = targets;
     f.N = static_cast<int>(N); f.H = g.H; f.V = g.V; f.ii = ignore_index; f.C = g.C; f.K = top_k;
-    f.hdr = hdr; f.idx = idx; f.tc = tc; f.xc = xc; f.counters = counters; f.n_counters = 1;
+    f.hdr = hdr; f.idx = idx; f.tc = tc; f.xc = xc;
     f.bound = g.bound; f.group_max = g.group_max; f.group_stride = g.group_stride;
     f.logp = logp; f.lse = lse; f.entropy = entropy; f.top_ids = top_ids; f.top_logp = top_logp;
     if (!chk(launch_probs_front(f, st))) return FLCE_ECUDA;
-  } else if (!chk(launch_prep(targets, N, static_cast<int>(V), ignore_index, hdr, idx, nullptr, counters, p.n_chunks,
-                              st))) {
+  } else if (!chk(launch_prep(targets, N, static_cast<int>(V), ignore_index, hdr, idx, nullptr, nullptr, 0, st))) {
     return FLCE_ECUDA;
   }
   for (long long c = 0; c < p.n_chunks; ++c) {
     g.c0 = c * p.C;
-    g.counter = counters + c;
     if (!front && !chk(launch_gather(static_cast<const uint16_t*>(hidden), targets, hdr, idx, g.c0, g.C, g.H, xc, tc, 0,
                                      g.V, st)))
       return FLCE_ECUDA;
