@@ -740,8 +740,9 @@ class _EmbeddingFn(torch.autograd.Function):
         ids = ids.contiguous()
         ctx.save_for_backward(ids)
         ctx.args = (weight.shape[0], weight.dtype, scale, padding_idx)
+        out = embedding_fwd(weight.contiguous(), ids, scale)
         _mark_leaves(ctx, weight.device)
-        return embedding_fwd(weight.contiguous(), ids, scale)
+        return out
 
     @staticmethod
     @torch.autograd.function.once_differentiable

@@ -41,3 +41,17 @@ def test_workspace_sizes(flce):  # noqa: F811
     f = flce.library().flce_embedding_bwd_workspace_bytes
     assert f(0, 64, 32) == 0 and f(16, 63, 32) == 0 and f(1 << 31, 64, 32) == 0
     assert 0 < f(1, 8, 1) < f(100000, 512, 16000) <= 8 * 512 * 100000
+
+
+def test_python_refusals_of_leaves(flce):  # noqa: F811
+    """A table that is not on a GPU is named as such, whether or not a gradient is wanted."""
+    torch = pytest.importorskip("torch")
+    ids = torch.zeros(4, dtype=torch.int32)
+    for grad in (False, True):
+        table = torch.zeros(32, 64, dtype=torch.bfloat16, requires_grad=grad)
+        with pytest.raises(ValueError, match="CUDA"):
+            flce.embedding(ids, table)
+        with pytest.raises(ValueError, match="CUDA"):
+            flce.ScaledEmbedding(table)(ids)
+        with pytest.raises(ValueError, match="CUDA"):
+            flce.linear_logprobs(table[:4], table, ids)
