@@ -540,6 +540,7 @@ flce_status run(const Job& j) {
   DzRow* rowc = probs ? at<DzRow>(ws, p.o_rowc) : nullptr;
   g.rowc = rowc;
   if (probs) g.c2 = 1.4426950408889634f / j.temperature;
+  g.seg_kb = segment_blocks(H);   // the same logits as the forward's
 
   // persistent grids: CTA pairs, no more than fit on the device at once
   const long long mt = cdiv(p.C, PAIR_M), ht = cdiv(H, BN);

@@ -30,6 +30,7 @@
 //                alternatives, the fp32 logits.
 //   MODE_DZ      z = Xc W^T once more, turned in registers into the gradient
 //                of the logits (bf16) that MODE_BWD consumes.
+//                Both take long sums over H in segments, see below.
 //
 // Each tile is 256 x 256 and is computed by a CTA pair (a cluster of two CTAs
 // on two SMs) with tcgen05.mma.cta_group::2: each CTA stages its 128 rows of
@@ -43,7 +44,7 @@
 // warp 1 allocates TMEM and, in CTA 0, one lane issues the MMAs for the pair,
 // and warps 2-17 are the epilogue: two sets of two warpgroups, set e draining
 // TMEM accumulator e (double buffered, 2 x 256 columns), one 128-column half
-// per warpgroup, so the epilogues of two consecutive tiles run at once and
+// per warpgroup (with segments all four read each accumulator), so the epilogues of two consecutive tiles run at once and
 // both overlap the next tile's main loop.  Every wait is bounded: on time-out
 // a CTA raises an abort flag, lets copies in flight land, waits for its MMAs,
 // frees TMEM and returns, and the workspace status word records
@@ -352,12 +353,90 @@ __device__ __forceinline__ void store_f32x32(float* dst, const float (&v)[32]) {
                       __float_as_uint(v[k + 6]), __float_as_uint(v[k + 7]));
 }
 
-// Bound by the tensor cores from H = 2048 up (4096 tokens at 2048 x 32000: 282
-// us, 1.90 PFLOP/s); at 8 K blocks a tile takes 2.9 us for 2.2 us of MMAs.
-// Statistics of one row and part.  With c2 = log2(e) / temperature and
-// d = (z - max) c2 <= 0: sum 2^d and sum d 2^d, from which the row kernel
-// forms log-sum-exp and entropy.  The stats array is part-major, so a warp's
-// 32 rows store 128 contiguous bytes per value.
+// Statistics of 32 logits of one row.  With c2 = log2(e) / temperature and
+// d = (z - max) c2 <= 0: the max, sum 2^d and sum d 2^d, from which the row
+// kernel forms log-sum-exp and entropy.  Three instructions an element, two of
+// them for pairs: the issue slots are shared with the warps that feed the MMAs,
+// and six an element slowed those (tiles of 8 K blocks: 3.6 us each, without the
+// arithmetic 2.7).
+__device__ __forceinline__ Stat stats32(const float (&v)[32], float c2) {
+  float mx = v[0];
+#pragma unroll
+  for (int k = 1; k + 1 < 32; k += 2) mx = ptx::max3(mx, v[k], v[k + 1]);
+  mx = fmaxf(mx, v[31]);
+  const bool none = !(mx > -INFINITY);          // nothing but -inf (or NaN, which the sums keep)
+  const float mb = none ? 0.f : -mx * c2;
+  const uint64_t cc = ptx::pack2(c2, c2), bb = ptx::pack2(mb, mb);
+  uint64_t s2 = 0, d2 = 0;                      // two zeros each
+#pragma unroll
+  for (int k = 0; k < 32; k += 2) {
+    const uint64_t d = ptx::fma2(ptx::pack2(v[k], v[k + 1]), cc, bb);
+    const float2 x = ptx::unpack2(d);
+    const uint64_t e = ptx::pack2(ptx::ex2(x.x), ptx::ex2(x.y));
+    s2 = ptx::add2(s2, e);
+    d2 = ptx::fma2(d, e, d2);
+  }
+  float sum = ptx::unpack2(s2).x + ptx::unpack2(s2).y;
+  float dsum = ptx::unpack2(d2).x + ptx::unpack2(d2).y;
+  if (dsum != dsum && sum == sum) {             // a logit of -inf: 0 times -inf; it adds nothing
+    dsum = 0.f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float d = fmaf(v[k], c2, mb);
+      dsum = fmaf(fmaxf(d, -1e30f), ptx::ex2(d), dsum);
+    }
+  }
+  // mb is rounded: every d is too large by rho = mx c2 + mb (exact in the
+  // fused multiply-add), which matters where the logits are large
+  const float rho = none ? 0.f : fmaf(mx, c2, mb);
+  const float back = ptx::ex2(-rho);
+  return Stat{mx, back * sum, back * fmaf(-rho, sum, dsum)};
+}
+
+// Part-major: a warp's 32 rows store 128 contiguous bytes per value.
+__device__ __forceinline__ void store_stats(const GemmArgs& a, int part, int grow, const Stat& st) {
+  const size_t np = static_cast<size_t>(a.nparts) * a.C;
+  float* p = a.stats + static_cast<size_t>(part) * a.C + grow;
+  p[0] = st.m;
+  p[np] = st.s;
+  p[2 * np] = st.d;
+}
+
+// Top alternatives: the logits of a part are kept unless K other parts of the
+// row are known to have a larger max.  The parts are dealt to K groups; the
+// least of the groups' maxima is such a bound, and only a part above it can
+// raise it.
+__device__ __forceinline__ void raise_bound(const GemmArgs& a, int part, int grow, uint32_t key, uint32_t bound) {
+  uint32_t* g = a.group_max + static_cast<size_t>(grow) * a.group_stride;
+  atomicMax(g + part % a.K, key);
+  uint32_t least = 0xffffffffu;
+  for (int k = 0; k < a.K; k += 4) {   // entries behind the K-th hold the largest integer
+    const uint4 q = __ldcg(reinterpret_cast<const uint4*>(g + k));
+    least = min(least, min(min(q.x, q.y), min(q.z, q.w)));
+  }
+  if (least > bound) atomicMax(a.bound + grow, least);
+}
+
+// The row's logit of target column tl - j0 if it is among these 32.
+__device__ __forceinline__ void pick_target(const float (&v)[32], int tl, int j0, float& zt) {
+  if (static_cast<unsigned>(tl - j0) < 32u) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (j0 + k == tl) zt = v[k];
+  }
+}
+
+__device__ __forceinline__ void blank_tail(float (&v)[32], int j0, int ncol, float with) {
+  if (j0 + 32 > ncol) {   // the block straddles the end of the vocabulary
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (j0 + k >= ncol) v[k] = with;
+  }
+}
+
+// Statistics of one row and part.  Bound by the tensor cores from H = 2048 up
+// (4096 tokens at 2048 x 32000: 282 us, 1.90 PFLOP/s); at 8 K blocks a tile
+// takes 2.9 us for 2.2 us of MMAs.
 __device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, const Unit& t, int row0, int col0,
                                           uint32_t tbase, int r) {
   const int grow = row0 + r;
@@ -376,78 +455,20 @@ __device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, con
     if (j * 32 >= ncol) break;                    // uniform
     float v[32];
     ptx::tmem_ld32(tbase + j * 32, v);
-    if (static_cast<unsigned>(tl - j * 32) < 32u) {
-#pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (j * 32 + k == tl) ztv = v[k];
-    }
+    pick_target(v, tl, j * 32, ztv);
     if (all) store_f32x32(zrow + j * 32, v);
-    if (j * 32 + 32 > ncol) {                     // the block straddles the end of the vocabulary
-#pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (j * 32 + k >= ncol) v[k] = -INFINITY;
-    }
-    // Three instructions an element, two of them for pairs: the issue slots are
-    // shared with the warps that feed the MMAs, and six an element slowed those
-    // (tiles of 8 K blocks: 3.6 us each, without the arithmetic 2.7).
-    float mx = v[0];
-#pragma unroll
-    for (int k = 1; k + 1 < 32; k += 2) mx = ptx::max3(mx, v[k], v[k + 1]);
-    mx = fmaxf(mx, v[31]);
-    const bool none = !(mx > -INFINITY);          // nothing but -inf (or NaN, which the sums keep)
-    const float mb = none ? 0.f : -mx * a.c2;
-    const uint64_t cc = ptx::pack2(a.c2, a.c2), bb = ptx::pack2(mb, mb);
-    uint64_t s2 = 0, d2 = 0;                      // two zeros each
-#pragma unroll
-    for (int k = 0; k < 32; k += 2) {
-      const uint64_t d = ptx::fma2(ptx::pack2(v[k], v[k + 1]), cc, bb);
-      const float2 x = ptx::unpack2(d);
-      const uint64_t e = ptx::pack2(ptx::ex2(x.x), ptx::ex2(x.y));
-      s2 = ptx::add2(s2, e);
-      d2 = ptx::fma2(d, e, d2);
-    }
-    float sum = ptx::unpack2(s2).x + ptx::unpack2(s2).y;
-    float dsum = ptx::unpack2(d2).x + ptx::unpack2(d2).y;
-    if (dsum != dsum && sum == sum) {             // a logit of -inf: 0 times -inf; it adds nothing
-      dsum = 0.f;
-#pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const float d = fmaf(v[k], a.c2, mb);
-        dsum = fmaf(fmaxf(d, -1e30f), ptx::ex2(d), dsum);
-      }
-    }
-    // mb is rounded: every d is too large by rho = mx c2 + mb (exact in the
-    // fused multiply-add), which matters where the logits are large
-    const float rho = none ? 0.f : fmaf(mx, a.c2, mb);
-    const float back = ptx::ex2(-rho);
-    st = merge(st, Stat{mx, back * sum, back * fmaf(-rho, sum, dsum)}, a.c2);
+    blank_tail(v, j * 32, ncol, -INFINITY);
+    st = merge(st, stats32(v, a.c2), a.c2);
   }
   if (rv) {
-    const size_t np = static_cast<size_t>(a.nparts) * a.C;
-    float* p = a.stats + static_cast<size_t>(c0 / PART_COLS) * a.C + grow;
-    p[0] = st.m;
-    p[np] = st.s;
-    p[2 * np] = st.d;
+    store_stats(a, c0 / PART_COLS, grow, st);
     if (tl >= 0 && tl < ncol) a.zt[grow] = ztv;
   }
   if (a.bound == nullptr) return;
-  // Top alternatives: the logits of this part are kept unless K other parts of
-  // the row are known to have a larger max.  The parts are dealt to K groups;
-  // the least of the groups' maxima is such a bound, and only a part above it
-  // can raise it.
   const uint32_t key = order_key(st.m);
   const bool keep = rv && key >= bound;
   if (!__any_sync(0xffffffffu, keep)) return;
-  if (keep) {
-    uint32_t* g = a.group_max + static_cast<size_t>(grow) * a.group_stride;
-    atomicMax(g + (c0 / PART_COLS) % a.K, key);
-    uint32_t least = 0xffffffffu;
-    for (int k = 0; k < a.K; k += 4) {   // entries behind the K-th hold the largest integer
-      const uint4 q = __ldcg(reinterpret_cast<const uint4*>(g + k));
-      least = min(least, min(min(q.x, q.y), min(q.z, q.w)));
-    }
-    if (least > bound) atomicMax(a.bound + grow, least);
-  }
+  if (keep) raise_bound(a, c0 / PART_COLS, grow, key, bound);
 #pragma unroll 1
   for (int j = 0; j * 32 < ncol; ++j) {   // uniform over the warp
     float v[32];
@@ -456,12 +477,51 @@ __device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, con
   }
 }
 
-// Gradient of the logits of one row and part, written as bf16 once: of the
-// fp32 accumulator, so the only rounding before the consuming GEMMs is that
-// of dz itself (relative 2^-9).  Rows between the valid ones and the next
-// multiple of 128 are written too (as zeros, their constants being zero): the
-// grad_weight GEMM reads them.  4096 tokens at 2048 x 32000: 295 us, 1.82
-// PFLOP/s, 262 MB of dz written meanwhile.
+// Gradient of 32 logits of one row, written as bf16 once: of the fp32
+// accumulator, so the only rounding before the consuming GEMMs is that of dz
+// itself (relative 2^-9).  j0: the block's first column in the row's window of
+// ncol, whose target is column tl.
+__device__ __forceinline__ void dz32(const GemmArgs& a, float (&v)[32], const DzRow& q, bool entropy, int tl, int j0,
+                                     int ncol, bool store, uint16_t* dst) {
+  const uint64_t cc = ptx::pack2(a.c2, a.c2), bb = ptx::pack2(-q.lse2, -q.lse2);
+  const uint64_t qa = ptx::pack2(q.a, q.a), qb = ptx::pack2(q.b, q.b);
+  if (entropy) {
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      const float2 l = ptx::unpack2(ptx::fma2(ptx::pack2(v[k], v[k + 1]), cc, bb));
+      const uint64_t f = ptx::fma2(ptx::pack2(fmaxf(l.x, -1e30f), fmaxf(l.y, -1e30f)), qb, qa);   // -inf: 0 below
+      const float2 r2 = ptx::unpack2(ptx::mul2(ptx::pack2(ptx::ex2(l.x), ptx::ex2(l.y)), f));
+      v[k] = r2.x;
+      v[k + 1] = r2.y;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+      const float2 l = ptx::unpack2(ptx::fma2(ptx::pack2(v[k], v[k + 1]), cc, bb));
+      const float2 r2 = ptx::unpack2(ptx::mul2(ptx::pack2(ptx::ex2(l.x), ptx::ex2(l.y)), qa));
+      v[k] = r2.x;
+      v[k + 1] = r2.y;
+    }
+  }
+  if (static_cast<unsigned>(tl - j0) < 32u) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (j0 + k == tl) v[k] += q.g;
+  }
+  blank_tail(v, j0, ncol, 0.f);
+  if (store) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) pk[k] = ptx::pack_bf16x2(v[2 * k], v[2 * k + 1]);
+    ptx::st_global_v8(dst, pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6], pk[7]);
+    ptx::st_global_v8(dst + 16, pk[8], pk[9], pk[10], pk[11], pk[12], pk[13], pk[14], pk[15]);
+  }
+}
+
+// One row and part.  Rows between the valid ones and the next multiple of 128
+// are written too (as zeros, their constants being zero): the grad_weight GEMM
+// reads them.  4096 tokens at 2048 x 32000: 295 us, 1.82 PFLOP/s, 262 MB of dz
+// written meanwhile.
 __device__ __forceinline__ void epi_dz(const GemmArgs& a, const Shape& s, const Unit& t, int row0, int col0,
                                        uint32_t tbase, int r) {
   const int grow = row0 + r;
@@ -473,50 +533,97 @@ __device__ __forceinline__ void epi_dz(const GemmArgs& a, const Shape& s, const 
   DzRow q = {0.f, 0.f, 0.f, 0.f};
   if (rw) q = a.rowc[grow];
   uint16_t* zrow = a.z + static_cast<size_t>(grow) * a.ldz + c0;
-  const uint64_t cc = ptx::pack2(a.c2, a.c2), bb = ptx::pack2(-q.lse2, -q.lse2);
-  const uint64_t qa = ptx::pack2(q.a, q.a), qb = ptx::pack2(q.b, q.b);
   const bool entropy = __any_sync(0xffffffffu, q.b != 0.f);   // else the gradient of the log probabilities alone
 #pragma unroll 1
   for (int j = 0; j < GROUP_COLS / 32; ++j) {
     float v[32];
     ptx::tmem_ld32(tbase + j * 32, v);
-    if (entropy) {
-#pragma unroll
-      for (int k = 0; k < 32; k += 2) {
-        const float2 l = ptx::unpack2(ptx::fma2(ptx::pack2(v[k], v[k + 1]), cc, bb));
-        const uint64_t f = ptx::fma2(ptx::pack2(fmaxf(l.x, -1e30f), fmaxf(l.y, -1e30f)), qb, qa);   // -inf: 0 below
-        const float2 r2 = ptx::unpack2(ptx::mul2(ptx::pack2(ptx::ex2(l.x), ptx::ex2(l.y)), f));
-        v[k] = r2.x;
-        v[k + 1] = r2.y;
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 32; k += 2) {
-        const float2 l = ptx::unpack2(ptx::fma2(ptx::pack2(v[k], v[k + 1]), cc, bb));
-        const float2 r2 = ptx::unpack2(ptx::mul2(ptx::pack2(ptx::ex2(l.x), ptx::ex2(l.y)), qa));
-        v[k] = r2.x;
-        v[k + 1] = r2.y;
-      }
-    }
-    if (static_cast<unsigned>(tl - j * 32) < 32u) {
-#pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (j * 32 + k == tl) v[k] += q.g;
-    }
-    if (j * 32 + 32 > ncol) {   // the block straddles the end of the vocabulary
-#pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (j * 32 + k >= ncol) v[k] = 0.f;
-    }
-    if (rw && c0 + j * 32 < a.ldz) {
-      uint32_t pk[16];
-#pragma unroll
-      for (int k = 0; k < 16; ++k) pk[k] = ptx::pack_bf16x2(v[2 * k], v[2 * k + 1]);
-      uint16_t* dst = zrow + j * 32;
-      ptx::st_global_v8(dst, pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6], pk[7]);
-      ptx::st_global_v8(dst + 16, pk[8], pk[9], pk[10], pk[11], pk[12], pk[13], pk[14], pk[15]);
-    }
+    dz32(a, v, q, entropy, tl, j * 32, ncol, rw && c0 + j * 32 < a.ldz, zrow + j * 32);
   }
+}
+
+// ---------------------------------------------------------------------------
+// Long sums of the token log probabilities, in segments (segment_blocks()): one
+// accumulator after the other, added up by the epilogue in registers.  All four
+// warpgroups read each segment, 64 of the 256 columns each, and hand the
+// accumulator back at once; what follows the last one needs registers only and
+// runs beside the next tile's first two segments.  A change of accumulator
+// costs the issuing thread about 0.2 us.  In segments and in one piece, error of
+// the entropies and time: 4096 tokens at 1024 x 16000 5.6e-7, 108 us and 1.2e-6,
+// 102 us; at 2048 x 32000 8.1e-7, 314 us and 2.6e-6, 303 us; 16384 tokens at
+// 4096 x 128256 1.25e-6, 11.0 ms and 5.1e-6, 10.9 ms.
+// ---------------------------------------------------------------------------
+constexpr int QUARTER = BN / EPI_GROUPS;   // columns of one warpgroup
+static_assert(2 * QUARTER == PART_COLS, "two warpgroups share a part");
+
+// Two warpgroups' statistics of one part, exchanged through shared memory;
+// two buffers, since a warp may start on the next tile while another reads.
+struct Exchange {
+  float v[2][EPI_GROUPS][3][BM];
+};
+static_assert(sizeof(Exchange) <= EPI_GROUPS * STG_BYTES, "fits in the staging area");
+
+// Statistics of one row and part from both halves' registers; false on abort.
+// bar: the named barrier of the part's two warpgroups.
+__device__ __forceinline__ bool epi_stats_seg(const GemmArgs& a, const Shape& s, const Unit& t, int row0, int grp,
+                                              float (&z)[2][32], int r, bool ok, float (*ex)[3][BM], uint32_t bar) {
+  const int grow = row0 + r;
+  const bool rv = grow < s.Cl;
+  const int c0 = t.n0 + grp * QUARTER, part = (t.n0 + grp / 2 * PART_COLS) / PART_COLS;
+  const int tl = (rv ? a.tc[grow] : -1) - c0;
+  const int ncol = min(QUARTER, a.V - c0);         // may be <= 0 past the vocabulary
+  Stat mine = {-INFINITY, 0.f, 0.f};
+  float* zrow = a.zf + static_cast<size_t>(grow) * a.ldz + c0;
+  const bool all = a.K > 0 && a.bound == nullptr && rv;   // every logit is kept
+  float ztv = 0.f;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if (j * 32 >= ncol) break;                    // uniform
+    pick_target(z[j], tl, j * 32, ztv);
+    if (all) store_f32x32(zrow + j * 32, z[j]);
+    blank_tail(z[j], j * 32, ncol, -INFINITY);
+    mine = merge(mine, stats32(z[j], a.c2), a.c2);
+  }
+  ex[grp][0][r] = mine.m;
+  ex[grp][1][r] = mine.s;
+  ex[grp][2][r] = mine.d;
+  if (!ptx::named_bar_and(bar, 2 * GROUP_THREADS, ok)) return false;
+  const int og = grp ^ 1;
+  const Stat other = {ex[og][0][r], ex[og][1][r], ex[og][2][r]};
+  const bool first = (grp & 1) == 0;
+  const Stat st = first ? merge(mine, other, a.c2) : merge(other, mine, a.c2);
+  if (rv && ncol > 0) {
+    if (first) store_stats(a, part, grow, st);
+    if (tl >= 0 && tl < ncol) a.zt[grow] = ztv;
+  }
+  if (a.bound == nullptr || ncol <= 0) return true;
+  // The halves may see different bounds.  Each is one: what may be among the K
+  // best is above all of them, and both halves keep it.
+  const uint32_t bound = rv ? ptx::ld_relaxed_gpu(a.bound + grow) : 0u;
+  const uint32_t key = order_key(st.m);
+  if (rv && key >= bound) {
+    if (first) raise_bound(a, part, grow, key, bound);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (j * 32 < ncol) store_f32x32(zrow + j * 32, z[j]);   // behind the vocabulary: never read
+  }
+  return true;
+}
+
+__device__ __forceinline__ void epi_dz_seg(const GemmArgs& a, const Shape& s, const Unit& t, int row0, int grp,
+                                           float (&z)[2][32], int r) {
+  const int grow = row0 + r;
+  const bool rw = grow < min(a.C, (s.Cl + BM - 1) / BM * BM);
+  const int c0 = t.n0 + grp * QUARTER;
+  const int tl = (rw ? a.tc[grow] : -1) - c0;
+  const int ncol = min(QUARTER, a.V - c0);
+  if (c0 >= a.ldz) return;                        // uniform over the warpgroup
+  DzRow q = {0.f, 0.f, 0.f, 0.f};
+  if (rw) q = a.rowc[grow];
+  uint16_t* zrow = a.z + static_cast<size_t>(grow) * a.ldz + c0;
+  const bool entropy = __any_sync(0xffffffffu, q.b != 0.f);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) dz32(a, z[j], q, entropy, tl, j * 32, ncol, rw && c0 + j * 32 < a.ldz, zrow + j * 32);
 }
 
 __device__ __forceinline__ void store_bf16_row(uint16_t* dst, const float* v, int h, int H) {
@@ -733,11 +840,15 @@ __device__ __forceinline__ bool epi_dx_split(const GemmArgs& a, const Shape& s, 
   return true;
 }
 
-// PROBS selects the two modes of the token log probabilities (MODE_STATS,
-// MODE_DZ); a kernel of their own leaves the loss kernel's registers alone.
-template <bool PROBS>
+// What a kernel is for: the loss, or the two modes of the token log
+// probabilities (MODE_STATS, MODE_DZ), whose kernels of their own leave the
+// loss kernel's registers alone; SEGMENTED those with long sums.
+enum Kind : int { K_LOSS = 0, K_PROBS = 1, K_SEGMENTED = 2 };
+
+template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     flce_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
+  constexpr bool PROBS = KIND != K_LOSS, SEG = KIND == K_SEGMENTED;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stg = smem + STAGES * STAGE_BYTES;
@@ -770,7 +881,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&ctl->tfull[i], 1);
-      ptx::mbar_init(&ctl->tempty[i], TEMPTY_ARRIVALS);
+      ptx::mbar_init(&ctl->tempty[i], SEG ? 2 * EPI_WARPS : TEMPTY_ARRIVALS);
     }
     for (int i = 0; i < SCHED_SLOTS; ++i) {
       ptx::mbar_init(&ctl->sfull[i], 1);
@@ -806,7 +917,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   // p + pairs, ... and no claim or hand-off stands between them (0.15 us a
   // tile).  The others are claimed from a counter.
   const int pair0 = static_cast<int>(blockIdx.x / 2), npairs = static_cast<int>(gridDim.x / 2);
-  const uint32_t nstages = PROBS || a.mode == MODE_LOGITS ? STAGES_LOGITS : STAGES;
+  // (segmented statistics exchange through the staging area)
+  const uint32_t nstages = (PROBS || a.mode == MODE_LOGITS) && !(SEG && a.mode == MODE_STATS) ? STAGES_LOGITS : STAGES;
 
   if (warp == 0 && lane == 0) {
     // ---------------- (CTA 0: scheduler +) TMA producer ----------------
@@ -903,32 +1015,86 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       const uint32_t idesc = ptx::idesc_bf16_f32(PAIR_M, BN, a_mn, b_mn);
       const uint32_t a_lbo = a_mn ? MN_BLOCK_BYTES : 16, b_lbo = b_mn ? MN_BLOCK_BYTES : 16;
       const uint32_t a_kstep = a_mn ? 16 * 128 : 32, b_kstep = b_mn ? 16 * 128 : 32;
-      if (!wait_phase(&ctl->tempty[acc], acc_phase ^ 1u, ctl, to, true, hdr, W_TMEM_EMPTY, u | (acc << 24))) break;
-      ptx::tc_fence_after();
-      const uint32_t d_tmem = tmem + acc * BN;
       bool ok = true;
-      for (int kb = t.kb0; kb < t.kb1; ++kb) {
-        if (!wait_stage(&ctl->full[stage], phase, ctl, to, hdr, W_STAGE_FULL, u | (stage << 24))) { ok = false; break; }
+      int kb = t.kb0;
+      do {   // one accumulator: the whole sum, or a segment of it
+        const int kb0 = kb, kb1 = SEG ? min(t.kb1, kb0 + a.seg_kb) : t.kb1;
+        // (between segments the wait is on the issuer's path: in line)
+        if (SEG ? !wait_stage(&ctl->tempty[acc], acc_phase ^ 1u, ctl, to, hdr, W_TMEM_EMPTY, u | (acc << 24))
+                : !wait_phase(&ctl->tempty[acc], acc_phase ^ 1u, ctl, to, true, hdr, W_TMEM_EMPTY, u | (acc << 24))) { ok = false; break; }
         ptx::tc_fence_after();
-        const uint32_t sa = ptx::smem_u32(smem + stage * STAGE_BYTES);
-        const uint32_t sb = sa + A_BYTES;
+        const uint32_t d_tmem = tmem + acc * BN;
+        for (; kb < kb1; ++kb) {
+          if (!wait_stage(&ctl->full[stage], phase, ctl, to, hdr, W_STAGE_FULL, u | (stage << 24))) { ok = false; break; }
+          ptx::tc_fence_after();
+          const uint32_t sa = ptx::smem_u32(smem + stage * STAGE_BYTES);
+          const uint32_t sb = sa + A_BYTES;
 #pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk) {
-          const uint64_t ad = ptx::smem_desc_sw128(sa + kk * a_kstep, a_lbo, 1024);
-          const uint64_t bd = ptx::smem_desc_sw128(sb + kk * b_kstep, b_lbo, 1024);
-          ptx::umma_bf16_pair(d_tmem, ad, bd, idesc, (kb > t.kb0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            uint64_t ad, bd;
+            if (PROBS) {   // one kind of operand: only the address field changes
+              ad = ptx::smem_desc_sw128(0, 16, 1024) | ((sa >> 4) + kk * 2);
+              bd = ptx::smem_desc_sw128(0, 16, 1024) | ((sb >> 4) + kk * 2);
+            } else {
+              ad = ptx::smem_desc_sw128(sa + kk * a_kstep, a_lbo, 1024);
+              bd = ptx::smem_desc_sw128(sb + kk * b_kstep, b_lbo, 1024);
+            }
+            ptx::umma_bf16_pair(d_tmem, ad, bd, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
+          }
+          ptx::umma_commit_pair(&ctl->empty[stage], PAIR_MASK);   // frees the slot in both CTAs
+          if (++stage == nstages) { stage = 0; phase ^= 1u; }
         }
-        ptx::umma_commit_pair(&ctl->empty[stage], PAIR_MASK);   // frees the slot in both CTAs
-        if (++stage == nstages) { stage = 0; phase ^= 1u; }
-      }
+        if (!ok) break;
+        if (!withhold) ptx::umma_commit_pair(&ctl->tfull[acc], PAIR_MASK);   // accumulator ready in both CTAs
+        withhold = false;
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+      } while (SEG && kb < t.kb1);
       if (!ok) break;
-      if (!withhold) ptx::umma_commit_pair(&ctl->tfull[acc], PAIR_MASK);   // accumulator ready in both CTAs
-      withhold = false;
-      acc ^= 1u;
-      if (acc == 0) acc_phase ^= 1u;
     }
     ptx::umma_commit_pair(&ctl->mma_done, 0x1);
     wait_phase(&ctl->mma_done, 0, ctl, to, false, hdr, W_MMA_DONE);
+  } else if (SEG && warp >= 2) {
+    // ---------------- epilogue of long sums: all warps on each segment ----------------
+    const int q = warp & 3, grp = (warp - 2) / 4;
+    const int r = q * 32 + lane;
+    Exchange* ex = reinterpret_cast<Exchange*>(stg);
+    const uint32_t tempty0 = ptx::map_to_rank(&ctl->tempty[0], 0);
+    const uint32_t tcol = tmem + (static_cast<uint32_t>(q * 32) << 16) + grp * QUARTER;
+    uint32_t acc = 0, acc_phase = 0, buf = 0;
+    for (int u = pair0; u < s.units; u += npairs) {
+      const Unit t = decode_unit<PROBS>(a, s, u);
+      float z[2][32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k) z[0][k] = z[1][k] = 0.f;
+      bool ok = true;
+#pragma unroll 1
+      for (int kb = 0; kb < s.kbt; kb += a.seg_kb) {
+        ok = ok && __all_sync(0xffffffffu, wait_stage(&ctl->tfull[acc], acc_phase, ctl, to, hdr, W_TMEM_FULL, u | (acc << 24)));
+        if (!ok) break;   // uniform over the warp; the others give up at their own wait
+        ptx::tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < QUARTER / 16; ++j) {
+          float v[16];
+          ptx::tmem_ld16(tcol + acc * BN + j * 16, v);
+#pragma unroll
+          for (int k = 0; k < 16; ++k) z[j / 2][j % 2 * 16 + k] += v[k];
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_remote_relaxed(tempty0 + acc * 8u);
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      const int row0 = t.m0 + half;
+      if (a.mode == MODE_STATS) {
+        ok = epi_stats_seg(a, s, t, row0, grp, z, r, ok, ex->v[buf], EPI_BAR_SET + static_cast<uint32_t>(grp / 2));
+        buf ^= 1u;
+      } else if (ok) {
+        epi_dz_seg(a, s, t, row0, grp, z, r);
+      }
+      if (!ok) break;
+    }
   } else if (warp >= 2) {
     // ---------------- epilogue (both CTAs: 128 rows each) ----------------
     // Set e drains accumulator e, i.e. every other tile of the pair; its two
@@ -1027,9 +1193,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 int gemm_smem_bytes() { return SMEM_BYTES; }
 
 cudaError_t gemm_prepare(int /*device*/) {
-  cudaError_t e = cudaFuncSetAttribute(flce_gemm_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(flce_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  cudaError_t e = cudaFuncSetAttribute(flce_gemm_kernel<K_LOSS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(flce_gemm_kernel<K_PROBS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(flce_gemm_kernel<K_SEGMENTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  return e;
 }
 
 cudaError_t gemm_max_pairs(int* pairs) {
@@ -1044,7 +1213,7 @@ cudaError_t gemm_max_pairs(int* pairs) {
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(pairs, flce_gemm_kernel<false>, &cfg);
+  return cudaOccupancyMaxActiveClusters(pairs, flce_gemm_kernel<K_LOSS>, &cfg);
 }
 
 cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps& m, int grid, cudaStream_t st, bool dependent) {
@@ -1060,8 +1229,9 @@ cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps& m, int grid, cudaStre
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   if (a.mode == MODE_STATS || a.mode == MODE_DZ)
-    return launch_result(cudaLaunchKernelEx(&cfg, flce_gemm_kernel<true>, m, a));
-  return launch_result(cudaLaunchKernelEx(&cfg, flce_gemm_kernel<false>, m, a));
+    return launch_result(a.seg_kb * BK < a.H ? cudaLaunchKernelEx(&cfg, flce_gemm_kernel<K_SEGMENTED>, m, a)
+                                           : cudaLaunchKernelEx(&cfg, flce_gemm_kernel<K_PROBS>, m, a));
+  return launch_result(cudaLaunchKernelEx(&cfg, flce_gemm_kernel<K_LOSS>, m, a));
 }
 
 }  // namespace flce

@@ -5,6 +5,9 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+#include <cmath>
+
 namespace flce {
 
 // Device status word bits (workspace header word 0).
@@ -92,6 +95,7 @@ struct GemmArgs {
   int gw_bf16;          // BWD of a call with one chunk: grad_weight tiles are rounded and stored as bf16
   float c2;             // log2(e) / temperature: z c2 is the scaled logit in base-2 units
   float* stats;         // STATS: [3][nparts][C] part max (raw z), sum of 2^d, sum of d 2^d, d = (z - max) c2
+  int seg_kb;           // STATS, DZ: K blocks of a segment of a logit's sum (segment_blocks)
   int K;                // STATS: top alternatives, and for K > 0
   float* zf;            //   [C][ldz] fp32 logits of the parts that may hold one
   uint32_t* bound;      //   [C] ordered integer that a part's max has to reach, or null: every part is kept
@@ -192,10 +196,23 @@ cudaError_t launch_zero_ignored(const int* hdr, const int* idx, long long N, lon
 cudaError_t launch_gather(const uint16_t* hidden, const int* targets, const int* hdr,
                           const int* idx, long long c0, int C, int H,
                           uint16_t* xc, int* tc, int v0, int vs, cudaStream_t s);
+// Segments of a logit's sum over H.  The tensor core cuts off what its fp32
+// accumulator cannot hold, at every 16-wide step, so a sum comes out short by a
+// part of itself that grows with its length (0.07e-6 of entropies per K block:
+// 1.1e-6 at H = 1024, 5e-6 at 4096).  The log probabilities therefore sum it in
+// segments, each from zero, and add these up rounded to nearest.  With
+// 2 sqrt(blocks) blocks a segment the error grows with H as that of an fp32
+// product on the CUDA cores does; up to 11 blocks it is below 1e-6 anyway.
+inline int segment_blocks(long long H) {
+  const int blocks = static_cast<int>(cdiv(H, BK));
+  const int most = std::max(11, static_cast<int>(2.0 * std::sqrt(static_cast<double>(blocks))));
+  return static_cast<int>(cdiv(blocks, cdiv(blocks, most)));   // of equal length
+}
 // Few tokens: the weight streamed once past all of them (flce_stream.cu).
 constexpr int STREAM_MAX_TOKENS = 128;
 struct StreamArgs {
   int N, H, V, K;          // K: top alternatives
+  int seg_kb;              // K blocks of a segment of a logit's sum
   int ctas;
   float c2;
   int ii;

@@ -557,6 +557,7 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
     StreamArgs a;
     std::memset(&a, 0, sizeof(a));
     a.N = static_cast<int>(N); a.H = static_cast<int>(H); a.V = static_cast<int>(V); a.K = top_k;
+    a.seg_kb = segment_blocks(H);
     a.ctas = p.ctas;
     a.c2 = LOG2E / temperature;
     a.ii = ignore_index;
@@ -630,6 +631,7 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
     g.group_max = at<uint32_t>(workspace, p.o_group);
   }
   g.group_stride = p.group_stride;
+  g.seg_kb = segment_blocks(H);
   g.c2 = LOG2E / temperature;
 
   const int grid = 2 * static_cast<int>(std::min<long long>(cdiv(p.C, PAIR_M) * p.nvt, dev.pairs));

@@ -22,6 +22,11 @@
 // alternatives at 2048 x 256000 184 us, with none stored 164; a sorted list per
 // CTA and token: 175, with 32 alternatives 212.)
 //
+// Long sums over H are taken in segments (segment_blocks()), each in an
+// accumulator of its own, which the epilogue warps add up in registers (1 to 64
+// tokens no slower; 128 tokens at 1024 x 128256 81 us, 76 in one piece, at 4096
+// 181 and 180).
+//
 // Bound by the weight's bytes: 2 H V at the HBM rate (4096 x 128256: 158 us for
 // 1 token, 6.66 TB/s; 164 for 64, 172 for 128).  Every wait is bounded:
 // on time-out the CTA lets its copies in flight land, waits for its MMAs, frees
@@ -109,7 +114,8 @@ __device__ __forceinline__ Range range_of(const StreamArgs& a, int cta) {
   return r;
 }
 
-template <int NT>
+// SEG: the sum over H in segments (segment_blocks()), added up in registers.
+template <int NT, bool SEG>
 __global__ void __launch_bounds__(THREADS, 1)
     logprob_stream_kernel(const __grid_constant__ StreamMaps maps, const StreamArgs a) {
   using C = Cfg<NT>;
@@ -196,28 +202,33 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool withhold = a.debug_stall != 0, ok = true;
     for (int i = 0; ok && i < range.tiles; ++i) {
       const bool two = range.start(i + 1) - range.start(i) > 128;
-      if (!wait(&ctl->tempty[acc], acc_phase ^ 1u, ctl, to, a.hdr, S_TMEM_EMPTY)) break;
-      ptx::tc_fence_after();
-      const uint32_t d = tmem + acc * 2 * NT;
-      for (int kb = 0; kb < kbt; ++kb) {
-        if (!wait(&ctl->full[stage], phase, ctl, to, a.hdr, S_STAGE_FULL)) { ok = false; break; }
+      int kb = 0;
+      do {   // one accumulator: the whole sum, or a segment of it
+        const int kb0 = kb, kb1 = SEG ? min(kbt, kb0 + a.seg_kb) : kbt;
+        if (!wait(&ctl->tempty[acc], acc_phase ^ 1u, ctl, to, a.hdr, S_TMEM_EMPTY)) { ok = false; break; }
         ptx::tc_fence_after();
-        const uint32_t sw = ptx::smem_u32(smem + stage * C::STAGE_BYTES);
+        const uint32_t d = tmem + acc * 2 * NT;
+        for (; kb < kb1; ++kb) {
+          if (!wait(&ctl->full[stage], phase, ctl, to, a.hdr, S_STAGE_FULL)) { ok = false; break; }
+          ptx::tc_fence_after();
+          const uint32_t sw = ptx::smem_u32(smem + stage * C::STAGE_BYTES);
 #pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk) {
-          const uint32_t go = (kb > 0 || kk > 0) ? 1u : 0u;
-          const uint64_t xd = ptx::smem_desc_sw128(sw + W_BYTES + kk * 32, 16, 1024);
-          ptx::umma_bf16(d, ptx::smem_desc_sw128(sw + kk * 32, 16, 1024), xd, idesc, go);
-          if (two) ptx::umma_bf16(d + NT, ptx::smem_desc_sw128(sw + 128 * BK * 2 + kk * 32, 16, 1024), xd, idesc, go);
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint32_t go = (kb > kb0 || kk > 0) ? 1u : 0u;
+            const uint64_t wd = ptx::smem_desc_sw128(0, 16, 1024) | ((sw >> 4) + kk * 2);
+            const uint64_t xd = wd + W_BYTES / 16;
+            ptx::umma_bf16(d, wd, xd, idesc, go);
+            if (two) ptx::umma_bf16(d + NT, wd + 128 * BK * 2 / 16, xd, idesc, go);
+          }
+          ptx::umma_commit(&ctl->empty[stage]);
+          if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
         }
-        ptx::umma_commit(&ctl->empty[stage]);
-        if (++stage == C::STAGES) { stage = 0; phase ^= 1u; }
-      }
-      if (!ok) break;
-      if (!withhold) ptx::umma_commit(&ctl->tfull[acc]);
-      withhold = false;
-      acc ^= 1u;
-      if (acc == 0) acc_phase ^= 1u;
+        if (!ok) break;
+        if (!withhold) ptx::umma_commit(&ctl->tfull[acc]);
+        withhold = false;
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+      } while (SEG && kb < kbt);
     }
     ptx::umma_commit(&ctl->mma_done);
     wait(&ctl->mma_done, 0, ctl, to, a.hdr, S_MMA_DONE, false);
@@ -249,21 +260,60 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
       }
       const int r0 = range.start(i), rows = min(range.start(i + 1), a.V) - r0;
-      const bool ok = wait(&ctl->tfull[acc], acc_phase, ctl, to, a.hdr, S_TMEM_FULL);
+      const uint32_t tb0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * NT;
+      float sum[SEG ? NT : 1];   // SEG: this row's logits so far
+      bool ok;
+      if constexpr (SEG) {
+        ok = true;
+#pragma unroll
+        for (int k = 0; k < NT; ++k) sum[k] = 0.f;
+#pragma unroll 1
+        for (int kb = 0; kb < kbt; kb += a.seg_kb) {
+          ok = __all_sync(0xffffffffu, wait(&ctl->tfull[acc], acc_phase, ctl, to, a.hdr, S_TMEM_FULL));
+          if (!ok) break;   // uniform over the warp; the others give up at their own wait
+          ptx::tc_fence_after();
+          if (half * 128 < rows) {
+#pragma unroll
+            for (int j = 0; j < NT; j += C::SLICE) {
+              if (j >= a.N) break;
+              float v[C::SLICE];
+              if constexpr (C::SLICE == 32) ptx::tmem_ld32(tb0 + acc * 2 * NT + j, v);
+              else ptx::tmem_ld16(tb0 + acc * 2 * NT + j, v);
+#pragma unroll
+              for (int k = 0; k < C::SLICE; ++k) sum[j + k] += v[k];
+            }
+          }
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&ctl->tempty[acc]);
+          acc ^= 1u;
+          if (acc == 0) acc_phase ^= 1u;
+        }
+      } else {
+        ok = wait(&ctl->tfull[acc], acc_phase, ctl, to, a.hdr, S_TMEM_FULL);
+      }
       if (!ptx::named_bar_and(EPI_BAR, EPI_THREADS, ok)) break;   // all epilogue threads leave together
       ptx::tc_fence_after();
-      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 2 * NT + half * NT;
-#pragma unroll 1
-      for (int n0 = 0; n0 < a.N; n0 += C::SLICE) {
+      const uint32_t tb = tb0 + acc * 2 * NT;
+      constexpr int UNROLL = SEG ? NT / C::SLICE : 1;   // registers have no index
+#pragma unroll UNROLL
+      for (int n0 = 0; n0 < NT; n0 += C::SLICE) {
+        if (n0 >= a.N) break;
         if (half * 128 < rows) {
           float v[C::SLICE];
-          if constexpr (C::SLICE == 32) ptx::tmem_ld32(tb + n0, v);
-          else ptx::tmem_ld16(tb + n0, v);
+          if constexpr (SEG) {
+#pragma unroll
+            for (int k = 0; k < C::SLICE; ++k) v[k] = sum[n0 + k];
+          } else if constexpr (C::SLICE == 32) {
+            ptx::tmem_ld32(tb + n0, v);
+          } else {
+            ptx::tmem_ld16(tb + n0, v);
+          }
           float* p = turn + half * 128 + q * 32 + lane;
 #pragma unroll
           for (int k = 0; k < C::SLICE; ++k) p[k * TILE_ROWS] = v[k];
         }
-        if (n0 + C::SLICE >= a.N) {   // this warp has read its part of the accumulator
+        if (!SEG && n0 + C::SLICE >= a.N) {   // this warp has read its part of the accumulator
           ptx::tc_fence_before();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&ctl->tempty[acc]);
@@ -320,8 +370,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         ptx::named_bar_sync(EPI_BAR, EPI_THREADS);   // the slice buffer is free again
       }
-      acc ^= 1u;
-      if (acc == 0) acc_phase ^= 1u;
+      if (!SEG) {
+        acc ^= 1u;
+        if (acc == 0) acc_phase ^= 1u;
+      }
     }
     for (int tk = w; tk < a.N; tk += EPI_WARPS) {
       __syncwarp();
@@ -466,20 +518,28 @@ __global__ void clear_groups_kernel(uint32_t* group_max, int n) {
 
 template <int NT>
 cudaError_t prepare() {
-  return cudaFuncSetAttribute(logprob_stream_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NT>::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(logprob_stream_kernel<NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Cfg<NT>::SMEM);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(logprob_stream_kernel<NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NT>::SMEM);
 }
 
-template <int NT>
-cudaError_t launch(const StreamArgs& a, const StreamMaps& m, cudaStream_t s) {
+template <int NT, bool SEG>
+cudaError_t launch_form(const StreamArgs& a, const StreamMaps& m, cudaStream_t s) {
   if (!a.group_max) {
-    logprob_stream_kernel<NT><<<a.ctas, THREADS, Cfg<NT>::SMEM, s>>>(m, a);
+    logprob_stream_kernel<NT, SEG><<<a.ctas, THREADS, Cfg<NT>::SMEM, s>>>(m, a);
     return cudaGetLastError();
   }
   // the weight streams while the groups' maxima are cleared
   clear_groups_kernel<<<1, 512, 0, s>>>(a.group_max, a.N * TopK::MAX);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_dependent_smem(logprob_stream_kernel<NT>, a.ctas, THREADS, Cfg<NT>::SMEM, s, m, a);
+  return launch_dependent_smem(logprob_stream_kernel<NT, SEG>, a.ctas, THREADS, Cfg<NT>::SMEM, s, m, a);
+}
+
+template <int NT>
+cudaError_t launch(const StreamArgs& a, const StreamMaps& m, cudaStream_t s) {
+  return a.seg_kb * BK < a.H ? launch_form<NT, true>(a, m, s) : launch_form<NT, false>(a, m, s);
 }
 
 }  // namespace

@@ -12,7 +12,7 @@ KEYS = ("logp", "lse", "entropy", "top_ids", "top_logp")
 
 
 @pytest.mark.parametrize("N,H,V", [(1, 64, 100003), (40, 320, 40000), (128, 128, 100003), (300, 64, 30000),
-                                   (300, 512, 30000)])
+                                   (300, 512, 30000), (300, 1024, 9000), (20, 1024, 60000)])
 def test_next_call_is_right(env, N, H, V):  # noqa: F811
     """Fewer K blocks than ring stages: the loads of the last tile are all issued when another role gives up."""
     flce, torch, dev = env
