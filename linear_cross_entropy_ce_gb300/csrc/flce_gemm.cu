@@ -547,11 +547,12 @@ __device__ __forceinline__ void epi_dz(const GemmArgs& a, const Shape& s, const 
 // accumulator after the other, added up by the epilogue in registers.  All four
 // warpgroups read each segment, 64 of the 256 columns each, and hand the
 // accumulator back at once; what follows the last one needs registers only and
-// runs beside the next tile's first two segments.  A change of accumulator
-// costs the issuing thread about 0.2 us.  In segments and in one piece, error of
-// the entropies and time: 4096 tokens at 1024 x 16000 5.6e-7, 108 us and 1.2e-6,
-// 102 us; at 2048 x 32000 8.1e-7, 314 us and 2.6e-6, 303 us; 16384 tokens at
-// 4096 x 128256 1.25e-6, 11.0 ms and 5.1e-6, 10.9 ms.
+// runs beside the next tile's first two segments.  The thread that issues the
+// MMAs is close to being what bounds a tile (an integer division per K block
+// makes it 20% slower), so a change of accumulator has to be short.  In segments
+// and in one piece, error of the entropies and time: 4096 tokens at 1024 x 16000
+// 5.6e-7, 105 us and 1.2e-6, 101 us; at 2048 x 32000 8.1e-7, 312 us and 2.6e-6,
+// 303 us; 16384 tokens at 4096 x 128256 1.25e-6, 10.8 ms and 5.1e-6, 10.9 ms.
 // ---------------------------------------------------------------------------
 constexpr int QUARTER = BN / EPI_GROUPS;   // columns of one warpgroup
 static_assert(2 * QUARTER == PART_COLS, "two warpgroups share a part");
@@ -1077,8 +1078,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         for (int j = 0; j < QUARTER / 16; ++j) {
           float v[16];
           ptx::tmem_ld16(tcol + acc * BN + j * 16, v);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) z[j / 2][j % 2 * 16 + k] += v[k];
+          ptx::add_pairs(z[j / 2] + j % 2 * 16, v);   // one by one: tiles up to 4% slower
         }
         ptx::tc_fence_before();
         __syncwarp();

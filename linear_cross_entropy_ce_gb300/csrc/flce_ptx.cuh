@@ -379,6 +379,16 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// s += v, pair by pair.
+template <int N>
+__device__ __forceinline__ void add_pairs(float* s, const float (&v)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    const float2 r = unpack2(add2(pack2(s[k], s[k + 1]), pack2(v[k], v[k + 1])));
+    s[k] = r.x;
+    s[k + 1] = r.y;
+  }
+}
 // Largest of three; NaN operands are ignored as by fmaxf.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;

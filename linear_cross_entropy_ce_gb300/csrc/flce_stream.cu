@@ -24,7 +24,7 @@
 //
 // Long sums over H are taken in segments (segment_blocks()), each in an
 // accumulator of its own, which the epilogue warps add up in registers (1 to 64
-// tokens no slower; 128 tokens at 1024 x 128256 81 us, 76 in one piece, at 4096
+// tokens no slower; 128 tokens at 1024 x 128256 80 us, 76 in one piece, at 4096
 // 181 and 180).
 //
 // Bound by the weight's bytes: 2 H V at the HBM rate (4096 x 128256: 158 us for
