@@ -248,9 +248,16 @@ flce_status flce_vocab_shard_bwd(const void* hidden, const void* weight_shard,
  * other rows are right.  A row with NaN or +inf logits gets NaN.  After a
  * pipeline time-out (FLCE_ETIMEOUT) every scored row is NaN (ids -1), those of
  * chunks that were done before it too.
- * The N x V logits are not kept: the workspace (flce_logprobs_workspace_bytes;
- * less runs in smaller chunks, down to 128 rows) stays below 5% of their bf16
- * size, or 512 MiB (2 GiB with top alternatives) where that is more.
+ * A logit's sum over H is as exact as an fp32 product on the CUDA cores.
+ * Workspace (flce_logprobs_workspace_bytes):
+ *   N <= 128     statistics, under 1 MB; with top alternatives also the N V 4
+ *                bytes of the fp32 logits.  Less is refused.
+ *   N > 128      one chunk of tokens: its rows, 12 bytes per row and 128
+ *                logits and, with top alternatives, its fp32 logits.  The
+ *                default is the largest chunk within 5% of the bf16 logits, or
+ *                within 512 MiB (2 GiB with top alternatives) where that is
+ *                more, and one of 128 rows at least; less runs in smaller ones.
+ *                Logits that fit in it are held all at once.
  * 0 < temperature < inf.  V <= 2^31 - 512; other sizes, alignment, streams and errors as flce_fwd_bwd;
  * top_k > V is FLCE_EINVAL, top_k > 32 FLCE_EUNSUPPORTED.
  */
@@ -270,13 +277,18 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
  * be NULL when grad_entropy is).  Either of grad_logp and grad_entropy may be
  * NULL (zero), and either of grad_hidden and grad_weight (not wanted).  The
  * logits are computed again chunk by chunk; dz is rounded to bf16 once, from
- * the fp32 accumulator, and the sums over it are kept in fp32, in a fixed order.
+ * the fp32 accumulator, and the sums over it are kept in fp32, in a fixed order:
+ * a gradient is off by about 1.7e-3 of its norm (a bf16 one by 2.4e-3, of which
+ * its own rounding is 1.7e-3).  p is formed from lse, so its relative error is
+ * that of an fp32 number of the size of lse: 2^-24 |lse|, more than bf16's
+ * rounding only from |lse| = 32768 on (temperatures of 1e-3 and less).
  * Targets outside [0, V) are treated as ignored (FLCE_EBADTARGET in the status
  * word); after a time-out the first element of each gradient is NaN.
  * Workspace: flce_logprobs_bwd_workspace_bytes (5% of the bf16 logits, or 2 GiB
  * where that is more and the problem needs it; plus V*H*4 bytes with
  * FLCE_GW_BF16 where that does not hold the batch in one chunk); less runs in
- * smaller chunks.
+ * smaller chunks.  It holds one chunk's dz in bf16, which is all N x V of it
+ * where that fits.
  */
 size_t flce_logprobs_bwd_workspace_bytes(int64_t N, int64_t H, int64_t V, uint32_t flags);
 flce_status flce_logprobs_bwd(const void* hidden, const void* weight, const int32_t* targets,

@@ -246,7 +246,9 @@ cudaError_t launch_stream(const StreamArgs& a, const StreamMaps& m, cudaStream_t
 
 // Token log probabilities (flce_logprobs.cu).
 // The first launch of a call of one chunk and at most FRONT_MAX_TOKENS tokens;
-// rowc selects the backward.
+// rowc selects the backward.  Its blocks read N^2 / 2 bytes of targets between
+// them (from L2: 134 MB at the most tokens); past that the loss's kernels
+// compact the tokens in one block and gather them in another launch.
 constexpr long long FRONT_MAX_TOKENS = 16384;
 struct FrontArgs {
   const uint16_t* hidden;

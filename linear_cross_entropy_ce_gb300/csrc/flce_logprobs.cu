@@ -1,5 +1,7 @@
-// Token log probabilities at the LM head, with entropy and top alternatives,
-// without the N x V logits:
+// Token log probabilities at the LM head, with entropy and top alternatives, in
+// chunks of tokens: of a chunk's logits only statistics are kept, and with top
+// alternatives those that may be among them (in fp32, in room for all: a chunk's
+// logits fit in the workspace, and so do all of a small problem's).
 //
 //   z = X W^T / T,   lse_n = log sum_v exp z_nv,   logp_n = z_{n,t_n} - lse_n,
 //   H_n = -sum_v p_nv log p_nv = lse_n - sum_v p_nv z_nv,   p = exp(z - lse),
