@@ -435,8 +435,8 @@ __device__ __forceinline__ void blank_tail(float (&v)[32], int j0, int ncol, flo
 }
 
 // Statistics of one row and part.  Bound by the tensor cores from H = 2048 up
-// (4096 tokens at 2048 x 32000: 282 us, 1.90 PFLOP/s); at 8 K blocks a tile
-// takes 2.9 us for 2.2 us of MMAs.
+// (4096 tokens at 2048 x 32000 in three segments: 290 us, 1.85 PFLOP/s); at 8 K
+// blocks a tile takes 2.9 us for 2.2 us of MMAs.
 __device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, const Unit& t, int row0, int col0,
                                           uint32_t tbase, int r) {
   const int grow = row0 + r;
@@ -520,7 +520,7 @@ __device__ __forceinline__ void dz32(const GemmArgs& a, float (&v)[32], const Dz
 
 // One row and part.  Rows between the valid ones and the next multiple of 128
 // are written too (as zeros, their constants being zero): the grad_weight GEMM
-// reads them.  4096 tokens at 2048 x 32000: 295 us, 1.82 PFLOP/s, 262 MB of dz
+// reads them.  4096 tokens at 2048 x 32000: 299 us, 1.80 PFLOP/s, 262 MB of dz
 // written meanwhile.
 __device__ __forceinline__ void epi_dz(const GemmArgs& a, const Shape& s, const Unit& t, int row0, int col0,
                                        uint32_t tbase, int r) {
