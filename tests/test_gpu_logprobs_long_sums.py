@@ -107,3 +107,50 @@ def test_gradients(env, N, H, V, grid):  # noqa: F811
         tol = ref["mag_" + k] * (2.0 ** -8 + 2e-4) * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref["grad_" + k])
         err = np.abs(np64(d["grad_" + k]) - ref["grad_" + k])
         assert np.all(err <= tol + 1e-30), (k, (err / (tol + 1e-30)).max())
+
+
+@pytest.mark.parametrize("N", [100, 300])
+def test_captured_and_on_two_streams(env, N):  # noqa: F811
+    """Replays on new inputs, and two calls at once, are bitwise the eager calls."""
+    flce, torch, dev = env
+    H, V, K = 1032, 3000, 4
+    probs = [continuous(torch, dev, N, H, V, s) for s in (1, 2)]
+    g = torch.randn(N, device=dev)
+
+    def both(h, w, t, stream=None):
+        o = flce.token_logprobs(h, w, t, top_k=K, stream=stream)
+        d = flce.token_logprobs_bwd(h, w, t, o["lse"], o["entropy"], g, g, stream=stream)
+        return [o[k] for k in ("logp", "entropy", "lse", "top_ids", "top_logp")] + [d["grad_hidden"], d["grad_weight"]]
+
+    want = [both(*p) for p in probs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        got = [both(*p, stream=s) for p, s in zip(probs, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    h, w, t = (x.clone() for x in probs[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = both(h, w, t)
+    for p, a in ((probs[1], want[1]), (probs[0], want[0])):
+        for x, y in zip((h, w, t), p):
+            x.copy_(y)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(out, a))
+
+
+@pytest.mark.parametrize("K", [0, 3, 32])
+def test_chunks(env, K):  # noqa: F811
+    """Chunks of 128 tokens give the values of one chunk, with and without a bound of the alternatives."""
+    flce, torch, dev = env
+    N, H, V = 500, 776, 20003
+    h, w, t = continuous(torch, dev, N, H, V, 3)
+    whole = flce.token_logprobs(h, w, t, top_k=K)
+    # a chunk of 128: its fp32 logits where there are alternatives, the statistics, its rows
+    nb = (128 * (V + 64) * 4 if K else 0) + 128 * 160 * 12 + 128 * H * 2 + (1 << 16)
+    part = flce.token_logprobs(h, w, t, top_k=K, workspace=torch.full((nb,), 255, dtype=torch.uint8, device=dev))
+    for k in ("logp", "lse", "entropy") + (("top_ids", "top_logp") if K else ()):
+        assert torch.equal(whole[k], part[k]), k
