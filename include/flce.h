@@ -35,7 +35,8 @@
  * one 4-byte value per token: 4-byte) and must not alias one another.  A
  * workspace must be 32-byte aligned where the call keeps logits or their
  * gradient in it: every call with gradients but flce_embedding_bwd, and
- * flce_logprobs of more than 128 tokens with top alternatives.
+ * flce_logprobs and flce_constrained_logprobs of more than 128 tokens with top
+ * alternatives.
  *
  * Streams.  Each call only enqueues kernels on `stream` (a cudaStream_t
  * passed as void*, NULL = legacy default stream) and returns; nothing
@@ -298,6 +299,121 @@ flce_status flce_logprobs_bwd(const void* hidden, const void* weight, const int3
                               const float* grad_entropy, void* grad_hidden,
                               float* grad_weight, void* workspace, size_t workspace_bytes,
                               void* stream);
+
+/*
+ * Log probabilities of the next token under constraints, for serving: the
+ * log-sum-exp, entropies, log probabilities and top alternatives of
+ * flce_logprobs, of logits that are changed first.  In this order, each step
+ * rounded to fp32, for every row n and token v of z = X W^T:
+ *   repetition  if v occurs in the row's history (prompt or output):
+ *               z <- z > 0 ? z / r_n : z * r_n
+ *   frequency   if it occurs c > 0 times in the output: z <- z - f_n * c
+ *   presence    and:                                    z <- z - p_n
+ *   bias        if the row's biases name it: z <- z + b; of a token named twice
+ *               the last entry holds.  Finite or -inf.
+ *   mask        if its bit is not set: z <- -inf
+ * and z / temperature is what the softmax sees.  A token's place is decided by
+ * the changed z; equal ones by the lower id.
+ *   history       [N, history_len] int32 token ids, rows history_stride apart
+ *                 (0: one sequence for all rows); the first history_lens[n] of
+ *                 them count (NULL: all), of which the first prompt_lens[n]
+ *                 (NULL: none) are the prompt.  Ids outside [0, V) count for
+ *                 nothing (padding).
+ *   repetition_penalty, frequency_penalty, presence_penalty
+ *                 [N] fp32, or NULL: 1, 0, 0.  r_n > 0.
+ *   bias_ids, bias  [N, n_bias] int32 and fp32, rows bias_ids_stride and
+ *                 bias_stride apart; ids outside [0, V) are passed over.
+ *   mask          [N, ceil(V / 32)] int32 words, rows mask_stride words apart,
+ *                 bit v % 32 of word v / 32 is token v's; or NULL.  Logits of
+ *                 forbidden tokens may be NaN or infinite.
+ * Lengths are clipped to what the arrays hold.
+ * Outputs as flce_logprobs; but targets may be NULL (every row counts, logp may
+ * be NULL then), a forbidden target's logp is -inf, forbidden tokens are no
+ * alternatives (ids -1, log probability -inf behind the last allowed one), and
+ * a row with nothing left has lse -inf and entropy 0.
+ * Workspace (flce_constrained_workspace_bytes): that of flce_logprobs, 8 bytes
+ * (12 with biases) for each of a row's up to min(V, history_len + n_bias)
+ * changed tokens, 4 more in the chunked form, and 4 bytes per row and tile of
+ * the vocabulary.  The lengths there are the history_len and n_bias of the call.
+ */
+typedef struct flce_constraints {
+  const int32_t* history;
+  int64_t history_len, history_stride;
+  const int32_t* history_lens;
+  const int32_t* prompt_lens;
+  const float* repetition_penalty;
+  const float* frequency_penalty;
+  const float* presence_penalty;
+  const int32_t* bias_ids;
+  const float* bias;
+  int64_t n_bias, bias_ids_stride, bias_stride;
+  const int32_t* mask;
+  int64_t mask_stride;
+} flce_constraints;
+size_t flce_constrained_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t top_k,
+                                        int64_t history_len, int64_t n_bias);
+flce_status flce_constrained_logprobs(const void* hidden, const void* weight,
+                                      const int32_t* targets, int64_t N, int64_t H,
+                                      int64_t V, int32_t ignore_index, float temperature,
+                                      int32_t top_k, const flce_constraints* rules,
+                                      float* logp, float* entropy, float* lse,
+                                      int32_t* top_ids, float* top_logp, void* workspace,
+                                      size_t workspace_bytes, void* stream);
+
+/*
+ * Distillation from a teacher's top log probabilities (those flce_logprobs or
+ * flce_constrained_logprobs give as top_ids and top_logp, or any other list).
+ * With q = softmax(X W^T / temperature), and a row's teacher tokens I with log
+ * masses t (natural logarithms):
+ *   tail = 1   p_i = exp(t_i); behind the list the teacher has r = max(0, 1 -
+ *              sum_I p_i) and the student s = sum of q over the other tokens:
+ *              kl = sum_I p_i (log p_i - log q_i) + r (log r - log s)
+ *   tail = 0   p = softmax of t over I (t: log probabilities or logits):
+ *              kl = sum_I p_i (log p_i - log q_i)
+ *   teacher_ids   [N, K] int32, 1 <= K <= 256; a negative id is no entry, a
+ *                 token named twice has the sum of its masses
+ *   teacher_logp  [N, K] fp32; -inf is no mass
+ *   kl            [N] fp32, natural logarithms, not scaled by temperature^2
+ *   lse, rest_logp [N] fp32: log sum_v exp(z_v / temperature), and log s (-inf
+ *                 where the list names every token; r counts as 0 then)
+ *   student_logp  [N, K] fp32: log q of the teacher's tokens, 0 for no entry
+ * A row without an entry gets 0 in all of them; one that names a token of V or
+ * more gets NaN and sets FLCE_EBADTARGET.  After a time-out every row with a
+ * teacher is NaN.  log q and log s are formed relative to the row's largest
+ * logit and s not as a difference, so that kl is off by a few 2^-24 of its
+ * largest term only.
+ * Workspace (flce_topk_distill_workspace_bytes): as flce_logprobs without
+ * alternatives, 14 bytes per entry and 4 bytes per row and tile (128 columns in
+ * the chunked form) of the vocabulary.
+ */
+size_t flce_topk_distill_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t K);
+flce_status flce_topk_distill(const void* hidden, const void* weight,
+                              const int32_t* teacher_ids, const float* teacher_logp,
+                              int64_t N, int64_t H, int64_t V, int32_t K, float temperature,
+                              int32_t tail, float* kl, float* lse, float* rest_logp,
+                              float* student_logp, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
+ * Its gradient: of L = sum_n grad_kl[n] kl[n], with A = sum_I p_i + r,
+ *   dz_nv = grad_kl[n] (A q_v - p_v - [v not in I] r q_v / s) / temperature
+ *   grad_hidden = dz W  (bf16; rows without a teacher are +0.0),
+ *   grad_weight = dz^T X (fp32, or bf16 with FLCE_GW_BF16);
+ * either may be NULL.  lse, rest_logp and student_logp are those
+ * flce_topk_distill gave for the same inputs.  The teacher gets no gradient.
+ * Rounding, failures and workspace (flce_topk_distill_bwd_workspace_bytes) as
+ * flce_logprobs_bwd, and 12 + 2 K bytes per row.
+ */
+size_t flce_topk_distill_bwd_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t K,
+                                             uint32_t flags);
+flce_status flce_topk_distill_bwd(const void* hidden, const void* weight,
+                                  const int32_t* teacher_ids, const float* teacher_logp,
+                                  int64_t N, int64_t H, int64_t V, int32_t K, uint32_t flags,
+                                  float temperature, int32_t tail, const float* lse,
+                                  const float* rest_logp, const float* student_logp,
+                                  const float* grad_kl, void* grad_hidden,
+                                  float* grad_weight, void* workspace,
+                                  size_t workspace_bytes, void* stream);
 
 /*
  * Scaled embedding lookup, the other reader of a tied [V,H] weight:

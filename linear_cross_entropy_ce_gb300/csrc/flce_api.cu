@@ -22,6 +22,7 @@
 
 #include "flce.h"
 #include "flce_internal.h"
+#include "flce_listed.cuh"
 
 namespace {
 
@@ -65,6 +66,8 @@ cudaError_t device_state(DeviceState* out) {
     if ((e = gemm_prepare(dev)) != cudaSuccess) return e;
     if ((e = stream_prepare()) != cudaSuccess) return e;
     if ((e = embedding_prepare()) != cudaSuccess) return e;
+    if ((e = distill_prepare()) != cudaSuccess) return e;
+    if ((e = constrained_prepare()) != cudaSuccess) return e;
     if ((e = gemm_max_pairs(&d.pairs)) != cudaSuccess) return e;
     if (d.pairs < 1) return cudaErrorInvalidConfiguration;
     d.ready = true;
@@ -427,6 +430,7 @@ struct Job {
   const float* grad_logp = nullptr;
   const float* grad_entropy = nullptr;
   float temperature = 1.f;
+  const DistillGrad* distill = nullptr;   // JOB_PROBS_BWD of the distillation loss: targets, lse and grad_logp are its
   void* ws = nullptr;
   size_t ws_bytes = 0;
   void* stream = nullptr;
@@ -559,6 +563,10 @@ flce_status run(const Job& j) {
   else
     count_launches(1 + (fwd_only ? 0 : 1) + (j.kind == JOB_SHARD_BWD ? 0 : 1) + p.n_chunks * (norm ? 4 : 2) +
                    (norm ? 1 : 0) + (p.gw32 ? 1 : 0));
+  if (j.distill) {
+    count_launches(1 + p.n_chunks);   // rows, one patch a chunk
+    if (!chk(launch_distill_grad_rows(*j.distill, N, static_cast<int>(V), j.temperature, st))) return FLCE_ECUDA;
+  }
   if (front) {
     FrontArgs f;
     std::memset(&f, 0, sizeof(f));
@@ -608,6 +616,9 @@ flce_status run(const Job& j) {
                            j.lse, idx, st)))
       return FLCE_ECUDA;
     if (fwd_only) continue;
+    if (j.distill && !chk(launch_distill_patch(hdr, idx, c0, g.C, j.distill->K, g.V, p.ldz, j.distill->ids,
+                                               j.distill->patch, z, st)))
+      return FLCE_ECUDA;
     g.mode = MODE_BWD;
     g.counter = sync + p.tile_counters - 1;
     g.flags = sync + p.tile_counters;
@@ -660,6 +671,23 @@ flce_status fwd_bwd_on_workspace(const void* hidden, const void* weight, const i
                                  void* workspace, size_t workspace_bytes, void* stream) {
   return run(hidden, weight, targets, N, H, V, ignore_index, flags, loss, n_valid, row_loss, grad_hidden,
              grad_weight, workspace, workspace_bytes, stream, false);
+}
+}  // namespace flce
+
+namespace flce {
+flce_status run_distill_grad(const DistillGrad& d, const void* hidden, const void* weight, int64_t N, int64_t H,
+                             int64_t V, uint32_t flags, float temperature, void* grad_hidden, float* grad_weight,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  if (flags & ~FLCE_GW_BF16) return FLCE_EINVAL;
+  Job j;
+  j.kind = JOB_PROBS_BWD;
+  j.distill = &d;
+  j.hidden = hidden; j.weight = weight; j.targets = d.targets;
+  j.N = N; j.H = H; j.V = V; j.V_total = V; j.ii = -1; j.flags = flags;
+  j.temperature = temperature; j.lse = d.lse; j.grad_logp = d.grad;
+  j.grad_hidden = grad_hidden; j.grad_weight = grad_weight;
+  j.ws = workspace; j.ws_bytes = workspace_bytes; j.stream = stream;
+  return run(j);
 }
 }  // namespace flce
 

@@ -434,11 +434,86 @@ __device__ __forceinline__ void blank_tail(float (&v)[32], int j0, int ncol, flo
   }
 }
 
+// What a row's lists say of the columns of one part: which are listed (taken
+// out; their logits are written side by side, in order) and which are allowed.
+// Fetched before the accumulator is waited for, so that the loads cost no time
+// where the tile's main loop is longer than they are.
+struct PartLists {
+  uint32_t listed[GROUP_COLS / 32], allowed[GROUP_COLS / 32];
+  float* slot;
+};
+
+// Columns [c0, c0 + ncol) of chunk row grow; they lie in part c0 / 128, whose
+// entries before c0 are passed over.
+__device__ __forceinline__ PartLists part_lists(const GemmArgs& a, bool rv, int grow, int c0, int ncol) {
+  PartLists p;
+  const ListView& l = a.lists;
+#pragma unroll
+  for (int j = 0; j < GROUP_COLS / 32; ++j) {
+    p.listed[j] = 0u;
+    p.allowed[j] = 0xffffffffu;
+  }
+  p.slot = nullptr;
+  if (!rv || ncol <= 0) return p;
+  const long long row = static_cast<long long>(grow) * l.cap;
+  const int* at = l.start + static_cast<long long>(c0 / PART_COLS) * a.C + grow;
+  int e = at[0];
+  const int e1 = at[a.C];
+  if (l.mask) {
+    const uint32_t* words = l.mask + a.idx[a.c0 + grow] * l.mask_stride + c0 / 32;
+#pragma unroll
+    for (int j = 0; j < GROUP_COLS / 32; ++j)
+      if (j * 32 < ncol) p.allowed[j] = words[j];
+  }
+  if (e < e1) {
+    int first = e1;
+    for (; e < e1; ++e) {
+      const int at_col = l.id[row + e] - c0;
+      if (at_col < 0 || at_col >= ncol) continue;
+      first = min(first, e);
+#pragma unroll
+      for (int j = 0; j < GROUP_COLS / 32; ++j)
+        if (at_col / 32 == j) p.listed[j] |= 1u << (at_col % 32);
+    }
+    p.slot = l.z + row + first;
+  }
+  return p;
+}
+
+// The next 32 columns' words (registers have no index), around.
+__device__ __forceinline__ void turn_lists(PartLists& p) {
+  const uint32_t l = p.listed[0], w = p.allowed[0];
+#pragma unroll
+  for (int j = 0; j + 1 < GROUP_COLS / 32; ++j) {
+    p.listed[j] = p.listed[j + 1];
+    p.allowed[j] = p.allowed[j + 1];
+  }
+  p.listed[GROUP_COLS / 32 - 1] = l;
+  p.allowed[GROUP_COLS / 32 - 1] = w;
+}
+
+// 32 logits of a row: the listed ones are written out (unless that was done
+// already) and leave, with the forbidden ones.
+template <bool TAKE>
+__device__ __forceinline__ void treat_listed(float (&v)[32], uint32_t listed, uint32_t allowed, float*& slot) {
+  if (TAKE && __any_sync(0xffffffffu, listed != 0u)) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if ((listed >> k) & 1u) *slot++ = v[k];
+  }
+  const uint32_t keep = allowed & ~listed;
+  if (__any_sync(0xffffffffu, keep != 0xffffffffu)) {
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = (keep >> k) & 1u ? v[k] : -INFINITY;
+  }
+}
+
 // Statistics of one row and part.  Bound by the tensor cores from H = 2048 up
 // (4096 tokens at 2048 x 32000 in three segments: 290 us, 1.85 PFLOP/s); at 8 K
 // blocks a tile takes 2.9 us for 2.2 us of MMAs.
+template <bool LISTED>
 __device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, const Unit& t, int row0, int col0,
-                                          uint32_t tbase, int r) {
+                                          uint32_t tbase, int r, PartLists& pl) {
   const int grow = row0 + r;
   const bool rv = grow < s.Cl;
   const int c0 = t.n0 + col0;
@@ -452,10 +527,18 @@ __device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, con
   Stat st = {-INFINITY, 0.f, 0.f};
 #pragma unroll 1
   for (int j = 0; j < GROUP_COLS / 32; ++j) {
-    if (j * 32 >= ncol) break;                    // uniform
+    if (j * 32 >= ncol) {                         // uniform
+      if constexpr (!LISTED) break;
+      turn_lists(pl);
+      continue;
+    }
     float v[32];
     ptx::tmem_ld32(tbase + j * 32, v);
     pick_target(v, tl, j * 32, ztv);
+    if constexpr (LISTED) {
+      treat_listed<true>(v, pl.listed[0], pl.allowed[0], pl.slot);
+      turn_lists(pl);
+    }
     if (all) store_f32x32(zrow + j * 32, v);
     blank_tail(v, j * 32, ncol, -INFINITY);
     st = merge(st, stats32(v, a.c2), a.c2);
@@ -473,6 +556,10 @@ __device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, con
   for (int j = 0; j * 32 < ncol; ++j) {   // uniform over the warp
     float v[32];
     ptx::tmem_ld32(tbase + j * 32, v);
+    if constexpr (LISTED) {
+      treat_listed<false>(v, pl.listed[0], pl.allowed[0], pl.slot);
+      turn_lists(pl);
+    }
     if (keep) store_f32x32(zrow + j * 32, v);
   }
 }
@@ -566,8 +653,10 @@ static_assert(sizeof(Exchange) <= EPI_GROUPS * STG_BYTES, "fits in the staging a
 
 // Statistics of one row and part from both halves' registers; false on abort.
 // bar: the named barrier of the part's two warpgroups.
+template <bool LISTED>
 __device__ __forceinline__ bool epi_stats_seg(const GemmArgs& a, const Shape& s, const Unit& t, int row0, int grp,
-                                              float (&z)[2][32], int r, bool ok, float (*ex)[3][BM], uint32_t bar) {
+                                              float (&z)[2][32], int r, bool ok, float (*ex)[3][BM], uint32_t bar,
+                                              PartLists& pl) {
   const int grow = row0 + r;
   const bool rv = grow < s.Cl;
   const int c0 = t.n0 + grp * QUARTER, part = (t.n0 + grp / 2 * PART_COLS) / PART_COLS;
@@ -581,6 +670,7 @@ __device__ __forceinline__ bool epi_stats_seg(const GemmArgs& a, const Shape& s,
   for (int j = 0; j < 2; ++j) {
     if (j * 32 >= ncol) break;                    // uniform
     pick_target(z[j], tl, j * 32, ztv);
+    if constexpr (LISTED) treat_listed<true>(z[j], pl.listed[j], pl.allowed[j], pl.slot);
     if (all) store_f32x32(zrow + j * 32, z[j]);
     blank_tail(z[j], j * 32, ncol, -INFINITY);
     mine = merge(mine, stats32(z[j], a.c2), a.c2);
@@ -844,12 +934,14 @@ __device__ __forceinline__ bool epi_dx_split(const GemmArgs& a, const Shape& s, 
 // What a kernel is for: the loss, or the two modes of the token log
 // probabilities (MODE_STATS, MODE_DZ), whose kernels of their own leave the
 // loss kernel's registers alone; SEGMENTED those with long sums.
-enum Kind : int { K_LOSS = 0, K_PROBS = 1, K_SEGMENTED = 2 };
+// LISTED: MODE_STATS of rows with lists, in both forms.
+enum Kind : int { K_LOSS = 0, K_PROBS = 1, K_SEGMENTED = 2, K_LISTED = 3, K_LISTED_SEGMENTED = 4 };
 
 template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     flce_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
-  constexpr bool PROBS = KIND != K_LOSS, SEG = KIND == K_SEGMENTED;
+  constexpr bool PROBS = KIND != K_LOSS, SEG = KIND == K_SEGMENTED || KIND == K_LISTED_SEGMENTED;
+  constexpr bool LISTED = KIND == K_LISTED || KIND == K_LISTED_SEGMENTED;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stg = smem + STAGES * STAGE_BYTES;
@@ -1065,6 +1157,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     uint32_t acc = 0, acc_phase = 0, buf = 0;
     for (int u = pair0; u < s.units; u += npairs) {
       const Unit t = decode_unit<PROBS>(a, s, u);
+      PartLists pl;
+      if constexpr (LISTED) {
+        const int grow = t.m0 + half + r, c0 = t.n0 + grp * QUARTER;
+        pl = part_lists(a, grow < s.Cl, grow, c0, min(QUARTER, a.V - c0));
+      }
       float z[2][32];
 #pragma unroll
       for (int k = 0; k < 32; ++k) z[0][k] = z[1][k] = 0.f;
@@ -1087,8 +1184,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         if (acc == 0) acc_phase ^= 1u;
       }
       const int row0 = t.m0 + half;
-      if (a.mode == MODE_STATS) {
-        ok = epi_stats_seg(a, s, t, row0, grp, z, r, ok, ex->v[buf], EPI_BAR_SET + static_cast<uint32_t>(grp / 2));
+      if (LISTED || a.mode == MODE_STATS) {
+        ok = epi_stats_seg<LISTED>(a, s, t, row0, grp, z, r, ok, ex->v[buf], EPI_BAR_SET + static_cast<uint32_t>(grp / 2),
+                                   pl);
         buf ^= 1u;
       } else if (ok) {
         epi_dz_seg(a, s, t, row0, grp, z, r);
@@ -1147,6 +1245,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             if (t.n0 + col0 + q4 * 32 < a.H) ptx::prefetch_l2(gp + q4 * 32);
         }
       }
+      PartLists pl;
+      if constexpr (LISTED) {
+        const int grow = t.m0 + half + r, c0 = t.n0 + col0;
+        pl = part_lists(a, grow < s.Cl, grow, c0, min(GROUP_COLS, a.V - c0));
+      }
       ok = wait_phase(&ctl->tfull[set], acc_phase, ctl, to, true, hdr, W_TMEM_FULL, u | (set << 24));
       if (!ptx::named_bar_and(sbar, SET_THREADS, ok)) break;
       ptx::tc_fence_after();
@@ -1154,7 +1257,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       const int row0 = t.m0 + half;
       bool cont = true;
       if constexpr (PROBS) {
-        if (a.mode == MODE_STATS) epi_stats(a, s, t, row0, col0, tbase, r);
+        if (LISTED || a.mode == MODE_STATS) epi_stats<LISTED>(a, s, t, row0, col0, tbase, r, pl);
         else epi_dz(a, s, t, row0, col0, tbase, r);
       } else if (t.kind == U_LOGITS)
         epi_logits(a, s, t, row0, col0, tbase, r);
@@ -1198,6 +1301,10 @@ cudaError_t gemm_prepare(int /*device*/) {
     e = cudaFuncSetAttribute(flce_gemm_kernel<K_PROBS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(flce_gemm_kernel<K_SEGMENTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(flce_gemm_kernel<K_LISTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(flce_gemm_kernel<K_LISTED_SEGMENTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   return e;
 }
 
@@ -1228,6 +1335,9 @@ cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps& m, int grid, cudaStre
   attr.val.programmaticStreamSerializationAllowed = dependent ? 1 : 0;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
+  if (a.mode == MODE_STATS && a.listed)
+    return launch_result(a.seg_kb * BK < a.H ? cudaLaunchKernelEx(&cfg, flce_gemm_kernel<K_LISTED_SEGMENTED>, m, a)
+                                             : cudaLaunchKernelEx(&cfg, flce_gemm_kernel<K_LISTED>, m, a));
   if (a.mode == MODE_STATS || a.mode == MODE_DZ)
     return launch_result(a.seg_kb * BK < a.H ? cudaLaunchKernelEx(&cfg, flce_gemm_kernel<K_SEGMENTED>, m, a)
                                            : cudaLaunchKernelEx(&cfg, flce_gemm_kernel<K_PROBS>, m, a));

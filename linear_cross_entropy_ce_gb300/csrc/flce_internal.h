@@ -8,6 +8,8 @@
 #include <algorithm>
 #include <cmath>
 
+#include "flce_lists.cuh"
+
 namespace flce {
 
 // Device status word bits (workspace header word 0).
@@ -102,6 +104,8 @@ struct GemmArgs {
   uint32_t* group_max;  //   [C][group_stride] largest part max of each of K groups of parts
   int group_stride;     //   K rounded up to 4
   const DzRow* rowc;    // DZ: [C] (rows past the valid ones hold zeros)
+  int listed;           // STATS: lists hold tokens that are treated apart
+  ListView lists;
 };
 
 // Tensor maps of one launch.  LOGITS: a0 = Xc (K-major), b0 = W (K-major).
@@ -237,12 +241,23 @@ struct StreamArgs {
 struct StreamMaps {
   CUtensorMap x, w[4];     // w[k]: boxes of 128 >> k weight rows
 };
+struct StreamLists {
+  ListView lists;
+  RuleView rules;
+};
 int stream_ctas(long long V, int sms);
 int stream_max_tiles(long long V, int ctas);
 int stream_tokens(int N);   // N padded to the tile sizes of the kernel
 cudaError_t stream_prepare();
 cudaError_t embedding_prepare();   // flce_embedding.cu
 cudaError_t launch_stream(const StreamArgs& a, const StreamMaps& m, cudaStream_t s);
+// The same with the listed tokens of each row under rules (flce_stream_ruled.cu),
+// and the kernel alone with them taken out (flce_stream_taken.cu); both are
+// launched while the kernel that makes the lists runs.
+cudaError_t stream_ruled_prepare();
+cudaError_t stream_taken_prepare();
+cudaError_t launch_stream_ruled(const StreamArgs& a, const StreamMaps& m, const StreamLists& l, cudaStream_t s);
+cudaError_t launch_stream_taken(const StreamArgs& a, const StreamMaps& m, const StreamLists& l, cudaStream_t s);
 
 // Token log probabilities (flce_logprobs.cu).
 // The first launch of a call of one chunk and at most FRONT_MAX_TOKENS tokens;
@@ -269,10 +284,29 @@ struct FrontArgs {
   uint16_t* grad_hidden;              // or null
 };
 cudaError_t launch_probs_front(const FrontArgs& a, cudaStream_t s);
+cudaError_t launch_clear_bounds(uint32_t* bound, uint32_t* group_max, int stride, int K, int C, cudaStream_t s);
 cudaError_t launch_gather_dz(const uint16_t* hidden, const int* targets, const int* hdr, const int* idx,
                              long long c0, int C, int H, float temperature, const float* lse, const float* entropy,
                              const float* grad_logp, const float* grad_entropy, uint16_t* xc, int* tc, DzRow* rowc,
                              cudaStream_t s);
+// The gradient of the distillation loss (flce_distill.cu): that of the log
+// probabilities with other row constants, and dz overwritten at listed places.
+struct DistillGrad {
+  const int* ids;                 // [N][K] teacher tokens
+  const float* logp;
+  int K, tail;
+  const float *lse_in, *rest_logp, *student_logp, *grad_kl;
+  int* targets;                   // made from these
+  float *lse, *grad;
+  uint16_t* patch;                // [N][K] dz at the teacher's tokens, bf16
+};
+cudaError_t launch_distill_grad_rows(const DistillGrad& d, long long N, int V, float temperature, cudaStream_t s);
+cudaError_t launch_distill_patch(const int* hdr, const int* idx, long long c0, int C, int K, int V, long long ldz,
+                                 const int* ids, const uint16_t* patch, uint16_t* z, cudaStream_t s);
+cudaError_t distill_prepare();
+cudaError_t constrained_prepare();
+// seg_kb, the time limit and the tensor maps of a streaming call.
+bool stream_setup(StreamArgs* a, StreamMaps* m, const void* hidden, const void* weight);
 cudaError_t launch_dx_reduce(const int* hdr, const int* idx, long long c0, int C, int H, int splits, const float* parts,
                              uint16_t* grad_hidden, cudaStream_t s);
 cudaError_t launch_mark_failed(const int* hdr, uint16_t* grad_hidden, float* grad_weight, int gw_bf16,

@@ -24,16 +24,12 @@
 #include "flce.h"
 #include "flce_internal.h"
 #include "flce_ptx.cuh"
+#include "flce_rows.cuh"
 #include "flce_softmax.cuh"
 #include "flce_topk.cuh"
 
 namespace flce {
 namespace {
-
-__device__ __forceinline__ int chunk_rows(const int* hdr, long long c0, int C) {
-  const long long rem = static_cast<long long>(hdr[HDR_NVALID]) - c0;
-  return rem <= 0 ? 0 : (rem >= C ? C : static_cast<int>(rem));
-}
 
 // The constants of MODE_DZ of token n (see DzRow).
 __device__ __forceinline__ DzRow dz_row(float temperature, float lse, const float* entropy, const float* grad_logp,
@@ -200,9 +196,6 @@ __global__ void __launch_bounds__(FRONT_THREADS) probs_front_kernel(const FrontA
 // warps and one part at a time).  Blocks past the chunk's (last chunk only) write the rows left out:
 // 0 for an ignored token, NaN for a target outside [0, V); and after a pipeline
 // time-out NaN for every other row, those of finished chunks too.
-constexpr int ROWS_WARPS = 32;
-constexpr int ROWS_BATCH = 4;
-
 struct RowArgs {
   const int* hdr;
   const int* idx;
@@ -244,29 +237,9 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) logprob_rows_kernel(const Row
   const int Cl = chunk_rows(a.hdr, a.c0, a.C);
   const int r = blockIdx.x * 32 + lane;
   if (static_cast<int>(blockIdx.x) * 32 >= Cl) return;
-  Stat acc = {-INFINITY, 0.f, 0.f};
-  if (r < Cl) {
-    const size_t np = static_cast<size_t>(a.nparts) * a.C;
-    for (int p0 = w; p0 < a.nparts; p0 += ROWS_BATCH * ROWS_WARPS) {
-      Stat q[ROWS_BATCH];
-#pragma unroll
-      for (int k = 0; k < ROWS_BATCH; ++k) {
-        const int p = p0 + k * ROWS_WARPS;
-        const float* f = a.stats + static_cast<size_t>(p) * a.C + r;
-        q[k] = p < a.nparts ? Stat{f[0], f[np], f[2 * np]} : Stat{-INFINITY, 0.f, 0.f};
-      }
-      static_assert(ROWS_BATCH == 4, "pairwise");
-      acc = merge(acc, merge(merge(q[0], q[1], a.c2), merge(q[2], q[3], a.c2), a.c2), a.c2);
-    }
-  }
-  part[w][lane] = acc;
-#pragma unroll
-  for (int o = ROWS_WARPS / 2; o > 0; o >>= 1) {   // fixed order
-    __syncthreads();
-    if (w < o) part[w][lane] = merge(part[w][lane], part[w + o][lane], a.c2);
-  }
+  merge_parts(a.stats, a.nparts, a.C, a.c2, r, r < Cl, lane, w, part);
   if (w != 0 || r >= Cl) return;
-  acc = part[0][lane];
+  Stat acc = part[0][lane];
   // after a pipeline time-out the statistics are not to be trusted
   if (a.hdr[HDR_STATUS] & STATUS_TIMEOUT) acc.m = __int_as_float(0x7fc00000);
   const float l2s = log2f(acc.s);
@@ -281,8 +254,6 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS) logprob_rows_kernel(const Row
 // then the K best of their logits by (value, id).  The loads of eight groups
 // (one or two parts) are in flight at a time.  Latency: 20 alternatives of 723
 // rows over 1002 parts take 20 us.
-constexpr int TOP_WARPS = 4;
-constexpr int TOP_BATCH = 8;
 __global__ void __launch_bounds__(32 * TOP_WARPS)
     logprob_top_kernel(const int* hdr, const int* idx, long long c0, int C, int V, long long ldz, int nparts, int K,
                        const float* stats, const float* zf, const float2* ml, float c2, int* top_ids,
@@ -301,41 +272,7 @@ __global__ void __launch_bounds__(32 * TOP_WARPS)
     }
     return;
   }
-  TopK best;
-  best.clear();
-  for (int p0 = w * 32; p0 < nparts; p0 += TOP_BATCH * TOP_WARPS * 32) {
-    float x[TOP_BATCH];
-    int id[TOP_BATCH];
-#pragma unroll
-    for (int k = 0; k < TOP_BATCH; ++k) {
-      const int p = p0 + k * (TOP_WARPS * 32) + lane;
-      x[k] = p < nparts ? stats[static_cast<size_t>(p) * C + r] : 0.f;
-      id[k] = p < nparts ? p : TopK::NONE;
-    }
-    best.offer_all(x, id, K, lane);
-  }
-  best.merge_block<TOP_WARPS>(sv, si, lane, w);   // every warp holds the K best parts
-  const int parts = best.id;
-  // K parts hold a logit of at least the K-th part's max: a smaller one is not
-  // among the K best (nothing is left out where fewer parts are numbers)
-  const float least = __shfl_sync(0xffffffffu, best.v, K - 1);
-  best.clear();
-  const float* zr = zf + static_cast<size_t>(r) * ldz;
-  for (int j = w; j < K; j += 2 * TOP_WARPS) {
-    float x[TOP_BATCH];
-    int id[TOP_BATCH];
-#pragma unroll
-    for (int k = 0; k < TOP_BATCH; ++k) {
-      const int jj = j + (k / 4) * TOP_WARPS;
-      const int p = __shfl_sync(0xffffffffu, parts, jj & 31);
-      const long long at = static_cast<long long>(p) * PART_COLS + (k % 4) * 32 + lane;
-      const bool in = jj < K && p != TopK::NONE && at < V;
-      x[k] = in ? zr[at] : 0.f;
-      id[k] = in && x[k] >= least ? static_cast<int>(at) : TopK::NONE;
-    }
-    best.offer_all(x, id, K, lane);
-  }
-  best.merge_block<TOP_WARPS>(sv, si, lane, w);
+  TopK best = top_of_parts(stats, zf + static_cast<size_t>(r) * ldz, nparts, C, V, K, r, lane, w, sv, si);
   if (w == 0 && lane < K) {
     const long long row = idx[c0 + r];
     const bool some = best.id != TopK::NONE;   // false only where fewer than K logits are numbers
@@ -494,6 +431,19 @@ StreamPlan stream_plan(long long N, long long V, int K, int sms) {
 
 }  // namespace
 
+bool stream_setup(StreamArgs* a, StreamMaps* m, const void* hidden, const void* weight) {
+  a->seg_kb = segment_blocks(a->H);
+  a->timeout_ns = wait_timeout_ns();
+  if (const unsigned long long t = take_armed_stall()) {
+    a->debug_stall = 1;
+    a->timeout_ns = t;
+  }
+  const unsigned long long hb = static_cast<unsigned long long>(a->H) * 2;
+  bool ok = make_map(&m->x, hidden, a->H, a->N, hb, BK, stream_tokens(a->N));
+  for (int k = 0; k < 4; ++k) ok = ok && make_map(&m->w[k], weight, a->H, a->V, hb, BK, 128u >> k);
+  return ok;
+}
+
 bool bad_temperature(float t) { return !(t > 0.f) || !std::isfinite(t) || !std::isfinite(LOG2E / t); }
 
 cudaError_t launch_dx_reduce(const int* hdr, const int* idx, long long c0, int C, int H, int splits, const float* parts,
@@ -511,6 +461,11 @@ cudaError_t launch_probs_front(const FrontArgs& a, cudaStream_t s) {
   // few tokens: several blocks share a row, 1024 columns each
   const unsigned slices = a.N <= 2048 ? static_cast<unsigned>(std::min<long long>(cdiv(a.H, 1024), 64)) : 1;
   probs_front_kernel<<<dim3(static_cast<unsigned>(cdiv(a.N, FRONT_TOKENS)), slices), FRONT_THREADS, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_clear_bounds(uint32_t* bound, uint32_t* group_max, int stride, int K, int C, cudaStream_t s) {
+  clear_bounds_kernel<<<152, 256, 0, s>>>(bound, group_max, stride, K, C);
   return cudaGetLastError();
 }
 
@@ -559,15 +514,9 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
     StreamArgs a;
     std::memset(&a, 0, sizeof(a));
     a.N = static_cast<int>(N); a.H = static_cast<int>(H); a.V = static_cast<int>(V); a.K = top_k;
-    a.seg_kb = segment_blocks(H);
     a.ctas = p.ctas;
     a.c2 = LOG2E / temperature;
     a.ii = ignore_index;
-    a.timeout_ns = wait_timeout_ns();
-    if (const unsigned long long t = take_armed_stall()) {
-      a.debug_stall = 1;
-      a.timeout_ns = t;
-    }
     a.targets = targets;
     a.hdr = hdr;
     a.zt = at<float>(workspace, p.o_zt);
@@ -582,10 +531,7 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
     a.fail = at<int>(workspace, p.o_fail);
     a.logp = logp; a.entropy = entropy; a.lse = lse; a.top_ids = top_ids; a.top_logp = top_logp;
     StreamMaps m;
-    const unsigned long long hb = static_cast<unsigned long long>(H) * 2;
-    bool ok = make_map(&m.x, hidden, H, N, hb, BK, stream_tokens(a.N));
-    for (int k = 0; k < 4; ++k) ok = ok && make_map(&m.w[k], weight, H, V, hb, BK, 128u >> k);
-    if (!ok) return FLCE_ECUDA;
+    if (!stream_setup(&a, &m, hidden, weight)) return FLCE_ECUDA;
     const ProfScope prof = prof_launch_begin(st);
     const cudaError_t e = launch_stream(a, m, st);
     prof_launch_end(prof, MODE_STATS, st);
@@ -666,8 +612,7 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
                                      g.V, st)))
       return FLCE_ECUDA;
     if (!front && g.bound) {
-      clear_bounds_kernel<<<152, 256, 0, st>>>(g.bound, g.group_max, g.group_stride, top_k, g.C);
-      if (!chk(cudaGetLastError())) return FLCE_ECUDA;
+      if (!chk(launch_clear_bounds(g.bound, g.group_max, g.group_stride, top_k, g.C, st))) return FLCE_ECUDA;
     }
     if (!chk(gemm_launch(g, m, grid, st, front))) return FLCE_ECUDA;
     ra.c0 = g.c0;

@@ -41,6 +41,15 @@ class PlanInfo(ctypes.Structure):
                 ("vocab_tiles", ctypes.c_int32), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class _Constraints(ctypes.Structure):
+    _fields_ = [("history", ctypes.c_void_p), ("history_len", ctypes.c_int64), ("history_stride", ctypes.c_int64),
+                ("history_lens", ctypes.c_void_p), ("prompt_lens", ctypes.c_void_p),
+                ("repetition_penalty", ctypes.c_void_p), ("frequency_penalty", ctypes.c_void_p),
+                ("presence_penalty", ctypes.c_void_p), ("bias_ids", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("n_bias", ctypes.c_int64), ("bias_ids_stride", ctypes.c_int64), ("bias_stride", ctypes.c_int64),
+                ("mask", ctypes.c_void_p), ("mask_stride", ctypes.c_int64)]
+
+
 def library() -> ctypes.CDLL:
     """Load libflce.so (built in-tree by ``linear_cross_entropy_ce_gb300.build``)."""
     global _lib
@@ -98,6 +107,20 @@ def library() -> ctypes.CDLL:
     lib.flce_logprobs_bwd_workspace_bytes.restype = sz
     lib.flce_logprobs_bwd.argtypes = [vp, vp, vp, i64, i64, i64, i32, u32, f32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.flce_logprobs_bwd.restype = ctypes.c_int
+    lib.flce_constrained_workspace_bytes.argtypes = [i64, i64, i64, i32, i64, i64]
+    lib.flce_constrained_workspace_bytes.restype = sz
+    lib.flce_constrained_logprobs.argtypes = [vp, vp, vp, i64, i64, i64, i32, f32, i32, ctypes.POINTER(_Constraints),
+                                              vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.flce_constrained_logprobs.restype = ctypes.c_int
+    lib.flce_topk_distill_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    lib.flce_topk_distill_workspace_bytes.restype = sz
+    lib.flce_topk_distill.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, f32, i32, vp, vp, vp, vp, vp, sz, vp]
+    lib.flce_topk_distill.restype = ctypes.c_int
+    lib.flce_topk_distill_bwd_workspace_bytes.argtypes = [i64, i64, i64, i32, u32]
+    lib.flce_topk_distill_bwd_workspace_bytes.restype = sz
+    lib.flce_topk_distill_bwd.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, u32, f32, i32, vp, vp, vp, vp, vp, vp, vp,
+                                          sz, vp]
+    lib.flce_topk_distill_bwd.restype = ctypes.c_int
     lib.flce_embedding.argtypes = [vp, vp, i64, i64, i64, i32, f32, vp, vp]
     lib.flce_embedding.restype = ctypes.c_int
     lib.flce_embedding_bwd_workspace_bytes.argtypes = [i64, i64, i64]
@@ -649,6 +672,269 @@ class LinearLogProbs(torch.nn.Module):
 
     def forward(self, hidden: torch.Tensor, targets: torch.Tensor):
         return linear_logprobs(hidden, self.weight, targets, self.ignore_index, self.temperature)
+
+
+# ---------------------------------------------------------------------------
+# the next token under constraints
+# ---------------------------------------------------------------------------
+
+def _check_head(hidden, weight):
+    if not (hidden.is_cuda and weight.is_cuda):
+        raise ValueError("hidden and weight must be CUDA tensors")
+    if hidden.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
+        raise TypeError("hidden and weight must be bfloat16")
+    if hidden.dim() != 2 or weight.dim() != 2 or weight.shape[1] != hidden.shape[1]:
+        raise ValueError("expected hidden [N,H], weight [V,H]")
+    if not (hidden.is_contiguous() and weight.is_contiguous()):
+        raise ValueError("hidden and weight must be contiguous")
+    return hidden.shape[0], hidden.shape[1], weight.shape[0], _check_same_device(hidden, weight)
+
+
+def _rows_of(t, name, dtype, rows, device) -> int:
+    """Row stride of a [rows, *] matrix whose rows are contiguous (0: one row for all, as expand gives)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError(f"{name} must be a matrix of {rows} rows")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.stride(0)
+
+
+def _row_values(t, name, dtype, rows, device):
+    """The address of a contiguous vector of one value per row, or of nothing."""
+    if t is None:
+        return None
+    _check_buffer(t, name, (rows,), dtype, device)
+    return t.data_ptr()
+
+
+def constrained_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: Optional[torch.Tensor] = None,
+                         ignore_index: int = -100, *, history: Optional[torch.Tensor] = None,
+                         history_lens: Optional[torch.Tensor] = None, prompt_lens: Optional[torch.Tensor] = None,
+                         repetition_penalty: Optional[torch.Tensor] = None,
+                         frequency_penalty: Optional[torch.Tensor] = None,
+                         presence_penalty: Optional[torch.Tensor] = None, bias_ids: Optional[torch.Tensor] = None,
+                         bias: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                         temperature: float = 1.0, top_k: int = 0, entropy: bool = True,
+                         workspace: Optional[torch.Tensor] = None, out: Optional[dict] = None, stream=None) -> dict:
+    """:func:`token_logprobs` of logits that penalties, biases and a mask have changed, as a decode step samples them.
+
+    For row n and token v, in this order: a token of the row's history has its
+    logit divided by ``repetition_penalty[n]`` where it is positive, else
+    multiplied; one that its output holds c > 0 times loses
+    ``frequency_penalty[n] * c + presence_penalty[n]``; a token that
+    ``bias_ids[n]`` names gets ``bias[n]`` added (of one named twice the last
+    entry holds); a token whose bit in ``mask`` is not set is forbidden.
+
+    ``history`` is int32 [N, L] (ids outside [0, V) are padding), of whose rows
+    the first ``history_lens`` entries count, of these the first ``prompt_lens``
+    as the prompt; ``bias_ids`` and ``bias`` are int32 and fp32 [N, B]; ``mask``
+    is int32 [N, ceil(V / 32)], bit v % 32 of word v // 32; the penalties and
+    lengths are [N].  The matrices' rows may be strided, or one row expanded.
+
+    Returns what :func:`token_logprobs` does; without ``targets`` every row
+    counts and ``logp`` is None.  A forbidden target has a log probability of
+    -inf, forbidden tokens are no alternatives (ids -1), and a row with nothing
+    left has ``lse`` -inf and entropy 0.  There is no gradient."""
+    N, H, V, dev = _check_head(hidden, weight)
+    if targets is not None:
+        _check_buffer(targets, "targets", (N,), torch.int32, dev)
+    top_k = int(top_k)
+    if not 0 <= top_k <= min(TOP_K_MAX, V):
+        raise ValueError(f"top_k must lie in [0, {min(TOP_K_MAX, V)}]")
+    c = _Constraints()
+    if history is not None:
+        c.history_stride = _rows_of(history, "history", torch.int32, N, dev)
+        c.history, c.history_len = history.data_ptr(), history.shape[1]
+    elif history_lens is not None or prompt_lens is not None:
+        raise ValueError("history_lens and prompt_lens need a history")
+    c.history_lens = _row_values(history_lens, "history_lens", torch.int32, N, dev)
+    c.prompt_lens = _row_values(prompt_lens, "prompt_lens", torch.int32, N, dev)
+    for name, t in (("repetition_penalty", repetition_penalty), ("frequency_penalty", frequency_penalty),
+                    ("presence_penalty", presence_penalty)):
+        if t is not None:
+            if history is None:
+                raise ValueError(f"{name} needs a history")
+            setattr(c, name, _row_values(t, name, torch.float32, N, dev))
+    if (bias_ids is None) != (bias is None):
+        raise ValueError("bias_ids and bias go together")
+    if bias is not None:
+        c.bias_ids_stride = _rows_of(bias_ids, "bias_ids", torch.int32, N, dev)
+        c.bias_stride = _rows_of(bias, "bias", torch.float32, N, dev)
+        if bias.shape != bias_ids.shape:
+            raise ValueError("bias_ids and bias must have one shape")
+        c.bias_ids, c.bias, c.n_bias = bias_ids.data_ptr(), bias.data_ptr(), bias.shape[1]
+    if mask is not None:
+        c.mask_stride = _rows_of(mask, "mask", torch.int32, N, dev)
+        if mask.shape[1] < (V + 31) // 32:
+            raise ValueError("mask must have a bit for every token")
+        c.mask = mask.data_ptr()
+    with _on(dev, stream) as st:
+        if workspace is None:
+            nb = library().flce_constrained_workspace_bytes(N, H, V, top_k, c.history_len, c.n_bias)
+            if nb == 0:
+                raise FlceError(FLCE_EINVAL, "workspace size")
+            workspace = new_workspace(nb, dev)
+        else:
+            _check_workspace(workspace, dev)
+        row = ((N,), torch.float32)
+        o, made = _outputs(out, {"logp": row if targets is not None else None, "lse": row,
+                                 "entropy": row if entropy else None,
+                                 "top_ids": ((N, top_k), torch.int32) if top_k else None,
+                                 "top_logp": ((N, top_k), torch.float32) if top_k else None}, dev)
+        _ok(library().flce_constrained_logprobs(_addr(hidden), _addr(weight), _addr(targets), N, H, V,
+                                                _ignored(ignore_index), float(temperature), top_k, ctypes.byref(c),
+                                                _addr(made["logp"]), _addr(made["entropy"]), _addr(made["lse"]),
+                                                _addr(made["top_ids"]), _addr(made["top_logp"]), _addr(workspace),
+                                                workspace.numel(), st), "flce_constrained_logprobs")
+    o["workspace"] = workspace
+    return o
+
+
+# ---------------------------------------------------------------------------
+# distillation from a teacher's top log probabilities
+# ---------------------------------------------------------------------------
+
+TEACHER_MAX = 256
+
+
+def _check_teacher(teacher_ids, teacher_logp, N, device) -> int:
+    if teacher_ids.dtype != torch.int32 or teacher_logp.dtype != torch.float32:
+        raise TypeError("teacher_ids must be int32, teacher_logp float32")
+    if teacher_ids.dim() != 2 or teacher_ids.shape[0] != N or teacher_logp.shape != teacher_ids.shape:
+        raise ValueError("expected teacher_ids [N,K], teacher_logp [N,K]")
+    if not (teacher_ids.is_contiguous() and teacher_logp.is_contiguous()):
+        raise ValueError("teacher_ids and teacher_logp must be contiguous")
+    if teacher_ids.device != device or teacher_logp.device != device:
+        raise ValueError("all tensors must be on one device")
+    K = teacher_ids.shape[1]
+    if not 1 <= K <= TEACHER_MAX:
+        raise ValueError(f"a row may have 1 to {TEACHER_MAX} teacher tokens")
+    return K
+
+
+def topk_distill(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor, teacher_logp: torch.Tensor, *,
+                 temperature: float = 1.0, tail: bool = True, workspace: Optional[torch.Tensor] = None,
+                 out: Optional[dict] = None, stream=None) -> dict:
+    """Kullback-Leibler divergence of ``softmax(hidden @ weight.T / temperature)`` from a teacher's list, per token.
+
+    ``teacher_ids`` (int32 [N, K], K <= 256; negative: no entry) and
+    ``teacher_logp`` (fp32 [N, K]) are a teacher's likeliest tokens and their log
+    probabilities at the same temperature, as :func:`token_logprobs` gives them
+    (``top_ids``, ``top_logp``).  With ``tail=True`` the mass that the list
+    leaves is compared with the student's behind it; with ``tail=False`` the
+    list is taken as the whole distribution (``softmax`` of ``teacher_logp``,
+    which may then be logits).
+
+    Returns fp32 ``kl`` [N] (not scaled by temperature squared), ``lse`` and
+    ``rest_logp`` [N] (the log of the student's mass behind the list), and
+    ``student_logp`` [N, K].  Rows without an entry hold 0; rows that name a
+    token of V or more hold NaN and set the status word."""
+    N, H, V, dev = _check_head(hidden, weight)
+    K = _check_teacher(teacher_ids, teacher_logp, N, dev)
+    with _on(dev, stream) as st:
+        if workspace is None:
+            nb = library().flce_topk_distill_workspace_bytes(N, H, V, K)
+            if nb == 0:
+                raise FlceError(FLCE_EINVAL, "workspace size")
+            workspace = new_workspace(nb, dev)
+        else:
+            _check_workspace(workspace, dev)
+        row = ((N,), torch.float32)
+        o, made = _outputs(out, {"kl": row, "lse": row, "rest_logp": row, "student_logp": ((N, K), torch.float32)}, dev)
+        _ok(library().flce_topk_distill(_addr(hidden), _addr(weight), _addr(teacher_ids), _addr(teacher_logp), N, H, V, K,
+                                        float(temperature), int(bool(tail)), _addr(made["kl"]), _addr(made["lse"]),
+                                        _addr(made["rest_logp"]), _addr(made["student_logp"]), _addr(workspace),
+                                        workspace.numel(), st), "flce_topk_distill")
+    o["workspace"] = workspace
+    return o
+
+
+def topk_distill_bwd(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor, teacher_logp: torch.Tensor,
+                     lse: torch.Tensor, rest_logp: torch.Tensor, student_logp: torch.Tensor, grad_kl: torch.Tensor, *,
+                     temperature: float = 1.0, tail: bool = True, grad_weight_dtype=torch.float32,
+                     need_hidden: bool = True, need_weight: bool = True, workspace: Optional[torch.Tensor] = None,
+                     out: Optional[dict] = None, stream=None) -> dict:
+    """Gradients of ``sum(grad_kl * kl)``; ``lse``, ``rest_logp`` and ``student_logp``
+    are those of :func:`topk_distill` on the same inputs.  Returns
+    ``grad_hidden`` (bf16 [N, H]) and ``grad_weight`` ([V, H], fp32 or bf16), or
+    only the one asked for.  The teacher gets no gradient."""
+    N, H, V, dev = _check_head(hidden, weight)
+    K = _check_teacher(teacher_ids, teacher_logp, N, dev)
+    if not (need_hidden or need_weight):
+        raise ValueError("need_hidden or need_weight must be set")
+    for name, t, shape in (("lse", lse, (N,)), ("rest_logp", rest_logp, (N,)), ("student_logp", student_logp, (N, K)),
+                           ("grad_kl", grad_kl, (N,))):
+        _check_buffer(t, name, shape, torch.float32, dev)
+    flags = _flags("mean", grad_weight_dtype) if need_weight else 0
+    with _on(dev, stream) as st:
+        if workspace is None:
+            nb = library().flce_topk_distill_bwd_workspace_bytes(N, H, V, K, flags)
+            if nb == 0:
+                raise FlceError(FLCE_EINVAL, "workspace size")
+            workspace = new_workspace(nb, dev)
+        else:
+            _check_workspace(workspace, dev)
+        o, made = _outputs(out, {"grad_hidden": ((N, H), torch.bfloat16) if need_hidden else None,
+                                 "grad_weight": ((V, H), grad_weight_dtype) if need_weight else None}, dev)
+        _ok(library().flce_topk_distill_bwd(_addr(hidden), _addr(weight), _addr(teacher_ids), _addr(teacher_logp), N, H,
+                                            V, K, flags, float(temperature), int(bool(tail)), _addr(lse),
+                                            _addr(rest_logp), _addr(student_logp), _addr(grad_kl),
+                                            _addr(made["grad_hidden"]), _addr(made["grad_weight"]), _addr(workspace),
+                                            workspace.numel(), st), "flce_topk_distill_bwd")
+    o["workspace"] = workspace
+    return o
+
+
+class _LinearTopKDistillFn(torch.autograd.Function):
+    """The backward recomputes the logits chunk by chunk from the saved row values."""
+
+    @staticmethod
+    def forward(ctx, hidden, weight, teacher_ids, teacher_logp, temperature, tail):
+        hidden, weight = hidden.contiguous(), weight.contiguous()
+        teacher_ids, teacher_logp = teacher_ids.contiguous(), teacher_logp.contiguous()
+        o = topk_distill(hidden, weight, teacher_ids, teacher_logp, temperature=temperature, tail=tail)
+        ctx.save_for_backward(hidden, weight, teacher_ids, teacher_logp, o["lse"], o["rest_logp"], o["student_logp"])
+        ctx.args = (temperature, tail)
+        _mark_leaves(ctx, hidden.device)
+        return o["kl"]
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_kl):
+        need_hidden, need_weight = ctx.needs_input_grad[:2]
+        if not (need_hidden or need_weight):
+            return None, None, None, None, None, None
+        _check_capture(ctx)
+        temperature, tail = ctx.args
+        o = topk_distill_bwd(*ctx.saved_tensors, grad_kl.to(torch.float32).contiguous(), temperature=temperature,
+                             tail=tail, grad_weight_dtype=ctx.saved_tensors[1].dtype, need_hidden=need_hidden,
+                             need_weight=need_weight)
+        return o["grad_hidden"], o["grad_weight"], None, None, None, None
+
+
+def linear_topk_distill(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.Tensor,
+                        teacher_logp: torch.Tensor, temperature: float = 1.0, tail: bool = True) -> torch.Tensor:
+    """:func:`topk_distill`'s ``kl`` (fp32 [N]) with autograd support for hidden and
+    weight; the teacher gets no gradient.  Captures as :func:`linear_logprobs`."""
+    return _LinearTopKDistillFn.apply(hidden, weight, teacher_ids, teacher_logp, temperature, tail)
+
+
+class LinearTopKDistill(torch.nn.Module):
+    """LM head as a distillation loss: ``kl = module(hidden, teacher_ids, teacher_logp)``;
+    the weight may be an embedding's (tied)."""
+
+    def __init__(self, weight: torch.Tensor, temperature: float = 1.0, tail: bool = True):
+        super().__init__()
+        self.weight = weight if isinstance(weight, torch.nn.Parameter) else torch.nn.Parameter(weight)
+        self.temperature = temperature
+        self.tail = tail
+
+    def forward(self, hidden: torch.Tensor, teacher_ids: torch.Tensor, teacher_logp: torch.Tensor) -> torch.Tensor:
+        return linear_topk_distill(hidden, self.weight, teacher_ids, teacher_logp, self.temperature, self.tail)
 
 
 # ---------------------------------------------------------------------------
