@@ -36,7 +36,7 @@
  * workspace must be 32-byte aligned where the call keeps logits or their
  * gradient in it: every call with gradients but flce_embedding_bwd, and
  * flce_logprobs and flce_constrained_logprobs of more than 128 tokens with top
- * alternatives.
+ * alternatives, flce_topk_distill of more than 128 tokens.
  *
  * Streams.  Each call only enqueues kernels on `stream` (a cudaStream_t
  * passed as void*, NULL = legacy default stream) and returns; nothing
@@ -383,8 +383,9 @@ flce_status flce_constrained_logprobs(const void* hidden, const void* weight,
  * logit and s not as a difference, so that kl is off by a few 2^-24 of its
  * largest term only.
  * Workspace (flce_topk_distill_workspace_bytes): as flce_logprobs without
- * alternatives, 14 bytes per entry and 4 bytes per row and tile (128 columns in
- * the chunked form) of the vocabulary.
+ * alternatives and 14 bytes per entry; up to 128 tokens 4 bytes per row and tile
+ * of the vocabulary, beyond 2 bytes per row and 128 of its tokens and 512 bytes
+ * per entry of one chunk's rows.
  */
 size_t flce_topk_distill_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t K);
 flce_status flce_topk_distill(const void* hidden, const void* weight,

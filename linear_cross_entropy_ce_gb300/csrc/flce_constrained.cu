@@ -26,10 +26,11 @@
 namespace flce {
 namespace {
 
-constexpr int RULE_THREADS = 512;
-constexpr int RULE_WARPS = RULE_THREADS / 32;
-constexpr int WINDOW_WORDS = 24576;   // of the vocabulary at a time: 786432 tokens, 192 KB with the words' ranks
-static_assert(WINDOW_WORDS * 32 % PART_COLS == 0, "windows end between parts");
+// Few rows: all of a block's latency counts, so it is wide; many rows: several
+// blocks an SM.  A thread keeps HELD ids and HELD words of the mask and bitmap
+// in registers, all loads at once.
+constexpr int HELD = 8;
+constexpr int STREAM_THREADS = 1024, CHUNK_THREADS = 512;
 
 struct RuleArgs {
   int V;
@@ -55,15 +56,21 @@ struct RuleArgs {
   long long cap;
 };
 
-// A block per row.  (57 ids at a vocabulary of 128256: see the streaming kernel,
-// which runs meanwhile.)
+// A block per row, in windows of 32 HELD THREADS tokens (262144 for few rows: one
+// window covers most vocabularies).  61 rows of 1500 ids at a vocabulary of
+// 256007 with masks 13 us, 2048 rows of up to 2947 ids at 128256 60.  (The bitmap in
+// memory, so that the blocks fit beside the streaming kernel's, took 53 us for the
+// former, longer than the first tile.)
 template <bool STREAM>
-__global__ void __launch_bounds__(RULE_THREADS) constrained_lists_kernel(const RuleArgs a) {
-  extern __shared__ uint32_t bits[];   // [window words] and their ranks
-  __shared__ int warp_sum[RULE_WARPS];
+__global__ void __launch_bounds__(STREAM ? STREAM_THREADS : CHUNK_THREADS, STREAM ? 1 : 2)
+    constrained_lists_kernel(const RuleArgs a) {
+  constexpr int THREADS = STREAM ? STREAM_THREADS : CHUNK_THREADS, WARPS = THREADS / 32;
+  constexpr int WINDOW = HELD * THREADS;   // words
+  constexpr int GROUPS = HELD * WARPS;     // of 32 words
+  extern __shared__ uint32_t bits[];       // [words of a window] the marked tokens, and the marked ones before each word
+  __shared__ int group[GROUPS];
+  __shared__ int sums[WARPS];
   const int tid = threadIdx.x, lane = tid % 32, w = tid / 32;
-  const int words = (a.V + 31) / 32, window = min(words, WINDOW_WORDS);
-  uint32_t* rank = bits + window;
   long long r = blockIdx.x, n = blockIdx.x;
   if constexpr (STREAM) {
     ptx::grid_launch_dependents();
@@ -73,118 +80,148 @@ __global__ void __launch_bounds__(RULE_THREADS) constrained_lists_kernel(const R
     if (r >= chunk_rows(a.hdr, a.c0, a.C)) return;
     n = a.idx[a.c0 + r];
   }
+  const int V = a.V, words = (V + 31) / 32, window = min(words, WINDOW);
+  uint32_t* rank = bits + window;
   const int* history = a.history + n * a.history_stride;
-  long long len = a.L, prompt = 0;
-  if (a.history_lens) len = max(0ll, min(a.L, static_cast<long long>(a.history_lens[n])));
-  if (a.prompt_lens) prompt = a.prompt_lens[n];
   const int* bias_ids = a.bias_ids + n * a.bias_ids_stride;
+  const uint32_t* mask = a.mask ? a.mask + n * a.mask_stride : nullptr;
+  int len = static_cast<int>(a.L), prompt = 0;
+  if (a.history_lens) len = max(0, min(len, a.history_lens[n]));
+  if (a.prompt_lens) prompt = a.prompt_lens[n];
   int* id = a.id + r * a.cap;
   int* seen = a.seen + r * a.cap;
   int* bias_at = a.bias_at ? a.bias_at + r * a.cap : nullptr;
   const int tiles = STREAM ? a.ctas * a.max_tiles : 0;
+  int held[HELD];
+#pragma unroll
+  for (int k = 0; k < HELD; ++k) held[k] = k * THREADS + tid < len ? history[k * THREADS + tid] : -1;
   int base = 0;   // listed tokens before this window
   for (int w0 = 0; w0 < words; w0 += window) {
     const int nw = min(window, words - w0);
-    const long long t0 = static_cast<long long>(w0) * 32, t1 = min(static_cast<long long>(a.V), t0 + nw * 32ll);
-    for (int i = tid; i < nw; i += RULE_THREADS) bits[i] = 0u;
+    uint32_t allowed[HELD];
+#pragma unroll
+    for (int k = 0; k < HELD; ++k)
+      allowed[k] = mask && k * THREADS + tid < nw ? mask[w0 + k * THREADS + tid] : 0xffffffffu;
+#pragma unroll
+    for (int k = 0; k < HELD; ++k)
+      if (k * THREADS + tid < nw) bits[k * THREADS + tid] = 0u;
     __syncthreads();
-    auto mark = [&](int x) {
-      if (x >= t0 && x < t1) atomicOr(bits + (x - t0) / 32, 1u << (x % 32));
+    const unsigned t0 = static_cast<unsigned>(w0) * 32u, span = min(static_cast<unsigned>(V) - t0, nw * 32u);
+    auto mark = [&](int x) {   // (negative ids are far above the span)
+      const unsigned at = static_cast<unsigned>(x) - t0;
+      if (at < span) atomicOr(bits + at / 32, 1u << (at % 32));
     };
+#pragma unroll
+    for (int k = 0; k < HELD; ++k) mark(held[k]);
 #pragma unroll 4
-    for (long long i = tid; i < len; i += RULE_THREADS) mark(history[i]);
-    for (int i = tid; i < a.B; i += RULE_THREADS) mark(bias_ids[i]);
+    for (int i = HELD * THREADS + tid; i < len; i += THREADS) mark(history[i]);
+    for (int i = tid; i < a.B; i += THREADS) mark(bias_ids[i]);
     __syncthreads();
-    // forbidden tokens leave; the words' ranks, a run of words per thread
-    const int each = (nw + RULE_THREADS - 1) / RULE_THREADS;
-    const int i0 = min(nw, tid * each), i1 = min(nw, i0 + each);
-    int sum = 0;
-    for (int i = i0; i < i1; ++i) {
-      uint32_t b = bits[i];
-      if (b != 0u && a.mask) bits[i] = b &= a.mask[n * a.mask_stride + w0 + i];
-      sum += __popc(b);
-    }
-    int incl = sum;
+    // Forbidden tokens leave; then the words' ranks, 32 words at a time by a warp.
+    uint32_t word[HELD];
+    int before[HELD];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
+    for (int k = 0; k < HELD; ++k) {
+      const int i = k * THREADS + tid;
+      word[k] = i < nw ? bits[i] & allowed[k] : 0u;
+      const int c = __popc(word[k]);
+      int incl = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      before[k] = incl - c;
+      if (lane == 31) group[k * WARPS + w] = incl;
     }
-    if (lane == 31) warp_sum[w] = incl;
     __syncthreads();
-    int before = base + incl - sum, total = 0;
+    // groups, in order: warp w sums HELD of them
+    static_assert(GROUPS / WARPS == HELD && HELD <= 32, "a lane per group");
+    {
+      const int g = w * HELD + lane;
+      const int c = lane < HELD ? group[g] : 0;
+      int incl = c;
 #pragma unroll
-    for (int k = 0; k < RULE_WARPS; ++k) {
-      if (k < w) before += warp_sum[k];
-      total += warp_sum[k];
+      for (int o = 1; o < HELD; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      if (lane == HELD - 1) sums[w] = incl;
+      __syncthreads();
+      int total = lane < WARPS ? sums[lane] : 0;
+      const int mine = __reduce_add_sync(0xffffffffu, lane < w ? total : 0);
+      if (lane < HELD) group[g] = base + mine + incl - c;
+      base += __reduce_add_sync(0xffffffffu, total);
     }
-    for (int i = i0; i < i1; ++i) {
-      rank[i] = static_cast<uint32_t>(before);
-      uint32_t b = bits[i];
-      while (b) {
-        const int k = __ffs(b) - 1;
-        b &= b - 1;
-        if (before < a.cap) {
-          id[before] = static_cast<int>(t0) + i * 32 + k;
-          seen[before] = 0;
-          if (bias_at) bias_at[before] = 0;
-        }
-        ++before;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < HELD; ++k) {
+      const int i = k * THREADS + tid;
+      if (i >= nw) continue;
+      int at = group[k * WARPS + w] + before[k];
+      rank[i] = static_cast<uint32_t>(at);
+      bits[i] = word[k];
+      for (uint32_t b = word[k]; b && at < a.cap; b &= b - 1, ++at) {
+        id[at] = static_cast<int>(t0) + i * 32 + __ffs(b) - 1;
+        seen[at] = 0;
+        if (bias_at) bias_at[at] = 0;
       }
     }
     __syncthreads();
-    // the place of a listed token, or -1
+    // the place of a listed token of this window, or -1
     auto place = [&](int x) {
-      if (x < t0 || x >= t1) return -1;
-      const int i = static_cast<int>(x - t0) / 32;
-      const uint32_t b = bits[i], below = (1u << (x % 32)) - 1u;
-      const int at = static_cast<int>(rank[i]) + __popc(b & below);
-      return (b >> (x % 32)) & 1u && at < a.cap ? at : -1;
+      const unsigned at = static_cast<unsigned>(x) - t0;
+      if (at >= span) return -1;
+      const uint32_t b = bits[at / 32];
+      const int p = static_cast<int>(rank[at / 32]) + __popc(b & ((1u << (at % 32)) - 1u));
+      return (b >> (at % 32)) & 1u && p < a.cap ? p : -1;
     };
-#pragma unroll 4
-    for (long long i = tid; i < len; i += RULE_THREADS) {
-      const int at = place(history[i]);
-      if (at < 0) continue;
+    auto count = [&](int i, int x) {
+      const int at = place(x);
+      if (at < 0) return;
       if (i < prompt) atomicOr(seen + at, static_cast<int>(0x80000000u));
       else atomicAdd(seen + at, 1);
-    }
-    for (int i = tid; i < a.B; i += RULE_THREADS) {
+    };
+#pragma unroll
+    for (int k = 0; k < HELD; ++k) count(k * THREADS + tid, held[k]);
+#pragma unroll 4
+    for (int i = HELD * THREADS + tid; i < len; i += THREADS) count(i, history[i]);
+    for (int i = tid; i < a.B; i += THREADS) {
       const int at = place(bias_ids[i]);
       if (at >= 0) atomicMax(bias_at + at, i + 1);
     }
     // where tiles or parts begin
     if constexpr (STREAM) {
-      for (int b = tid; b < tiles; b += RULE_THREADS) {
-        const Range g = range_of(a.V, a.ctas, b / a.max_tiles);
-        const int x = b % a.max_tiles < g.tiles ? g.start(b % a.max_tiles) : g.u1 * UNIT_ROWS;
-        if (x >= t0 && x < t1) {
-          const int i = static_cast<int>(x - t0) / 32;
-          a.start[r * (tiles + 1) + b] = static_cast<int>(rank[i]) + __popc(bits[i] & ((1u << (x % 32)) - 1u));
-        }
+      for (int b = tid; b < tiles; b += THREADS) {
+        const Range g = range_of(V, a.ctas, b / a.max_tiles);
+        const unsigned x = b % a.max_tiles < g.tiles ? g.start(b % a.max_tiles) : g.u1 * UNIT_ROWS;
+        const unsigned at = x - t0;
+        if (at < span)
+          a.start[r * (tiles + 1) + b] = static_cast<int>(rank[at / 32]) + __popc(bits[at / 32] & ((1u << (at % 32)) - 1u));
       }
     } else {
-      for (int p = w0 / (PART_COLS / 32) + tid; p < a.nparts && p * static_cast<long long>(PART_COLS) < t1; p += RULE_THREADS)
-        a.start[static_cast<long long>(p) * a.C + r] = static_cast<int>(rank[p * (PART_COLS / 32) - w0]);
+      for (int i = tid * (PART_COLS / 32); i < nw; i += THREADS * (PART_COLS / 32))
+        a.start[static_cast<long long>((w0 + i) / (PART_COLS / 32)) * a.C + r] = static_cast<int>(rank[i]);
     }
-    base += total;
-    __syncthreads();
+    if (w0 + window < words) __syncthreads();
   }
   base = static_cast<int>(min(static_cast<long long>(base), a.cap));
-  if constexpr (STREAM) {
-    for (int b = tid; b <= tiles; b += RULE_THREADS) {
-      int x = a.V;
+  if constexpr (STREAM) {   // boundaries at the end of the vocabulary
+    for (int b = tid; b <= tiles; b += THREADS) {
+      int x = V;
       if (b < tiles) {
-        const Range g = range_of(a.V, a.ctas, b / a.max_tiles);
+        const Range g = range_of(V, a.ctas, b / a.max_tiles);
         x = b % a.max_tiles < g.tiles ? g.start(b % a.max_tiles) : g.u1 * UNIT_ROWS;
       }
-      if (x >= a.V) a.start[r * (tiles + 1) + b] = base;
+      if (x >= V) a.start[r * (tiles + 1) + b] = base;
     }
   } else if (tid == 0) {
     a.start[static_cast<long long>(a.nparts) * a.C + r] = base;
   }
   if (bias_at) {
+    __syncthreads();
     const float* bias = a.bias + n * a.bias_stride;
-    for (int i = tid; i < base; i += RULE_THREADS) {
+    for (int i = tid; i < base; i += THREADS) {
       const int at = __ldcg(bias_at + i);
       reinterpret_cast<float*>(bias_at)[i] = at > 0 ? bias[at - 1] : 0.f;
     }
@@ -206,49 +243,73 @@ struct RowsArgs {
   float2* ml;
 };
 
-// 32 rows of a chunk: the parts' statistics merged with a lane a row, then a
-// warp a row brings the listed logits in, under their rules, and leaves them so
-// for the alternatives.
-__global__ void __launch_bounds__(32 * ROWS_WARPS) constrained_rows_kernel(const RowsArgs a) {
-  __shared__ Stat part[ROWS_WARPS][32];
-  const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+// 8 rows of a chunk.  Eight warps merge the parts' statistics; three warps a row
+// meanwhile bring its listed logits under their rules, where they stay for the
+// alternatives, and into statistics of their own.  (2048 rows of 1900 entries
+// over 1002 parts 32 us, by a warp a row 62.)
+constexpr int ROW_SHARES = 3;
+constexpr int ROW_WARPS = ROWS8 * (1 + ROW_SHARES);
+__global__ void __launch_bounds__(32 * ROW_WARPS) constrained_rows_kernel(const RowsArgs a) {
+  __shared__ Stat part[32][ROWS8];
+  __shared__ Stat share[1 + ROW_SHARES][ROWS8];
+  __shared__ int hits[ROW_SHARES][ROWS8];
+  const int lane = threadIdx.x % 32, w = threadIdx.x / 32, k = w % ROWS8;
   ptx::grid_dependency_wait();
   const int Cl = chunk_rows(a.hdr, a.c0, a.C);
-  const int r0 = blockIdx.x * 32;
+  const int r0 = blockIdx.x * ROWS8;
   if (r0 >= Cl) return;
-  merge_parts(a.stats, a.nparts, a.C, a.c2, r0 + lane, r0 + lane < Cl, lane, w, part);
+  const long long r = r0 + k, at = r * a.lists.cap;
+  const bool valid = r < Cl;
+  const long long row = valid ? a.idx[a.c0 + r] : 0;
+  const int t = a.targets ? a.targets[row] : 0;
+  if (w < ROWS8) {
+    const Stat s = merge_parts8(a.stats, a.nparts, a.C, a.c2, r0, Cl, lane, w, part);
+    if (lane == 0) share[0][w] = s;
+  } else {
+    const int sub = w / ROWS8 - 1;
+    const RowRules rules = row_rules(a.rules, row);
+    const int n = valid ? static_cast<int>(min(
+        a.lists.cap, static_cast<long long>(a.lists.start[static_cast<long long>(a.nparts) * a.C + r]))) : 0;
+    float m = -INFINITY;
+    int hit = -1;
+#pragma unroll 4
+    for (int e = sub * 32 + lane; e < n; e += 32 * ROW_SHARES) {
+      const float z = ruled(a.lists.z[at + e], a.rules.seen[at + e], a.rules.bias ? a.rules.bias[at + e] : 0.f, rules);
+      a.lists.z[at + e] = z;
+      if (a.lists.id[at + e] == t) hit = e;
+      m = fmaxf(m, z);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    hit = __reduce_max_sync(0xffffffffu, hit);
+    Stat mine = {m, 0.f, 0.f};
+#pragma unroll 4
+    for (int e = sub * 32 + lane; e < n; e += 32 * ROW_SHARES) {   // what this lane has written
+      const float y = (a.lists.z[at + e] - m) * a.c2;              // NaN where all are -inf: no term
+      const float x = m == -INFINITY && y != y ? 0.f : ptx::ex2(y);
+      mine.s += x;
+      mine.d = fmaf(fmaxf(y, -1e30f), x, mine.d);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {   // fixed order
+      mine.s += __shfl_xor_sync(0xffffffffu, mine.s, o);
+      mine.d += __shfl_xor_sync(0xffffffffu, mine.d, o);
+    }
+    if (lane == 0) {
+      share[1 + sub][k] = mine;
+      hits[sub][k] = hit;
+    }
+  }
   __syncthreads();
-  const long long r = r0 + w;
-  if (r >= Cl) return;
-  const long long row = a.idx[a.c0 + r];
-  const int t = a.targets[row];
-  const RowRules rules = row_rules(a.rules, row);
-  const int n = static_cast<int>(min(a.lists.cap, static_cast<long long>(a.lists.start[static_cast<long long>(a.nparts) * a.C + r])));
+  if (w >= ROWS8 || !valid || lane != 0) return;
   float zt = a.zt[r];
   if (a.lists.mask && !((a.lists.mask[row * a.lists.mask_stride + t / 32] >> (t % 32)) & 1u)) zt = -INFINITY;
-  Stat mine = {-INFINITY, 0.f, 0.f};
-  const long long at = r * a.lists.cap;
-  for (int e0 = 0; e0 < n; e0 += 32) {
-    const int e = e0 + lane;
-    float z = -INFINITY;
-    bool hit = false;
-    if (e < n) {
-      z = ruled(a.lists.z[at + e], a.rules.seen[at + e], a.rules.bias ? a.rules.bias[at + e] : 0.f, rules);
-      a.lists.z[at + e] = z;
-      hit = a.lists.id[at + e] == t;
-      mine = merge(mine, Stat{z, z != z ? z : (z > -INFINITY ? 1.f : 0.f), 0.f}, a.c2);
-    }
-    const unsigned found = __ballot_sync(0xffffffffu, hit);
-    if (found) zt = __shfl_sync(0xffffffffu, z, __ffs(found) - 1);
-  }
+  Stat acc = share[0][k];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {   // fixed order; lane 0 holds the result
-    const Stat other = {__shfl_down_sync(0xffffffffu, mine.m, o), __shfl_down_sync(0xffffffffu, mine.s, o),
-                        __shfl_down_sync(0xffffffffu, mine.d, o)};
-    mine = merge(mine, other, a.c2);
+  for (int i = 0; i < ROW_SHARES; ++i) {
+    acc = merge(acc, share[1 + i][k], a.c2);
+    if (hits[i][k] >= 0) zt = a.lists.z[at + hits[i][k]];
   }
-  if (lane != 0) return;
-  Stat acc = merge(part[0][w], mine, a.c2);
   if (a.hdr[HDR_STATUS] & STATUS_TIMEOUT) acc.m = acc.s = __int_as_float(0x7fc00000);
   const float l2s = log2f(acc.s);
   const bool nan = acc.s != acc.s, nothing = acc.m == -INFINITY && acc.s == 0.f;
@@ -343,7 +404,7 @@ __global__ void __launch_bounds__(256) all_rows_kernel(int* targets, long long N
   for (long long i = blockIdx.x * 256ll + threadIdx.x; i < N; i += gridDim.x * 256ll) targets[i] = 0;
 }
 
-size_t rule_smem(long long V) { return size_t(std::min<long long>(cdiv(V, 32), WINDOW_WORDS)) * 8; }
+size_t rule_smem(long long V, int threads) { return size_t(std::min<long long>(cdiv(V, 32), HELD * threads)) * 8; }
 
 // Entries of a row at most.
 long long list_cap(long long V, long long L, long long B) { return std::max(1ll, std::min(V, L + B)); }
@@ -382,7 +443,7 @@ ConstrainedStream constrained_stream_plan(long long N, long long V, int K, long 
 
 ListedSizes constrained_sizes(long long N, long long H, long long V, int K, long long L, long long B) {
   const long long cap = list_cap(V, L, B);
-  return ListedSizes{N, H, V, K, cap, cap * (B > 0 ? 8 : 4), 0};   // seen, biases
+  return ListedSizes{N, H, V, K, cap, cap * (B > 0 ? 8 : 4), 4, cap};   // seen, biases
 }
 
 bool sizes_bad(int64_t N, int64_t H, int64_t V) { return !sizes_ok(N, H, V) || V > PROBS_MAX_V; }
@@ -392,10 +453,8 @@ constexpr long long MAX_LIST = (1ll << 31) - 1;
 }  // namespace
 
 cudaError_t constrained_prepare() {
-  const int most = WINDOW_WORDS * 8;
-  cudaError_t e = cudaFuncSetAttribute(constrained_lists_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(constrained_lists_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  return cudaFuncSetAttribute(constrained_lists_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              HELD * STREAM_THREADS * 8);
 }
 
 }  // namespace flce
@@ -482,9 +541,9 @@ flce_status flce_constrained_logprobs(const void* hidden, const void* weight, co
     la.bias_at = B > 0 ? at<int>(workspace, p.o_bias) : nullptr;
     rv.bias = reinterpret_cast<const float*>(la.bias_at);
     l.rules = rv;
-    if (!stream_setup(&a, &m, hidden, weight)) return FLCE_ECUDA;
+    if (!stream_setup(&a, &m, hidden, weight, segment_blocks(H))) return FLCE_ECUDA;
     count_launches(2);   // lists, the merge
-    constrained_lists_kernel<true><<<static_cast<unsigned>(N), RULE_THREADS, rule_smem(V), st>>>(la);
+    constrained_lists_kernel<true><<<static_cast<unsigned>(N), STREAM_THREADS, rule_smem(V, STREAM_THREADS), st>>>(la);
     if (!ok(launch_result(cudaGetLastError()))) return FLCE_ECUDA;
     const ProfScope prof = prof_launch_begin(st);
     const cudaError_t e = launch_stream_ruled(a, m, l, st);
@@ -496,17 +555,18 @@ flce_status flce_constrained_logprobs(const void* hidden, const void* weight, co
   std::memset(&k, 0, sizeof(k));
   k.q = constrained_sizes(N, H, V, top_k, L, B);
   if (!listed_plan(k.q, workspace_bytes, &p)) return FLCE_EWORKSPACE;
-  if (!targets) {
+  if (!targets) ignore_index = -1;
+  if (!targets && !listed_front(p, N)) {   // the loss's compaction reads targets
     int* all = at<int>(workspace, p.o_targets);
     count_launches(1);
     all_rows_kernel<<<static_cast<unsigned>(std::min<long long>(cdiv(N, 256), 152)), 256, 0, st>>>(all, N);
     if (!ok(launch_result(cudaGetLastError()))) return FLCE_ECUDA;
     targets = all;
-    ignore_index = -1;
   }
   k.hidden = hidden; k.weight = weight; k.targets = targets; k.ii = ignore_index; k.temperature = temperature;
   k.mask = la.mask; k.mask_stride = la.mask_stride;
   k.logp = logp ? logp : lse; k.entropy = entropy; k.lse = lse; k.top_ids = top_ids; k.top_logp = top_logp;
+  k.seg_kb = segment_blocks(H);
   k.ws = workspace; k.st = st;
   rv.seen = la.seen = at<int>(workspace, p.o_rows);
   la.bias_at = B > 0 ? la.seen + p.C * la.cap : nullptr;
@@ -518,16 +578,16 @@ flce_status flce_constrained_logprobs(const void* hidden, const void* weight, co
         la.start = const_cast<int*>(ch.g->lists.start);
         la.id = const_cast<int*>(ch.g->lists.id);
         count_launches(1);
-        return launch_dependent_smem(constrained_lists_kernel<false>, static_cast<unsigned>(la.C), RULE_THREADS,
-                                     rule_smem(V), st, la);
+        return launch_dependent_smem(constrained_lists_kernel<false>, static_cast<unsigned>(la.C), CHUNK_THREADS,
+                                     rule_smem(V, CHUNK_THREADS), st, la);
       },
       [&](const ListedChunk& ch) {
         float2* ml = at<float2>(workspace, p.o_ml);
         const RowsArgs ra{ch.g->hdr, ch.g->idx, targets, ch.c0, ch.g->C, ch.g->nparts, top_k, ch.g->stats, ch.g->zt,
                           ch.g->c2, ch.g->lists, rv, logp, entropy, lse, ml};
         count_launches(top_k > 0 ? 2 : 1);
-        const cudaError_t e = launch_dependent(constrained_rows_kernel, static_cast<unsigned>(cdiv(ch.g->C, 32)),
-                                               32 * ROWS_WARPS, st, ra);
+        const cudaError_t e = launch_dependent(constrained_rows_kernel, static_cast<unsigned>(cdiv(ch.g->C, ROWS8)),
+                                               32 * ROW_WARPS, st, ra);
         if (e != cudaSuccess || top_k == 0) return e;
         const TopArgs ta{ch.g->hdr, ch.g->idx, ch.c0, ch.g->C, ch.g->V, ch.g->nparts, top_k, p.ldz, ch.g->stats,
                          ch.g->zf, ml, ch.g->c2, ch.g->lists, top_ids, top_logp};

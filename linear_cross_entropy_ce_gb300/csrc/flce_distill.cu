@@ -10,9 +10,11 @@
 //     kl = sum_I p_i (log p_i - log q_i),   dkl/dz_v = (q_v - p_v) / T
 //
 // The mass s behind the list is what is left of 1 and may be tiny, so it is not
-// formed as a difference: the GEMM's epilogue takes the listed logits out of
-// the row's statistics and writes them side by side, and the row kernel brings
-// them back in.  All of a row's log probabilities are formed relative to its
+// formed as a difference: the GEMM's epilogue leaves the 128-column parts that
+// hold listed tokens out of the row's statistics and writes their logits side by
+// side (K parts at most), and the row kernel goes through those.  (Taking the
+// listed logits out one by one cost the epilogue more than the products: 4096
+// tokens, 20 entries, at 512 x 16000 112 us a GEMM, 76 so.)  All of a row's log probabilities are formed relative to its
 // largest logit (an fp32 log-sum-exp of 20 is off by 1e-6, as much as kl is
 // where student and teacher nearly agree), and r as (1 - p_max) - the others.
 //
@@ -37,58 +39,122 @@ constexpr int NO_TOKEN = INT_MAX;
 // lists
 // ---------------------------------------------------------------------------
 
-// A row's teacher tokens in ascending order, each once, by G threads (g: the
-// thread's place among them).  id: shared copy of the sorted tokens; gid, gt:
-// the same in memory with their log masses; slot[j]: the place of entry j, -1
-// where there is none.  Returns their number.  K^2 comparisons: with 64 entries
-// 128 a lane.
-template <int G, class Sync>
-__device__ __forceinline__ int sort_row(const int* ids, const float* t, int K, int g, int* all, int* first, int* id,
-                                        int* gid, float* gt, short* slot, Sync sync) {
-  for (int j = g; j < K; j += G) {
-    const int x = ids[j];
-    all[j] = x < 0 ? NO_TOKEN : x;
+// Shared scratch of one row's sort, by a warp.
+struct SortRow {
+  int* raw;      // [K rounded up to 32] as given (NO_TOKEN where there is none)
+  int* id;       // [K] sorted, then each token once
+  float* t;      // [K] their log masses
+  short* at;     // [K] place of sorted entry i in the list of single tokens
+};
+__host__ __device__ __forceinline__ int sort_words(int K) { return ((K + 31) / 32 * 32 + 2 * K + (K + 1) / 2 + 3) / 4 * 4; }
+__host__ __device__ __forceinline__ int list_words(int K) { return (sort_words(K) + (K + 1) / 2 + 3) / 4 * 4; }
+__device__ __forceinline__ SortRow sort_scratch(int* p, int K) {
+  const int padded = (K + 31) / 32 * 32;
+  return SortRow{p, p + padded, reinterpret_cast<float*>(p + padded + K), reinterpret_cast<short*>(p + padded + 2 * K)};
+}
+
+// A row's teacher tokens in ascending order, each once, with their log masses,
+// by a warp: s.id[0 .. n), s.t[0 .. n); slot[k]: the place of entry
+// lane + 32 k, -1 where there is none.  Returns n.  An entry's rank is the
+// number of smaller tokens and of equal ones before it: two instructions a
+// pair, K^2 / 16 a lane (64 entries 256), which no order of the entries makes
+// slower: lists and tables of 5735 rows of 32 over 2001 parts take 23 us, of 724
+// of 100 17.
+// SORT_GROUPS: 32s of entries, 1, 2, 4 or 8.
+template <int SORT_GROUPS>
+__device__ __forceinline__ int sort_row(const int* ids, const float* t, int K, int lane, const SortRow& s,
+                                        int (&slot)[SORT_GROUPS]) {
+  const int groups = (K + 31) / 32;
+  unsigned x[SORT_GROUPS];
+  int rank[SORT_GROUPS];
+#pragma unroll
+  for (int e = 0; e < SORT_GROUPS; ++e) {
+    const int j = e * 32 + lane;
+    const int v = j < K ? ids[j] : -1;
+    x[e] = v < 0 ? NO_TOKEN : v;
+    rank[e] = 0;
+    if (e < groups) s.raw[j] = static_cast<int>(x[e]);
   }
-  sync();
-  for (int j = g; j < K; j += G) {
-    const int x = all[j];
-    bool f = true;
-    for (int i = 0; i < j; ++i) f = f && all[i] != x;
-    first[j] = f ? x : NO_TOKEN;
+  __syncwarp();
+  for (int g = 0; g < groups; ++g) {
+    const uint4* from = reinterpret_cast<const uint4*>(s.raw + g * 32);
+#pragma unroll
+    for (int e = 0; e < SORT_GROUPS; ++e) {
+      if (e >= groups) break;
+      // equal tokens of groups before this one stand before it, of groups behind it do not
+      const unsigned limit = x[e] + (g < e ? 1u : 0u);
+      int r = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint4 b = from[i];
+        if (g == e) {
+          r += b.x < limit + (i * 4 < lane) ? 1 : 0;
+          r += b.y < limit + (i * 4 + 1 < lane) ? 1 : 0;
+          r += b.z < limit + (i * 4 + 2 < lane) ? 1 : 0;
+          r += b.w < limit + (i * 4 + 3 < lane) ? 1 : 0;
+        } else {
+          r += b.x < limit ? 1 : 0;
+          r += b.y < limit ? 1 : 0;
+          r += b.z < limit ? 1 : 0;
+          r += b.w < limit ? 1 : 0;
+        }
+      }
+      rank[e] += r;
+    }
   }
-  sync();
   int n = 0;
-  for (int i = 0; i < K; ++i) n += first[i] != NO_TOKEN;
-  for (int j = g; j < K; j += G) {
-    const int x = all[j];
-    if (x == NO_TOKEN) {
-      slot[j] = -1;
-      continue;
+#pragma unroll
+  for (int e = 0; e < SORT_GROUPS; ++e) {
+    const bool there = e < groups && x[e] != NO_TOKEN;
+    if (there) {
+      s.id[rank[e]] = static_cast<int>(x[e]);
+      s.t[rank[e]] = t[e * 32 + lane];
     }
-    int u = 0, same = 0;
-    for (int i = 0; i < K; ++i) {
-      u += first[i] < x;
-      same += all[i] == x;
-    }
-    slot[j] = static_cast<short>(u);
-    if (first[j] != x) continue;
-    float m = t[j];
-    if (same > 1) {   // the token's masses add up
-      for (int i = j + 1; i < K; ++i)
-        if (all[i] == x) m = fmaxf(m, t[i]);
-      if (m > -INFINITY) {
-        float sum = 0.f;
-        for (int i = j; i < K; ++i)
-          if (all[i] == x) sum += expf(t[i] - m);
-        m += logf(sum);
+    n += __popc(__ballot_sync(0xffffffffu, there));
+  }
+  __syncwarp();
+  // each token once: its place is the number of different tokens before it
+  int singles = 0;
+  int id[SORT_GROUPS];
+  float m[SORT_GROUPS];
+  int place[SORT_GROUPS];
+#pragma unroll
+  for (int e = 0; e < SORT_GROUPS; ++e) {
+    const int i = e * 32 + lane;
+    place[e] = -1;
+    if (e >= groups) continue;
+    const bool there = i < n;
+    id[e] = there ? s.id[i] : NO_TOKEN;
+    m[e] = there ? s.t[i] : 0.f;
+    const bool first = there && (i == 0 || s.id[i - 1] != id[e]);
+    const unsigned f = __ballot_sync(0xffffffffu, first);
+    const int u = singles + __popc(f & (0xffffffffu >> (31 - lane))) - 1;
+    singles += __popc(f);
+    if (there) s.at[i] = static_cast<short>(u);
+    if (first) {
+      place[e] = u;
+      if (i + 1 < n && s.id[i + 1] == id[e]) {   // the token's masses add up
+        float top = m[e];
+        for (int k = i + 1; k < n && s.id[k] == id[e]; ++k) top = fmaxf(top, s.t[k]);
+        if (top > -INFINITY) {
+          float sum = 0.f;
+          for (int k = i; k < n && s.id[k] == id[e]; ++k) sum += expf(s.t[k] - top);
+          m[e] = top + logf(sum);
+        }
       }
     }
-    id[u] = x;
-    gid[u] = x;
-    gt[u] = m;
   }
-  sync();
-  return n;
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < SORT_GROUPS; ++e) {
+    if (place[e] >= 0) {
+      s.id[place[e]] = id[e];
+      s.t[place[e]] = m[e];
+    }
+    slot[e] = e < groups && x[e] != NO_TOKEN ? s.at[rank[e]] : -1;
+  }
+  __syncwarp();
+  return singles;
 }
 
 __device__ __forceinline__ int lower_bound(const int* id, int n, int x) {
@@ -109,6 +175,8 @@ struct ListArgs {
   const int* idx;
   long long c0;
   int C, nparts;
+  short* slab;                // [nparts][C] which of the row's slabs takes the part's logits, -1: none
+  int* count;                 // [C] tokens of the row
   int ctas, max_tiles;        // streaming form
   int* start;
   int* id;                    // [rows][K]
@@ -116,50 +184,92 @@ struct ListArgs {
   short* slot;                // [rows][K] place of each given entry
 };
 
-// Chunked: 32 rows a block, a warp sorts four of them; then a lane walks a
-// row's list along the parts, so that the boundaries are written 128 bytes at a
-// time.
-constexpr int LIST_ROWS = 32;
-constexpr int LIST_WARPS = 8;
+template <int SORT_GROUPS>
+__device__ __forceinline__ void store_row(const ListArgs& a, long long row, const SortRow& s, int n,
+                                          const int (&slot)[SORT_GROUPS], int lane) {
+  const long long to = row * a.K;
+  for (int u = lane; u < n; u += 32) {
+    a.id[to + u] = s.id[u];
+    a.t[to + u] = s.t[u];
+  }
+#pragma unroll
+  for (int e = 0; e < SORT_GROUPS; ++e)
+    if (e * 32 + lane < a.K) a.slot[to + e * 32 + lane] = static_cast<short>(slot[e]);
+}
+
+// Chunked: 8 rows a block, each sorted by a warp; then a lane walks a run of
+// one row's parts, four runs a warp.
+constexpr int LIST_WARPS = ROWS8;
+template <int SORT_GROUPS>
 __global__ void __launch_bounds__(32 * LIST_WARPS) distill_lists_kernel(const ListArgs a) {
-  extern __shared__ int smem[];   // [32][K | 1] sorted, [8][2 K] scratch
-  __shared__ int count[LIST_ROWS];
+  extern __shared__ int smem[];   // per row: scratch of its sort, the slabs of its tokens
+  __shared__ int count[ROWS8];
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
-  const int pitch = a.K | 1;      // odd: a column of the sorted lists is in 32 banks
+  const int words = list_words(a.K), slabs_at = sort_words(a.K);
   ptx::grid_dependency_wait();
   const int Cl = chunk_rows(a.hdr, a.c0, a.C);
-  const int r0 = blockIdx.x * LIST_ROWS;
+  const int r0 = blockIdx.x * ROWS8;
   if (r0 >= Cl) return;
-  int* scratch = smem + LIST_ROWS * pitch + w * 2 * a.K;
-  for (int k = w; k < LIST_ROWS && r0 + k < Cl; k += LIST_WARPS) {
-    const long long row = r0 + k, from = static_cast<long long>(a.idx[a.c0 + row]) * a.K, to = row * a.K;
-    const int n = sort_row<32>(a.teacher_ids + from, a.teacher_logp + from, a.K, lane, scratch, scratch + a.K,
-                               smem + k * pitch, a.id + to, a.t + to, a.slot + to, [] { __syncwarp(); });
-    if (lane == 0) count[k] = n;
+  if (r0 + w < Cl) {
+    const long long row = r0 + w, from = static_cast<long long>(a.idx[a.c0 + row]) * a.K;
+    const SortRow s = sort_scratch(smem + w * words, a.K);
+    int slot[SORT_GROUPS];
+    const int n = sort_row(a.teacher_ids + from, a.teacher_logp + from, a.K, lane, s, slot);
+    store_row(a, row, s, n, slot, lane);
+    short* slab = reinterpret_cast<short*>(smem + w * words + slabs_at);
+    int q = -1;   // the last slab so far
+    for (int u0 = 0; u0 < n; u0 += 32) {
+      const int u = u0 + lane;
+      const bool first = u < n && (u == 0 || s.id[u - 1] / PART_COLS != s.id[u] / PART_COLS);
+      const unsigned f = __ballot_sync(0xffffffffu, first);
+      if (u < n) slab[u] = static_cast<short>(q + __popc(f & (0xffffffffu >> (31 - lane))));
+      q += __popc(f);
+    }
+    if (lane == 0) {
+      count[w] = n;
+      a.count[row] = n;
+    }
   }
   __syncthreads();
-  const int r = r0 + lane;
+  const int k = lane % ROWS8, r = r0 + k;
   if (r >= Cl) return;
-  const int n = count[lane];
-  const int* id = smem + lane * pitch;
-  const int bounds = a.nparts + 1, each = (bounds + LIST_WARPS - 1) / LIST_WARPS;
-  const int p1 = min(bounds, (w + 1) * each);
-  int p = w * each;
-  int e = lower_bound(id, n, p * PART_COLS);
+  const int n = count[k];
+  const int* id = sort_scratch(smem + k * words, a.K).id;
+  const short* slab = reinterpret_cast<const short*>(smem + k * words + slabs_at);
+  const int each = (a.nparts + 31) / 32;
+  int p = (w * 4 + lane / ROWS8) * each;
+  const int p1 = min(a.nparts, p + each);
+  int e = p < p1 ? lower_bound(id, n, p * PART_COLS) : n;   // the next token
+  int at = e < n ? id[e] / PART_COLS : a.nparts;            // its part
   for (; p < p1; ++p) {
-    while (e < n && id[e] < p * PART_COLS) ++e;
-    a.start[static_cast<long long>(p) * a.C + r] = p == a.nparts ? n : e;
+    int q = -1;
+    if (at == p) {
+      q = slab[e];
+      do ++e;
+      while (e < n && id[e] / PART_COLS == p);
+      at = e < n ? id[e] / PART_COLS : a.nparts;
+    }
+    a.slab[static_cast<long long>(p) * a.C + r] = static_cast<short>(q);
   }
 }
 
-// Streaming: a block per row; the weight streams meanwhile.
+// Streaming: a block per row; the weight streams meanwhile, on the same SMs
+// (few threads, and less shared memory than the streaming kernel leaves).
 constexpr int STREAM_LIST_THREADS = 128;
+template <int SORT_GROUPS>
 __global__ void __launch_bounds__(STREAM_LIST_THREADS) distill_stream_lists_kernel(const ListArgs a) {
-  __shared__ int all[MAX_TEACHER], first[MAX_TEACHER], id[MAX_TEACHER];
+  __shared__ __align__(16) int scratch[MAX_TEACHER + 2 * MAX_TEACHER + MAX_TEACHER / 2];
+  __shared__ int count;
   ptx::grid_launch_dependents();
   const long long from = static_cast<long long>(blockIdx.x) * a.K;
-  const int n = sort_row<STREAM_LIST_THREADS>(a.teacher_ids + from, a.teacher_logp + from, a.K, threadIdx.x, all, first,
-                                              id, a.id + from, a.t + from, a.slot + from, [] { __syncthreads(); });
+  const SortRow s = sort_scratch(scratch, a.K);
+  if (threadIdx.x < 32) {
+    int slot[SORT_GROUPS];
+    const int n = sort_row(a.teacher_ids + from, a.teacher_logp + from, a.K, threadIdx.x, s, slot);
+    store_row(a, blockIdx.x, s, n, slot, threadIdx.x);
+    if (threadIdx.x == 0) count = n;
+  }
+  __syncthreads();
   const int tiles = a.ctas * a.max_tiles;
   int* start = a.start + static_cast<long long>(blockIdx.x) * (tiles + 1);
   for (int b = threadIdx.x; b <= tiles; b += STREAM_LIST_THREADS) {
@@ -168,7 +278,7 @@ __global__ void __launch_bounds__(STREAM_LIST_THREADS) distill_stream_lists_kern
       const Range r = range_of(a.V, a.ctas, b / a.max_tiles);
       x = b % a.max_tiles < r.tiles ? r.start(b % a.max_tiles) : r.u1 * UNIT_ROWS;
     }
-    start[b] = lower_bound(id, n, min(x, a.V));
+    start[b] = lower_bound(s.id, count, min(x, a.V));
   }
 }
 
@@ -231,9 +341,20 @@ __device__ __forceinline__ void fill_row(const DistillOut& o, long long row, int
 }
 
 // One row by a warp, from the statistics of the logits behind its list and the
-// listed logits z[0 .. n).
-__device__ __forceinline__ void finish_row(const DistillOut& o, long long row, int K, bool tail, float c2, Stat rest,
-                                           const float* z, const float* t, const short* slot, int n, int lane) {
+// listed logits z[0 .. n), which may be shared memory.
+//
+// kl is what is left of terms that nearly cancel, and a common error of all log
+// probabilities goes straight into it, so what they share is kept apart: with
+// x = (z - m) / T, s = sum exp(x) = 2^k f, b the sum behind the list (at its own
+// largest logit m_b),
+//   kl = sum p (t - x) + P (k ln 2 + ln f) + r (ln(r s / b) - (m_b - m) / T),
+// P = sum p.  An entry's own rounding (2^-24 of |t| + |x|) is weighed by its p,
+// and k ln 2 P is formed in 64 bits (an fp32 ln s of 10 alone is off by 5e-7).
+// (All in 64 bits, three logarithms a row, the row kernel took 120 us for 5735
+// rows, with this 97 then.)
+__device__ __forceinline__ void finish_row(const DistillOut& o, long long row, int K, bool tail, float c2, float inv_t,
+                                           Stat rest, const float* z, const float* t, const short* slot, int n,
+                                           int lane) {
   float m = rest.m;
   bool nan = false;
   for (int u = lane; u < n; u += 32) {
@@ -243,32 +364,38 @@ __device__ __forceinline__ void finish_row(const DistillOut& o, long long row, i
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
   if (__any_sync(0xffffffffu, nan)) m = __int_as_float(0x7fc00000);
-  float s = 0.f;
-  for (int u = lane; u < n; u += 32) s += exp2f((z[u] - m) * c2);
-#pragma unroll
-  for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-  const bool none = rest.m == -INFINITY && rest.s == 0.f;   // nothing behind the list
-  if (!none) s += rest.s * exp2f((rest.m - m) * c2);
-  const float l2s = log2f(s);
-  const float rest_logp = none ? -INFINITY : fmaf(rest.m - m, c2, log2f(rest.s) - l2s) * LN2;
   Teacher q = teacher_of(t, n, tail, lane);
+  const bool none = rest.m == -INFINITY && rest.s == 0.f;   // nothing behind the list
   if (none) q.rest = 0.f;
-  double kl = 0.0;   // of terms that nearly cancel
+  float s = 0.f, mass = 0.f, sum = 0.f;
   for (int u = lane; u < n; u += 32) {
-    const float lp = t[u] - q.shift, p = expf(lp), lq = fmaf(z[u] - m, c2, -l2s) * LN2;
-    if (!(p == 0.f)) kl += static_cast<double>(p) * static_cast<double>(lp - lq);
+    const float lp = t[u] - q.shift, p = expf(lp), x = (z[u] - m) * inv_t;
+    s += expf(x);
+    mass += p;
+    if (!(p == 0.f)) sum = fmaf(p, lp - x, sum);
   }
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, k);
+    mass += __shfl_xor_sync(0xffffffffu, mass, k);
+    sum += __shfl_xor_sync(0xffffffffu, sum, k);
+  }
+  const float far = none ? -INFINITY : (rest.m - m) * inv_t;
+  if (!none) s += rest.s * expf(far);
+  int k = 0;
+  const float f = frexpf(s, &k), lf = logf(f);
+  const float ls = fmaf(static_cast<float>(k), LN2, lf);
   for (int j = lane; j < K; j += 32) {
     const int u = slot[j];
-    o.student_logp[row * K + j] = u < 0 || u >= n ? 0.f : fmaf(z[u] - m, c2, -l2s) * LN2;
+    o.student_logp[row * K + j] = u < 0 || u >= n ? 0.f : fmaf(z[u] - m, inv_t, -ls);
   }
-#pragma unroll
-  for (int k = 16; k > 0; k >>= 1) kl += __shfl_xor_sync(0xffffffffu, kl, k);
   if (lane == 0) {
-    if (!(q.rest == 0.f)) kl += static_cast<double>(q.rest) * static_cast<double>(logf(q.rest) - rest_logp);
+    double kl = static_cast<double>(mass) * k * 0.6931471805599453 + fmaf(mass, lf, sum);
+    // a teacher without any mass asks for nothing
+    if (!(q.rest == 0.f)) kl += q.rest * (logf(q.rest * (s / rest.s)) - far);
     o.kl[row] = static_cast<float>(kl);
-    o.lse[row] = fmaf(m, c2, l2s) * LN2;
-    o.rest_logp[row] = rest_logp;
+    o.lse[row] = fmaf(m, inv_t, ls);
+    o.rest_logp[row] = none ? -INFINITY : far - logf(s / rest.s);
   }
 }
 
@@ -302,32 +429,114 @@ struct RowsArgs {
   const int* hdr;
   const int* idx;
   long long c0;
-  int C, nparts, K, tail;
+  int C, nparts, V, K, tail, slabs;
   const float* stats;
-  const int* start;
-  const float *z, *t;
+  const int* count;
+  const int* id;
+  float* z;                   // [C][slabs][128] logits of the parts that hold listed tokens
+  const float* t;
   const short* slot;
-  float c2;
+  float c2, inv_t;
   DistillOut out;
 };
 
-// 32 rows of a chunk: the parts' statistics merged with a lane a row, then a
-// warp a row.
-__global__ void __launch_bounds__(32 * ROWS_WARPS) distill_rows_kernel(const RowsArgs a) {
-  __shared__ Stat part[ROWS_WARPS][32];
-  const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
+// 8 rows of a chunk.  Eight warps merge the statistics of the parts without listed
+// tokens; SHARES warps a row go through the other parts' logits meanwhile: the
+// listed ones aside, the others into statistics of their own.  Then a warp a row
+// puts it all together.  All of it is loads (5735 rows of 32 entries over 2001
+// parts: 230 MB, 57 us).  Long lists get three warps a row (724 rows of 100
+// entries 24 us, with one 140), short ones one, and two blocks an SM.
+template <int SHARES>
+__global__ void __launch_bounds__(32 * ROWS8 * (1 + SHARES)) distill_rows_kernel(const RowsArgs a) {
+  __shared__ Stat part[32][ROWS8];
+  __shared__ Stat share[1 + SHARES][ROWS8];
+  __shared__ int slabs_used[ROWS8];
+  extern __shared__ float4 smem4[];   // [8][slabs] which of a slab's columns are left out, [8][K] listed logits
+  const int lane = threadIdx.x % 32, w = threadIdx.x / 32, k = w % ROWS8;
   ptx::grid_dependency_wait();
   const int Cl = chunk_rows(a.hdr, a.c0, a.C);
-  const int r0 = blockIdx.x * 32;
+  const int r0 = blockIdx.x * ROWS8;
   if (r0 >= Cl) return;
-  merge_parts(a.stats, a.nparts, a.C, a.c2, r0 + lane, r0 + lane < Cl, lane, w, part);
+  const long long r = r0 + k;
+  const bool valid = r < Cl;
+  float* mine = reinterpret_cast<float*>(smem4 + ROWS8 * a.slabs) + k * a.K;
+  const int n = valid ? min(a.K, a.count[r]) : 0;
+  if (w < ROWS8) {
+    const Stat s = merge_parts8(a.stats, a.nparts, a.C, a.c2, r0, Cl, lane, w, part);
+    if (lane == 0) share[0][w] = s;
+  } else {
+    uint32_t* out = reinterpret_cast<uint32_t*>(smem4 + k * a.slabs);   // [slabs][4] bits of the columns left out
+    const float* slabs = a.z + r * a.slabs * PART_COLS;
+    const int sub = w / ROWS8 - 1;
+    if (sub == 0) {
+      for (int q = lane; q < a.slabs * 4; q += 32) out[q] = 0u;
+      __syncwarp();
+      int used = 0;
+      for (int u0 = 0; u0 < n; u0 += 32) {
+        const int u = u0 + lane;
+        const int id = u < n ? a.id[r * a.K + u] : 0, in = id / PART_COLS;
+        const bool first = u < n && (u == 0 || a.id[r * a.K + u - 1] / PART_COLS != in);
+        const unsigned f = __ballot_sync(0xffffffffu, first);
+        if (u < n) {
+          const int q = used + __popc(f & (0xffffffffu >> (31 - lane))) - 1, at = id % PART_COLS;
+          mine[u] = slabs[q * PART_COLS + at];
+          atomicOr(out + q * 4 + at / 32, 1u << (at % 32));
+          const int left = a.V - in * PART_COLS;   // columns of the vocabulary
+          if (first && left < PART_COLS)
+            for (int j = 0; j < 4; ++j)
+              if (left < (j + 1) * 32) atomicOr(out + q * 4 + j, 0xffffffffu << max(0, left - j * 32));
+        }
+        used += __popc(f);
+      }
+      if (lane == 0) slabs_used[k] = used;
+    }
+    ptx::named_bar_sync(ROWS8_BAR_OTHERS, 32 * ROWS8 * SHARES);
+    const int used = slabs_used[k];
+    const float4* slab = reinterpret_cast<const float4*>(slabs) + lane;
+    Stat acc = {-INFINITY, 0.f, 0.f};
+    for (int q = sub * 4; q < used; q += 4 * SHARES) {
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 x = q + i < used ? slab[(q + i) * (PART_COLS / 4)]
+                                      : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t b = q + i < used ? out[(q + i) * 4 + lane / 8] >> (lane % 8 * 4) & 15u : 0u;
+        if (b) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if ((b >> j) & 1u) v[4 * i + j] = -INFINITY;
+        }
+      }
+      float m = fmaxf(acc.m, fmaxf(v[14], v[15]));
+#pragma unroll
+      for (int i = 0; i < 14; i += 2) m = ptx::max3(m, v[i], v[i + 1]);
+      const float mb = m == -INFINITY ? 0.f : -m * a.c2;   // (nothing yet: every term is 0)
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s += ptx::ex2(fmaf(v[i], a.c2, mb));
+      // mb is rounded: every exponent is too large by rho (exact in the fused multiply-add)
+      const float rho = m == -INFINITY ? 0.f : fmaf(m, a.c2, mb);
+      acc = merge(acc, Stat{m, s * ptx::ex2(-rho), 0.f}, a.c2);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {   // fixed order; lane 0 holds the result
+      const Stat other = {__shfl_down_sync(0xffffffffu, acc.m, o), __shfl_down_sync(0xffffffffu, acc.s, o), 0.f};
+      acc = merge(acc, other, a.c2);
+    }
+    if (lane == 0) share[1 + sub][k] = acc;
+  }
   __syncthreads();
-  const long long r = r0 + w;
-  if (r >= Cl) return;
+  if (w >= ROWS8 || !valid) return;
   const long long row = a.idx[a.c0 + r];
   if (a.hdr[HDR_STATUS] & STATUS_TIMEOUT) return fill_row(a.out, row, a.K, __int_as_float(0x7fc00000), lane);
-  const int n = min(a.K, a.start[static_cast<long long>(a.nparts) * a.C + r]);
-  finish_row(a.out, row, a.K, a.tail, a.c2, part[0][w], a.z + r * a.K, a.t + r * a.K, a.slot + r * a.K, n, lane);
+  Stat rest = share[0][k];
+#pragma unroll
+  for (int i = 1; i <= SHARES; ++i) rest = merge(rest, share[i][k], a.c2);
+  finish_row(a.out, row, a.K, a.tail, a.c2, a.inv_t, rest, mine, a.t + r * a.K, a.slot + r * a.K, n, lane);
 }
 
 // After a call of several chunks: a pipeline that timed out in one of them
@@ -349,7 +558,7 @@ struct StreamRowsArgs {
   const int* start;
   const float *z, *t;
   const short* slot;
-  float c2;
+  float c2, inv_t;
   DistillOut out;
 };
 
@@ -381,7 +590,7 @@ __global__ void __launch_bounds__(32) distill_stream_rows_kernel(const StreamRow
   if (failed || bad) return fill_row(a.out, n0, a.K, __int_as_float(0x7fc00000), lane);
   const long long at = static_cast<long long>(n0) * a.K;
   const int n = min(a.K, a.start[static_cast<long long>(n0) * (a.tiles + 1) + a.tiles]);
-  finish_row(a.out, n0, a.K, a.tail, a.c2, acc, a.z + at, a.t + at, a.slot + at, n, lane);
+  finish_row(a.out, n0, a.K, a.tail, a.c2, a.inv_t, acc, a.z + at, a.t + at, a.slot + at, n, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -391,75 +600,41 @@ __global__ void __launch_bounds__(32) distill_stream_rows_kernel(const StreamRow
 // What the gradient needs of a row, by a warp: its target (for the kernels that
 // compact the rows), the log-sum-exp and upstream gradient for MODE_DZ, which
 // sets dz = -grad / T exp(z - lse), and dz at the listed tokens.
+template <int SORT_GROUPS>
 __global__ void __launch_bounds__(32 * TARGET_WARPS)
     distill_grad_rows_kernel(const int* ids, const float* logp, long long N, int K, int V, int tail, float temperature,
                              const float* lse, const float* rest_logp, const float* student_logp, const float* grad_kl,
                              int* targets, float* dz_lse, float* dz_grad, uint16_t* patch) {
-  extern __shared__ float smem_t[];   // [warps][2 K]: log masses, each token's once, and ids
+  extern __shared__ int smem[];   // scratch of a sort per warp
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   const long long row = static_cast<long long>(blockIdx.x) * TARGET_WARPS + w;
   if (row >= N) return;
   ids += row * K;
-  logp += row * K;
   const int target = row_target(ids, K, V, lane);
   if (lane == 0) targets[row] = target;
   if (target < 0 || target >= V) return;
-  float* t = smem_t + w * 2 * K;
-  int* all = reinterpret_cast<int*>(t + K);
-  for (int j = lane; j < K; j += 32) all[j] = ids[j];
-  __syncwarp();
-  // each entry's token's mass in all; of a token named twice only the first entry has any in the row's sums
-  for (int j = lane; j < K; j += 32) {
-    const int x = all[j];
-    float m = -INFINITY;
-    if (x >= 0) {
-      m = logp[j];
-      bool first = true, again = false;
-      for (int i = 0; i < K; ++i) {
-        if (i != j && all[i] == x) {
-          if (i < j) first = false;
-          else again = true;
-        }
-      }
-      if (!first) {
-        m = -INFINITY;
-      } else if (again) {
-        for (int i = j + 1; i < K; ++i)
-          if (all[i] == x) m = fmaxf(m, logp[i]);
-        if (m > -INFINITY) {
-          float sum = 0.f;
-          for (int i = j; i < K; ++i)
-            if (all[i] == x) sum += expf(logp[i] - m);
-          m += logf(sum);
-        }
-      }
-    }
-    t[j] = m;
-  }
-  __syncwarp();
-  Teacher q = teacher_of(t, K, tail, lane);
+  const SortRow s = sort_scratch(smem + w * sort_words(K), K);
+  int slot[SORT_GROUPS];
+  const int n = sort_row(ids, logp + row * K, K, lane, s, slot);
+  Teacher q = teacher_of(s.t, n, tail, lane);
   const float rl = rest_logp[row], g = grad_kl[row];
   const bool none = rl == -INFINITY;
   if (none) q.rest = 0.f;
   float mass = 0.f;
-  for (int j = lane; j < K; j += 32) mass += expf(t[j] - q.shift);
+  for (int u = lane; u < n; u += 32) mass += expf(s.t[u] - q.shift);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mass += __shfl_xor_sync(0xffffffffu, mass, o);
   mass += q.rest;
-  if (q.top == -INFINITY && !tail) mass = 0.f;   // a teacher without any mass asks for nothing
   if (lane == 0) {
     dz_lse[row] = none ? lse[row] : lse[row] + rl;
     dz_grad[row] = none ? -g * mass : -g * (mass * expf(rl) - q.rest);
   }
   const float gt = g / temperature;
-  for (int j = lane; j < K; j += 32) {
-    const int x = all[j];
-    float p = 0.f;
-    if (x >= 0) {
-      int i = 0;
-      while (all[i] != x) ++i;   // the token's first entry; ends at j
-      p = expf(t[i] - q.shift);
-    }
+#pragma unroll
+  for (int e = 0; e < SORT_GROUPS; ++e) {
+    const int j = e * 32 + lane;
+    if (j >= K) break;
+    const float p = slot[e] >= 0 ? expf(s.t[slot[e]] - q.shift) : 0.f;
     const float dz = gt * (mass * expf(student_logp[row * K + j]) - p);
     patch[row * K + j] = static_cast<uint16_t>(ptx::pack_bf16x2(dz, 0.f) & 0xffffu);
   }
@@ -478,7 +653,21 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-size_t lists_smem(int K) { return (size_t(LIST_ROWS) * (K | 1) + size_t(LIST_WARPS) * 2 * K) * 4; }
+size_t lists_smem(int K) { return size_t(ROWS8) * list_words(K) * 4; }
+size_t rows_smem(int K, int slabs) { return size_t(ROWS8) * (size_t(slabs) * 16 + size_t(K) * 4); }
+size_t grad_smem(int K) { return size_t(TARGET_WARPS) * sort_words(K) * 4; }
+static_assert(ROWS8 * (MAX_TEACHER * 5 + 8) * 4 + 4096 <= 49152, "shared memory that needs no attribute");
+
+// f(32s of entries of a sort, as a type)
+template <int G>
+struct Groups { static constexpr int value = G; };
+template <class F>
+cudaError_t by_groups(int K, F&& f) {
+  if (K <= 32) return f(Groups<1>());
+  if (K <= 64) return f(Groups<2>());
+  if (K <= 128) return f(Groups<4>());
+  return f(Groups<8>());
+}
 
 struct DistillStream {
   int ctas, max_tiles;
@@ -507,7 +696,9 @@ DistillStream distill_stream_plan(long long N, long long V, int K, int sms) {
 }
 
 ListedSizes distill_sizes(long long N, long long H, long long V, int K) {
-  return ListedSizes{N, H, V, 0, K, 6ll * K, 0};   // log masses and places
+  // of a row: log masses and places of the entries, and the logits of the parts that hold any
+  const long long slabs = std::min<long long>(K, cdiv(V, PART_COLS));
+  return ListedSizes{N, H, V, 0, K, 6ll * K + 4, 2, slabs * PART_COLS};
 }
 
 // What the backward keeps of the call beside the workspace of the log
@@ -530,17 +721,14 @@ bool sizes_bad(int64_t N, int64_t H, int64_t V) { return !sizes_ok(N, H, V) || V
 
 }  // namespace
 
-cudaError_t distill_prepare() {
-  return cudaFuncSetAttribute(distill_lists_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(lists_smem(MAX_TEACHER)));
-}
-
 cudaError_t launch_distill_grad_rows(const DistillGrad& d, long long N, int V, float temperature, cudaStream_t s) {
-  distill_grad_rows_kernel<<<static_cast<unsigned>(cdiv(N, TARGET_WARPS)), 32 * TARGET_WARPS,
-                             size_t(TARGET_WARPS) * 2 * d.K * 4, s>>>(
-      d.ids, d.logp, N, d.K, V, d.tail, temperature, d.lse_in, d.rest_logp, d.student_logp, d.grad_kl, d.targets, d.lse,
-      d.grad, d.patch);
-  return launch_result(cudaGetLastError());
+  return by_groups(d.K, [&](auto g) {
+    distill_grad_rows_kernel<decltype(g)::value>
+        <<<static_cast<unsigned>(cdiv(N, TARGET_WARPS)), 32 * TARGET_WARPS, grad_smem(d.K), s>>>(
+            d.ids, d.logp, N, d.K, V, d.tail, temperature, d.lse_in, d.rest_logp, d.student_logp, d.grad_kl, d.targets,
+            d.lse, d.grad, d.patch);
+    return launch_result(cudaGetLastError());
+  });
 }
 
 cudaError_t launch_distill_patch(const int* hdr, const int* idx, long long c0, int C, int K, int V, long long ldz,
@@ -572,6 +760,8 @@ flce_status flce_topk_distill(const void* hidden, const void* weight, const int3
   if (!aligned16(hidden) || !aligned16(weight) || !aligned16(workspace) || !aligned4(teacher_ids) ||
       !aligned4(teacher_logp) || !aligned4(kl) || !aligned4(lse) || !aligned4(rest_logp) || !aligned4(student_logp))
     return FLCE_EUNSUPPORTED;
+  // the logits of the chunked form are stored 32 bytes at a time
+  if (N > STREAM_MAX_TOKENS && !aligned32(workspace)) return FLCE_EUNSUPPORTED;
   DeviceState dev;
   if (device_state(&dev) != cudaSuccess) { cudaGetLastError(); return FLCE_ECUDA; }
   if (dev.major < 10) return FLCE_EUNSUPPORTED;
@@ -603,16 +793,19 @@ flce_status flce_topk_distill(const void* hidden, const void* weight, const int3
     la.ctas = p.ctas; la.max_tiles = p.max_tiles;
     la.t = at<float>(workspace, p.o_t);
     la.slot = at<short>(workspace, p.o_slot);
-    if (!stream_setup(&a, &m, hidden, weight)) return FLCE_ECUDA;
+    if (!stream_setup(&a, &m, hidden, weight, segment_blocks(H, 1))) return FLCE_ECUDA;
     count_launches(2);   // lists, rows
-    distill_stream_lists_kernel<<<static_cast<unsigned>(N), STREAM_LIST_THREADS, 0, st>>>(la);
-    if (!ok(launch_result(cudaGetLastError()))) return FLCE_ECUDA;
+    if (!ok(by_groups(K, [&](auto g) {
+          distill_stream_lists_kernel<decltype(g)::value><<<static_cast<unsigned>(N), STREAM_LIST_THREADS, 0, st>>>(la);
+          return launch_result(cudaGetLastError());
+        })))
+      return FLCE_ECUDA;
     const ProfScope prof = prof_launch_begin(st);
     const cudaError_t e = launch_stream_taken(a, m, l, st);
     prof_launch_end(prof, MODE_STATS, st);
     if (!ok(e)) return FLCE_ECUDA;
     const StreamRowsArgs ra{a.hdr, teacher_ids, K, a.V, p.ctas, tail, p.ctas * p.max_tiles, a.stat, a.fail, la.start,
-                            l.lists.z, la.t, la.slot, a.c2, out};
+                            l.lists.z, la.t, la.slot, a.c2, 1.f / temperature, out};
     if (!ok(launch_dependent(distill_stream_rows_kernel, static_cast<unsigned>(N), 32, st, ra))) return FLCE_ECUDA;
     return FLCE_OK;
   }
@@ -628,24 +821,31 @@ flce_status flce_topk_distill(const void* hidden, const void* weight, const int3
   if (!ok(launch_result(cudaGetLastError()))) return FLCE_ECUDA;
   c.hidden = hidden; c.weight = weight; c.targets = targets; c.ii = -1; c.temperature = temperature;
   c.logp = kl; c.entropy = rest_logp; c.lse = lse;
+  c.seg_kb = segment_blocks(H, 1);
   c.ws = workspace; c.st = st;
   la.t = at<float>(workspace, p.o_rows);
-  la.slot = reinterpret_cast<short*>(la.t + p.C * K);
+  la.count = reinterpret_cast<int*>(la.t + p.C * K);
+  la.slot = reinterpret_cast<short*>(la.count + p.C);
   flce_status s = listed_chunks(
       p, c, dev,
       [&](const ListedChunk& ch) {
         la.hdr = ch.g->hdr; la.idx = ch.g->idx; la.c0 = ch.c0; la.C = ch.g->C; la.nparts = ch.g->nparts;
-        la.start = const_cast<int*>(ch.g->lists.start);
+        la.slab = const_cast<short*>(ch.g->slab);
         la.id = const_cast<int*>(ch.g->lists.id);
         count_launches(1);
-        return launch_dependent_smem(distill_lists_kernel, static_cast<unsigned>(cdiv(la.C, LIST_ROWS)), 32 * LIST_WARPS,
-                                     lists_smem(K), st, la);
+        return by_groups(K, [&](auto g) {
+          return launch_dependent_smem(distill_lists_kernel<decltype(g)::value>, static_cast<unsigned>(cdiv(la.C, ROWS8)),
+                                       32 * LIST_WARPS, lists_smem(K), st, la);
+        });
       },
       [&](const ListedChunk& ch) {
-        const RowsArgs ra{ch.g->hdr, ch.g->idx, ch.c0, ch.g->C, ch.g->nparts, K, tail, ch.g->stats, ch.g->lists.start,
-                          ch.g->lists.z, la.t, la.slot, ch.g->c2, out};
+        const RowsArgs ra{ch.g->hdr, ch.g->idx, ch.c0, ch.g->C, ch.g->nparts, ch.g->V, K, tail, ch.g->slabs_per_row,
+                          ch.g->stats, la.count, la.id, ch.g->lists.z, la.t, la.slot, ch.g->c2, 1.f / temperature, out};
         count_launches(1);
-        return launch_dependent(distill_rows_kernel, static_cast<unsigned>(cdiv(ch.g->C, 32)), 32 * ROWS_WARPS, st, ra);
+        const unsigned blocks = static_cast<unsigned>(cdiv(ch.g->C, ROWS8));
+        const size_t smem = rows_smem(K, ch.g->slabs_per_row);
+        return K <= 32 ? launch_dependent_smem(distill_rows_kernel<1>, blocks, 32 * ROWS8 * 2, smem, st, ra)
+                       : launch_dependent_smem(distill_rows_kernel<3>, blocks, 32 * ROWS8 * 4, smem, st, ra);
       });
   if (s == FLCE_OK && p.n_chunks > 1) {
     count_launches(1);

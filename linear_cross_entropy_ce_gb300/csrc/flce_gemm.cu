@@ -359,6 +359,9 @@ __device__ __forceinline__ void store_f32x32(float* dst, const float (&v)[32]) {
 // them for pairs: the issue slots are shared with the warps that feed the MMAs,
 // and six an element slowed those (tiles of 8 K blocks: 3.6 us each, without the
 // arithmetic 2.7).
+// OFTEN: logits of -inf are common (forbidden and listed tokens), and two more
+// instructions an element are cheaper than going through them again.
+template <bool OFTEN = false>
 __device__ __forceinline__ Stat stats32(const float (&v)[32], float c2) {
   float mx = v[0];
 #pragma unroll
@@ -374,7 +377,7 @@ __device__ __forceinline__ Stat stats32(const float (&v)[32], float c2) {
     const float2 x = ptx::unpack2(d);
     const uint64_t e = ptx::pack2(ptx::ex2(x.x), ptx::ex2(x.y));
     s2 = ptx::add2(s2, e);
-    d2 = ptx::fma2(d, e, d2);
+    d2 = ptx::fma2(OFTEN ? ptx::pack2(fmaxf(x.x, -1e30f), fmaxf(x.y, -1e30f)) : d, e, d2);
   }
   float sum = ptx::unpack2(s2).x + ptx::unpack2(s2).y;
   float dsum = ptx::unpack2(d2).x + ptx::unpack2(d2).y;
@@ -480,6 +483,14 @@ __device__ __forceinline__ PartLists part_lists(const GemmArgs& a, bool rv, int 
   return p;
 }
 
+// Where columns from c0 on of chunk row grow go if their part is left out.
+__device__ __forceinline__ float* part_slab(const GemmArgs& a, bool rv, int grow, int c0) {
+  const int part = c0 / PART_COLS;
+  if (!rv || part >= a.nparts) return nullptr;
+  const int q = a.slab[static_cast<long long>(part) * a.C + grow];
+  return q < 0 ? nullptr : a.lists.z + (static_cast<long long>(grow) * a.slabs_per_row + q) * PART_COLS + c0 % PART_COLS;
+}
+
 // The next 32 columns' words (registers have no index), around.
 __device__ __forceinline__ void turn_lists(PartLists& p) {
   const uint32_t l = p.listed[0], w = p.allowed[0];
@@ -493,25 +504,28 @@ __device__ __forceinline__ void turn_lists(PartLists& p) {
 }
 
 // 32 logits of a row: the listed ones are written out (unless that was done
-// already) and leave, with the forbidden ones.
+// already) and leave, with the forbidden ones.  True if any row of the warp
+// lost one.
 template <bool TAKE>
-__device__ __forceinline__ void treat_listed(float (&v)[32], uint32_t listed, uint32_t allowed, float*& slot) {
+__device__ __forceinline__ bool treat_listed(float (&v)[32], uint32_t listed, uint32_t allowed, float*& slot) {
   if (TAKE && __any_sync(0xffffffffu, listed != 0u)) {
 #pragma unroll
     for (int k = 0; k < 32; ++k)
       if ((listed >> k) & 1u) *slot++ = v[k];
   }
   const uint32_t keep = allowed & ~listed;
-  if (__any_sync(0xffffffffu, keep != 0xffffffffu)) {
+  const bool some = __any_sync(0xffffffffu, keep != 0xffffffffu);
+  if (some) {
 #pragma unroll
     for (int k = 0; k < 32; ++k) v[k] = (keep >> k) & 1u ? v[k] : -INFINITY;
   }
+  return some;
 }
 
 // Statistics of one row and part.  Bound by the tensor cores from H = 2048 up
 // (4096 tokens at 2048 x 32000 in three segments: 290 us, 1.85 PFLOP/s); at 8 K
 // blocks a tile takes 2.9 us for 2.2 us of MMAs.
-template <bool LISTED>
+template <int LISTED>
 __device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, const Unit& t, int row0, int col0,
                                           uint32_t tbase, int r, PartLists& pl) {
   const int grow = row0 + r;
@@ -528,21 +542,24 @@ __device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, con
 #pragma unroll 1
   for (int j = 0; j < GROUP_COLS / 32; ++j) {
     if (j * 32 >= ncol) {                         // uniform
-      if constexpr (!LISTED) break;
+      if constexpr (LISTED != LISTED_OUT) break;
       turn_lists(pl);
       continue;
     }
     float v[32];
     ptx::tmem_ld32(tbase + j * 32, v);
     pick_target(v, tl, j * 32, ztv);
-    if constexpr (LISTED) {
-      treat_listed<true>(v, pl.listed[0], pl.allowed[0], pl.slot);
+    bool often = false;
+    if constexpr (LISTED == LISTED_OUT) {
+      often = treat_listed<true>(v, pl.listed[0], pl.allowed[0], pl.slot);
       turn_lists(pl);
     }
+    if (LISTED == LISTED_SLABS && pl.slot) store_f32x32(pl.slot + j * 32, v);   // behind the vocabulary: never read
     if (all) store_f32x32(zrow + j * 32, v);
     blank_tail(v, j * 32, ncol, -INFINITY);
-    st = merge(st, stats32(v, a.c2), a.c2);
+    st = merge(st, LISTED == LISTED_OUT && often ? stats32<true>(v, a.c2) : stats32(v, a.c2), a.c2);
   }
+  if (LISTED == LISTED_SLABS && pl.slot) st = Stat{-INFINITY, 0.f, 0.f};   // the row kernel goes through this part
   if (rv) {
     store_stats(a, c0 / PART_COLS, grow, st);
     if (tl >= 0 && tl < ncol) a.zt[grow] = ztv;
@@ -556,7 +573,7 @@ __device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, con
   for (int j = 0; j * 32 < ncol; ++j) {   // uniform over the warp
     float v[32];
     ptx::tmem_ld32(tbase + j * 32, v);
-    if constexpr (LISTED) {
+    if constexpr (LISTED == LISTED_OUT) {
       treat_listed<false>(v, pl.listed[0], pl.allowed[0], pl.slot);
       turn_lists(pl);
     }
@@ -653,7 +670,7 @@ static_assert(sizeof(Exchange) <= EPI_GROUPS * STG_BYTES, "fits in the staging a
 
 // Statistics of one row and part from both halves' registers; false on abort.
 // bar: the named barrier of the part's two warpgroups.
-template <bool LISTED>
+template <int LISTED>
 __device__ __forceinline__ bool epi_stats_seg(const GemmArgs& a, const Shape& s, const Unit& t, int row0, int grp,
                                               float (&z)[2][32], int r, bool ok, float (*ex)[3][BM], uint32_t bar,
                                               PartLists& pl) {
@@ -670,10 +687,12 @@ __device__ __forceinline__ bool epi_stats_seg(const GemmArgs& a, const Shape& s,
   for (int j = 0; j < 2; ++j) {
     if (j * 32 >= ncol) break;                    // uniform
     pick_target(z[j], tl, j * 32, ztv);
-    if constexpr (LISTED) treat_listed<true>(z[j], pl.listed[j], pl.allowed[j], pl.slot);
+    bool often = false;
+    if constexpr (LISTED == LISTED_OUT) often = treat_listed<true>(z[j], pl.listed[j], pl.allowed[j], pl.slot);
+    if (LISTED == LISTED_SLABS && pl.slot) store_f32x32(pl.slot + j * 32, z[j]);
     if (all) store_f32x32(zrow + j * 32, z[j]);
     blank_tail(z[j], j * 32, ncol, -INFINITY);
-    mine = merge(mine, stats32(z[j], a.c2), a.c2);
+    mine = merge(mine, LISTED == LISTED_OUT && often ? stats32<true>(z[j], a.c2) : stats32(z[j], a.c2), a.c2);
   }
   ex[grp][0][r] = mine.m;
   ex[grp][1][r] = mine.s;
@@ -682,7 +701,8 @@ __device__ __forceinline__ bool epi_stats_seg(const GemmArgs& a, const Shape& s,
   const int og = grp ^ 1;
   const Stat other = {ex[og][0][r], ex[og][1][r], ex[og][2][r]};
   const bool first = (grp & 1) == 0;
-  const Stat st = first ? merge(mine, other, a.c2) : merge(other, mine, a.c2);
+  Stat st = first ? merge(mine, other, a.c2) : merge(other, mine, a.c2);
+  if (LISTED == LISTED_SLABS && pl.slot) st = Stat{-INFINITY, 0.f, 0.f};   // the row kernel goes through this part
   if (rv && ncol > 0) {
     if (first) store_stats(a, part, grow, st);
     if (tl >= 0 && tl < ncol) a.zt[grow] = ztv;
@@ -934,14 +954,18 @@ __device__ __forceinline__ bool epi_dx_split(const GemmArgs& a, const Shape& s, 
 // What a kernel is for: the loss, or the two modes of the token log
 // probabilities (MODE_STATS, MODE_DZ), whose kernels of their own leave the
 // loss kernel's registers alone; SEGMENTED those with long sums.
-// LISTED: MODE_STATS of rows with lists, in both forms.
-enum Kind : int { K_LOSS = 0, K_PROBS = 1, K_SEGMENTED = 2, K_LISTED = 3, K_LISTED_SEGMENTED = 4 };
+// LISTED, SLABS: MODE_STATS of rows with lists, in both forms.
+enum Kind : int {
+  K_LOSS = 0, K_PROBS = 1, K_SEGMENTED = 2, K_LISTED = 3, K_LISTED_SEGMENTED = 4, K_SLABS = 5, K_SLABS_SEGMENTED = 6
+};
 
 template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     flce_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
-  constexpr bool PROBS = KIND != K_LOSS, SEG = KIND == K_SEGMENTED || KIND == K_LISTED_SEGMENTED;
-  constexpr bool LISTED = KIND == K_LISTED || KIND == K_LISTED_SEGMENTED;
+  constexpr bool PROBS = KIND != K_LOSS;
+  constexpr bool SEG = KIND == K_SEGMENTED || KIND == K_LISTED_SEGMENTED || KIND == K_SLABS_SEGMENTED;
+  constexpr int LISTED = KIND == K_LISTED || KIND == K_LISTED_SEGMENTED ? LISTED_OUT
+                         : (KIND == K_SLABS || KIND == K_SLABS_SEGMENTED ? LISTED_SLABS : 0);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* stg = smem + STAGES * STAGE_BYTES;
@@ -1158,9 +1182,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     for (int u = pair0; u < s.units; u += npairs) {
       const Unit t = decode_unit<PROBS>(a, s, u);
       PartLists pl;
-      if constexpr (LISTED) {
+      if constexpr (LISTED != 0) {
         const int grow = t.m0 + half + r, c0 = t.n0 + grp * QUARTER;
-        pl = part_lists(a, grow < s.Cl, grow, c0, min(QUARTER, a.V - c0));
+        if constexpr (LISTED == LISTED_OUT) pl = part_lists(a, grow < s.Cl, grow, c0, min(QUARTER, a.V - c0));
+        else pl.slot = part_slab(a, grow < s.Cl, grow, c0);
       }
       float z[2][32];
 #pragma unroll
@@ -1184,7 +1209,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         if (acc == 0) acc_phase ^= 1u;
       }
       const int row0 = t.m0 + half;
-      if (LISTED || a.mode == MODE_STATS) {
+      if (LISTED != 0 || a.mode == MODE_STATS) {
         ok = epi_stats_seg<LISTED>(a, s, t, row0, grp, z, r, ok, ex->v[buf], EPI_BAR_SET + static_cast<uint32_t>(grp / 2),
                                    pl);
         buf ^= 1u;
@@ -1246,9 +1271,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         }
       }
       PartLists pl;
-      if constexpr (LISTED) {
+      if constexpr (LISTED != 0) {
         const int grow = t.m0 + half + r, c0 = t.n0 + col0;
-        pl = part_lists(a, grow < s.Cl, grow, c0, min(GROUP_COLS, a.V - c0));
+        if constexpr (LISTED == LISTED_OUT) pl = part_lists(a, grow < s.Cl, grow, c0, min(GROUP_COLS, a.V - c0));
+        else pl.slot = part_slab(a, grow < s.Cl, grow, c0);
       }
       ok = wait_phase(&ctl->tfull[set], acc_phase, ctl, to, true, hdr, W_TMEM_FULL, u | (set << 24));
       if (!ptx::named_bar_and(sbar, SET_THREADS, ok)) break;
@@ -1257,7 +1283,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       const int row0 = t.m0 + half;
       bool cont = true;
       if constexpr (PROBS) {
-        if (LISTED || a.mode == MODE_STATS) epi_stats<LISTED>(a, s, t, row0, col0, tbase, r, pl);
+        if (LISTED != 0 || a.mode == MODE_STATS) epi_stats<LISTED>(a, s, t, row0, col0, tbase, r, pl);
         else epi_dz(a, s, t, row0, col0, tbase, r);
       } else if (t.kind == U_LOGITS)
         epi_logits(a, s, t, row0, col0, tbase, r);
@@ -1305,6 +1331,10 @@ cudaError_t gemm_prepare(int /*device*/) {
     e = cudaFuncSetAttribute(flce_gemm_kernel<K_LISTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(flce_gemm_kernel<K_LISTED_SEGMENTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(flce_gemm_kernel<K_SLABS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(flce_gemm_kernel<K_SLABS_SEGMENTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   return e;
 }
 
@@ -1335,7 +1365,10 @@ cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps& m, int grid, cudaStre
   attr.val.programmaticStreamSerializationAllowed = dependent ? 1 : 0;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (a.mode == MODE_STATS && a.listed)
+  if (a.mode == MODE_STATS && a.listed == LISTED_SLABS)
+    return launch_result(a.seg_kb * BK < a.H ? cudaLaunchKernelEx(&cfg, flce_gemm_kernel<K_SLABS_SEGMENTED>, m, a)
+                                             : cudaLaunchKernelEx(&cfg, flce_gemm_kernel<K_SLABS>, m, a));
+  if (a.mode == MODE_STATS && a.listed == LISTED_OUT)
     return launch_result(a.seg_kb * BK < a.H ? cudaLaunchKernelEx(&cfg, flce_gemm_kernel<K_LISTED_SEGMENTED>, m, a)
                                              : cudaLaunchKernelEx(&cfg, flce_gemm_kernel<K_LISTED>, m, a));
   if (a.mode == MODE_STATS || a.mode == MODE_DZ)

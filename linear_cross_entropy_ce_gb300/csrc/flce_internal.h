@@ -47,6 +47,10 @@ enum GemmMode : int {
                     // rows' log-sum-exp, entropy and upstream gradients, as bf16
 };
 
+// Tokens of a row that MODE_STATS treats apart (GemmArgs::listed).
+constexpr int LISTED_OUT = 1;     // taken out one by one, forbidden ones left out; their logits in lists.z [C][cap]
+constexpr int LISTED_SLABS = 2;   // a part that holds any is left out whole, its logits in lists.z [C][slabs_per_row][128]
+
 // Unit kinds a MODE_BWD launch leaves out (GemmArgs::skip).
 constexpr int SKIP_DX = 1;
 constexpr int SKIP_DW = 2;
@@ -104,8 +108,10 @@ struct GemmArgs {
   uint32_t* group_max;  //   [C][group_stride] largest part max of each of K groups of parts
   int group_stride;     //   K rounded up to 4
   const DzRow* rowc;    // DZ: [C] (rows past the valid ones hold zeros)
-  int listed;           // STATS: lists hold tokens that are treated apart
-  ListView lists;
+  int listed;           // STATS: LISTED_*
+  ListView lists;       // LISTED_OUT: the tokens taken out; z of both
+  const short* slab;    // LISTED_SLABS: [nparts][C] the row's slab of the part, or -1
+  int slabs_per_row;
 };
 
 // Tensor maps of one launch.  LOGITS: a0 = Xc (K-major), b0 = W (K-major).
@@ -207,9 +213,12 @@ cudaError_t launch_gather(const uint16_t* hidden, const int* targets, const int*
 // segments, each from zero, and add these up rounded to nearest.  With
 // 2 sqrt(blocks) blocks a segment the error grows with H as that of an fp32
 // product on the CUDA cores does; up to 11 blocks it is below 1e-6 anyway.
-inline int segment_blocks(long long H) {
+// A divergence of distributions that nearly agree keeps the logits' absolute
+// errors, so it takes them in two segments from H = 320 on (4096 tokens at
+// 512 x 16000: kl off by 6e-7 of its norm, 1.3e-6 in one piece).
+inline int segment_blocks(long long H, int whole = 11) {
   const int blocks = static_cast<int>(cdiv(H, BK));
-  const int most = std::max(11, static_cast<int>(2.0 * std::sqrt(static_cast<double>(blocks))));
+  const int most = std::max(whole, static_cast<int>(2.0 * std::sqrt(static_cast<double>(blocks))));
   return static_cast<int>(cdiv(blocks, cdiv(blocks, most)));   // of equal length
 }
 // Few tokens: the weight streamed once past all of them (flce_stream.cu).
@@ -267,7 +276,7 @@ cudaError_t launch_stream_taken(const StreamArgs& a, const StreamMaps& m, const 
 constexpr long long FRONT_MAX_TOKENS = 16384;
 struct FrontArgs {
   const uint16_t* hidden;
-  const int* targets;
+  const int* targets;                 // null: every token counts, with target 0
   int N, H, V, ii, C, K;
   int *hdr, *idx, *tc;
   uint16_t* xc;
@@ -303,10 +312,9 @@ struct DistillGrad {
 cudaError_t launch_distill_grad_rows(const DistillGrad& d, long long N, int V, float temperature, cudaStream_t s);
 cudaError_t launch_distill_patch(const int* hdr, const int* idx, long long c0, int C, int K, int V, long long ldz,
                                  const int* ids, const uint16_t* patch, uint16_t* z, cudaStream_t s);
-cudaError_t distill_prepare();
 cudaError_t constrained_prepare();
-// seg_kb, the time limit and the tensor maps of a streaming call.
-bool stream_setup(StreamArgs* a, StreamMaps* m, const void* hidden, const void* weight);
+// The time limit and the tensor maps of a streaming call.
+bool stream_setup(StreamArgs* a, StreamMaps* m, const void* hidden, const void* weight, int seg_kb);
 cudaError_t launch_dx_reduce(const int* hdr, const int* idx, long long c0, int C, int H, int splits, const float* parts,
                              uint16_t* grad_hidden, cudaStream_t s);
 cudaError_t launch_mark_failed(const int* hdr, uint16_t* grad_hidden, float* grad_weight, int gw_bf16,

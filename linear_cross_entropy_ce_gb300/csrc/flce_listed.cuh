@@ -1,8 +1,8 @@
 // The chunked form (more than STREAM_MAX_TOKENS tokens) of the operators whose
 // rows have lists: workspace and launch sequence.  Per chunk of valid tokens:
-// rows gathered, lists made, the logits GEMM with the listed tokens taken out
-// (MODE_STATS, GemmArgs::listed), and the operator's own row kernels, which
-// bring the listed logits back in.
+// rows gathered, lists made, the logits GEMM with the listed tokens or their
+// parts left out (MODE_STATS, GemmArgs::listed), and the operator's own row
+// kernels, which bring them back in.
 #pragma once
 
 #include <algorithm>
@@ -25,13 +25,14 @@ struct ListedSizes {
   int K;                 // top alternatives
   long long cap;         // entries of a row at most
   long long row_bytes;   // what the operator keeps per chunk row beside them
-  long long call_bytes;  // and per call
+  int table;             // bytes of a row's place in the table by parts: 4 (where a part's entries begin), 2 (its slab)
+  long long z;           // logits kept of a row
 };
 
 struct ListedPlan {
   long long C = 0, n_chunks = 0, ldz = 0;
   int nvt = 0, nparts = 0, group_stride = 0;
-  size_t o_idx = 0, o_targets = 0, o_call = 0, o_xc = 0, o_tc = 0, o_zt = 0, o_ml = 0, o_stats = 0, o_bound = 0,
+  size_t o_idx = 0, o_targets = 0, o_xc = 0, o_tc = 0, o_zt = 0, o_ml = 0, o_stats = 0, o_bound = 0,
          o_group = 0, o_zf = 0, o_start = 0, o_id = 0, o_z = 0, o_rows = 0, total = 0;
 };
 
@@ -51,7 +52,6 @@ inline ListedPlan listed_layout(const ListedSizes& q, long long C) {
   };
   p.o_idx = take(size_t(q.N) * 4);
   p.o_targets = take(size_t(q.N) * 4);
-  p.o_call = take(size_t(q.call_bytes));
   p.o_xc = take(size_t(C) * q.H * 2);
   p.o_tc = take(size_t(C) * 4);
   p.o_zt = take(size_t(C) * 4);
@@ -62,9 +62,9 @@ inline ListedPlan listed_layout(const ListedSizes& q, long long C) {
     p.o_group = take(size_t(C) * p.group_stride * 4);
     p.o_zf = take(size_t(C) * p.ldz * 4);
   }
-  p.o_start = take(size_t(C) * (p.nparts + 1) * 4);
+  p.o_start = take(size_t(C) * (p.nparts + 1) * q.table);
   p.o_id = take(size_t(C) * q.cap * 4);
-  p.o_z = take(size_t(C) * q.cap * 4);
+  p.o_z = take(size_t(C) * q.z * 4);
   p.o_rows = take(size_t(C) * q.row_bytes);
   p.total = off;
   return p;
@@ -95,9 +95,10 @@ inline size_t listed_default_bytes(const ListedSizes& q) {
 struct ListedCall {
   ListedSizes q;
   const void *hidden, *weight;
-  const int* targets;       // which rows count, and what is picked
+  const int* targets;       // which rows count, and what is picked; null with listed_front(): all rows
   int ii;
   float temperature;
+  int seg_kb;               // segment_blocks()
   const uint32_t* mask;     // or null
   long long mask_stride;
   float *logp, *entropy, *lse;   // what left-out rows get 0 (or NaN) in, in a call of one chunk
@@ -112,6 +113,9 @@ struct ListedChunk {
   bool last, only;          // the last chunk; the only one, whose rows the front kernel has gathered
   const GemmArgs* g;
 };
+
+// One kernel compacts the tokens and gathers their rows.
+inline bool listed_front(const ListedPlan& p, long long N) { return p.n_chunks == 1 && N <= FRONT_MAX_TOKENS; }
 
 // lists(chunk): launches what fills the lists of the chunk's rows; it waits for
 // its predecessor.  rows(chunk): launches the row kernels.
@@ -148,9 +152,11 @@ flce_status listed_chunks(const ListedPlan& p, const ListedCall& c, const Device
     g.group_max = at<uint32_t>(ws, p.o_group);
   }
   g.group_stride = p.group_stride;
-  g.seg_kb = segment_blocks(q.H);
+  g.seg_kb = c.seg_kb;
   g.c2 = 1.4426950408889634f / c.temperature;
-  g.listed = 1;
+  g.listed = q.table == 4 ? LISTED_OUT : LISTED_SLABS;
+  g.slab = at<short>(ws, p.o_start);
+  g.slabs_per_row = static_cast<int>(q.z / PART_COLS);
   g.lists.start = at<int>(ws, p.o_start);
   g.lists.boundaries = p.nparts + 1;
   g.lists.id = at<int>(ws, p.o_id);
@@ -160,7 +166,7 @@ flce_status listed_chunks(const ListedPlan& p, const ListedCall& c, const Device
   g.lists.mask_stride = c.mask_stride;
 
   const int grid = 2 * static_cast<int>(std::min<long long>(cdiv(p.C, PAIR_M) * p.nvt, dev.pairs));
-  const bool front = p.n_chunks == 1 && q.N <= FRONT_MAX_TOKENS;
+  const bool front = listed_front(p, q.N);
   int* hdr = at<int>(ws, 0);
   int* idx = at<int>(ws, p.o_idx);
   if (front) {

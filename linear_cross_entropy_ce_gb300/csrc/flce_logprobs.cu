@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(FRONT_THREADS) probs_front_kernel(const FrontA
   int before = 0, total = 0, bad = 0;
 #pragma unroll 8
   for (int i = tid; i < a.N; i += FRONT_THREADS) {
-    const int x = a.targets[i];
+    const int x = a.targets ? a.targets[i] : 0;
     const bool in = x >= 0 && x < a.V;
     const bool valid = in && x != a.ii;
     total += valid;
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(FRONT_THREADS) probs_front_kernel(const FrontA
   }
   if (w == 0) {   // the place of each token of this block, or -1
     const int n = n0 + lane;
-    const int x = lane < FRONT_TOKENS && n < a.N ? a.targets[n] : -1;
+    const int x = lane < FRONT_TOKENS && n < a.N ? (a.targets ? a.targets[n] : 0) : -1;
     const bool valid = x >= 0 && x < a.V && x != a.ii && lane < FRONT_TOKENS && n < a.N;
     const unsigned m = __ballot_sync(0xffffffffu, valid);
     if (lane < FRONT_TOKENS) dst[lane] = valid ? before + __popc(m & ((1u << lane) - 1u)) : -1;
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(FRONT_THREADS) probs_front_kernel(const FrontA
 #pragma unroll 8
       for (int c = lo + lane; c < hi; c += 32) to[c] = from[c];
       if (first && lane == 0) {
-        a.tc[r] = a.targets[n];
+        a.tc[r] = a.targets ? a.targets[n] : 0;
         a.idx[r] = static_cast<int>(n);
         if (a.rowc) a.rowc[r] = dz_row(a.temperature, a.lse_in[n], a.entropy_in, a.grad_logp, a.grad_entropy, n);
       }
@@ -431,8 +431,8 @@ StreamPlan stream_plan(long long N, long long V, int K, int sms) {
 
 }  // namespace
 
-bool stream_setup(StreamArgs* a, StreamMaps* m, const void* hidden, const void* weight) {
-  a->seg_kb = segment_blocks(a->H);
+bool stream_setup(StreamArgs* a, StreamMaps* m, const void* hidden, const void* weight, int seg_kb) {
+  a->seg_kb = seg_kb;
   a->timeout_ns = wait_timeout_ns();
   if (const unsigned long long t = take_armed_stall()) {
     a->debug_stall = 1;
@@ -531,7 +531,7 @@ flce_status flce_logprobs(const void* hidden, const void* weight, const int32_t*
     a.fail = at<int>(workspace, p.o_fail);
     a.logp = logp; a.entropy = entropy; a.lse = lse; a.top_ids = top_ids; a.top_logp = top_logp;
     StreamMaps m;
-    if (!stream_setup(&a, &m, hidden, weight)) return FLCE_ECUDA;
+    if (!stream_setup(&a, &m, hidden, weight, segment_blocks(H))) return FLCE_ECUDA;
     const ProfScope prof = prof_launch_begin(st);
     const cudaError_t e = launch_stream(a, m, st);
     prof_launch_end(prof, MODE_STATS, st);

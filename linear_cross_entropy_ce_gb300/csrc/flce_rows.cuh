@@ -43,6 +43,40 @@ __device__ __forceinline__ void merge_parts(const float* stats, int nparts, int 
   }
 }
 
+// The same for 8 rows by a block's first 8 warps, of which warp w gets row w: for
+// row kernels with work of their own, whose other warps do that meanwhile.  A
+// warp reads four parts at a time, 32 bytes of each.  The order is that of
+// merge_parts.
+constexpr int ROWS8 = 8;
+constexpr uint32_t ROWS8_BAR = 1, ROWS8_BAR_OTHERS = 2;   // named barriers of the 8 warps, and of the others
+__device__ __forceinline__ Stat merge_parts8(const float* stats, int nparts, int C, float c2, int r0, int Cl, int lane,
+                                             int w, Stat (*part)[ROWS8]) {
+  const int r = r0 + lane % ROWS8;
+  Stat acc = {-INFINITY, 0.f, 0.f};
+  if (r < Cl) {
+    const size_t np = static_cast<size_t>(nparts) * C;
+    for (int p0 = w * 4 + lane / ROWS8; p0 < nparts; p0 += 2 * ROWS_BATCH * 32) {
+      Stat q[2 * ROWS_BATCH];   // in flight
+#pragma unroll
+      for (int k = 0; k < 2 * ROWS_BATCH; ++k) {
+        const int p = p0 + k * 32;
+        const float* f = stats + static_cast<size_t>(p) * C + r;
+        q[k] = p < nparts ? Stat{f[0], f[np], f[2 * np]} : Stat{-INFINITY, 0.f, 0.f};
+      }
+      acc = merge(acc, merge(merge(q[0], q[1], c2), merge(q[2], q[3], c2), c2), c2);
+      if (p0 + ROWS_BATCH * 32 < nparts) acc = merge(acc, merge(merge(q[4], q[5], c2), merge(q[6], q[7], c2), c2), c2);
+    }
+  }
+  part[w * 4 + lane / ROWS8][lane % ROWS8] = acc;
+  ptx::named_bar_sync(ROWS8_BAR, 32 * ROWS8);
+  acc = part[lane][w];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    acc = merge(acc, Stat{__shfl_down_sync(0xffffffffu, acc.m, o), __shfl_down_sync(0xffffffffu, acc.s, o),
+                          __shfl_down_sync(0xffffffffu, acc.d, o)}, c2);
+  return acc;   // in lane 0
+}
+
 constexpr int TOP_WARPS = 4;
 constexpr int TOP_BATCH = 8;
 

@@ -37,7 +37,7 @@ cudaError_t launch_stream(const StreamArgs& a, const StreamMaps& m, cudaStream_t
   }
   const cudaError_t e = launch_all<LISTS_NONE>(a, m, StreamLists{}, a.group_max != nullptr, s);
   if (e != cudaSuccess) return e;
-  return launch_dependent(logprob_stream_merge_kernel<false>, a.N, MERGE_THREADS, s, a);
+  return launch_dependent(logprob_stream_merge_kernel<false>, a.N, MERGE_THREADS, s, a, ListView{});
 }
 
 }  // namespace flce

@@ -35,10 +35,12 @@
 // With lists (ListView; the streaming kernel waits for them before its first
 // finished tile, the weight streams meanwhile) a warp that has turned a token's
 // tile around first treats the token's listed logits of that tile: under rules
-// (LISTS_RULED) they are changed in place and forbidden tokens become -inf, so
-// that all else sees the constrained logits; a teacher's tokens (LISTS_TAKEN)
-// are written out and leave the statistics.  Where the tile's entries begin and
-// the words of its mask are fetched while the tile is being computed.
+// (LISTS_RULED) they are changed in place, and forbidden tokens count as -inf; a
+// teacher's tokens (LISTS_TAKEN) are written out and leave the statistics.  Where
+// the tile's entries begin and the words of its mask are fetched while the tile
+// is being computed, a token's entries while the one before it is worked on.
+// (128 tokens with 4001 ids of history, masks and 20 alternatives at 4096 x
+// 128256: 210 us, fetched when needed 240.)
 #pragma once
 
 #include "flce_internal.h"
@@ -109,38 +111,48 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctl* ctl, u
   return ptx::mbar_test(bar, parity) || wait_slow(bar, parity, ctl, timeout_ns, honor_abort, hdr, site);
 }
 
-// One token's listed logits of a tile, [r0, r0 + rows) of the vocabulary, in its
-// slice z of shared memory, by the warp that goes on with it.
+// One of a token's entries in a tile, per lane: fetched while the two tokens
+// before it are worked on (the loads of one entry after the other cost the epilogue 1.5
+// us a token and tile).
+struct Entry {
+  int id, seen;
+  float bias;
+};
+
 template <int LISTS>
-__device__ __forceinline__ void treat_listed(const StreamLists& l, int tk, const int* ahead, int r0, int rows, float* z,
-                                             int lane) {
-  const int e1 = ahead[1];
-  const long long row = tk * l.lists.cap;
-  if (LISTS == LISTS_RULED) {
-    if (ahead[0] < e1) {
-      const RowRules rules = row_rules(l.rules, tk);
-      for (int e = ahead[0] + lane; e < e1; e += 32) {
-        const int at = l.lists.id[row + e] - r0;
-        if (static_cast<unsigned>(at) < static_cast<unsigned>(rows))
-          z[at] = ruled(z[at], l.rules.seen[row + e], l.rules.bias ? l.rules.bias[row + e] : 0.f, rules);
-      }
-      __syncwarp();
+__device__ __forceinline__ Entry fetch_entry(const StreamLists& l, int tk, int e, int e1) {
+  Entry x = {-1, 0, 0.f};
+  if (e < e1) {
+    const long long at = tk * l.lists.cap + e;
+    x.id = l.lists.id[at];
+    if (LISTS == LISTS_RULED) {
+      x.seen = l.rules.seen[at];
+      if (l.rules.bias) x.bias = l.rules.bias[at];
     }
-    if (l.lists.mask) {
-#pragma unroll
-      for (int j = 0; j < TILE_ROWS; j += 32) {
-        const int bit = r0 % 32 + j + lane;   // r0: a multiple of 16
-        if (!((ahead[2 + bit / 32] >> (bit % 32)) & 1)) z[j + lane] = -INFINITY;
-      }
-    }
-  } else {
-    for (int e = ahead[0] + lane; e < e1; e += 32) {
-      const int at = l.lists.id[row + e] - r0;
-      if (static_cast<unsigned>(at) < static_cast<unsigned>(rows)) {
-        l.lists.z[row + e] = z[at];
+  }
+  return x;
+}
+
+// One token's listed logits of a tile, [r0, r0 + rows) of the vocabulary, in its
+// slice z of shared memory, by the warp that goes on with it.  x: each lane's
+// first entry.
+template <int LISTS>
+__device__ __forceinline__ void treat_listed(const StreamLists& l, int tk, int e0, int e1, Entry x, const RowRules& rules,
+                                             int r0, int rows, float* z, int lane) {
+  if (e0 >= e1) return;   // uniform
+  for (int e = e0 + lane;;) {
+    const int at = x.id - r0;
+    if (x.id >= 0 && static_cast<unsigned>(at) < static_cast<unsigned>(rows)) {
+      if (LISTS == LISTS_RULED) {
+        z[at] = ruled(z[at], x.seen, x.bias, rules);
+      } else {
+        l.lists.z[tk * l.lists.cap + e] = z[at];
         z[at] = -INFINITY;
       }
     }
+    e += 32;
+    if (e >= e1) break;
+    x = fetch_entry<LISTS>(l, tk, e, e1);
   }
   __syncwarp();
 }
@@ -274,6 +286,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
     // the groups' maxima have been cleared, the lists have been made
     if (LISTS != LISTS_NONE || a.group_max) ptx::grid_dependency_wait();
+    RowRules rules = {1.f, 0.f, 0.f};   // lane j: of this warp's j-th token
+    static_assert(NT / EPI_WARPS <= 32, "a lane per token");
+    if (LISTS == LISTS_RULED && lane < NT / EPI_WARPS && w + lane * EPI_WARPS < a.N)
+      rules = row_rules(l.rules, w + lane * EPI_WARPS);
     uint32_t acc = 0, acc_phase = 0;
     for (int i = 0; i < range.tiles; ++i) {
       if (a.group_max) {   // the bounds of this warp's tokens
@@ -306,6 +322,15 @@ __global__ void __launch_bounds__(THREADS, 1)
           ahead[tk * AHEAD + c] = x;
         }
         __syncwarp();
+      }
+      constexpr int DEPTH = 2;   // tokens whose entries are on their way
+      Entry entry[DEPTH];
+#pragma unroll
+      for (int k = 0; k < DEPTH; ++k) {
+        entry[k] = Entry{-1, 0, 0.f};
+        const int tk = w + k * EPI_WARPS;
+        if (LISTS != LISTS_NONE && tk < a.N)
+          entry[k] = fetch_entry<LISTS>(l, tk, ahead[tk * AHEAD] + lane, ahead[tk * AHEAD + 1]);
       }
       const uint32_t tb0 = tmem + (static_cast<uint32_t>(q * 32) << 16) + half * NT;
       float sum[SEG ? NT : 1];   // SEG: this row's logits so far
@@ -371,11 +396,26 @@ __global__ void __launch_bounds__(THREADS, 1)
           const int tk = n0 + k;
           if (tk >= a.N) break;
           float* z = turn + k * TILE_ROWS;
-          if constexpr (LISTS != LISTS_NONE) treat_listed<LISTS>(l, tk, ahead + tk * AHEAD, r0, rows, z, lane);
+          if constexpr (LISTS != LISTS_NONE) {
+            const Entry now = entry[0];
+#pragma unroll
+            for (int e = 0; e + 1 < DEPTH; ++e) entry[e] = entry[e + 1];
+            const int next = tk + DEPTH * EPI_WARPS;
+            if (next < a.N)
+              entry[DEPTH - 1] = fetch_entry<LISTS>(l, next, ahead[next * AHEAD] + lane, ahead[next * AHEAD + 1]);
+            const int j = tk / EPI_WARPS;
+            const RowRules mine = {__shfl_sync(0xffffffffu, rules.repetition, j), __shfl_sync(0xffffffffu, rules.frequency, j),
+                                   __shfl_sync(0xffffffffu, rules.presence, j)};
+            treat_listed<LISTS>(l, tk, ahead[tk * AHEAD], ahead[tk * AHEAD + 1], now, mine, r0, rows, z, lane);
+          }
           float x[8], mx = -INFINITY;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             x[j] = j * 32 + lane < rows ? z[j * 32 + lane] : -INFINITY;
+            if (LISTS == LISTS_RULED && l.lists.mask) {
+              const int bit = r0 % 32 + lane;   // r0: a multiple of 16
+              if (!((ahead[tk * AHEAD + 2 + j + bit / 32] >> (bit % 32)) & 1)) x[j] = -INFINITY;
+            }
             mx = fmaxf(mx, x[j]);
           }
 #pragma unroll
@@ -457,7 +497,7 @@ constexpr int MERGE_BATCH = 4;   // tile maxima per thread in flight
 // forbidden target has a log probability of -inf, and a row with nothing left a
 // log-sum-exp of -inf and no entropy; without targets all rows count.
 template <bool RULED>
-__global__ void __launch_bounds__(MERGE_THREADS) logprob_stream_merge_kernel(const StreamArgs a) {
+__global__ void __launch_bounds__(MERGE_THREADS) logprob_stream_merge_kernel(const StreamArgs a, const ListView v) {
   __shared__ Stat part[MERGE_WARPS];
   __shared__ float sv[MERGE_WARPS][32];
   __shared__ int si[MERGE_WARPS][32];
@@ -467,7 +507,8 @@ __global__ void __launch_bounds__(MERGE_THREADS) logprob_stream_merge_kernel(con
   const bool left = scored && t == a.ii;
   const bool bad = scored && !left && (t < 0 || t >= a.V);
   ptx::grid_dependency_wait();
-  const float zt = bad || left || !scored ? 0.f : a.zt[n];
+  float zt = bad || left || !scored ? 0.f : a.zt[n];
+  if (RULED && scored && !left && !bad && v.mask && !((v.mask[n * v.mask_stride + t / 32] >> (t % 32)) & 1u)) zt = -INFINITY;
   const int tiles = a.K > 0 ? a.ctas * a.max_tiles : 0;
   const float* tile_max = a.tile_max + static_cast<size_t>(n) * tiles;
   float cv[MERGE_BATCH];

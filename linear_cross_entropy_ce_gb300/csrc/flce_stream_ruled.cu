@@ -8,7 +8,7 @@ cudaError_t stream_ruled_prepare() { return prepare_all<LISTS_RULED>(); }
 cudaError_t launch_stream_ruled(const StreamArgs& a, const StreamMaps& m, const StreamLists& l, cudaStream_t s) {
   const cudaError_t e = launch_all<LISTS_RULED>(a, m, l, true, s);
   if (e != cudaSuccess) return e;
-  return launch_dependent(logprob_stream_merge_kernel<true>, a.N, MERGE_THREADS, s, a);
+  return launch_dependent(logprob_stream_merge_kernel<true>, a.N, MERGE_THREADS, s, a, l.lists);
 }
 
 }  // namespace flce
