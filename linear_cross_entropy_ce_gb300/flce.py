@@ -780,11 +780,19 @@ def constrained_logprobs(hidden: torch.Tensor, weight: torch.Tensor, targets: Op
             workspace = new_workspace(nb, dev)
         else:
             _check_workspace(workspace, dev)
-        row = ((N,), torch.float32)
-        o, made = _outputs(out, {"logp": row if targets is not None else None, "lse": row,
-                                 "entropy": row if entropy else None,
-                                 "top_ids": ((N, top_k), torch.int32) if top_k else None,
-                                 "top_logp": ((N, top_k), torch.float32) if top_k else None}, dev)
+        if out is None:   # spelled out: a decode step is as short as its host work
+            f32 = torch.float32
+            o = made = {"logp": torch.empty(N, dtype=f32, device=dev) if targets is not None else None,
+                        "lse": torch.empty(N, dtype=f32, device=dev),
+                        "entropy": torch.empty(N, dtype=f32, device=dev) if entropy else None,
+                        "top_ids": torch.empty((N, top_k), dtype=torch.int32, device=dev) if top_k else None,
+                        "top_logp": torch.empty((N, top_k), dtype=f32, device=dev) if top_k else None}
+        else:
+            row = ((N,), torch.float32)
+            o, made = _outputs(out, {"logp": row if targets is not None else None, "lse": row,
+                                     "entropy": row if entropy else None,
+                                     "top_ids": ((N, top_k), torch.int32) if top_k else None,
+                                     "top_logp": ((N, top_k), torch.float32) if top_k else None}, dev)
         _ok(library().flce_constrained_logprobs(_addr(hidden), _addr(weight), _addr(targets), N, H, V,
                                                 _ignored(ignore_index), float(temperature), top_k, ctypes.byref(c),
                                                 _addr(made["logp"]), _addr(made["entropy"]), _addr(made["lse"]),
@@ -843,8 +851,15 @@ def topk_distill(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: torch.
             workspace = new_workspace(nb, dev)
         else:
             _check_workspace(workspace, dev)
-        row = ((N,), torch.float32)
-        o, made = _outputs(out, {"kl": row, "lse": row, "rest_logp": row, "student_logp": ((N, K), torch.float32)}, dev)
+        if out is None:   # spelled out: a small call is as short as its host work
+            f32 = torch.float32
+            o = made = {"kl": torch.empty(N, dtype=f32, device=dev), "lse": torch.empty(N, dtype=f32, device=dev),
+                        "rest_logp": torch.empty(N, dtype=f32, device=dev),
+                        "student_logp": torch.empty((N, K), dtype=f32, device=dev)}
+        else:
+            row = ((N,), torch.float32)
+            o, made = _outputs(out, {"kl": row, "lse": row, "rest_logp": row, "student_logp": ((N, K), torch.float32)},
+                               dev)
         _ok(library().flce_topk_distill(_addr(hidden), _addr(weight), _addr(teacher_ids), _addr(teacher_logp), N, H, V, K,
                                         float(temperature), int(bool(tail)), _addr(made["kl"]), _addr(made["lse"]),
                                         _addr(made["rest_logp"]), _addr(made["student_logp"]), _addr(workspace),

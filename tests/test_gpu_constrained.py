@@ -112,7 +112,9 @@ CASES = [  # N, H, V, K, L, B, mask, targets, T
     (129, 64, 512, 9, 64, 0, True, True, 1.0), (257, 192, 1030, 4, 900, 11, True, False, 1.0),
     (300, 64, 512, 0, 0, 3, False, True, 0.9), (700, 520, 4099, 12, 100, 0, True, True, 1.0),
     (200, 8, 1, 1, 2, 2, True, True, 1.0), (200, 8, 300, 32, 310, 20, False, False, 1.0),
-    (300, 1024, 9001, 6, 500, 4, True, True, 1.0), (131, 64, 40003, 8, 60, 0, False, False, 1.0)]
+    (300, 1024, 9001, 6, 500, 4, True, True, 1.0), (131, 64, 40003, 8, 60, 0, False, False, 1.0),
+    (150, 1024, 30000, 4, 900, 3, True, True, 1.0), (16500, 8, 300, 3, 20, 2, True, True, 1.0),
+    (16500, 8, 40, 0, 9, 0, False, False, 1.0)]
 
 
 @pytest.mark.parametrize("N,H,V,K,L,B,mask,scored,T", CASES)
@@ -338,3 +340,80 @@ def test_time_out_marks_every_row(env, N):
     assert torch.isnan(o["lse"]).all() and (o["top_ids"] == -1).all() and torch.isnan(o["top_logp"]).all()
     again = flce.constrained_logprobs(f(X), f(W), top_k=3, **kw)
     assert flce.query_status(again["workspace"]) == flce.FLCE_OK and torch.equal(again["lse"], good["lse"])
+
+
+@pytest.mark.parametrize("N", [3, 130])
+def test_rows_further_apart_than_32_bits(env, N):
+    """Rows of the matrices whose offsets, in elements, pass 2^31."""
+    flce, torch, dev = env
+    V, L, B = 700, 40, 3
+    X, W = head(N, 64, V, 8)
+    k = rules(N, V, L, B, True, 8)
+    f = lambda a: torch.from_numpy(a).to(torch.bfloat16).to(dev)  # noqa: E731
+    kw = to_kw(torch, dev, k)
+    want = flce.constrained_logprobs(f(X), f(W), top_k=4, **kw)
+    stride = (1 << 31) // (N - 1) + 64
+    ints = torch.empty((N - 1) * stride + 256, dtype=torch.int32, device=dev)
+    assert (N - 1) * stride > 1 << 31
+
+    def far(a, at):
+        flat = ints if a.dtype == torch.int32 else ints.view(torch.float32)
+        v = flat[at:].as_strided((N, a.shape[1]), (stride, 1), at)
+        v.copy_(a)
+        return v
+
+    far_kw = dict(kw, history=far(kw["history"], 0), bias_ids=far(kw["bias_ids"], 50), bias=far(kw["bias"], 60),
+                  mask=far(kw["mask"], 70))
+    assert far_kw["history"].stride(0) == stride
+    got = flce.constrained_logprobs(f(X), f(W), top_k=4, **far_kw)
+    for n in ("lse", "entropy", "top_ids", "top_logp"):
+        assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("N", [2, 140])
+def test_one_token_said_very_often(env, N):
+    """Histories longer than a block holds, of few different tokens."""
+    flce, torch, dev = env
+    V, L = 900, 30011
+    X, W = head(N, 64, V, 9)
+    r = np.random.default_rng(9)
+    h = np.where(r.random((N, L)) < 0.7, 17, r.integers(0, 30, (N, L))).astype(np.int32)
+    k = dict(history=h, prompt_lens=np.full(N, 11, np.int32), frequency=np.full(N, 2.0 ** -12, np.float32),
+             repetition=np.full(N, 1.25, np.float32))
+    f = lambda a: torch.from_numpy(a).to(torch.bfloat16).to(dev)  # noqa: E731
+    o = flce.constrained_logprobs(f(X), f(W), top_k=6, **to_kw(torch, dev, k))
+    rows = [0, N - 1]
+    ref = constrained_oracle(rules_oracle(X[rows] @ W.T, **{n: a[rows] for n, a in k.items()}), top_k=6)
+    check({n: o[n][rows] for n in ("lse", "entropy", "top_ids", "top_logp")}, ref, 6, False)
+
+
+@pytest.mark.parametrize("N", [6, 150])
+def test_repeated_calls_agree_bit_for_bit(env, N):
+    flce, torch, dev = env
+    X, W = head(N, 64, 2000, 10)
+    kw = to_kw(torch, dev, rules(N, 2000, 3000, 40, True, 10))
+    f = lambda a: torch.from_numpy(a).to(torch.bfloat16).to(dev)  # noqa: E731
+    a = flce.constrained_logprobs(f(X), f(W), top_k=7, **kw)
+    for _ in range(5):
+        b = flce.constrained_logprobs(f(X), f(W), top_k=7, **kw)
+        for n in ("lse", "entropy", "top_ids", "top_logp"):
+            assert torch.equal(a[n], b[n]), n
+
+
+def test_empty_histories_and_biases(env):
+    flce, torch, dev = env
+    for N in (4, 140):
+        X, W = head(N, 64, 500, 11)
+        f = lambda a: torch.from_numpy(a).to(torch.bfloat16).to(dev)  # noqa: E731
+        h, w = f(X), f(W)
+        ones = torch.ones(N, device=dev)
+        want = flce.constrained_logprobs(h, w, top_k=3)
+        got = flce.constrained_logprobs(h, w, top_k=3, history=torch.zeros((N, 0), dtype=torch.int32, device=dev),
+                                        repetition_penalty=2 * ones, presence_penalty=ones,
+                                        bias_ids=torch.zeros((N, 0), dtype=torch.int32, device=dev),
+                                        bias=torch.zeros((N, 0), device=dev))
+        none = flce.constrained_logprobs(h, w, top_k=3, history=torch.zeros((N, 9), dtype=torch.int32, device=dev),
+                                         history_lens=torch.zeros(N, dtype=torch.int32, device=dev), presence_penalty=ones)
+        for o in (got, none):
+            for n in ("lse", "entropy", "top_ids", "top_logp"):
+                assert torch.equal(o[n], want[n]), n

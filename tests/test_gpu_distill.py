@@ -94,7 +94,8 @@ SHAPES = [  # N, H, V, K, T, tail
     (64, 1024, 4096, 256, 1.0, True), (100, 264, 3001, 3, 2.0, True), (128, 128, 300, 255, 1.0, True),
     (129, 64, 512, 9, 1.0, True), (257, 192, 1030, 40, 1.0, False), (300, 64, 512, 8, 0.9, True),
     (700, 520, 4099, 129, 1.0, True), (200, 8, 1, 1, 1.0, True), (200, 8, 300, 256, 1.0, True),
-    (300, 1024, 9001, 33, 1.0, True), (140, 64, 64, 64, 1.0, True)]
+    (300, 1024, 9001, 33, 1.0, True), (140, 64, 64, 64, 1.0, True), (16500, 8, 300, 5, 1.0, True),
+    (150, 512, 2000, 20, 1.0, True), (40, 384, 2000, 20, 1.0, False), (129, 704, 999, 70, 1.0, True)]
 
 
 @pytest.mark.parametrize("N,H,V,K,T,tail", SHAPES)
@@ -393,3 +394,33 @@ def test_generate_under_rules_then_distill(env):
     err = np.abs(np64(x.grad) - g["grad_hidden"])
     assert np.all(err <= g["mag_hidden"] * (2.0 ** -8 + 2e-4) * 1.01 + 2.0 ** -8 * np.abs(g["grad_hidden"]) + 1e-30)
     assert student.grad is not None and torch.isfinite(student.grad).all()
+
+
+def test_repeated_calls_agree_bit_for_bit(env):
+    flce, torch, dev = env
+    for N in (20, 300):
+        X, W, ids, t = problem(N, 128, 3000, 40, 6)
+        a = to_gpu(torch, dev, X, W, ids, t)
+        one = torch.ones(N, device=dev)
+        first = None
+        for _ in range(4):
+            o = flce.topk_distill(*a)
+            d = flce.topk_distill_bwd(*a, o["lse"], o["rest_logp"], o["student_logp"], one)
+            got = [o["kl"], o["lse"], o["rest_logp"], o["student_logp"], d["grad_hidden"], d["grad_weight"]]
+            first = first or got
+            assert all(torch.equal(x, y) for x, y in zip(first, got))
+
+
+def test_two_streams_at_once(env):
+    flce, torch, dev = env
+    sets = []
+    for seed, N in ((1, 90), (2, 260)):
+        a = to_gpu(torch, dev, *problem(N, 64, 2000, 30, seed))
+        sets.append((a, flce.topk_distill(*a)))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [flce.topk_distill(*a, stream=st) for st, (a, _) in zip(streams, sets) for _ in range(3)]
+    torch.cuda.synchronize()
+    for i, o in enumerate(got):
+        for k in ("kl", "rest_logp", "student_logp"):
+            assert torch.equal(o[k], sets[i // 3][1][k]), k
