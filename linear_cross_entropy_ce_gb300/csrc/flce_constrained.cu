@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(32 * ROW_WARPS) constrained_rows_kernel(const 
   const long long row = valid ? a.idx[a.c0 + r] : 0;
   const int t = a.targets ? a.targets[row] : 0;
   if (w < ROWS8) {
-    const Stat s = merge_parts8(a.stats, a.nparts, a.C, a.c2, r0, Cl, lane, w, part);
+    const Stat s = merge_parts8<true>(a.stats, a.nparts, a.C, a.c2, r0, Cl, lane, w, part);
     if (lane == 0) share[0][w] = s;
   } else {
     const int sub = w / ROWS8 - 1;

@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(32 * ROWS8 * (1 + SHARES)) distill_rows_kernel
   float* mine = reinterpret_cast<float*>(smem4 + ROWS8 * a.slabs) + k * a.K;
   const int n = valid ? min(a.K, a.count[r]) : 0;
   if (w < ROWS8) {
-    const Stat s = merge_parts8(a.stats, a.nparts, a.C, a.c2, r0, Cl, lane, w, part);
+    const Stat s = merge_parts8<false>(a.stats, a.nparts, a.C, a.c2, r0, Cl, lane, w, part);
     if (lane == 0) share[0][w] = s;
   } else {
     uint32_t* out = reinterpret_cast<uint32_t*>(smem4 + k * a.slabs);   // [slabs][4] bits of the columns left out

@@ -360,8 +360,9 @@ __device__ __forceinline__ void store_f32x32(float* dst, const float (&v)[32]) {
 // and six an element slowed those (tiles of 8 K blocks: 3.6 us each, without the
 // arithmetic 2.7).
 // OFTEN: logits of -inf are common (forbidden and listed tokens), and two more
-// instructions an element are cheaper than going through them again.
-template <bool OFTEN = false>
+// instructions an element are cheaper than going through them again.  WEIGHTED
+// false: without sum d 2^d.
+template <bool OFTEN = false, bool WEIGHTED = true>
 __device__ __forceinline__ Stat stats32(const float (&v)[32], float c2) {
   float mx = v[0];
 #pragma unroll
@@ -377,11 +378,11 @@ __device__ __forceinline__ Stat stats32(const float (&v)[32], float c2) {
     const float2 x = ptx::unpack2(d);
     const uint64_t e = ptx::pack2(ptx::ex2(x.x), ptx::ex2(x.y));
     s2 = ptx::add2(s2, e);
-    d2 = ptx::fma2(OFTEN ? ptx::pack2(fmaxf(x.x, -1e30f), fmaxf(x.y, -1e30f)) : d, e, d2);
+    if (WEIGHTED) d2 = ptx::fma2(OFTEN ? ptx::pack2(fmaxf(x.x, -1e30f), fmaxf(x.y, -1e30f)) : d, e, d2);
   }
   float sum = ptx::unpack2(s2).x + ptx::unpack2(s2).y;
   float dsum = ptx::unpack2(d2).x + ptx::unpack2(d2).y;
-  if (dsum != dsum && sum == sum) {             // a logit of -inf: 0 times -inf; it adds nothing
+  if (WEIGHTED && dsum != dsum && sum == sum) {             // a logit of -inf: 0 times -inf; it adds nothing
     dsum = 0.f;
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
@@ -397,12 +398,13 @@ __device__ __forceinline__ Stat stats32(const float (&v)[32], float c2) {
 }
 
 // Part-major: a warp's 32 rows store 128 contiguous bytes per value.
+template <bool WEIGHTED = true>
 __device__ __forceinline__ void store_stats(const GemmArgs& a, int part, int grow, const Stat& st) {
   const size_t np = static_cast<size_t>(a.nparts) * a.C;
   float* p = a.stats + static_cast<size_t>(part) * a.C + grow;
   p[0] = st.m;
   p[np] = st.s;
-  p[2 * np] = st.d;
+  if (WEIGHTED) p[2 * np] = st.d;
 }
 
 // Top alternatives: the logits of a part are kept unless K other parts of the
@@ -444,6 +446,7 @@ __device__ __forceinline__ void blank_tail(float (&v)[32], int j0, int ncol, flo
 struct PartLists {
   uint32_t listed[GROUP_COLS / 32], allowed[GROUP_COLS / 32];
   float* slot;
+  int slab;   // of a part left out whole, or -1
 };
 
 // Columns [c0, c0 + ncol) of chunk row grow; they lie in part c0 / 128, whose
@@ -483,12 +486,14 @@ __device__ __forceinline__ PartLists part_lists(const GemmArgs& a, bool rv, int 
   return p;
 }
 
-// Where columns from c0 on of chunk row grow go if their part is left out.
-__device__ __forceinline__ float* part_slab(const GemmArgs& a, bool rv, int grow, int c0) {
+// The slab of the part that holds column c0 of chunk row grow, and the place of
+// columns from c0 on there.
+__device__ __forceinline__ int part_slab(const GemmArgs& a, bool rv, int grow, int c0) {
   const int part = c0 / PART_COLS;
-  if (!rv || part >= a.nparts) return nullptr;
-  const int q = a.slab[static_cast<long long>(part) * a.C + grow];
-  return q < 0 ? nullptr : a.lists.z + (static_cast<long long>(grow) * a.slabs_per_row + q) * PART_COLS + c0 % PART_COLS;
+  return rv && part < a.nparts ? a.slab[static_cast<long long>(part) * a.C + grow] : -1;
+}
+__device__ __forceinline__ float* slab_place(const GemmArgs& a, int slab, int grow, int c0) {
+  return a.lists.z + (static_cast<long long>(grow) * a.slabs_per_row + slab) * PART_COLS + c0 % PART_COLS;
 }
 
 // The next 32 columns' words (registers have no index), around.
@@ -534,6 +539,21 @@ __device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, con
   const int tl = (rv ? a.tc[grow] : -1) - c0;
   const int ncol = min(GROUP_COLS, a.V - c0);
   if (ncol <= 0) return;                          // uniform over the warpgroup
+  if constexpr (LISTED == LISTED_SLABS) {
+    Stat st = {-INFINITY, 0.f, 0.f};
+#pragma unroll 1
+    for (int j = 0; j < GROUP_COLS / 32; ++j) {
+      if (j * 32 >= ncol) break;                  // uniform
+      float v[32];
+      ptx::tmem_ld32(tbase + j * 32, v);
+      if (pl.slab >= 0) store_f32x32(slab_place(a, pl.slab, grow, c0) + j * 32, v);   // behind the vocabulary: never read
+      blank_tail(v, j * 32, ncol, -INFINITY);
+      st = merge(st, stats32<false, false>(v, a.c2), a.c2);
+    }
+    // the row kernel goes through a part that is left out
+    if (rv) store_stats<false>(a, c0 / PART_COLS, grow, pl.slab >= 0 ? Stat{-INFINITY, 0.f, 0.f} : st);
+    return;
+  }
   float ztv = 0.f;
   float* zrow = a.zf + static_cast<size_t>(grow) * a.ldz + c0;
   const bool all = a.K > 0 && a.bound == nullptr && rv;   // every logit is kept
@@ -554,12 +574,10 @@ __device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, con
       often = treat_listed<true>(v, pl.listed[0], pl.allowed[0], pl.slot);
       turn_lists(pl);
     }
-    if (LISTED == LISTED_SLABS && pl.slot) store_f32x32(pl.slot + j * 32, v);   // behind the vocabulary: never read
     if (all) store_f32x32(zrow + j * 32, v);
     blank_tail(v, j * 32, ncol, -INFINITY);
     st = merge(st, LISTED == LISTED_OUT && often ? stats32<true>(v, a.c2) : stats32(v, a.c2), a.c2);
   }
-  if (LISTED == LISTED_SLABS && pl.slot) st = Stat{-INFINITY, 0.f, 0.f};   // the row kernel goes through this part
   if (rv) {
     store_stats(a, c0 / PART_COLS, grow, st);
     if (tl >= 0 && tl < ncol) a.zt[grow] = ztv;
@@ -677,6 +695,25 @@ __device__ __forceinline__ bool epi_stats_seg(const GemmArgs& a, const Shape& s,
   const int grow = row0 + r;
   const bool rv = grow < s.Cl;
   const int c0 = t.n0 + grp * QUARTER, part = (t.n0 + grp / 2 * PART_COLS) / PART_COLS;
+  if constexpr (LISTED == LISTED_SLABS) {
+    const int ncol = min(QUARTER, a.V - c0);       // may be <= 0 past the vocabulary
+    Stat mine = {-INFINITY, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (j * 32 >= ncol) break;                  // uniform
+      if (pl.slab >= 0) store_f32x32(slab_place(a, pl.slab, grow, c0) + j * 32, z[j]);
+      blank_tail(z[j], j * 32, ncol, -INFINITY);
+      mine = merge(mine, stats32<false, false>(z[j], a.c2), a.c2);
+    }
+    ex[grp][0][r] = mine.m;
+    ex[grp][1][r] = mine.s;
+    if (!ptx::named_bar_and(bar, 2 * GROUP_THREADS, ok)) return false;
+    if ((grp & 1) == 0 && rv && ncol > 0) {
+      const Stat st = merge(mine, Stat{ex[grp ^ 1][0][r], ex[grp ^ 1][1][r], 0.f}, a.c2);
+      store_stats<false>(a, part, grow, pl.slab >= 0 ? Stat{-INFINITY, 0.f, 0.f} : st);
+    }
+    return true;
+  }
   const int tl = (rv ? a.tc[grow] : -1) - c0;
   const int ncol = min(QUARTER, a.V - c0);         // may be <= 0 past the vocabulary
   Stat mine = {-INFINITY, 0.f, 0.f};
@@ -689,7 +726,6 @@ __device__ __forceinline__ bool epi_stats_seg(const GemmArgs& a, const Shape& s,
     pick_target(z[j], tl, j * 32, ztv);
     bool often = false;
     if constexpr (LISTED == LISTED_OUT) often = treat_listed<true>(z[j], pl.listed[j], pl.allowed[j], pl.slot);
-    if (LISTED == LISTED_SLABS && pl.slot) store_f32x32(pl.slot + j * 32, z[j]);
     if (all) store_f32x32(zrow + j * 32, z[j]);
     blank_tail(z[j], j * 32, ncol, -INFINITY);
     mine = merge(mine, LISTED == LISTED_OUT && often ? stats32<true>(z[j], a.c2) : stats32(z[j], a.c2), a.c2);
@@ -701,8 +737,7 @@ __device__ __forceinline__ bool epi_stats_seg(const GemmArgs& a, const Shape& s,
   const int og = grp ^ 1;
   const Stat other = {ex[og][0][r], ex[og][1][r], ex[og][2][r]};
   const bool first = (grp & 1) == 0;
-  Stat st = first ? merge(mine, other, a.c2) : merge(other, mine, a.c2);
-  if (LISTED == LISTED_SLABS && pl.slot) st = Stat{-INFINITY, 0.f, 0.f};   // the row kernel goes through this part
+  const Stat st = first ? merge(mine, other, a.c2) : merge(other, mine, a.c2);
   if (rv && ncol > 0) {
     if (first) store_stats(a, part, grow, st);
     if (tl >= 0 && tl < ncol) a.zt[grow] = ztv;
@@ -1185,7 +1220,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       if constexpr (LISTED != 0) {
         const int grow = t.m0 + half + r, c0 = t.n0 + grp * QUARTER;
         if constexpr (LISTED == LISTED_OUT) pl = part_lists(a, grow < s.Cl, grow, c0, min(QUARTER, a.V - c0));
-        else pl.slot = part_slab(a, grow < s.Cl, grow, c0);
+        else pl.slab = part_slab(a, grow < s.Cl, grow, c0);
       }
       float z[2][32];
 #pragma unroll
@@ -1274,7 +1309,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       if constexpr (LISTED != 0) {
         const int grow = t.m0 + half + r, c0 = t.n0 + col0;
         if constexpr (LISTED == LISTED_OUT) pl = part_lists(a, grow < s.Cl, grow, c0, min(GROUP_COLS, a.V - c0));
-        else pl.slot = part_slab(a, grow < s.Cl, grow, c0);
+        else pl.slab = part_slab(a, grow < s.Cl, grow, c0);
       }
       ok = wait_phase(&ctl->tfull[set], acc_phase, ctl, to, true, hdr, W_TMEM_FULL, u | (set << 24));
       if (!ptx::named_bar_and(sbar, SET_THREADS, ok)) break;

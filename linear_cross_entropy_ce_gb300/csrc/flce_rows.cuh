@@ -48,7 +48,9 @@ __device__ __forceinline__ void merge_parts(const float* stats, int nparts, int 
 // warp reads four parts at a time, 32 bytes of each.  The order is that of
 // merge_parts.
 constexpr int ROWS8 = 8;
+// WEIGHTED false: the statistics have no third value.
 constexpr uint32_t ROWS8_BAR = 1, ROWS8_BAR_OTHERS = 2;   // named barriers of the 8 warps, and of the others
+template <bool WEIGHTED>
 __device__ __forceinline__ Stat merge_parts8(const float* stats, int nparts, int C, float c2, int r0, int Cl, int lane,
                                              int w, Stat (*part)[ROWS8]) {
   const int r = r0 + lane % ROWS8;
@@ -61,7 +63,7 @@ __device__ __forceinline__ Stat merge_parts8(const float* stats, int nparts, int
       for (int k = 0; k < 2 * ROWS_BATCH; ++k) {
         const int p = p0 + k * 32;
         const float* f = stats + static_cast<size_t>(p) * C + r;
-        q[k] = p < nparts ? Stat{f[0], f[np], f[2 * np]} : Stat{-INFINITY, 0.f, 0.f};
+        q[k] = p < nparts ? Stat{f[0], f[np], WEIGHTED ? f[2 * np] : 0.f} : Stat{-INFINITY, 0.f, 0.f};
       }
       acc = merge(acc, merge(merge(q[0], q[1], c2), merge(q[2], q[3], c2), c2), c2);
       if (p0 + ROWS_BATCH * 32 < nparts) acc = merge(acc, merge(merge(q[4], q[5], c2), merge(q[6], q[7], c2), c2), c2);
