@@ -28,6 +28,10 @@
 //                part the max m, sum 2^d and sum d 2^d of d = (z - m) c2 (the
 //                entropy needs the third), the target logit and, for top
 //                alternatives, the fp32 logits.
+//                Rows with lists (GemmArgs::listed): listed tokens are taken
+//                out one by one and forbidden ones left out (LISTED_OUT), or
+//                the parts that hold listed tokens are left out whole, their
+//                logits stored (LISTED_SLABS).
 //   MODE_DZ      z = Xc W^T once more, turned in registers into the gradient
 //                of the logits (bf16) that MODE_BWD consumes.
 //                Both take long sums over H in segments, see below.

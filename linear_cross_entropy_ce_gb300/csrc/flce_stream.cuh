@@ -10,8 +10,8 @@
 // in tiles of up to 256 rows.  Warp 0 streams W (and, from L2, X) through a
 // TMA ring of 64-column K blocks, warp 1 issues the MMAs into one of two TMEM
 // accumulators, and eight epilogue warps turn a finished 256 x 32 slice of
-// logits around in shared memory, where each warp takes whole tokens: the
-// running softmax statistics and the target's logit.  Every CTA leaves its
+// logits around in shared memory, where each warp takes whole tokens, two at a
+// time: the running softmax statistics and the target's logit.  Every CTA leaves its
 // statistics per token; the second kernel, a block per token, merges them.
 // For top alternatives a tile's max and, where it matters, its logits are
 // stored, and the second kernel reads back the K best tiles only.  It does not
@@ -38,9 +38,10 @@
 // (LISTS_RULED) they are changed in place, and forbidden tokens count as -inf; a
 // teacher's tokens (LISTS_TAKEN) are written out and leave the statistics.  Where
 // the tile's entries begin and the words of its mask are fetched while the tile
-// is being computed, a token's entries while the one before it is worked on.
+// is being computed, a token's entries while the two before it are worked on.
 // (128 tokens with 4001 ids of history, masks and 20 alternatives at 4096 x
-// 128256: 210 us, fetched when needed 240.)
+// 128256, a call: fetched when needed 253 us, ahead 224, and with two tokens at a
+// time 218; without lists 197 and 194.)
 #pragma once
 
 #include "flce_internal.h"
@@ -323,10 +324,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         __syncwarp();
       }
-      constexpr int DEPTH = 2;   // tokens whose entries are on their way
-      Entry entry[DEPTH];
+      Entry entry[2];   // of the next two tokens
 #pragma unroll
-      for (int k = 0; k < DEPTH; ++k) {
+      for (int k = 0; k < 2; ++k) {
         entry[k] = Entry{-1, 0, 0.f};
         const int tk = w + k * EPI_WARPS;
         if (LISTS != LISTS_NONE && tk < a.N)
@@ -391,71 +391,103 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (lane == 0) ptx::mbar_arrive(&ctl->tempty[acc]);
         }
         ptx::named_bar_sync(EPI_BAR, EPI_THREADS);
+        // two tokens at a time, whose chains of latencies overlap
+        static_assert(C::SLICE % (2 * EPI_WARPS) == 0, "pairs of a warp's tokens");
 #pragma unroll 1
-        for (int k = w; k < C::SLICE; k += EPI_WARPS) {
+        for (int k = w; k < C::SLICE; k += 2 * EPI_WARPS) {
           const int tk = n0 + k;
           if (tk >= a.N) break;
-          float* z = turn + k * TILE_ROWS;
+          const bool two = tk + EPI_WARPS < a.N;   // else the second is the first again, and writes nothing
+          const int other = two ? EPI_WARPS : 0;
+          float* z[2] = {turn + k * TILE_ROWS, turn + (k + other) * TILE_ROWS};
           if constexpr (LISTS != LISTS_NONE) {
-            const Entry now = entry[0];
+            const Entry now[2] = {entry[0], entry[1]};
 #pragma unroll
-            for (int e = 0; e + 1 < DEPTH; ++e) entry[e] = entry[e + 1];
-            const int next = tk + DEPTH * EPI_WARPS;
-            if (next < a.N)
-              entry[DEPTH - 1] = fetch_entry<LISTS>(l, next, ahead[next * AHEAD] + lane, ahead[next * AHEAD + 1]);
-            const int j = tk / EPI_WARPS;
-            const RowRules mine = {__shfl_sync(0xffffffffu, rules.repetition, j), __shfl_sync(0xffffffffu, rules.frequency, j),
-                                   __shfl_sync(0xffffffffu, rules.presence, j)};
-            treat_listed<LISTS>(l, tk, ahead[tk * AHEAD], ahead[tk * AHEAD + 1], now, mine, r0, rows, z, lane);
-          }
-          float x[8], mx = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            x[j] = j * 32 + lane < rows ? z[j * 32 + lane] : -INFINITY;
-            if (LISTS == LISTS_RULED && l.lists.mask) {
-              const int bit = r0 % 32 + lane;   // r0: a multiple of 16
-              if (!((ahead[tk * AHEAD + 2 + j + bit / 32] >> (bit % 32)) & 1)) x[j] = -INFINITY;
+            for (int p = 0; p < 2; ++p) {
+              const int next = tk + (2 + p) * EPI_WARPS;
+              if (next < a.N)
+                entry[p] = fetch_entry<LISTS>(l, next, ahead[next * AHEAD] + lane, ahead[next * AHEAD + 1]);
             }
-            mx = fmaxf(mx, x[j]);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              if (p == 1 && !two) break;
+              const int t = tk + p * EPI_WARPS, j = t / EPI_WARPS;
+              const RowRules mine = {__shfl_sync(0xffffffffu, rules.repetition, j),
+                                     __shfl_sync(0xffffffffu, rules.frequency, j),
+                                     __shfl_sync(0xffffffffu, rules.presence, j)};
+              treat_listed<LISTS>(l, t, ahead[t * AHEAD], ahead[t * AHEAD + 1], now[p], mine, r0, rows, z[p], lane);
+            }
+          }
+          float x[2][8], mx[2];
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            mx[p] = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              x[p][j] = j * 32 + lane < rows ? z[p][j * 32 + lane] : -INFINITY;
+              if (LISTS == LISTS_RULED && l.lists.mask) {
+                const int bit = r0 % 32 + lane;   // r0: a multiple of 16
+                if (!((ahead[(tk + p * other) * AHEAD + 2 + j + bit / 32] >> (bit % 32)) & 1)) x[p][j] = -INFINITY;
+              }
+              mx[p] = fmaxf(mx[p], x[p][j]);
+            }
           }
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          const float mb = mx == -INFINITY ? 0.f : -mx * a.c2;
-          float s = 0.f, d = 0.f;
+          for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float y = fmaf(x[j], a.c2, mb);
-            const float e = ptx::ex2(y);
-            s += e;
-            d = fmaf(fmaxf(y, -1e30f), e, d);
+            for (int p = 0; p < 2; ++p) mx[p] = fmaxf(mx[p], __shfl_xor_sync(0xffffffffu, mx[p], o));
+          float mb[2], s[2], d[2];
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            mb[p] = mx[p] == -INFINITY ? 0.f : -mx[p] * a.c2;
+            s[p] = d[p] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float y = fmaf(x[p][j], a.c2, mb[p]);
+              const float e = ptx::ex2(y);
+              s[p] += e;
+              d[p] = fmaf(fmaxf(y, -1e30f), e, d[p]);
+            }
           }
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1) {
-            s += __shfl_xor_sync(0xffffffffu, s, o);
-            d += __shfl_xor_sync(0xffffffffu, d, o);
-          }
-          if (lane == 0) {
+          for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              s[p] += __shfl_xor_sync(0xffffffffu, s[p], o);
+              d[p] += __shfl_xor_sync(0xffffffffu, d[p], o);
+            }
+          if (lane < (two ? 2 : 1)) {   // a lane per token
+            const bool q = lane == 1;
+            const int t = tk + lane * EPI_WARPS;
+            const float m = q ? mx[1] : mx[0], b = q ? mb[1] : mb[0], sum = q ? s[1] : s[0], wsum = q ? d[1] : d[0];
             // mb is rounded: every y is too large by rho (exact in the fused multiply-add)
-            const float rho = mx == -INFINITY ? 0.f : fmaf(mx, a.c2, mb);
+            const float rho = m == -INFINITY ? 0.f : fmaf(m, a.c2, b);
             const float back = ptx::ex2(-rho);
-            const float4 old = stat[tk];
-            const Stat t = merge(Stat{old.x, old.y, old.z}, Stat{mx, back * s, back * fmaf(-rho, s, d)}, a.c2);
-            stat[tk] = make_float4(t.m, t.s, t.d, 0.f);
+            const float4 old = stat[t];
+            const Stat r = merge(Stat{old.x, old.y, old.z}, Stat{m, back * sum, back * fmaf(-rho, sum, wsum)}, a.c2);
+            stat[t] = make_float4(r.m, r.s, r.d, 0.f);
             if (LISTS == LISTS_NONE || a.targets) {
-              const unsigned at = static_cast<unsigned>(a.targets[tk]) - static_cast<unsigned>(r0);
-              if (at < static_cast<unsigned>(rows)) a.zt[tk] = z[at];
+              const unsigned at = static_cast<unsigned>(a.targets[t]) - static_cast<unsigned>(r0);
+              if (at < static_cast<unsigned>(rows)) a.zt[t] = (q ? z[1] : z[0])[at];
+            }
+            if (a.K > 0) {
+              a.tile_max[static_cast<size_t>(t) * a.ctas * a.max_tiles + blockIdx.x * a.max_tiles + i] = m;
+              if (a.group_max && order_key(m) >= bound[t])
+                atomicMax(a.group_max + t * TopK::MAX + (blockIdx.x + i) % a.K, order_key(m));
             }
           }
           if (a.K > 0) {
-            if (!a.group_max || order_key(mx) >= bound[tk]) {
-              float* zf = a.zf + static_cast<size_t>(tk) * a.ldz + r0 + lane;
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (j * 32 + lane < rows) zf[j * 32] = x[j];
-              if (a.group_max && lane == 0) atomicMax(a.group_max + tk * TopK::MAX + (blockIdx.x + i) % a.K, order_key(mx));
+            for (int p = 0; p < 2; ++p) {
+              if (p == 1 && !two) break;
+              const int t = tk + p * EPI_WARPS;
+              if (!a.group_max || order_key(mx[p]) >= bound[t]) {
+                float* zf = a.zf + static_cast<size_t>(t) * a.ldz + r0 + lane;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  if (j * 32 + lane < rows) zf[j * 32] = x[p][j];
+              }
             }
-            if (lane == 0)
-              a.tile_max[static_cast<size_t>(tk) * a.ctas * a.max_tiles + blockIdx.x * a.max_tiles + i] = mx;
           }
         }
         ptx::named_bar_sync(EPI_BAR, EPI_THREADS);   // the slice buffer is free again
