@@ -669,6 +669,19 @@ cudaError_t by_groups(int K, F&& f) {
   return f(Groups<8>());
 }
 
+// K blocks of a segment of a logit's sum (see segment_blocks()).  A divergence of
+// distributions that nearly agree keeps the logits' absolute errors, so its
+// segments are shorter than those of the log probabilities: kl is off by no more
+// than with an fp32 product on the CUDA cores (2000 tokens at 1024, 2048, 4096 x
+// 60000: 1.0e-6, 1.5e-6, 2.1e-6 of its norm and 1.1e-6, 1.7e-6, 2.7e-6; with the
+// log probabilities' segments 1.5e-6, 2.1e-6, 3.0e-6 and 1 to 2% faster).  Up to
+// 64 tokens four blocks cost nothing, since the weight's bytes bound the kernel.
+int distill_segment(long long N, long long H) {
+  const int blocks = static_cast<int>(cdiv(H, BK));
+  const int most = N <= 64 ? 4 : std::max(4, static_cast<int>(1.75 * std::sqrt(static_cast<double>(blocks))));
+  return static_cast<int>(cdiv(blocks, cdiv(blocks, N <= STREAM_MAX_TOKENS ? std::min(most, 8) : most)));   // of equal length
+}
+
 struct DistillStream {
   int ctas, max_tiles;
   size_t o_stat, o_start, o_id, o_z, o_t, o_slot, o_fail, total;
@@ -793,7 +806,7 @@ flce_status flce_topk_distill(const void* hidden, const void* weight, const int3
     la.ctas = p.ctas; la.max_tiles = p.max_tiles;
     la.t = at<float>(workspace, p.o_t);
     la.slot = at<short>(workspace, p.o_slot);
-    if (!stream_setup(&a, &m, hidden, weight, segment_blocks(H, 1))) return FLCE_ECUDA;
+    if (!stream_setup(&a, &m, hidden, weight, distill_segment(N, H))) return FLCE_ECUDA;
     count_launches(2);   // lists, rows
     if (!ok(by_groups(K, [&](auto g) {
           distill_stream_lists_kernel<decltype(g)::value><<<static_cast<unsigned>(N), STREAM_LIST_THREADS, 0, st>>>(la);
@@ -821,7 +834,7 @@ flce_status flce_topk_distill(const void* hidden, const void* weight, const int3
   if (!ok(launch_result(cudaGetLastError()))) return FLCE_ECUDA;
   c.hidden = hidden; c.weight = weight; c.targets = targets; c.ii = -1; c.temperature = temperature;
   c.logp = kl; c.entropy = rest_logp; c.lse = lse;
-  c.seg_kb = segment_blocks(H, 1);
+  c.seg_kb = distill_segment(N, H);
   c.ws = workspace; c.st = st;
   la.t = at<float>(workspace, p.o_rows);
   la.count = reinterpret_cast<int*>(la.t + p.C * K);

@@ -213,12 +213,9 @@ cudaError_t launch_gather(const uint16_t* hidden, const int* targets, const int*
 // segments, each from zero, and add these up rounded to nearest.  With
 // 2 sqrt(blocks) blocks a segment the error grows with H as that of an fp32
 // product on the CUDA cores does; up to 11 blocks it is below 1e-6 anyway.
-// A divergence of distributions that nearly agree keeps the logits' absolute
-// errors, so it takes them in two segments from H = 320 on (4096 tokens at
-// 512 x 16000: kl off by 6e-7 of its norm, 1.3e-6 in one piece).
-inline int segment_blocks(long long H, int whole = 11) {
+inline int segment_blocks(long long H) {
   const int blocks = static_cast<int>(cdiv(H, BK));
-  const int most = std::max(whole, static_cast<int>(2.0 * std::sqrt(static_cast<double>(blocks))));
+  const int most = std::max(11, static_cast<int>(2.0 * std::sqrt(static_cast<double>(blocks))));
   return static_cast<int>(cdiv(blocks, cdiv(blocks, most)));   // of equal length
 }
 // Few tokens: the weight streamed once past all of them (flce_stream.cu).
