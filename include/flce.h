@@ -326,7 +326,8 @@ flce_status flce_logprobs_bwd(const void* hidden, const void* weight, const int3
  *   mask          [N, ceil(V / 32)] int32 words, rows mask_stride words apart,
  *                 bit v % 32 of word v / 32 is token v's; or NULL.  Logits of
  *                 forbidden tokens may be NaN or infinite.
- * Lengths are clipped to what the arrays hold.
+ * Lengths are clipped to what the arrays hold; history_len <= 2^30, n_bias <=
+ * 2^20.
  * Outputs as flce_logprobs; but targets may be NULL (every row counts, logp may
  * be NULL then), a forbidden target's logp is -inf, forbidden tokens are no
  * alternatives (ids -1, log probability -inf behind the last allowed one), and

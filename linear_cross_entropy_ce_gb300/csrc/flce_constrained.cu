@@ -448,7 +448,8 @@ ListedSizes constrained_sizes(long long N, long long H, long long V, int K, long
 
 bool sizes_bad(int64_t N, int64_t H, int64_t V) { return !sizes_ok(N, H, V) || V > PROBS_MAX_V; }
 
-constexpr long long MAX_LIST = (1ll << 31) - 1;
+// An index and a block's stride stay in 32 bits.
+constexpr long long MAX_HISTORY = 1ll << 30, MAX_BIASES = 1ll << 20;
 
 }  // namespace
 
@@ -464,8 +465,8 @@ using namespace flce;
 extern "C" {
 
 size_t flce_constrained_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t top_k, int64_t history, int64_t biases) {
-  if (sizes_bad(N, H, V) || top_k < 0 || top_k > TopK::MAX || top_k > V || history < 0 || history > MAX_LIST ||
-      biases < 0 || biases > MAX_LIST)
+  if (sizes_bad(N, H, V) || top_k < 0 || top_k > TopK::MAX || top_k > V || history < 0 || history > MAX_HISTORY ||
+      biases < 0 || biases > MAX_BIASES)
     return 0;
   if (N <= STREAM_MAX_TOKENS) return constrained_stream_plan(N, V, top_k, history, biases, device_sms()).total;
   return listed_default_bytes(constrained_sizes(N, H, V, top_k, history, biases));
@@ -483,7 +484,7 @@ flce_status flce_constrained_logprobs(const void* hidden, const void* weight, co
   if (c.history_len < 0 || (c.history_len > 0 && !c.history) || c.history_stride < 0 || c.n_bias < 0 ||
       (c.n_bias > 0 && (!c.bias_ids || !c.bias)) || c.bias_ids_stride < 0 || c.bias_stride < 0 || c.mask_stride < 0)
     return FLCE_EINVAL;
-  if (sizes_bad(N, H, V) || top_k > TopK::MAX || c.history_len > MAX_LIST || c.n_bias > MAX_LIST) return FLCE_EUNSUPPORTED;
+  if (sizes_bad(N, H, V) || top_k > TopK::MAX || c.history_len > MAX_HISTORY || c.n_bias > MAX_BIASES) return FLCE_EUNSUPPORTED;
   if (!aligned16(hidden) || !aligned16(weight) || !aligned16(workspace) || !aligned4(targets) || !aligned4(logp) ||
       !aligned4(entropy) || !aligned4(lse) || !aligned4(top_ids) || !aligned4(top_logp) || !aligned4(c.history) ||
       !aligned4(c.history_lens) || !aligned4(c.prompt_lens) || !aligned4(c.repetition_penalty) ||

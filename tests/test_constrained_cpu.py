@@ -44,7 +44,8 @@ def test_refusals(flce, kw, want):
 @pytest.mark.parametrize("rules,want", [
     (dict(history=None), 1), (dict(history_len=-1), 1), (dict(history_stride=-1), 1), (dict(n_bias=-1), 1),
     (dict(n_bias=3), 1), (dict(n_bias=3, bias_ids=1 << 20), 1), (dict(mask_stride=-2), 1), (dict(bias_stride=-2), 1),
-    (dict(bias_ids_stride=-2), 1), (dict(history_len=1 << 31), 2), (dict(history=(1 << 20) + 2), 2),
+    (dict(bias_ids_stride=-2), 1), (dict(history_len=1 << 31), 2), (dict(history_len=(1 << 30) + 1), 2),
+    (dict(n_bias=(1 << 20) + 1, bias_ids=1 << 20, bias=1 << 20), 2), (dict(history=(1 << 20) + 2), 2),
     (dict(mask=(1 << 20) + 1), 2), (dict(repetition_penalty=(1 << 20) + 2), 2), (dict(prompt_lens=(1 << 20) + 3), 2),
     (dict(bias=(1 << 20) + 3, bias_ids=1 << 20, n_bias=2), 2)])
 def test_refused_rules(flce, rules, want):
@@ -65,7 +66,7 @@ def test_workspace_sizes(flce):
     assert 0 < lib.flce_constrained_workspace_bytes(N, H, V, 0, 4000, 16) <= 512 << 20
     assert 0 < lib.flce_constrained_workspace_bytes(N, H, V, 8, 4000, 16) <= 2 << 30
     for bad in [(0, H, V, 0, 0, 0), (N, 63, V, 0, 0, 0), (N, H, V, 33, 0, 0), (N, H, 4, 5, 0, 0), (N, H, V, -1, 0, 0),
-                (N, H, V, 0, -1, 0), (N, H, V, 0, 0, -1), (N, H, V, 0, 1 << 31, 0)]:
+                (N, H, V, 0, -1, 0), (N, H, V, 0, 0, -1), (N, H, V, 0, 1 << 31, 0), (N, H, V, 0, (1 << 30) + 1, 0), (N, H, V, 0, 0, (1 << 20) + 1)]:
         assert lib.flce_constrained_workspace_bytes(*bad) == 0
 
 

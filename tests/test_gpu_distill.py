@@ -424,3 +424,51 @@ def test_two_streams_at_once(env):
     for i, o in enumerate(got):
         for k in ("kl", "rest_logp", "student_logp"):
             assert torch.equal(o[k], sets[i // 3][1][k]), k
+
+
+def test_capture_beside_a_living_graph_is_refused(env):
+    """Autograd would order the default stream behind the capture, which ends the process: refused before that."""
+    flce, torch, dev = env
+    h, w, i, tt = to_gpu(torch, dev, *problem(150, 64, 500, 6, 4))
+    w.requires_grad_(True)
+    step = lambda: flce.linear_topk_distill(h, w, i, tt).sum()  # noqa: E731
+    want = torch.autograd.grad(step(), w)[0]
+    alive = step()
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="alive"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            torch.autograd.grad(step(), w)
+    del alive
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = torch.autograd.grad(step(), w)[0]
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("N", [60, 300])
+def test_two_captures_replayed_in_turn(env, N):
+    """Two captured calls from one pool of memory, replayed one after the other on new lists."""
+    flce, torch, dev = env
+    sets = [to_gpu(torch, dev, *problem(N, 64, 2000, 30, seed)) for seed in (1, 2, 3)]
+    want = [flce.topk_distill(*a) for a in sets]
+    live = [[x.clone() for x in sets[0]], [x.clone() for x in sets[1]]]
+    torch.cuda.synchronize()
+    graphs, outs, pool = [], [], None
+    for a in live:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, pool=pool):
+            outs.append({k: v for k, v in flce.topk_distill(*a).items() if k != "workspace"})
+        pool = g.pool()
+        graphs.append(g)
+    for which in ((0, 1), (2, 0), (1, 2)):
+        for a, s in zip(live, which):
+            for x, y in zip(a, sets[s]):
+                x.copy_(y)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for o, s in zip(outs, which):
+            for k in ("kl", "lse", "rest_logp", "student_logp"):
+                assert torch.equal(o[k], want[s][k]), (k, which)
