@@ -123,6 +123,9 @@ __global__ void __launch_bounds__(STREAM ? STREAM_THREADS : CHUNK_THREADS, STREA
 #pragma unroll
     for (int k = 0; k < HELD; ++k) {
       const int i = k * THREADS + tid;
+      word[k] = 0u;
+      before[k] = 0;
+      if (k * THREADS >= nw) continue;   // uniform
       word[k] = i < nw ? bits[i] & allowed[k] : 0u;
       const int c = __popc(word[k]);
       int incl = c;
@@ -139,7 +142,7 @@ __global__ void __launch_bounds__(STREAM ? STREAM_THREADS : CHUNK_THREADS, STREA
     static_assert(GROUPS / WARPS == HELD && HELD <= 32, "a lane per group");
     {
       const int g = w * HELD + lane;
-      const int c = lane < HELD ? group[g] : 0;
+      const int c = lane < HELD && g / WARPS * THREADS < nw ? group[g] : 0;
       int incl = c;
 #pragma unroll
       for (int o = 1; o < HELD; o <<= 1) {

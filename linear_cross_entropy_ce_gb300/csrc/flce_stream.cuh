@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 constexpr int MERGE_WARPS = 8;
 constexpr int MERGE_THREADS = 32 * MERGE_WARPS;
 constexpr int MERGE_BATCH = 4;   // tile maxima per thread in flight
-//
+
 // RULED: forbidden tokens have logits of -inf.  They are no alternatives, a
 // forbidden target has a log probability of -inf, and a row with nothing left a
 // log-sum-exp of -inf and no entropy; without targets all rows count.

@@ -12,6 +12,8 @@ Gradients: dz is rounded to bf16 once (2^-8 of it), its fp32 value is off by les
 than 2e-4 of the sum of its terms' magnitudes (the errors above), and a bf16
 output is rounded once more.
 """
+import gc
+
 import numpy as np
 import pytest
 
@@ -439,6 +441,7 @@ def test_capture_beside_a_living_graph_is_refused(env):
         with torch.cuda.graph(torch.cuda.CUDAGraph()):
             torch.autograd.grad(step(), w)
     del alive
+    gc.collect()   # the refused step's graph hangs on its exception's traceback, a cycle, and keeps the leaf's accumulator
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         got = torch.autograd.grad(step(), w)[0]
