@@ -35,6 +35,33 @@ namespace {
 constexpr int MAX_TEACHER = 256;   // teacher tokens of a row at most
 constexpr int NO_TOKEN = INT_MAX;
 
+struct DistillOut {
+  float *kl, *lse, *rest_logp, *student_logp;   // [N] x3, [N][K]
+};
+
+__device__ __forceinline__ void fill_row(const DistillOut& o, long long row, int K, float v, int lane) {
+  if (lane == 0) {
+    o.kl[row] = v;
+    o.lse[row] = v;
+    o.rest_logp[row] = v;
+  }
+  for (int j = lane; j < K; j += 32) o.student_logp[row * K + j] = v;
+}
+
+// A teacher row before anything else: the first token that it names, -1 where
+// it names none, or one outside [0, V).  That is the row's target for the
+// kernels that compact the rows.
+__device__ __forceinline__ int row_target(const int* ids, int K, int V, int lane) {
+  int t = -1;
+  for (int j0 = 0; j0 < K; j0 += 32) {
+    const int x = j0 + lane < K ? ids[j0 + lane] : -1;
+    const unsigned bad = __ballot_sync(0xffffffffu, x >= V), some = __ballot_sync(0xffffffffu, x >= 0);
+    if (bad) return __shfl_sync(0xffffffffu, x, __ffs(bad) - 1);
+    if (t < 0 && some) t = __shfl_sync(0xffffffffu, x, __ffs(some) - 1);
+  }
+  return t;
+}
+
 // ---------------------------------------------------------------------------
 // lists
 // ---------------------------------------------------------------------------
@@ -172,9 +199,9 @@ struct ListArgs {
   const float* teacher_logp;
   int K, V;
   const int* hdr;             // chunked form
-  const int* idx;
+  const int* idx;             // null: lists of all N tokens, by token
   long long c0;
-  int C, nparts;
+  int C, nparts, N;
   short* slab;                // [nparts][C] which of the row's slabs takes the part's logits, -1: none
   int* count;                 // [C] tokens of the row
   int ctas, max_tiles;        // streaming form
@@ -198,20 +225,33 @@ __device__ __forceinline__ void store_row(const ListArgs& a, long long row, cons
 }
 
 // Chunked: 8 rows a block, each sorted by a warp; then a lane walks a run of
-// one row's parts, four runs a warp.
+// one row's parts, four runs a warp.  By token (calls of one chunk), the kernel
+// also does what distill_targets_kernel does, a launch less.
 constexpr int LIST_WARPS = ROWS8;
 template <int SORT_GROUPS>
-__global__ void __launch_bounds__(32 * LIST_WARPS) distill_lists_kernel(const ListArgs a) {
+__global__ void __launch_bounds__(32 * LIST_WARPS)
+    distill_lists_kernel(const ListArgs a, int* targets, const DistillOut out) {
   extern __shared__ int smem[];   // per row: scratch of its sort, the slabs of its tokens
   __shared__ int count[ROWS8];
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   const int words = list_words(a.K), slabs_at = sort_words(a.K);
   ptx::grid_dependency_wait();
-  const int Cl = chunk_rows(a.hdr, a.c0, a.C);
+  const int Cl = a.idx ? chunk_rows(a.hdr, a.c0, a.C) : a.N;
   const int r0 = blockIdx.x * ROWS8;
   if (r0 >= Cl) return;
-  if (r0 + w < Cl) {
-    const long long row = r0 + w, from = static_cast<long long>(a.idx[a.c0 + row]) * a.K;
+  bool sort = r0 + w < Cl;
+  if (!a.idx && sort) {
+    const long long row = r0 + w;
+    const int t = row_target(a.teacher_ids + row * a.K, a.K, a.V, lane);
+    if (lane == 0) {
+      targets[row] = t;
+      count[w] = a.count[row] = 0;
+    }
+    sort = t >= 0 && t < a.V;
+    if (!sort) fill_row(out, row, a.K, t < 0 ? 0.f : __int_as_float(0x7fc00000), lane);
+  }
+  if (sort) {
+    const long long row = r0 + w, from = (a.idx ? a.idx[a.c0 + row] : row) * a.K;
     const SortRow s = sort_scratch(smem + w * words, a.K);
     int slot[SORT_GROUPS];
     const int n = sort_row(a.teacher_ids + from, a.teacher_logp + from, a.K, lane, s, slot);
@@ -327,19 +367,6 @@ __device__ __forceinline__ Teacher teacher_of(const float* t, int n, bool tail, 
   return q;
 }
 
-struct DistillOut {
-  float *kl, *lse, *rest_logp, *student_logp;   // [N] x3, [N][K]
-};
-
-__device__ __forceinline__ void fill_row(const DistillOut& o, long long row, int K, float v, int lane) {
-  if (lane == 0) {
-    o.kl[row] = v;
-    o.lse[row] = v;
-    o.rest_logp[row] = v;
-  }
-  for (int j = lane; j < K; j += 32) o.student_logp[row * K + j] = v;
-}
-
 // One row by a warp, from the statistics of the logits behind its list and the
 // listed logits z[0 .. n), which may be shared memory.
 //
@@ -399,20 +426,6 @@ __device__ __forceinline__ void finish_row(const DistillOut& o, long long row, i
   }
 }
 
-// A teacher row before anything else: the first token that it names, -1 where
-// it names none, or one outside [0, V).  That is the row's target for the
-// kernels that compact the rows.
-__device__ __forceinline__ int row_target(const int* ids, int K, int V, int lane) {
-  int t = -1;
-  for (int j0 = 0; j0 < K; j0 += 32) {
-    const int x = j0 + lane < K ? ids[j0 + lane] : -1;
-    const unsigned bad = __ballot_sync(0xffffffffu, x >= V), some = __ballot_sync(0xffffffffu, x >= 0);
-    if (bad) return __shfl_sync(0xffffffffu, x, __ffs(bad) - 1);
-    if (t < 0 && some) t = __shfl_sync(0xffffffffu, x, __ffs(some) - 1);
-  }
-  return t;
-}
-
 constexpr int TARGET_WARPS = 8;
 // The rows' targets, and the outputs of the rows without a teacher.
 __global__ void __launch_bounds__(32 * TARGET_WARPS)
@@ -431,6 +444,7 @@ struct RowsArgs {
   long long c0;
   int C, nparts, V, K, tail, slabs;
   const float* stats;
+  int by_token;               // lists, not slabs
   const int* count;
   const int* id;
   float* z;                   // [C][slabs][128] logits of the parts that hold listed tokens
@@ -460,7 +474,8 @@ __global__ void __launch_bounds__(32 * ROWS8 * (1 + SHARES)) distill_rows_kernel
   const long long r = r0 + k;
   const bool valid = r < Cl;
   float* mine = reinterpret_cast<float*>(smem4 + ROWS8 * a.slabs) + k * a.K;
-  const int n = valid ? min(a.K, a.count[r]) : 0;
+  const long long row = valid ? a.idx[a.c0 + r] : 0, list = a.by_token ? row : r;
+  const int n = valid ? min(a.K, a.count[list]) : 0;
   if (w < ROWS8) {
     const Stat s = merge_parts8<false>(a.stats, a.nparts, a.C, a.c2, r0, Cl, lane, w, part);
     if (lane == 0) share[0][w] = s;
@@ -474,8 +489,8 @@ __global__ void __launch_bounds__(32 * ROWS8 * (1 + SHARES)) distill_rows_kernel
       int used = 0;
       for (int u0 = 0; u0 < n; u0 += 32) {
         const int u = u0 + lane;
-        const int id = u < n ? a.id[r * a.K + u] : 0, in = id / PART_COLS;
-        const bool first = u < n && (u == 0 || a.id[r * a.K + u - 1] / PART_COLS != in);
+        const int id = u < n ? a.id[list * a.K + u] : 0, in = id / PART_COLS;
+        const bool first = u < n && (u == 0 || a.id[list * a.K + u - 1] / PART_COLS != in);
         const unsigned f = __ballot_sync(0xffffffffu, first);
         if (u < n) {
           const int q = used + __popc(f & (0xffffffffu >> (31 - lane))) - 1, at = id % PART_COLS;
@@ -531,12 +546,11 @@ __global__ void __launch_bounds__(32 * ROWS8 * (1 + SHARES)) distill_rows_kernel
   }
   __syncthreads();
   if (w >= ROWS8 || !valid) return;
-  const long long row = a.idx[a.c0 + r];
   if (a.hdr[HDR_STATUS] & STATUS_TIMEOUT) return fill_row(a.out, row, a.K, __int_as_float(0x7fc00000), lane);
   Stat rest = share[0][k];
 #pragma unroll
   for (int i = 1; i <= SHARES; ++i) rest = merge(rest, share[i][k], a.c2);
-  finish_row(a.out, row, a.K, a.tail, a.c2, a.inv_t, rest, mine, a.t + r * a.K, a.slot + r * a.K, n, lane);
+  finish_row(a.out, row, a.K, a.tail, a.c2, a.inv_t, rest, mine, a.t + list * a.K, a.slot + list * a.K, n, lane);
 }
 
 // After a call of several chunks: a pipeline that timed out in one of them
@@ -828,10 +842,22 @@ flce_status flce_topk_distill(const void* hidden, const void* weight, const int3
   c.q = distill_sizes(N, H, V, K);
   if (!listed_plan(c.q, workspace_bytes, &p)) return FLCE_EWORKSPACE;
   int* targets = at<int>(workspace, p.o_targets);
-  count_launches(1);
-  distill_targets_kernel<<<static_cast<unsigned>(cdiv(N, TARGET_WARPS)), 32 * TARGET_WARPS, 0, st>>>(
-      teacher_ids, N, K, static_cast<int>(V), targets, out);
-  if (!ok(launch_result(cudaGetLastError()))) return FLCE_ECUDA;
+  const bool by_token = listed_front(p, N);
+  la.N = static_cast<int>(N);
+  auto launch_lists = [&](const int* idx) {
+    la.idx = idx;
+    count_launches(1);
+    return by_groups(K, [&](auto g) {
+      return launch_dependent_smem(distill_lists_kernel<decltype(g)::value>, static_cast<unsigned>(cdiv(idx ? la.C : N, ROWS8)),
+                                   32 * LIST_WARPS, lists_smem(K), st, la, targets, out);
+    });
+  };
+  if (!by_token) {
+    count_launches(1);
+    distill_targets_kernel<<<static_cast<unsigned>(cdiv(N, TARGET_WARPS)), 32 * TARGET_WARPS, 0, st>>>(
+        teacher_ids, N, K, static_cast<int>(V), targets, out);
+    if (!ok(launch_result(cudaGetLastError()))) return FLCE_ECUDA;
+  }
   c.hidden = hidden; c.weight = weight; c.targets = targets; c.ii = -1; c.temperature = temperature;
   c.logp = kl; c.entropy = rest_logp; c.lse = lse;
   c.seg_kb = distill_segment(N, H);
@@ -839,21 +865,22 @@ flce_status flce_topk_distill(const void* hidden, const void* weight, const int3
   la.t = at<float>(workspace, p.o_rows);
   la.count = reinterpret_cast<int*>(la.t + p.C * K);
   la.slot = reinterpret_cast<short*>(la.count + p.C);
+  la.C = static_cast<int>(p.C);
+  la.nparts = p.nparts;
+  la.slab = at<short>(workspace, p.o_start);
+  la.id = at<int>(workspace, p.o_id);
+  c.by_token = by_token;
+  if (by_token && !ok(launch_lists(nullptr))) return FLCE_ECUDA;
   flce_status s = listed_chunks(
       p, c, dev,
       [&](const ListedChunk& ch) {
-        la.hdr = ch.g->hdr; la.idx = ch.g->idx; la.c0 = ch.c0; la.C = ch.g->C; la.nparts = ch.g->nparts;
-        la.slab = const_cast<short*>(ch.g->slab);
-        la.id = const_cast<int*>(ch.g->lists.id);
-        count_launches(1);
-        return by_groups(K, [&](auto g) {
-          return launch_dependent_smem(distill_lists_kernel<decltype(g)::value>, static_cast<unsigned>(cdiv(la.C, ROWS8)),
-                                       32 * LIST_WARPS, lists_smem(K), st, la);
-        });
+        if (by_token) return cudaSuccess;
+        la.hdr = ch.g->hdr; la.c0 = ch.c0;
+        return launch_lists(ch.g->idx);
       },
       [&](const ListedChunk& ch) {
         const RowsArgs ra{ch.g->hdr, ch.g->idx, ch.c0, ch.g->C, ch.g->nparts, ch.g->V, K, tail, ch.g->slabs_per_row,
-                          ch.g->stats, la.count, la.id, ch.g->lists.z, la.t, la.slot, ch.g->c2, 1.f / temperature, out};
+                          ch.g->stats, by_token, la.count, la.id, ch.g->lists.z, la.t, la.slot, ch.g->c2, 1.f / temperature, out};
         count_launches(1);
         const unsigned blocks = static_cast<unsigned>(cdiv(ch.g->C, ROWS8));
         const size_t smem = rows_smem(K, ch.g->slabs_per_row);

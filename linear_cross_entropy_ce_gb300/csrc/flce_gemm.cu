@@ -494,7 +494,8 @@ __device__ __forceinline__ PartLists part_lists(const GemmArgs& a, bool rv, int 
 // columns from c0 on there.
 __device__ __forceinline__ int part_slab(const GemmArgs& a, bool rv, int grow, int c0) {
   const int part = c0 / PART_COLS;
-  return rv && part < a.nparts ? a.slab[static_cast<long long>(part) * a.C + grow] : -1;
+  if (!rv || part >= a.nparts) return -1;
+  return a.slab[static_cast<long long>(part) * a.C + (a.slab_by_token ? a.idx[a.c0 + grow] : grow)];
 }
 __device__ __forceinline__ float* slab_place(const GemmArgs& a, int slab, int grow, int c0) {
   return a.lists.z + (static_cast<long long>(grow) * a.slabs_per_row + slab) * PART_COLS + c0 % PART_COLS;

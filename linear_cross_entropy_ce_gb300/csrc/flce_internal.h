@@ -111,6 +111,7 @@ struct GemmArgs {
   int listed;           // STATS: LISTED_*
   ListView lists;       // LISTED_OUT: the tokens taken out; z of both
   const short* slab;    // LISTED_SLABS: [nparts][C] the row's slab of the part, or -1
+  int slab_by_token;    //   by token, not by row of the chunk
   int slabs_per_row;
 };
 

@@ -99,6 +99,7 @@ struct ListedCall {
   int ii;
   float temperature;
   int seg_kb;               // segment_blocks()
+  bool by_token;            // the slabs' table has a column per token, not per row of the chunk
   const uint32_t* mask;     // or null
   long long mask_stride;
   float *logp, *entropy, *lse;   // what left-out rows get 0 (or NaN) in, in a call of one chunk
@@ -156,6 +157,7 @@ flce_status listed_chunks(const ListedPlan& p, const ListedCall& c, const Device
   g.c2 = 1.4426950408889634f / c.temperature;
   g.listed = q.table == 4 ? LISTED_OUT : LISTED_SLABS;
   g.slab = at<short>(ws, p.o_start);
+  g.slab_by_token = c.by_token;
   g.slabs_per_row = static_cast<int>(q.z / PART_COLS);
   g.lists.start = at<int>(ws, p.o_start);
   g.lists.boundaries = p.nparts + 1;
