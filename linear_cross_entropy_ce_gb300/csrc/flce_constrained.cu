@@ -356,7 +356,9 @@ __global__ void __launch_bounds__(32 * TOP_WARPS) constrained_top_kernel(const T
   TopK best = top_of_parts(a.stats, a.zf + static_cast<size_t>(r) * a.ldz, a.nparts, a.C, a.V, a.K, r, lane, w, sv, si);
   const int n = static_cast<int>(min(a.lists.cap, static_cast<long long>(a.lists.start[static_cast<long long>(a.nparts) * a.C + r])));
   const long long at = r * a.lists.cap;
-  // Each warp's own share of the list (from empty, since the list before is in every warp)
+  // Each warp's own share of the list (from empty, since the best so far are in every warp); what is below the K-th of
+  // those is not among the K best.
+  const float least = __shfl_sync(0xffffffffu, best.v, a.K - 1);
   TopK mine;
   mine.clear();
   for (int e0 = w * 32; e0 < n; e0 += TOP_BATCH * TOP_WARPS * 32) {
@@ -366,7 +368,7 @@ __global__ void __launch_bounds__(32 * TOP_WARPS) constrained_top_kernel(const T
     for (int k = 0; k < TOP_BATCH; ++k) {
       const int e = e0 + k * (TOP_WARPS * 32) + lane;
       x[k] = e < n ? a.lists.z[at + e] : 0.f;
-      id[k] = e < n ? a.lists.id[at + e] : TopK::NONE;
+      id[k] = e < n && x[k] >= least ? a.lists.id[at + e] : TopK::NONE;
     }
     mine.offer_all(x, id, a.K, lane);
   }

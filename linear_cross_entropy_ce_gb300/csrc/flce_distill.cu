@@ -14,9 +14,10 @@
 // hold listed tokens out of the row's statistics and writes their logits side by
 // side (K parts at most), and the row kernel goes through those.  (Taking the
 // listed logits out one by one cost the epilogue more than the products: 4096
-// tokens, 20 entries, at 512 x 16000 112 us a GEMM, 76 so.)  All of a row's log probabilities are formed relative to its
-// largest logit (an fp32 log-sum-exp of 20 is off by 1e-6, as much as kl is
-// where student and teacher nearly agree), and r as (1 - p_max) - the others.
+// tokens, 20 entries, at 512 x 16000 112 us a GEMM, so 57.)  All of a row's log
+// probabilities are formed relative to its largest logit (an fp32 log-sum-exp of
+// 20 is off by 1e-6, as much as kl is where student and teacher nearly agree),
+// and r as (1 - p_max) - the others.
 //
 // Backward: behind the list dz_v = g (A s - r) / T * exp(z_v - lse_rest), one
 // exponential per logit with constants of its row that neither overflow nor

@@ -477,13 +477,19 @@ __device__ __forceinline__ PartLists part_lists(const GemmArgs& a, bool rv, int 
   }
   if (e < e1) {
     int first = e1;
-    for (; e < e1; ++e) {
-      const int at_col = l.id[row + e] - c0;
-      if (at_col < 0 || at_col >= ncol) continue;
-      first = min(first, e);
+    for (; e < e1; e += 4) {
+      int id[4];   // in flight
 #pragma unroll
-      for (int j = 0; j < GROUP_COLS / 32; ++j)
-        if (at_col / 32 == j) p.listed[j] |= 1u << (at_col % 32);
+      for (int k = 0; k < 4; ++k) id[k] = e + k < e1 ? l.id[row + e + k] : -1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int at_col = id[k] - c0;
+        if (id[k] < 0 || at_col < 0 || at_col >= ncol) continue;
+        first = min(first, e + k);
+#pragma unroll
+        for (int j = 0; j < GROUP_COLS / 32; ++j)
+          if (at_col / 32 == j) p.listed[j] |= 1u << (at_col % 32);
+      }
     }
     p.slot = l.z + row + first;
   }
