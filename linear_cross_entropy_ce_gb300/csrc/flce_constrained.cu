@@ -32,6 +32,8 @@ namespace {
 constexpr int HELD = 8;
 constexpr int STREAM_THREADS = 1024, CHUNK_THREADS = 512;
 
+__host__ __device__ __forceinline__ int pad_words(int words) { return (words + HELD - 1) / HELD * HELD; }
+
 struct RuleArgs {
   int V;
   const int* history;          // [N][L] by stride
@@ -58,7 +60,7 @@ struct RuleArgs {
 
 // A block per row, in windows of 32 HELD THREADS tokens (262144 for few rows: one
 // window covers most vocabularies).  61 rows of 1500 ids at a vocabulary of
-// 256007 with masks 13 us, 2048 rows of up to 2947 ids at 128256 60.  (The bitmap in
+// 256007 with masks 12 us, 2048 rows of up to 2947 ids at 128256 55.  (The bitmap in
 // memory, so that the blocks fit beside the streaming kernel's, took 53 us for the
 // former, longer than the first tile.)
 template <bool STREAM>
@@ -66,9 +68,7 @@ __global__ void __launch_bounds__(STREAM ? STREAM_THREADS : CHUNK_THREADS, STREA
     constrained_lists_kernel(const RuleArgs a) {
   constexpr int THREADS = STREAM ? STREAM_THREADS : CHUNK_THREADS, WARPS = THREADS / 32;
   constexpr int WINDOW = HELD * THREADS;   // words
-  constexpr int GROUPS = HELD * WARPS;     // of 32 words
-  extern __shared__ uint32_t bits[];       // [words of a window] the marked tokens, and the marked ones before each word
-  __shared__ int group[GROUPS];
+  extern __shared__ __align__(16) uint32_t bits[];   // [words of a window] the marked tokens, and the marked ones before each word
   __shared__ int sums[WARPS];
   const int tid = threadIdx.x, lane = tid % 32, w = tid / 32;
   long long r = blockIdx.x, n = blockIdx.x;
@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(STREAM ? STREAM_THREADS : CHUNK_THREADS, STREA
     n = a.idx[a.c0 + r];
   }
   const int V = a.V, words = (V + 31) / 32, window = min(words, WINDOW);
-  uint32_t* rank = bits + window;
+  const int padded = pad_words(window);
+  uint32_t* rank = bits + padded;
   const int* history = a.history + n * a.history_stride;
   const int* bias_ids = a.bias_ids + n * a.bias_ids_stride;
   const uint32_t* mask = a.mask ? a.mask + n * a.mask_stride : nullptr;
@@ -102,9 +103,7 @@ __global__ void __launch_bounds__(STREAM ? STREAM_THREADS : CHUNK_THREADS, STREA
 #pragma unroll
     for (int k = 0; k < HELD; ++k)
       allowed[k] = mask && k * THREADS + tid < nw ? mask[w0 + k * THREADS + tid] : 0xffffffffu;
-#pragma unroll
-    for (int k = 0; k < HELD; ++k)
-      if (k * THREADS + tid < nw) bits[k * THREADS + tid] = 0u;
+    for (int i = tid; i < padded / 4; i += THREADS) reinterpret_cast<uint4*>(bits)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     const unsigned t0 = static_cast<unsigned>(w0) * 32u, span = min(static_cast<unsigned>(V) - t0, nw * 32u);
     auto mark = [&](int x) {   // (negative ids are far above the span)
@@ -117,55 +116,45 @@ __global__ void __launch_bounds__(STREAM ? STREAM_THREADS : CHUNK_THREADS, STREA
     for (int i = HELD * THREADS + tid; i < len; i += THREADS) mark(history[i]);
     for (int i = tid; i < a.B; i += THREADS) mark(bias_ids[i]);
     __syncthreads();
-    // Forbidden tokens leave; then the words' ranks, 32 words at a time by a warp.
-    uint32_t word[HELD];
-    int before[HELD];
+    if (mask) {   // forbidden tokens leave
 #pragma unroll
-    for (int k = 0; k < HELD; ++k) {
-      const int i = k * THREADS + tid;
-      word[k] = 0u;
-      before[k] = 0;
-      if (k * THREADS >= nw) continue;   // uniform
-      word[k] = i < nw ? bits[i] & allowed[k] : 0u;
-      const int c = __popc(word[k]);
-      int incl = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
+      for (int k = 0; k < HELD; ++k) {
+        const int i = k * THREADS + tid;
+        if (i >= nw) break;
+        const uint32_t b = bits[i];
+        if (b & ~allowed[k]) bits[i] = b & allowed[k];
       }
-      before[k] = incl - c;
-      if (lane == 31) group[k * WARPS + w] = incl;
-    }
-    __syncthreads();
-    // groups, in order: warp w sums HELD of them
-    static_assert(GROUPS / WARPS == HELD && HELD <= 32, "a lane per group");
-    {
-      const int g = w * HELD + lane;
-      const int c = lane < HELD && g / WARPS * THREADS < nw ? group[g] : 0;
-      int incl = c;
-#pragma unroll
-      for (int o = 1; o < HELD; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      if (lane == HELD - 1) sums[w] = incl;
       __syncthreads();
-      int total = lane < WARPS ? sums[lane] : 0;
-      const int mine = __reduce_add_sync(0xffffffffu, lane < w ? total : 0);
-      if (lane < HELD) group[g] = base + mine + incl - c;
-      base += __reduce_add_sync(0xffffffffu, total);
     }
+    // the words' ranks: a thread has a run of 4 or HELD words
+    const int run = nw <= 4 * THREADS ? 4 : HELD, i0 = tid * run;
+    uint32_t word[HELD];
+    int count_here = 0;
+#pragma unroll
+    for (int k = 0; k < HELD; k += 4) {
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (k < run && i0 + k < nw) x = *reinterpret_cast<const uint4*>(bits + i0 + k);
+      word[k] = x.x; word[k + 1] = x.y; word[k + 2] = x.z; word[k + 3] = x.w;
+      count_here += __popc(x.x) + __popc(x.y) + __popc(x.z) + __popc(x.w);
+    }
+    int incl = count_here;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) sums[w] = incl;
     __syncthreads();
+    const int of_warp = lane < WARPS ? sums[lane] : 0;
+    int at = base + __reduce_add_sync(0xffffffffu, lane < w ? of_warp : 0) + incl - count_here;
+    base += __reduce_add_sync(0xffffffffu, of_warp);
 #pragma unroll
     for (int k = 0; k < HELD; ++k) {
-      const int i = k * THREADS + tid;
-      if (i >= nw) continue;
-      int at = group[k * WARPS + w] + before[k];
-      rank[i] = static_cast<uint32_t>(at);
-      bits[i] = word[k];
-      for (uint32_t b = word[k]; b && at < a.cap; b &= b - 1, ++at) {
-        id[at] = static_cast<int>(t0) + i * 32 + __ffs(b) - 1;
+      if (k >= run || i0 + k >= nw) break;
+      rank[i0 + k] = static_cast<uint32_t>(at);
+      for (uint32_t b = word[k]; b; b &= b - 1, ++at) {
+        if (at >= a.cap) break;
+        id[at] = static_cast<int>(t0) + (i0 + k) * 32 + __ffs(b) - 1;
         seen[at] = 0;
         if (bias_at) bias_at[at] = 0;
       }
@@ -409,7 +398,9 @@ __global__ void __launch_bounds__(256) all_rows_kernel(int* targets, long long N
   for (long long i = blockIdx.x * 256ll + threadIdx.x; i < N; i += gridDim.x * 256ll) targets[i] = 0;
 }
 
-size_t rule_smem(long long V, int threads) { return size_t(std::min<long long>(cdiv(V, 32), HELD * threads)) * 8; }
+size_t rule_smem(long long V, int threads) {
+  return size_t(pad_words(static_cast<int>(std::min<long long>(cdiv(V, 32), HELD * threads)))) * 8;
+}
 
 // Entries of a row at most.
 long long list_cap(long long V, long long L, long long B) { return std::max(1ll, std::min(V, L + B)); }
