@@ -27,10 +27,14 @@ namespace flce {
 namespace {
 
 // Few rows: all of a block's latency counts, so it is wide; many rows: several
-// blocks an SM.  A thread keeps HELD ids and HELD words of the mask and bitmap
-// in registers, all loads at once.
+// blocks an SM, and narrow ones where there is little to do (a call of 4096 rows of
+// 200 ids at a vocabulary of 4000 74 us with 128 threads a list, 110 with 512; 1307
+// of 1359 ids at 753 103 and 124; but 2000 of 6000 ids at 16000 483 and 444).  A
+// thread keeps HELD ids and HELD words of the mask and bitmap in registers, all
+// loads at once.
 constexpr int HELD = 8;
-constexpr int STREAM_THREADS = 1024, CHUNK_THREADS = 512;
+constexpr int STREAM_THREADS = 1024, CHUNK_THREADS = 512, SMALL_THREADS = 128;
+constexpr int SMALL_VOCABULARY = 8192, SMALL_HISTORY = 4096;
 
 __host__ __device__ __forceinline__ int pad_words(int words) { return (words + HELD - 1) / HELD * HELD; }
 
@@ -63,10 +67,9 @@ struct RuleArgs {
 // 256007 with masks 12 us, 2048 rows of up to 2947 ids at 128256 55.  (The bitmap in
 // memory, so that the blocks fit beside the streaming kernel's, took 53 us for the
 // former, longer than the first tile.)
-template <bool STREAM>
-__global__ void __launch_bounds__(STREAM ? STREAM_THREADS : CHUNK_THREADS, STREAM ? 1 : 2)
-    constrained_lists_kernel(const RuleArgs a) {
-  constexpr int THREADS = STREAM ? STREAM_THREADS : CHUNK_THREADS, WARPS = THREADS / 32;
+template <bool STREAM, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) constrained_lists_kernel(const RuleArgs a) {
+  constexpr int WARPS = THREADS / 32;
   constexpr int WINDOW = HELD * THREADS;   // words
   extern __shared__ __align__(16) uint32_t bits[];   // [words of a window] the marked tokens, and the marked ones before each word
   __shared__ int sums[WARPS];
@@ -450,7 +453,7 @@ constexpr long long MAX_HISTORY = 1ll << 30, MAX_BIASES = 1ll << 20;
 }  // namespace
 
 cudaError_t constrained_prepare() {
-  return cudaFuncSetAttribute(constrained_lists_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(constrained_lists_kernel<true, STREAM_THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               HELD * STREAM_THREADS * 8);
 }
 
@@ -540,7 +543,7 @@ flce_status flce_constrained_logprobs(const void* hidden, const void* weight, co
     l.rules = rv;
     if (!stream_setup(&a, &m, hidden, weight, segment_blocks(H))) return FLCE_ECUDA;
     count_launches(2);   // lists, the merge
-    constrained_lists_kernel<true><<<static_cast<unsigned>(N), STREAM_THREADS, rule_smem(V, STREAM_THREADS), st>>>(la);
+    constrained_lists_kernel<true, STREAM_THREADS><<<static_cast<unsigned>(N), STREAM_THREADS, rule_smem(V, STREAM_THREADS), st>>>(la);
     if (!ok(launch_result(cudaGetLastError()))) return FLCE_ECUDA;
     const ProfScope prof = prof_launch_begin(st);
     const cudaError_t e = launch_stream_ruled(a, m, l, st);
@@ -575,7 +578,11 @@ flce_status flce_constrained_logprobs(const void* hidden, const void* weight, co
         la.start = const_cast<int*>(ch.g->lists.start);
         la.id = const_cast<int*>(ch.g->lists.id);
         count_launches(1);
-        return launch_dependent_smem(constrained_lists_kernel<false>, static_cast<unsigned>(la.C), CHUNK_THREADS,
+        const unsigned blocks = static_cast<unsigned>(la.C);
+        if (V <= SMALL_VOCABULARY && L + B <= SMALL_HISTORY)
+          return launch_dependent_smem(constrained_lists_kernel<false, SMALL_THREADS>, blocks, SMALL_THREADS,
+                                       rule_smem(V, SMALL_THREADS), st, la);
+        return launch_dependent_smem(constrained_lists_kernel<false, CHUNK_THREADS>, blocks, CHUNK_THREADS,
                                      rule_smem(V, CHUNK_THREADS), st, la);
       },
       [&](const ListedChunk& ch) {
