@@ -60,6 +60,7 @@ struct RuleArgs {
   int* seen;
   int* bias_at;                // the last entry that names the token + 1, then its bias (as a float), or null
   long long cap;
+  int counts;                  // tokens of a window whose times are counted in shared memory
 };
 
 // A block per row, in windows of 32 HELD THREADS tokens (262144 for few rows: one
@@ -71,7 +72,8 @@ template <bool STREAM, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) constrained_lists_kernel(const RuleArgs a) {
   constexpr int WARPS = THREADS / 32;
   constexpr int WINDOW = HELD * THREADS;   // words
-  extern __shared__ __align__(16) uint32_t bits[];   // [words of a window] the marked tokens, and the marked ones before each word
+  // [words of a window] the marked tokens, and the marked ones before each word; [counts] times of its first tokens
+  extern __shared__ __align__(16) uint32_t bits[];
   __shared__ int sums[WARPS];
   const int tid = threadIdx.x, lane = tid % 32, w = tid / 32;
   long long r = blockIdx.x, n = blockIdx.x;
@@ -86,6 +88,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) constrained_lists_ker
   const int V = a.V, words = (V + 31) / 32, window = min(words, WINDOW);
   const int padded = pad_words(window);
   uint32_t* rank = bits + padded;
+  int* times = reinterpret_cast<int*>(rank + padded);
   const int* history = a.history + n * a.history_stride;
   const int* bias_ids = a.bias_ids + n * a.bias_ids_stride;
   const uint32_t* mask = a.mask ? a.mask + n * a.mask_stride : nullptr;
@@ -107,6 +110,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) constrained_lists_ker
     for (int k = 0; k < HELD; ++k)
       allowed[k] = mask && k * THREADS + tid < nw ? mask[w0 + k * THREADS + tid] : 0xffffffffu;
     for (int i = tid; i < padded / 4; i += THREADS) reinterpret_cast<uint4*>(bits)[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = tid; i < a.counts; i += THREADS) times[i] = 0;
+    const int base0 = base;
     __syncthreads();
     const unsigned t0 = static_cast<unsigned>(w0) * 32u, span = min(static_cast<unsigned>(V) - t0, nw * 32u);
     auto mark = [&](int x) {   // (negative ids are far above the span)
@@ -158,7 +163,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) constrained_lists_ker
       for (uint32_t b = word[k]; b; b &= b - 1, ++at) {
         if (at >= a.cap) break;
         id[at] = static_cast<int>(t0) + (i0 + k) * 32 + __ffs(b) - 1;
-        seen[at] = 0;
+        if (at - base0 >= a.counts) seen[at] = 0;
         if (bias_at) bias_at[at] = 0;
       }
     }
@@ -174,8 +179,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) constrained_lists_ker
     auto count = [&](int i, int x) {
       const int at = place(x);
       if (at < 0) return;
-      if (i < prompt) atomicOr(seen + at, static_cast<int>(0x80000000u));
-      else atomicAdd(seen + at, 1);
+      int* to = at - base0 < a.counts ? times + (at - base0) : seen + at;
+      if (i < prompt) atomicOr(to, static_cast<int>(0x80000000u));
+      else atomicAdd(to, 1);
     };
 #pragma unroll
     for (int k = 0; k < HELD; ++k) count(k * THREADS + tid, held[k]);
@@ -185,6 +191,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) constrained_lists_ker
       const int at = place(bias_ids[i]);
       if (at >= 0) atomicMax(bias_at + at, i + 1);
     }
+    __syncthreads();
+    for (int i = tid; i < min(a.counts, base - base0); i += THREADS)
+      if (base0 + i < a.cap) seen[base0 + i] = times[i];
     // where tiles or parts begin
     if constexpr (STREAM) {
       for (int b = tid; b < tiles; b += THREADS) {
@@ -401,8 +410,12 @@ __global__ void __launch_bounds__(256) all_rows_kernel(int* targets, long long N
   for (long long i = blockIdx.x * 256ll + threadIdx.x; i < N; i += gridDim.x * 256ll) targets[i] = 0;
 }
 
-size_t rule_smem(long long V, int threads) {
-  return size_t(pad_words(static_cast<int>(std::min<long long>(cdiv(V, 32), HELD * threads)))) * 8;
+// Times are counted in shared memory for this many listed tokens of a window (a
+// call of 2000 rows of 6000 ids at a vocabulary of 16000 383 us, with all of the
+// 12 million atomics in L2 449; histories of some hundred ids are level).
+constexpr int MAX_COUNTS = 8192;
+size_t rule_smem(long long V, int threads, int counts) {
+  return size_t(pad_words(static_cast<int>(std::min<long long>(cdiv(V, 32), HELD * threads)))) * 8 + size_t(counts) * 4;
 }
 
 // Entries of a row at most.
@@ -453,8 +466,12 @@ constexpr long long MAX_HISTORY = 1ll << 30, MAX_BIASES = 1ll << 20;
 }  // namespace
 
 cudaError_t constrained_prepare() {
-  return cudaFuncSetAttribute(constrained_lists_kernel<true, STREAM_THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              HELD * STREAM_THREADS * 8);
+  const cudaError_t e =
+      cudaFuncSetAttribute(constrained_lists_kernel<true, STREAM_THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           HELD * STREAM_THREADS * 8 + MAX_COUNTS * 4);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(constrained_lists_kernel<false, CHUNK_THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              HELD * CHUNK_THREADS * 8 + MAX_COUNTS * 4);
 }
 
 }  // namespace flce
@@ -507,6 +524,7 @@ flce_status flce_constrained_logprobs(const void* hidden, const void* weight, co
   la.bias_ids_stride = c.bias_ids_stride; la.bias_stride = c.bias_stride;
   la.mask = reinterpret_cast<const uint32_t*>(c.mask); la.mask_stride = c.mask_stride;
   la.cap = list_cap(V, L, B);
+  la.counts = static_cast<int>(std::min<long long>(L > 0 ? la.cap : 0, MAX_COUNTS));
   RuleView rv;
   rv.repetition = c.repetition_penalty; rv.frequency = c.frequency_penalty; rv.presence = c.presence_penalty;
   if (N <= STREAM_MAX_TOKENS) {
@@ -543,7 +561,7 @@ flce_status flce_constrained_logprobs(const void* hidden, const void* weight, co
     l.rules = rv;
     if (!stream_setup(&a, &m, hidden, weight, segment_blocks(H))) return FLCE_ECUDA;
     count_launches(2);   // lists, the merge
-    constrained_lists_kernel<true, STREAM_THREADS><<<static_cast<unsigned>(N), STREAM_THREADS, rule_smem(V, STREAM_THREADS), st>>>(la);
+    constrained_lists_kernel<true, STREAM_THREADS><<<static_cast<unsigned>(N), STREAM_THREADS, rule_smem(V, STREAM_THREADS, la.counts), st>>>(la);
     if (!ok(launch_result(cudaGetLastError()))) return FLCE_ECUDA;
     const ProfScope prof = prof_launch_begin(st);
     const cudaError_t e = launch_stream_ruled(a, m, l, st);
@@ -581,9 +599,9 @@ flce_status flce_constrained_logprobs(const void* hidden, const void* weight, co
         const unsigned blocks = static_cast<unsigned>(la.C);
         if (V <= SMALL_VOCABULARY && L + B <= SMALL_HISTORY)
           return launch_dependent_smem(constrained_lists_kernel<false, SMALL_THREADS>, blocks, SMALL_THREADS,
-                                       rule_smem(V, SMALL_THREADS), st, la);
+                                       rule_smem(V, SMALL_THREADS, la.counts), st, la);
         return launch_dependent_smem(constrained_lists_kernel<false, CHUNK_THREADS>, blocks, CHUNK_THREADS,
-                                     rule_smem(V, CHUNK_THREADS), st, la);
+                                     rule_smem(V, CHUNK_THREADS, la.counts), st, la);
       },
       [&](const ListedChunk& ch) {
         float2* ml = at<float2>(workspace, p.o_ml);
