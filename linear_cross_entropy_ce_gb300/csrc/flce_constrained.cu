@@ -68,7 +68,7 @@ struct RuleArgs {
 // 256007 with masks 12 us, 2048 rows of up to 2947 ids at 128256 55.  (The bitmap in
 // memory, so that the blocks fit beside the streaming kernel's, took 53 us for the
 // former, longer than the first tile.)
-template <bool STREAM, int THREADS>
+template <bool STREAM, int THREADS, bool COUNTED>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS) constrained_lists_kernel(const RuleArgs a) {
   constexpr int WARPS = THREADS / 32;
   constexpr int WINDOW = HELD * THREADS;   // words
@@ -110,8 +110,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) constrained_lists_ker
     for (int k = 0; k < HELD; ++k)
       allowed[k] = mask && k * THREADS + tid < nw ? mask[w0 + k * THREADS + tid] : 0xffffffffu;
     for (int i = tid; i < padded / 4; i += THREADS) reinterpret_cast<uint4*>(bits)[i] = make_uint4(0u, 0u, 0u, 0u);
-    for (int i = tid; i < a.counts; i += THREADS) times[i] = 0;
     const int base0 = base;
+    if constexpr (COUNTED)
+      for (int i = tid; i < a.counts; i += THREADS) times[i] = 0;
     __syncthreads();
     const unsigned t0 = static_cast<unsigned>(w0) * 32u, span = min(static_cast<unsigned>(V) - t0, nw * 32u);
     auto mark = [&](int x) {   // (negative ids are far above the span)
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) constrained_lists_ker
       for (uint32_t b = word[k]; b; b &= b - 1, ++at) {
         if (at >= a.cap) break;
         id[at] = static_cast<int>(t0) + (i0 + k) * 32 + __ffs(b) - 1;
-        if (at - base0 >= a.counts) seen[at] = 0;
+        if (!COUNTED || at - base0 >= a.counts) seen[at] = 0;
         if (bias_at) bias_at[at] = 0;
       }
     }
@@ -179,7 +180,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) constrained_lists_ker
     auto count = [&](int i, int x) {
       const int at = place(x);
       if (at < 0) return;
-      int* to = at - base0 < a.counts ? times + (at - base0) : seen + at;
+      int* to = COUNTED && at - base0 < a.counts ? times + (at - base0) : seen + at;
       if (i < prompt) atomicOr(to, static_cast<int>(0x80000000u));
       else atomicAdd(to, 1);
     };
@@ -191,9 +192,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) constrained_lists_ker
       const int at = place(bias_ids[i]);
       if (at >= 0) atomicMax(bias_at + at, i + 1);
     }
-    __syncthreads();
-    for (int i = tid; i < min(a.counts, base - base0); i += THREADS)
-      if (base0 + i < a.cap) seen[base0 + i] = times[i];
+    if constexpr (COUNTED) {
+      __syncthreads();
+      for (int i = tid; i < min(a.counts, base - base0); i += THREADS)
+        if (base0 + i < a.cap) seen[base0 + i] = times[i];
+    }
     // where tiles or parts begin
     if constexpr (STREAM) {
       for (int b = tid; b < tiles; b += THREADS) {
@@ -410,10 +413,14 @@ __global__ void __launch_bounds__(256) all_rows_kernel(int* targets, long long N
   for (long long i = blockIdx.x * 256ll + threadIdx.x; i < N; i += gridDim.x * 256ll) targets[i] = 0;
 }
 
-// Times are counted in shared memory for this many listed tokens of a window (a
-// call of 2000 rows of 6000 ids at a vocabulary of 16000 383 us, with all of the
-// 12 million atomics in L2 449; histories of some hundred ids are level).
-constexpr int MAX_COUNTS = 8192;
+// Histories of LONG_HISTORY ids and more have their times counted in shared
+// memory, for the first MAX_COUNTS listed tokens of a window; the others' go to L2.
+// Calls with the atomics in L2 and in shared memory: 2000 rows of 6000 ids at a
+// vocabulary of 16000 441 and 375 us, 2000 of 4000 at 8000 281 and 232, 1024 of
+// 1500 at 16000 89.5 and 86.6, 1307 of 1359 at 753 102.4 and 103.1; below that it
+// loses: 1307 of 1024 at 753 92.6 and 95.3, 4096 of 200 at 4000 73.9 and 76.9.  Two
+// kernels, as one with the choice at run time costs short histories as much.
+constexpr int MAX_COUNTS = 8192, LONG_HISTORY = 1280;
 size_t rule_smem(long long V, int threads, int counts) {
   return size_t(pad_words(static_cast<int>(std::min<long long>(cdiv(V, 32), HELD * threads)))) * 8 + size_t(counts) * 4;
 }
@@ -466,12 +473,15 @@ constexpr long long MAX_HISTORY = 1ll << 30, MAX_BIASES = 1ll << 20;
 }  // namespace
 
 cudaError_t constrained_prepare() {
-  const cudaError_t e =
-      cudaFuncSetAttribute(constrained_lists_kernel<true, STREAM_THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           HELD * STREAM_THREADS * 8 + MAX_COUNTS * 4);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(constrained_lists_kernel<false, CHUNK_THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              HELD * CHUNK_THREADS * 8 + MAX_COUNTS * 4);
+  cudaError_t e = cudaSuccess;
+  auto allow = [&](auto* kernel, size_t bytes) {
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+  };
+  allow(constrained_lists_kernel<true, STREAM_THREADS, false>, HELD * STREAM_THREADS * 8);
+  allow(constrained_lists_kernel<true, STREAM_THREADS, true>, HELD * STREAM_THREADS * 8 + MAX_COUNTS * 4);
+  allow(constrained_lists_kernel<false, CHUNK_THREADS, true>, HELD * CHUNK_THREADS * 8 + MAX_COUNTS * 4);
+  return e;
 }
 
 }  // namespace flce
@@ -524,7 +534,7 @@ flce_status flce_constrained_logprobs(const void* hidden, const void* weight, co
   la.bias_ids_stride = c.bias_ids_stride; la.bias_stride = c.bias_stride;
   la.mask = reinterpret_cast<const uint32_t*>(c.mask); la.mask_stride = c.mask_stride;
   la.cap = list_cap(V, L, B);
-  la.counts = static_cast<int>(std::min<long long>(L > 0 ? la.cap : 0, MAX_COUNTS));
+  la.counts = static_cast<int>(std::min<long long>(L >= LONG_HISTORY ? la.cap : 0, MAX_COUNTS));
   RuleView rv;
   rv.repetition = c.repetition_penalty; rv.frequency = c.frequency_penalty; rv.presence = c.presence_penalty;
   if (N <= STREAM_MAX_TOKENS) {
@@ -561,7 +571,9 @@ flce_status flce_constrained_logprobs(const void* hidden, const void* weight, co
     l.rules = rv;
     if (!stream_setup(&a, &m, hidden, weight, segment_blocks(H))) return FLCE_ECUDA;
     count_launches(2);   // lists, the merge
-    constrained_lists_kernel<true, STREAM_THREADS><<<static_cast<unsigned>(N), STREAM_THREADS, rule_smem(V, STREAM_THREADS, la.counts), st>>>(la);
+    auto* const lists =
+        la.counts > 0 ? constrained_lists_kernel<true, STREAM_THREADS, true> : constrained_lists_kernel<true, STREAM_THREADS, false>;
+    lists<<<static_cast<unsigned>(N), STREAM_THREADS, rule_smem(V, STREAM_THREADS, la.counts), st>>>(la);
     if (!ok(launch_result(cudaGetLastError()))) return FLCE_ECUDA;
     const ProfScope prof = prof_launch_begin(st);
     const cudaError_t e = launch_stream_ruled(a, m, l, st);
@@ -596,12 +608,14 @@ flce_status flce_constrained_logprobs(const void* hidden, const void* weight, co
         la.start = const_cast<int*>(ch.g->lists.start);
         la.id = const_cast<int*>(ch.g->lists.id);
         count_launches(1);
-        const unsigned blocks = static_cast<unsigned>(la.C);
-        if (V <= SMALL_VOCABULARY && L + B <= SMALL_HISTORY)
-          return launch_dependent_smem(constrained_lists_kernel<false, SMALL_THREADS>, blocks, SMALL_THREADS,
-                                       rule_smem(V, SMALL_THREADS, la.counts), st, la);
-        return launch_dependent_smem(constrained_lists_kernel<false, CHUNK_THREADS>, blocks, CHUNK_THREADS,
-                                     rule_smem(V, CHUNK_THREADS, la.counts), st, la);
+        const bool small = V <= SMALL_VOCABULARY && L + B <= SMALL_HISTORY, counted = la.counts > 0;
+        const unsigned threads = small ? SMALL_THREADS : CHUNK_THREADS;
+        auto* const lists = small ? counted ? constrained_lists_kernel<false, SMALL_THREADS, true>
+                                            : constrained_lists_kernel<false, SMALL_THREADS, false>
+                                  : counted ? constrained_lists_kernel<false, CHUNK_THREADS, true>
+                                            : constrained_lists_kernel<false, CHUNK_THREADS, false>;
+        return launch_dependent_smem(lists, static_cast<unsigned>(la.C), threads, rule_smem(V, static_cast<int>(threads), la.counts),
+                                     st, la);
       },
       [&](const ListedChunk& ch) {
         float2* ml = at<float2>(workspace, p.o_ml);
