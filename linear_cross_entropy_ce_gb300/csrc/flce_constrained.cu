@@ -29,7 +29,7 @@ namespace {
 // Few rows: all of a block's latency counts, so it is wide; many rows: several
 // blocks an SM, and narrow ones where there is little to do (a call of 4096 rows of
 // 200 ids at a vocabulary of 4000 74 us with 128 threads a list, 110 with 512; 1307
-// of 1359 ids at 753 103 and 124; but 2000 of 6000 ids at 16000 483 and 444).  A
+// of 1359 ids at 753 103 and 133; but 2000 of 6000 ids at 16000 384 and 374).  A
 // thread keeps HELD ids and HELD words of the mask and bitmap in registers, all
 // loads at once.
 constexpr int HELD = 8;
