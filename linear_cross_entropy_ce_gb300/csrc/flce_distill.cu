@@ -651,6 +651,8 @@ __global__ void __launch_bounds__(32 * TARGET_WARPS)
     if (j >= K) break;
     const float p = slot[e] >= 0 ? expf(s.t[slot[e]] - q.shift) : 0.f;
     const float dz = gt * (mass * expf(student_logp[row * K + j]) - p);
+    // bf16, as MODE_DZ stores all of dz: the operand type of both gradient products.  A
+    // few rows that a few entries dominate keep up to 3.4e-3 of that (2.3e-3 for many).
     patch[row * K + j] = static_cast<uint16_t>(ptx::pack_bf16x2(dz, 0.f) & 0xffffu);
   }
 }
