@@ -403,10 +403,12 @@ flce_status flce_topk_distill(const void* hidden, const void* weight,
  *   grad_weight = dz^T X (fp32, or bf16 with FLCE_GW_BF16);
  * either may be NULL.  lse, rest_logp and student_logp are those
  * flce_topk_distill gave for the same inputs.  The teacher gets no gradient.
- * Rounding, failures and workspace (flce_topk_distill_bwd_workspace_bytes) as
- * flce_logprobs_bwd, and 12 + 2 K bytes per row; a few rows that a few entries
- * dominate do not average the rounding of dz out (up to 3.4e-3 of a bf16
- * gradient's norm).
+ * dz is held as two bf16 parts (2^-16 of itself is lost), so that the gradients
+ * are those of an fp32 dz; a bf16 output is rounded once.  Failures as
+ * flce_logprobs_bwd.
+ * Workspace (flce_topk_distill_bwd_workspace_bytes): what all rows need in one
+ * chunk, 4 bytes per logit, where that is up to 4 GiB, else as much as
+ * flce_logprobs_bwd; and 12 + 4 K bytes per row.
  */
 size_t flce_topk_distill_bwd_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t K,
                                              uint32_t flags);

@@ -94,7 +94,7 @@ struct Plan {
   long long N = 0, H = 0, V = 0, C = 0, ldz = 0, n_chunks = 0;
   int nvt = 0, nparts = 0, splits = 1, kb_per_split = 0, tile_counters = 2;
   long long n_counters = 0, flags_per_chunk = 0;
-  bool fwd_only = false, norm = false, gw32 = false, probs = false, slabs = false;
+  bool fwd_only = false, norm = false, gw32 = false, probs = false, slabs = false, two = false;
   size_t o_idx = 0, o_rl = 0, o_cnt = 0, o_xc = 0, o_tc = 0, o_zt = 0, o_part = 0, o_z = 0, o_dx = 0, o_rinv = 0,
          o_dg = 0, o_gw = 0, o_rowc = 0, total = 0;
 };
@@ -106,10 +106,12 @@ constexpr int DX_UNIT_KB = 128;  // preferred K blocks of one dX unit
 // Workspace layout for chunks of C rows.  Only the bf16 C x V logits buffer
 // (absent for the forward-only call) grows with V; with a bf16 grad_weight
 // (gw32) the fp32 V x H accumulator of grad_weight lives here as well.
-// probs: the backward of the token log probabilities (per-row constants).
+// probs: the backward of the token log probabilities (per-row constants); two:
+// dz in two parts, whose chunks may be of 64 rows, the least that a K block takes.
 Plan layout(long long N, long long H, long long V, long long C, int S, bool fwd_only, bool norm = false,
-            bool gw32 = false, bool probs = false, bool slabs = false) {
+            bool gw32 = false, bool probs = false, bool slabs = false, bool two = false) {
   Plan p;
+  p.two = two;
   p.N = N; p.H = H; p.V = V; p.C = C; p.fwd_only = fwd_only; p.norm = norm; p.gw32 = gw32 && !fwd_only;
   p.ldz = cdiv(V, 64) * 64;
   p.nvt = static_cast<int>(cdiv(V, BN));
@@ -132,7 +134,7 @@ Plan layout(long long N, long long H, long long V, long long C, int S, bool fwd_
   p.o_xc = off;   off += al256(size_t(C) * H * 2);
   p.o_tc = off;   off += al256(size_t(C) * 4);
   p.o_zt = off;   off += al256(size_t(C) * 4);
-  if (!fwd_only) { p.o_z = off; off += al256(size_t(C) * p.ldz * 2); }
+  if (!fwd_only) { p.o_z = off; off += al256(size_t(C) * p.ldz * (two ? 4 : 2)); }
   // The per-part (max, sum exp) of a chunk are read by lse_dz before the
   // backward launch, and the fp32 sum of a split grad_hidden GEMM lives only
   // inside that launch (the next chunk's logits rewrite the parts after it):
@@ -212,30 +214,32 @@ int probs_splits(long long C, long long H, long long V, int pairs, bool* slabs) 
 long long max_chunk(long long N) { return cdiv(N, BM) * BM; }
 
 Plan plan_for_chunk(long long N, long long H, long long V, long long C, bool fwd_only, int pairs, size_t bytes,
-                    bool norm = false, bool gw32 = false, bool probs = false) {
+                    bool norm = false, bool gw32 = false, bool probs = false, bool two = false) {
   bool slabs = false;
   const int S = probs ? probs_splits(C, H, V, pairs, &slabs) : preferred_splits(C, H, V, pairs);
-  Plan p = layout(N, H, V, C, S, fwd_only, norm, gw32, probs, slabs);
-  if (p.total > bytes) p = layout(N, H, V, C, 1, fwd_only, norm, gw32, probs);
+  Plan p = layout(N, H, V, C, S, fwd_only, norm, gw32, probs, slabs, two);
+  if (p.total > bytes) p = layout(N, H, V, C, 1, fwd_only, norm, gw32, probs, false, two);
   return p;
 }
 
-// Largest chunk (multiple of 128 rows) whose plan fits in `bytes`.
+// Largest chunk (multiple of 128 rows, of 64 with two parts) whose plan fits in `bytes`.
 bool plan_for_bytes(long long N, long long H, long long V, bool fwd_only, size_t bytes, int pairs, Plan* out,
-                    bool norm = false, bool gw32 = false, bool probs = false) {
-  long long lo = BM, hi = max_chunk(N);
+                    bool norm = false, bool gw32 = false, bool probs = false, bool two = false) {
+  const long long unit = two ? BK : BM;
+  long long lo = unit, hi = max_chunk(N);
+  auto total = [&](long long C) { return layout(N, H, V, C, 1, fwd_only, norm, gw32, probs, false, two).total; };
   // one chunk needs no fp32 accumulator for a bf16 grad_weight: less than several
-  if (probs && gw32 && layout(N, H, V, hi, 1, fwd_only, norm, gw32, probs).total <= bytes) {
-    *out = plan_for_chunk(N, H, V, hi, fwd_only, pairs, bytes, norm, gw32, probs);
+  if (probs && gw32 && total(hi) <= bytes) {
+    *out = plan_for_chunk(N, H, V, hi, fwd_only, pairs, bytes, norm, gw32, probs, two);
     return true;
   }
-  if (layout(N, H, V, lo, 1, fwd_only, norm, gw32, probs).total > bytes) return false;
+  if (total(lo) > bytes) return false;
   while (lo < hi) {   // the size shrinks as C grows only through the d(gain) partials: bisect on the total
-    const long long mid = ((lo / BM + hi / BM + 1) / 2) * BM;
-    if (layout(N, H, V, mid, 1, fwd_only, norm, gw32, probs).total <= bytes) lo = mid;
-    else hi = mid - BM;
+    const long long mid = ((lo / unit + hi / unit + 1) / 2) * unit;
+    if (total(mid) <= bytes) lo = mid;
+    else hi = mid - unit;
   }
-  *out = plan_for_chunk(N, H, V, lo, fwd_only, pairs, bytes, norm, gw32, probs);
+  *out = plan_for_chunk(N, H, V, lo, fwd_only, pairs, bytes, norm, gw32, probs, two);
   return true;
 }
 
@@ -284,6 +288,19 @@ size_t default_bytes(long long N, long long H, long long V, bool fwd_only, bool 
   Plan p;
   if (plan_for_bytes(N, H, V, fwd_only, budget, pairs, &p, norm, gw32, probs)) return p.total;
   return plan_for_chunk(N, H, V, BM, fwd_only, pairs, ~size_t(0), norm, gw32, probs).total;
+}
+
+// The same for the gradient of the distillation loss, whose dz takes twice the
+// bytes: all rows in one chunk where that is up to 4 GiB (a second chunk reads and
+// rewrites grad_weight), else as much as for the log probabilities.
+size_t two_part_bytes(long long N, long long H, long long V, bool gw32, size_t reserve) {
+  const size_t own = default_bytes(N, H, V, false, false, gw32, true);
+  if (own == 0) return 0;
+  constexpr size_t MOST = size_t(4) << 30;
+  const Plan one = plan_for_chunk(N, H, V, max_chunk(N), false, device_pairs(), MOST, false, gw32, true, true);
+  if (one.total <= MOST) return std::max(own, one.total);
+  const size_t least = layout(N, H, V, BK, 1, false, false, gw32, true, false, true).total;
+  return std::max({own - std::min(own, reserve), own / 2, least});
 }
 
 constexpr uint32_t KNOWN_FLAGS = FLCE_REDUCE_SUM | FLCE_GW_BF16;
@@ -469,7 +486,8 @@ flce_status run(const Job& j) {
   if (device_state(&dev) != cudaSuccess) { cudaGetLastError(); return FLCE_ECUDA; }
   if (dev.major < 10) return FLCE_EUNSUPPORTED;
   Plan p;
-  if (!plan_for_bytes(N, H, V, fwd_only, j.ws_bytes, dev.pairs, &p, norm, gw_bf16, probs)) return FLCE_EWORKSPACE;
+  const bool two = j.distill != nullptr;
+  if (!plan_for_bytes(N, H, V, fwd_only, j.ws_bytes, dev.pairs, &p, norm, gw_bf16, probs, two)) return FLCE_EWORKSPACE;
 
   cudaStream_t st = static_cast<cudaStream_t>(j.stream);
   void* ws = j.ws;
@@ -495,10 +513,11 @@ flce_status run(const Job& j) {
   std::memset(&fm, 0, sizeof(fm));
   std::memset(&bm, 0, sizeof(bm));
   const unsigned long long hb = static_cast<unsigned long long>(H) * 2;
+  const long long zrows = two ? 2 * p.C : p.C;
   bool ok = make_map(&fm.a0, xc, H, p.C, hb, BK, BM) && make_map(&fm.b0, j.weight, H, V, hb, BK, BN / 2);
   if (!fwd_only)
-    ok = ok && make_map(&bm.a0, z, V, p.C, p.ldz * 2, BK, BM) && make_map(&bm.b0, j.weight, H, V, hb, 64, BK) &&
-         make_map(&bm.a1, z, V, p.C, p.ldz * 2, 64, BK) && make_map(&bm.b1, xc, H, p.C, hb, 64, BK) &&
+    ok = ok && make_map(&bm.a0, z, V, zrows, p.ldz * 2, BK, BM) && make_map(&bm.b0, j.weight, H, V, hb, 64, BK) &&
+         make_map(&bm.a1, z, V, zrows, p.ldz * 2, 64, BK) && make_map(&bm.b1, xc, H, p.C, hb, 64, BK) &&
          (!gwacc || (direct ? make_map(&bm.out, gwacc, H, V, hb, 64, 64)
                             : make_map(&bm.out, gwacc, H, V, static_cast<unsigned long long>(H) * 4, 32, 64,
                                        CU_TENSOR_MAP_DATA_TYPE_FLOAT32, CU_TENSOR_MAP_SWIZZLE_128B)));
@@ -538,6 +557,7 @@ flce_status run(const Job& j) {
   g.pf_threads = p.C <= 512 ? 1 : 0;
   g.dxacc = dxacc;
   g.skip = skip;
+  g.two = two ? 1 : 0;
   g.slabs = p.slabs ? 1 : 0;
   g.gw_bf16 = direct ? 1 : 0;
   DzRow* rowc = probs ? at<DzRow>(ws, p.o_rowc) : nullptr;
@@ -674,6 +694,11 @@ flce_status fwd_bwd_on_workspace(const void* hidden, const void* weight, const i
 }  // namespace flce
 
 namespace flce {
+size_t distill_grad_bytes(int64_t N, int64_t H, int64_t V, uint32_t flags, size_t reserve) {
+  if (flags & ~FLCE_GW_BF16) return 0;
+  return two_part_bytes(N, H, V, (flags & FLCE_GW_BF16) != 0, reserve);
+}
+
 flce_status run_distill_grad(const DistillGrad& d, const void* hidden, const void* weight, int64_t N, int64_t H,
                              int64_t V, uint32_t flags, float temperature, void* grad_hidden, float* grad_weight,
                              void* workspace, size_t workspace_bytes, void* stream) {

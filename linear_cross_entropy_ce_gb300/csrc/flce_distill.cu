@@ -619,7 +619,7 @@ template <int SORT_GROUPS>
 __global__ void __launch_bounds__(32 * TARGET_WARPS)
     distill_grad_rows_kernel(const int* ids, const float* logp, long long N, int K, int V, int tail, float temperature,
                              const float* lse, const float* rest_logp, const float* student_logp, const float* grad_kl,
-                             int* targets, float* dz_lse, float* dz_grad, uint16_t* patch) {
+                             int* targets, float* dz_lse, float* dz_grad, uint32_t* patch) {
   extern __shared__ int smem[];   // scratch of a sort per warp
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   const long long row = static_cast<long long>(blockIdx.x) * TARGET_WARPS + w;
@@ -651,22 +651,25 @@ __global__ void __launch_bounds__(32 * TARGET_WARPS)
     if (j >= K) break;
     const float p = slot[e] >= 0 ? expf(s.t[slot[e]] - q.shift) : 0.f;
     const float dz = gt * (mass * expf(student_logp[row * K + j]) - p);
-    // bf16, as MODE_DZ stores all of dz: the operand type of both gradient products.  A
-    // few rows that a few entries dominate keep up to 3.4e-3 of that (2.3e-3 for many).
-    patch[row * K + j] = static_cast<uint16_t>(ptx::pack_bf16x2(dz, 0.f) & 0xffffu);
+    // two bf16 parts, as MODE_DZ stores all of dz
+    const uint32_t hi = ptx::pack_bf16x2(dz, 0.f) & 0xffffu;
+    patch[row * K + j] = hi | ptx::pack_bf16x2(dz - __uint_as_float(hi << 16), 0.f) << 16;
   }
 }
 
-// dz of a chunk's listed tokens.  (Entries of the same token hold the same.)
+// dz of a chunk's listed tokens, both parts.  (Entries of the same token hold the same.)
 __global__ void __launch_bounds__(256)
     distill_patch_kernel(const int* hdr, const int* idx, long long c0, int C, int K, int V, long long ldz, const int* ids,
-                         const uint16_t* patch, uint16_t* z) {
+                         const uint32_t* patch, uint16_t* z) {
   ptx::grid_dependency_wait();
   const long long total = static_cast<long long>(chunk_rows(hdr, c0, C)) * K;
   for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
     const long long r = i / K, from = idx[c0 + r] * static_cast<long long>(K) + (i - r * K);
     const int x = ids[from];
-    if (x >= 0 && x < V) z[r * ldz + x] = patch[from];
+    if (x < 0 || x >= V) continue;
+    const uint32_t dz = patch[from];
+    z[r * ldz + x] = static_cast<uint16_t>(dz & 0xffffu);
+    z[(C + r) * ldz + x] = static_cast<uint16_t>(dz >> 16);
   }
 }
 
@@ -743,7 +746,7 @@ GradExtra grad_extra(long long N, int K) {
   x.o_lse = al256(size_t(N) * 4);
   x.o_grad = 2 * x.o_lse;
   x.o_patch = 3 * x.o_lse;
-  x.total = x.o_patch + al256(size_t(N) * K * 2);
+  x.total = x.o_patch + al256(size_t(N) * K * 4);
   return x;
 }
 
@@ -762,7 +765,7 @@ cudaError_t launch_distill_grad_rows(const DistillGrad& d, long long N, int V, f
 }
 
 cudaError_t launch_distill_patch(const int* hdr, const int* idx, long long c0, int C, int K, int V, long long ldz,
-                                 const int* ids, const uint16_t* patch, uint16_t* z, cudaStream_t s) {
+                                 const int* ids, const uint32_t* patch, uint16_t* z, cudaStream_t s) {
   const unsigned blocks = static_cast<unsigned>(std::min<long long>(cdiv(static_cast<long long>(C) * K, 256), 152 * 8));
   return launch_dependent(distill_patch_kernel, blocks, 256, s, hdr, idx, c0, C, K, V, ldz, ids, patch, z);
 }
@@ -900,8 +903,8 @@ flce_status flce_topk_distill(const void* hidden, const void* weight, const int3
 
 size_t flce_topk_distill_bwd_workspace_bytes(int64_t N, int64_t H, int64_t V, int32_t K, uint32_t flags) {
   if (sizes_bad(N, H, V) || K < 1 || K > MAX_TEACHER) return 0;
-  const size_t n = flce_logprobs_bwd_workspace_bytes(N, H, V, flags);
-  return n == 0 ? 0 : al256(n) + grad_extra(N, K).total;
+  const size_t extra = grad_extra(N, K).total, n = distill_grad_bytes(N, H, V, flags, al256(size_t(N) * K * 2));
+  return n == 0 ? 0 : al256(n) + extra;
 }
 
 flce_status flce_topk_distill_bwd(const void* hidden, const void* weight, const int32_t* teacher_ids,
@@ -924,7 +927,7 @@ flce_status flce_topk_distill_bwd(const void* hidden, const void* weight, const 
   d.targets = at<int>(workspace, own + x.o_targets);
   d.lse = at<float>(workspace, own + x.o_lse);
   d.grad = at<float>(workspace, own + x.o_grad);
-  d.patch = at<uint16_t>(workspace, own + x.o_patch);
+  d.patch = at<uint32_t>(workspace, own + x.o_patch);
   d.logp = teacher_logp; d.tail = tail; d.lse_in = lse; d.rest_logp = rest_logp; d.student_logp = student_logp;
   d.grad_kl = grad_kl;
   return run_distill_grad(d, hidden, weight, N, H, V, flags, temperature, grad_hidden, grad_weight, workspace, own,

@@ -34,6 +34,10 @@
 //                logits stored (LISTED_SLABS).
 //   MODE_DZ      z = Xc W^T once more, turned in registers into the gradient
 //                of the logits (bf16) that MODE_BWD consumes.
+//                With two parts (GemmArgs::two) the first rounding's remainder
+//                is stored as bf16 too, C rows further on, and MODE_BWD takes
+//                every K block once per part: dz counts with 2^-16 of itself
+//                instead of 2^-8, for twice the products.
 //                Both take long sums over H in segments, see below.
 //
 // Each tile is 256 x 256 and is computed by a CTA pair (a cluster of two CTAs
@@ -613,7 +617,9 @@ __device__ __forceinline__ void epi_stats(const GemmArgs& a, const Shape& s, con
 // Gradient of 32 logits of one row, written as bf16 once: of the fp32
 // accumulator, so the only rounding before the consuming GEMMs is that of dz
 // itself (relative 2^-9).  j0: the block's first column in the row's window of
-// ncol, whose target is column tl.
+// ncol, whose target is column tl.  TWO: what that rounding leaves goes, as
+// bf16, to dst + C ldz.
+template <bool TWO>
 __device__ __forceinline__ void dz32(const GemmArgs& a, float (&v)[32], const DzRow& q, bool entropy, int tl, int j0,
                                      int ncol, bool store, uint16_t* dst) {
   const uint64_t cc = ptx::pack2(a.c2, a.c2), bb = ptx::pack2(-q.lse2, -q.lse2);
@@ -648,6 +654,15 @@ __device__ __forceinline__ void dz32(const GemmArgs& a, float (&v)[32], const Dz
     for (int k = 0; k < 16; ++k) pk[k] = ptx::pack_bf16x2(v[2 * k], v[2 * k + 1]);
     ptx::st_global_v8(dst, pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6], pk[7]);
     ptx::st_global_v8(dst + 16, pk[8], pk[9], pk[10], pk[11], pk[12], pk[13], pk[14], pk[15]);
+    if constexpr (TWO) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        pk[k] = ptx::pack_bf16x2(v[2 * k] - __uint_as_float(pk[k] << 16),
+                                 v[2 * k + 1] - __uint_as_float(pk[k] & 0xffff0000u));
+      uint16_t* rest = dst + static_cast<size_t>(a.C) * a.ldz;
+      ptx::st_global_v8(rest, pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6], pk[7]);
+      ptx::st_global_v8(rest + 16, pk[8], pk[9], pk[10], pk[11], pk[12], pk[13], pk[14], pk[15]);
+    }
   }
 }
 
@@ -655,6 +670,7 @@ __device__ __forceinline__ void dz32(const GemmArgs& a, float (&v)[32], const Dz
 // are written too (as zeros, their constants being zero): the grad_weight GEMM
 // reads them.  4096 tokens at 2048 x 32000: 299 us, 1.80 PFLOP/s, 262 MB of dz
 // written meanwhile.
+template <bool TWO>
 __device__ __forceinline__ void epi_dz(const GemmArgs& a, const Shape& s, const Unit& t, int row0, int col0,
                                        uint32_t tbase, int r) {
   const int grow = row0 + r;
@@ -671,7 +687,7 @@ __device__ __forceinline__ void epi_dz(const GemmArgs& a, const Shape& s, const 
   for (int j = 0; j < GROUP_COLS / 32; ++j) {
     float v[32];
     ptx::tmem_ld32(tbase + j * 32, v);
-    dz32(a, v, q, entropy, tl, j * 32, ncol, rw && c0 + j * 32 < a.ldz, zrow + j * 32);
+    dz32<TWO>(a, v, q, entropy, tl, j * 32, ncol, rw && c0 + j * 32 < a.ldz, zrow + j * 32);
   }
 }
 
@@ -767,6 +783,7 @@ __device__ __forceinline__ bool epi_stats_seg(const GemmArgs& a, const Shape& s,
   return true;
 }
 
+template <bool TWO>
 __device__ __forceinline__ void epi_dz_seg(const GemmArgs& a, const Shape& s, const Unit& t, int row0, int grp,
                                            float (&z)[2][32], int r) {
   const int grow = row0 + r;
@@ -780,7 +797,8 @@ __device__ __forceinline__ void epi_dz_seg(const GemmArgs& a, const Shape& s, co
   uint16_t* zrow = a.z + static_cast<size_t>(grow) * a.ldz + c0;
   const bool entropy = __any_sync(0xffffffffu, q.b != 0.f);
 #pragma unroll
-  for (int j = 0; j < 2; ++j) dz32(a, z[j], q, entropy, tl, j * 32, ncol, rw && c0 + j * 32 < a.ldz, zrow + j * 32);
+  for (int j = 0; j < 2; ++j)
+    dz32<TWO>(a, z[j], q, entropy, tl, j * 32, ncol, rw && c0 + j * 32 < a.ldz, zrow + j * 32);
 }
 
 __device__ __forceinline__ void store_bf16_row(uint16_t* dst, const float* v, int h, int H) {
@@ -1000,16 +1018,21 @@ __device__ __forceinline__ bool epi_dx_split(const GemmArgs& a, const Shape& s, 
 // What a kernel is for: the loss, or the two modes of the token log
 // probabilities (MODE_STATS, MODE_DZ), whose kernels of their own leave the
 // loss kernel's registers alone; SEGMENTED those with long sums.
-// LISTED, SLABS: MODE_STATS of rows with lists, in both forms.
+// LISTED, SLABS: MODE_STATS of rows with lists, in both forms.  TWO: MODE_DZ and
+// MODE_BWD with dz in two parts.
 enum Kind : int {
-  K_LOSS = 0, K_PROBS = 1, K_SEGMENTED = 2, K_LISTED = 3, K_LISTED_SEGMENTED = 4, K_SLABS = 5, K_SLABS_SEGMENTED = 6
+  K_LOSS = 0, K_PROBS = 1, K_SEGMENTED = 2, K_LISTED = 3, K_LISTED_SEGMENTED = 4, K_SLABS = 5, K_SLABS_SEGMENTED = 6,
+  K_TWO_DZ = 7, K_TWO_DZ_SEGMENTED = 8, K_TWO_BWD = 9
 };
 
 template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     flce_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
-  constexpr bool PROBS = KIND != K_LOSS;
-  constexpr bool SEG = KIND == K_SEGMENTED || KIND == K_LISTED_SEGMENTED || KIND == K_SLABS_SEGMENTED;
+  constexpr bool PROBS = KIND != K_LOSS && KIND != K_TWO_BWD;
+  constexpr bool SEG =
+      KIND == K_SEGMENTED || KIND == K_LISTED_SEGMENTED || KIND == K_SLABS_SEGMENTED || KIND == K_TWO_DZ_SEGMENTED;
+  constexpr bool TWO_DZ = KIND == K_TWO_DZ || KIND == K_TWO_DZ_SEGMENTED;
+  constexpr int PARTS = KIND == K_TWO_BWD ? 2 : 1;   // steps of a tile per K block
   constexpr int LISTED = KIND == K_LISTED || KIND == K_LISTED_SEGMENTED ? LISTED_OUT
                          : (KIND == K_SLABS || KIND == K_SLABS_SEGMENTED ? LISTED_SLABS : 0);
   extern __shared__ uint8_t smem_raw[];
@@ -1123,7 +1146,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       if (u < 0) break;
       const Unit t = decode_unit<PROBS>(a, s, u);
       if (!PROBS && lead && t.kb1 - t.kb0 <= SHORT_TILE_KB) next = atomicAdd(a.counter, 1);
-      for (int kb = t.kb0; kb < t.kb1; ++kb) {
+      for (int step = t.kb0 * PARTS; step < t.kb1 * PARTS; ++step) {
+        const int kb = step / PARTS, part = PARTS > 1 && (step & 1) ? a.C : 0;   // rows of dz further on
         if (!wait_stage(&ctl->empty[stage], phase ^ 1u, ctl, to, hdr, W_STAGE_EMPTY, u | (stage << 24))) { ok = false; break; }
         uint8_t* sa = smem + stage * STAGE_BYTES;
         uint8_t* sb = sa + A_BYTES;
@@ -1134,14 +1158,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           ptx::tma_load_2d_pair(sa, &maps.a0, fb, k0, t.m0 + half);      // Xc rows, cols k0..
           ptx::tma_load_2d_pair(sb, &maps.b0, fb, k0, t.n0 + half);      // W rows (vocab), cols k0..
         } else if (t.kind == U_DX) {
-          ptx::tma_load_2d_pair(sa, &maps.a0, fb, k0, t.m0 + half);      // dz rows, vocab k0..
+          ptx::tma_load_2d_pair(sa, &maps.a0, fb, k0, part + t.m0 + half);   // dz rows, vocab k0..
 #pragma unroll
           for (int j = 0; j < BN / 128; ++j)                              // W rows k0.., cols n0+half+64j
             ptx::tma_load_2d_pair(sb + j * MN_BLOCK_BYTES, &maps.b0, fb, t.n0 + half + 64 * j, k0);
         } else {
 #pragma unroll
           for (int j = 0; j < BM / 64; ++j)                               // dz rows k0.., vocab m0+half+64j
-            ptx::tma_load_2d_pair(sa + j * MN_BLOCK_BYTES, &maps.a1, fb, t.m0 + half + 64 * j, k0);
+            ptx::tma_load_2d_pair(sa + j * MN_BLOCK_BYTES, &maps.a1, fb, t.m0 + half + 64 * j, part + k0);
 #pragma unroll
           for (int j = 0; j < BN / 128; ++j)                              // Xc rows k0.., cols n0+half+64j
             ptx::tma_load_2d_pair(sb + j * MN_BLOCK_BYTES, &maps.b1, fb, t.n0 + half + 64 * j, k0);
@@ -1179,9 +1203,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       const uint32_t a_lbo = a_mn ? MN_BLOCK_BYTES : 16, b_lbo = b_mn ? MN_BLOCK_BYTES : 16;
       const uint32_t a_kstep = a_mn ? 16 * 128 : 32, b_kstep = b_mn ? 16 * 128 : 32;
       bool ok = true;
-      int kb = t.kb0;
+      int kb = t.kb0 * PARTS;   // (as the producer's steps)
+      const int kb_end = t.kb1 * PARTS;
       do {   // one accumulator: the whole sum, or a segment of it
-        const int kb0 = kb, kb1 = SEG ? min(t.kb1, kb0 + a.seg_kb) : t.kb1;
+        const int kb0 = kb, kb1 = SEG ? min(kb_end, kb0 + a.seg_kb) : kb_end;
         // (between segments the wait is on the issuer's path: in line)
         if (SEG ? !wait_stage(&ctl->tempty[acc], acc_phase ^ 1u, ctl, to, hdr, W_TMEM_EMPTY, u | (acc << 24))
                 : !wait_phase(&ctl->tempty[acc], acc_phase ^ 1u, ctl, to, true, hdr, W_TMEM_EMPTY, u | (acc << 24))) { ok = false; break; }
@@ -1212,7 +1237,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         withhold = false;
         acc ^= 1u;
         if (acc == 0) acc_phase ^= 1u;
-      } while (SEG && kb < t.kb1);
+      } while (SEG && kb < kb_end);
       if (!ok) break;
     }
     ptx::umma_commit_pair(&ctl->mma_done, 0x1);
@@ -1255,12 +1280,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         if (acc == 0) acc_phase ^= 1u;
       }
       const int row0 = t.m0 + half;
-      if (LISTED != 0 || a.mode == MODE_STATS) {
+      if (!TWO_DZ && (LISTED != 0 || a.mode == MODE_STATS)) {
         ok = epi_stats_seg<LISTED>(a, s, t, row0, grp, z, r, ok, ex->v[buf], EPI_BAR_SET + static_cast<uint32_t>(grp / 2),
                                    pl);
         buf ^= 1u;
       } else if (ok) {
-        epi_dz_seg(a, s, t, row0, grp, z, r);
+        epi_dz_seg<TWO_DZ>(a, s, t, row0, grp, z, r);
       }
       if (!ok) break;
     }
@@ -1329,8 +1354,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       const int row0 = t.m0 + half;
       bool cont = true;
       if constexpr (PROBS) {
-        if (LISTED != 0 || a.mode == MODE_STATS) epi_stats<LISTED>(a, s, t, row0, col0, tbase, r, pl);
-        else epi_dz(a, s, t, row0, col0, tbase, r);
+        if (!TWO_DZ && (LISTED != 0 || a.mode == MODE_STATS)) epi_stats<LISTED>(a, s, t, row0, col0, tbase, r, pl);
+        else epi_dz<TWO_DZ>(a, s, t, row0, col0, tbase, r);
       } else if (t.kind == U_LOGITS)
         epi_logits(a, s, t, row0, col0, tbase, r);
       else if (t.kind == U_DX && a.splits == 1)
@@ -1368,19 +1393,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 int gemm_smem_bytes() { return SMEM_BYTES; }
 
 cudaError_t gemm_prepare(int /*device*/) {
-  cudaError_t e = cudaFuncSetAttribute(flce_gemm_kernel<K_LOSS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(flce_gemm_kernel<K_PROBS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(flce_gemm_kernel<K_SEGMENTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(flce_gemm_kernel<K_LISTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(flce_gemm_kernel<K_LISTED_SEGMENTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(flce_gemm_kernel<K_SLABS>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(flce_gemm_kernel<K_SLABS_SEGMENTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  cudaError_t e = cudaSuccess;
+  auto allow = [&](auto* kernel) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  };
+  allow(flce_gemm_kernel<K_LOSS>);
+  allow(flce_gemm_kernel<K_PROBS>);
+  allow(flce_gemm_kernel<K_SEGMENTED>);
+  allow(flce_gemm_kernel<K_LISTED>);
+  allow(flce_gemm_kernel<K_LISTED_SEGMENTED>);
+  allow(flce_gemm_kernel<K_SLABS>);
+  allow(flce_gemm_kernel<K_SLABS_SEGMENTED>);
+  allow(flce_gemm_kernel<K_TWO_DZ>);
+  allow(flce_gemm_kernel<K_TWO_DZ_SEGMENTED>);
+  allow(flce_gemm_kernel<K_TWO_BWD>);
   return e;
 }
 
@@ -1417,6 +1443,10 @@ cudaError_t launch_gemm(const GemmArgs& a, const GemmMaps& m, int grid, cudaStre
   if (a.mode == MODE_STATS && a.listed == LISTED_OUT)
     return launch_result(a.seg_kb * BK < a.H ? cudaLaunchKernelEx(&cfg, flce_gemm_kernel<K_LISTED_SEGMENTED>, m, a)
                                              : cudaLaunchKernelEx(&cfg, flce_gemm_kernel<K_LISTED>, m, a));
+  if (a.two && a.mode == MODE_DZ)
+    return launch_result(a.seg_kb * BK < a.H ? cudaLaunchKernelEx(&cfg, flce_gemm_kernel<K_TWO_DZ_SEGMENTED>, m, a)
+                                             : cudaLaunchKernelEx(&cfg, flce_gemm_kernel<K_TWO_DZ>, m, a));
+  if (a.two && a.mode == MODE_BWD) return launch_result(cudaLaunchKernelEx(&cfg, flce_gemm_kernel<K_TWO_BWD>, m, a));
   if (a.mode == MODE_STATS || a.mode == MODE_DZ)
     return launch_result(a.seg_kb * BK < a.H ? cudaLaunchKernelEx(&cfg, flce_gemm_kernel<K_SEGMENTED>, m, a)
                                            : cudaLaunchKernelEx(&cfg, flce_gemm_kernel<K_PROBS>, m, a));

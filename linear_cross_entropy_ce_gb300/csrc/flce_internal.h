@@ -98,6 +98,7 @@ struct GemmArgs {
   int skip;             // BWD: SKIP_DX, SKIP_DW
   int slabs;            // BWD, splits > 1: each split stores its fp32 part to dxacc + split C H
                         // (dx_reduce adds them) instead of adding onto the previous one
+  int two;              // DZ, BWD: dz in two bf16 parts, the second C rows behind the first
   int gw_bf16;          // BWD of a call with one chunk: grad_weight tiles are rounded and stored as bf16
   float c2;             // log2(e) / temperature: z c2 is the scaled logit in base-2 units
   float* stats;         // STATS: [3][nparts][C] part max (raw z), sum of 2^d, sum of d 2^d, d = (z - max) c2
@@ -305,11 +306,11 @@ struct DistillGrad {
   const float *lse_in, *rest_logp, *student_logp, *grad_kl;
   int* targets;                   // made from these
   float *lse, *grad;
-  uint16_t* patch;                // [N][K] dz at the teacher's tokens, bf16
+  uint32_t* patch;                // [N][K] dz at the teacher's tokens, both bf16 parts (the first in the low half)
 };
 cudaError_t launch_distill_grad_rows(const DistillGrad& d, long long N, int V, float temperature, cudaStream_t s);
 cudaError_t launch_distill_patch(const int* hdr, const int* idx, long long c0, int C, int K, int V, long long ldz,
-                                 const int* ids, const uint16_t* patch, uint16_t* z, cudaStream_t s);
+                                 const int* ids, const uint32_t* patch, uint16_t* z, cudaStream_t s);
 cudaError_t constrained_prepare();
 // The time limit and the tensor maps of a streaming call.
 bool stream_setup(StreamArgs* a, StreamMaps* m, const void* hidden, const void* weight, int seg_kb);

@@ -15,7 +15,9 @@
 namespace flce {
 
 // flce_api.cu: the gradients of the log probabilities' call with a
-// distillation's row constants.
+// distillation's row constants, and dz in two parts.  Its workspace by default:
+// `reserve` less than that call's where this is not one chunk of all rows.
+size_t distill_grad_bytes(int64_t N, int64_t H, int64_t V, uint32_t flags, size_t reserve);
 flce_status run_distill_grad(const DistillGrad& d, const void* hidden, const void* weight, int64_t N, int64_t H,
                              int64_t V, uint32_t flags, float temperature, void* grad_hidden, float* grad_weight,
                              void* workspace, size_t workspace_bytes, void* stream);
