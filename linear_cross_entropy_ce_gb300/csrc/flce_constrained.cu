@@ -292,8 +292,8 @@ __global__ void __launch_bounds__(32 * ROW_WARPS) constrained_rows_kernel(const 
     Stat mine = {m, 0.f, 0.f};
 #pragma unroll 4
     for (int e = sub * 32 + lane; e < n; e += 32 * ROW_SHARES) {   // what this lane has written
-      const float y = (a.lists.z[at + e] - m) * a.c2;              // NaN where all are -inf: no term
-      const float x = m == -INFINITY && y != y ? 0.f : ptx::ex2(y);
+      const float z = a.lists.z[at + e], y = (z - m) * a.c2;
+      const float x = z == -INFINITY ? 0.f : ptx::ex2(y);          // (where all are -inf, y is not a number)
       mine.s += x;
       mine.d = fmaf(fmaxf(y, -1e30f), x, mine.d);
     }
