@@ -421,6 +421,12 @@ __global__ void __launch_bounds__(256) all_rows_kernel(int* targets, long long N
 // loses: 1307 of 1024 at 753 92.6 and 95.3, 4096 of 200 at 4000 73.9 and 76.9.  Two
 // kernels, as one with the choice at run time costs short histories as much.
 constexpr int MAX_COUNTS = 8192, LONG_HISTORY = 1280;
+// Ids (of history and biases) times windows up to which the streaming kernel comes
+// up while the lists are made: its waits, which are limited, then last as long as
+// that takes, 0.8 to 1.2 ns an id and window (1.2 ms here).  Side by side saves 4 to
+// 16 us: 64 ids at 512 x 600000 128 us, one after the other 144; 2^18 ids 781 and
+// 785, 2^20 2422 and 2426.
+constexpr long long LISTS_BESIDE = 1ll << 20;
 size_t rule_smem(long long V, int threads, int counts) {
   return size_t(pad_words(static_cast<int>(std::min<long long>(cdiv(V, 32), HELD * threads)))) * 8 + size_t(counts) * 4;
 }
@@ -576,7 +582,8 @@ flce_status flce_constrained_logprobs(const void* hidden, const void* weight, co
     lists<<<static_cast<unsigned>(N), STREAM_THREADS, rule_smem(V, STREAM_THREADS, la.counts), st>>>(la);
     if (!ok(launch_result(cudaGetLastError()))) return FLCE_ECUDA;
     const ProfScope prof = prof_launch_begin(st);
-    const cudaError_t e = launch_stream_ruled(a, m, l, st);
+    const long long windows = cdiv(cdiv(V, 32), HELD * STREAM_THREADS);
+    const cudaError_t e = launch_stream_ruled(a, m, l, (L + B) * windows <= LISTS_BESIDE, st);
     prof_launch_end(prof, MODE_STATS, st);
     return ok(e) ? FLCE_OK : FLCE_ECUDA;
   }

@@ -261,10 +261,11 @@ cudaError_t embedding_prepare();   // flce_embedding.cu
 cudaError_t launch_stream(const StreamArgs& a, const StreamMaps& m, cudaStream_t s);
 // The same with the listed tokens of each row under rules (flce_stream_ruled.cu),
 // and the kernel alone with them taken out (flce_stream_taken.cu); both are
-// launched while the kernel that makes the lists runs.
+// launched while the kernel that makes the lists runs, unless `beside` is false.
 cudaError_t stream_ruled_prepare();
 cudaError_t stream_taken_prepare();
-cudaError_t launch_stream_ruled(const StreamArgs& a, const StreamMaps& m, const StreamLists& l, cudaStream_t s);
+cudaError_t launch_stream_ruled(const StreamArgs& a, const StreamMaps& m, const StreamLists& l, bool beside,
+                                cudaStream_t s);
 cudaError_t launch_stream_taken(const StreamArgs& a, const StreamMaps& m, const StreamLists& l, cudaStream_t s);
 
 // Token log probabilities (flce_logprobs.cu).
