@@ -381,8 +381,10 @@ flce_status flce_constrained_logprobs(const void* hidden, const void* weight,
  * A row without an entry gets 0 in all of them; one that names a token of V or
  * more gets NaN and sets FLCE_EBADTARGET.  After a time-out every row with a
  * teacher is NaN.  log q and log s are formed relative to the row's largest
- * logit and s not as a difference, so that kl is off by a few 2^-24 of its
- * largest term only.
+ * logit and s not as a difference, so that for given logits kl is off by a few
+ * 2^-24 of the sum of its terms' magnitudes, however small it is itself (logits
+ * that are exact, student and teacher nearly agreeing: 5e-8 at the median).  The
+ * logits' own rounding, in fp32, adds 6e-7 to 2e-6 of kl's norm.
  * Workspace (flce_topk_distill_workspace_bytes): as flce_logprobs without
  * alternatives and 14 bytes per entry; up to 128 tokens 4 bytes per row and tile
  * of the vocabulary, beyond 2 bytes per row and 128 of its tokens and 512 bytes
