@@ -56,9 +56,11 @@ inline ListedPlan listed_layout(const ListedSizes& q, long long C) {
   p.o_targets = take(size_t(q.N) * 4);
   p.o_xc = take(size_t(C) * q.H * 2);
   p.o_tc = take(size_t(C) * 4);
-  p.o_zt = take(size_t(C) * 4);
-  p.o_ml = take(size_t(C) * 8);
-  p.o_stats = take(size_t(C) * p.nparts * 12);
+  // slabs leave max and sum of a part only, and pick no target
+  const bool slabs = q.table == 2;
+  p.o_zt = take(slabs ? 0 : size_t(C) * 4);
+  p.o_ml = take(q.K > 0 ? size_t(C) * 8 : 0);
+  p.o_stats = take(size_t(C) * p.nparts * (slabs ? 8 : 12));
   if (q.K > 0) {
     p.o_bound = take(size_t(C) * 4);
     p.o_group = take(size_t(C) * p.group_stride * 4);
@@ -113,7 +115,6 @@ struct ListedCall {
 
 struct ListedChunk {
   long long c0;
-  bool last, only;          // the last chunk; the only one, whose rows the front kernel has gathered
   const GemmArgs* g;
 };
 
@@ -145,7 +146,7 @@ flce_status listed_chunks(const ListedPlan& p, const ListedCall& c, const Device
   g.nparts = p.nparts;
   g.timeout_ns = wait_timeout_ns();
   g.tc = at<int>(ws, p.o_tc);
-  g.zt = at<float>(ws, p.o_zt);
+  g.zt = q.table == 4 ? at<float>(ws, p.o_zt) : nullptr;
   g.idx = at<int>(ws, p.o_idx);
   g.stats = at<float>(ws, p.o_stats);
   g.K = q.K;
@@ -162,7 +163,6 @@ flce_status listed_chunks(const ListedPlan& p, const ListedCall& c, const Device
   g.slab_by_token = c.by_token;
   g.slabs_per_row = static_cast<int>(q.z / PART_COLS);
   g.lists.start = at<int>(ws, p.o_start);
-  g.lists.boundaries = p.nparts + 1;
   g.lists.id = at<int>(ws, p.o_id);
   g.lists.z = at<float>(ws, p.o_z);
   g.lists.cap = q.cap;
@@ -189,7 +189,7 @@ flce_status listed_chunks(const ListedPlan& p, const ListedCall& c, const Device
     if (launch_prep(c.targets, q.N, g.V, c.ii, hdr, idx, nullptr, nullptr, 0, c.st) != cudaSuccess) return FLCE_ECUDA;
   }
   for (long long i = 0; i < p.n_chunks; ++i) {
-    const ListedChunk ch{i * p.C, i == p.n_chunks - 1, front, &g};
+    const ListedChunk ch{i * p.C, &g};
     g.c0 = ch.c0;
     if (!front && launch_gather(static_cast<const uint16_t*>(c.hidden), c.targets, hdr, idx, g.c0, g.C, g.H, xc,
                                 at<int>(ws, p.o_tc), 0, g.V, c.st) != cudaSuccess)

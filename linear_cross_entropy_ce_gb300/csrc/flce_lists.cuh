@@ -17,7 +17,7 @@ namespace flce {
 struct ListView {
   const int* start;        // entries before each boundary: [boundaries][C] for the chunked form (one every 128
                            // columns, and the end), [rows][boundaries] for the streaming form (one a tile, and the end)
-  int boundaries;
+  int boundaries;          // of the streaming form
   const int* id;           // [rows][cap] ascending, each token once
   float* z;                // [rows][cap] their logits, left out of the statistics
   long long cap;
