@@ -459,8 +459,12 @@ struct RowsArgs {
 // tokens; SHARES warps a row go through the other parts' logits meanwhile: the
 // listed ones aside, the others into statistics of their own.  Then a warp a row
 // puts it all together.  All of it is loads (5735 rows of 32 entries over 2001
-// parts: 230 MB, 57 us).  Long lists get three warps a row (724 rows of 100
-// entries 24 us, with one 140), short ones one, and two blocks an SM.
+// parts: 230 MB, 57 us).  Three warps a row where the blocks are one wave and there
+// is something to share, else one, and two blocks an SM: calls at H = 64 with one
+// and three, 1152 rows at a vocabulary of 60000 with lists of 8, 32, 64, 200: 51, 57,
+// 69, 127 and 51, 56, 64, 106 us; 1280 rows 52, 60, 71, 136 and 56, 63, 75, 142; 300
+// rows at 16000 28, 34, 40, 69 and 28, 32, 36, 60; 2048 rows 38, 44, 54, 110 and 43,
+// 48, 58, 118.
 template <int SHARES>
 __global__ void __launch_bounds__(32 * ROWS8 * (1 + SHARES)) distill_rows_kernel(const RowsArgs a) {
   __shared__ Stat part[32][ROWS8];
@@ -890,8 +894,9 @@ flce_status flce_topk_distill(const void* hidden, const void* weight, const int3
         count_launches(1);
         const unsigned blocks = static_cast<unsigned>(cdiv(ch.g->C, ROWS8));
         const size_t smem = rows_smem(K, ch.g->slabs_per_row);
-        return K <= 32 ? launch_dependent_smem(distill_rows_kernel<1>, blocks, 32 * ROWS8 * 2, smem, st, ra)
-                       : launch_dependent_smem(distill_rows_kernel<3>, blocks, 32 * ROWS8 * 4, smem, st, ra);
+        return blocks > static_cast<unsigned>(dev.sms) || ch.g->slabs_per_row < 16
+                   ? launch_dependent_smem(distill_rows_kernel<1>, blocks, 32 * ROWS8 * 2, smem, st, ra)
+                   : launch_dependent_smem(distill_rows_kernel<3>, blocks, 32 * ROWS8 * 4, smem, st, ra);
       });
   if (s == FLCE_OK && p.n_chunks > 1) {
     count_launches(1);
