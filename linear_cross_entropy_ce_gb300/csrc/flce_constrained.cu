@@ -415,11 +415,18 @@ __global__ void __launch_bounds__(256) all_rows_kernel(int* targets, long long N
 
 // Histories of LONG_HISTORY ids and more have their times counted in shared
 // memory, for the first MAX_COUNTS listed tokens of a window; the others' go to L2.
-// Calls with the atomics in L2 and in shared memory: 2000 rows of 6000 ids at a
-// vocabulary of 16000 441 and 375 us, 2000 of 4000 at 8000 281 and 232, 1024 of
-// 1500 at 16000 89.5 and 86.6, 1307 of 1359 at 753 102.4 and 103.1; below that it
-// loses: 1307 of 1024 at 753 92.6 and 95.3, 4096 of 200 at 4000 73.9 and 76.9.  Two
-// kernels, as one with the choice at run time costs short histories as much.
+// Calls at H = 64, ids of a Zipf distribution, in L2 and in shared memory, us:
+//   rows x vocabulary   300 ids       1280          4000          16000
+//   1 x 4000            21.6   18.6   22.7   19.6   25.1   23.7   36.0   33.9
+//   1 x 128256          25.7   25.7   25.7   25.7   27.7   27.7   42.1   35.9
+//   128 x 128256        72.8   72.8   81.0   83.0   87.2   85.1   108.6  96.4
+//   300 x 16000         32.9   33.9   41.1   41.1   58.5   52.3   121.9  93.3
+//   2048 x 4000         48.2   48.3   74.8   66.7   146.7  111.7  287.9  194.7
+//   2048 x 16000        87.1   91.2   111.8  113.8  181.4  156.8  318.6  222.3
+//   2048 x 128256       260.2  263.3  320.6  323.7  418.9  400.5  539.7  443.5
+// Around the border both are within 3% of each other but for few rows at a very small
+// vocabulary (1 x 753: 25.7 and 27.8 at 1280, 37.0 and 36.0 at 16000).  Two kernels,
+// as one with the choice at run time costs short histories as much.
 constexpr int MAX_COUNTS = 8192, LONG_HISTORY = 1280;
 // Ids (of history and biases) times windows up to which the streaming kernel comes
 // up while the lists are made: its waits, which are limited, then last as long as
