@@ -36,8 +36,8 @@
 //                of the logits (bf16) that MODE_BWD consumes.
 //                With two parts (GemmArgs::two) the first rounding's remainder
 //                is stored as bf16 too, C rows further on, and MODE_BWD takes
-//                every K block once per part: dz counts with 2^-16 of itself
-//                instead of 2^-8, for twice the products.
+//                both parts of a K block one after the other: 2^-16 of dz is
+//                lost instead of 2^-8, for twice the products.
 //                Both take long sums over H in segments, see below.
 //
 // Each tile is 256 x 256 and is computed by a CTA pair (a cluster of two CTAs
@@ -1032,7 +1032,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   constexpr bool SEG =
       KIND == K_SEGMENTED || KIND == K_LISTED_SEGMENTED || KIND == K_SLABS_SEGMENTED || KIND == K_TWO_DZ_SEGMENTED;
   constexpr bool TWO_DZ = KIND == K_TWO_DZ || KIND == K_TWO_DZ_SEGMENTED;
-  constexpr int PARTS = KIND == K_TWO_BWD ? 2 : 1;   // steps of a tile per K block
+  // Both parts of dz are in one stage with the block of the other operand, which
+  // is loaded once for the two.
+  constexpr bool TWO_BWD = KIND == K_TWO_BWD;
+  constexpr int A_PARTS = TWO_BWD ? 2 : 1;
+  constexpr int STAGE = A_PARTS * A_BYTES + B_BYTES;
   constexpr int LISTED = KIND == K_LISTED || KIND == K_LISTED_SEGMENTED ? LISTED_OUT
                          : (KIND == K_SLABS || KIND == K_SLABS_SEGMENTED ? LISTED_SLABS : 0);
   extern __shared__ uint8_t smem_raw[];
@@ -1104,7 +1108,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   // tile).  The others are claimed from a counter.
   const int pair0 = static_cast<int>(blockIdx.x / 2), npairs = static_cast<int>(gridDim.x / 2);
   // (segmented statistics exchange through the staging area)
-  const uint32_t nstages = (PROBS || a.mode == MODE_LOGITS) && !(SEG && a.mode == MODE_STATS) ? STAGES_LOGITS : STAGES;
+  const uint32_t nstages = TWO_BWD ? STAGES * STAGE_BYTES / STAGE : (PROBS || a.mode == MODE_LOGITS) && !(SEG && a.mode == MODE_STATS) ? STAGES_LOGITS : STAGES;
 
   if (warp == 0 && lane == 0) {
     // ---------------- (CTA 0: scheduler +) TMA producer ----------------
@@ -1146,26 +1150,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       if (u < 0) break;
       const Unit t = decode_unit<PROBS>(a, s, u);
       if (!PROBS && lead && t.kb1 - t.kb0 <= SHORT_TILE_KB) next = atomicAdd(a.counter, 1);
-      for (int step = t.kb0 * PARTS; step < t.kb1 * PARTS; ++step) {
-        const int kb = step / PARTS, part = PARTS > 1 && (step & 1) ? a.C : 0;   // rows of dz further on
+      for (int kb = t.kb0; kb < t.kb1; ++kb) {
         if (!wait_stage(&ctl->empty[stage], phase ^ 1u, ctl, to, hdr, W_STAGE_EMPTY, u | (stage << 24))) { ok = false; break; }
-        uint8_t* sa = smem + stage * STAGE_BYTES;
-        uint8_t* sb = sa + A_BYTES;
+        uint8_t* sa = smem + stage * STAGE;
+        uint8_t* sb = sa + A_PARTS * A_BYTES;
         const uint32_t fb = full0 + stage * 8u;                        // CTA 0's barrier of this stage
-        if (lead) ptx::mbar_arrive_expect_tx(&ctl->full[stage], 2 * STAGE_BYTES);
+        if (lead) ptx::mbar_arrive_expect_tx(&ctl->full[stage], 2 * STAGE);
         const int k0 = kb * BK;
         if (t.kind == U_LOGITS) {
           ptx::tma_load_2d_pair(sa, &maps.a0, fb, k0, t.m0 + half);      // Xc rows, cols k0..
           ptx::tma_load_2d_pair(sb, &maps.b0, fb, k0, t.n0 + half);      // W rows (vocab), cols k0..
         } else if (t.kind == U_DX) {
-          ptx::tma_load_2d_pair(sa, &maps.a0, fb, k0, part + t.m0 + half);   // dz rows, vocab k0..
+#pragma unroll
+          for (int p = 0; p < A_PARTS; ++p)                               // dz rows, vocab k0..
+            ptx::tma_load_2d_pair(sa + p * A_BYTES, &maps.a0, fb, k0, p * a.C + t.m0 + half);
 #pragma unroll
           for (int j = 0; j < BN / 128; ++j)                              // W rows k0.., cols n0+half+64j
             ptx::tma_load_2d_pair(sb + j * MN_BLOCK_BYTES, &maps.b0, fb, t.n0 + half + 64 * j, k0);
         } else {
 #pragma unroll
-          for (int j = 0; j < BM / 64; ++j)                               // dz rows k0.., vocab m0+half+64j
-            ptx::tma_load_2d_pair(sa + j * MN_BLOCK_BYTES, &maps.a1, fb, t.m0 + half + 64 * j, part + k0);
+          for (int p = 0; p < A_PARTS; ++p)
+#pragma unroll
+            for (int j = 0; j < BM / 64; ++j)                             // dz rows k0.., vocab m0+half+64j
+              ptx::tma_load_2d_pair(sa + p * A_BYTES + j * MN_BLOCK_BYTES, &maps.a1, fb, t.m0 + half + 64 * j,
+                                    p * a.C + k0);
 #pragma unroll
           for (int j = 0; j < BN / 128; ++j)                              // Xc rows k0.., cols n0+half+64j
             ptx::tma_load_2d_pair(sb + j * MN_BLOCK_BYTES, &maps.b1, fb, t.n0 + half + 64 * j, k0);
@@ -1203,10 +1211,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       const uint32_t a_lbo = a_mn ? MN_BLOCK_BYTES : 16, b_lbo = b_mn ? MN_BLOCK_BYTES : 16;
       const uint32_t a_kstep = a_mn ? 16 * 128 : 32, b_kstep = b_mn ? 16 * 128 : 32;
       bool ok = true;
-      int kb = t.kb0 * PARTS;   // (as the producer's steps)
-      const int kb_end = t.kb1 * PARTS;
+      int kb = t.kb0;
       do {   // one accumulator: the whole sum, or a segment of it
-        const int kb0 = kb, kb1 = SEG ? min(kb_end, kb0 + a.seg_kb) : kb_end;
+        const int kb0 = kb, kb1 = SEG ? min(t.kb1, kb0 + a.seg_kb) : t.kb1;
         // (between segments the wait is on the issuer's path: in line)
         if (SEG ? !wait_stage(&ctl->tempty[acc], acc_phase ^ 1u, ctl, to, hdr, W_TMEM_EMPTY, u | (acc << 24))
                 : !wait_phase(&ctl->tempty[acc], acc_phase ^ 1u, ctl, to, true, hdr, W_TMEM_EMPTY, u | (acc << 24))) { ok = false; break; }
@@ -1215,8 +1222,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         for (; kb < kb1; ++kb) {
           if (!wait_stage(&ctl->full[stage], phase, ctl, to, hdr, W_STAGE_FULL, u | (stage << 24))) { ok = false; break; }
           ptx::tc_fence_after();
-          const uint32_t sa = ptx::smem_u32(smem + stage * STAGE_BYTES);
-          const uint32_t sb = sa + A_BYTES;
+          const uint32_t sa = ptx::smem_u32(smem + stage * STAGE);
+          const uint32_t sb = sa + A_PARTS * A_BYTES;
 #pragma unroll
           for (int kk = 0; kk < BK / 16; ++kk) {
             uint64_t ad, bd;
@@ -1228,6 +1235,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
               bd = ptx::smem_desc_sw128(sb + kk * b_kstep, b_lbo, 1024);
             }
             ptx::umma_bf16_pair(d_tmem, ad, bd, idesc, (kb > kb0 || kk > 0) ? 1u : 0u);
+            if constexpr (TWO_BWD) ptx::umma_bf16_pair(d_tmem, ad + A_BYTES / 16, bd, idesc, 1u);
           }
           ptx::umma_commit_pair(&ctl->empty[stage], PAIR_MASK);   // frees the slot in both CTAs
           if (++stage == nstages) { stage = 0; phase ^= 1u; }
@@ -1237,7 +1245,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         withhold = false;
         acc ^= 1u;
         if (acc == 0) acc_phase ^= 1u;
-      } while (SEG && kb < kb_end);
+      } while (SEG && kb < t.kb1);
       if (!ok) break;
     }
     ptx::umma_commit_pair(&ctl->mma_done, 0x1);
