@@ -88,9 +88,13 @@ __device__ __forceinline__ SortRow sort_scratch(int* p, int K) {
 // pair, K^2 / 16 a lane (64 entries 256), which no order of the entries makes
 // slower: lists and tables of 5735 rows of 32 over 2001 parts take 23 us, of 724
 // of 100 17.
+// Without a tail the log masses are made relative to the row's largest (exact, or
+// rounded to 2^-24 of the difference), so that logits which all are large, or log
+// probabilities of unlikely tokens alone, do not cost the masses' digits: sums of
+// theirs, rounded, would be off by 2^-24 of what they share.
 // SORT_GROUPS: 32s of entries, 1, 2, 4 or 8.
 template <int SORT_GROUPS>
-__device__ __forceinline__ int sort_row(const int* ids, const float* t, int K, int lane, const SortRow& s,
+__device__ __forceinline__ int sort_row(const int* ids, const float* t, int K, bool tail, int lane, const SortRow& s,
                                         int (&slot)[SORT_GROUPS]) {
   const int groups = (K + 31) / 32;
   unsigned x[SORT_GROUPS];
@@ -130,13 +134,23 @@ __device__ __forceinline__ int sort_row(const int* ids, const float* t, int K, i
       rank[e] += r;
     }
   }
+  float base = 0.f;
+  if (!tail) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < SORT_GROUPS; ++e)
+      if (e < groups && x[e] != NO_TOKEN) top = fmaxf(top, t[e * 32 + lane]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top > -INFINITY) base = top;
+  }
   int n = 0;
 #pragma unroll
   for (int e = 0; e < SORT_GROUPS; ++e) {
     const bool there = e < groups && x[e] != NO_TOKEN;
     if (there) {
       s.id[rank[e]] = static_cast<int>(x[e]);
-      s.t[rank[e]] = t[e * 32 + lane];
+      s.t[rank[e]] = t[e * 32 + lane] - base;
     }
     n += __popc(__ballot_sync(0xffffffffu, there));
   }
@@ -198,7 +212,7 @@ __device__ __forceinline__ int lower_bound(const int* id, int n, int x) {
 struct ListArgs {
   const int* teacher_ids;     // [N][K]
   const float* teacher_logp;
-  int K, V;
+  int K, V, tail;
   const int* hdr;             // chunked form
   const int* idx;             // null: lists of all N tokens, by token
   long long c0;
@@ -208,7 +222,7 @@ struct ListArgs {
   int ctas, max_tiles;        // streaming form
   int* start;
   int* id;                    // [rows][K]
-  float* t;                   // [rows][K] log masses of the sorted tokens
+  float* t;                   // [rows][K] log masses of the sorted tokens (without a tail, relative to the largest)
   short* slot;                // [rows][K] place of each given entry
 };
 
@@ -255,7 +269,7 @@ __global__ void __launch_bounds__(32 * LIST_WARPS)
     const long long row = r0 + w, from = (a.idx ? a.idx[a.c0 + row] : row) * a.K;
     const SortRow s = sort_scratch(smem + w * words, a.K);
     int slot[SORT_GROUPS];
-    const int n = sort_row(a.teacher_ids + from, a.teacher_logp + from, a.K, lane, s, slot);
+    const int n = sort_row(a.teacher_ids + from, a.teacher_logp + from, a.K, a.tail, lane, s, slot);
     store_row(a, row, s, n, slot, lane);
     short* slab = reinterpret_cast<short*>(smem + w * words + slabs_at);
     int q = -1;   // the last slab so far
@@ -306,7 +320,7 @@ __global__ void __launch_bounds__(STREAM_LIST_THREADS) distill_stream_lists_kern
   const SortRow s = sort_scratch(scratch, a.K);
   if (threadIdx.x < 32) {
     int slot[SORT_GROUPS];
-    const int n = sort_row(a.teacher_ids + from, a.teacher_logp + from, a.K, threadIdx.x, s, slot);
+    const int n = sort_row(a.teacher_ids + from, a.teacher_logp + from, a.K, a.tail, threadIdx.x, s, slot);
     store_row(a, blockIdx.x, s, n, slot, threadIdx.x);
     if (threadIdx.x == 0) count = n;
   }
@@ -634,7 +648,7 @@ __global__ void __launch_bounds__(32 * TARGET_WARPS)
   if (target < 0 || target >= V) return;
   const SortRow s = sort_scratch(smem + w * sort_words(K), K);
   int slot[SORT_GROUPS];
-  const int n = sort_row(ids, logp + row * K, K, lane, s, slot);
+  const int n = sort_row(ids, logp + row * K, K, tail, lane, s, slot);
   Teacher q = teacher_of(s.t, n, tail, lane);
   const float rl = rest_logp[row], g = grad_kl[row];
   const bool none = rl == -INFINITY;
@@ -807,7 +821,7 @@ flce_status flce_topk_distill(const void* hidden, const void* weight, const int3
   const DistillOut out{kl, lse, rest_logp, student_logp};
   ListArgs la;
   std::memset(&la, 0, sizeof(la));
-  la.teacher_ids = teacher_ids; la.teacher_logp = teacher_logp; la.K = K; la.V = static_cast<int>(V);
+  la.teacher_ids = teacher_ids; la.teacher_logp = teacher_logp; la.K = K; la.V = static_cast<int>(V); la.tail = tail;
   if (N <= STREAM_MAX_TOKENS) {
     const DistillStream p = distill_stream_plan(N, V, K, dev.sms);
     if (p.total > workspace_bytes) return FLCE_EWORKSPACE;
