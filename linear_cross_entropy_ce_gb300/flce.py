@@ -876,7 +876,8 @@ def topk_distill_bwd(hidden: torch.Tensor, weight: torch.Tensor, teacher_ids: to
     """Gradients of ``sum(grad_kl * kl)``; ``lse``, ``rest_logp`` and ``student_logp``
     are those of :func:`topk_distill` on the same inputs.  Returns
     ``grad_hidden`` (bf16 [N, H]) and ``grad_weight`` ([V, H], fp32 or bf16), or
-    only the one asked for.  The teacher gets no gradient."""
+    only the one asked for, as exact as an fp32 gradient of the logits gives them.
+    The teacher gets no gradient."""
     N, H, V, dev = _check_head(hidden, weight)
     K = _check_teacher(teacher_ids, teacher_logp, N, dev)
     if not (need_hidden or need_weight):
