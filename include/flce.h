@@ -380,11 +380,11 @@ flce_status flce_constrained_logprobs(const void* hidden, const void* weight,
  *   student_logp  [N, K] fp32: log q of the teacher's tokens, 0 for no entry
  * A row without an entry gets 0 in all of them; one that names a token of V or
  * more gets NaN and sets FLCE_EBADTARGET.  After a time-out every row with a
- * teacher is NaN.  log q and log s are formed relative to the row's largest
- * logit and s not as a difference, so that for given logits kl is off by a few
- * 2^-24 of the sum of its terms' magnitudes, however small it is itself (logits
- * that are exact, student and teacher nearly agreeing: 5e-8 at the median).  The
- * logits' own rounding, in fp32, adds 6e-7 to 2e-6 of kl's norm.
+ * teacher is NaN.  Where student and teacher nearly agree kl is what is left of
+ * terms that cancel: for given logits it is off by 2^-24 of itself and some 1e-9,
+ * however small it is.  The logits' own rounding, in fp32, counts with the
+ * difference of the two distributions, as that of any fp32 product (5e-7 to 2e-6 of
+ * kl's norm where they are not close).
  * Workspace (flce_topk_distill_workspace_bytes): as flce_logprobs without
  * alternatives and 14 bytes per entry; up to 128 tokens 4 bytes per row and tile
  * of the vocabulary, beyond 2 bytes per row and 128 of its tokens and 512 bytes

@@ -25,6 +25,7 @@
 // gradient (MODE_DZ) with another log-sum-exp and another upstream gradient.
 // Between it and the two products a small kernel overwrites the listed places.
 #include "flce_listed.cuh"
+#include "flce_pair.cuh"
 #include "flce_ptx.cuh"
 #include "flce_rows.cuh"
 #include "flce_softmax.cuh"
@@ -385,59 +386,95 @@ __device__ __forceinline__ Teacher teacher_of(const float* t, int n, bool tail, 
 // One row by a warp, from the statistics of the logits behind its list and the
 // listed logits z[0 .. n), which may be shared memory.
 //
-// kl is what is left of terms that nearly cancel, and a common error of all log
-// probabilities goes straight into it, so what they share is kept apart: with
-// x = (z - m) / T, s = sum exp(x) = 2^k f, b the sum behind the list (at its own
-// largest logit m_b),
-//   kl = sum p (t - x) + P (k ln 2 + ln f) + r (ln(r s / b) - (m_b - m) / T),
-// P = sum p.  An entry's own rounding (2^-24 of |t| + |x|) is weighed by its p,
-// and k ln 2 P is formed in 64 bits (an fp32 ln s of 10 alone is off by 5e-7).
-// (All in 64 bits, three logarithms a row, the row kernel took 120 us for 5735
-// rows, with this 97 then.)
+// With x = (z - m) / T, m the largest logit, e the sum of exp(x) and b its part
+// behind the list, and w = exp(t - base) with sum P (base 0 with a tail, else the
+// largest log mass), r = 1 - P:
+//   with a tail   kl = sum w (t - x) + P ln e + r (ln r + ln e - ln b)
+//   without       kl = sum w (t - base - x) / P + ln e - ln P
+// kl is what is left of terms that nearly cancel where student and teacher nearly
+// agree, so whatever enters it to the first order there, w, r, e and the logarithms,
+// is held to about 2^-28 (Pair).  Not so the logits: an error of theirs counts with
+// the difference of the two distributions only.  (In fp32, with what the terms share
+// kept apart, kl was off by 5.5e-8 however small it was: 5e-6 of divergences of 1e-2.
+// In 64 bits, three logarithms a row, the row kernel took 120 us for 5735 rows, with
+// fp32 97 then.)
 __device__ __forceinline__ void finish_row(const DistillOut& o, long long row, int K, bool tail, float c2, float inv_t,
                                            Stat rest, const float* z, const float* t, const short* slot, int n,
                                            int lane) {
-  float m = rest.m;
-  bool nan = false;
+  float m = rest.m, top = -INFINITY;
+  bool nan = false, t_nan = false;
   for (int u = lane; u < n; u += 32) {
     m = fmaxf(m, z[u]);
+    top = fmaxf(top, t[u]);
     nan = nan || z[u] != z[u];
-  }
-#pragma unroll
-  for (int k = 16; k > 0; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-  if (__any_sync(0xffffffffu, nan)) m = __int_as_float(0x7fc00000);
-  Teacher q = teacher_of(t, n, tail, lane);
-  const bool none = rest.m == -INFINITY && rest.s == 0.f;   // nothing behind the list
-  if (none) q.rest = 0.f;
-  float s = 0.f, mass = 0.f, sum = 0.f;
-  for (int u = lane; u < n; u += 32) {
-    const float lp = t[u] - q.shift, p = expf(lp), x = (z[u] - m) * inv_t;
-    s += expf(x);
-    mass += p;
-    if (!(p == 0.f)) sum = fmaf(p, lp - x, sum);
+    t_nan = t_nan || t[u] != t[u];
   }
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) {
-    s += __shfl_xor_sync(0xffffffffu, s, k);
-    mass += __shfl_xor_sync(0xffffffffu, mass, k);
-    sum += __shfl_xor_sync(0xffffffffu, sum, k);
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
   }
+  if (__any_sync(0xffffffffu, nan)) m = __int_as_float(0x7fc00000);
+  if (__any_sync(0xffffffffu, t_nan)) top = __int_as_float(0x7fc00000);
+  const bool none = rest.m == -INFINITY && rest.s == 0.f;   // nothing behind the list
+  const float base = tail || top == -INFINITY ? 0.f : top;
+  PairSum e, others, terms;   // sum exp(x); sum w but for one of the largest; sum w (t - base - x)
+  bool never = false;         // the student gives a token of some mass no chance
+  int tops = 0;
+  for (int u = lane; u < n; u += 32) {
+    const float x = (z[u] - m) * inv_t, lp = t[u] - base;
+    const Pair ex = exp_pair(x), w = exp_pair(lp);
+    e.add(ex.hi, ex.lo);
+    if (t[u] == top) ++tops;
+    else others.add(w.hi, w.lo);
+    if (w.hi == 0.f) continue;
+    if (x == -INFINITY) { never = true; continue; }
+    const float d = lp - x, b = d - lp, d_lo = (lp - (d - b)) - (x + b);   // two-sum of lp and -x
+    const float q = w.hi * d;
+    terms.add(q, fmaf(w.hi, d, -q) + fmaf(w.hi, d_lo, w.lo * d));
+  }
+  e.add_lanes();
+  others.add_lanes();
+  terms.add_lanes();
+  tops = __reduce_add_sync(0xffffffffu, tops);
+  const Pair wt = exp_pair(top - base);
+  const double w_top = static_cast<double>(wt.hi) + static_cast<double>(wt.lo);
+  const double but_one = others.value() + (tops - 1) * w_top, mass = w_top + but_one;
+  double r = 0.0;
+  if (tail && !none)   // (1 - the largest) - the others: nothing is lost where the largest is nearly 1
+    r = fmax(0.0, (top > -0.0625f ? -static_cast<double>(expm1f(top)) : 1.0 - w_top) - but_one);
   const float far = none ? -INFINITY : (rest.m - m) * inv_t;
-  if (!none) s += rest.s * expf(far);
-  int k = 0;
-  const float f = frexpf(s, &k), lf = logf(f);
-  const float ls = fmaf(static_cast<float>(k), LN2, lf);
+  double all = e.value();
+  if (!none) {
+    const Pair f = exp_pair(far);
+    all += static_cast<double>(rest.s) * (static_cast<double>(f.hi) + static_cast<double>(f.lo));
+  }
+  // three logarithms, a lane each; what is not used may be no number
+  const double mine = log_of(lane == 0 ? all : (lane == 1 ? (tail ? r : mass) : static_cast<double>(rest.s)));
+  const double le = __shfl_sync(0xffffffffu, mine, 0), lm = __shfl_sync(0xffffffffu, mine, 1),
+               lb = __shfl_sync(0xffffffffu, mine, 2);
+  const float ls = static_cast<float>(le), ls_rest = static_cast<float>(le - static_cast<double>(ls));
   for (int j = lane; j < K; j += 32) {
     const int u = slot[j];
-    o.student_logp[row * K + j] = u < 0 || u >= n ? 0.f : fmaf(z[u] - m, inv_t, -ls);
+    o.student_logp[row * K + j] = u < 0 || u >= n ? 0.f : fmaf(z[u] - m, inv_t, -ls) - ls_rest;
   }
+  never = __any_sync(0xffffffffu, never);
   if (lane == 0) {
-    double kl = static_cast<double>(mass) * k * 0.6931471805599453 + fmaf(mass, lf, sum);
-    // a teacher without any mass asks for nothing
-    if (!(q.rest == 0.f)) kl += q.rest * (logf(q.rest * (s / rest.s)) - far);
+    double kl = terms.value();
+    if (tail) {
+      kl += mass * le;
+      // a teacher without any mass asks for nothing
+      if (!(r == 0.0)) kl += r * (lm + (le - lb) - static_cast<double>(far));
+    } else if (mass > 0.0) {
+      double inv = 1.f / static_cast<float>(mass);
+      inv = inv * (2.0 - mass * inv);
+      kl = kl * inv + (le - lm);
+    }
+    if (never) kl += INFINITY;
+    if (top != top) kl = top;
     o.kl[row] = static_cast<float>(kl);
     o.lse[row] = fmaf(m, inv_t, ls);
-    o.rest_logp[row] = none ? -INFINITY : far - logf(s / rest.s);
+    o.rest_logp[row] = none ? -INFINITY : static_cast<float>(static_cast<double>(far) - (le - lb));
   }
 }
 
