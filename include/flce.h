@@ -383,8 +383,8 @@ flce_status flce_constrained_logprobs(const void* hidden, const void* weight,
  * teacher is NaN.  Where student and teacher nearly agree kl is what is left of
  * terms that cancel: for given logits it is off by 2^-24 of itself and some 1e-9,
  * however small it is.  The logits' own rounding, in fp32, counts with the
- * difference of the two distributions, as that of any fp32 product (5e-7 to 2e-6 of
- * kl's norm where they are not close).
+ * difference of the two distributions, about as that of any fp32 product (5e-7 to 2e-6
+ * of kl's norm where they are not close).
  * Workspace (flce_topk_distill_workspace_bytes): as flce_logprobs without
  * alternatives and 14 bytes per entry; up to 128 tokens 4 bytes per row and tile
  * of the vocabulary, beyond 2 bytes per row and 128 of its tokens and 512 bytes

@@ -746,15 +746,22 @@ cudaError_t by_groups(int K, F&& f) {
 
 // K blocks of a segment of a logit's sum (see segment_blocks()).  A divergence of
 // distributions that nearly agree keeps the logits' absolute errors, so its
-// segments are shorter than those of the log probabilities: kl is off by no more
-// than with an fp32 product on the CUDA cores (2000 tokens at 1024, 2048, 4096 x
+// segments are shorter than those of the log probabilities: kl is off by about as
+// much as with an fp32 product on the CUDA cores (2000 tokens at 1024, 2048, 4096 x
 // 60000: 1.0e-6, 1.5e-6, 2.1e-6 of its norm and 1.1e-6, 1.7e-6, 2.7e-6; with the
-// log probabilities' segments 1.5e-6, 2.1e-6, 3.0e-6 and 1 to 2% faster).  Up to
-// 64 tokens four blocks cost nothing, since the weight's bytes bound the kernel.
+// log probabilities' segments 1.5e-6, 2.1e-6, 3.0e-6 and 1 to 2% faster; 0.4 to 1.3
+// times elsewhere, 1.5 for the one segment of 128).  Up to 64 tokens four blocks cost
+// nothing, since the weight's bytes bound the kernel.
+// Sums of 3 blocks and more are in two segments at least: in one, 600 tokens at 192
+// and 248 x 2250 were off by 1.4 to 1.9 times what the fp32 product was, in two by 0.7
+// to 0.9.  That costs short tiles much (8192 tokens at 256 x 128256 437 -> 713 us, 4096
+// at 256 x 16000 64 -> 82, 300 at 16000 25 -> 29), as it does from five blocks on.
 int distill_segment(long long N, long long H) {
   const int blocks = static_cast<int>(cdiv(H, BK));
-  const int most = N <= 64 ? 4 : std::max(4, static_cast<int>(1.75 * std::sqrt(static_cast<double>(blocks))));
-  return static_cast<int>(cdiv(blocks, cdiv(blocks, N <= STREAM_MAX_TOKENS ? std::min(most, 8) : most)));   // of equal length
+  int most = N <= 64 ? 4 : std::max(4, static_cast<int>(1.75 * std::sqrt(static_cast<double>(blocks))));
+  if (N <= STREAM_MAX_TOKENS) most = std::min(most, 8);
+  most = std::min(most, std::max(2, (blocks + 1) / 2));
+  return static_cast<int>(cdiv(blocks, cdiv(blocks, most)));   // of equal length
 }
 
 struct DistillStream {
