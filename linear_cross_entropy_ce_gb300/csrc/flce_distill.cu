@@ -398,8 +398,8 @@ __device__ __forceinline__ Teacher teacher_of(const float* t, int n, bool tail, 
 // kept apart, kl was off by 5.5e-8 however small it was: 5e-6 of divergences of 1e-2.
 // In 64 bits, three logarithms a row, the row kernel took 120 us for 5735 rows, with
 // fp32 97 then.)
-__device__ __forceinline__ void finish_row(const DistillOut& o, long long row, int K, bool tail, float c2, float inv_t,
-                                           Stat rest, const float* z, const float* t, const short* slot, int n,
+__device__ __forceinline__ void finish_row(const DistillOut& o, long long row, int K, bool tail, float inv_t, Stat rest,
+                                           const float* z, const float* t, const short* slot, int n,
                                            int lane) {
   float m = rest.m, top = -INFINITY;
   bool nan = false, t_nan = false;
@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(32 * ROWS8 * (1 + SHARES)) distill_rows_kernel
   Stat rest = share[0][k];
 #pragma unroll
   for (int i = 1; i <= SHARES; ++i) rest = merge(rest, share[i][k], a.c2);
-  finish_row(a.out, row, a.K, a.tail, a.c2, a.inv_t, rest, mine, a.t + list * a.K, a.slot + list * a.K, n, lane);
+  finish_row(a.out, row, a.K, a.tail, a.inv_t, rest, mine, a.t + list * a.K, a.slot + list * a.K, n, lane);
 }
 
 // After a call of several chunks: a pipeline that timed out in one of them
@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(32) distill_stream_rows_kernel(const StreamRow
   if (failed || bad) return fill_row(a.out, n0, a.K, __int_as_float(0x7fc00000), lane);
   const long long at = static_cast<long long>(n0) * a.K;
   const int n = min(a.K, a.start[static_cast<long long>(n0) * (a.tiles + 1) + a.tiles]);
-  finish_row(a.out, n0, a.K, a.tail, a.c2, a.inv_t, acc, a.z + at, a.t + at, a.slot + at, n, lane);
+  finish_row(a.out, n0, a.K, a.tail, a.inv_t, acc, a.z + at, a.t + at, a.slot + at, n, lane);
 }
 
 // ---------------------------------------------------------------------------
