@@ -437,44 +437,43 @@ __device__ __forceinline__ void finish_row(const DistillOut& o, long long row, i
   others.add_lanes();
   terms.add_lanes();
   tops = __reduce_add_sync(0xffffffffu, tops);
-  const Pair wt = exp_pair(top - base);
-  const double w_top = static_cast<double>(wt.hi) + static_cast<double>(wt.lo);
-  const double but_one = others.value() + (tops - 1) * w_top, mass = w_top + but_one;
-  double r = 0.0;
-  if (tail && !none)   // (1 - the largest) - the others: nothing is lost where the largest is nearly 1
-    r = fmax(0.0, (top > -0.0625f ? -static_cast<double>(expm1f(top)) : 1.0 - w_top) - but_one);
-  const float far = none ? -INFINITY : (rest.m - m) * inv_t;
-  double all = e.value();
-  if (!none) {
-    const Pair f = exp_pair(far);
-    all += static_cast<double>(rest.s) * (static_cast<double>(f.hi) + static_cast<double>(f.lo));
+  const Pair w_top = exp_pair(top - base);
+  const Pair but_one = others.value() + Pair{static_cast<float>(tops - 1), 0.f} * w_top, mass = w_top + but_one;
+  Pair r = {0.f, 0.f};
+  if (tail && !none) {   // (1 - the largest) - the others: nothing is lost where the largest is nearly 1
+    r = (top > -0.0625f ? Pair{-expm1f(top), 0.f} : Pair{1.f, 0.f} - w_top) - but_one;
+    if (r.hi <= 0.f) r = Pair{0.f, 0.f};
   }
+  const float far = none ? -INFINITY : (rest.m - m) * inv_t;
+  Pair all = e.value();
+  if (!none) all = all + Pair{rest.s, 0.f} * exp_pair(far);
   // three logarithms, a lane each; what is not used may be no number
-  const double mine = log_of(lane == 0 ? all : (lane == 1 ? (tail ? r : mass) : static_cast<double>(rest.s)));
-  const double le = __shfl_sync(0xffffffffu, mine, 0), lm = __shfl_sync(0xffffffffu, mine, 1),
-               lb = __shfl_sync(0xffffffffu, mine, 2);
-  const float ls = static_cast<float>(le), ls_rest = static_cast<float>(le - static_cast<double>(ls));
+  const Pair mine = log_of(lane == 0 ? all : (lane == 1 ? (tail ? r : mass) : Pair{rest.s, 0.f}));
+  auto of_lane = [&](int i) {
+    return Pair{__shfl_sync(0xffffffffu, mine.hi, i), __shfl_sync(0xffffffffu, mine.lo, i)};
+  };
+  const Pair le = of_lane(0), lm = of_lane(1), lb = of_lane(2);
   for (int j = lane; j < K; j += 32) {
     const int u = slot[j];
-    o.student_logp[row * K + j] = u < 0 || u >= n ? 0.f : fmaf(z[u] - m, inv_t, -ls) - ls_rest;
+    o.student_logp[row * K + j] = u < 0 || u >= n ? 0.f : fmaf(z[u] - m, inv_t, -le.hi) - le.lo;
   }
   never = __any_sync(0xffffffffu, never);
   if (lane == 0) {
-    double kl = terms.value();
+    Pair kl = terms.value();
+    const Pair behind = Pair{far, 0.f} - (le - lb);   // log s
     if (tail) {
-      kl += mass * le;
+      kl = kl + mass * le;
       // a teacher without any mass asks for nothing
-      if (!(r == 0.0)) kl += r * (lm + (le - lb) - static_cast<double>(far));
-    } else if (mass > 0.0) {
-      double inv = 1.f / static_cast<float>(mass);
-      inv = inv * (2.0 - mass * inv);
-      kl = kl * inv + (le - lm);
+      if (!(r.hi == 0.f)) kl = kl + r * (lm - behind);
+    } else if (mass.hi > 0.f) {
+      kl = kl / mass + (le - lm);
     }
-    if (never) kl += INFINITY;
-    if (top != top) kl = top;
-    o.kl[row] = static_cast<float>(kl);
-    o.lse[row] = fmaf(m, inv_t, ls);
-    o.rest_logp[row] = none ? -INFINITY : static_cast<float>(static_cast<double>(far) - (le - lb));
+    float k = kl.hi + kl.lo;
+    if (never) k += INFINITY;
+    if (top != top) k = top;
+    o.kl[row] = k;
+    o.lse[row] = fmaf(m, inv_t, le.hi);
+    o.rest_logp[row] = none ? -INFINITY : behind.hi;
   }
 }
 
