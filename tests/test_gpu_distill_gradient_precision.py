@@ -21,7 +21,7 @@ pytestmark = pytest.mark.gpu
 CASES = [  # N, H, V, K, T, tail
     (2, 64, 500, 1, 1.0, True), (2, 512, 3001, 8, 1.0, True), (17, 136, 1000, 5, 1.0, False), (63, 264, 2049, 20, 2.0, True),
     (128, 64, 512, 64, 1.0, True), (129, 72, 4000, 3, 0.7, True), (300, 64, 512, 8, 2.0, False), (450, 520, 999, 1, 1.0, False),
-    (453, 256, 3000, 32, 1.0, True), (900, 64, 2000, 256, 1.0, True)]
+    (453, 256, 3000, 32, 1.0, True), (900, 64, 2000, 256, 1.0, True), (16500, 8, 300, 5, 1.0, True)]
 
 
 def gradients(flce, torch, dev, X, W, ids, t, g, T, tail, **kw):
